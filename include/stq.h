@@ -304,6 +304,100 @@ stq_status stq_q2_roundtrip(const float* w, int64_t n_rows, int64_t k, float* ou
 stq_status stq_greedy_allocation(const double* gain, const double* extra_bytes, int64_t n_layers,
                                  double budget, uint8_t* chosen);
 
+/* Rows of 8-bit integers with one fp32 scale each, the form in which a model
+ * keeps what its allocation leaves above the ternary format (attention
+ * projections, the output head; lemmy post 66506, paragraph "Precision
+ * follows weight sensitivity") and in which the activations meet it.  Per row
+ *     scale = fp32(max |x| / 127),  q = nearest integer to x / scale
+ * (the exact quotient, halves to even, held to +-127); a row of zeros, or one
+ * whose scale underflows to 0, gives scale 0 and q = 0; a row that holds a
+ * NaN or an infinity gives scale NaN and q = 0, so that every product with it
+ * is NaN.
+ *   x      [n_rows, k] fp32 (STQ_X_F32) or bf16 bits (STQ_X_BF16), rows
+ *          x_row_stride elements apart, aligned to its elements; rows that
+ *          start on 16 bytes load faster
+ *   q      int8, row r at q + r*q_row_stride, 16-byte aligned, q_row_stride a
+ *          multiple of 16 and at least k rounded up to 16; the bytes from k
+ *          up to that multiple are written 0, those behind it are left
+ *   scale  [n_rows] fp32
+ * k >= 1; at most 2^23 rows per call. */
+stq_status stq_q8_quantize_rows(const void* x, int x_dtype, int64_t x_row_stride, int64_t n_rows, int64_t k,
+                                int8_t* q, int64_t q_row_stride, float* scale, stq_stream_t stream);
+
+/* Product of two sets of such rows:
+ *     y[i, j] = (sum_c a[i, c] * w[j, c]) * a_scale[i] * w_scale[j]
+ * with the sum exact (int32) and the scaling in fp32.
+ *   a, a_scale   [m, k] int8 and [m] fp32: the tokens
+ *   w, w_scale   [n, k] int8 and [n] fp32: the output channels
+ *                both 16-byte aligned with row strides (bytes) that are
+ *                multiples of 16, at least k rounded up to 16 and at most
+ *                2^23; a row's bytes behind k, up to that multiple, may be
+ *                read and count for nothing
+ *   y            [m, n] fp32 (STQ_X_F32) or bf16 (STQ_X_BF16, one rounding of
+ *                the fp32 value), rows y_row_stride elements apart; rows that
+ *                start on four elements store faster
+ *   workspace, workspace_bytes   scratch for split sums, at least what
+ *                stq_q8_matmul_workspace reports (may be NULL when that is 0)
+ * 1 <= k <= 131071 (any sum of products of bytes then fits 32 bits); m up to
+ * 2^22.  Integer sums do not depend on their order: a result's bits do not
+ * depend on m, n, the strides or the device. */
+stq_status stq_q8_matmul(const int8_t* a, int64_t a_row_stride, const float* a_scale, const int8_t* w,
+                         int64_t w_row_stride, const float* w_scale, int64_t m, int64_t n, int64_t k, void* y,
+                         int y_dtype, int64_t y_row_stride, void* workspace, int64_t workspace_bytes,
+                         stq_stream_t stream);
+
+/* Workspace bytes stq_q8_matmul needs for these shapes on a device with n_cus
+ * compute units (0: the current device's); host only, same checks and errors
+ * as the call.  workspace_bytes is a HOST pointer. */
+stq_status stq_q8_matmul_workspace(int64_t m, int64_t n, int64_t k, int32_t n_cus, int64_t* workspace_bytes);
+
+/* Log probabilities of given tokens under rows of logits, with each row's
+ * log-sum-exp, entropy and most likely alternatives: how a compressed model
+ * is scored token by token against its original.  With p = softmax(l):
+ *     lse = log sum_i exp(l_i)            logprob = l_target - lse
+ *     entropy = -sum_i p_i log p_i        top: the top_n largest l_i
+ *   logits    [n_rows, vocab] fp32 (STQ_X_F32) or bf16 bits (STQ_X_BF16), rows
+ *             row_stride elements apart, aligned to its elements.  -inf masks
+ *             an entry (p = 0).
+ *   targets   int32 [n_rows]; outside [0, vocab): logprob NaN
+ *   logprob   fp32 [n_rows];  lse, entropy  fp32 [n_rows] or NULL
+ *   top_n     0..32, at most vocab
+ *   top_ids, top_logprobs  int32 / fp32 [n_rows, top_n], most likely first,
+ *             equal logits by lowest id (may be NULL when top_n is 0)
+ *   workspace, workspace_bytes  scratch for rows that are split, at least
+ *             what stq_token_logprobs_workspace reports (may be NULL when 0)
+ * A row without a distribution gives NaN log probabilities and entropy and
+ * ids -1: one that is masked throughout (lse = -inf) or that holds a NaN or a
+ * +inf (lse = NaN).  Sums and maxima are fp32; the order of summation is fixed
+ * for a device, so repeated calls give identical bits.  At most 2^22 rows. */
+stq_status stq_token_logprobs(const void* logits, int x_dtype, int64_t row_stride, int64_t n_rows, int64_t vocab,
+                              const int32_t* targets, float* logprob, float* lse, float* entropy, int64_t top_n,
+                              int32_t* top_ids, float* top_logprobs, void* workspace, int64_t workspace_bytes,
+                              stq_stream_t stream);
+
+/* Workspace bytes stq_token_logprobs needs for these shapes on a device with
+ * n_cus compute units (0: the current device's); host only, same checks and
+ * errors as the call.  workspace_bytes is a HOST pointer. */
+stq_status stq_token_logprobs_workspace(int x_dtype, int64_t n_rows, int64_t vocab, int64_t top_n, int32_t n_cus,
+                                        int64_t* workspace_bytes);
+
+/* Gradient of stq_token_logprobs with respect to the logits, for gradients
+ * that arrive at logprob and entropy (the alternatives carry none):
+ *     d_i = g_logprob * (1[i = target] - p_i) - g_entropy * p_i * (log p_i + entropy)
+ *   logits, x_dtype, row_stride, targets   as for the call above
+ *   lse, entropy   fp32 [n_rows], what the call above gave (entropy may be
+ *                  NULL when grad_entropy is)
+ *   grad_logprob, grad_entropy   fp32 [n_rows]; either may be NULL (zeros)
+ *   d_logits       [n_rows, vocab], the logits' type, rows d_row_stride
+ *                  elements apart; may be the logits themselves (same pointer
+ *                  and stride), else it may not overlap them
+ * A target outside [0, vocab) takes no grad_logprob; a row with lse = -inf
+ * gives zeros, one with lse = NaN gives NaN.  At most 2^22 rows. */
+stq_status stq_token_logprobs_backward(const void* logits, int x_dtype, int64_t row_stride, int64_t n_rows,
+                                       int64_t vocab, const int32_t* targets, const float* lse, const float* entropy,
+                                       const float* grad_logprob, const float* grad_entropy, void* d_logits,
+                                       int64_t d_row_stride, stq_stream_t stream);
+
 /* Measurement helper, not part of the method: reads `bytes` bytes of the
  * device buffer `buf` once with 16-byte loads, the streaming-read rate this
  * GPU sustains, against which the decode GEMV's effective bandwidth is

@@ -17,7 +17,8 @@ __all__ = [
     "QK", "BLOCK_BYTES", "ENC_WLS", "ENC_AMAX", "StqError", "lib", "lib_path",
     "row_bytes", "quantize_rows", "dequantize_rows", "gemv", "gemv_noalloc", "gemv_plan", "grouped_gemm",
     "moe_ffn_decode",
-    "moe_ffn_workspace", "layer_errors", "layer_errors_workspace", "q2_roundtrip", "greedy_allocation",
+    "moe_ffn_workspace", "q8_quantize_rows", "q8_matmul", "q8_matmul_workspace", "token_logprobs",
+    "token_logprobs_workspace", "token_logprobs_backward", "layer_errors", "layer_errors_workspace", "q2_roundtrip", "greedy_allocation",
     "stream_read_probe", "mfma_loop_probe", "lds_read_probe", "MFMA_PROBE_FLOP_PER_ROUND",
     "LDS_PROBE_READS_PER_ROUND",
 ]
@@ -95,6 +96,22 @@ def lib() -> ctypes.CDLL:
     L.stq_q2_roundtrip.restype = _c_int
     L.stq_greedy_allocation.argtypes = [_c_vp, _c_vp, _c_i64, ctypes.c_double, _c_vp]
     L.stq_greedy_allocation.restype = _c_int
+    L.stq_q8_quantize_rows.argtypes = [_c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64, _c_vp, _c_vp]
+    L.stq_q8_quantize_rows.restype = _c_int
+    L.stq_q8_matmul.argtypes = [_c_vp, _c_i64, _c_vp, _c_vp, _c_i64, _c_vp, _c_i64, _c_i64, _c_i64, _c_vp, _c_int,
+                                _c_i64, _c_vp, _c_i64, _c_vp]
+    L.stq_q8_matmul.restype = _c_int
+    L.stq_q8_matmul_workspace.argtypes = [_c_i64, _c_i64, _c_i64, ctypes.c_int32, ctypes.POINTER(_c_i64)]
+    L.stq_q8_matmul_workspace.restype = _c_int
+    L.stq_token_logprobs.argtypes = [_c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_vp, _c_vp, _c_vp, _c_vp, _c_i64,
+                                     _c_vp, _c_vp, _c_vp, _c_i64, _c_vp]
+    L.stq_token_logprobs.restype = _c_int
+    L.stq_token_logprobs_workspace.argtypes = [_c_int, _c_i64, _c_i64, _c_i64, ctypes.c_int32,
+                                               ctypes.POINTER(_c_i64)]
+    L.stq_token_logprobs_workspace.restype = _c_int
+    L.stq_token_logprobs_backward.argtypes = [_c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_vp, _c_vp, _c_vp, _c_vp,
+                                              _c_vp, _c_vp, _c_i64, _c_vp]
+    L.stq_token_logprobs_backward.restype = _c_int
     L.stq_stream_read_probe.argtypes = [_c_vp, _c_i64, _c_vp, _c_vp]
     L.stq_stream_read_probe.restype = _c_int
     L.stq_mfma_loop_probe.argtypes = [_c_i64, _c_vp, _c_vp]
@@ -162,6 +179,50 @@ def _ws_args(ws: torch.Tensor | None) -> tuple:
 def _table(name: str, t: torch.Tensor, n_experts: int, stride: int, n: int, k: int) -> None:
     if n_experts > 0 and n > 0:
         _holds(name, t, (int(n_experts) - 1) * int(stride) + int(n) * row_bytes(k))
+
+
+def _together(**tensors) -> torch.device:
+    """The one GPU every given tensor lives on."""
+    dev = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a GPU tensor")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the other tensors are on {dev}")
+    return dev
+
+
+def _call(device: torch.device, func: str, *args) -> None:
+    """Run an entry point on `device`'s current stream, with that device current."""
+    f = getattr(lib(), func)
+    if device.index == torch.cuda.current_device():
+        _check(func, f(*args, torch.cuda.current_stream().cuda_stream))
+    else:
+        with torch.cuda.device(device):
+            _check(func, f(*args, torch.cuda.current_stream().cuda_stream))
+
+
+def _rows(name: str, t: torch.Tensor, *dtypes: torch.dtype) -> int:
+    """Row stride in elements of a matrix whose rows are contiguous (any distance apart)."""
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a matrix with contiguous rows")
+    # a one-row view may carry any stride in its first dimension
+    return t.stride(0) if t.shape[0] > 1 else max(1, t.shape[1])
+
+
+def _vector(name: str, t: torch.Tensor, dtype: torch.dtype, n: int) -> None:
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.numel() != n:
+        raise ValueError(f"{name} must hold {n} entries, got {t.numel()}")
 
 
 def row_bytes(k: int) -> int:
@@ -354,6 +415,145 @@ def moe_ffn_decode(w_gate_up: torch.Tensor, gate_up_stride: int, w_down: torch.T
                                     int(n_experts), int(d_model), int(d_ff), x.data_ptr(), n_tokens,
                                     pair_expert.data_ptr(), pair_weight.data_ptr(), int(top_k), out.data_ptr(),
                                     *_ws_args(workspace), _stream()))
+    return out
+
+
+def _q8_stride(name: str, t: torch.Tensor) -> int:
+    """Row stride in bytes of int8 rows, which own their bytes up to the next multiple of 16."""
+    stride = _rows(name, t, torch.int8)
+    kp = (t.shape[1] + 15) // 16 * 16
+    if t.shape[0] == 1:
+        stride = kp
+    if t.numel() and t.storage_offset() + (t.shape[0] - 1) * stride + kp > t.untyped_storage().nbytes():
+        raise ValueError(f"{name}'s last row must own its bytes up to the next multiple of 16")
+    return stride
+
+
+def q8_quantize_rows(x: torch.Tensor, out: torch.Tensor | None = None, scale: torch.Tensor | None = None):
+    """Rows of 8-bit integers with one scale each: (q int8 [n, k], scale fp32 [n]) of x fp32 or bf16
+    [n, k], scale = max|x| / 127 and q the nearest integer to x / scale.  Without `out` the rows are
+    k rounded up to 16 bytes apart (the layout q8_matmul reads), padded with zeros."""
+    dev = _together(x=x, out=out, scale=scale)
+    stride = _rows("x", x, torch.float32, torch.bfloat16)
+    n, k = x.shape
+    if out is None:
+        out = torch.empty((n, (k + 15) // 16 * 16), dtype=torch.int8, device=dev)[:, :k]
+    if tuple(out.shape) != (n, k):
+        raise ValueError("out must be [n, k] like x")
+    qs = _q8_stride("out", out)
+    if scale is None:
+        scale = torch.empty(n, dtype=torch.float32, device=dev)
+    _vector("scale", scale, torch.float32, n)
+    _call(dev, "stq_q8_quantize_rows", x.data_ptr(), X_BF16 if x.dtype == torch.bfloat16 else X_F32, stride, n, k,
+          out.data_ptr(), qs, scale.data_ptr())
+    return out, scale
+
+
+def q8_matmul_workspace(m: int, n: int, k: int, n_cus: int = 0) -> int:
+    """Workspace bytes q8_matmul needs for these shapes on n_cus compute units (0: the current
+    device's); host only."""
+    wb = ctypes.c_int64()
+    _check("stq_q8_matmul_workspace", lib().stq_q8_matmul_workspace(int(m), int(n), int(k), int(n_cus),
+                                                                    ctypes.byref(wb)))
+    return wb.value
+
+
+def q8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+              out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16,
+              workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """y[i, j] = (a[i] . w[j]) a_scale[i] w_scale[j] for int8 rows a [m, k] and w [n, k], the sum exact;
+    y is bf16 or fp32 [m, n].  `workspace` (GPU bytes, at least q8_matmul_workspace(m, n, k)) is
+    allocated here when not given."""
+    dev = _together(a=a, a_scale=a_scale, w=w, w_scale=w_scale, out=out, workspace=workspace)
+    lda, ldw = _q8_stride("a", a), _q8_stride("w", w)
+    m, k = a.shape
+    n = w.shape[0]
+    if w.shape[1] != k:
+        raise ValueError("a and w must have rows of the same length")
+    _vector("a_scale", a_scale, torch.float32, m)
+    _vector("w_scale", w_scale, torch.float32, n)
+    if out is None:
+        if out_dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError("out_dtype must be bfloat16 or float32")
+        out = torch.empty((m, n), dtype=out_dtype, device=dev)
+    if tuple(out.shape) != (m, n):
+        raise ValueError("out must be [m, n]")
+    ldy = _rows("out", out, torch.bfloat16, torch.float32)
+    if workspace is None and m > 0 and n > 0:
+        workspace = _workspace(None, q8_matmul_workspace(m, n, k, _device_cus(dev)), dev)
+    else:
+        workspace = _workspace(workspace, 0, dev)
+    _call(dev, "stq_q8_matmul", a.data_ptr(), lda, a_scale.data_ptr(), w.data_ptr(), ldw, w_scale.data_ptr(), m, n, k,
+          out.data_ptr(), X_BF16 if out.dtype == torch.bfloat16 else X_F32, ldy, *_ws_args(workspace))
+    return out
+
+
+def token_logprobs_workspace(x_dtype: int, n_rows: int, vocab: int, top_n: int, n_cus: int = 0) -> int:
+    """Workspace bytes token_logprobs needs for these shapes (x_dtype X_F32 or X_BF16) on n_cus
+    compute units (0: the current device's); host only."""
+    wb = ctypes.c_int64()
+    _check("stq_token_logprobs_workspace",
+           lib().stq_token_logprobs_workspace(int(x_dtype), int(n_rows), int(vocab), int(top_n), int(n_cus),
+                                              ctypes.byref(wb)))
+    return wb.value
+
+
+def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, top_n: int = 0, logprob: torch.Tensor | None = None,
+                   lse: torch.Tensor | None = None, entropy: torch.Tensor | None = None,
+                   top_ids: torch.Tensor | None = None, top_logprobs: torch.Tensor | None = None,
+                   workspace: torch.Tensor | None = None):
+    """(logprob, lse, entropy, top_ids, top_logprobs) of logits fp32 or bf16 [n, vocab] at targets
+    int32 [n]: log probability of each row's target, log-sum-exp, entropy, and the top_n (at most 32)
+    most likely ids with their log probabilities, equal logits by lowest id.  Outputs and `workspace`
+    (GPU bytes, at least token_logprobs_workspace(...)) are allocated here when not given."""
+    dev = _together(logits=logits, targets=targets, logprob=logprob, lse=lse, entropy=entropy, top_ids=top_ids,
+                    top_logprobs=top_logprobs, workspace=workspace)
+    stride = _rows("logits", logits, torch.float32, torch.bfloat16)
+    n, vocab = logits.shape
+    top_n = int(top_n)
+    if top_n < 0:
+        raise ValueError("top_n must not be negative")
+    _vector("targets", targets, torch.int32, n)
+    outs = []
+    for name, t, dtype, shape in (("logprob", logprob, torch.float32, (n,)), ("lse", lse, torch.float32, (n,)),
+                                  ("entropy", entropy, torch.float32, (n,)), ("top_ids", top_ids, torch.int32, (n, top_n)),
+                                  ("top_logprobs", top_logprobs, torch.float32, (n, top_n))):
+        if t is None:
+            t = torch.empty(shape, dtype=dtype, device=dev)
+        else:
+            _vector(name, t, dtype, n * (top_n if len(shape) == 2 else 1))
+        outs.append(t)
+    xd = X_BF16 if logits.dtype == torch.bfloat16 else X_F32
+    if workspace is None and n > 0:
+        workspace = _workspace(None, token_logprobs_workspace(xd, n, vocab, top_n, _device_cus(dev)), dev)
+    else:
+        workspace = _workspace(workspace, 0, dev)
+    _call(dev, "stq_token_logprobs", logits.data_ptr(), xd, stride, n, vocab, targets.data_ptr(), outs[0].data_ptr(),
+          outs[1].data_ptr(), outs[2].data_ptr(), top_n, outs[3].data_ptr(), outs[4].data_ptr(), *_ws_args(workspace))
+    return tuple(outs)
+
+
+def token_logprobs_backward(logits: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor,
+                            entropy: torch.Tensor | None, grad_logprob: torch.Tensor | None,
+                            grad_entropy: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of token_logprobs with respect to the logits, for gradients fp32 [n] arriving at
+    logprob and entropy (either may be None); lse and entropy are what the forward call gave.
+    `out` has the logits' type and shape and may be the logits themselves."""
+    dev = _together(logits=logits, targets=targets, lse=lse, entropy=entropy, grad_logprob=grad_logprob,
+                    grad_entropy=grad_entropy, out=out)
+    stride = _rows("logits", logits, torch.float32, torch.bfloat16)
+    n, vocab = logits.shape
+    _vector("targets", targets, torch.int32, n)
+    for name, t in (("lse", lse), ("entropy", entropy), ("grad_logprob", grad_logprob), ("grad_entropy", grad_entropy)):
+        if t is not None:
+            _vector(name, t, torch.float32, n)
+    if out is None:
+        out = torch.empty((n, vocab), dtype=logits.dtype, device=dev)
+    if tuple(out.shape) != (n, vocab):
+        raise ValueError("out must be [n, vocab] like the logits")
+    _call(dev, "stq_token_logprobs_backward", logits.data_ptr(), X_BF16 if logits.dtype == torch.bfloat16 else X_F32,
+          stride, n, vocab, targets.data_ptr(), lse.data_ptr(), _ptr(entropy), _ptr(grad_logprob), _ptr(grad_entropy),
+          out.data_ptr(), _rows("out", out, logits.dtype))
     return out
 
 

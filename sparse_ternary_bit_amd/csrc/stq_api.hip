@@ -380,6 +380,179 @@ stq_status stq_greedy_allocation(const double* gain, const double* extra_bytes, 
   return ok();
 }
 
+namespace {
+
+constexpr int64_t kMaxStride8 = int64_t{1} << 23;  // bytes between 8-bit rows: a tile's rows stay within 32-bit offsets
+constexpr int64_t kMaxK8 = 131071;                 // k * 128 * 128 < 2^31
+
+// Bytes of a [rows, cols] array with the given row stride stay far inside 63 bits.
+bool fits(int64_t rows, int64_t stride, int64_t esz) {
+  return stride <= 0 || rows <= (INT64_MAX >> 2) / stride / esz;
+}
+
+stq_status q8_shape_check(int64_t m, int64_t n, int64_t k, const char* who) {
+  if (m < 0 || n < 0) return fail(STQ_E_ARG, "%s: negative count", who);
+  if (k < 1 || k > kMaxK8) return fail(STQ_E_SHAPE, "%s: k=%lld outside 1..%lld", who, (long long)k, (long long)kMaxK8);
+  if (n > INT_MAX / 2) return fail(STQ_E_SHAPE, "%s: more than 2^30 channels", who);
+  if (m > (int64_t{1} << 22)) return fail(STQ_E_SHAPE, "%s: more than 2^22 tokens in one call", who);
+  return STQ_OK;
+}
+
+}  // namespace
+
+stq_status stq_q8_quantize_rows(const void* x, int x_dtype, int64_t x_row_stride, int64_t n_rows, int64_t k,
+                                int8_t* q, int64_t q_row_stride, float* scale, stq_stream_t stream) {
+  const char* who = "stq_q8_quantize_rows";
+  if (n_rows < 0) return fail(STQ_E_ARG, "%s: n_rows < 0", who);
+  if (k < 1) return fail(STQ_E_SHAPE, "%s: k=%lld is not positive", who, (long long)k);
+  if (x_dtype != STQ_X_F32 && x_dtype != STQ_X_BF16) return fail(STQ_E_ARG, "%s: unknown x_dtype %d", who, x_dtype);
+  if (k > INT_MAX || n_rows > (int64_t{1} << 23)) return fail(STQ_E_SHAPE, "%s: more than 2^23 rows or k above int32", who);
+  if (n_rows > 1 && x_row_stride < k) return fail(STQ_E_SHAPE, "%s: x_row_stride < k", who);
+  if (q_row_stride < (k + 15) / 16 * 16) return fail(STQ_E_SHAPE, "%s: q_row_stride < k rounded up to 16", who);
+  if (n_rows == 0) return ok();
+  if (!x || !q || !scale) return fail(STQ_E_ARG, "%s: null pointer", who);
+  const int esz = x_dtype == STQ_X_BF16 ? 2 : 4;
+  if (!fits(n_rows, x_row_stride, esz) || !fits(n_rows, q_row_stride, 1)) return fail(STQ_E_SHAPE, "%s: row stride too large", who);
+  if (!aligned(x, esz) || !aligned(scale, 4)) return fail(STQ_E_ALIGN, "%s: x or scale not aligned to its elements", who);
+  if (!aligned(q, 16) || q_row_stride % 16) return fail(STQ_E_ALIGN, "%s: q / q_row_stride not 16-byte aligned", who);
+  const stq::Q8QuantArgs a{x, x_dtype == STQ_X_BF16 ? 1 : 0, x_row_stride, n_rows, k, q, q_row_stride, scale};
+  hipError_t e = stq::launch_q8_quantize(a, reinterpret_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "stq_q8_quantize_rows launch");
+  return ok();
+}
+
+stq_status stq_q8_matmul_workspace(int64_t m, int64_t n, int64_t k, int32_t n_cus, int64_t* workspace_bytes) {
+  if (!workspace_bytes) return fail(STQ_E_ARG, "stq_q8_matmul_workspace: null output pointer");
+  *workspace_bytes = 0;
+  if (n_cus < 0) return fail(STQ_E_ARG, "stq_q8_matmul_workspace: n_cus < 0");
+  const stq_status st = q8_shape_check(m, n, k, "stq_q8_matmul_workspace");
+  if (st != STQ_OK) return st;
+  if (m > 0 && n > 0)
+    *workspace_bytes = stq::q8_matmul_scratch_bytes(m, n, k, n_cus > 0 ? n_cus : stq::cus_of_current_device());
+  return ok();
+}
+
+stq_status stq_q8_matmul(const int8_t* a, int64_t a_row_stride, const float* a_scale, const int8_t* w,
+                         int64_t w_row_stride, const float* w_scale, int64_t m, int64_t n, int64_t k, void* y,
+                         int y_dtype, int64_t y_row_stride, void* workspace, int64_t workspace_bytes,
+                         stq_stream_t stream) {
+  const char* who = "stq_q8_matmul";
+  stq_status st = q8_shape_check(m, n, k, who);
+  if (st != STQ_OK) return st;
+  if (y_dtype != STQ_X_F32 && y_dtype != STQ_X_BF16) return fail(STQ_E_ARG, "%s: unknown y_dtype %d", who, y_dtype);
+  const int64_t kp = (k + 15) / 16 * 16;
+  if (a_row_stride < kp || w_row_stride < kp) return fail(STQ_E_SHAPE, "%s: row stride of a or w < k rounded up to 16", who);
+  if (a_row_stride > kMaxStride8 || w_row_stride > kMaxStride8) return fail(STQ_E_SHAPE, "%s: row stride of a or w above 2^23", who);
+  if (m > 1 && y_row_stride < n) return fail(STQ_E_SHAPE, "%s: y_row_stride < n", who);
+  if (workspace_bytes < 0) return fail(STQ_E_ARG, "%s: workspace_bytes < 0", who);
+  if (m == 0 || n == 0) return ok();
+  if (!a || !a_scale || !w || !w_scale || !y) return fail(STQ_E_ARG, "%s: null pointer", who);
+  const int esz = y_dtype == STQ_X_BF16 ? 2 : 4;
+  if (!fits(m, y_row_stride, esz)) return fail(STQ_E_SHAPE, "%s: y_row_stride too large", who);
+  if (!aligned(a, 16) || !aligned(w, 16) || a_row_stride % 16 || w_row_stride % 16)
+    return fail(STQ_E_ALIGN, "%s: a, w or their row strides not 16-byte aligned", who);
+  if (!aligned(a_scale, 4) || !aligned(w_scale, 4) || !aligned(y, esz)) return fail(STQ_E_ALIGN, "%s: scales or y not aligned to their elements", who);
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const int cus = stq::cus_of_stream(s);
+  st = check_workspace(workspace, workspace_bytes, stq::q8_matmul_scratch_bytes(m, n, k, cus), who);
+  if (st != STQ_OK) return st;
+  const stq::Q8MatmulArgs g{a, a_row_stride, a_scale, w, w_row_stride, w_scale, m, n, k, y,
+                            y_dtype == STQ_X_BF16 ? 1 : 0, y_row_stride, cus};
+  hipError_t e = stq::launch_q8_matmul(g, workspace, s);
+  if (e != hipSuccess) return hip_fail(e, "stq_q8_matmul launch");
+  return ok();
+}
+
+namespace {
+
+stq_status logprobs_shape_check(int x_dtype, int64_t n_rows, int64_t vocab, const char* who) {
+  if (x_dtype != STQ_X_F32 && x_dtype != STQ_X_BF16) return fail(STQ_E_ARG, "%s: unknown x_dtype %d", who, x_dtype);
+  if (n_rows < 0) return fail(STQ_E_ARG, "%s: n_rows < 0", who);
+  if (vocab < 1 || vocab > INT_MAX - 64) return fail(STQ_E_SHAPE, "%s: vocab=%lld outside 1..2^31-65", who, (long long)vocab);
+  if (n_rows > (int64_t{1} << 22)) return fail(STQ_E_SHAPE, "%s: more than 2^22 rows in one call", who);
+  return STQ_OK;
+}
+
+stq_status top_check(int64_t top_n, int64_t vocab, const char* who) {
+  if (top_n < 0) return fail(STQ_E_ARG, "%s: top_n < 0", who);
+  if (top_n > 32 || top_n > vocab) return fail(STQ_E_SHAPE, "%s: top_n=%lld above 32 or the vocabulary", who, (long long)top_n);
+  return STQ_OK;
+}
+
+}  // namespace
+
+stq_status stq_token_logprobs_workspace(int x_dtype, int64_t n_rows, int64_t vocab, int64_t top_n, int32_t n_cus,
+                                        int64_t* workspace_bytes) {
+  const char* who = "stq_token_logprobs_workspace";
+  if (!workspace_bytes) return fail(STQ_E_ARG, "%s: null output pointer", who);
+  *workspace_bytes = 0;
+  if (n_cus < 0) return fail(STQ_E_ARG, "%s: n_cus < 0", who);
+  stq_status st = logprobs_shape_check(x_dtype, n_rows, vocab, who);
+  if (st == STQ_OK) st = top_check(top_n, vocab, who);
+  if (st != STQ_OK) return st;
+  if (n_rows > 0)
+    *workspace_bytes = stq::plan_logprobs(n_rows, vocab, x_dtype == STQ_X_BF16 ? 2 : 4, static_cast<int>(top_n),
+                                          n_cus > 0 ? n_cus : stq::cus_of_current_device()).bytes;
+  return ok();
+}
+
+stq_status stq_token_logprobs(const void* logits, int x_dtype, int64_t row_stride, int64_t n_rows, int64_t vocab,
+                              const int32_t* targets, float* logprob, float* lse, float* entropy, int64_t top_n,
+                              int32_t* top_ids, float* top_logprobs, void* workspace, int64_t workspace_bytes,
+                              stq_stream_t stream) {
+  const char* who = "stq_token_logprobs";
+  stq_status st = logprobs_shape_check(x_dtype, n_rows, vocab, who);
+  if (st == STQ_OK) st = top_check(top_n, vocab, who);
+  if (st != STQ_OK) return st;
+  if (n_rows > 1 && row_stride < vocab) return fail(STQ_E_SHAPE, "%s: row_stride < vocab", who);
+  if (workspace_bytes < 0) return fail(STQ_E_ARG, "%s: workspace_bytes < 0", who);
+  if (n_rows == 0) return ok();
+  if (!logits || !targets || !logprob) return fail(STQ_E_ARG, "%s: null pointer", who);
+  if (top_n > 0 && (!top_ids || !top_logprobs)) return fail(STQ_E_ARG, "%s: null top outputs", who);
+  const int esz = x_dtype == STQ_X_BF16 ? 2 : 4;
+  if (!fits(n_rows, row_stride, esz)) return fail(STQ_E_SHAPE, "%s: row_stride too large", who);
+  if (!aligned(logits, esz)) return fail(STQ_E_ALIGN, "%s: logits not aligned to their elements", who);
+  if (!aligned(targets, 4) || !aligned(logprob, 4) || !aligned(lse, 4) || !aligned(entropy, 4) ||
+      !aligned(top_ids, 4) || !aligned(top_logprobs, 4))
+    return fail(STQ_E_ALIGN, "%s: targets or outputs not 4-byte aligned", who);
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const stq::LogprobsPlan pl = stq::plan_logprobs(n_rows, vocab, esz, static_cast<int>(top_n), stq::cus_of_stream(s));
+  st = check_workspace(workspace, workspace_bytes, pl.bytes, who);
+  if (st != STQ_OK) return st;
+  const stq::LogprobsArgs a{logits, x_dtype == STQ_X_BF16 ? 1 : 0, row_stride, n_rows, vocab, targets, logprob, lse,
+                            entropy, top_ids, top_logprobs, static_cast<int>(top_n)};
+  hipError_t e = stq::launch_logprobs(a, pl, workspace, s);
+  if (e != hipSuccess) return hip_fail(e, "stq_token_logprobs launch");
+  return ok();
+}
+
+stq_status stq_token_logprobs_backward(const void* logits, int x_dtype, int64_t row_stride, int64_t n_rows,
+                                       int64_t vocab, const int32_t* targets, const float* lse, const float* entropy,
+                                       const float* grad_logprob, const float* grad_entropy, void* d_logits,
+                                       int64_t d_row_stride, stq_stream_t stream) {
+  const char* who = "stq_token_logprobs_backward";
+  const stq_status st = logprobs_shape_check(x_dtype, n_rows, vocab, who);
+  if (st != STQ_OK) return st;
+  if (n_rows > 1 && (row_stride < vocab || d_row_stride < vocab)) return fail(STQ_E_SHAPE, "%s: row stride < vocab", who);
+  if (n_rows == 0) return ok();
+  if (!logits || !targets || !lse || !d_logits) return fail(STQ_E_ARG, "%s: null pointer", who);
+  if (grad_entropy && !entropy) return fail(STQ_E_ARG, "%s: grad_entropy needs entropy", who);
+  const int esz = x_dtype == STQ_X_BF16 ? 2 : 4;
+  if (!fits(n_rows, row_stride, esz) || !fits(n_rows, d_row_stride, esz)) return fail(STQ_E_SHAPE, "%s: row stride too large", who);
+  if (logits == d_logits && n_rows > 1 && row_stride != d_row_stride)
+    return fail(STQ_E_ARG, "%s: in place needs equal row strides", who);
+  if (n_rows * stq::logprobs_bwd_parts(vocab, esz) > (int64_t{1} << 23))
+    return fail(STQ_E_SHAPE, "%s: too many rows of this vocabulary for one call", who);
+  if (!aligned(logits, esz) || !aligned(d_logits, esz)) return fail(STQ_E_ALIGN, "%s: logits or d_logits not aligned to their elements", who);
+  if (!aligned(targets, 4) || !aligned(lse, 4) || !aligned(entropy, 4) || !aligned(grad_logprob, 4) || !aligned(grad_entropy, 4))
+    return fail(STQ_E_ALIGN, "%s: targets, lse, entropy or gradients not 4-byte aligned", who);
+  const stq::LogprobsBwdArgs a{logits, x_dtype == STQ_X_BF16 ? 1 : 0, row_stride, n_rows, vocab, targets, lse, entropy,
+                               grad_logprob, grad_entropy, d_logits, d_row_stride};
+  hipError_t e = stq::launch_logprobs_bwd(a, reinterpret_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "stq_token_logprobs_backward launch");
+  return ok();
+}
+
 stq_status stq_stream_read_probe(const void* buf, int64_t bytes, uint32_t* sink, stq_stream_t stream) {
   if (bytes < 0 || bytes % 16) return fail(STQ_E_ARG, "stq_stream_read_probe: bytes must be a non-negative multiple of 16");
   if (bytes == 0) return ok();

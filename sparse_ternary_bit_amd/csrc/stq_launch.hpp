@@ -99,6 +99,74 @@ hipError_t launch_layer_errors(const float* w, const float* w_hat, int64_t n_row
 // 2-bit stand-in format: quantize and reconstruct in one pass
 hipError_t launch_q2_roundtrip(const float* w, int64_t n_rows, int64_t k, float* out, hipStream_t s);
 
+// 8-bit rows with one scale each, and their product
+struct Q8QuantArgs {
+  const void* x;
+  int bf16;           // 0 fp32, 1 bf16
+  int64_t x_stride;   // elements
+  int64_t rows, k;
+  int8_t* q;
+  int64_t ldq;        // bytes
+  float* scale;
+};
+hipError_t launch_q8_quantize(const Q8QuantArgs& a, hipStream_t s);
+
+struct Q8MatmulArgs {
+  const int8_t* a;
+  int64_t lda;
+  const float* a_scale;
+  const int8_t* w;
+  int64_t ldw;
+  const float* w_scale;
+  int64_t m, n, k;
+  void* y;
+  int bf16;
+  int64_t ldy;
+  int cus;            // compute units to plan for
+};
+// `ws` holds q8_matmul_scratch_bytes(...) bytes for the same shape and CU count
+int64_t q8_matmul_scratch_bytes(int64_t m, int64_t n, int64_t k, int cus);
+hipError_t launch_q8_matmul(const Q8MatmulArgs& a, void* ws, hipStream_t s);
+
+// Token log probabilities, entropy and top alternatives of rows of logits
+struct LogprobsArgs {
+  const void* logits;
+  int bf16;
+  int64_t stride;     // elements
+  int64_t rows, vocab;
+  const int32_t* targets;
+  float* logprob;
+  float* lse;         // may be NULL
+  float* entropy;     // may be NULL
+  int32_t* top_ids;
+  float* top_lp;
+  int top_n;
+};
+struct LogprobsPlan {
+  int splits;           // workgroups a row is cut into
+  int64_t per;          // 16-byte chunks per split
+  int64_t stats_bytes;  // offset of the splits' keys in the workspace
+  int64_t bytes;        // workspace bytes (0: one workgroup a row)
+};
+LogprobsPlan plan_logprobs(int64_t rows, int64_t vocab, int elem_bytes, int top_n, int cus);
+hipError_t launch_logprobs(const LogprobsArgs& a, const LogprobsPlan& plan, void* ws, hipStream_t s);
+
+struct LogprobsBwdArgs {
+  const void* logits;
+  int bf16;
+  int64_t stride;
+  int64_t rows, vocab;
+  const int32_t* targets;
+  const float* lse;
+  const float* entropy;  // read with g_ent only
+  const float* g_lp;     // may be NULL
+  const float* g_ent;    // may be NULL
+  void* out;
+  int64_t out_stride;
+};
+int64_t logprobs_bwd_parts(int64_t vocab, int elem_bytes);  // workgroups per row
+hipError_t launch_logprobs_bwd(const LogprobsBwdArgs& a, hipStream_t s);
+
 // Streaming-read reference (measurement only): reads `bytes` bytes of `buf`
 hipError_t launch_stream_read(const void* buf, int64_t bytes, uint32_t* sink, hipStream_t s);
 

@@ -1,0 +1,174 @@
+"""Host-side checks of the 8-bit product and the token scoring entry points:
+bad arguments are refused with a status and a message before any GPU call,
+empty work is fine without one, and the workspace queries agree with the
+calls.  No kernel runs."""
+import ctypes
+import os
+
+import pytest
+
+FAKE = 0x100000  # never dereferenced: every call below fails validation first
+
+
+@pytest.fixture(scope="module")
+def L():
+    import sparse_ternary_bit_amd as stq
+    if not os.path.exists(stq.lib_path()):
+        from sparse_ternary_bit_amd import build
+        build.build(verbose=False)
+    return stq.lib()
+
+
+def _err(L):
+    return L.stq_last_error().decode()
+
+
+def _quant(L, **kw):
+    a = dict(x=FAKE, xd=1, xs=100, n=4, k=100, q=FAKE, qs=112, sc=FAKE)
+    a.update(kw)
+    return L.stq_q8_quantize_rows(a["x"], a["xd"], a["xs"], a["n"], a["k"], a["q"], a["qs"], a["sc"], None)
+
+
+@pytest.mark.parametrize("kw, status", [
+    (dict(n=-1), 1), (dict(k=0), 2), (dict(k=-3), 2), (dict(xd=2), 1), (dict(xs=99), 2), (dict(qs=96), 2),
+    (dict(qs=120), 3), (dict(q=FAKE + 8), 3), (dict(x=FAKE + 1), 3), (dict(xd=0, x=FAKE + 2), 3),
+    (dict(sc=FAKE + 2), 3), (dict(x=None), 1), (dict(q=None), 1), (dict(sc=None), 1), (dict(n=(1 << 23) + 1), 2),
+    (dict(xs=1 << 62), 2), (dict(k=1 << 31, xs=1 << 31, qs=1 << 31), 2),
+])
+def test_quantize_refusals(L, kw, status):
+    assert _quant(L, **kw) == status
+    assert _err(L).startswith("stq_q8_quantize_rows")
+
+
+def test_quantize_nothing_to_do(L):
+    assert _quant(L, n=0, x=None, q=None, sc=None) == 0
+
+
+def _mm(L, **kw):
+    a = dict(a=FAKE, lda=112, as_=FAKE, w=FAKE, ldw=112, ws=FAKE, m=128, n=64, k=100, y=FAKE, yd=1, ldy=64,
+             wk=FAKE, wkb=1 << 40)
+    a.update(kw)
+    return L.stq_q8_matmul(a["a"], a["lda"], a["as_"], a["w"], a["ldw"], a["ws"], a["m"], a["n"], a["k"], a["y"],
+                           a["yd"], a["ldy"], a["wk"], a["wkb"], None)
+
+
+@pytest.mark.parametrize("kw, status", [
+    (dict(m=-1), 1), (dict(n=-1), 1), (dict(k=0), 2), (dict(k=131072, lda=131072, ldw=131072), 2), (dict(yd=3), 1),
+    (dict(lda=96), 2), (dict(ldw=96), 2), (dict(lda=120), 3), (dict(ldw=120), 3), (dict(lda=(1 << 23) + 16), 2),
+    (dict(ldw=(1 << 23) + 16), 2), (dict(ldy=63), 2), (dict(a=None), 1), (dict(as_=None), 1), (dict(w=None), 1),
+    (dict(ws=None), 1), (dict(y=None), 1), (dict(a=FAKE + 8), 3), (dict(w=FAKE + 8), 3), (dict(as_=FAKE + 2), 3),
+    (dict(ws=FAKE + 2), 3), (dict(y=FAKE + 1), 3), (dict(yd=0, y=FAKE + 2), 3), (dict(m=(1 << 22) + 1), 2),
+    (dict(n=1 << 31, ldy=1 << 31), 2), (dict(ldy=1 << 62), 2), (dict(wkb=-1), 1),
+])
+def test_matmul_refusals(L, kw, status):
+    assert _mm(L, **kw) == status
+    assert _err(L).startswith("stq_q8_matmul")
+
+
+def test_matmul_nothing_to_do(L):
+    none = dict(a=None, as_=None, w=None, ws=None, y=None, wk=None, wkb=0)
+    assert _mm(L, m=0, **none) == 0
+    assert _mm(L, n=0, **none) == 0
+
+
+def test_matmul_workspace_query(L):
+    wb = ctypes.c_int64(-7)
+    f = L.stq_q8_matmul_workspace
+    assert f(0, 4096, 7168, 256, ctypes.byref(wb)) == 0 and wb.value == 0
+    assert f(4, 0, 7168, 256, ctypes.byref(wb)) == 0 and wb.value == 0
+    assert f(-1, 4, 4, 256, ctypes.byref(wb)) == 1
+    assert f(4, 4, 0, 256, ctypes.byref(wb)) == 2
+    assert f(4, 4, 4, -1, ctypes.byref(wb)) == 1
+    assert f(4, 4, 4, 256, None) == 1
+    for m, n, k in ((1, 4096, 7168), (16, 4096, 7168), (64, 512, 7168), (65, 300, 5000), (2048, 256, 16)):
+        assert f(m, n, k, 256, ctypes.byref(wb)) == 0 and wb.value >= 0
+        if wb.value:
+            args = dict(m=m, n=n, k=k, lda=(k + 15) // 16 * 16, ldw=(k + 15) // 16 * 16, ldy=n)
+            wb2 = ctypes.c_int64()
+            assert f(m, n, k, 0, ctypes.byref(wb2)) == 0     # what the call itself plans for here
+            if wb2.value:
+                assert _mm(L, wk=None, wkb=0, **args) == 1 and "workspace" in _err(L)
+                assert _mm(L, wk=FAKE, wkb=wb2.value - 1, **args) == 1
+                assert _mm(L, wk=FAKE + 16, wkb=wb2.value, **args) == 3
+
+
+def _lp(L, **kw):
+    a = dict(x=FAKE, xd=1, xs=1000, n=4, v=1000, t=FAKE, lp=FAKE, lse=FAKE, ent=FAKE, top=5, ids=FAKE, tlp=FAKE,
+             ws=FAKE, wsb=1 << 40)
+    a.update(kw)
+    return L.stq_token_logprobs(a["x"], a["xd"], a["xs"], a["n"], a["v"], a["t"], a["lp"], a["lse"], a["ent"],
+                                a["top"], a["ids"], a["tlp"], a["ws"], a["wsb"], None)
+
+
+@pytest.mark.parametrize("kw, status", [
+    (dict(xd=7), 1), (dict(n=-1), 1), (dict(v=0), 2), (dict(v=1 << 31, xs=1 << 31), 2), (dict(n=(1 << 22) + 1), 2),
+    (dict(top=-1), 1), (dict(top=33), 2), (dict(v=4, top=5), 2), (dict(xs=999), 2), (dict(wsb=-1), 1),
+    (dict(x=None), 1), (dict(t=None), 1), (dict(lp=None), 1), (dict(ids=None), 1), (dict(tlp=None), 1),
+    (dict(xs=1 << 62), 2), (dict(x=FAKE + 1), 3), (dict(xd=0, x=FAKE + 2), 3), (dict(t=FAKE + 2), 3),
+    (dict(lp=FAKE + 2), 3), (dict(lse=FAKE + 2), 3), (dict(ent=FAKE + 2), 3), (dict(ids=FAKE + 2), 3),
+    (dict(tlp=FAKE + 2), 3),
+])
+def test_logprobs_refusals(L, kw, status):
+    assert _lp(L, **kw) == status
+    assert _err(L).startswith("stq_token_logprobs")
+
+
+def test_logprobs_nothing_to_do(L):
+    assert _lp(L, n=0, x=None, t=None, lp=None, lse=None, ent=None, ids=None, tlp=None, ws=None, wsb=0) == 0
+
+
+def test_logprobs_workspace_query_and_refusal(L):
+    wb = ctypes.c_int64(-7)
+    f = L.stq_token_logprobs_workspace
+    assert f(1, 0, 1000, 5, 256, ctypes.byref(wb)) == 0 and wb.value == 0
+    assert f(1, 4096, 131072, 5, 256, ctypes.byref(wb)) == 0 and wb.value == 0      # enough rows to fill the chip
+    assert f(0, 1, 131072, 20, 256, ctypes.byref(wb)) == 0 and wb.value > 0          # one row is split
+    assert f(5, 1, 1000, 5, 256, ctypes.byref(wb)) == 1
+    assert f(1, 1, 1000, 33, 256, ctypes.byref(wb)) == 2
+    assert f(1, 1, 1000, 5, -2, ctypes.byref(wb)) == 1
+    assert f(1, 1, 1000, 5, 256, None) == 1
+    assert f(0, 1, 131072, 20, 0, ctypes.byref(wb)) == 0
+    need = wb.value
+    big = dict(xd=0, n=1, v=131072, xs=131072, top=20)
+    assert _lp(L, ws=None, wsb=0, **big) == 1 and "workspace" in _err(L)
+    assert _lp(L, ws=FAKE, wsb=need - 1, **big) == 1
+    assert _lp(L, ws=FAKE + 16, wsb=need, **big) == 3
+
+
+def _bw(L, **kw):
+    a = dict(x=FAKE, xd=1, xs=1000, n=4, v=1000, t=FAKE, lse=FAKE, ent=FAKE, g=FAKE, ge=FAKE, d=2 * FAKE, ds=1000)
+    a.update(kw)
+    return L.stq_token_logprobs_backward(a["x"], a["xd"], a["xs"], a["n"], a["v"], a["t"], a["lse"], a["ent"],
+                                         a["g"], a["ge"], a["d"], a["ds"], None)
+
+
+@pytest.mark.parametrize("kw, status", [
+    (dict(xd=7), 1), (dict(n=-1), 1), (dict(v=0), 2), (dict(n=(1 << 22) + 1), 2), (dict(xs=999), 2), (dict(ds=999), 2),
+    (dict(x=None), 1), (dict(t=None), 1), (dict(lse=None), 1), (dict(d=None), 1), (dict(ent=None), 1),
+    (dict(d=FAKE, ds=1008), 1), (dict(x=FAKE + 1), 3), (dict(d=2 * FAKE + 1), 3), (dict(t=FAKE + 2), 3),
+    (dict(lse=FAKE + 2), 3), (dict(ent=FAKE + 2), 3), (dict(g=FAKE + 2), 3), (dict(ge=FAKE + 2), 3),
+    (dict(ds=1 << 62), 2), (dict(n=1 << 22, v=1 << 20, xs=1 << 20, ds=1 << 20), 2),
+])
+def test_logprobs_backward_refusals(L, kw, status):
+    assert _bw(L, **kw) == status
+    assert _err(L).startswith("stq_token_logprobs_backward")
+
+
+def test_logprobs_backward_nothing_to_do(L):
+    assert _bw(L, n=0, x=None, t=None, lse=None, ent=None, g=None, ge=None, d=None) == 0
+
+
+def test_binding_refuses_cpu_tensors_and_wrong_shapes():
+    import torch
+    import sparse_ternary_bit_amd as stq
+    x = torch.zeros(2, 32)
+    i = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="GPU"):
+        stq.q8_quantize_rows(x)
+    with pytest.raises(ValueError, match="GPU"):
+        stq.token_logprobs(x, i)
+    with pytest.raises(ValueError, match="GPU"):
+        stq.token_logprobs_backward(x, i, x[:, 0], None, x[:, 0])
+    q = torch.zeros(2, 32, dtype=torch.int8)
+    with pytest.raises(ValueError, match="GPU"):
+        stq.q8_matmul(q, x[:, 0], q, x[:, 0])
