@@ -304,6 +304,58 @@ stq_status stq_q2_roundtrip(const float* w, int64_t n_rows, int64_t k, float* ou
 stq_status stq_greedy_allocation(const double* gain, const double* extra_bytes, int64_t n_layers,
                                  double budget, uint8_t* chosen);
 
+/* Gated feed-forward of the prefill path: the gate and up products of every
+ * token with its expert, the activation and their product in one pass, for
+ * rows grouped by expert as in stq_grouped_gemm (same source passages):
+ *     g, u = rows [0, d_ff) and [d_ff, 2*d_ff) of W_e x_r
+ *     h[r] = silu(g) * u,          silu(v) = v / (1 + exp(-v))
+ *   w_gate_up, gate_up_stride_bytes   the experts' packed [2*d_ff, d_model]
+ *                   matrices (gate rows, then up rows) as in
+ *                   stq_moe_ffn_decode: 16-byte aligned, stride a multiple of
+ *                   16, d_model and d_ff multiples of 256
+ *   x_sorted        [total_m, d_model] bf16 bits, row-major, 16-byte aligned
+ *   expert_offsets  DEVICE int32 [n_experts+1] as in stq_grouped_gemm,
+ *                   clamped the same way: rows in no range stay unwritten
+ *   h               bf16 [total_m, d_ff], the down projection's input of
+ *                   stq_grouped_gemm; 8-byte aligned
+ *   gate_up         bf16 [total_m, 2*d_ff] = [g | u], what the backward pass
+ *                   reads, or NULL; 8-byte aligned
+ * bf16 x ternary products are exact, sums fp32, and h and gate_up are each
+ * rounded from the fp32 sums once.  d_ff * row_bytes(d_model) is below 2^31. */
+stq_status stq_grouped_swiglu(const uint8_t* w_gate_up, int64_t gate_up_stride_bytes, int64_t n_experts,
+                              int64_t d_model, int64_t d_ff, const uint16_t* x_sorted, const int32_t* expert_offsets,
+                              int64_t total_m, uint16_t* h, uint16_t* gate_up, stq_stream_t stream);
+
+/* Its gradients: with s = 1 / (1 + exp(-g)) and dh the gradient at h,
+ *     dg = dh u s (1 + g (1 - s)),   du = dh g s,   dz = [dg | du]
+ *     dx[r] = dz_r W_e                 (through the decoded, frozen weights)
+ *     dw[e] = sum over e's rows of dz_r^T x_r   (the gradient with respect to
+ *             the decoded weights, e.g. for the weights behind an encoder)
+ *   gate_up   bf16 [total_m, 2*d_ff], from the forward call; 16-byte aligned
+ *   dh        bf16 [total_m, d_ff]; 16-byte aligned
+ *   dx        bf16 [total_m, d_model] or NULL (not wanted); 8-byte aligned;
+ *             rows in no range stay unwritten
+ *   dw        bf16 [n_experts, 2*d_ff, d_model] or NULL; 8-byte aligned; every
+ *             element is written (zeros for an expert without rows)
+ *   w_gate_up is read for dx only and x_sorted for dw only; either may be
+ *   NULL otherwise.  The other arguments are as for stq_grouped_swiglu.
+ *   workspace, workspace_bytes   at least what
+ *             stq_grouped_swiglu_backward_workspace reports
+ * dz is formed in fp32 and rounded once for each product: to fp16 after a
+ * power-of-two scaling of each row (the decoded weights are fp16 numbers, so
+ * they enter exactly) for dx, to bf16 for dw.  Sums are fp32 in a fixed
+ * order; dx and dw are rounded from them once.  total_m is at most 2^23. */
+stq_status stq_grouped_swiglu_backward(const uint8_t* w_gate_up, int64_t gate_up_stride_bytes, int64_t n_experts,
+                                       int64_t d_model, int64_t d_ff, const uint16_t* x_sorted,
+                                       const int32_t* expert_offsets, int64_t total_m, const uint16_t* gate_up,
+                                       const uint16_t* dh, uint16_t* dx, uint16_t* dw, void* workspace,
+                                       int64_t workspace_bytes, stq_stream_t stream);
+
+/* Workspace bytes stq_grouped_swiglu_backward needs for these shapes and the
+ * outputs wanted (0 or 1 each); host only.  workspace_bytes is a HOST pointer. */
+stq_status stq_grouped_swiglu_backward_workspace(int64_t n_experts, int64_t d_model, int64_t d_ff, int64_t total_m,
+                                                 int want_dx, int want_dw, int64_t* workspace_bytes);
+
 /* Rows of 8-bit integers with one fp32 scale each, the form in which a model
  * keeps what its allocation leaves above the ternary format (attention
  * projections, the output head; lemmy post 66506, paragraph "Precision

@@ -17,7 +17,8 @@ __all__ = [
     "QK", "BLOCK_BYTES", "ENC_WLS", "ENC_AMAX", "StqError", "lib", "lib_path",
     "row_bytes", "quantize_rows", "dequantize_rows", "gemv", "gemv_noalloc", "gemv_plan", "grouped_gemm",
     "moe_ffn_decode",
-    "moe_ffn_workspace", "q8_quantize_rows", "q8_matmul", "q8_matmul_workspace", "token_logprobs",
+    "moe_ffn_workspace", "grouped_swiglu", "grouped_swiglu_backward", "grouped_swiglu_backward_workspace",
+    "q8_quantize_rows", "q8_matmul", "q8_matmul_workspace", "token_logprobs",
     "token_logprobs_workspace", "token_logprobs_backward", "layer_errors", "layer_errors_workspace", "q2_roundtrip", "greedy_allocation",
     "stream_read_probe", "mfma_loop_probe", "lds_read_probe", "MFMA_PROBE_FLOP_PER_ROUND",
     "LDS_PROBE_READS_PER_ROUND",
@@ -96,6 +97,15 @@ def lib() -> ctypes.CDLL:
     L.stq_q2_roundtrip.restype = _c_int
     L.stq_greedy_allocation.argtypes = [_c_vp, _c_vp, _c_i64, ctypes.c_double, _c_vp]
     L.stq_greedy_allocation.restype = _c_int
+    L.stq_grouped_swiglu.argtypes = [_c_vp, _c_i64, _c_i64, _c_i64, _c_i64, _c_vp, _c_vp, _c_i64, _c_vp, _c_vp,
+                                     _c_vp]
+    L.stq_grouped_swiglu.restype = _c_int
+    L.stq_grouped_swiglu_backward.argtypes = [_c_vp, _c_i64, _c_i64, _c_i64, _c_i64, _c_vp, _c_vp, _c_i64, _c_vp,
+                                              _c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_vp]
+    L.stq_grouped_swiglu_backward.restype = _c_int
+    L.stq_grouped_swiglu_backward_workspace.argtypes = [_c_i64, _c_i64, _c_i64, _c_i64, _c_int, _c_int,
+                                                        ctypes.POINTER(_c_i64)]
+    L.stq_grouped_swiglu_backward_workspace.restype = _c_int
     L.stq_q8_quantize_rows.argtypes = [_c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64, _c_vp, _c_vp]
     L.stq_q8_quantize_rows.restype = _c_int
     L.stq_q8_matmul.argtypes = [_c_vp, _c_i64, _c_vp, _c_vp, _c_i64, _c_vp, _c_i64, _c_i64, _c_i64, _c_vp, _c_int,
@@ -416,6 +426,89 @@ def moe_ffn_decode(w_gate_up: torch.Tensor, gate_up_stride: int, w_down: torch.T
                                     pair_expert.data_ptr(), pair_weight.data_ptr(), int(top_k), out.data_ptr(),
                                     *_ws_args(workspace), _stream()))
     return out
+
+
+def _matrix(name: str, t: torch.Tensor, dtype: torch.dtype, rows: int, cols: int) -> None:
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2 or tuple(t.shape) != (rows, cols) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous [{rows}, {cols}], got {tuple(t.shape)}")
+
+
+def _swiglu_args(w_gate_up, expert_stride, n_experts, d_model, d_ff, x_sorted, offsets) -> int:
+    """Checks shared by the gated feed-forward and its gradients; returns the number of rows."""
+    if w_gate_up.dtype != torch.uint8 or not w_gate_up.is_contiguous():
+        raise ValueError("w_gate_up must be contiguous torch.uint8")
+    _vector("offsets", offsets, torch.int32, int(n_experts) + 1)
+    if x_sorted.dim() != 2:
+        raise ValueError("x_sorted must be [total_m, d_model]")
+    total_m = x_sorted.shape[0]
+    _matrix("x_sorted", x_sorted, torch.bfloat16, total_m, int(d_model))
+    if total_m > 0:
+        _table("w_gate_up", w_gate_up, n_experts, expert_stride, 2 * int(d_ff), d_model)
+    return total_m
+
+
+def grouped_swiglu(w_gate_up: torch.Tensor, expert_stride: int, n_experts: int, d_model: int, d_ff: int,
+                   x_sorted: torch.Tensor, offsets: torch.Tensor, out: torch.Tensor | None = None,
+                   gate_up: torch.Tensor | None = None) -> torch.Tensor:
+    """h = silu(W_gate_e x) * (W_up_e x), bf16 [total_m, d_ff], for rows x_sorted bf16 [total_m, d_model]
+    grouped by expert (offsets as in grouped_gemm) and packed [2*d_ff, d_model] experts.  `gate_up`
+    (bf16 [total_m, 2*d_ff]) receives the pre-activations that grouped_swiglu_backward reads."""
+    dev = _together(w_gate_up=w_gate_up, x_sorted=x_sorted, offsets=offsets, out=out, gate_up=gate_up)
+    total_m = _swiglu_args(w_gate_up, expert_stride, n_experts, d_model, d_ff, x_sorted, offsets)
+    if out is None:
+        out = torch.empty((total_m, int(d_ff)), dtype=torch.bfloat16, device=dev)
+    _matrix("out", out, torch.bfloat16, total_m, int(d_ff))
+    if gate_up is not None:
+        _matrix("gate_up", gate_up, torch.bfloat16, total_m, 2 * int(d_ff))
+    _call(dev, "stq_grouped_swiglu", w_gate_up.data_ptr(), int(expert_stride), int(n_experts), int(d_model), int(d_ff),
+          x_sorted.data_ptr(), offsets.data_ptr(), total_m, out.data_ptr(), _ptr(gate_up))
+    return out
+
+
+def grouped_swiglu_backward_workspace(n_experts: int, d_model: int, d_ff: int, total_m: int, need_dx: bool = True,
+                                      need_dw: bool = True) -> int:
+    """Workspace bytes grouped_swiglu_backward needs for these shapes (host only)."""
+    wb = ctypes.c_int64()
+    _check("stq_grouped_swiglu_backward_workspace",
+           lib().stq_grouped_swiglu_backward_workspace(int(n_experts), int(d_model), int(d_ff), int(total_m),
+                                                       int(bool(need_dx)), int(bool(need_dw)), ctypes.byref(wb)))
+    return wb.value
+
+
+def grouped_swiglu_backward(w_gate_up: torch.Tensor, expert_stride: int, n_experts: int, d_model: int, d_ff: int,
+                            x_sorted: torch.Tensor, offsets: torch.Tensor, gate_up: torch.Tensor, dh: torch.Tensor,
+                            need_dx: bool = True, need_dw: bool = True, dx: torch.Tensor | None = None,
+                            dw: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """(dx, dw) of grouped_swiglu for the gradient dh bf16 [total_m, d_ff] at h and the gate_up it saved:
+    dx bf16 [total_m, d_model] through the decoded weights, dw bf16 [n_experts, 2*d_ff, d_model] the
+    gradient of the decoded weights; None for the one not needed.  `workspace` (GPU bytes, at least
+    grouped_swiglu_backward_workspace(...)) is allocated here when not given."""
+    dev = _together(w_gate_up=w_gate_up, x_sorted=x_sorted, offsets=offsets, gate_up=gate_up, dh=dh, dx=dx, dw=dw,
+                    workspace=workspace)
+    total_m = _swiglu_args(w_gate_up, expert_stride, n_experts, d_model, d_ff, x_sorted, offsets)
+    E, d, f = int(n_experts), int(d_model), int(d_ff)
+    _matrix("gate_up", gate_up, torch.bfloat16, total_m, 2 * f)
+    _matrix("dh", dh, torch.bfloat16, total_m, f)
+    if need_dx:
+        dx = torch.empty((total_m, d), dtype=torch.bfloat16, device=dev) if dx is None else dx
+        _matrix("dx", dx, torch.bfloat16, total_m, d)
+    elif dx is not None:
+        raise ValueError("dx is given but need_dx is False")
+    if need_dw:
+        dw = torch.empty((E, 2 * f, d), dtype=torch.bfloat16, device=dev) if dw is None else dw
+        if dw.dtype != torch.bfloat16 or tuple(dw.shape) != (E, 2 * f, d) or not dw.is_contiguous():
+            raise ValueError(f"dw must be contiguous bfloat16 [{E}, {2 * f}, {d}]")
+    elif dw is not None:
+        raise ValueError("dw is given but need_dw is False")
+    if workspace is None:
+        workspace = _workspace(None, grouped_swiglu_backward_workspace(E, d, f, total_m, need_dx, need_dw), dev)
+    else:
+        workspace = _workspace(workspace, 0, dev)
+    _call(dev, "stq_grouped_swiglu_backward", w_gate_up.data_ptr(), int(expert_stride), E, d, f, x_sorted.data_ptr(),
+          offsets.data_ptr(), total_m, gate_up.data_ptr(), dh.data_ptr(), _ptr(dx), _ptr(dw), *_ws_args(workspace))
+    return dx, dw
 
 
 def _q8_stride(name: str, t: torch.Tensor) -> int:

@@ -50,6 +50,13 @@ namespace {
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+
+// two fp32 values as bf16, round to nearest even, the first in the low half
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  return static_cast<uint32_t>(__builtin_bit_cast(uint16_t, static_cast<__bf16>(a))) |
+         static_cast<uint32_t>(__builtin_bit_cast(uint16_t, static_cast<__bf16>(b))) << 16;
+}
 
 constexpr int kWaves = 4;
 constexpr int kThreads = kWaves * 64;
@@ -74,6 +81,10 @@ struct GArgs {
   float* y;
   int nslab;
   int vec4;  // n % 4 == 0: outputs stored 16 bytes at a time
+  // gated form only
+  int d_ff;       // gate rows [0, d_ff), up rows [d_ff, 2 d_ff)
+  uint16_t* h;    // [total_m, d_ff] bf16
+  uint16_t* gu;   // [total_m, 2 d_ff] bf16, or NULL
 };
 
 struct Smem {
@@ -110,7 +121,7 @@ __device__ __forceinline__ int pass_tid() {
   return t;
 }
 
-template <int NT>
+template <int NT, bool kGated>
 __device__ __forceinline__ void run_pass(const GArgs& a, Smem& sh, const uint8_t* wexp, int slab, int64_t row0,
                                          int mt) {
   const int tid = pass_tid();
@@ -118,11 +129,14 @@ __device__ __forceinline__ void run_pass(const GArgs& a, Smem& sh, const uint8_t
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int q = lane >> 4, r = lane & 15;
 
-  // this wavefront's weight rows: one 64-row tile of the packed matrix
-  const int trow0 = slab * kSlab + wave * kTileRows;
-  const int valid = max(0, min(kTileRows, a.n - trow0));
+  // this wavefront's weight rows: one 64-row tile of the packed matrix, or
+  // (gated) half a tile of gate rows and the half tile of the same up rows
+  const int hrow0 = slab * (kSlab / 2) + wave * (kTileRows / 2);  // gated: its outputs
+  const int trow0 = kGated ? hrow0 & ~(kTileRows - 1) : slab * kSlab + wave * kTileRows;
+  const int valid = kGated ? kTileRows : max(0, min(kTileRows, a.n - trow0));
   const uint8_t* tb = wexp + static_cast<int64_t>(min(trow0, a.n)) * a.nb * kBlockBytes;
-  const Rsrc rs = make_rsrc(tb, (static_cast<uint32_t>(valid) * a.nb * kBlockBytes + 3u) & ~3u);
+  const uint32_t to_up = kGated ? static_cast<uint32_t>(a.d_ff) * a.nb * kBlockBytes : 0u;
+  const Rsrc rs = make_rsrc(tb, ((static_cast<uint32_t>(valid) * a.nb * kBlockBytes + 3u) & ~3u) + to_up);
 
   // activations, half a block (128 of them, 16 chunks of 16 bytes) per token
   // at a time: 4 tokens per wavefront instruction; chunk c of token t goes to
@@ -148,7 +162,27 @@ __device__ __forceinline__ void run_pass(const GArgs& a, Smem& sh, const uint8_t
   // from the 16-byte boundary at or below its start; the buffer range check
   // turns bytes past the tile into zeros
   auto run_start = [&](int b) { return static_cast<uint32_t>(b) * valid * kBlockBytes; };
+  // gated: 16-byte pieces 0..83 of the window are the gate half's run of the
+  // block, 84..167 the up half's (half a tile's run, 1344 bytes, is a multiple
+  // of 16, so both start on 16 bytes)
+  constexpr uint32_t kHalfRun = kTileRows / 2 * kBlockBytes;
+  auto gated_piece = [&](int c) {
+    const uint32_t half = (hrow0 & (kTileRows / 2)) ? kHalfRun : 0u;
+    return half + (c < static_cast<int>(kHalfRun / 16) ? c * 16u : to_up + (c * 16u - kHalfRun));
+  };
   auto stage_w = [&](int b) {
+    if constexpr (kGated) {
+      const uint32_t st = run_start(b);
+#pragma unroll
+      for (int j = 0; j < kWRaw / 1024; ++j) {
+        const int c = j * 64 + lane;
+        const uint32_t off = c < static_cast<int>(2 * kHalfRun / 16) ? st + gated_piece(c) : 0xFFFFFFF0u;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            rs, reinterpret_cast<__attribute__((address_space(3))) void*>(reinterpret_cast<uintptr_t>(sh.wraw[wave] + j * 1024)),
+            16, static_cast<int>(off), 0, 0, 0);
+      }
+      return;
+    }
     const uint32_t st = run_start(b) & ~15u;
 #pragma unroll
     for (int j = 0; j < kWRaw / 1024; ++j)
@@ -299,6 +333,37 @@ __device__ __forceinline__ void run_pass(const GArgs& a, Smem& sh, const uint8_t
     }
   }
 
+  if constexpr (kGated) {
+    // tot[0..1] are the gate rows, tot[2..3] the same up rows: h = silu(g) u,
+    // formed in fp32 from the fp32 sums and rounded to bf16 once (the type the
+    // down projection's matrix cores take); the saved pre-activations are the
+    // same sums rounded to bf16
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int tok = 16 * t + r;
+      if (tok >= mt) continue;
+      const int64_t row = row0 + tok;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int col = hrow0 + 16 * i + 4 * q;
+        float h[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float g = tot[i][t][j];
+          h[j] = g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504088896340736f * g)) * tot[i + 2][t][j];
+        }
+        *reinterpret_cast<u32x2_t*>(a.h + row * a.d_ff + col) = u32x2_t{bf16_pair(h[0], h[1]), bf16_pair(h[2], h[3])};
+        if (a.gu) {
+          uint16_t* gr = a.gu + row * 2 * a.d_ff + col;
+          const f32x4_t g = tot[i][t], u = tot[i + 2][t];
+          *reinterpret_cast<u32x2_t*>(gr) = u32x2_t{bf16_pair(g[0], g[1]), bf16_pair(g[2], g[3])};
+          *reinterpret_cast<u32x2_t*>(gr + a.d_ff) = u32x2_t{bf16_pair(u[0], u[1]), bf16_pair(u[2], u[3])};
+        }
+      }
+    }
+    return;
+  }
+
   // y[row0 + 16t + r, trow0 + 16i + 4q + j]
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -321,6 +386,7 @@ __device__ __forceinline__ void run_pass(const GArgs& a, Smem& sh, const uint8_t
 
 // Two workgroups per CU (LDS ~69 KB each, 256 VGPRs per wavefront), so one
 // workgroup's barriers and block boundaries overlap the other's MFMAs.
+template <bool kGated>
 __global__ __launch_bounds__(kThreads, 2) void grouped_gemm_kernel(GArgs a) {
   __shared__ Smem sh;
   // workgroup -> (expert, slab): the slabs of one expert share an XCD
@@ -357,11 +423,11 @@ __global__ __launch_bounds__(kThreads, 2) void grouped_gemm_kernel(GArgs a) {
     const int mt = min(per, m - base);
     const int64_t row0 = static_cast<int64_t>(m0) + base;
     switch ((mt + 15) >> 4) {
-      case 1: run_pass<1>(a, sh, wexp, slab, row0, mt); break;
-      case 2: run_pass<2>(a, sh, wexp, slab, row0, mt); break;
-      case 3: run_pass<3>(a, sh, wexp, slab, row0, mt); break;
-      case 4: run_pass<4>(a, sh, wexp, slab, row0, mt); break;
-      default: run_pass<5>(a, sh, wexp, slab, row0, mt); break;
+      case 1: run_pass<1, kGated>(a, sh, wexp, slab, row0, mt); break;
+      case 2: run_pass<2, kGated>(a, sh, wexp, slab, row0, mt); break;
+      case 3: run_pass<3, kGated>(a, sh, wexp, slab, row0, mt); break;
+      case 4: run_pass<4, kGated>(a, sh, wexp, slab, row0, mt); break;
+      default: run_pass<5, kGated>(a, sh, wexp, slab, row0, mt); break;
     }
   }
 }
@@ -385,7 +451,29 @@ hipError_t launch_grouped_gemm(const GemmArgs& ga, hipStream_t s) {
   a.vec4 = (ga.n % 4) == 0;
   const int64_t groups = (ga.n_experts + kXcds - 1) / kXcds;
   const int64_t grid = groups * kXcds * a.nslab;
-  hipLaunchKernelGGL(grouped_gemm_kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s, a);
+  hipLaunchKernelGGL(grouped_gemm_kernel<false>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_grouped_swiglu(const SwigluArgs& g, hipStream_t s) {
+  if (g.total_m == 0) return hipSuccess;
+  GArgs a{};
+  a.w = g.w_table;
+  a.estride = g.expert_stride;
+  a.n_experts = static_cast<int>(g.n_experts);
+  a.n = static_cast<int>(2 * g.d_ff);
+  a.nb = static_cast<int>(g.d_model / kQK);
+  a.k = g.d_model;
+  a.x = g.x;
+  a.offsets = g.offsets;
+  a.total_m = g.total_m;
+  a.d_ff = static_cast<int>(g.d_ff);
+  a.h = g.h;
+  a.gu = g.gate_up;
+  a.nslab = static_cast<int>(g.d_ff / (kSlab / 2));
+  const int64_t groups = (g.n_experts + kXcds - 1) / kXcds;
+  const int64_t grid = groups * kXcds * a.nslab;
+  hipLaunchKernelGGL(grouped_gemm_kernel<true>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 

@@ -1,0 +1,486 @@
+// Gradients of the gated feed-forward h = silu(Wg x) * (Wu x) over the packed
+// experts (its forward is the gated form of the grouped GEMM).
+//
+// With the saved pre-activations g, u, s = 1 / (1 + exp(-g)) and the gradient
+// dh that arrives at h:
+//     dg = dh u s (1 + g (1 - s)),   du = dh g s,   dz = [dg | du]
+//     dx   = dz W        (W the expert's decoded [2 d_ff, d_model] matrix)
+//     dW_e = dz_e^T x_e  over the expert's rows
+//
+// dz_kernel forms dz once per row in fp32.  The product with W takes it as
+// fp16, each row scaled by a power of two that puts its largest magnitude in
+// [2^14, 2^15): the weights are +-d with d an fp16 number, so they enter the
+// fp16 matrix cores exactly and the only rounding ahead of the fp32 sums is
+// dz's own to 11 bits.  (Folding d into a bf16 operand instead would round
+// twice to 8 bits.)  The product with x takes dz as bf16, x's own type.
+#include "stq_device.hpp"
+#include "stq_launch.hpp"
+
+namespace stq {
+namespace {
+
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  return static_cast<uint32_t>(__builtin_bit_cast(uint16_t, static_cast<__bf16>(a))) |
+         static_cast<uint32_t>(__builtin_bit_cast(uint16_t, static_cast<__bf16>(b))) << 16;
+}
+__device__ __forceinline__ uint32_t f16_pair(float a, float b) {
+  return static_cast<uint32_t>(__builtin_bit_cast(uint16_t, static_cast<_Float16>(a))) |
+         static_cast<uint32_t>(__builtin_bit_cast(uint16_t, static_cast<_Float16>(b))) << 16;
+}
+__device__ __forceinline__ void unpack_bf16(const u32x4_t& w, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t d = w[i];
+    v[2 * i] = __builtin_bit_cast(float, d << 16);
+    v[2 * i + 1] = __builtin_bit_cast(float, d & 0xFFFF0000u);
+  }
+}
+
+__device__ __forceinline__ void* lds_at(void* base, int byte) { return static_cast<char*>(base) + byte; }
+__device__ __forceinline__ void lds_load16(Rsrc rs, void* lds, uint32_t voff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(
+      rs, reinterpret_cast<__attribute__((address_space(3))) void*>(reinterpret_cast<uintptr_t>(lds)), 16,
+      static_cast<int>(voff), 0, 0, 0);
+}
+
+// ---------------------------------------------------------------------------
+// dz
+// ---------------------------------------------------------------------------
+
+struct DzArgs {
+  const uint16_t* gu;  // [rows, 2 d_ff] bf16
+  const uint16_t* dh;  // [rows, d_ff] bf16
+  int d_ff;
+  uint16_t* dz16;      // fp16 [rows, 2 d_ff], scaled, or NULL
+  float* inv;          // [rows]: what undoes the row's scale
+  uint16_t* dzb;       // bf16 [rows, 2 d_ff], or NULL
+};
+
+__device__ __forceinline__ void dz_of(const u32x4_t& gw, const u32x4_t& uw, const u32x4_t& hw, float (&dg)[8],
+                                      float (&du)[8]) {
+  float g[8], u[8], h[8];
+  unpack_bf16(gw, g);
+  unpack_bf16(uw, u);
+  unpack_bf16(hw, h);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504088896340736f * g[i]));
+    const float gs = g[i] * s;
+    // 1 + g (1 - s) = 1 + g - g s; times s it is s + g s (1 - s)
+    dg[i] = h[i] * u[i] * fmaf(gs, 1.0f - s, s);
+    du[i] = h[i] * gs;
+  }
+}
+
+// One workgroup a row; 8 columns of gate and up per thread and step.  The
+// scaled form needs the row's largest magnitude first; the row is then read
+// again (from cache) and formed again, which costs less than keeping it.
+__global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
+  __shared__ uint32_t wmax[4];
+  const int64_t r = blockIdx.x;
+  const u32x4_t* g = reinterpret_cast<const u32x4_t*>(a.gu + r * 2 * a.d_ff);
+  const u32x4_t* u = reinterpret_cast<const u32x4_t*>(a.gu + r * 2 * a.d_ff + a.d_ff);
+  const u32x4_t* h = reinterpret_cast<const u32x4_t*>(a.dh + r * a.d_ff);
+  const int n8 = a.d_ff / 8;
+  float scale = 1.0f;
+  if (a.dz16) {
+    uint32_t mx = 0;  // magnitudes as bits: infinities and NaN order above every number
+    for (int i = threadIdx.x; i < n8; i += 256) {
+      float dg[8], du[8];
+      dz_of(g[i], u[i], h[i], dg, du);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        mx = max(mx, max(__builtin_bit_cast(uint32_t, dg[j]) & 0x7FFFFFFFu, __builtin_bit_cast(uint32_t, du[j]) & 0x7FFFFFFFu));
+    }
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) mx = max(mx, static_cast<uint32_t>(__shfl_xor(static_cast<int>(mx), o)));
+    if ((threadIdx.x & 63) == 0) wmax[threadIdx.x >> 6] = mx;
+    __syncthreads();
+    mx = max(max(wmax[0], wmax[1]), max(wmax[2], wmax[3]));
+    // 2^e with e = 14 - floor(log2 max), held where 2^e and 2^-e are normal numbers; a row of
+    // zeros, or one that is not finite, keeps 1
+    const int ex = static_cast<int>(mx >> 23);
+    const int e = (mx == 0 || ex == 255) ? 0 : max(-126, min(126, 14 + 127 - ex));
+    scale = __builtin_bit_cast(float, static_cast<uint32_t>(127 + e) << 23);
+    if (threadIdx.x == 0) a.inv[r] = __builtin_bit_cast(float, static_cast<uint32_t>(127 - e) << 23);
+  }
+  for (int i = threadIdx.x; i < n8; i += 256) {
+    float dg[8], du[8];
+    dz_of(g[i], u[i], h[i], dg, du);
+    u32x4_t og, ou;
+    if (a.dzb) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        og[j] = bf16_pair(dg[2 * j], dg[2 * j + 1]);
+        ou[j] = bf16_pair(du[2 * j], du[2 * j + 1]);
+      }
+      reinterpret_cast<u32x4_t*>(a.dzb + r * 2 * a.d_ff)[i] = og;
+      reinterpret_cast<u32x4_t*>(a.dzb + r * 2 * a.d_ff + a.d_ff)[i] = ou;
+    }
+    if (a.dz16) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        og[j] = f16_pair(dg[2 * j] * scale, dg[2 * j + 1] * scale);
+        ou[j] = f16_pair(du[2 * j] * scale, du[2 * j + 1] * scale);
+      }
+      reinterpret_cast<u32x4_t*>(a.dz16 + r * 2 * a.d_ff)[i] = og;
+      reinterpret_cast<u32x4_t*>(a.dz16 + r * 2 * a.d_ff + a.d_ff)[i] = ou;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// dx = dz W
+// ---------------------------------------------------------------------------
+// A workgroup of 4 wavefronts owns one 256-weight block column of one expert
+// (256 of dx's columns) and all of the expert's rows in passes of at most 128
+// tokens; the sum runs over the matrix's 64-row tiles, whose runs of that
+// block (2688 bytes) and whose 64 columns of dz stream into LDS one tile
+// ahead.  W enters transposed: an MFMA lane takes 8 consecutive rows of one
+// group of four columns.  Per tile a wavefront turns its 16 groups' codes
+// (lane = row) into bytes laid out [group][row], so a lane fetches its 8 rows'
+// codes with one 8-byte read; each code is the offset of its four fp16 lanes
+// in a 32-entry table.  Byte permutes then pair neighbouring rows into the
+// operands of four column sets (column 4 group + j, j = 0..3) and a packed
+// fp16 product puts in the rows' d.  A lane so ends with four neighbouring
+// columns of every token it holds.
+
+constexpr int kWaves = 4;
+constexpr int kThreads = kWaves * 64;
+constexpr int kXcds = 8;
+constexpr int kMaxTok = 128;
+constexpr int kRecStride = 72;  // bytes between groups' codes: 64 rows, then 8 to spread the banks
+constexpr int kRun = kTileRows * kBlockBytes;
+
+struct DxArgs {
+  const uint8_t* w;
+  int64_t estride;
+  int n_experts;
+  int nb;            // blocks per matrix row
+  int tiles;         // 64-row tiles of the matrix
+  const int32_t* offsets;
+  int64_t total_m;
+  const uint16_t* dz;  // fp16 [total_m, 64 tiles]
+  const float* inv;
+  uint16_t* dx;        // bf16 [total_m, 256 nb]
+};
+
+struct DxSmem {
+  uint64_t lut[32];                           // four fp16 lanes of each code; at byte 0
+  alignas(16) char a[2][kMaxTok * 128];       // dz: 64 columns of each token, 16-byte chunks swizzled
+  alignas(16) char w[2][3 * 1024];            // the tile's run of the block
+  alignas(16) uint8_t rec[kWaves][16 * kRecStride];
+  alignas(16) uint16_t d[kWaves][kTileRows];
+};
+
+template <int NT>
+__device__ __forceinline__ void dx_pass(const DxArgs& a, DxSmem& sh, const uint8_t* wexp, int b, int64_t row0, int mt) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int q = lane >> 4, r = lane & 15;
+  const uint32_t zrow = static_cast<uint32_t>(a.tiles) * 128u;  // bytes of a row of dz
+  const Rsrc rz = make_rsrc(a.dz + row0 * a.tiles * 64, static_cast<uint32_t>(mt) * zrow);
+  const int n_ins = (mt + 7) >> 3;
+  auto stage = [&](int t, int buf) {
+    for (int j = wave; j < n_ins; j += kWaves) {
+      const int row = j * 8 + (lane >> 3);
+      lds_load16(rz, sh.a[buf] + j * 1024, row * zrow + t * 128 + (((lane & 7) ^ ((row >> 1) & 7)) << 4));
+    }
+    // 168 chunks of 16 bytes, at 1 KB a wavefront instruction
+    const Rsrc rw = make_rsrc(wexp + (static_cast<int64_t>(t) * a.nb + b) * kRun, kRun);
+    if (wave < 3) lds_load16(rw, sh.w[buf] + wave * 1024, wave * 1024 + lane * 16);
+  };
+  auto make_records = [&](int buf) {
+    const uint8_t* blk = reinterpret_cast<const uint8_t*>(sh.w[buf]) + lane * kBlockBytes;
+    auto half = [&](int off) { return static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(blk + off)); };
+    auto word = [&](int off) { return half(off) | half(off + 2) << 16; };
+    sh.d[wave][lane] = static_cast<uint16_t>(half(0));
+    const uint32_t QH = word(34 + 4 * (wave >> 1));
+    uint8_t* out = sh.rec[wave] + lane;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t W = word(2 + 4 * (2 * wave + i));
+      const int p = 2 * ((2 * wave + i) & 3);
+      // byte j of lo: 8 * code of local group 8i + j; of hi: of 8i + 4 + j
+      const uint32_t lo = ((W << 3) & 0x78787878u) | ((QH << (7 - p)) & 0x80808080u);
+      const uint32_t hi = ((W >> 1) & 0x78787878u) | ((QH << (6 - p)) & 0x80808080u);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        out[(8 * i + j) * kRecStride] = static_cast<uint8_t>(lo >> (8 * j));
+        out[(8 * i + 4 + j) * kRecStride] = static_cast<uint8_t>(hi >> (8 * j));
+      }
+    }
+  };
+
+  f32x4_t acc[4][NT];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[j][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const int x = (r >> 1) & 7;
+  stage(0, 0);
+  for (int t = 0; t < a.tiles; ++t) {
+    const int buf = t & 1;
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wavefront's share of tile t is in LDS
+    __syncthreads();
+    if (t + 1 < a.tiles) stage(t + 1, buf ^ 1);
+    make_records(buf);
+    // the records and scales are this wavefront's own: LDS serves its instructions in order
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const u32x2_t codes = *reinterpret_cast<const u32x2_t*>(sh.rec[wave] + r * kRecStride + 32 * s + 8 * q);
+      const u32x4_t dw = *reinterpret_cast<const u32x4_t*>(&sh.d[wave][32 * s + 8 * q]);
+      f16x8_t A[NT];
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+        A[i] = *reinterpret_cast<const f16x8_t*>(sh.a[buf] + (16 * i + r) * 128 + (((4 * s + q) ^ x) << 4));
+      u32x2_t v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t cw = codes[i >> 2];
+        const uint32_t c = __builtin_amdgcn_ubfe(cw, 8 * (i & 3), 8);
+        v[i] = *reinterpret_cast<const u32x2_t*>(reinterpret_cast<const char*>(sh.lut) + c);
+      }
+      u32x4_t B[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t dword = dw[i];
+        const f16x2_t d2 = __builtin_bit_cast(f16x2_t, dword);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t even = v[2 * i][j >> 1], odd = v[2 * i + 1][j >> 1];
+          const uint32_t pr = __builtin_amdgcn_perm(odd, even, (j & 1) ? 0x07060302u : 0x05040100u);
+          B[j][i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, pr) * d2);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(A[i], __builtin_bit_cast(f16x8_t, B[j]), acc[j][i], 0, 0, 0);
+    }
+  }
+  // dx[row0 + 16i + 4q + e, 256b + 64 wave + 4r + 0..3]
+  const int64_t ld = static_cast<int64_t>(a.nb) * kQK;
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int tok = 16 * i + 4 * q + e;
+      if (tok >= mt) continue;
+      const float inv = a.inv[row0 + tok];
+      *reinterpret_cast<u32x2_t*>(a.dx + (row0 + tok) * ld + b * kQK + 64 * wave + 4 * r) =
+          u32x2_t{bf16_pair(acc[0][i][e] * inv, acc[1][i][e] * inv), bf16_pair(acc[2][i][e] * inv, acc[3][i][e] * inv)};
+    }
+  }
+}
+
+__device__ __forceinline__ void expert_rows(const int32_t* offsets, int e, int64_t total_m, int64_t* lo, int* m) {
+  // clamped to [0, total_m], so that offsets outside the contract reach no row that is not there
+  *lo = min(max(static_cast<int64_t>(offsets[e]), int64_t{0}), total_m);
+  const int64_t hi = min(max(static_cast<int64_t>(offsets[e + 1]), *lo), total_m);
+  *m = static_cast<int>(hi - *lo);
+}
+
+__global__ __launch_bounds__(kThreads, 2) void swiglu_dx_kernel(DxArgs a) {
+  __shared__ DxSmem sh;
+  // the blocks of one expert share an XCD, and with it the expert's dz in that L2
+  const int xcd = blockIdx.x % kXcds;
+  const int local = blockIdx.x / kXcds;
+  const int b = local % a.nb;
+  const int e = (local / a.nb) * kXcds + xcd;
+  if (e >= a.n_experts) return;
+  int64_t lo;
+  int m;
+  expert_rows(a.offsets, e, a.total_m, &lo, &m);
+  if (m <= 0) return;
+  if (threadIdx.x < 32) {
+    uint64_t v = 0;
+    for (int l = 0; l < 4; ++l) {
+      const int t = code_lane_value(threadIdx.x, l);
+      v |= static_cast<uint64_t>(t == 0 ? 0u : (t > 0 ? 0x3C00u : 0xBC00u)) << (16 * l);  // fp16 +-1
+    }
+    sh.lut[threadIdx.x] = v;
+  }
+  const uint8_t* wexp = a.w + static_cast<int64_t>(e) * a.estride;
+  const int np = (m + kMaxTok - 1) / kMaxTok;
+  const int per = (m + np - 1) / np;
+  for (int p = 0; p < np; ++p) {
+    const int base = p * per;
+    const int mt = min(per, m - base);
+    __syncthreads();
+    switch ((mt + 15) >> 4) {
+      case 1: dx_pass<1>(a, sh, wexp, b, lo + base, mt); break;
+      case 2: dx_pass<2>(a, sh, wexp, b, lo + base, mt); break;
+      case 3: dx_pass<3>(a, sh, wexp, b, lo + base, mt); break;
+      case 4: dx_pass<4>(a, sh, wexp, b, lo + base, mt); break;
+      case 5: case 6: dx_pass<6>(a, sh, wexp, b, lo + base, mt); break;
+      default: dx_pass<8>(a, sh, wexp, b, lo + base, mt); break;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// dW_e = dz_e^T x_e
+// ---------------------------------------------------------------------------
+// A workgroup owns 128 rows x 128 columns of one expert's dW; the sum runs
+// over the expert's tokens, 64 at a time.  Both operands lie [token][column]
+// while the matrix cores want 8 consecutive tokens of one column, so they are
+// read with the transposing 8-byte LDS read: 16 lanes give four tokens' 16
+// columns and each takes back four tokens of one.  The 32-byte pieces of a
+// token's 256 bytes are XORed by three bits of the token index, so the 16
+// tokens of one such read fall on different banks.
+
+constexpr int kTW = 128;     // tile edge
+constexpr int kTok = 64;     // tokens per stage
+
+struct DwArgs {
+  int n_experts;
+  int n_r;           // matrix rows (2 d_ff)
+  int n_c;           // d_model
+  const int32_t* offsets;
+  int64_t total_m;
+  const uint16_t* dz;  // bf16 [total_m, n_r]
+  const uint16_t* x;   // bf16 [total_m, n_c]
+  uint16_t* dw;        // bf16 [n_experts, n_r, n_c]
+};
+
+__device__ __forceinline__ int tok_swizzle(int t) { return 2 * ((t & 3) | ((t >> 1) & 4)); }
+
+__global__ __launch_bounds__(kThreads, 2) void swiglu_dw_kernel(DwArgs a) {
+  __shared__ __align__(16) char sz[2][kTok * kTW * 2];
+  __shared__ __align__(16) char sx[2][kTok * kTW * 2];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int q = lane >> 4, r = lane & 15;
+  const int tr = a.n_r / kTW, tc = a.n_c / kTW;
+  int id = blockIdx.x;
+  const int c0 = (id % tc) * kTW;
+  id /= tc;
+  const int r0 = (id % tr) * kTW;
+  const int e = id / tr;
+  int64_t lo;
+  int m;
+  expert_rows(a.offsets, e, a.total_m, &lo, &m);
+  const uint32_t zrow = static_cast<uint32_t>(a.n_r) * 2, xrow = static_cast<uint32_t>(a.n_c) * 2;
+  auto stage = [&](int s, int buf) {
+    const int64_t t0 = lo + static_cast<int64_t>(s) * kTok;
+    const int tv = min(kTok, m - s * kTok);
+    // tokens past the expert's rows lie past the descriptors' ranges and read as zeros
+    const Rsrc rz = make_rsrc(a.dz + t0 * a.n_r + r0, (tv - 1) * zrow + kTW * 2);
+    const Rsrc rx = make_rsrc(a.x + t0 * a.n_c + c0, (tv - 1) * xrow + kTW * 2);
+#pragma unroll
+    for (int j = 0; j < kTok / 4 / kWaves; ++j) {
+      const int ins = wave + j * kWaves;
+      const int t = ins * 4 + (lane >> 4);
+      const uint32_t piece = static_cast<uint32_t>((lane & 15) ^ tok_swizzle(t)) * 16;
+      lds_load16(rz, sz[buf] + ins * 1024, t < tv ? t * zrow + piece : 0xFFFFFFF0u);
+      lds_load16(rx, sx[buf] + ins * 1024, t < tv ? t * xrow + piece : 0xFFFFFFF0u);
+    }
+  };
+  f32x4_t acc[4][4];  // [column tile][row tile]
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const int wr = (wave >> 1) * 64, wc = (wave & 1) * 64;
+  const int ns = (m + kTok - 1) / kTok;
+  // this lane's part of a transposing read of tokens k0 + 0..3 (k0 = 8q, or 8q + 4), columns col..col+15
+  auto frag = [&](const char* base, int step, int col) {
+    u32x4_t v;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int t = 32 * step + 8 * q + 4 * h + (r >> 2);
+      const int byte = t * (kTW * 2) + (((col >> 3) ^ tok_swizzle(t)) << 4) + (r & 3) * 8;
+      const s16x4_t p = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          reinterpret_cast<__attribute__((address_space(3))) s16x4_t*>(reinterpret_cast<uintptr_t>(base + byte)));
+      const u32x2_t w = __builtin_bit_cast(u32x2_t, p);
+      v[2 * h] = w[0];
+      v[2 * h + 1] = w[1];
+    }
+    return __builtin_bit_cast(bf16x8_t, v);
+  };
+  if (ns > 0) stage(0, 0);
+  for (int s = 0; s < ns; ++s) {
+    const int buf = s & 1;
+    __builtin_amdgcn_s_waitcnt(0x0F70);
+    __syncthreads();
+    if (s + 1 < ns) stage(s + 1, buf ^ 1);
+#pragma unroll
+    for (int step = 0; step < kTok / 32; ++step) {
+      bf16x8_t X[4], Z[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) X[i] = frag(sx[buf], step, wc + 16 * i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) Z[j] = frag(sz[buf], step, wr + 16 * j);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(X[i], Z[j], acc[i][j], 0, 0, 0);
+    }
+  }
+  // dw[e, r0 + wr + 16j + r, c0 + wc + 16i + 4q + 0..3]
+  uint16_t* out = a.dw + (static_cast<int64_t>(e) * a.n_r + r0 + wr) * a.n_c + c0 + wc;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<u32x2_t*>(out + static_cast<int64_t>(16 * j + r) * a.n_c + 16 * i + 4 * q) =
+          u32x2_t{bf16_pair(acc[i][j][0], acc[i][j][1]), bf16_pair(acc[i][j][2], acc[i][j][3])};
+}
+
+}  // namespace
+
+SwigluBwdLayout swiglu_bwd_layout(int64_t d_ff, int64_t total_m, bool dx, bool dw) {
+  auto up = [](int64_t b) { return (b + 255) / 256 * 256; };
+  SwigluBwdLayout l{};
+  const int64_t z = up(total_m * 2 * d_ff * 2);
+  if (dx) {
+    l.inv = z;
+    l.dzb = z + up(total_m * 4);
+  }
+  l.bytes = l.dzb + (dw ? z : 0);
+  return l;
+}
+
+hipError_t launch_swiglu_bwd(const SwigluBwdArgs& g, void* ws, hipStream_t s) {
+  const SwigluBwdLayout l = swiglu_bwd_layout(g.d_ff, g.total_m, g.dx != nullptr, g.dw != nullptr);
+  char* base = static_cast<char*>(ws);
+  uint16_t* dz16 = g.dx ? reinterpret_cast<uint16_t*>(base) : nullptr;
+  float* inv = g.dx ? reinterpret_cast<float*>(base + l.inv) : nullptr;
+  uint16_t* dzb = g.dw ? reinterpret_cast<uint16_t*>(base + l.dzb) : nullptr;
+  if (g.total_m > 0) {
+    const DzArgs za{g.gate_up, g.dh, static_cast<int>(g.d_ff), dz16, inv, dzb};
+    hipLaunchKernelGGL(dz_kernel, dim3(static_cast<unsigned>(g.total_m)), dim3(256), 0, s, za);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (g.dx && g.total_m > 0) {
+    DxArgs a{g.w_table, g.expert_stride, static_cast<int>(g.n_experts), static_cast<int>(g.d_model / kQK),
+             static_cast<int>(2 * g.d_ff / kTileRows), g.offsets, g.total_m, dz16, inv, g.dx};
+    const int64_t groups = (g.n_experts + kXcds - 1) / kXcds;
+    hipLaunchKernelGGL(swiglu_dx_kernel, dim3(static_cast<unsigned>(groups * kXcds * a.nb)), dim3(kThreads), 0, s, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (g.dw) {
+    DwArgs a{static_cast<int>(g.n_experts), static_cast<int>(2 * g.d_ff), static_cast<int>(g.d_model), g.offsets,
+             g.total_m, dzb, g.x, g.dw};
+    const int64_t grid = g.n_experts * (2 * g.d_ff / kTW) * (g.d_model / kTW);
+    hipLaunchKernelGGL(swiglu_dw_kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace stq

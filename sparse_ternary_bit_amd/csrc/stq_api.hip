@@ -382,6 +382,100 @@ stq_status stq_greedy_allocation(const double* gain, const double* extra_bytes, 
 
 namespace {
 
+stq_status swiglu_shape_check(int64_t n_experts, int64_t d_model, int64_t d_ff, int64_t total_m, const char* who) {
+  if (n_experts < 1 || total_m < 0) return fail(STQ_E_ARG, "%s: negative count or no experts", who);
+  if (d_model <= 0 || d_model % STQ_QK || d_ff <= 0 || d_ff % STQ_QK)
+    return fail(STQ_E_SHAPE, "%s: d_model and d_ff must be positive multiples of 256", who);
+  if (n_experts > 65535) return fail(STQ_E_SHAPE, "%s: more than 65535 experts", who);
+  if (total_m > (int64_t{1} << 23)) return fail(STQ_E_SHAPE, "%s: more than 2^23 rows in one call", who);
+  // the kernels reach gate and up rows, and a pass's activations, with 32-bit byte offsets
+  if (d_model > (int64_t{1} << 22) || d_ff > (int64_t{1} << 21) || d_ff * stq_row_bytes(d_model) >= (int64_t{1} << 31))
+    return fail(STQ_E_SHAPE, "%s: matrix too large", who);
+  return STQ_OK;
+}
+
+}  // namespace
+
+stq_status stq_grouped_swiglu(const uint8_t* w_gate_up, int64_t gate_up_stride_bytes, int64_t n_experts,
+                              int64_t d_model, int64_t d_ff, const uint16_t* x_sorted, const int32_t* expert_offsets,
+                              int64_t total_m, uint16_t* h, uint16_t* gate_up, stq_stream_t stream) {
+  const char* who = "stq_grouped_swiglu";
+  const stq_status st = swiglu_shape_check(n_experts, d_model, d_ff, total_m, who);
+  if (st != STQ_OK) return st;
+  if (gate_up_stride_bytes < 2 * d_ff * stq_row_bytes(d_model)) return fail(STQ_E_SHAPE, "%s: expert stride smaller than the packed matrix", who);
+  if (((n_experts + 7) / 8 * 8) * (d_ff / 128) > (int64_t{1} << 23)) return fail(STQ_E_SHAPE, "%s: too many experts of this size", who);
+  if (!expert_offsets) return fail(STQ_E_ARG, "%s: null offsets", who);
+  if (total_m == 0) return ok();
+  if (!w_gate_up || !x_sorted || !h) return fail(STQ_E_ARG, "%s: null pointer", who);
+  if (!aligned(w_gate_up, 16) || gate_up_stride_bytes % 16) return fail(STQ_E_ALIGN, "%s: w_gate_up / expert stride not 16-byte aligned", who);
+  if (!aligned(x_sorted, 16)) return fail(STQ_E_ALIGN, "%s: x_sorted not 16-byte aligned", who);
+  if (!aligned(expert_offsets, 4) || !aligned(h, 8) || !aligned(gate_up, 8))
+    return fail(STQ_E_ALIGN, "%s: offsets not 4-byte, or h / gate_up not 8-byte aligned", who);
+  const stq::SwigluArgs a{w_gate_up, gate_up_stride_bytes, n_experts, d_model, d_ff, x_sorted, expert_offsets, total_m,
+                          h, gate_up};
+  hipError_t e = stq::launch_grouped_swiglu(a, reinterpret_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "stq_grouped_swiglu launch");
+  return ok();
+}
+
+namespace {
+
+stq_status swiglu_bwd_check(int64_t n_experts, int64_t d_model, int64_t d_ff, int64_t total_m, bool dx, bool dw,
+                            const char* who) {
+  const stq_status st = swiglu_shape_check(n_experts, d_model, d_ff, total_m, who);
+  if (st != STQ_OK) return st;
+  if (dx && ((n_experts + 7) / 8 * 8) * (d_model / STQ_QK) > (int64_t{1} << 23))
+    return fail(STQ_E_SHAPE, "%s: too many experts of this size", who);
+  if (dw && n_experts * (2 * d_ff / 128) > (int64_t{1} << 23) / (d_model / 128))
+    return fail(STQ_E_SHAPE, "%s: weight gradients of too many experts of this size", who);
+  return STQ_OK;
+}
+
+}  // namespace
+
+stq_status stq_grouped_swiglu_backward_workspace(int64_t n_experts, int64_t d_model, int64_t d_ff, int64_t total_m,
+                                                 int want_dx, int want_dw, int64_t* workspace_bytes) {
+  const char* who = "stq_grouped_swiglu_backward_workspace";
+  if (!workspace_bytes) return fail(STQ_E_ARG, "%s: null output pointer", who);
+  *workspace_bytes = 0;
+  const stq_status st = swiglu_bwd_check(n_experts, d_model, d_ff, total_m, want_dx != 0, want_dw != 0, who);
+  if (st != STQ_OK) return st;
+  *workspace_bytes = stq::swiglu_bwd_layout(d_ff, total_m, want_dx != 0, want_dw != 0).bytes;
+  return ok();
+}
+
+stq_status stq_grouped_swiglu_backward(const uint8_t* w_gate_up, int64_t gate_up_stride_bytes, int64_t n_experts,
+                                       int64_t d_model, int64_t d_ff, const uint16_t* x_sorted,
+                                       const int32_t* expert_offsets, int64_t total_m, const uint16_t* gate_up,
+                                       const uint16_t* dh, uint16_t* dx, uint16_t* dw, void* workspace,
+                                       int64_t workspace_bytes, stq_stream_t stream) {
+  const char* who = "stq_grouped_swiglu_backward";
+  stq_status st = swiglu_bwd_check(n_experts, d_model, d_ff, total_m, dx != nullptr, dw != nullptr, who);
+  if (st != STQ_OK) return st;
+  if (dx && gate_up_stride_bytes < 2 * d_ff * stq_row_bytes(d_model)) return fail(STQ_E_SHAPE, "%s: expert stride smaller than the packed matrix", who);
+  if (!expert_offsets) return fail(STQ_E_ARG, "%s: null offsets", who);
+  if (workspace_bytes < 0) return fail(STQ_E_ARG, "%s: workspace_bytes < 0", who);
+  if (!dx && !dw) return ok();
+  if (total_m == 0 && !dw) return ok();
+  if (total_m > 0 && (!gate_up || !dh)) return fail(STQ_E_ARG, "%s: null gate_up or dh", who);
+  if (total_m > 0 && dx && !w_gate_up) return fail(STQ_E_ARG, "%s: dx needs w_gate_up", who);
+  if (total_m > 0 && dw && !x_sorted) return fail(STQ_E_ARG, "%s: dw needs x_sorted", who);
+  if (dx && (!aligned(w_gate_up, 16) || gate_up_stride_bytes % 16)) return fail(STQ_E_ALIGN, "%s: w_gate_up / expert stride not 16-byte aligned", who);
+  if (!aligned(gate_up, 16) || !aligned(dh, 16) || (dw && !aligned(x_sorted, 16)))
+    return fail(STQ_E_ALIGN, "%s: gate_up, dh or x_sorted not 16-byte aligned", who);
+  if (!aligned(expert_offsets, 4) || !aligned(dx, 8) || !aligned(dw, 8))
+    return fail(STQ_E_ALIGN, "%s: offsets not 4-byte, or dx / dw not 8-byte aligned", who);
+  st = check_workspace(workspace, workspace_bytes, stq::swiglu_bwd_layout(d_ff, total_m, dx != nullptr, dw != nullptr).bytes, who);
+  if (st != STQ_OK) return st;
+  const stq::SwigluBwdArgs a{w_gate_up, gate_up_stride_bytes, n_experts, d_model, d_ff, x_sorted, expert_offsets,
+                             total_m, gate_up, dh, dx, dw};
+  hipError_t e = stq::launch_swiglu_bwd(a, workspace, reinterpret_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "stq_grouped_swiglu_backward launch");
+  return ok();
+}
+
+namespace {
+
 constexpr int64_t kMaxStride8 = int64_t{1} << 23;  // bytes between 8-bit rows: a tile's rows stay within 32-bit offsets
 constexpr int64_t kMaxK8 = 131071;                 // k * 128 * 128 < 2^31
 

@@ -90,6 +90,42 @@ struct GemmArgs {
 };
 hipError_t launch_grouped_gemm(const GemmArgs& a, hipStream_t s);
 
+// Gated feed-forward over the packed experts, rows grouped by expert, and its
+// gradients
+struct SwigluArgs {
+  const uint8_t* w_table;
+  int64_t expert_stride;
+  int64_t n_experts;
+  int64_t d_model, d_ff;
+  const uint16_t* x;
+  const int32_t* offsets;
+  int64_t total_m;
+  uint16_t* h;
+  uint16_t* gate_up;  // may be NULL
+};
+hipError_t launch_grouped_swiglu(const SwigluArgs& a, hipStream_t s);
+
+struct SwigluBwdArgs {
+  const uint8_t* w_table;
+  int64_t expert_stride;
+  int64_t n_experts;
+  int64_t d_model, d_ff;
+  const uint16_t* x;         // read with dw
+  const int32_t* offsets;
+  int64_t total_m;
+  const uint16_t* gate_up;
+  const uint16_t* dh;
+  uint16_t* dx;              // may be NULL
+  uint16_t* dw;              // may be NULL
+};
+// Workspace: the scaled fp16 dz at 0 and its row scales at `inv` (dx), the
+// bf16 dz at `dzb` (dw)
+struct SwigluBwdLayout {
+  int64_t inv, dzb, bytes;
+};
+SwigluBwdLayout swiglu_bwd_layout(int64_t d_ff, int64_t total_m, bool dx, bool dw);
+hipError_t launch_swiglu_bwd(const SwigluBwdArgs& a, void* ws, hipStream_t s);
+
 // Layer error under calibration activations (full Hessian and diagonal);
 // `scratch` holds layer_errors_scratch_bytes(...) bytes.
 int64_t layer_errors_scratch_bytes(int64_t n_rows, int64_t k, int64_t n_cal);

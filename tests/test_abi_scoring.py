@@ -1,4 +1,4 @@
-"""Host-side checks of the 8-bit product and the token scoring entry points:
+"""Host-side checks of the gated feed-forward, the 8-bit product and the token scoring:
 bad arguments are refused with a status and a message before any GPU call,
 empty work is fine without one, and the workspace queries agree with the
 calls.  No kernel runs."""
@@ -156,6 +156,70 @@ def test_logprobs_backward_refusals(L, kw, status):
 
 def test_logprobs_backward_nothing_to_do(L):
     assert _bw(L, n=0, x=None, t=None, lse=None, ent=None, g=None, ge=None, d=None) == 0
+
+
+ROWB = 4096 // 256 * 42      # packed bytes of a row of 4096
+STRIDE = 2 * 512 * ROWB
+
+
+def _fw(L, **kw):
+    a = dict(w=FAKE, st=STRIDE, ne=4, d=4096, f=512, x=FAKE, off=FAKE, m=10, h=FAKE, gu=FAKE)
+    a.update(kw)
+    return L.stq_grouped_swiglu(a["w"], a["st"], a["ne"], a["d"], a["f"], a["x"], a["off"], a["m"], a["h"], a["gu"],
+                                None)
+
+
+SHAPE_REFUSALS = [(dict(ne=0), 1), (dict(m=-1), 1), (dict(d=100), 2), (dict(f=128), 2), (dict(f=0), 2),
+                  (dict(ne=65536), 2), (dict(m=(1 << 23) + 1), 2), (dict(d=1 << 23), 2), (dict(f=1 << 22), 2),
+                  (dict(d=1 << 17, f=1 << 17, st=1 << 60), 2), (dict(st=STRIDE - 16), 2), (dict(off=None), 1),
+                  (dict(st=STRIDE + 8), 3), (dict(w=FAKE + 8), 3), (dict(off=FAKE + 2), 3), (dict(w=None), 1)]
+
+
+@pytest.mark.parametrize("kw, status", SHAPE_REFUSALS + [
+    (dict(x=None), 1), (dict(h=None), 1), (dict(x=FAKE + 8), 3), (dict(h=FAKE + 4), 3), (dict(gu=FAKE + 4), 3)])
+def test_swiglu_refusals(L, kw, status):
+    assert _fw(L, **kw) == status
+    assert _err(L).startswith("stq_grouped_swiglu")
+
+
+def _bwd(L, **kw):
+    a = dict(w=FAKE, st=STRIDE, ne=4, d=4096, f=512, x=FAKE, off=FAKE, m=10, gu=FAKE, dh=FAKE, dx=FAKE, dw=FAKE,
+             ws=FAKE, wsb=1 << 40)
+    a.update(kw)
+    return L.stq_grouped_swiglu_backward(a["w"], a["st"], a["ne"], a["d"], a["f"], a["x"], a["off"], a["m"], a["gu"],
+                                         a["dh"], a["dx"], a["dw"], a["ws"], a["wsb"], None)
+
+
+@pytest.mark.parametrize("kw, status", SHAPE_REFUSALS + [
+    (dict(gu=None), 1), (dict(dh=None), 1), (dict(x=None), 1), (dict(gu=FAKE + 8), 3), (dict(dh=FAKE + 8), 3),
+    (dict(x=FAKE + 8), 3), (dict(dx=FAKE + 4), 3), (dict(dw=FAKE + 4), 3), (dict(wsb=-1), 1),
+    (dict(ne=60000, d=1 << 16, f=1 << 14, st=1 << 40), 2)])
+def test_swiglu_backward_refusals(L, kw, status):
+    assert _bwd(L, **kw) == status
+    assert _err(L).startswith("stq_grouped_swiglu_backward")
+
+
+def test_swiglu_nothing_to_do(L):
+    assert _fw(L, m=0, w=None, x=None, h=None, gu=None) == 0
+    assert _bwd(L, dx=None, dw=None, w=None, x=None, gu=None, dh=None, ws=None, wsb=0) == 0
+    assert _bwd(L, m=0, dw=None, w=None, x=None, gu=None, dh=None, ws=None, wsb=0) == 0
+
+
+def test_swiglu_backward_workspace(L):
+    wb = ctypes.c_int64(-7)
+    f = L.stq_grouped_swiglu_backward_workspace
+    z = 10 * 1024 * 2
+    assert f(4, 4096, 512, 10, 1, 0, ctypes.byref(wb)) == 0 and wb.value == z + 256
+    assert f(4, 4096, 512, 10, 0, 1, ctypes.byref(wb)) == 0 and wb.value == z
+    assert f(4, 4096, 512, 10, 1, 1, ctypes.byref(wb)) == 0 and wb.value == 2 * z + 256
+    need = wb.value
+    assert f(4, 4096, 512, 0, 1, 1, ctypes.byref(wb)) == 0 and wb.value == 0
+    assert f(4, 4096, 500, 10, 1, 1, ctypes.byref(wb)) == 2
+    assert f(4, 4096, 512, -1, 1, 1, ctypes.byref(wb)) == 1
+    assert f(4, 4096, 512, 10, 1, 1, None) == 1
+    assert _bwd(L, ws=None, wsb=0) == 1 and "workspace" in _err(L)
+    assert _bwd(L, wsb=need - 1) == 1 and str(need) in _err(L)
+    assert _bwd(L, ws=FAKE + 16, wsb=need) == 3
 
 
 def test_binding_refuses_cpu_tensors_and_wrong_shapes():
