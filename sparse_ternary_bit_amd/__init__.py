@@ -9,6 +9,7 @@ fallback.  If the library is not built, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -191,29 +192,27 @@ def _table(name: str, t: torch.Tensor, n_experts: int, stride: int, n: int, k: i
         _holds(name, t, (int(n_experts) - 1) * int(stride) + int(n) * row_bytes(k))
 
 
-def _together(**tensors) -> torch.device:
-    """The one GPU every given tensor lives on."""
-    dev = None
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a GPU tensor")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the other tensors are on {dev}")
+def _one_gpu(first: torch.Tensor, *others) -> torch.device:
+    """The GPU `first` lives on; every other tensor given must live there too."""
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError(f"the tensors must be GPU tensors, got one on {dev}")
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"the tensors must be on one GPU, got {t.device} beside {dev}")
     return dev
 
 
 def _call(device: torch.device, func: str, *args) -> None:
     """Run an entry point on `device`'s current stream, with that device current."""
-    f = getattr(lib(), func)
+    f = getattr(_lib or lib(), func)
     if device.index == torch.cuda.current_device():
-        _check(func, f(*args, torch.cuda.current_stream().cuda_stream))
+        status = f(*args, torch._C._cuda_getCurrentRawStream(device.index))
     else:
         with torch.cuda.device(device):
-            _check(func, f(*args, torch.cuda.current_stream().cuda_stream))
+            status = f(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    if status != 0:
+        _check(func, status)
 
 
 def _rows(name: str, t: torch.Tensor, *dtypes: torch.dtype) -> int:
@@ -455,7 +454,7 @@ def grouped_swiglu(w_gate_up: torch.Tensor, expert_stride: int, n_experts: int, 
     """h = silu(W_gate_e x) * (W_up_e x), bf16 [total_m, d_ff], for rows x_sorted bf16 [total_m, d_model]
     grouped by expert (offsets as in grouped_gemm) and packed [2*d_ff, d_model] experts.  `gate_up`
     (bf16 [total_m, 2*d_ff]) receives the pre-activations that grouped_swiglu_backward reads."""
-    dev = _together(w_gate_up=w_gate_up, x_sorted=x_sorted, offsets=offsets, out=out, gate_up=gate_up)
+    dev = _one_gpu(w_gate_up, x_sorted, offsets, out, gate_up)
     total_m = _swiglu_args(w_gate_up, expert_stride, n_experts, d_model, d_ff, x_sorted, offsets)
     if out is None:
         out = torch.empty((total_m, int(d_ff)), dtype=torch.bfloat16, device=dev)
@@ -485,8 +484,8 @@ def grouped_swiglu_backward(w_gate_up: torch.Tensor, expert_stride: int, n_exper
     dx bf16 [total_m, d_model] through the decoded weights, dw bf16 [n_experts, 2*d_ff, d_model] the
     gradient of the decoded weights; None for the one not needed.  `workspace` (GPU bytes, at least
     grouped_swiglu_backward_workspace(...)) is allocated here when not given."""
-    dev = _together(w_gate_up=w_gate_up, x_sorted=x_sorted, offsets=offsets, gate_up=gate_up, dh=dh, dx=dx, dw=dw,
-                    workspace=workspace)
+    dev = _one_gpu(w_gate_up, x_sorted, offsets, gate_up, dh, dx, dw,
+                    workspace)
     total_m = _swiglu_args(w_gate_up, expert_stride, n_experts, d_model, d_ff, x_sorted, offsets)
     E, d, f = int(n_experts), int(d_model), int(d_ff)
     _matrix("gate_up", gate_up, torch.bfloat16, total_m, 2 * f)
@@ -526,7 +525,7 @@ def q8_quantize_rows(x: torch.Tensor, out: torch.Tensor | None = None, scale: to
     """Rows of 8-bit integers with one scale each: (q int8 [n, k], scale fp32 [n]) of x fp32 or bf16
     [n, k], scale = max|x| / 127 and q the nearest integer to x / scale.  Without `out` the rows are
     k rounded up to 16 bytes apart (the layout q8_matmul reads), padded with zeros."""
-    dev = _together(x=x, out=out, scale=scale)
+    dev = _one_gpu(x, out, scale)
     stride = _rows("x", x, torch.float32, torch.bfloat16)
     n, k = x.shape
     if out is None:
@@ -551,13 +550,18 @@ def q8_matmul_workspace(m: int, n: int, k: int, n_cus: int = 0) -> int:
     return wb.value
 
 
+@functools.lru_cache(maxsize=256)
+def _q8_need(m: int, n: int, k: int, n_cus: int) -> int:
+    return q8_matmul_workspace(m, n, k, n_cus)
+
+
 def q8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
               out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16,
               workspace: torch.Tensor | None = None) -> torch.Tensor:
     """y[i, j] = (a[i] . w[j]) a_scale[i] w_scale[j] for int8 rows a [m, k] and w [n, k], the sum exact;
     y is bf16 or fp32 [m, n].  `workspace` (GPU bytes, at least q8_matmul_workspace(m, n, k)) is
     allocated here when not given."""
-    dev = _together(a=a, a_scale=a_scale, w=w, w_scale=w_scale, out=out, workspace=workspace)
+    dev = _one_gpu(a, a_scale, w, w_scale, out, workspace)
     lda, ldw = _q8_stride("a", a), _q8_stride("w", w)
     m, k = a.shape
     n = w.shape[0]
@@ -573,7 +577,7 @@ def q8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: 
         raise ValueError("out must be [m, n]")
     ldy = _rows("out", out, torch.bfloat16, torch.float32)
     if workspace is None and m > 0 and n > 0:
-        workspace = _workspace(None, q8_matmul_workspace(m, n, k, _device_cus(dev)), dev)
+        workspace = _workspace(None, _q8_need(m, n, k, _device_cus(dev)), dev)
     else:
         workspace = _workspace(workspace, 0, dev)
     _call(dev, "stq_q8_matmul", a.data_ptr(), lda, a_scale.data_ptr(), w.data_ptr(), ldw, w_scale.data_ptr(), m, n, k,
@@ -591,6 +595,11 @@ def token_logprobs_workspace(x_dtype: int, n_rows: int, vocab: int, top_n: int, 
     return wb.value
 
 
+@functools.lru_cache(maxsize=256)
+def _logprobs_need(x_dtype: int, n_rows: int, vocab: int, top_n: int, n_cus: int) -> int:
+    return token_logprobs_workspace(x_dtype, n_rows, vocab, top_n, n_cus)
+
+
 def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, top_n: int = 0, logprob: torch.Tensor | None = None,
                    lse: torch.Tensor | None = None, entropy: torch.Tensor | None = None,
                    top_ids: torch.Tensor | None = None, top_logprobs: torch.Tensor | None = None,
@@ -599,31 +608,34 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, top_n: int = 0, 
     int32 [n]: log probability of each row's target, log-sum-exp, entropy, and the top_n (at most 32)
     most likely ids with their log probabilities, equal logits by lowest id.  Outputs and `workspace`
     (GPU bytes, at least token_logprobs_workspace(...)) are allocated here when not given."""
-    dev = _together(logits=logits, targets=targets, logprob=logprob, lse=lse, entropy=entropy, top_ids=top_ids,
-                    top_logprobs=top_logprobs, workspace=workspace)
+    dev = _one_gpu(logits, targets, logprob, lse, entropy, top_ids,
+                    top_logprobs, workspace)
     stride = _rows("logits", logits, torch.float32, torch.bfloat16)
     n, vocab = logits.shape
     top_n = int(top_n)
     if top_n < 0:
         raise ValueError("top_n must not be negative")
     _vector("targets", targets, torch.int32, n)
-    outs = []
-    for name, t, dtype, shape in (("logprob", logprob, torch.float32, (n,)), ("lse", lse, torch.float32, (n,)),
-                                  ("entropy", entropy, torch.float32, (n,)), ("top_ids", top_ids, torch.int32, (n, top_n)),
-                                  ("top_logprobs", top_logprobs, torch.float32, (n, top_n))):
-        if t is None:
-            t = torch.empty(shape, dtype=dtype, device=dev)
-        else:
-            _vector(name, t, dtype, n * (top_n if len(shape) == 2 else 1))
-        outs.append(t)
+    # the fp32 vectors not given share one allocation
+    new = iter(torch.empty(((logprob is None) + (lse is None) + (entropy is None), n), dtype=torch.float32,
+                           device=dev).unbind(0))
+    logprob, lse, entropy = (next(new) if t is None else t for t in (logprob, lse, entropy))
+    for name, t in (("logprob", logprob), ("lse", lse), ("entropy", entropy)):
+        _vector(name, t, torch.float32, n)
+    if top_ids is None:
+        top_ids = torch.empty((n, top_n), dtype=torch.int32, device=dev)
+    if top_logprobs is None:
+        top_logprobs = torch.empty((n, top_n), dtype=torch.float32, device=dev)
+    _vector("top_ids", top_ids, torch.int32, n * top_n)
+    _vector("top_logprobs", top_logprobs, torch.float32, n * top_n)
     xd = X_BF16 if logits.dtype == torch.bfloat16 else X_F32
     if workspace is None and n > 0:
-        workspace = _workspace(None, token_logprobs_workspace(xd, n, vocab, top_n, _device_cus(dev)), dev)
+        workspace = _workspace(None, _logprobs_need(xd, n, vocab, top_n, _device_cus(dev)), dev)
     else:
         workspace = _workspace(workspace, 0, dev)
-    _call(dev, "stq_token_logprobs", logits.data_ptr(), xd, stride, n, vocab, targets.data_ptr(), outs[0].data_ptr(),
-          outs[1].data_ptr(), outs[2].data_ptr(), top_n, outs[3].data_ptr(), outs[4].data_ptr(), *_ws_args(workspace))
-    return tuple(outs)
+    _call(dev, "stq_token_logprobs", logits.data_ptr(), xd, stride, n, vocab, targets.data_ptr(), logprob.data_ptr(),
+          lse.data_ptr(), entropy.data_ptr(), top_n, top_ids.data_ptr(), top_logprobs.data_ptr(), *_ws_args(workspace))
+    return logprob, lse, entropy, top_ids, top_logprobs
 
 
 def token_logprobs_backward(logits: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor,
@@ -632,8 +644,8 @@ def token_logprobs_backward(logits: torch.Tensor, targets: torch.Tensor, lse: to
     """Gradient of token_logprobs with respect to the logits, for gradients fp32 [n] arriving at
     logprob and entropy (either may be None); lse and entropy are what the forward call gave.
     `out` has the logits' type and shape and may be the logits themselves."""
-    dev = _together(logits=logits, targets=targets, lse=lse, entropy=entropy, grad_logprob=grad_logprob,
-                    grad_entropy=grad_entropy, out=out)
+    dev = _one_gpu(logits, targets, lse, entropy, grad_logprob,
+                    grad_entropy, out)
     stride = _rows("logits", logits, torch.float32, torch.bfloat16)
     n, vocab = logits.shape
     _vector("targets", targets, torch.int32, n)

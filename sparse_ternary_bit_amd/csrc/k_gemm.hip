@@ -43,6 +43,7 @@
 // and shared by its 16 slabs.
 #include "stq_device.hpp"
 #include "stq_launch.hpp"
+#include "stq_passes.hpp"
 
 namespace stq {
 namespace {
@@ -64,8 +65,8 @@ constexpr int kSlab = kWaves * kTileRows;   // 256 weight rows per workgroup
 constexpr int kMaxTiles = 5;                // token tiles of 16 per pass
 constexpr int kMaxTok = kMaxTiles * 16;     // 80 tokens per pass
 constexpr int kHalfBytes = kQK;             // one token's 128 activations: half a block
-constexpr int kXBuf = kMaxTok * kHalfBytes; // 20480 bytes per buffer
 constexpr int kXcds = 8;
+constexpr int kFewRows = 8;                 // gated form: mean rows an expert up to which passes are of 32
 constexpr int kWRaw = 3 * 1024;             // 16-byte aligned window over one 2688-byte tile run
 
 struct GArgs {
@@ -87,6 +88,7 @@ struct GArgs {
   uint16_t* gu;   // [total_m, 2 d_ff] bf16, or NULL
 };
 
+template <int kTiles>
 struct Smem {
   // Pattern table: entry c of lut[0..31] holds lanes 0,1 of code c as bf16,
   // entry c of lut[32..63] lanes 2,3.  Kept at byte 0 so a code times 4 is
@@ -99,7 +101,7 @@ struct Smem {
   // (the writers, a row tile per 16 lanes, meet 2-way bank conflicts on
   // their 4-byte stores, which cost less than the 4-byte reads they replace)
   alignas(16) uint32_t rec[kWaves][4][4][16][4];
-  alignas(16) char x[2][kXBuf];           // activations, current and next half block
+  alignas(16) char x[2][kTiles * 16 * kHalfBytes];  // activations, current and next half block
   alignas(16) char wraw[kWaves][kWRaw];   // each wavefront's tile run of the next block
 };
 
@@ -121,8 +123,8 @@ __device__ __forceinline__ int pass_tid() {
   return t;
 }
 
-template <int NT, bool kGated>
-__device__ __forceinline__ void run_pass(const GArgs& a, Smem& sh, const uint8_t* wexp, int slab, int64_t row0,
+template <int NT, bool kGated, int kTiles>
+__device__ __forceinline__ void run_pass(const GArgs& a, Smem<kTiles>& sh, const uint8_t* wexp, int slab, int64_t row0,
                                          int mt) {
   const int tid = pass_tid();
   const int lane = tid & 63;
@@ -384,11 +386,18 @@ __device__ __forceinline__ void run_pass(const GArgs& a, Smem& sh, const uint8_t
   }
 }
 
+__device__ __forceinline__ uint32_t pattern_word(uint32_t c, int lane) {
+  auto bf = [&](int l) -> uint32_t {
+    const int t = code_lane_value(c, l);
+    return t == 0 ? 0u : (t > 0 ? 0x3F80u : 0xBF80u);  // bf16 +1, -1
+  };
+  return bf(lane) | (bf(lane + 1) << 16);
+}
+
 // Two workgroups per CU (LDS ~69 KB each, 256 VGPRs per wavefront), so one
 // workgroup's barriers and block boundaries overlap the other's MFMAs.
-template <bool kGated>
 __global__ __launch_bounds__(kThreads, 2) void grouped_gemm_kernel(GArgs a) {
-  __shared__ Smem sh;
+  __shared__ Smem<kMaxTiles> sh;
   // workgroup -> (expert, slab): the slabs of one expert share an XCD
   const int wg = blockIdx.x;
   const int xcd = wg % kXcds;
@@ -405,13 +414,8 @@ __global__ __launch_bounds__(kThreads, 2) void grouped_gemm_kernel(GArgs a) {
   if (m <= 0) return;
 
   if (threadIdx.x < 32) {
-    const uint32_t c = threadIdx.x;
-    auto bf = [&](int lane) -> uint32_t {
-      const int t = code_lane_value(c, lane);
-      return t == 0 ? 0u : (t > 0 ? 0x3F80u : 0xBF80u);  // bf16 +1, -1
-    };
-    sh.lut[c] = bf(0) | (bf(1) << 16);
-    sh.lut[32 + c] = bf(2) | (bf(3) << 16);
+    sh.lut[threadIdx.x] = pattern_word(threadIdx.x, 0);
+    sh.lut[32 + threadIdx.x] = pattern_word(threadIdx.x, 2);
   }
   __syncthreads();
 
@@ -423,12 +427,42 @@ __global__ __launch_bounds__(kThreads, 2) void grouped_gemm_kernel(GArgs a) {
     const int mt = min(per, m - base);
     const int64_t row0 = static_cast<int64_t>(m0) + base;
     switch ((mt + 15) >> 4) {
-      case 1: run_pass<1, kGated>(a, sh, wexp, slab, row0, mt); break;
-      case 2: run_pass<2, kGated>(a, sh, wexp, slab, row0, mt); break;
-      case 3: run_pass<3, kGated>(a, sh, wexp, slab, row0, mt); break;
-      case 4: run_pass<4, kGated>(a, sh, wexp, slab, row0, mt); break;
-      default: run_pass<5, kGated>(a, sh, wexp, slab, row0, mt); break;
+      case 1: run_pass<1, false>(a, sh, wexp, slab, row0, mt); break;
+      case 2: run_pass<2, false>(a, sh, wexp, slab, row0, mt); break;
+      case 3: run_pass<3, false>(a, sh, wexp, slab, row0, mt); break;
+      case 4: run_pass<4, false>(a, sh, wexp, slab, row0, mt); break;
+      default: run_pass<5, false>(a, sh, wexp, slab, row0, mt); break;
     }
+  }
+}
+
+// The gated form: one workgroup per (pass of an expert's tokens, slab), so an
+// expert with many tokens is spread over the chip (a router's load is rarely
+// even: 8191 rows over 32 experts with loads ~ 1/rank took 1303 us with each
+// expert's passes in turn).  Which pass a workgroup has is found on the device
+// from the offsets; the grid holds as many as the row count allows and the
+// rest leave.  Passes are dealt to the XCDs in turn, a pass's slabs sharing one.
+template <int kTiles, int kPerCu>
+__global__ __launch_bounds__(kThreads, kPerCu) void grouped_swiglu_kernel(GArgs a) {
+  __shared__ Smem<kTiles> sh;
+  const int xcd = blockIdx.x % kXcds;
+  const int local = blockIdx.x / kXcds;
+  const int slab = local % a.nslab;
+  const PassUnit u = find_pass(a.offsets, a.n_experts, a.total_m, (local / a.nslab) * kXcds + xcd, kTiles * 16);
+  if (u.mt <= 0) return;
+  if (threadIdx.x < 32) {
+    sh.lut[threadIdx.x] = pattern_word(threadIdx.x, 0);
+    sh.lut[32 + threadIdx.x] = pattern_word(threadIdx.x, 2);
+  }
+  __syncthreads();
+  const uint8_t* wexp = a.w + static_cast<int64_t>(u.expert) * a.estride;
+  const int nt = (u.mt + 15) >> 4;
+  if (nt == 1) run_pass<1, true>(a, sh, wexp, slab, u.row0, u.mt);
+  else if (nt == 2 || kTiles == 2) run_pass<2, true>(a, sh, wexp, slab, u.row0, u.mt);
+  else if constexpr (kTiles > 2) {
+    if (nt == 3) run_pass<3, true>(a, sh, wexp, slab, u.row0, u.mt);
+    else if (nt == 4) run_pass<4, true>(a, sh, wexp, slab, u.row0, u.mt);
+    else run_pass<5, true>(a, sh, wexp, slab, u.row0, u.mt);
   }
 }
 
@@ -451,7 +485,7 @@ hipError_t launch_grouped_gemm(const GemmArgs& ga, hipStream_t s) {
   a.vec4 = (ga.n % 4) == 0;
   const int64_t groups = (ga.n_experts + kXcds - 1) / kXcds;
   const int64_t grid = groups * kXcds * a.nslab;
-  hipLaunchKernelGGL(grouped_gemm_kernel<false>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s, a);
+  hipLaunchKernelGGL(grouped_gemm_kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 
@@ -471,9 +505,13 @@ hipError_t launch_grouped_swiglu(const SwigluArgs& g, hipStream_t s) {
   a.h = g.h;
   a.gu = g.gate_up;
   a.nslab = static_cast<int>(g.d_ff / (kSlab / 2));
-  const int64_t groups = (g.n_experts + kXcds - 1) / kXcds;
-  const int64_t grid = groups * kXcds * a.nslab;
-  hipLaunchKernelGGL(grouped_gemm_kernel<true>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s, a);
+  // Few tokens an expert: the weights' stream is the bound, and a workgroup
+  // sized for 32 tokens (two thirds of the LDS and registers) runs three to a CU
+  const bool few = g.total_m <= kFewRows * g.n_experts;
+  const int64_t units = (pass_units(g.total_m, g.n_experts, few ? 32 : kMaxTok) + kXcds - 1) / kXcds * kXcds;
+  const dim3 grid(static_cast<unsigned>(units * a.nslab));
+  if (few) hipLaunchKernelGGL((grouped_swiglu_kernel<2, 3>), grid, dim3(kThreads), 0, s, a);
+  else hipLaunchKernelGGL((grouped_swiglu_kernel<kMaxTiles, 2>), grid, dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 

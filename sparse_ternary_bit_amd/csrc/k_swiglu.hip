@@ -15,6 +15,7 @@
 // twice to 8 bits.)  The product with x takes dz as bf16, x's own type.
 #include "stq_device.hpp"
 #include "stq_launch.hpp"
+#include "stq_passes.hpp"
 
 namespace stq {
 namespace {
@@ -291,18 +292,16 @@ __device__ __forceinline__ void expert_rows(const int32_t* offsets, int e, int64
   *m = static_cast<int>(hi - *lo);
 }
 
+// One workgroup per (pass of an expert's tokens, block), passes found on the
+// device and dealt to the XCDs as in the forward kernel: a pass's blocks share
+// an XCD, and with it the pass's dz in that L2.
 __global__ __launch_bounds__(kThreads, 2) void swiglu_dx_kernel(DxArgs a) {
   __shared__ DxSmem sh;
-  // the blocks of one expert share an XCD, and with it the expert's dz in that L2
   const int xcd = blockIdx.x % kXcds;
   const int local = blockIdx.x / kXcds;
   const int b = local % a.nb;
-  const int e = (local / a.nb) * kXcds + xcd;
-  if (e >= a.n_experts) return;
-  int64_t lo;
-  int m;
-  expert_rows(a.offsets, e, a.total_m, &lo, &m);
-  if (m <= 0) return;
+  const PassUnit u = find_pass(a.offsets, a.n_experts, a.total_m, (local / a.nb) * kXcds + xcd, kMaxTok);
+  if (u.mt <= 0) return;
   if (threadIdx.x < 32) {
     uint64_t v = 0;
     for (int l = 0; l < 4; ++l) {
@@ -311,21 +310,14 @@ __global__ __launch_bounds__(kThreads, 2) void swiglu_dx_kernel(DxArgs a) {
     }
     sh.lut[threadIdx.x] = v;
   }
-  const uint8_t* wexp = a.w + static_cast<int64_t>(e) * a.estride;
-  const int np = (m + kMaxTok - 1) / kMaxTok;
-  const int per = (m + np - 1) / np;
-  for (int p = 0; p < np; ++p) {
-    const int base = p * per;
-    const int mt = min(per, m - base);
-    __syncthreads();
-    switch ((mt + 15) >> 4) {
-      case 1: dx_pass<1>(a, sh, wexp, b, lo + base, mt); break;
-      case 2: dx_pass<2>(a, sh, wexp, b, lo + base, mt); break;
-      case 3: dx_pass<3>(a, sh, wexp, b, lo + base, mt); break;
-      case 4: dx_pass<4>(a, sh, wexp, b, lo + base, mt); break;
-      case 5: case 6: dx_pass<6>(a, sh, wexp, b, lo + base, mt); break;
-      default: dx_pass<8>(a, sh, wexp, b, lo + base, mt); break;
-    }
+  const uint8_t* wexp = a.w + static_cast<int64_t>(u.expert) * a.estride;
+  switch ((u.mt + 15) >> 4) {
+    case 1: dx_pass<1>(a, sh, wexp, b, u.row0, u.mt); break;
+    case 2: dx_pass<2>(a, sh, wexp, b, u.row0, u.mt); break;
+    case 3: dx_pass<3>(a, sh, wexp, b, u.row0, u.mt); break;
+    case 4: dx_pass<4>(a, sh, wexp, b, u.row0, u.mt); break;
+    case 5: case 6: dx_pass<6>(a, sh, wexp, b, u.row0, u.mt); break;
+    default: dx_pass<8>(a, sh, wexp, b, u.row0, u.mt); break;
   }
 }
 
@@ -467,8 +459,8 @@ hipError_t launch_swiglu_bwd(const SwigluBwdArgs& g, void* ws, hipStream_t s) {
   if (g.dx && g.total_m > 0) {
     DxArgs a{g.w_table, g.expert_stride, static_cast<int>(g.n_experts), static_cast<int>(g.d_model / kQK),
              static_cast<int>(2 * g.d_ff / kTileRows), g.offsets, g.total_m, dz16, inv, g.dx};
-    const int64_t groups = (g.n_experts + kXcds - 1) / kXcds;
-    hipLaunchKernelGGL(swiglu_dx_kernel, dim3(static_cast<unsigned>(groups * kXcds * a.nb)), dim3(kThreads), 0, s, a);
+    const int64_t units = (pass_units(g.total_m, g.n_experts, kMaxTok) + kXcds - 1) / kXcds * kXcds;
+    hipLaunchKernelGGL(swiglu_dx_kernel, dim3(static_cast<unsigned>(units * a.nb)), dim3(kThreads), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

@@ -14,6 +14,7 @@
 
 #include "stq.h"
 #include "stq_launch.hpp"
+#include "stq_passes.hpp"
 
 namespace {
 
@@ -403,7 +404,8 @@ stq_status stq_grouped_swiglu(const uint8_t* w_gate_up, int64_t gate_up_stride_b
   const stq_status st = swiglu_shape_check(n_experts, d_model, d_ff, total_m, who);
   if (st != STQ_OK) return st;
   if (gate_up_stride_bytes < 2 * d_ff * stq_row_bytes(d_model)) return fail(STQ_E_SHAPE, "%s: expert stride smaller than the packed matrix", who);
-  if (((n_experts + 7) / 8 * 8) * (d_ff / 128) > (int64_t{1} << 23)) return fail(STQ_E_SHAPE, "%s: too many experts of this size", who);
+  if ((stq::pass_units(total_m, n_experts, 32) + 8) * (d_ff / 128) > (int64_t{1} << 23))
+    return fail(STQ_E_SHAPE, "%s: too many rows and experts of this size for one call", who);
   if (!expert_offsets) return fail(STQ_E_ARG, "%s: null offsets", who);
   if (total_m == 0) return ok();
   if (!w_gate_up || !x_sorted || !h) return fail(STQ_E_ARG, "%s: null pointer", who);
@@ -424,8 +426,8 @@ stq_status swiglu_bwd_check(int64_t n_experts, int64_t d_model, int64_t d_ff, in
                             const char* who) {
   const stq_status st = swiglu_shape_check(n_experts, d_model, d_ff, total_m, who);
   if (st != STQ_OK) return st;
-  if (dx && ((n_experts + 7) / 8 * 8) * (d_model / STQ_QK) > (int64_t{1} << 23))
-    return fail(STQ_E_SHAPE, "%s: too many experts of this size", who);
+  if (dx && (stq::pass_units(total_m, n_experts, 32) + 8) * (d_model / STQ_QK) > (int64_t{1} << 23))
+    return fail(STQ_E_SHAPE, "%s: too many rows and experts of this size for one call", who);
   if (dw && n_experts * (2 * d_ff / 128) > (int64_t{1} << 23) / (d_model / 128))
     return fail(STQ_E_SHAPE, "%s: weight gradients of too many experts of this size", who);
   return STQ_OK;
