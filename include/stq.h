@@ -372,7 +372,7 @@ stq_status stq_grouped_swiglu_backward_workspace(int64_t n_experts, int64_t d_mo
  *          multiple of 16 and at least k rounded up to 16; the bytes from k
  *          up to that multiple are written 0, those behind it are left
  *   scale  [n_rows] fp32
- * k >= 1; at most 2^23 rows per call. */
+ * k >= 1; at most 2^22 rows per call. */
 stq_status stq_q8_quantize_rows(const void* x, int x_dtype, int64_t x_row_stride, int64_t n_rows, int64_t k,
                                 int8_t* q, int64_t q_row_stride, float* scale, stq_stream_t stream);
 
@@ -388,20 +388,12 @@ stq_status stq_q8_quantize_rows(const void* x, int x_dtype, int64_t x_row_stride
  *   y            [m, n] fp32 (STQ_X_F32) or bf16 (STQ_X_BF16, one rounding of
  *                the fp32 value), rows y_row_stride elements apart; rows that
  *                start on four elements store faster
- *   workspace, workspace_bytes   scratch for split sums, at least what
- *                stq_q8_matmul_workspace reports (may be NULL when that is 0)
  * 1 <= k <= 131071 (any sum of products of bytes then fits 32 bits); m up to
  * 2^22.  Integer sums do not depend on their order: a result's bits do not
  * depend on m, n, the strides or the device. */
 stq_status stq_q8_matmul(const int8_t* a, int64_t a_row_stride, const float* a_scale, const int8_t* w,
                          int64_t w_row_stride, const float* w_scale, int64_t m, int64_t n, int64_t k, void* y,
-                         int y_dtype, int64_t y_row_stride, void* workspace, int64_t workspace_bytes,
-                         stq_stream_t stream);
-
-/* Workspace bytes stq_q8_matmul needs for these shapes on a device with n_cus
- * compute units (0: the current device's); host only, same checks and errors
- * as the call.  workspace_bytes is a HOST pointer. */
-stq_status stq_q8_matmul_workspace(int64_t m, int64_t n, int64_t k, int32_t n_cus, int64_t* workspace_bytes);
+                         int y_dtype, int64_t y_row_stride, stq_stream_t stream);
 
 /* Log probabilities of given tokens under rows of logits, with each row's
  * log-sum-exp, entropy and most likely alternatives: how a compressed model

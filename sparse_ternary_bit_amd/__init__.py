@@ -19,7 +19,7 @@ __all__ = [
     "row_bytes", "quantize_rows", "dequantize_rows", "gemv", "gemv_noalloc", "gemv_plan", "grouped_gemm",
     "moe_ffn_decode",
     "moe_ffn_workspace", "grouped_swiglu", "grouped_swiglu_backward", "grouped_swiglu_backward_workspace",
-    "q8_quantize_rows", "q8_matmul", "q8_matmul_workspace", "token_logprobs",
+    "q8_quantize_rows", "q8_matmul", "token_logprobs",
     "token_logprobs_workspace", "token_logprobs_backward", "layer_errors", "layer_errors_workspace", "q2_roundtrip", "greedy_allocation",
     "stream_read_probe", "mfma_loop_probe", "lds_read_probe", "MFMA_PROBE_FLOP_PER_ROUND",
     "LDS_PROBE_READS_PER_ROUND",
@@ -110,10 +110,8 @@ def lib() -> ctypes.CDLL:
     L.stq_q8_quantize_rows.argtypes = [_c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64, _c_vp, _c_vp]
     L.stq_q8_quantize_rows.restype = _c_int
     L.stq_q8_matmul.argtypes = [_c_vp, _c_i64, _c_vp, _c_vp, _c_i64, _c_vp, _c_i64, _c_i64, _c_i64, _c_vp, _c_int,
-                                _c_i64, _c_vp, _c_i64, _c_vp]
+                                _c_i64, _c_vp]
     L.stq_q8_matmul.restype = _c_int
-    L.stq_q8_matmul_workspace.argtypes = [_c_i64, _c_i64, _c_i64, ctypes.c_int32, ctypes.POINTER(_c_i64)]
-    L.stq_q8_matmul_workspace.restype = _c_int
     L.stq_token_logprobs.argtypes = [_c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_vp, _c_vp, _c_vp, _c_vp, _c_i64,
                                      _c_vp, _c_vp, _c_vp, _c_i64, _c_vp]
     L.stq_token_logprobs.restype = _c_int
@@ -219,10 +217,13 @@ def _rows(name: str, t: torch.Tensor, *dtypes: torch.dtype) -> int:
     """Row stride in elements of a matrix whose rows are contiguous (any distance apart)."""
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix with contiguous rows")
+    (n, k), (ld, step) = t.shape, t.stride()
+    if step != 1 and k > 1:
         raise ValueError(f"{name} must be a matrix with contiguous rows")
     # a one-row view may carry any stride in its first dimension
-    return t.stride(0) if t.shape[0] > 1 else max(1, t.shape[1])
+    return ld if n > 1 else max(1, k)
 
 
 def _vector(name: str, t: torch.Tensor, dtype: torch.dtype, n: int) -> None:
@@ -513,10 +514,11 @@ def grouped_swiglu_backward(w_gate_up: torch.Tensor, expert_stride: int, n_exper
 def _q8_stride(name: str, t: torch.Tensor) -> int:
     """Row stride in bytes of int8 rows, which own their bytes up to the next multiple of 16."""
     stride = _rows(name, t, torch.int8)
-    kp = (t.shape[1] + 15) // 16 * 16
-    if t.shape[0] == 1:
+    n, k = t.shape
+    kp = (k + 15) // 16 * 16
+    if n == 1:
         stride = kp
-    if t.numel() and t.storage_offset() + (t.shape[0] - 1) * stride + kp > t.untyped_storage().nbytes():
+    if kp != k and n > 0 and t.storage_offset() + (n - 1) * stride + kp > t.untyped_storage().nbytes():
         raise ValueError(f"{name}'s last row must own its bytes up to the next multiple of 16")
     return stride
 
@@ -529,39 +531,28 @@ def q8_quantize_rows(x: torch.Tensor, out: torch.Tensor | None = None, scale: to
     stride = _rows("x", x, torch.float32, torch.bfloat16)
     n, k = x.shape
     if out is None:
-        out = torch.empty((n, (k + 15) // 16 * 16), dtype=torch.int8, device=dev)[:, :k]
-    if tuple(out.shape) != (n, k):
-        raise ValueError("out must be [n, k] like x")
-    qs = _q8_stride("out", out)
+        qs = (k + 15) // 16 * 16
+        out = torch.empty((n, qs), dtype=torch.int8, device=dev)
+        if qs != k:
+            out = out[:, :k]
+    else:
+        if tuple(out.shape) != (n, k):
+            raise ValueError("out must be [n, k] like x")
+        qs = _q8_stride("out", out)
     if scale is None:
         scale = torch.empty(n, dtype=torch.float32, device=dev)
-    _vector("scale", scale, torch.float32, n)
+    else:
+        _vector("scale", scale, torch.float32, n)
     _call(dev, "stq_q8_quantize_rows", x.data_ptr(), X_BF16 if x.dtype == torch.bfloat16 else X_F32, stride, n, k,
           out.data_ptr(), qs, scale.data_ptr())
     return out, scale
 
 
-def q8_matmul_workspace(m: int, n: int, k: int, n_cus: int = 0) -> int:
-    """Workspace bytes q8_matmul needs for these shapes on n_cus compute units (0: the current
-    device's); host only."""
-    wb = ctypes.c_int64()
-    _check("stq_q8_matmul_workspace", lib().stq_q8_matmul_workspace(int(m), int(n), int(k), int(n_cus),
-                                                                    ctypes.byref(wb)))
-    return wb.value
-
-
-@functools.lru_cache(maxsize=256)
-def _q8_need(m: int, n: int, k: int, n_cus: int) -> int:
-    return q8_matmul_workspace(m, n, k, n_cus)
-
-
 def q8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
-              out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16,
-              workspace: torch.Tensor | None = None) -> torch.Tensor:
+              out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
     """y[i, j] = (a[i] . w[j]) a_scale[i] w_scale[j] for int8 rows a [m, k] and w [n, k], the sum exact;
-    y is bf16 or fp32 [m, n].  `workspace` (GPU bytes, at least q8_matmul_workspace(m, n, k)) is
-    allocated here when not given."""
-    dev = _one_gpu(a, a_scale, w, w_scale, out, workspace)
+    y is bf16 or fp32 [m, n]."""
+    dev = _one_gpu(a, a_scale, w, w_scale, out)
     lda, ldw = _q8_stride("a", a), _q8_stride("w", w)
     m, k = a.shape
     n = w.shape[0]
@@ -573,15 +564,13 @@ def q8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: 
         if out_dtype not in (torch.bfloat16, torch.float32):
             raise ValueError("out_dtype must be bfloat16 or float32")
         out = torch.empty((m, n), dtype=out_dtype, device=dev)
-    if tuple(out.shape) != (m, n):
-        raise ValueError("out must be [m, n]")
-    ldy = _rows("out", out, torch.bfloat16, torch.float32)
-    if workspace is None and m > 0 and n > 0:
-        workspace = _workspace(None, _q8_need(m, n, k, _device_cus(dev)), dev)
+        ldy = n
     else:
-        workspace = _workspace(workspace, 0, dev)
+        if tuple(out.shape) != (m, n):
+            raise ValueError("out must be [m, n]")
+        ldy = _rows("out", out, torch.bfloat16, torch.float32)
     _call(dev, "stq_q8_matmul", a.data_ptr(), lda, a_scale.data_ptr(), w.data_ptr(), ldw, w_scale.data_ptr(), m, n, k,
-          out.data_ptr(), X_BF16 if out.dtype == torch.bfloat16 else X_F32, ldy, *_ws_args(workspace))
+          out.data_ptr(), X_BF16 if out.dtype == torch.bfloat16 else X_F32, ldy)
     return out
 
 
@@ -616,18 +605,22 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, top_n: int = 0, 
     if top_n < 0:
         raise ValueError("top_n must not be negative")
     _vector("targets", targets, torch.int32, n)
-    # the fp32 vectors not given share one allocation
-    new = iter(torch.empty(((logprob is None) + (lse is None) + (entropy is None), n), dtype=torch.float32,
-                           device=dev).unbind(0))
-    logprob, lse, entropy = (next(new) if t is None else t for t in (logprob, lse, entropy))
     for name, t in (("logprob", logprob), ("lse", lse), ("entropy", entropy)):
-        _vector(name, t, torch.float32, n)
+        if t is not None:
+            _vector(name, t, torch.float32, n)
+    if logprob is None and lse is None and entropy is None:
+        logprob, lse, entropy = torch.empty((3, n), dtype=torch.float32, device=dev).unbind(0)
+    else:
+        logprob, lse, entropy = (torch.empty(n, dtype=torch.float32, device=dev) if t is None else t
+                                 for t in (logprob, lse, entropy))
     if top_ids is None:
         top_ids = torch.empty((n, top_n), dtype=torch.int32, device=dev)
+    else:
+        _vector("top_ids", top_ids, torch.int32, n * top_n)
     if top_logprobs is None:
         top_logprobs = torch.empty((n, top_n), dtype=torch.float32, device=dev)
-    _vector("top_ids", top_ids, torch.int32, n * top_n)
-    _vector("top_logprobs", top_logprobs, torch.float32, n * top_n)
+    else:
+        _vector("top_logprobs", top_logprobs, torch.float32, n * top_n)
     xd = X_BF16 if logits.dtype == torch.bfloat16 else X_F32
     if workspace is None and n > 0:
         workspace = _workspace(None, _logprobs_need(xd, n, vocab, top_n, _device_cus(dev)), dev)
@@ -654,11 +647,14 @@ def token_logprobs_backward(logits: torch.Tensor, targets: torch.Tensor, lse: to
             _vector(name, t, torch.float32, n)
     if out is None:
         out = torch.empty((n, vocab), dtype=logits.dtype, device=dev)
-    if tuple(out.shape) != (n, vocab):
-        raise ValueError("out must be [n, vocab] like the logits")
+        ds = vocab
+    else:
+        if tuple(out.shape) != (n, vocab):
+            raise ValueError("out must be [n, vocab] like the logits")
+        ds = _rows("out", out, logits.dtype)
     _call(dev, "stq_token_logprobs_backward", logits.data_ptr(), X_BF16 if logits.dtype == torch.bfloat16 else X_F32,
           stride, n, vocab, targets.data_ptr(), lse.data_ptr(), _ptr(entropy), _ptr(grad_logprob), _ptr(grad_entropy),
-          out.data_ptr(), _rows("out", out, logits.dtype))
+          out.data_ptr(), ds)
     return out
 
 

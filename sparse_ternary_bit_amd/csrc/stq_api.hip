@@ -502,7 +502,7 @@ stq_status stq_q8_quantize_rows(const void* x, int x_dtype, int64_t x_row_stride
   if (n_rows < 0) return fail(STQ_E_ARG, "%s: n_rows < 0", who);
   if (k < 1) return fail(STQ_E_SHAPE, "%s: k=%lld is not positive", who, (long long)k);
   if (x_dtype != STQ_X_F32 && x_dtype != STQ_X_BF16) return fail(STQ_E_ARG, "%s: unknown x_dtype %d", who, x_dtype);
-  if (k > INT_MAX || n_rows > (int64_t{1} << 23)) return fail(STQ_E_SHAPE, "%s: more than 2^23 rows or k above int32", who);
+  if (k > INT_MAX || n_rows > (int64_t{1} << 22)) return fail(STQ_E_SHAPE, "%s: more than 2^22 rows or k above int32", who);
   if (n_rows > 1 && x_row_stride < k) return fail(STQ_E_SHAPE, "%s: x_row_stride < k", who);
   if (q_row_stride < (k + 15) / 16 * 16) return fail(STQ_E_SHAPE, "%s: q_row_stride < k rounded up to 16", who);
   if (n_rows == 0) return ok();
@@ -517,30 +517,17 @@ stq_status stq_q8_quantize_rows(const void* x, int x_dtype, int64_t x_row_stride
   return ok();
 }
 
-stq_status stq_q8_matmul_workspace(int64_t m, int64_t n, int64_t k, int32_t n_cus, int64_t* workspace_bytes) {
-  if (!workspace_bytes) return fail(STQ_E_ARG, "stq_q8_matmul_workspace: null output pointer");
-  *workspace_bytes = 0;
-  if (n_cus < 0) return fail(STQ_E_ARG, "stq_q8_matmul_workspace: n_cus < 0");
-  const stq_status st = q8_shape_check(m, n, k, "stq_q8_matmul_workspace");
-  if (st != STQ_OK) return st;
-  if (m > 0 && n > 0)
-    *workspace_bytes = stq::q8_matmul_scratch_bytes(m, n, k, n_cus > 0 ? n_cus : stq::cus_of_current_device());
-  return ok();
-}
-
 stq_status stq_q8_matmul(const int8_t* a, int64_t a_row_stride, const float* a_scale, const int8_t* w,
                          int64_t w_row_stride, const float* w_scale, int64_t m, int64_t n, int64_t k, void* y,
-                         int y_dtype, int64_t y_row_stride, void* workspace, int64_t workspace_bytes,
-                         stq_stream_t stream) {
+                         int y_dtype, int64_t y_row_stride, stq_stream_t stream) {
   const char* who = "stq_q8_matmul";
-  stq_status st = q8_shape_check(m, n, k, who);
+  const stq_status st = q8_shape_check(m, n, k, who);
   if (st != STQ_OK) return st;
   if (y_dtype != STQ_X_F32 && y_dtype != STQ_X_BF16) return fail(STQ_E_ARG, "%s: unknown y_dtype %d", who, y_dtype);
   const int64_t kp = (k + 15) / 16 * 16;
   if (a_row_stride < kp || w_row_stride < kp) return fail(STQ_E_SHAPE, "%s: row stride of a or w < k rounded up to 16", who);
   if (a_row_stride > kMaxStride8 || w_row_stride > kMaxStride8) return fail(STQ_E_SHAPE, "%s: row stride of a or w above 2^23", who);
   if (m > 1 && y_row_stride < n) return fail(STQ_E_SHAPE, "%s: y_row_stride < n", who);
-  if (workspace_bytes < 0) return fail(STQ_E_ARG, "%s: workspace_bytes < 0", who);
   if (m == 0 || n == 0) return ok();
   if (!a || !a_scale || !w || !w_scale || !y) return fail(STQ_E_ARG, "%s: null pointer", who);
   const int esz = y_dtype == STQ_X_BF16 ? 2 : 4;
@@ -549,12 +536,9 @@ stq_status stq_q8_matmul(const int8_t* a, int64_t a_row_stride, const float* a_s
     return fail(STQ_E_ALIGN, "%s: a, w or their row strides not 16-byte aligned", who);
   if (!aligned(a_scale, 4) || !aligned(w_scale, 4) || !aligned(y, esz)) return fail(STQ_E_ALIGN, "%s: scales or y not aligned to their elements", who);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  const int cus = stq::cus_of_stream(s);
-  st = check_workspace(workspace, workspace_bytes, stq::q8_matmul_scratch_bytes(m, n, k, cus), who);
-  if (st != STQ_OK) return st;
   const stq::Q8MatmulArgs g{a, a_row_stride, a_scale, w, w_row_stride, w_scale, m, n, k, y,
-                            y_dtype == STQ_X_BF16 ? 1 : 0, y_row_stride, cus};
-  hipError_t e = stq::launch_q8_matmul(g, workspace, s);
+                            y_dtype == STQ_X_BF16 ? 1 : 0, y_row_stride, stq::cus_of_stream(s)};
+  hipError_t e = stq::launch_q8_matmul(g, s);
   if (e != hipSuccess) return hip_fail(e, "stq_q8_matmul launch");
   return ok();
 }

@@ -160,9 +160,7 @@ struct Q8MatmulArgs {
   int64_t ldy;
   int cus;            // compute units to plan for
 };
-// `ws` holds q8_matmul_scratch_bytes(...) bytes for the same shape and CU count
-int64_t q8_matmul_scratch_bytes(int64_t m, int64_t n, int64_t k, int cus);
-hipError_t launch_q8_matmul(const Q8MatmulArgs& a, void* ws, hipStream_t s);
+hipError_t launch_q8_matmul(const Q8MatmulArgs& a, hipStream_t s);
 
 // Token log probabilities, entropy and top alternatives of rows of logits
 struct LogprobsArgs {

@@ -32,7 +32,7 @@ def _quant(L, **kw):
 @pytest.mark.parametrize("kw, status", [
     (dict(n=-1), 1), (dict(k=0), 2), (dict(k=-3), 2), (dict(xd=2), 1), (dict(xs=99), 2), (dict(qs=96), 2),
     (dict(qs=120), 3), (dict(q=FAKE + 8), 3), (dict(x=FAKE + 1), 3), (dict(xd=0, x=FAKE + 2), 3),
-    (dict(sc=FAKE + 2), 3), (dict(x=None), 1), (dict(q=None), 1), (dict(sc=None), 1), (dict(n=(1 << 23) + 1), 2),
+    (dict(sc=FAKE + 2), 3), (dict(x=None), 1), (dict(q=None), 1), (dict(sc=None), 1), (dict(n=(1 << 22) + 1), 2),
     (dict(xs=1 << 62), 2), (dict(k=1 << 31, xs=1 << 31, qs=1 << 31), 2),
 ])
 def test_quantize_refusals(L, kw, status):
@@ -45,11 +45,10 @@ def test_quantize_nothing_to_do(L):
 
 
 def _mm(L, **kw):
-    a = dict(a=FAKE, lda=112, as_=FAKE, w=FAKE, ldw=112, ws=FAKE, m=128, n=64, k=100, y=FAKE, yd=1, ldy=64,
-             wk=FAKE, wkb=1 << 40)
+    a = dict(a=FAKE, lda=112, as_=FAKE, w=FAKE, ldw=112, ws=FAKE, m=128, n=64, k=100, y=FAKE, yd=1, ldy=64)
     a.update(kw)
     return L.stq_q8_matmul(a["a"], a["lda"], a["as_"], a["w"], a["ldw"], a["ws"], a["m"], a["n"], a["k"], a["y"],
-                           a["yd"], a["ldy"], a["wk"], a["wkb"], None)
+                           a["yd"], a["ldy"], None)
 
 
 @pytest.mark.parametrize("kw, status", [
@@ -58,7 +57,7 @@ def _mm(L, **kw):
     (dict(ldw=(1 << 23) + 16), 2), (dict(ldy=63), 2), (dict(a=None), 1), (dict(as_=None), 1), (dict(w=None), 1),
     (dict(ws=None), 1), (dict(y=None), 1), (dict(a=FAKE + 8), 3), (dict(w=FAKE + 8), 3), (dict(as_=FAKE + 2), 3),
     (dict(ws=FAKE + 2), 3), (dict(y=FAKE + 1), 3), (dict(yd=0, y=FAKE + 2), 3), (dict(m=(1 << 22) + 1), 2),
-    (dict(n=1 << 31, ldy=1 << 31), 2), (dict(ldy=1 << 62), 2), (dict(wkb=-1), 1),
+    (dict(n=1 << 31, ldy=1 << 31), 2), (dict(ldy=1 << 62), 2),
 ])
 def test_matmul_refusals(L, kw, status):
     assert _mm(L, **kw) == status
@@ -66,30 +65,9 @@ def test_matmul_refusals(L, kw, status):
 
 
 def test_matmul_nothing_to_do(L):
-    none = dict(a=None, as_=None, w=None, ws=None, y=None, wk=None, wkb=0)
+    none = dict(a=None, as_=None, w=None, ws=None, y=None)
     assert _mm(L, m=0, **none) == 0
     assert _mm(L, n=0, **none) == 0
-
-
-def test_matmul_workspace_query(L):
-    wb = ctypes.c_int64(-7)
-    f = L.stq_q8_matmul_workspace
-    assert f(0, 4096, 7168, 256, ctypes.byref(wb)) == 0 and wb.value == 0
-    assert f(4, 0, 7168, 256, ctypes.byref(wb)) == 0 and wb.value == 0
-    assert f(-1, 4, 4, 256, ctypes.byref(wb)) == 1
-    assert f(4, 4, 0, 256, ctypes.byref(wb)) == 2
-    assert f(4, 4, 4, -1, ctypes.byref(wb)) == 1
-    assert f(4, 4, 4, 256, None) == 1
-    for m, n, k in ((1, 4096, 7168), (16, 4096, 7168), (64, 512, 7168), (65, 300, 5000), (2048, 256, 16)):
-        assert f(m, n, k, 256, ctypes.byref(wb)) == 0 and wb.value >= 0
-        if wb.value:
-            args = dict(m=m, n=n, k=k, lda=(k + 15) // 16 * 16, ldw=(k + 15) // 16 * 16, ldy=n)
-            wb2 = ctypes.c_int64()
-            assert f(m, n, k, 0, ctypes.byref(wb2)) == 0     # what the call itself plans for here
-            if wb2.value:
-                assert _mm(L, wk=None, wkb=0, **args) == 1 and "workspace" in _err(L)
-                assert _mm(L, wk=FAKE, wkb=wb2.value - 1, **args) == 1
-                assert _mm(L, wk=FAKE + 16, wkb=wb2.value, **args) == 3
 
 
 def _lp(L, **kw):

@@ -36,7 +36,7 @@ def _quant_ref(x):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("n, k", [(1, 1), (1, 7168), (3, 15), (5, 16), (2, 17), (130, 4099), (64, 256), (1, 20001)])
+@pytest.mark.parametrize("n, k", [(1, 1), (1, 7168), (3, 15), (5, 16), (2, 17), (130, 4099), (64, 256), (1, 20001), (1500, 77), (1030, 9000)])
 def test_quantize_is_exact(stq, dtype, n, k):
     x = _rand((n, k), 7 * n + k).to(dtype)
     q, s = stq.q8_quantize_rows(x.cuda())
@@ -121,7 +121,8 @@ def _check(y, a, sa, w, sw):
 
 SHAPES = [(1, 1, 1), (1, 64, 16), (1, 4096, 7168), (2, 100, 130), (7, 333, 1000), (16, 65, 4096), (17, 64, 127),
           (33, 129, 257), (64, 1003, 2049), (65, 128, 128), (100, 77, 15), (128, 256, 512), (129, 513, 333),
-          (300, 200, 1111), (512, 640, 4096), (1000, 1000, 100), (257, 300, 20000)]
+          (300, 200, 1111), (512, 640, 4096), (1000, 1000, 100), (257, 300, 20000), (5, 9001, 320), (20, 20011, 500), (50, 17000, 777),
+          (1100, 2100, 200), (2100, 4200, 300), (2048, 4096, 1024)]
 
 
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
@@ -190,11 +191,10 @@ def test_linear_under_graph_and_on_another_stream(stq, m):
     x = _rand((m, k), 22).bfloat16().cuda()
     q, s = stq.q8_quantize_rows(x)
     y = torch.empty((m, n), dtype=torch.bfloat16, device="cuda")
-    ws = torch.empty(max(1, stq.q8_matmul_workspace(m, n, k)), dtype=torch.uint8, device="cuda")
 
     def call():
         stq.q8_quantize_rows(x, out=q, scale=s)
-        stq.q8_matmul(q, s, W, sw, out=y, workspace=ws)
+        stq.q8_matmul(q, s, W, sw, out=y)
     call()
     torch.cuda.synchronize()
     side = torch.cuda.Stream()
