@@ -28,6 +28,9 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / 64;
 constexpr int kCap = 1024;           // candidates ranked at once
+constexpr int kMaxTop = 32;
+constexpr int kMaxSplits = 64;       // one lane each where they are joined
+static_assert(kMaxTop * kMaxTop <= kCap, "the join's candidates fit");
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kFloor = -200.0f;    // exp2 of anything at or below this is 0 in fp32
@@ -47,20 +50,31 @@ __device__ __forceinline__ float key_value(uint64_t k) {
 }
 __device__ __forceinline__ uint32_t key_pos(uint64_t k) { return 0xFFFFFFFFu - static_cast<uint32_t>(k); }
 
-// Running maximum, sum of exponentials and their first moment (in units of
-// log2, relative to the maximum).
+// Running maximum m, sum of 2^x and first moment of x, x = l log2(e) - m2.
 struct Stat {
   float m, s, t;
 };
+
+// Maxima so large that m2's rounding is no longer small, or overflows (the
+// type's lowest value as a mask on a whole row, say): x is (l - m) log2(e).
+__device__ __forceinline__ bool wide(float m) { return fabsf(m) > 1024.0f; }
+__device__ __forceinline__ float m2_of(float m) { return m * kLog2e; }
+// What x holds beyond (l - m) log2(e): m log2(e) - m2, exactly
+__device__ __forceinline__ float excess(float m) { return wide(m) ? 0.0f : fmaf(m, kLog2e, -m2_of(m)); }
 
 __device__ __forceinline__ void rescale(Stat& a, float m) {
   if (a.m == -INFINITY) {        // nothing but masked logits (or NaN, which s keeps) so far
     a.m = m;
     return;
   }
-  const float dlt = fmaxf((a.m - m) * kLog2e, kFloor);
+  float dlt;
+  {
+#pragma clang fp contract(off)
+    dlt = wide(a.m) || wide(m) ? (a.m - m) * kLog2e - excess(a.m) + excess(m) : m2_of(a.m) - m2_of(m);
+  }
+  dlt = fmaxf(dlt, kFloor);
   const float f = __builtin_amdgcn_exp2f(dlt);
-  a.t = f * (a.t + a.s * dlt);
+  a.t = f * fmaf(a.s, dlt, a.t);
   a.s *= f;
   a.m = m;
 }
@@ -72,9 +86,45 @@ __device__ __forceinline__ Stat merge(Stat a, Stat b) {
   return Stat{m, a.s + b.s, a.t + b.t};
 }
 
-__device__ __forceinline__ uint64_t shfl64(uint64_t v, int src) {
-  const uint32_t lo = __shfl(static_cast<uint32_t>(v), src);
-  const uint32_t hi = __shfl(static_cast<uint32_t>(v >> 32), src);
+// Reductions over a wavefront: row shifts inside 16 lanes, then the row
+// broadcasts; every lane gets the result.
+template <int kCtrl>
+__device__ __forceinline__ float dpp(float old, float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, old), __builtin_bit_cast(int, v),
+                                                               kCtrl, 0xF, 0xF, false));
+}
+__device__ __forceinline__ float last_lane(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+}
+__device__ __forceinline__ float wave_max(float v) {
+  v = fmaxf(v, dpp<0x111>(v, v));
+  v = fmaxf(v, dpp<0x112>(v, v));
+  v = fmaxf(v, dpp<0x114>(v, v));
+  v = fmaxf(v, dpp<0x118>(v, v));
+  v = fmaxf(v, dpp<0x142>(v, v));
+  v = fmaxf(v, dpp<0x143>(v, v));
+  return last_lane(v);
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v += dpp<0x111>(0.0f, v);
+  v += dpp<0x112>(0.0f, v);
+  v += dpp<0x114>(0.0f, v);
+  v += dpp<0x118>(0.0f, v);
+  // lane 15 (then 31) of the rows below into the rows above only
+  v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x142, 0xA, 0xF, false));
+  v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x143, 0xC, 0xF, false));
+  return last_lane(v);
+}
+__device__ __forceinline__ Stat merge_wave(Stat st) {
+  const float m = wave_max(st.m);
+  if (st.m < m) rescale(st, m);
+  return Stat{m, wave_sum(st.s), wave_sum(st.t)};
+}
+
+// Lane j's value, j the same for every lane
+__device__ __forceinline__ uint64_t lane64(uint64_t v, int j) {
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(v), j);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(v >> 32), j);
   return (static_cast<uint64_t>(hi) << 32) | lo;
 }
 
@@ -114,22 +164,25 @@ struct Row<uint16_t> {
 template <typename T>
 struct RowView {
   const T* p;
-  int64_t vocab;
+  int vocab;
   int skew;
-  int64_t chunks;
-  __device__ __forceinline__ RowView(const T* row, int64_t n) : p(row), vocab(n) {
+  int chunks;
+  __device__ __forceinline__ RowView(const T* row, int64_t n) : p(row), vocab(static_cast<int>(n)) {
     skew = static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
-    chunks = (n + skew + Row<T>::kE - 1) / Row<T>::kE;
+    chunks = (vocab + skew + Row<T>::kE - 1) / Row<T>::kE;
   }
-  __device__ __forceinline__ int64_t first(int64_t c) const { return c * Row<T>::kE - skew; }
-  __device__ __forceinline__ bool whole(int64_t c) const {
-    const int64_t i = first(c);
+  __device__ __forceinline__ int first(int c) const { return c * Row<T>::kE - skew; }
+  __device__ __forceinline__ bool whole(int c) const {
+    const int i = first(c);
     return i >= 0 && i + Row<T>::kE <= vocab;
   }
-  __device__ __forceinline__ void load(int64_t c, float (&v)[Row<T>::kE]) const {
-    const int64_t i0 = first(c);
+  __device__ __forceinline__ u32x4_t raw(int c) const {  // a whole chunk
+    return *reinterpret_cast<const u32x4_t*>(p + first(c));
+  }
+  __device__ __forceinline__ void load(int c, float (&v)[Row<T>::kE]) const {
+    const int i0 = first(c);
     if (whole(c)) {
-      Row<T>::unpack(*reinterpret_cast<const u32x4_t*>(p + i0), v);
+      Row<T>::unpack(raw(c), v);
     } else {
 #pragma unroll
       for (int i = 0; i < Row<T>::kE; ++i)
@@ -182,22 +235,20 @@ __device__ __forceinline__ void rank_out(const uint64_t* cand, int count, int n,
 // n-th largest of the 64 keys held one per lane by a wavefront (0 if fewer
 // than n are nonzero), n <= 64.
 __device__ __forceinline__ uint64_t nth_of_wave(uint64_t k, int n) {
+  if (k == 0) k = threadIdx.x & 63;  // below every key, and all keys differ
   int rank = 0;
-  const int lane = threadIdx.x & 63;
-  for (int j = 0; j < 64; ++j) {
-    const uint64_t o = shfl64(k, j);
-    rank += (o > k) || (o == k && j < lane);
-  }
-  const uint64_t hit = __ballot(rank == n - 1);
-  return shfl64(k, __builtin_ctzll(hit));
+#pragma unroll
+  for (int j = 0; j < 64; ++j) rank += lane64(k, j) > k;
+  const uint64_t b = lane64(k, __builtin_ctzll(__ballot(rank == n - 1)));
+  return b < 64 ? 0 : b;
 }
 
 // The n largest elements of the workgroup's chunks [c0, c1): out(rank, key).
 // best / best_chunk: this thread's largest value and the first of its chunks
 // that holds it (best_chunk < 0: no chunk).
 template <typename T, typename F>
-__device__ __forceinline__ void select_top(const RowView<T>& row, int64_t c0, int64_t c1, int n, float best,
-                                           int64_t best_chunk, SelectSmem& sh, F out) {
+__device__ __forceinline__ void select_top(const RowView<T>& row, int c0, int c1, int n, float best,
+                                           int best_chunk, SelectSmem& sh, F out) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const uint64_t mine = best_chunk < 0 ? 0 : make_key(best, static_cast<uint32_t>(best_chunk));
   sh.lane_key[wave][lane] = mine;
@@ -219,16 +270,15 @@ __device__ __forceinline__ void select_top(const RowView<T>& row, int64_t c0, in
   __syncthreads();
   // every chunk of those threads, dealt over the workgroup
   const int n_thr = sh.n_thr;
-  const int64_t span = c1 - c0;
-  const int per = static_cast<int>((span + kThreads - 1) / kThreads);
+  const int per = (c1 - c0 + kThreads - 1) / kThreads;
   auto scan = [&](auto visit) {
     for (int64_t w = tid; w < static_cast<int64_t>(n_thr) * per; w += kThreads) {
       const int j = static_cast<int>(w / per);
-      const int64_t c = c0 + sh.thr[j] + (w - static_cast<int64_t>(j) * per) * kThreads;
+      const int c = c0 + sh.thr[j] + static_cast<int>(w - static_cast<int64_t>(j) * per) * kThreads;
       if (c >= c1) continue;
       float v[Row<T>::kE];
       row.load(c, v);
-      const int64_t i0 = row.first(c);
+      const int i0 = row.first(c);
 #pragma unroll
       for (int i = 0; i < Row<T>::kE; ++i) {
         if (i0 + i < 0 || i0 + i >= row.vocab) continue;
@@ -270,18 +320,21 @@ __device__ __forceinline__ void select_top(const RowView<T>& row, int64_t c0, in
 struct Result {
   Stat a;
   bool ok;
-  float log_s;  // the library's logf: the hardware's log2 loses digits where a likely token leaves s near 1
+  float log_s;   // log of the sum as it is (the library's logf: the hardware's log2 loses digits where a likely
+                 // token leaves s near 1)
+  float log_sm;  // relative to m itself: m2's rounding taken out
   __device__ __forceinline__ explicit Result(const Stat& st) : a(st) {
     ok = st.s > 0.0f && st.s < INFINITY;
     log_s = ok ? logf(st.s) : 0.0f;
+    log_sm = fmaf(-kLn2, excess(st.m), log_s);
   }
   __device__ __forceinline__ float lse() const {
     if (!ok) return a.s == 0.0f ? -INFINITY : NAN;
-    return a.m + log_s;
+    return a.m + log_sm;
   }
   __device__ __forceinline__ float logprob(float l) const {
     if (!ok) return NAN;
-    return (l - a.m) - log_s;
+    return (l - a.m) - log_sm;
   }
   __device__ __forceinline__ float entropy() const { return ok ? log_s - kLn2 * (a.t / a.s) : NAN; }
 };
@@ -302,31 +355,46 @@ __device__ __forceinline__ void write_top(const LArgs& a, int64_t r, const Resul
   a.top_lp[r * a.top_n + rank] = ok ? res.logprob(key_value(k)) : NAN;
 }
 
-__device__ __forceinline__ Stat merge_wave(Stat st) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) {
-    const Stat b{__shfl_xor(st.m, o), __shfl_xor(st.s, o), __shfl_xor(st.t, o)};
-    st = merge(st, b);
-  }
-  return st;
-}
-
-// Workgroup (split, row).
+// Workgroup (split, row): thread i takes chunks c0 + i, c0 + i + 512, ..., four
+// loads in flight.
 template <typename T>
-__global__ __launch_bounds__(kThreads) void logprobs_kernel(LArgs a) {
+__global__ __launch_bounds__(kThreads, 8) void logprobs_kernel(LArgs a) {
   __shared__ SelectSmem sh;
   __shared__ Stat wst[kWaves];
   constexpr int kE = Row<T>::kE;
+  constexpr int kFlight = 4;
   const int tid = threadIdx.x;
   const int split = blockIdx.x % a.splits;
   const int64_t r = blockIdx.x / a.splits;
   const RowView<T> row(static_cast<const T*>(a.logits) + r * a.stride, a.vocab);
-  const int64_t c0 = min(row.chunks, split * a.per), c1 = min(row.chunks, c0 + a.per);
+  const int c0 = static_cast<int>(min(static_cast<int64_t>(row.chunks), split * a.per));
+  const int c1 = static_cast<int>(min(static_cast<int64_t>(row.chunks), c0 + a.per));
 
   Stat st{-INFINITY, 0.0f, 0.0f};
   float best = -INFINITY;
-  int64_t best_chunk = -1;
-  auto take = [&](const float (&v)[kE], int64_t c) {
+  int best_chunk = -1;
+  auto add = [&](const float (&v)[kE]) {
+    const float m = st.m == -INFINITY ? 0.0f : st.m;
+    if (!wide(m)) {
+      const float m2 = m2_of(m);
+#pragma unroll
+      for (int i = 0; i < kE; ++i) {
+        const float x = fmaf(v[i], kLog2e, -m2);
+        const float e = __builtin_amdgcn_exp2f(x);
+        st.s += e;
+        st.t = fmaf(e, fmaxf(x, kFloor), st.t);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kE; ++i) {
+        const float x = (v[i] - m) * kLog2e;
+        const float e = __builtin_amdgcn_exp2f(x);
+        st.s += e;
+        st.t = fmaf(e, fmaxf(x, kFloor), st.t);
+      }
+    }
+  };
+  auto top = [&](const float (&v)[kE], int c) {
     float cm = v[0];
 #pragma unroll
     for (int i = 1; i < kE; ++i) cm = fmaxf(cm, v[i]);
@@ -334,21 +402,40 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LArgs a) {
       best = cm;
       best_chunk = c;
     }
-    if (cm > st.m) rescale(st, cm);
-    const float m = st.m == -INFINITY ? 0.0f : st.m;
-#pragma unroll
-    for (int i = 0; i < kE; ++i) {
-      const float x = (v[i] - m) * kLog2e;
-      const float e = __builtin_amdgcn_exp2f(x);
-      st.s += e;
-      st.t = fmaf(e, fmaxf(x, kFloor), st.t);
-    }
   };
-  for (int64_t c = c0 + tid; c < c1; c += kThreads) {
+  auto one = [&](int c) {
     float v[kE];
     row.load(c, v);
-    take(v, c);
+    top(v, c);
+    if (best > st.m) rescale(st, best);
+    add(v);
+  };
+  int c = c0 + tid;
+  if (c < c1 && !row.whole(c)) {  // the row's first chunk, if it starts inside one (or its only one)
+    one(c);
+    c += kThreads;
   }
+  const int cw = c1 - (c1 > c0 && !row.whole(c1 - 1) ? 1 : 0);  // whole chunks end here
+  for (; c + (kFlight - 1) * kThreads < cw; c += kFlight * kThreads) {
+    u32x4_t w[kFlight];
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f) w[f] = row.raw(c + f * kThreads);
+    // the running maximum moves at most once per four chunks
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f) {
+      float v[kE];
+      Row<T>::unpack(w[f], v);
+      top(v, c + f * kThreads);
+    }
+    if (best > st.m) rescale(st, best);
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f) {
+      float v[kE];
+      Row<T>::unpack(w[f], v);
+      add(v);
+    }
+  }
+  for (; c < c1; c += kThreads) one(c);
   st = merge_wave(st);
   if ((tid & 63) == 0) wst[tid >> 6] = st;
   __syncthreads();
@@ -372,29 +459,34 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LArgs a) {
 }
 
 // Joins the splits of a row: one workgroup a row.  Every split's list is
-// sorted, so the n-th largest of the lists' heads (64 lanes' maxima of them)
-// bounds the n-th largest key, as in select_top.
+// sorted, so the n-th largest of the lists' heads bounds the n-th largest key,
+// as in select_top.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void logprobs_join_kernel(LArgs a) {
   __shared__ uint64_t cand[kCap];
   __shared__ uint64_t bound;
   __shared__ int count;
   __shared__ Stat total;
+  constexpr int kKeys = kMaxSplits * kMaxTop / kThreads;
   const int tid = threadIdx.x;
   const int64_t r = blockIdx.x;
   const uint64_t* keys = a.keys + r * a.splits * a.top_n;
+  const int n_keys = a.splits * a.top_n;
+  uint64_t mine[kKeys];
+#pragma unroll
+  for (int i = 0; i < kKeys; ++i) mine[i] = tid + i * kThreads < n_keys ? keys[tid + i * kThreads] : 0;
   if (tid == 0) count = 0;
   if (tid < 64) {
     Stat st{-INFINITY, 0.0f, 0.0f};
-    for (int s = tid; s < a.splits; s += 64) {
-      const float4 v = *reinterpret_cast<const float4*>(a.stats + (r * a.splits + s) * 4);
-      st = merge(st, Stat{v.x, v.y, v.z});
+    uint64_t head = 0;
+    if (tid < a.splits) {
+      const float4 v = *reinterpret_cast<const float4*>(a.stats + (r * a.splits + tid) * 4);
+      st = Stat{v.x, v.y, v.z};
+      if (a.top_n) head = keys[tid * a.top_n];
     }
     st = merge_wave(st);
     if (a.top_n) {
-      uint64_t k = 0;
-      for (int s = tid; s < a.splits; s += 64) k = max(k, keys[static_cast<int64_t>(s) * a.top_n]);
-      const uint64_t b = nth_of_wave(k, a.top_n);
+      const uint64_t b = nth_of_wave(head, a.top_n);
       if (tid == 0) bound = b;
     }
     if (tid == 0) total = st;
@@ -403,10 +495,10 @@ __global__ __launch_bounds__(kThreads) void logprobs_join_kernel(LArgs a) {
   const Result res(total);
   if (tid == 0) write_row<T>(a, r, res);
   if (!a.top_n) return;
-  for (int i = tid; i < a.splits * a.top_n; i += kThreads) {
-    const uint64_t k = keys[i];
-    if (k != 0 && k >= bound) cand[atomicAdd(&count, 1)] = k;
-  }
+  // only the lists whose head reaches the bound hold such keys: top_n^2 at most
+#pragma unroll
+  for (int i = 0; i < kKeys; ++i)
+    if (mine[i] != 0 && mine[i] >= bound) cand[atomicAdd(&count, 1)] = mine[i];
   __syncthreads();
   rank_out(cand, count, a.top_n, [&](int rank, uint64_t k) { write_top(a, r, res, rank, k); });
 }
@@ -434,13 +526,25 @@ __device__ __forceinline__ uint32_t bf16_bits(float f) {
   return __builtin_bit_cast(uint16_t, static_cast<__bf16>(f));
 }
 
+template <typename T>
+__device__ __forceinline__ u32x4_t pack(const float (&v)[Row<T>::kE]) {
+  u32x4_t o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 4) o[i] = __builtin_bit_cast(uint32_t, v[i]);
+    else o[i] = bf16_bits(v[2 * i]) | (bf16_bits(v[2 * i + 1]) << 16);
+  }
+  return o;
+}
+
 constexpr int kBwdThreads = 256;
-constexpr int kBwdChunks = 8;  // chunks per thread
+constexpr int kBwdChunks = 8;       // chunks per thread
+constexpr int kBwdChunksSmall = 2;  // where that would leave CUs idle
 
 // d l_i = g_lp (1[i = target] - p_i) - g_ent p_i (log p_i + H), element by
 // element: workgroup (part, row).  Reads a row once and writes it once; the
 // same thread reads and writes an element, so `out` may be the logits.
-template <typename T>
+template <typename T, int kChunks>
 __global__ __launch_bounds__(kBwdThreads) void logprobs_bwd_kernel(BArgs a, int parts) {
   constexpr int kE = Row<T>::kE;
   const int64_t r = blockIdx.x / parts;
@@ -456,40 +560,51 @@ __global__ __launch_bounds__(kBwdThreads) void logprobs_bwd_kernel(BArgs a, int 
   const float ge = a.g_ent ? a.g_ent[r] : 0.0f;
   const float ent = a.g_ent ? a.entropy[r] : 0.0f;
   const bool empty = lse == -INFINITY;
-  const int64_t base = static_cast<int64_t>(part) * kBwdChunks * kBwdThreads + threadIdx.x;
-#pragma unroll
-  for (int j = 0; j < kBwdChunks; ++j) {
-    const int64_t c = base + j * kBwdThreads;
-    if (c >= row.chunks) break;
-    float v[kE];
-    row.load(c, v);
-    const int64_t i0 = row.first(c);
+  auto grad = [&](float (&v)[kE], int i0) {
 #pragma unroll
     for (int i = 0; i < kE; ++i) {
       const float lp = v[i] - lse;
       const float p = __builtin_amdgcn_exp2f(lp * kLog2e);
-      float d = -p * fmaf(ge, fmaxf(lp, kFloor) + ent, g);
-      if (empty) d = 0.0f;
-      if (i0 + i == tgt) d += empty ? 0.0f : g;
-      v[i] = d;
+      v[i] = empty ? 0.0f : -p * fmaf(ge, fmaxf(lp, kFloor) + ent, g);
     }
+    const int at = tgt - i0;
+    if (at >= 0 && at < kE && !empty) {
+#pragma unroll
+      for (int i = 0; i < kE; ++i)
+        if (i == at) v[i] += g;
+    }
+  };
+  // whole chunks first, all loads in flight together; then the ends of the row
+  // (and everything, where the two rows' phases differ) element by element
+  const int first = part * kChunks * kBwdThreads + threadIdx.x;
+  u32x4_t w[kChunks];
+#pragma unroll
+  for (int j = 0; j < kChunks; ++j) {
+    const int c = first + j * kBwdThreads;
+    if (same && row.whole(c)) w[j] = row.raw(c);
+  }
+#pragma unroll
+  for (int j = 0; j < kChunks; ++j) {
+    const int c = first + j * kBwdThreads;
     if (same && row.whole(c)) {
-      u32x4_t o;
-      if constexpr (sizeof(T) == 4) {
+      float v[kE];
+      Row<T>::unpack(w[j], v);
+      grad(v, row.first(c));
+      __builtin_nontemporal_store(pack<T>(v), reinterpret_cast<u32x4_t*>(out + row.first(c)));
+    }
+  }
+  for (int j = 0; j < kChunks; ++j) {
+    const int c = first + j * kBwdThreads;
+    if (c >= row.chunks || (same && row.whole(c))) continue;
+    float v[kE];
+    row.load(c, v);
+    const int i0 = row.first(c);
+    grad(v, i0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = __builtin_bit_cast(uint32_t, v[i]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = bf16_bits(v[2 * i]) | (bf16_bits(v[2 * i + 1]) << 16);
-      }
-      *reinterpret_cast<u32x4_t*>(out + i0) = o;
-    } else {
-#pragma unroll
-      for (int i = 0; i < kE; ++i) {
-        if (i0 + i < 0 || i0 + i >= a.vocab) continue;
-        if constexpr (sizeof(T) == 4) out[i0 + i] = v[i];
-        else out[i0 + i] = static_cast<T>(bf16_bits(v[i]));
-      }
+    for (int i = 0; i < kE; ++i) {
+      if (i0 + i < 0 || i0 + i >= row.vocab) continue;
+      if constexpr (sizeof(T) == 4) out[i0 + i] = v[i];
+      else out[i0 + i] = static_cast<T>(bf16_bits(v[i]));
     }
   }
 }
@@ -504,7 +619,7 @@ LogprobsPlan plan_logprobs(int64_t rows, int64_t vocab, int elem_bytes, int top_
   const int64_t chunks = (vocab * elem_bytes + 15) / 16 + 1;  // one more where a row starts inside a chunk
   int64_t splits = rows > 0 ? (2 * cus) / rows : 1;
   splits = splits < chunks / kThreads ? splits : chunks / kThreads;
-  if (splits > 64) splits = 64;
+  if (splits > kMaxSplits) splits = kMaxSplits;
   if (splits < 1) splits = 1;
   p.per = (chunks + splits - 1) / splits;
   p.splits = static_cast<int>((chunks + p.per - 1) / p.per);
@@ -533,17 +648,24 @@ hipError_t launch_logprobs(const LogprobsArgs& g, const LogprobsPlan& plan, void
   return hipGetLastError();
 }
 
-int64_t logprobs_bwd_parts(int64_t vocab, int elem_bytes) {
+namespace {
+int64_t bwd_parts(int64_t vocab, int elem_bytes, int chunks_per_thread) {
   const int64_t chunks = (vocab * elem_bytes + 15) / 16 + 1;
-  return (chunks + kBwdThreads * kBwdChunks - 1) / (kBwdThreads * kBwdChunks);
+  return (chunks + kBwdThreads * chunks_per_thread - 1) / (kBwdThreads * chunks_per_thread);
 }
+}  // namespace
+
+int64_t logprobs_bwd_parts(int64_t vocab, int elem_bytes) { return bwd_parts(vocab, elem_bytes, kBwdChunks); }
 
 hipError_t launch_logprobs_bwd(const LogprobsBwdArgs& g, hipStream_t s) {
   const BArgs a{g.logits, g.stride, g.rows, g.vocab, g.targets, g.lse, g.entropy, g.g_lp, g.g_ent, g.out, g.out_stride};
-  const int64_t parts = logprobs_bwd_parts(g.vocab, g.bf16 ? 2 : 4);
+  const int esz = g.bf16 ? 2 : 4;
+  const bool small = g.rows * bwd_parts(g.vocab, esz, kBwdChunks) < 2 * cus_of_stream(s);
+  const int64_t parts = bwd_parts(g.vocab, esz, small ? kBwdChunksSmall : kBwdChunks);
   const dim3 grid(static_cast<unsigned>(g.rows * parts));
-  if (g.bf16) hipLaunchKernelGGL(logprobs_bwd_kernel<uint16_t>, grid, dim3(kBwdThreads), 0, s, a, static_cast<int>(parts));
-  else hipLaunchKernelGGL(logprobs_bwd_kernel<float>, grid, dim3(kBwdThreads), 0, s, a, static_cast<int>(parts));
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(kBwdThreads), 0, s, a, static_cast<int>(parts)); };
+  if (g.bf16) small ? go(logprobs_bwd_kernel<uint16_t, kBwdChunksSmall>) : go(logprobs_bwd_kernel<uint16_t, kBwdChunks>);
+  else small ? go(logprobs_bwd_kernel<float, kBwdChunksSmall>) : go(logprobs_bwd_kernel<float, kBwdChunks>);
   return hipGetLastError();
 }
 
