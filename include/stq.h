@@ -341,10 +341,11 @@ stq_status stq_grouped_swiglu(const uint8_t* w_gate_up, int64_t gate_up_stride_b
  *   NULL otherwise.  The other arguments are as for stq_grouped_swiglu.
  *   workspace, workspace_bytes   at least what
  *             stq_grouped_swiglu_backward_workspace reports
- * dz is formed in fp32 and rounded once for each product: to fp16 after a
- * power-of-two scaling of each row (the decoded weights are fp16 numbers, so
- * they enter exactly) for dx, to bf16 for dw.  Sums are fp32 in a fixed
- * order; dx and dw are rounded from them once.  total_m is at most 2^23. */
+ * dz is formed in fp32 and rounded for each product: for dx to fp16 (after a
+ * power-of-two scaling of each row), and once more times the block scales, so
+ * that the weights' patterns enter exactly; for dw to bf16.  Sums are fp32 in
+ * a fixed order; dx and dw are rounded from them once.  total_m is at most
+ * 2^23. */
 stq_status stq_grouped_swiglu_backward(const uint8_t* w_gate_up, int64_t gate_up_stride_bytes, int64_t n_experts,
                                        int64_t d_model, int64_t d_ff, const uint16_t* x_sorted,
                                        const int32_t* expert_offsets, int64_t total_m, const uint16_t* gate_up,

@@ -9,10 +9,10 @@
 //
 // dz_kernel forms dz once per row in fp32.  The product with W takes it as
 // fp16, each row scaled by a power of two that puts its largest magnitude in
-// [2^14, 2^15): the weights are +-d with d an fp16 number, so they enter the
-// fp16 matrix cores exactly and the only rounding ahead of the fp32 sums is
-// dz's own to 11 bits.  (Folding d into a bf16 operand instead would round
-// twice to 8 bits.)  The product with x takes dz as bf16, x's own type.
+// [2^14, 2^15), and folds the block scales d (fp16 numbers) into it: the
+// weights' patterns enter the fp16 matrix cores exactly, and dz is rounded to
+// 11 bits twice (itself, and times d) ahead of the fp32 sums.  A bf16 operand
+// would round to 8.  The product with x takes dz as bf16, x's own type.
 #include "stq_device.hpp"
 #include "stq_launch.hpp"
 #include "stq_passes.hpp"
@@ -142,23 +142,35 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
 // dx = dz W
 // ---------------------------------------------------------------------------
 // A workgroup of 4 wavefronts owns one 256-weight block column of one expert
-// (256 of dx's columns) and all of the expert's rows in passes of at most 128
-// tokens; the sum runs over the matrix's 64-row tiles, whose runs of that
-// block (2688 bytes) and whose 64 columns of dz stream into LDS one tile
-// ahead.  W enters transposed: an MFMA lane takes 8 consecutive rows of one
-// group of four columns.  Per tile a wavefront turns its 16 groups' codes
-// (lane = row) into bytes laid out [group][row], so a lane fetches its 8 rows'
-// codes with one 8-byte read; each code is the offset of its four fp16 lanes
-// in a 32-entry table.  Byte permutes then pair neighbouring rows into the
-// operands of four column sets (column 4 group + j, j = 0..3) and a packed
-// fp16 product puts in the rows' d.  A lane so ends with four neighbouring
-// columns of every token it holds.
+// (256 of dx's columns) and a pass of at most 96 of its rows; the sum runs
+// over the matrix's 64-row tiles.  W enters transposed: an MFMA lane takes 8
+// consecutive rows of one group of four columns.
+//
+//  * Codes: per tile a wavefront loads the words of its 16 groups (lane = row)
+//    and writes the row's 16 code bytes to LDS; the transposing 8-byte LDS read
+//    hands a lane its group's codes of 8 rows.  Each code is the offset of its
+//    four fp16 lanes (+-1, 0) in a 32-entry table; byte permutes pair
+//    neighbouring rows into the operands of four column sets (column 4 group +
+//    j, j = 0..3), so a lane ends with four neighbouring columns of every token
+//    it holds.
+//  * Scales: d varies along the sum, so it goes into dz: a thread loads 8
+//    columns of a token, multiplies them by the 8 rows' d / D (packed fp16) and
+//    writes them to LDS.  D is a power of two at or above every |d| met so far,
+//    so nothing leaves fp16's range; where a tile raises it the sums are scaled
+//    down once.
+//
+// All of it runs ahead of the matrix cores: while they multiply one 32-row
+// step, the next step's table reads are in flight, and the next tile's codes
+// and dz are written during a tile's first step.  For 16384 rows of 256
+// experts of 4096 x 7168 the products alone take about half the kernel's time;
+// the rest is the instructions of the decode (a form that multiplied d into
+// the weights and transposed the codes in registers had 135 VALU instructions
+// per tile and 34 products, and took 1270 us).
 
 constexpr int kWaves = 4;
 constexpr int kThreads = kWaves * 64;
 constexpr int kXcds = 8;
-constexpr int kMaxTok = 128;
-constexpr int kRecStride = 72;  // bytes between groups' codes: 64 rows, then 8 to spread the banks
+constexpr int kMaxTok = 96;
 constexpr int kRun = kTileRows * kBlockBytes;
 
 struct DxArgs {
@@ -176,11 +188,22 @@ struct DxArgs {
 
 struct DxSmem {
   uint64_t lut[32];                           // four fp16 lanes of each code; at byte 0
-  alignas(16) char a[2][kMaxTok * 128];       // dz: 64 columns of each token, 16-byte chunks swizzled
-  alignas(16) char w[2][3 * 1024];            // the tile's run of the block
-  alignas(16) uint8_t rec[kWaves][16 * kRecStride];
+  alignas(16) char a[2][kMaxTok * 128];       // dz d / D: 64 columns of each token, 16-byte chunks swizzled
+  alignas(16) uint8_t rec[kWaves][kTileRows * 16];  // code bytes, [row][group of the wavefront]
   alignas(16) uint16_t d[kWaves][kTileRows];
 };
+
+// The largest of the lanes' values, as bits of non-negative numbers
+__device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
+  auto step = [&](uint32_t o) { v = max(v, o); };
+  step(__builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false));
+  step(__builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false));
+  step(__builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false));
+  step(__builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false));
+  step(__builtin_amdgcn_update_dpp(0, v, 0x142, 0xF, 0xF, false));
+  step(__builtin_amdgcn_update_dpp(0, v, 0x143, 0xF, 0xF, false));
+  return __builtin_amdgcn_readlane(v, 63);
+}
 
 template <int NT>
 __device__ __forceinline__ void dx_pass(const DxArgs& a, DxSmem& sh, const uint8_t* wexp, int b, int64_t row0, int mt) {
@@ -188,37 +211,111 @@ __device__ __forceinline__ void dx_pass(const DxArgs& a, DxSmem& sh, const uint8
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int q = lane >> 4, r = lane & 15;
   const uint32_t zrow = static_cast<uint32_t>(a.tiles) * 128u;  // bytes of a row of dz
+  // rows past the pass lie past the descriptor's range and read as zeros
   const Rsrc rz = make_rsrc(a.dz + row0 * a.tiles * 64, static_cast<uint32_t>(mt) * zrow);
-  const int n_ins = (mt + 7) >> 3;
-  auto stage = [&](int t, int buf) {
-    for (int j = wave; j < n_ins; j += kWaves) {
-      const int row = j * 8 + (lane >> 3);
-      lds_load16(rz, sh.a[buf] + j * 1024, row * zrow + t * 128 + (((lane & 7) ^ ((row >> 1) & 7)) << 4));
-    }
-    // 168 chunks of 16 bytes, at 1 KB a wavefront instruction
-    const Rsrc rw = make_rsrc(wexp + (static_cast<int64_t>(t) * a.nb + b) * kRun, kRun);
-    if (wave < 3) lds_load16(rw, sh.w[buf] + wave * 1024, wave * 1024 + lane * 16);
+  // dz staging: this thread's chunk (8 columns) of tokens t0, t0 + 32, ...: 32
+  // apart, so the chunk's place in a token's 128 bytes stays the same
+  constexpr int NJ = (NT + 1) / 2;
+  const int t0 = wave * 8 + (lane >> 3);
+  const uint32_t z_first = t0 * zrow + (lane & 7) * 16;
+  char* const z_put = sh.a[0] + t0 * 128 + (((lane & 7) ^ ((t0 >> 1) & 7)) << 4);
+  struct Z {
+    u32x4_t v[NJ];
   };
-  auto make_records = [&](int buf) {
-    const uint8_t* blk = reinterpret_cast<const uint8_t*>(sh.w[buf]) + lane * kBlockBytes;
-    auto half = [&](int off) { return static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(blk + off)); };
-    auto word = [&](int off) { return half(off) | half(off + 2) << 16; };
-    sh.d[wave][lane] = static_cast<uint16_t>(half(0));
-    const uint32_t QH = word(34 + 4 * (wave >> 1));
-    uint8_t* out = sh.rec[wave] + lane;
+  auto load_z = [&](int t) {
+    Z z;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+      z.v[j] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rz, static_cast<int>(z_first + j * 32 * zrow + t * 128), 0, 0));
+    return z;
+  };
+  // This wavefront's words of a tile, lane = row: code words 2w and 2w + 1 (12
+  // aligned bytes around them), select word w / 2 (8 bytes around it) and d.
+  // Rows lie 42 bytes apart: even rows' words start 2 bytes into an aligned one.
+  typedef int v3i __attribute__((ext_vector_type(3)));
+  typedef int v2i __attribute__((ext_vector_type(2)));
+  struct Raw {
+    v3i w;
+    v2i h;
+    uint16_t d;
+  };
+  const int off_w = (lane * kBlockBytes + 2 + 8 * wave) & ~3, off_h = (lane * kBlockBytes + 34 + 4 * (wave >> 1)) & ~3;
+  const uint32_t realign = (lane & 1) ? 0x03020100u : 0x05040302u;  // of (next, this)
+  auto load_raw = [&](int t) {
+    const Rsrc rw = make_rsrc(wexp + (static_cast<int64_t>(t) * a.nb + b) * kRun, kRun);
+    Raw x;
+    x.w = __builtin_amdgcn_raw_buffer_load_b96(rw, off_w, 0, 0);
+    x.h = __builtin_amdgcn_raw_buffer_load_b64(rw, off_h, 0, 0);
+    x.d = __builtin_amdgcn_raw_buffer_load_b16(rw, lane * kBlockBytes, 0, 0);
+    return x;
+  };
+  auto put_codes = [&](const Raw& x) {
+    sh.d[wave][lane] = x.d;
+    const uint32_t QH = __builtin_amdgcn_perm(x.h[1], x.h[0], realign);
+    u32x4_t o;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint32_t W = word(2 + 4 * (2 * wave + i));
+      const uint32_t W = __builtin_amdgcn_perm(x.w[i + 1], x.w[i], realign);
       const int p = 2 * ((2 * wave + i) & 3);
-      // byte j of lo: 8 * code of local group 8i + j; of hi: of 8i + 4 + j
-      const uint32_t lo = ((W << 3) & 0x78787878u) | ((QH << (7 - p)) & 0x80808080u);
-      const uint32_t hi = ((W >> 1) & 0x78787878u) | ((QH << (6 - p)) & 0x80808080u);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        out[(8 * i + j) * kRecStride] = static_cast<uint8_t>(lo >> (8 * j));
-        out[(8 * i + 4 + j) * kRecStride] = static_cast<uint8_t>(hi >> (8 * j));
-      }
+      // byte j: 8 * code of local group 8i + j, then of 8i + 4 + j
+      o[2 * i] = ((W << 3) & 0x78787878u) | ((QH << (7 - p)) & 0x80808080u);
+      o[2 * i + 1] = ((W >> 1) & 0x78787878u) | ((QH << (6 - p)) & 0x80808080u);
     }
+    *reinterpret_cast<u32x4_t*>(sh.rec[wave] + lane * 16) = o;
+  };
+  // D = 2^expo with 2^expo > every |d| so far; below 2^-15 there is nothing to
+  // gain (1 / D has to be an fp16 number)
+  int expo = -15;
+  auto raise = [&](const Raw& x) {
+    const int e = static_cast<int>(wave_umax(x.d & 0x7FFFu) >> 10) - 14;  // |d| < 2^e
+    return max(expo, e);
+  };
+  auto put_z = [&](const Z& z, int buf, int e) {
+    const _Float16 f = __builtin_bit_cast(_Float16, static_cast<uint16_t>(e <= 14 ? (15 - e) << 10 : 0x0400 >> (e - 14)));  // 2^-e
+    const u32x4_t dw = *reinterpret_cast<const u32x4_t*>(&sh.d[wave][8 * (lane & 7)]);
+    f16x2_t d[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = dw[i];
+      d[i] = __builtin_bit_cast(f16x2_t, w) * f;
+    }
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      u32x4_t o;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t w = z.v[j][i];
+        o[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, w) * d[i]);
+      }
+      *reinterpret_cast<u32x4_t*>(z_put + buf * (kMaxTok * 128) + j * 32 * 128) = o;
+    }
+  };
+  typedef int i32x2_t __attribute__((ext_vector_type(2)));
+  typedef __attribute__((address_space(3))) i32x2_t* Lds8;
+  struct Step {
+    u32x2_t v[8];  // four fp16 lanes of each of 8 rows
+  };
+  // 16 lanes hand over 8 rows of 16 codes; lane r takes group r's 8
+  const Lds8 get = reinterpret_cast<Lds8>(reinterpret_cast<uintptr_t>(sh.rec[wave] + lane * 8));
+  auto look_up = [&](int s, Step& p) {
+    const i32x2_t codes = __builtin_amdgcn_ds_read_tr8_b64_v2i32(get + s * 64);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t cw = codes[i >> 2];
+      const uint32_t c = __builtin_amdgcn_ubfe(cw, 8 * (i & 3), 8);
+      p.v[i] = *reinterpret_cast<const u32x2_t*>(reinterpret_cast<const char*>(sh.lut) + c);
+    }
+  };
+  auto combine = [&](const Step& p, f16x8_t (&B)[4]) {
+    u32x4_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        o[j][i] = __builtin_amdgcn_perm(p.v[2 * i + 1][j >> 1], p.v[2 * i][j >> 1], (j & 1) ? 0x07060302u : 0x05040100u);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) B[j] = __builtin_bit_cast(f16x8_t, o[j]);
   };
 
   f32x4_t acc[4][NT];
@@ -227,51 +324,74 @@ __device__ __forceinline__ void dx_pass(const DxArgs& a, DxSmem& sh, const uint8
 #pragma unroll
     for (int t = 0; t < NT; ++t) acc[j][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   const int x = (r >> 1) & 7;
-  stage(0, 0);
-  for (int t = 0; t < a.tiles; ++t) {
-    const int buf = t & 1;
-    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wavefront's share of tile t is in LDS
-    __syncthreads();
-    if (t + 1 < a.tiles) stage(t + 1, buf ^ 1);
-    make_records(buf);
-    // the records and scales are this wavefront's own: LDS serves its instructions in order
-    __builtin_amdgcn_wave_barrier();
+  int oa[2];
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const u32x2_t codes = *reinterpret_cast<const u32x2_t*>(sh.rec[wave] + r * kRecStride + 32 * s + 8 * q);
-      const u32x4_t dw = *reinterpret_cast<const u32x4_t*>(&sh.d[wave][32 * s + 8 * q]);
-      f16x8_t A[NT];
+  for (int s = 0; s < 2; ++s) oa[s] = r * 128 + (((4 * s + q) ^ x) << 4);
+  auto read_a = [&](int buf, int s, f16x8_t (&A)[NT]) {
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
-        A[i] = *reinterpret_cast<const f16x8_t*>(sh.a[buf] + (16 * i + r) * 128 + (((4 * s + q) ^ x) << 4));
-      u32x2_t v[8];
+    for (int i = 0; i < NT; ++i) A[i] = *reinterpret_cast<const f16x8_t*>(sh.a[buf] + 16 * i * 128 + oa[s]);
+  };
+  auto multiply = [&](const f16x8_t (&A)[NT], const f16x8_t (&B)[4]) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t cw = codes[i >> 2];
-        const uint32_t c = __builtin_amdgcn_ubfe(cw, 8 * (i & 3), 8);
-        v[i] = *reinterpret_cast<const u32x2_t*>(reinterpret_cast<const char*>(sh.lut) + c);
-      }
-      u32x4_t B[4];
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t dword = dw[i];
-        const f16x2_t d2 = __builtin_bit_cast(f16x2_t, dword);
+      for (int j = 0; j < 4; ++j) acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(A[i], B[j], acc[j][i], 0, 0, 0);
+  };
+
+  const int last = a.tiles - 1;
+  Raw raw[2];
+  Z z[2];
+  raw[0] = load_raw(0);
+  z[0] = load_z(0);
+  raw[1] = load_raw(min(1, last));
+  z[1] = load_z(min(1, last));
+  put_codes(raw[0]);
+  expo = raise(raw[0]);
+  put_z(z[0], 0, expo);
+  raw[0] = load_raw(min(2, last));
+  z[0] = load_z(min(2, last));
+  f16x8_t A[NT], B[4];
+  Step p;
+  look_up(0, p);
+  combine(p, B);
+  // Tile t; n holds tile t + 1, on its way since tile t - 1, and then takes t + 3
+  auto tile = [&](int t, int buf, Raw& n, Z& nz) {
+    // this wavefront's dz of tile t is written and its reads of tile t - 1 are
+    // done; then everyone's (loads in flight need not be waited for here)
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    read_a(buf, 0, A);
+    look_up(1, p);  // the second step's codes are taken before the next tile's are written
+    put_codes(n);   // of tile t + 1 (of the last tile once more, unused, at the end)
+    const int next = raise(n);
+    put_z(nz, buf ^ 1, next);
+    n = load_raw(min(t + 3, last));
+    nz = load_z(min(t + 3, last));
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(A, B);
+    __builtin_amdgcn_sched_barrier(0);
+    combine(p, B);
+    read_a(buf, 1, A);
+    look_up(0, p);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(A, B);
+    __builtin_amdgcn_sched_barrier(0);
+    combine(p, B);
+    if (next != expo && t < last) {
+      const float f = ldexpf(1.0f, expo - next);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t even = v[2 * i][j >> 1], odd = v[2 * i + 1][j >> 1];
-          const uint32_t pr = __builtin_amdgcn_perm(odd, even, (j & 1) ? 0x07060302u : 0x05040100u);
-          B[j][i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, pr) * d2);
-        }
-      }
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(A[i], __builtin_bit_cast(f16x8_t, B[j]), acc[j][i], 0, 0, 0);
+        for (int i = 0; i < NT; ++i) acc[j][i] *= f;
+      expo = next;
     }
+  };
+  for (int t = 0; t < last; t += 2) {  // an even number of tiles: the matrix has 512 rows or a multiple
+    tile(t, 0, raw[1], z[1]);
+    tile(t + 1, 1, raw[0], z[0]);
   }
   // dx[row0 + 16i + 4q + e, 256b + 64 wave + 4r + 0..3]
   const int64_t ld = static_cast<int64_t>(a.nb) * kQK;
+  const float big = ldexpf(1.0f, expo);
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
 #pragma unroll
@@ -279,17 +399,13 @@ __device__ __forceinline__ void dx_pass(const DxArgs& a, DxSmem& sh, const uint8
       const int tok = 16 * i + 4 * q + e;
       if (tok >= mt) continue;
       const float inv = a.inv[row0 + tok];
+      float v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = acc[j][i][e] * big * inv;
       *reinterpret_cast<u32x2_t*>(a.dx + (row0 + tok) * ld + b * kQK + 64 * wave + 4 * r) =
-          u32x2_t{bf16_pair(acc[0][i][e] * inv, acc[1][i][e] * inv), bf16_pair(acc[2][i][e] * inv, acc[3][i][e] * inv)};
+          u32x2_t{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
     }
   }
-}
-
-__device__ __forceinline__ void expert_rows(const int32_t* offsets, int e, int64_t total_m, int64_t* lo, int* m) {
-  // clamped to [0, total_m], so that offsets outside the contract reach no row that is not there
-  *lo = min(max(static_cast<int64_t>(offsets[e]), int64_t{0}), total_m);
-  const int64_t hi = min(max(static_cast<int64_t>(offsets[e + 1]), *lo), total_m);
-  *m = static_cast<int>(hi - *lo);
 }
 
 // One workgroup per (pass of an expert's tokens, block), passes found on the
@@ -310,14 +426,15 @@ __global__ __launch_bounds__(kThreads, 2) void swiglu_dx_kernel(DxArgs a) {
     }
     sh.lut[threadIdx.x] = v;
   }
+  __syncthreads();
   const uint8_t* wexp = a.w + static_cast<int64_t>(u.expert) * a.estride;
   switch ((u.mt + 15) >> 4) {
     case 1: dx_pass<1>(a, sh, wexp, b, u.row0, u.mt); break;
     case 2: dx_pass<2>(a, sh, wexp, b, u.row0, u.mt); break;
     case 3: dx_pass<3>(a, sh, wexp, b, u.row0, u.mt); break;
     case 4: dx_pass<4>(a, sh, wexp, b, u.row0, u.mt); break;
-    case 5: case 6: dx_pass<6>(a, sh, wexp, b, u.row0, u.mt); break;
-    default: dx_pass<8>(a, sh, wexp, b, u.row0, u.mt); break;
+    case 5: dx_pass<5>(a, sh, wexp, b, u.row0, u.mt); break;
+    default: dx_pass<6>(a, sh, wexp, b, u.row0, u.mt); break;
   }
 }
 
@@ -345,6 +462,13 @@ struct DwArgs {
   const uint16_t* x;   // bf16 [total_m, n_c]
   uint16_t* dw;        // bf16 [n_experts, n_r, n_c]
 };
+
+__device__ __forceinline__ void expert_rows(const int32_t* offsets, int e, int64_t total_m, int64_t* lo, int* m) {
+  // clamped to [0, total_m], so that offsets outside the contract reach no row that is not there
+  *lo = min(max(static_cast<int64_t>(offsets[e]), int64_t{0}), total_m);
+  const int64_t hi = min(max(static_cast<int64_t>(offsets[e + 1]), *lo), total_m);
+  *m = static_cast<int>(hi - *lo);
+}
 
 __device__ __forceinline__ int tok_swizzle(int t) { return 2 * ((t & 3) | ((t >> 1) & 4)); }
 

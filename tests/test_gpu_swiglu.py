@@ -10,8 +10,12 @@ e = u (2 |g| + 10) relative.  So
     h        1.1 dg (|u| + du) + |silu(g)| du + e |h| + b |h|     (silu' < 1.1)
     gate_up  dz + b |z|
     dz       |dh u| e s (1 + 2 |g|) and |dh g s| e for the two halves, then
-             its rounding: f |dz| + 2^-39 max |dz| of the row (fp16, scaled so
-             that the row's largest is at least 2^14) or b |dz| (bf16)
+             its roundings: for dx two to fp16, dz itself and its product with
+             the block scale d / D, 2 f |dz| |w|; dz is scaled so that the row's
+             largest is at least 2^14, where a subnormal step errs by 2^-25,
+             2^-39 of it, and once more for the product, 2^-39 max |dz| times
+             D, a power of two at most twice the largest |d| of the column block
+             (or 2^-15); for dw one to bf16, b |dz|
     dx, dw   the sums of those against the other factor's magnitudes, the
              accumulation, and b of the result."""
 import numpy as np
@@ -97,8 +101,11 @@ class Case:
         return self.stq.grouped_swiglu_backward(*self.args(), self.gu, self.dh, **kw)
 
     def dx_tol(self, dz, err, w):
-        t = err + 2.0 ** -11 * dz.abs() + 2.0 ** -39 * dz.abs().amax(1, keepdim=True)
-        return (t + 2 * U * (2 * self.f / 32 + 40) * dz.abs()) @ w.abs()
+        F = 2.0 ** -11
+        top = 2.0 ** -39 * dz.abs().amax(1, keepdim=True)
+        t = (err + F * dz.abs() + top) * (1 + F) + F * dz.abs()
+        D = 2 * w.abs().amax(0).view(-1, QK).amax(1).clamp(min=2.0 ** -16).repeat_interleave(QK)   # per column
+        return (t + 2 * U * (2 * self.f / 32 + 40) * dz.abs()) @ w.abs() + top * 2 * self.f * D
 
     def check_backward(self, dx, dw):
         dz, err = self.dz_ref()
