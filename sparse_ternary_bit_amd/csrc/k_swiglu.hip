@@ -161,7 +161,7 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
 //
 // All of it runs ahead of the matrix cores: while they multiply one 32-row
 // step, the next step's table reads are in flight, and the next tile's codes
-// and dz are written during a tile's first step.  For 16384 rows of 256
+// and dz are written between a tile's two steps.  For 16384 rows of 256
 // experts of 4096 x 7168 the products alone take about half the kernel's time;
 // the rest is the instructions of the decode (a form that multiplied d into
 // the weights and transposed the codes in registers had 135 VALU instructions
@@ -171,6 +171,7 @@ constexpr int kWaves = 4;
 constexpr int kThreads = kWaves * 64;
 constexpr int kXcds = 8;
 constexpr int kMaxTok = 96;
+constexpr int kRing = 8;            // a power of two, at least 5 (see the order of a tile)
 constexpr int kRun = kTileRows * kBlockBytes;
 
 struct DxArgs {
@@ -189,8 +190,9 @@ struct DxArgs {
 struct DxSmem {
   uint64_t lut[32];                           // four fp16 lanes of each code; at byte 0
   alignas(16) char a[2][kMaxTok * 128];       // dz d / D: 64 columns of each token, 16-byte chunks swizzled
+  alignas(16) char w[kRing][3 * 1024];        // the tiles' runs of the block, here or on their way
   alignas(16) uint8_t rec[kWaves][kTileRows * 16];  // code bytes, [row][group of the wavefront]
-  alignas(16) uint16_t d[kWaves][kTileRows];
+  alignas(16) uint16_t d[2][kWaves][kTileRows];
 };
 
 // The largest of the lanes' values, as bits of non-negative numbers
@@ -207,7 +209,12 @@ __device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
 
 template <int NT>
 __device__ __forceinline__ void dx_pass(const DxArgs& a, DxSmem& sh, const uint8_t* wexp, int b, int64_t row0, int mt) {
-  const int tid = threadIdx.x, lane = tid & 63;
+  // through an opaque move: what derives from the thread index is then computed
+  // in each instantiation instead of being hoisted ahead of their choice, where
+  // it would cost registers
+  int tid;
+  asm volatile("v_mov_b32 %0, %1" : "=v"(tid) : "v"(static_cast<int>(threadIdx.x)));
+  const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int q = lane >> 4, r = lane & 15;
   const uint32_t zrow = static_cast<uint32_t>(a.tiles) * 128u;  // bytes of a row of dz
@@ -229,28 +236,32 @@ __device__ __forceinline__ void dx_pass(const DxArgs& a, DxSmem& sh, const uint8
       z.v[j] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rz, static_cast<int>(z_first + j * 32 * zrow + t * 128), 0, 0));
     return z;
   };
+  // the tile's run of this block: 168 pieces of 16 bytes, 1 KB a wavefront
+  auto stage_w = [&](int t) {
+    const Rsrc rw = make_rsrc(wexp + (static_cast<int64_t>(t) * a.nb + b) * kRun, kRun);
+    if (wave < 3) lds_load16(rw, sh.w[t % kRing] + wave * 1024, wave * 1024 + lane * 16);
+  };
   // This wavefront's words of a tile, lane = row: code words 2w and 2w + 1 (12
-  // aligned bytes around them), select word w / 2 (8 bytes around it) and d.
-  // Rows lie 42 bytes apart: even rows' words start 2 bytes into an aligned one.
-  typedef int v3i __attribute__((ext_vector_type(3)));
-  typedef int v2i __attribute__((ext_vector_type(2)));
+  // aligned bytes around them) and select word w / 2 (8 bytes around it).  Rows
+  // lie 42 bytes apart: even rows' words start 2 bytes into an aligned one.
+  // (Loaded straight from memory, 42 bytes apart, they kept the L1's return
+  // path busy 83 % of the time.)
   struct Raw {
-    v3i w;
-    v2i h;
-    uint16_t d;
+    uint32_t w[3], h[2];
   };
   const int off_w = (lane * kBlockBytes + 2 + 8 * wave) & ~3, off_h = (lane * kBlockBytes + 34 + 4 * (wave >> 1)) & ~3;
   const uint32_t realign = (lane & 1) ? 0x03020100u : 0x05040302u;  // of (next, this)
-  auto load_raw = [&](int t) {
-    const Rsrc rw = make_rsrc(wexp + (static_cast<int64_t>(t) * a.nb + b) * kRun, kRun);
+  auto read_raw = [&](int t) {
+    const char* base = sh.w[t % kRing];
     Raw x;
-    x.w = __builtin_amdgcn_raw_buffer_load_b96(rw, off_w, 0, 0);
-    x.h = __builtin_amdgcn_raw_buffer_load_b64(rw, off_h, 0, 0);
-    x.d = __builtin_amdgcn_raw_buffer_load_b16(rw, lane * kBlockBytes, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) x.w[i] = *reinterpret_cast<const uint32_t*>(base + off_w + 4 * i);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) x.h[i] = *reinterpret_cast<const uint32_t*>(base + off_h + 4 * i);
     return x;
   };
+  auto read_d = [&](int t) { return *reinterpret_cast<const uint16_t*>(sh.w[t % kRing] + lane * kBlockBytes); };
   auto put_codes = [&](const Raw& x) {
-    sh.d[wave][lane] = x.d;
     const uint32_t QH = __builtin_amdgcn_perm(x.h[1], x.h[0], realign);
     u32x4_t o;
 #pragma unroll
@@ -266,13 +277,14 @@ __device__ __forceinline__ void dx_pass(const DxArgs& a, DxSmem& sh, const uint8
   // D = 2^expo with 2^expo > every |d| so far; below 2^-15 there is nothing to
   // gain (1 / D has to be an fp16 number)
   int expo = -15;
-  auto raise = [&](const Raw& x) {
-    const int e = static_cast<int>(wave_umax(x.d & 0x7FFFu) >> 10) - 14;  // |d| < 2^e
-    return max(expo, e);
+  auto raise = [&](uint16_t d, int e) {
+    const uint32_t mag = d & 0x7FFFu;
+    if (__ballot(mag >= static_cast<uint32_t>(e + 15) << 10) == 0) return e;  // every |d| < 2^e
+    return max(e, static_cast<int>(wave_umax(mag) >> 10) - 14);
   };
-  auto put_z = [&](const Z& z, int buf, int e) {
+  auto read_scales = [&](int slot) { return *reinterpret_cast<const u32x4_t*>(&sh.d[slot][wave][8 * (lane & 7)]); };
+  auto put_z = [&](const Z& z, const u32x4_t& dw, int buf, int e) {
     const _Float16 f = __builtin_bit_cast(_Float16, static_cast<uint16_t>(e <= 14 ? (15 - e) << 10 : 0x0400 >> (e - 14)));  // 2^-e
-    const u32x4_t dw = *reinterpret_cast<const u32x4_t*>(&sh.d[wave][8 * (lane & 7)]);
     f16x2_t d[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -290,15 +302,25 @@ __device__ __forceinline__ void dx_pass(const DxArgs& a, DxSmem& sh, const uint8
       *reinterpret_cast<u32x4_t*>(z_put + buf * (kMaxTok * 128) + j * 32 * 128) = o;
     }
   };
-  typedef int i32x2_t __attribute__((ext_vector_type(2)));
-  typedef __attribute__((address_space(3))) i32x2_t* Lds8;
   struct Step {
     u32x2_t v[8];  // four fp16 lanes of each of 8 rows
   };
-  // 16 lanes hand over 8 rows of 16 codes; lane r takes group r's 8
-  const Lds8 get = reinterpret_cast<Lds8>(reinterpret_cast<uintptr_t>(sh.rec[wave] + lane * 8));
-  auto look_up = [&](int s, Step& p) {
-    const i32x2_t codes = __builtin_amdgcn_ds_read_tr8_b64_v2i32(get + s * 64);
+  // The tile's codes of both steps: 16 lanes hand over 8 rows of 16 codes, lane
+  // r takes group r's 8.  In one block with the wait for this wavefront's LDS
+  // instructions and the barrier, both due here: the compiler cannot tell the
+  // transposing read from the direct loads to LDS and would wait for those.
+  const uint32_t get = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(sh.rec[wave] + lane * 8));
+  auto take_codes = [&](u32x2_t (&c)[2]) {
+    asm volatile(
+        "ds_read_b64_tr_b8 %0, %2\n\t"
+        "ds_read_b64_tr_b8 %1, %2 offset:512\n\t"
+        "s_waitcnt lgkmcnt(0)\n\t"
+        "s_barrier"
+        : "=&v"(c[0]), "=&v"(c[1])
+        : "v"(get)
+        : "memory");
+  };
+  auto look_up = [&](const u32x2_t& codes, Step& p) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const uint32_t cw = codes[i >> 2];
@@ -327,54 +349,71 @@ __device__ __forceinline__ void dx_pass(const DxArgs& a, DxSmem& sh, const uint8
   int oa[2];
 #pragma unroll
   for (int s = 0; s < 2; ++s) oa[s] = r * 128 + (((4 * s + q) ^ x) << 4);
-  auto read_a = [&](int buf, int s, f16x8_t (&A)[NT]) {
+  f16x8_t A[NT], B[4];
+  auto read_a = [&](int buf, int s, int i) { A[i] = *reinterpret_cast<const f16x8_t*>(sh.a[buf] + 16 * i * 128 + oa[s]); };
+  // One step's products; each token operand is read for the step (buf, s) that
+  // follows as soon as its last use is issued
+  auto multiply = [&](int buf, int s) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i) A[i] = *reinterpret_cast<const f16x8_t*>(sh.a[buf] + 16 * i * 128 + oa[s]);
-  };
-  auto multiply = [&](const f16x8_t (&A)[NT], const f16x8_t (&B)[4]) {
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int i = 0; i < NT; ++i) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(A[i], B[j], acc[j][i], 0, 0, 0);
+      read_a(buf, s, i);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   };
 
-  const int last = a.tiles - 1;
-  Raw raw[2];
+  // Prologue: the first five runs, the scales of tiles 0 and 1, tile 0's codes and dz
+  const int last = a.tiles - 1;  // there are at least 8 tiles
+#pragma unroll
+  for (int t = 0; t < 5; ++t) stage_w(t);
   Z z[2];
-  raw[0] = load_raw(0);
   z[0] = load_z(0);
-  raw[1] = load_raw(min(1, last));
-  z[1] = load_z(min(1, last));
-  put_codes(raw[0]);
-  expo = raise(raw[0]);
-  put_z(z[0], 0, expo);
-  raw[0] = load_raw(min(2, last));
-  z[0] = load_z(min(2, last));
-  f16x8_t A[NT], B[4];
+  asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+  u32x2_t codes[2];
+  int next;  // D's exponent with tile t + 1
+  {
+    const uint16_t d0 = read_d(0), d1 = read_d(1);
+    sh.d[0][wave][lane] = d0;
+    sh.d[1][wave][lane] = d1;
+    put_codes(read_raw(0));
+    expo = raise(d0, expo);
+    next = raise(d1, expo);
+    put_z(z[0], read_scales(0), 0, expo);
+  }
+  z[1] = load_z(1);
+  z[0] = load_z(2);
+  take_codes(codes);
   Step p;
-  look_up(0, p);
+#pragma unroll
+  for (int i = 0; i < NT; ++i) read_a(0, 0, i);
+  look_up(codes[0], p);
   combine(p, B);
-  // Tile t; n holds tile t + 1, on its way since tile t - 1, and then takes t + 3
-  auto tile = [&](int t, int buf, Raw& n, Z& nz) {
-    // this wavefront's dz of tile t is written and its reads of tile t - 1 are
-    // done; then everyone's (loads in flight need not be waited for here)
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    read_a(buf, 0, A);
-    look_up(1, p);  // the second step's codes are taken before the next tile's are written
-    put_codes(n);   // of tile t + 1 (of the last tile once more, unused, at the end)
-    const int next = raise(n);
-    put_z(nz, buf ^ 1, next);
-    n = load_raw(min(t + 3, last));
-    nz = load_z(min(t + 3, last));
+  // Tile t, its first step's operands ready.  nz holds dz of tile t + 1, on its
+  // way since tile t - 2, and then takes t + 3.  The run of tile t + 5 starts
+  // ahead of those loads, so when dz of tile t + 3 has arrived (in tile t + 2)
+  // it has too, and that tile's barrier shows it to every wavefront: its scales
+  // are read in tile t + 3, its codes in tile t + 4.
+  auto tile = [&](int t, int buf, Z& nz) {
+    look_up(codes[1], p);
+    const Raw n = read_raw(t + 1);  // past the last tile: runs read before, not used
+    const uint16_t d = read_d(t + 2);
+    const u32x4_t dw = read_scales(buf ^ 1);
     __builtin_amdgcn_sched_barrier(0);
-    multiply(A, B);
-    __builtin_amdgcn_sched_barrier(0);
+    multiply(buf, 1);
     combine(p, B);
-    read_a(buf, 1, A);
-    look_up(0, p);
+    put_codes(n);
+    put_z(nz, dw, buf ^ 1, next);
+    sh.d[buf][wave][lane] = d;
     __builtin_amdgcn_sched_barrier(0);
-    multiply(A, B);
+    if (t + 5 <= last) stage_w(t + 5);
     __builtin_amdgcn_sched_barrier(0);
+    nz = load_z(min(t + 3, last));
+    // tile t + 1's dz is written and tile t's is read, by everyone
+    take_codes(codes);
+    look_up(codes[0], p);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(buf ^ 1, 0);
     combine(p, B);
     if (next != expo && t < last) {
       const float f = ldexpf(1.0f, expo - next);
@@ -384,10 +423,11 @@ __device__ __forceinline__ void dx_pass(const DxArgs& a, DxSmem& sh, const uint8
         for (int i = 0; i < NT; ++i) acc[j][i] *= f;
       expo = next;
     }
+    if (t + 2 <= last) next = raise(d, next);
   };
   for (int t = 0; t < last; t += 2) {  // an even number of tiles: the matrix has 512 rows or a multiple
-    tile(t, 0, raw[1], z[1]);
-    tile(t + 1, 1, raw[0], z[0]);
+    tile(t, 0, z[1]);
+    tile(t + 1, 1, z[0]);
   }
   // dx[row0 + 16i + 4q + e, 256b + 64 wave + 4r + 0..3]
   const int64_t ld = static_cast<int64_t>(a.nb) * kQK;
