@@ -142,7 +142,7 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
 // dx = dz W
 // ---------------------------------------------------------------------------
 // A workgroup of 4 wavefronts owns one 256-weight block column of one expert
-// (256 of dx's columns) and a pass of at most 96 of its rows; the sum runs
+// (256 of dx's columns) and a pass of at most 80 of its rows; the sum runs
 // over the matrix's 64-row tiles.  W enters transposed: an MFMA lane takes 8
 // consecutive rows of one group of four columns.
 //
@@ -170,7 +170,8 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
 constexpr int kWaves = 4;
 constexpr int kThreads = kWaves * 64;
 constexpr int kXcds = 8;
-constexpr int kMaxTok = 96;
+constexpr int kMaxTok = 80;
+constexpr int kStageTok = (kMaxTok + 31) / 32 * 32;
 constexpr int kRing = 8;            // a power of two, at least 5 (see the order of a tile)
 constexpr int kRun = kTileRows * kBlockBytes;
 
@@ -189,7 +190,9 @@ struct DxArgs {
 
 struct DxSmem {
   uint64_t lut[32];                           // four fp16 lanes of each code; at byte 0
-  alignas(16) char a[2][kMaxTok * 128];       // dz d / D: 64 columns of each token, 16-byte chunks swizzled
+  // dz d / D: 64 columns of each token, 16-byte chunks swizzled; written 32
+  // tokens at a time
+  alignas(16) char a[2][kStageTok * 128];
   alignas(16) char w[kRing][3 * 1024];        // the tiles' runs of the block, here or on their way
   alignas(16) uint8_t rec[kWaves][kTileRows * 16];  // code bytes, [row][group of the wavefront]
   alignas(16) uint16_t d[2][kWaves][kTileRows];
@@ -223,6 +226,7 @@ __device__ __forceinline__ void dx_pass(const DxArgs& a, DxSmem& sh, const uint8
   // dz staging: this thread's chunk (8 columns) of tokens t0, t0 + 32, ...: 32
   // apart, so the chunk's place in a token's 128 bytes stays the same
   constexpr int NJ = (NT + 1) / 2;
+  static_assert(NJ * 32 <= kStageTok, "every token written has its place");
   const int t0 = wave * 8 + (lane >> 3);
   const uint32_t z_first = t0 * zrow + (lane & 7) * 16;
   char* const z_put = sh.a[0] + t0 * 128 + (((lane & 7) ^ ((t0 >> 1) & 7)) << 4);
@@ -299,7 +303,7 @@ __device__ __forceinline__ void dx_pass(const DxArgs& a, DxSmem& sh, const uint8
         const uint32_t w = z.v[j][i];
         o[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, w) * d[i]);
       }
-      *reinterpret_cast<u32x4_t*>(z_put + buf * (kMaxTok * 128) + j * 32 * 128) = o;
+      *reinterpret_cast<u32x4_t*>(z_put + buf * (kStageTok * 128) + j * 32 * 128) = o;
     }
   };
   struct Step {
@@ -320,24 +324,22 @@ __device__ __forceinline__ void dx_pass(const DxArgs& a, DxSmem& sh, const uint8
         : "v"(get)
         : "memory");
   };
-  auto look_up = [&](const u32x2_t& codes, Step& p) {
+  // rows 4h .. 4h + 3 of a lane's 8
+  auto look_up = [&](const u32x2_t& codes, Step& p, int h) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t cw = codes[i >> 2];
+    for (int i = 4 * h; i < 4 * h + 4; ++i) {
+      const uint32_t cw = codes[h];
       const uint32_t c = __builtin_amdgcn_ubfe(cw, 8 * (i & 3), 8);
       p.v[i] = *reinterpret_cast<const u32x2_t*>(reinterpret_cast<const char*>(sh.lut) + c);
     }
   };
-  auto combine = [&](const Step& p, f16x8_t (&B)[4]) {
-    u32x4_t o[4];
+  // their half of the four column sets' operands
+  auto combine = [&](const Step& p, u32x4_t (&o)[4], int h) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 2 * h; i < 2 * h + 2; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         o[j][i] = __builtin_amdgcn_perm(p.v[2 * i + 1][j >> 1], p.v[2 * i][j >> 1], (j & 1) ? 0x07060302u : 0x05040100u);
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) B[j] = __builtin_bit_cast(f16x8_t, o[j]);
   };
 
   f32x4_t acc[4][NT];
@@ -349,16 +351,29 @@ __device__ __forceinline__ void dx_pass(const DxArgs& a, DxSmem& sh, const uint8
   int oa[2];
 #pragma unroll
   for (int s = 0; s < 2; ++s) oa[s] = r * 128 + (((4 * s + q) ^ x) << 4);
-  f16x8_t A[NT], B[4];
+  f16x8_t A[NT];
+  u32x4_t B[2][4];
   auto read_a = [&](int buf, int s, int i) { A[i] = *reinterpret_cast<const f16x8_t*>(sh.a[buf] + 16 * i * 128 + oa[s]); };
-  // One step's products; each token operand is read for the step (buf, s) that
-  // follows as soon as its last use is issued
-  auto multiply = [&](int buf, int s) {
+  // One step's products with B[s].  Each token operand is read for the step
+  // (buf, s ^ 1) that follows as soon as its last use is issued, and `side`, the
+  // work of the steps to come in four pieces, is spread between the products:
+  // a wavefront can issue three other instructions while one product runs.
+  auto multiply = [&](int buf, int s, auto side) {
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(A[i], B[j], acc[j][i], 0, 0, 0);
-      read_a(buf, s, i);
+      for (int j = 0; j < 4; ++j)
+        acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(A[i], __builtin_bit_cast(f16x8_t, B[s][j]), acc[j][i], 0, 0, 0);
+      read_a(buf, s ^ 1, i);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (k * NT / 4 == i) side(k);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // a product
+        __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);  // up to three VALU instructions
+        __builtin_amdgcn_sched_group_barrier(0x300, 2, 0);  // and two of LDS
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
   };
@@ -387,34 +402,37 @@ __device__ __forceinline__ void dx_pass(const DxArgs& a, DxSmem& sh, const uint8
   Step p;
 #pragma unroll
   for (int i = 0; i < NT; ++i) read_a(0, 0, i);
-  look_up(codes[0], p);
-  combine(p, B);
+  for (int h = 0; h < 2; ++h) {
+    look_up(codes[0], p, h);
+    combine(p, B[0], h);
+  }
   // Tile t, its first step's operands ready.  nz holds dz of tile t + 1, on its
   // way since tile t - 2, and then takes t + 3.  The run of tile t + 5 starts
   // ahead of those loads, so when dz of tile t + 3 has arrived (in tile t + 2)
   // it has too, and that tile's barrier shows it to every wavefront: its scales
   // are read in tile t + 3, its codes in tile t + 4.
   auto tile = [&](int t, int buf, Z& nz) {
-    look_up(codes[1], p);
     const Raw n = read_raw(t + 1);  // past the last tile: runs read before, not used
     const uint16_t d = read_d(t + 2);
     const u32x4_t dw = read_scales(buf ^ 1);
-    __builtin_amdgcn_sched_barrier(0);
-    multiply(buf, 1);
-    combine(p, B);
-    put_codes(n);
-    put_z(nz, dw, buf ^ 1, next);
-    sh.d[buf][wave][lane] = d;
-    __builtin_amdgcn_sched_barrier(0);
+    multiply(buf, 0, [&](int k) {
+      if (k < 2) look_up(codes[1], p, k);
+      else combine(p, B[1], k - 2);
+      if (k == 2) put_codes(n);
+      if (k == 3) {
+        put_z(nz, dw, buf ^ 1, next);
+        sh.d[buf][wave][lane] = d;
+      }
+    });
     if (t + 5 <= last) stage_w(t + 5);
     __builtin_amdgcn_sched_barrier(0);
     nz = load_z(min(t + 3, last));
     // tile t + 1's dz is written and tile t's is read, by everyone
     take_codes(codes);
-    look_up(codes[0], p);
-    __builtin_amdgcn_sched_barrier(0);
-    multiply(buf ^ 1, 0);
-    combine(p, B);
+    multiply(buf ^ 1, 1, [&](int k) {
+      if (k < 2) look_up(codes[0], p, k);
+      else combine(p, B[0], k - 2);
+    });
     if (next != expo && t < last) {
       const float f = ldexpf(1.0f, expo - next);
 #pragma unroll
@@ -473,8 +491,7 @@ __global__ __launch_bounds__(kThreads, 2) void swiglu_dx_kernel(DxArgs a) {
     case 2: dx_pass<2>(a, sh, wexp, b, u.row0, u.mt); break;
     case 3: dx_pass<3>(a, sh, wexp, b, u.row0, u.mt); break;
     case 4: dx_pass<4>(a, sh, wexp, b, u.row0, u.mt); break;
-    case 5: dx_pass<5>(a, sh, wexp, b, u.row0, u.mt); break;
-    default: dx_pass<6>(a, sh, wexp, b, u.row0, u.mt); break;
+    default: dx_pass<5>(a, sh, wexp, b, u.row0, u.mt); break;
   }
 }
 
