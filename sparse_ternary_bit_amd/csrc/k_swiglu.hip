@@ -498,16 +498,21 @@ __global__ __launch_bounds__(kThreads, 2) void swiglu_dx_kernel(DxArgs a) {
 // ---------------------------------------------------------------------------
 // dW_e = dz_e^T x_e
 // ---------------------------------------------------------------------------
-// A workgroup owns 128 rows x 128 columns of one expert's dW; the sum runs
-// over the expert's tokens, 64 at a time.  Both operands lie [token][column]
-// while the matrix cores want 8 consecutive tokens of one column, so they are
-// read with the transposing 8-byte LDS read: 16 lanes give four tokens' 16
-// columns and each takes back four tokens of one.  The 32-byte pieces of a
-// token's 256 bytes are XORed by three bits of the token index, so the 16
-// tokens of one such read fall on different banks.
+// A workgroup owns 256 rows x 128 columns of one expert's dW (a wavefront 64 x
+// 128); the sum runs over the expert's tokens, 32 (one matrix-core step) at a
+// time, through three LDS buffers.  Both operands lie [token][column] while
+// the matrix cores want 8 consecutive tokens of one column, so they are read
+// with the transposing 8-byte LDS read: 16 lanes give four tokens' 16 columns
+// and each takes back four tokens of one.  The 16-byte pieces of a token are
+// XORed by three bits of the token index, so the 16 tokens of one such read
+// fall on different banks.  A step's 24 reads per 32 products are issued in
+// one block that ends with their wait: left to the compiler, every one of them
+// also waits for the direct loads to LDS in flight, which it cannot tell apart
+// (439 us for 4099 rows of 8 experts of 4096 x 7168 in that form).
 
-constexpr int kTW = 128;     // tile edge
-constexpr int kTok = 64;     // tokens per stage
+constexpr int kTR = 256, kTC = 128;  // rows and columns of a tile
+constexpr int kTok = 32;             // tokens per stage
+constexpr int kDwBuf = 3;
 
 struct DwArgs {
   int n_experts;
@@ -530,83 +535,111 @@ __device__ __forceinline__ void expert_rows(const int32_t* offsets, int e, int64
 __device__ __forceinline__ int tok_swizzle(int t) { return 2 * ((t & 3) | ((t >> 1) & 4)); }
 
 __global__ __launch_bounds__(kThreads, 2) void swiglu_dw_kernel(DwArgs a) {
-  __shared__ __align__(16) char sz[2][kTok * kTW * 2];
-  __shared__ __align__(16) char sx[2][kTok * kTW * 2];
+  __shared__ __align__(16) char sz[kDwBuf][kTok * kTR * 2];
+  __shared__ __align__(16) char sx[kDwBuf][kTok * kTC * 2];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int q = lane >> 4, r = lane & 15;
-  const int tr = a.n_r / kTW, tc = a.n_c / kTW;
-  int id = blockIdx.x;
-  const int c0 = (id % tc) * kTW;
-  id /= tc;
-  const int r0 = (id % tr) * kTW;
-  const int e = id / tr;
+  // Workgroups are dealt to the XCDs in turn: each takes one run of an
+  // expert's tiles, rows fastest, so that its L2 holds the expert's dz and a
+  // few columns of x.
+  const int tr = a.n_r / kTR, tc = a.n_c / kTC;
+  const int per = (tr * tc + kXcds - 1) / kXcds;
+  const int e = blockIdx.x / (per * kXcds), in = blockIdx.x % (per * kXcds);
+  const int tile = (in % kXcds) * per + in / kXcds;
+  if (tile >= tr * tc) return;
+  const int r0 = (tile % tr) * kTR, c0 = (tile / tr) * kTC;
   int64_t lo;
   int m;
   expert_rows(a.offsets, e, a.total_m, &lo, &m);
   const uint32_t zrow = static_cast<uint32_t>(a.n_r) * 2, xrow = static_cast<uint32_t>(a.n_c) * 2;
-  auto stage = [&](int s, int buf) {
+  // a wavefront instruction brings 2 tokens of dz (32 pieces each), 4 of x (16 each)
+  constexpr int kLoads = kTok / 2 / kWaves + kTok / 4 / kWaves;
+  auto stage = [&](int s) {
+    const int buf = s % kDwBuf;
     const int64_t t0 = lo + static_cast<int64_t>(s) * kTok;
     const int tv = min(kTok, m - s * kTok);
     // tokens past the expert's rows lie past the descriptors' ranges and read as zeros
-    const Rsrc rz = make_rsrc(a.dz + t0 * a.n_r + r0, (tv - 1) * zrow + kTW * 2);
-    const Rsrc rx = make_rsrc(a.x + t0 * a.n_c + c0, (tv - 1) * xrow + kTW * 2);
+    const Rsrc rz = make_rsrc(a.dz + t0 * a.n_r + r0, (tv - 1) * zrow + kTR * 2);
+    const Rsrc rx = make_rsrc(a.x + t0 * a.n_c + c0, (tv - 1) * xrow + kTC * 2);
+#pragma unroll
+    for (int j = 0; j < kTok / 2 / kWaves; ++j) {
+      const int ins = wave + j * kWaves, t = ins * 2 + (lane >> 5);
+      lds_load16(rz, sz[buf] + ins * 1024, t < tv ? t * zrow + ((lane & 31) ^ tok_swizzle(t)) * 16 : 0xFFFFFFF0u);
+    }
 #pragma unroll
     for (int j = 0; j < kTok / 4 / kWaves; ++j) {
-      const int ins = wave + j * kWaves;
-      const int t = ins * 4 + (lane >> 4);
-      const uint32_t piece = static_cast<uint32_t>((lane & 15) ^ tok_swizzle(t)) * 16;
-      lds_load16(rz, sz[buf] + ins * 1024, t < tv ? t * zrow + piece : 0xFFFFFFF0u);
-      lds_load16(rx, sx[buf] + ins * 1024, t < tv ? t * xrow + piece : 0xFFFFFFF0u);
+      const int ins = wave + j * kWaves, t = ins * 4 + (lane >> 4);
+      lds_load16(rx, sx[buf] + ins * 1024, t < tv ? t * xrow + ((lane & 15) ^ tok_swizzle(t)) * 16 : 0xFFFFFFF0u);
     }
   };
-  f32x4_t acc[4][4];  // [column tile][row tile]
+  f32x4_t acc[8][4];  // [column tile][row tile]
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 8; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const int wr = (wave >> 1) * 64, wc = (wave & 1) * 64;
+  // This lane's part of the transposing read of tokens 8q + 0..3 (the other
+  // four lie four tokens' bytes on, in the same swizzle) and 16 columns: token
+  // 8q + r / 4, columns 4 (r % 4) ..+3 of them.  Column tile i is 32 bytes on,
+  // under the swizzle an XOR of 32 i, so one address a tile.
+  const int t = 8 * q + (r >> 2);
+  const int fz = t * kTR * 2, fx = t * kTC * 2, sw = tok_swizzle(t) * 16 + (r & 3) * 8;
+  auto lds = [](const void* p) { return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)); };
   const int ns = (m + kTok - 1) / kTok;
-  // this lane's part of a transposing read of tokens k0 + 0..3 (k0 = 8q, or 8q + 4), columns col..col+15
-  auto frag = [&](const char* base, int step, int col) {
-    u32x4_t v;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int t = 32 * step + 8 * q + 4 * h + (r >> 2);
-      const int byte = t * (kTW * 2) + (((col >> 3) ^ tok_swizzle(t)) << 4) + (r & 3) * 8;
-      const s16x4_t p = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          reinterpret_cast<__attribute__((address_space(3))) s16x4_t*>(reinterpret_cast<uintptr_t>(base + byte)));
-      const u32x2_t w = __builtin_bit_cast(u32x2_t, p);
-      v[2 * h] = w[0];
-      v[2 * h + 1] = w[1];
-    }
-    return __builtin_bit_cast(bf16x8_t, v);
-  };
-  if (ns > 0) stage(0, 0);
+  for (int s = 0; s < kDwBuf - 1; ++s)
+    if (s < ns) stage(s);
   for (int s = 0; s < ns; ++s) {
-    const int buf = s & 1;
-    __builtin_amdgcn_s_waitcnt(0x0F70);
-    __syncthreads();
-    if (s + 1 < ns) stage(s + 1, buf ^ 1);
+    // stage s has landed (s + 1 may be on its way), here and for everyone, and
+    // everyone has read stage s - 1, whose buffer the next loads take
+    if (s + 1 < ns) asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kLoads) : "memory");
+    else asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+    if (s + kDwBuf - 1 < ns) stage(s + kDwBuf - 1);
+    const uint32_t bz = lds(sz[s % kDwBuf]) + fz, bx = lds(sx[s % kDwBuf]) + fx;
+    u32x2_t z[4][2], x[8][2];
+    uint32_t az[4], ax[8];
 #pragma unroll
-    for (int step = 0; step < kTok / 32; ++step) {
-      bf16x8_t X[4], Z[4];
+    for (int j = 0; j < 4; ++j) az[j] = bz + (sw ^ (128 * wave + 32 * j));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) X[i] = frag(sx[buf], step, wc + 16 * i);
+    for (int i = 0; i < 8; ++i) ax[i] = bx + (sw ^ (32 * i));
+    // tokens +4: 4 rows of 512 (dz) or 256 (x) bytes on
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %24\n\tds_read_b64_tr_b16 %1, %24 offset:2048\n\t"
+        "ds_read_b64_tr_b16 %2, %25\n\tds_read_b64_tr_b16 %3, %25 offset:2048\n\t"
+        "ds_read_b64_tr_b16 %4, %26\n\tds_read_b64_tr_b16 %5, %26 offset:2048\n\t"
+        "ds_read_b64_tr_b16 %6, %27\n\tds_read_b64_tr_b16 %7, %27 offset:2048\n\t"
+        "ds_read_b64_tr_b16 %8, %28\n\tds_read_b64_tr_b16 %9, %28 offset:1024\n\t"
+        "ds_read_b64_tr_b16 %10, %29\n\tds_read_b64_tr_b16 %11, %29 offset:1024\n\t"
+        "ds_read_b64_tr_b16 %12, %30\n\tds_read_b64_tr_b16 %13, %30 offset:1024\n\t"
+        "ds_read_b64_tr_b16 %14, %31\n\tds_read_b64_tr_b16 %15, %31 offset:1024\n\t"
+        "ds_read_b64_tr_b16 %16, %32\n\tds_read_b64_tr_b16 %17, %32 offset:1024\n\t"
+        "ds_read_b64_tr_b16 %18, %33\n\tds_read_b64_tr_b16 %19, %33 offset:1024\n\t"
+        "ds_read_b64_tr_b16 %20, %34\n\tds_read_b64_tr_b16 %21, %34 offset:1024\n\t"
+        "ds_read_b64_tr_b16 %22, %35\n\tds_read_b64_tr_b16 %23, %35 offset:1024\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(z[0][0]), "=&v"(z[0][1]), "=&v"(z[1][0]), "=&v"(z[1][1]), "=&v"(z[2][0]), "=&v"(z[2][1]), "=&v"(z[3][0]),
+          "=&v"(z[3][1]), "=&v"(x[0][0]), "=&v"(x[0][1]), "=&v"(x[1][0]), "=&v"(x[1][1]), "=&v"(x[2][0]), "=&v"(x[2][1]),
+          "=&v"(x[3][0]), "=&v"(x[3][1]), "=&v"(x[4][0]), "=&v"(x[4][1]), "=&v"(x[5][0]), "=&v"(x[5][1]), "=&v"(x[6][0]),
+          "=&v"(x[6][1]), "=&v"(x[7][0]), "=&v"(x[7][1])
+        : "v"(az[0]), "v"(az[1]), "v"(az[2]), "v"(az[3]), "v"(ax[0]), "v"(ax[1]), "v"(ax[2]), "v"(ax[3]), "v"(ax[4]),
+          "v"(ax[5]), "v"(ax[6]), "v"(ax[7])
+        : "memory");
+    bf16x8_t Z[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) Z[j] = frag(sz[buf], step, wr + 16 * j);
+    for (int j = 0; j < 4; ++j) Z[j] = __builtin_bit_cast(bf16x8_t, u32x4_t{z[j][0][0], z[j][0][1], z[j][1][0], z[j][1][1]});
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 8; ++i) {
+      const bf16x8_t X = __builtin_bit_cast(bf16x8_t, u32x4_t{x[i][0][0], x[i][0][1], x[i][1][0], x[i][1][1]});
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(X[i], Z[j], acc[i][j], 0, 0, 0);
+      for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(X, Z[j], acc[i][j], 0, 0, 0);
     }
   }
-  // dw[e, r0 + wr + 16j + r, c0 + wc + 16i + 4q + 0..3]
-  uint16_t* out = a.dw + (static_cast<int64_t>(e) * a.n_r + r0 + wr) * a.n_c + c0 + wc;
+  // dw[e, r0 + 64 wave + 16j + r, c0 + 16i + 4q + 0..3]
+  uint16_t* out = a.dw + (static_cast<int64_t>(e) * a.n_r + r0 + 64 * wave) * a.n_c + c0;
 #pragma unroll
   for (int j = 0; j < 4; ++j)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 8; ++i)
       *reinterpret_cast<u32x2_t*>(out + static_cast<int64_t>(16 * j + r) * a.n_c + 16 * i + 4 * q) =
           u32x2_t{bf16_pair(acc[i][j][0], acc[i][j][1]), bf16_pair(acc[i][j][2], acc[i][j][3])};
 }
@@ -648,7 +681,8 @@ hipError_t launch_swiglu_bwd(const SwigluBwdArgs& g, void* ws, hipStream_t s) {
   if (g.dw) {
     DwArgs a{static_cast<int>(g.n_experts), static_cast<int>(2 * g.d_ff), static_cast<int>(g.d_model), g.offsets,
              g.total_m, dzb, g.x, g.dw};
-    const int64_t grid = g.n_experts * (2 * g.d_ff / kTW) * (g.d_model / kTW);
+    const int64_t tiles = (2 * g.d_ff / kTR) * (g.d_model / kTC);
+    const int64_t grid = g.n_experts * ((tiles + kXcds - 1) / kXcds * kXcds);
     hipLaunchKernelGGL(swiglu_dw_kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
