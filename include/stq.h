@@ -321,10 +321,24 @@ stq_status stq_greedy_allocation(const double* gain, const double* extra_bytes, 
  *   gate_up         bf16 [total_m, 2*d_ff] = [g | u], what the backward pass
  *                   reads, or NULL; 8-byte aligned
  * bf16 x ternary products are exact, sums fp32, and h and gate_up are each
- * rounded from the fp32 sums once.  d_ff * row_bytes(d_model) is below 2^31. */
+ * rounded from the fp32 sums once.  Few rows run through stq_gemv's kernels
+ * and need scratch:
+ *   workspace, workspace_bytes   at least what stq_grouped_swiglu_workspace
+ *                   reports for these shapes on this stream's device (may be
+ *                   NULL when that is 0)
+ * d_ff * row_bytes(d_model) is below 2^31, total_m at most 2^23.  Repeated
+ * calls give identical bits; they depend on the form taken (and, through the
+ * GEMV's plan, on the device), as stq_gemv's do. */
 stq_status stq_grouped_swiglu(const uint8_t* w_gate_up, int64_t gate_up_stride_bytes, int64_t n_experts,
                               int64_t d_model, int64_t d_ff, const uint16_t* x_sorted, const int32_t* expert_offsets,
-                              int64_t total_m, uint16_t* h, uint16_t* gate_up, stq_stream_t stream);
+                              int64_t total_m, uint16_t* h, uint16_t* gate_up, void* workspace,
+                              int64_t workspace_bytes, stq_stream_t stream);
+
+/* Workspace bytes stq_grouped_swiglu needs for these shapes on a device with
+ * n_cus compute units (0: the current device's); host only, same checks and
+ * errors as the call.  workspace_bytes is a HOST pointer. */
+stq_status stq_grouped_swiglu_workspace(int64_t n_experts, int64_t d_model, int64_t d_ff, int64_t total_m,
+                                        int32_t n_cus, int64_t* workspace_bytes);
 
 /* Its gradients: with s = 1 / (1 + exp(-g)) and dh the gradient at h,
  *     dg = dh u s (1 + g (1 - s)),   du = dh g s,   dz = [dg | du]

@@ -18,7 +18,8 @@ __all__ = [
     "QK", "BLOCK_BYTES", "ENC_WLS", "ENC_AMAX", "StqError", "lib", "lib_path",
     "row_bytes", "quantize_rows", "dequantize_rows", "gemv", "gemv_noalloc", "gemv_plan", "grouped_gemm",
     "moe_ffn_decode",
-    "moe_ffn_workspace", "grouped_swiglu", "grouped_swiglu_backward", "grouped_swiglu_backward_workspace",
+    "moe_ffn_workspace", "grouped_swiglu", "grouped_swiglu_workspace", "grouped_swiglu_backward",
+    "grouped_swiglu_backward_workspace",
     "q8_quantize_rows", "q8_matmul", "token_logprobs",
     "token_logprobs_workspace", "token_logprobs_backward", "layer_errors", "layer_errors_workspace", "q2_roundtrip", "greedy_allocation",
     "stream_read_probe", "mfma_loop_probe", "lds_read_probe", "MFMA_PROBE_FLOP_PER_ROUND",
@@ -99,8 +100,10 @@ def lib() -> ctypes.CDLL:
     L.stq_greedy_allocation.argtypes = [_c_vp, _c_vp, _c_i64, ctypes.c_double, _c_vp]
     L.stq_greedy_allocation.restype = _c_int
     L.stq_grouped_swiglu.argtypes = [_c_vp, _c_i64, _c_i64, _c_i64, _c_i64, _c_vp, _c_vp, _c_i64, _c_vp, _c_vp,
-                                     _c_vp]
+                                     _c_vp, _c_i64, _c_vp]
     L.stq_grouped_swiglu.restype = _c_int
+    L.stq_grouped_swiglu_workspace.argtypes = [_c_i64, _c_i64, _c_i64, _c_i64, ctypes.c_int32, ctypes.POINTER(_c_i64)]
+    L.stq_grouped_swiglu_workspace.restype = _c_int
     L.stq_grouped_swiglu_backward.argtypes = [_c_vp, _c_i64, _c_i64, _c_i64, _c_i64, _c_vp, _c_vp, _c_i64, _c_vp,
                                               _c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_vp]
     L.stq_grouped_swiglu_backward.restype = _c_int
@@ -449,21 +452,45 @@ def _swiglu_args(w_gate_up, expert_stride, n_experts, d_model, d_ff, x_sorted, o
     return total_m
 
 
+def grouped_swiglu_workspace(n_experts: int, d_model: int, d_ff: int, total_m: int, n_cus: int = 0) -> int:
+    """Workspace bytes grouped_swiglu needs for these shapes on n_cus compute units (0: the
+    current device's); host only."""
+    wb = ctypes.c_int64()
+    _check("stq_grouped_swiglu_workspace",
+           lib().stq_grouped_swiglu_workspace(int(n_experts), int(d_model), int(d_ff), int(total_m), int(n_cus),
+                                              ctypes.byref(wb)))
+    return wb.value
+
+
+@functools.lru_cache(maxsize=256)
+def _swiglu_need(n_experts: int, d_model: int, d_ff: int, total_m: int, n_cus: int, gemv_plan_override) -> int:
+    return grouped_swiglu_workspace(n_experts, d_model, d_ff, total_m, n_cus)
+
+
 def grouped_swiglu(w_gate_up: torch.Tensor, expert_stride: int, n_experts: int, d_model: int, d_ff: int,
                    x_sorted: torch.Tensor, offsets: torch.Tensor, out: torch.Tensor | None = None,
-                   gate_up: torch.Tensor | None = None) -> torch.Tensor:
+                   gate_up: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
     """h = silu(W_gate_e x) * (W_up_e x), bf16 [total_m, d_ff], for rows x_sorted bf16 [total_m, d_model]
     grouped by expert (offsets as in grouped_gemm) and packed [2*d_ff, d_model] experts.  `gate_up`
-    (bf16 [total_m, 2*d_ff]) receives the pre-activations that grouped_swiglu_backward reads."""
-    dev = _one_gpu(w_gate_up, x_sorted, offsets, out, gate_up)
-    total_m = _swiglu_args(w_gate_up, expert_stride, n_experts, d_model, d_ff, x_sorted, offsets)
+    (bf16 [total_m, 2*d_ff]) receives the pre-activations that grouped_swiglu_backward reads.
+    `workspace` (GPU bytes, at least grouped_swiglu_workspace(...)) is allocated here when not given."""
+    dev = _one_gpu(w_gate_up, x_sorted, offsets, out, gate_up, workspace)
+    E, d, f = int(n_experts), int(d_model), int(d_ff)
+    total_m = _swiglu_args(w_gate_up, expert_stride, E, d, f, x_sorted, offsets)
     if out is None:
-        out = torch.empty((total_m, int(d_ff)), dtype=torch.bfloat16, device=dev)
-    _matrix("out", out, torch.bfloat16, total_m, int(d_ff))
+        out = torch.empty((total_m, f), dtype=torch.bfloat16, device=dev)
+    else:
+        _matrix("out", out, torch.bfloat16, total_m, f)
     if gate_up is not None:
-        _matrix("gate_up", gate_up, torch.bfloat16, total_m, 2 * int(d_ff))
-    _call(dev, "stq_grouped_swiglu", w_gate_up.data_ptr(), int(expert_stride), int(n_experts), int(d_model), int(d_ff),
-          x_sorted.data_ptr(), offsets.data_ptr(), total_m, out.data_ptr(), _ptr(gate_up))
+        _matrix("gate_up", gate_up, torch.bfloat16, total_m, 2 * f)
+    if workspace is None:
+        # the GEMV's tuning override changes its scratch, and so is part of the key
+        need = _swiglu_need(E, d, f, total_m, _device_cus(dev), os.environ.get("STQ_GEMV_PLAN"))
+        workspace = _workspace(None, need, dev)
+    else:
+        workspace = _workspace(workspace, 0, dev)
+    _call(dev, "stq_grouped_swiglu", w_gate_up.data_ptr(), int(expert_stride), E, d, f, x_sorted.data_ptr(),
+          offsets.data_ptr(), total_m, out.data_ptr(), _ptr(gate_up), *_ws_args(workspace))
     return out
 
 
@@ -487,8 +514,8 @@ def grouped_swiglu_backward(w_gate_up: torch.Tensor, expert_stride: int, n_exper
     grouped_swiglu_backward_workspace(...)) is allocated here when not given."""
     dev = _one_gpu(w_gate_up, x_sorted, offsets, gate_up, dh, dx, dw,
                     workspace)
-    total_m = _swiglu_args(w_gate_up, expert_stride, n_experts, d_model, d_ff, x_sorted, offsets)
     E, d, f = int(n_experts), int(d_model), int(d_ff)
+    total_m = _swiglu_args(w_gate_up, expert_stride, E, d, f, x_sorted, offsets)
     _matrix("gate_up", gate_up, torch.bfloat16, total_m, 2 * f)
     _matrix("dh", dh, torch.bfloat16, total_m, f)
     if need_dx:

@@ -41,6 +41,9 @@
 // launched on the same XCD (workgroup ids are dealt to the 8 XCDs round
 // robin), so the expert's activations are fetched once into that XCD's L2
 // and shared by its 16 slabs.
+#include <algorithm>
+#include <cmath>
+
 #include "stq_device.hpp"
 #include "stq_launch.hpp"
 #include "stq_passes.hpp"
@@ -489,8 +492,64 @@ hipError_t launch_grouped_gemm(const GemmArgs& ga, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_grouped_swiglu(const SwigluArgs& g, hipStream_t s) {
+namespace {
+
+GemvArgs swiglu_gemv(const SwigluArgs& g, const int32_t* pe, float* gu) {
+  return GemvArgs{g.w_table, g.expert_stride, g.n_experts, 2 * g.d_ff, g.d_model, g.x, 1, g.d_model, g.total_m,
+                  pe, nullptr, g.total_m, gu, 1};
+}
+
+}  // namespace
+
+// The matrix-core kernel walks a pass's blocks one after another, about 1.2 us
+// each and 0.0225 more a row, and streams packed weights at no more than 3.0
+// TB/s (its decode's LDS reads); the GEMV splits k over the chip and streams
+// at 4.6 TB/s, but pays for every row beyond an expert's first.  Both in us,
+// from the rows' expected spread over the experts; measured on 256 CUs
+// (matrix cores / GEMV, 2 x 2048 rows of 7168 unless stated):
+//   1 expert: 1 row 39 / 14, 32 rows 50 / 40, 80 rows 87 / 72, 300 rows 86 / 231
+//   8 experts: 64 rows 39 / 38, 256 rows 57 / 98
+//   256 experts: 37 rows 79 / 48, 296 rows 278 / 190, 800 rows 391 / 334, 1600
+//   rows 410 / 477
+//   2 x 1024 of 4096, 32 experts: 32 rows 24 / 24, 128 rows 25 / 33
+//   2 x 512 of 1024, 1 expert: 1 row 9 / 11
+bool swiglu_takes_gemv(const SwigluArgs& g, int cus) {
+  if (g.total_m > 4096) return false;  // the GEMV scans its pairs
+  const double rows = static_cast<double>(g.total_m), E = static_cast<double>(g.n_experts);
+  const double used = E * (1.0 - std::pow(1.0 - 1.0 / E, rows));
+  const double mb = 2e-6 * static_cast<double>(g.d_ff) * (g.d_model / kQK) * kBlockBytes;  // an expert's packed bytes
+  const double fill = 256.0 / cus;  // rates of a chip of other size
+  const double mfma = std::max(2.0 + static_cast<double>(g.d_model / kQK) * (1.2 + 0.0225 * std::min(80.0, rows / used)),
+                               used * mb / 3.0 * fill);
+  const double gemv = 10.0 + (used * mb / 4.6 + (rows - used) * (0.13 + 0.6 / std::sqrt(used)) * mb / 4.8) * fill;
+  return gemv < mfma;
+}
+
+SwigluPlan plan_swiglu(const SwigluArgs& g, int cus) {
+  SwigluPlan p{};
+  p.gemv = swiglu_takes_gemv(g, cus);
+  if (!p.gemv) return p;
+  auto up = [](int64_t b) { return (b + 255) / 256 * 256; };
+  p.plan = plan_gemv(swiglu_gemv(g, nullptr, nullptr), cus);
+  p.part = up(p.plan.partial_bytes);
+  p.pe = up(g.total_m * 4);
+  p.gu = g.total_m * 2 * g.d_ff * 4;
+  p.bytes = p.part + p.pe + p.gu;
+  return p;
+}
+
+hipError_t launch_grouped_swiglu(const SwigluArgs& g, const SwigluPlan& plan, void* ws, hipStream_t s) {
   if (g.total_m == 0) return hipSuccess;
+  if (plan.gemv) {
+    char* b = static_cast<char*>(ws);
+    int32_t* pe = reinterpret_cast<int32_t*>(b + plan.part);
+    float* gu = reinterpret_cast<float*>(b + plan.part + plan.pe);
+    hipError_t e = launch_row_expert(g.offsets, g.n_experts, g.total_m, pe, s);
+    if (e != hipSuccess) return e;
+    e = launch_gemv(swiglu_gemv(g, pe, gu), plan.plan, b, s, false);
+    if (e != hipSuccess) return e;
+    return launch_swiglu_rows(gu, gemv_partials(plan.plan, b), pe, g.n_experts, g.total_m, g.d_ff, g.h, g.gate_up, s);
+  }
   GArgs a{};
   a.w = g.w_table;
   a.estride = g.expert_stride;

@@ -77,6 +77,47 @@ __global__ __launch_bounds__(256) void swiglu_kernel(SplitRows gu, int64_t quads
   *reinterpret_cast<float4*>(h + e) = o;
 }
 
+// The gated feed-forward's form of the same: rows grouped by expert (`pe` the
+// row's expert or -1, whose outputs stay unwritten), bf16 outputs, each
+// rounded once from fp32, and the pre-activations if they are wanted.
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  return static_cast<uint32_t>(__builtin_bit_cast(uint16_t, static_cast<__bf16>(a))) |
+         static_cast<uint32_t>(__builtin_bit_cast(uint16_t, static_cast<__bf16>(b))) << 16;
+}
+
+__global__ __launch_bounds__(256) void swiglu_rows_kernel(SplitRows gu, int64_t quads, int64_t d_ff,
+                                                          uint16_t* __restrict__ h, uint16_t* __restrict__ gate_up) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= quads) return;
+  const int64_t e = 4 * i;
+  const int64_t p = e / d_ff;
+  const int64_t c = e - p * d_ff;
+  if (gu.pe[p] < 0) return;
+  const float4 g = gu.quad(static_cast<int>(p), p * 2 * d_ff + c);
+  const float4 u = gu.quad(static_cast<int>(p), p * 2 * d_ff + d_ff + c);
+  *reinterpret_cast<uint2*>(h + e) = make_uint2(bf16_pair(g.x / (1.0f + expf(-g.x)) * u.x, g.y / (1.0f + expf(-g.y)) * u.y),
+                                                bf16_pair(g.z / (1.0f + expf(-g.z)) * u.z, g.w / (1.0f + expf(-g.w)) * u.w));
+  if (gate_up) {
+    *reinterpret_cast<uint2*>(gate_up + p * 2 * d_ff + c) = make_uint2(bf16_pair(g.x, g.y), bf16_pair(g.z, g.w));
+    *reinterpret_cast<uint2*>(gate_up + p * 2 * d_ff + d_ff + c) = make_uint2(bf16_pair(u.x, u.y), bf16_pair(u.z, u.w));
+  }
+}
+
+// Expert of every row, from the offsets: the last expert that starts at or
+// before the row, if the row is inside it; -1 otherwise.
+__global__ __launch_bounds__(256) void row_expert_kernel(const int32_t* __restrict__ offsets, int n_experts, int rows,
+                                                         int32_t* __restrict__ pe) {
+  const int r = blockIdx.x * 256 + threadIdx.x;
+  if (r >= rows) return;
+  int lo = 0, hi = n_experts;  // offsets[lo] <= r unless lo is 0
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (offsets[mid] <= r) lo = mid;
+    else hi = mid;
+  }
+  pe[r] = offsets[lo] <= r && r < offsets[lo + 1] ? lo : -1;
+}
+
 // Workgroup (x, t): columns 256x.. of token t, so each routed pair's slot
 // count is uniform.  Up to 8 pairs at a time: every load of their direct
 // rows or split slots (at most kS slots a pair; kS = 0: any count, slot by
@@ -139,6 +180,25 @@ hipError_t launch_swiglu(const float* gu, const GemvPartials& parts, const int32
                     n_pairs * 2 * d_ff};
   hipLaunchKernelGGL(swiglu_kernel, dim3(static_cast<unsigned>((quads + 255) / 256)), dim3(256), 0, s, r,
                      quads, d_ff, h);
+  return hipGetLastError();
+}
+
+hipError_t launch_swiglu_rows(const float* gu, const GemvPartials& parts, const int32_t* pair_expert, int64_t n_experts,
+                              int64_t rows, int64_t d_ff, uint16_t* h, uint16_t* gate_up, hipStream_t s) {
+  const int64_t quads = rows * d_ff / 4;
+  if (quads == 0) return hipSuccess;
+  const SplitRows r{gu, parts.partial, parts.splits, parts.pair_sub, pair_expert, static_cast<int>(n_experts),
+                    rows * 2 * d_ff};
+  hipLaunchKernelGGL(swiglu_rows_kernel, dim3(static_cast<unsigned>((quads + 255) / 256)), dim3(256), 0, s, r, quads,
+                     d_ff, h, gate_up);
+  return hipGetLastError();
+}
+
+hipError_t launch_row_expert(const int32_t* offsets, int64_t n_experts, int64_t rows, int32_t* pair_expert,
+                             hipStream_t s) {
+  if (rows == 0) return hipSuccess;
+  hipLaunchKernelGGL(row_expert_kernel, dim3(static_cast<unsigned>((rows + 255) / 256)), dim3(256), 0, s, offsets,
+                     static_cast<int>(n_experts), static_cast<int>(rows), pair_expert);
   return hipGetLastError();
 }
 

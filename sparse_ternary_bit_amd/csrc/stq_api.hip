@@ -397,16 +397,43 @@ stq_status swiglu_shape_check(int64_t n_experts, int64_t d_model, int64_t d_ff, 
 
 }  // namespace
 
-stq_status stq_grouped_swiglu(const uint8_t* w_gate_up, int64_t gate_up_stride_bytes, int64_t n_experts,
-                              int64_t d_model, int64_t d_ff, const uint16_t* x_sorted, const int32_t* expert_offsets,
-                              int64_t total_m, uint16_t* h, uint16_t* gate_up, stq_stream_t stream) {
-  const char* who = "stq_grouped_swiglu";
+namespace {
+
+stq_status swiglu_fwd_check(int64_t n_experts, int64_t d_model, int64_t d_ff, int64_t total_m, const char* who) {
   const stq_status st = swiglu_shape_check(n_experts, d_model, d_ff, total_m, who);
   if (st != STQ_OK) return st;
-  if (gate_up_stride_bytes < 2 * d_ff * stq_row_bytes(d_model)) return fail(STQ_E_SHAPE, "%s: expert stride smaller than the packed matrix", who);
   if ((stq::pass_units(total_m, n_experts, 32) + 8) * (d_ff / 128) > (int64_t{1} << 23))
     return fail(STQ_E_SHAPE, "%s: too many rows and experts of this size for one call", who);
+  return STQ_OK;
+}
+
+}  // namespace
+
+stq_status stq_grouped_swiglu_workspace(int64_t n_experts, int64_t d_model, int64_t d_ff, int64_t total_m,
+                                        int32_t n_cus, int64_t* workspace_bytes) {
+  const char* who = "stq_grouped_swiglu_workspace";
+  if (!workspace_bytes) return fail(STQ_E_ARG, "%s: null output pointer", who);
+  *workspace_bytes = 0;
+  if (n_cus < 0) return fail(STQ_E_ARG, "%s: n_cus < 0", who);
+  const stq_status st = swiglu_fwd_check(n_experts, d_model, d_ff, total_m, who);
+  if (st != STQ_OK) return st;
+  if (total_m == 0) return ok();
+  const stq::SwigluArgs a{nullptr, 2 * d_ff * stq_row_bytes(d_model), n_experts, d_model, d_ff, nullptr, nullptr, total_m,
+                          nullptr, nullptr};
+  *workspace_bytes = stq::plan_swiglu(a, n_cus > 0 ? n_cus : stq::cus_of_current_device()).bytes;
+  return ok();
+}
+
+stq_status stq_grouped_swiglu(const uint8_t* w_gate_up, int64_t gate_up_stride_bytes, int64_t n_experts,
+                              int64_t d_model, int64_t d_ff, const uint16_t* x_sorted, const int32_t* expert_offsets,
+                              int64_t total_m, uint16_t* h, uint16_t* gate_up, void* workspace,
+                              int64_t workspace_bytes, stq_stream_t stream) {
+  const char* who = "stq_grouped_swiglu";
+  stq_status st = swiglu_fwd_check(n_experts, d_model, d_ff, total_m, who);
+  if (st != STQ_OK) return st;
+  if (gate_up_stride_bytes < 2 * d_ff * stq_row_bytes(d_model)) return fail(STQ_E_SHAPE, "%s: expert stride smaller than the packed matrix", who);
   if (!expert_offsets) return fail(STQ_E_ARG, "%s: null offsets", who);
+  if (workspace_bytes < 0) return fail(STQ_E_ARG, "%s: workspace_bytes < 0", who);
   if (total_m == 0) return ok();
   if (!w_gate_up || !x_sorted || !h) return fail(STQ_E_ARG, "%s: null pointer", who);
   if (!aligned(w_gate_up, 16) || gate_up_stride_bytes % 16) return fail(STQ_E_ALIGN, "%s: w_gate_up / expert stride not 16-byte aligned", who);
@@ -415,7 +442,11 @@ stq_status stq_grouped_swiglu(const uint8_t* w_gate_up, int64_t gate_up_stride_b
     return fail(STQ_E_ALIGN, "%s: offsets not 4-byte, or h / gate_up not 8-byte aligned", who);
   const stq::SwigluArgs a{w_gate_up, gate_up_stride_bytes, n_experts, d_model, d_ff, x_sorted, expert_offsets, total_m,
                           h, gate_up};
-  hipError_t e = stq::launch_grouped_swiglu(a, reinterpret_cast<hipStream_t>(stream));
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const stq::SwigluPlan pl = stq::plan_swiglu(a, stq::cus_of_stream(s));
+  st = check_workspace(workspace, workspace_bytes, pl.bytes, who);
+  if (st != STQ_OK) return st;
+  hipError_t e = stq::launch_grouped_swiglu(a, pl, workspace, s);
   if (e != hipSuccess) return hip_fail(e, "stq_grouped_swiglu launch");
   return ok();
 }

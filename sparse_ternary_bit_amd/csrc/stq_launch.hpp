@@ -103,7 +103,21 @@ struct SwigluArgs {
   uint16_t* h;
   uint16_t* gate_up;  // may be NULL
 };
-hipError_t launch_grouped_swiglu(const SwigluArgs& a, hipStream_t s);
+// Few rows go through the decode GEMV (one pair a row), the rest through the
+// matrix-core kernel.
+struct SwigluPlan {
+  bool gemv;
+  GemvPlan plan;          // gemv: of the gate/up product
+  int64_t part, pe, gu;   // gemv: workspace bytes of the split outputs, the rows' experts, the fp32 rows
+  int64_t bytes;          // workspace bytes
+};
+SwigluPlan plan_swiglu(const SwigluArgs& a, int cus);
+hipError_t launch_grouped_swiglu(const SwigluArgs& a, const SwigluPlan& plan, void* ws, hipStream_t s);
+
+// The GEMV form's own kernels (k_moe.hip)
+hipError_t launch_row_expert(const int32_t* offsets, int64_t n_experts, int64_t rows, int32_t* pair_expert, hipStream_t s);
+hipError_t launch_swiglu_rows(const float* gu, const GemvPartials& parts, const int32_t* pair_expert, int64_t n_experts,
+                              int64_t rows, int64_t d_ff, uint16_t* h, uint16_t* gate_up, hipStream_t s);
 
 struct SwigluBwdArgs {
   const uint8_t* w_table;

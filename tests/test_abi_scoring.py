@@ -141,10 +141,10 @@ STRIDE = 2 * 512 * ROWB
 
 
 def _fw(L, **kw):
-    a = dict(w=FAKE, st=STRIDE, ne=4, d=4096, f=512, x=FAKE, off=FAKE, m=10, h=FAKE, gu=FAKE)
+    a = dict(w=FAKE, st=STRIDE, ne=4, d=4096, f=512, x=FAKE, off=FAKE, m=10, h=FAKE, gu=FAKE, ws=FAKE, wsb=1 << 40)
     a.update(kw)
     return L.stq_grouped_swiglu(a["w"], a["st"], a["ne"], a["d"], a["f"], a["x"], a["off"], a["m"], a["h"], a["gu"],
-                                None)
+                                a["ws"], a["wsb"], None)
 
 
 SHAPE_REFUSALS = [(dict(ne=0), 1), (dict(m=-1), 1), (dict(d=100), 2), (dict(f=128), 2), (dict(f=0), 2),
@@ -154,7 +154,8 @@ SHAPE_REFUSALS = [(dict(ne=0), 1), (dict(m=-1), 1), (dict(d=100), 2), (dict(f=12
 
 
 @pytest.mark.parametrize("kw, status", SHAPE_REFUSALS + [
-    (dict(x=None), 1), (dict(h=None), 1), (dict(x=FAKE + 8), 3), (dict(h=FAKE + 4), 3), (dict(gu=FAKE + 4), 3)])
+    (dict(x=None), 1), (dict(h=None), 1), (dict(x=FAKE + 8), 3), (dict(h=FAKE + 4), 3), (dict(gu=FAKE + 4), 3),
+    (dict(wsb=-1), 1)])
 def test_swiglu_refusals(L, kw, status):
     assert _fw(L, **kw) == status
     assert _err(L).startswith("stq_grouped_swiglu")
@@ -177,8 +178,30 @@ def test_swiglu_backward_refusals(L, kw, status):
     assert _err(L).startswith("stq_grouped_swiglu_backward")
 
 
+def test_swiglu_workspace(L, monkeypatch):
+    monkeypatch.delenv("STQ_GEMV_PLAN", raising=False)
+    wb = ctypes.c_int64(-7)
+    f = L.stq_grouped_swiglu_workspace
+    assert f(256, 7168, 2048, 16384, 256, ctypes.byref(wb)) == 0 and wb.value == 0    # the matrix-core kernel
+    assert f(4, 4096, 512, 0, 256, ctypes.byref(wb)) == 0 and wb.value == 0
+    assert f(4, 4096, 500, 10, 256, ctypes.byref(wb)) == 2
+    assert f(4, 4096, 512, -1, 256, ctypes.byref(wb)) == 1
+    assert f(4, 4096, 512, 10, -1, ctypes.byref(wb)) == 1
+    assert f(4, 4096, 512, 10, 256, None) == 1
+    # few rows: the rows' experts, their fp32 pre-activations, and the GEMV's split outputs
+    assert f(4, 4096, 512, 10, 256, ctypes.byref(wb)) == 0
+    sp, mp, scratch = ctypes.c_int32(), ctypes.c_int32(), ctypes.c_int64()
+    assert L.stq_gemv_plan(4, 1024, 4096, 10, 256, ctypes.byref(sp), ctypes.byref(mp), ctypes.byref(scratch)) == 0
+    assert wb.value == (scratch.value + 255) // 256 * 256 + 256 + 10 * 1024 * 4
+    assert f(4, 4096, 512, 10, 0, ctypes.byref(wb)) == 0
+    need = wb.value
+    assert _fw(L, ws=None, wsb=0) == 1 and "workspace" in _err(L)
+    assert _fw(L, wsb=need - 1) == 1
+    assert _fw(L, ws=FAKE + 16, wsb=need) == 3
+
+
 def test_swiglu_nothing_to_do(L):
-    assert _fw(L, m=0, w=None, x=None, h=None, gu=None) == 0
+    assert _fw(L, m=0, w=None, x=None, h=None, gu=None, ws=None, wsb=0) == 0
     assert _bwd(L, dx=None, dw=None, w=None, x=None, gu=None, dh=None, ws=None, wsb=0) == 0
     assert _bwd(L, m=0, dw=None, w=None, x=None, gu=None, dh=None, ws=None, wsb=0) == 0
 
