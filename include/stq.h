@@ -404,7 +404,7 @@ stq_status stq_q8_quantize_rows(const void* x, int x_dtype, int64_t x_row_stride
  *                the fp32 value), rows y_row_stride elements apart; rows that
  *                start on four elements store faster
  * 1 <= k <= 131071 (any sum of products of bytes then fits 32 bits); m up to
- * 2^22.  Integer sums do not depend on their order: a result's bits do not
+ * 2^22, n up to 2^26, m * n up to 2^38.  Integer sums do not depend on their order: a result's bits do not
  * depend on m, n, the strides or the device. */
 stq_status stq_q8_matmul(const int8_t* a, int64_t a_row_stride, const float* a_scale, const int8_t* w,
                          int64_t w_row_stride, const float* w_scale, int64_t m, int64_t n, int64_t k, void* y,
@@ -428,7 +428,8 @@ stq_status stq_q8_matmul(const int8_t* a, int64_t a_row_stride, const float* a_s
  * A row without a distribution gives NaN log probabilities and entropy and
  * ids -1: one that is masked throughout (lse = -inf) or that holds a NaN or a
  * +inf (lse = NaN).  Sums and maxima are fp32; the order of summation is fixed
- * for a device, so repeated calls give identical bits.  At most 2^22 rows. */
+ * for a device, so repeated calls give identical bits.  At most 2^22 rows of at
+ * most 2^30 entries. */
 stq_status stq_token_logprobs(const void* logits, int x_dtype, int64_t row_stride, int64_t n_rows, int64_t vocab,
                               const int32_t* targets, float* logprob, float* lse, float* entropy, int64_t top_n,
                               int32_t* top_ids, float* top_logprobs, void* workspace, int64_t workspace_bytes,

@@ -520,8 +520,9 @@ bool fits(int64_t rows, int64_t stride, int64_t esz) {
 stq_status q8_shape_check(int64_t m, int64_t n, int64_t k, const char* who) {
   if (m < 0 || n < 0) return fail(STQ_E_ARG, "%s: negative count", who);
   if (k < 1 || k > kMaxK8) return fail(STQ_E_SHAPE, "%s: k=%lld outside 1..%lld", who, (long long)k, (long long)kMaxK8);
-  if (n > INT_MAX / 2) return fail(STQ_E_SHAPE, "%s: more than 2^30 channels", who);
-  if (m > (int64_t{1} << 22)) return fail(STQ_E_SHAPE, "%s: more than 2^22 tokens in one call", who);
+  if (m > (int64_t{1} << 22) || n > (int64_t{1} << 26))
+    return fail(STQ_E_SHAPE, "%s: more than 2^22 tokens or 2^26 channels in one call", who);
+  if (m * n > (int64_t{1} << 38)) return fail(STQ_E_SHAPE, "%s: more than 2^38 products in one call", who);
   return STQ_OK;
 }
 
@@ -579,7 +580,7 @@ namespace {
 stq_status logprobs_shape_check(int x_dtype, int64_t n_rows, int64_t vocab, const char* who) {
   if (x_dtype != STQ_X_F32 && x_dtype != STQ_X_BF16) return fail(STQ_E_ARG, "%s: unknown x_dtype %d", who, x_dtype);
   if (n_rows < 0) return fail(STQ_E_ARG, "%s: n_rows < 0", who);
-  if (vocab < 1 || vocab > INT_MAX - 64) return fail(STQ_E_SHAPE, "%s: vocab=%lld outside 1..2^31-65", who, (long long)vocab);
+  if (vocab < 1 || vocab > (int64_t{1} << 30)) return fail(STQ_E_SHAPE, "%s: vocab=%lld outside 1..2^30", who, (long long)vocab);
   if (n_rows > (int64_t{1} << 22)) return fail(STQ_E_SHAPE, "%s: more than 2^22 rows in one call", who);
   return STQ_OK;
 }

@@ -57,7 +57,7 @@ def _mm(L, **kw):
     (dict(ldw=(1 << 23) + 16), 2), (dict(ldy=63), 2), (dict(a=None), 1), (dict(as_=None), 1), (dict(w=None), 1),
     (dict(ws=None), 1), (dict(y=None), 1), (dict(a=FAKE + 8), 3), (dict(w=FAKE + 8), 3), (dict(as_=FAKE + 2), 3),
     (dict(ws=FAKE + 2), 3), (dict(y=FAKE + 1), 3), (dict(yd=0, y=FAKE + 2), 3), (dict(m=(1 << 22) + 1), 2),
-    (dict(n=1 << 31, ldy=1 << 31), 2), (dict(ldy=1 << 62), 2),
+    (dict(n=(1 << 26) + 1, ldy=1 << 27), 2), (dict(m=1 << 20, n=1 << 20, ldy=1 << 20), 2), (dict(ldy=1 << 62), 2),
 ])
 def test_matmul_refusals(L, kw, status):
     assert _mm(L, **kw) == status
@@ -79,7 +79,7 @@ def _lp(L, **kw):
 
 
 @pytest.mark.parametrize("kw, status", [
-    (dict(xd=7), 1), (dict(n=-1), 1), (dict(v=0), 2), (dict(v=1 << 31, xs=1 << 31), 2), (dict(n=(1 << 22) + 1), 2),
+    (dict(xd=7), 1), (dict(n=-1), 1), (dict(v=0), 2), (dict(v=(1 << 30) + 1, xs=1 << 31), 2), (dict(n=(1 << 22) + 1), 2),
     (dict(top=-1), 1), (dict(top=33), 2), (dict(v=4, top=5), 2), (dict(xs=999), 2), (dict(wsb=-1), 1),
     (dict(x=None), 1), (dict(t=None), 1), (dict(lp=None), 1), (dict(ids=None), 1), (dict(tlp=None), 1),
     (dict(xs=1 << 62), 2), (dict(x=FAKE + 1), 3), (dict(xd=0, x=FAKE + 2), 3), (dict(t=FAKE + 2), 3),

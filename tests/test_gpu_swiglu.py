@@ -158,6 +158,54 @@ def test_odd_block_scales_and_expert_stride(stq):
     c.check_backward(*c.backward())
 
 
+@pytest.mark.parametrize("counts, d, f, tail", [([1], 7168, 2048, 0), ([0, 3, 0, 17, 1, 0], 7168, 512, 5),
+                                                 ([1, 1, 0, 2] * 10, 7168, 1024, 1), ([40], 7168, 1024, 0), ([1, 0, 5], 7168, 256, 3)])
+def test_few_rows_through_the_gemv(stq, counts, d, f, tail):
+    c = Case(stq, counts, d, f, seed=d + f, tail=tail)
+    need = stq.grouped_swiglu_workspace(c.E, d, f, c.m)
+    assert need > 0                                        # the GEMV's form
+    h = torch.full((c.m, f), 3.0, dtype=torch.bfloat16, device="cuda")
+    gu = torch.full((c.m, 2 * f), 3.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    c.forward(out=h, gate_up=gu, workspace=ws)
+    c.check_forward(h, gu)
+    used = c.bounds[-1]
+    assert bool((h[used:] == 3.0).all()) and bool((gu[used:] == 3.0).all())
+    assert torch.equal(c.forward()[:used], h[:used])
+    c.x[0, 1] = float("nan")                               # stays in its row
+    assert torch.equal(c.forward()[1:used], h[1:used])
+    for bad in ([c.m + 7] * (c.E + 1), [-3] * (c.E + 1), list(range(c.E + 1))[::-1]):
+        c.offsets.copy_(torch.tensor(bad, dtype=torch.int32))
+        guard = torch.full((c.m + 8, f), 3.0, dtype=torch.bfloat16, device="cuda")
+        c.forward(out=guard[:c.m])
+        torch.cuda.synchronize()
+        assert bool((guard[c.m:] == 3.0).all())
+
+
+def test_few_rows_under_graph(stq):
+    c = Case(stq, [1, 0, 2, 1], 7168, 512, seed=15)
+    h = torch.empty((c.m, c.f), dtype=torch.bfloat16, device="cuda")
+    need = stq.grouped_swiglu_workspace(c.E, c.d, c.f, c.m)
+    assert need > 0
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    c.forward(out=h, workspace=ws)
+    torch.cuda.synchronize()
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(g, stream=side):
+            c.forward(out=h, workspace=ws)
+    torch.cuda.synchronize()
+    for r in range(4):
+        c.x.copy_(torch.randn(c.x.shape, generator=torch.Generator().manual_seed(r)).bfloat16())
+        c.offsets.copy_(torch.tensor([[0, 1, 1, 3, 4], [0, 4, 4, 4, 4], [0, 0, 0, 0, 4], [0, 1, 2, 3, 4]][r], dtype=torch.int32))
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        got = h.clone()
+        assert torch.equal(got, c.forward()), r
+
+
 def test_full_width_expert(stq):
     c = Case(stq, [0, 70, 131], 7168, 2048, seed=4)
     c.check_forward(c.forward())
@@ -175,6 +223,16 @@ def test_rows_behind_the_last_expert_stay_as_they_were(stq):
         assert bool((t[45:] == 3.0).all())
     c.check_forward(h, gu)
     c.check_backward(dx, dw)
+
+
+def test_rows_of_uneven_experts_beyond_one_pass(stq):
+    # hundreds of experts, most without rows, one with many passes: the passes are found on the device
+    counts = [0] * 600
+    counts[3], counts[255], counts[256], counts[599] = 500, 1, 81, 160
+    c = Case(stq, counts, 256, 256, seed=14)
+    c.check_forward(c.forward())
+    dx, _ = c.backward(need_dw=False)
+    c.check_backward(dx, None)
 
 
 def test_nothing_routed(stq):
