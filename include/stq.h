@@ -349,8 +349,8 @@ stq_status stq_grouped_swiglu_workspace(int64_t n_experts, int64_t d_model, int6
  *   dh        bf16 [total_m, d_ff]; 16-byte aligned
  *   dx        bf16 [total_m, d_model] or NULL (not wanted); 8-byte aligned;
  *             rows in no range stay unwritten
- *   dw        bf16 [n_experts, 2*d_ff, d_model] or NULL; 8-byte aligned; every
- *             element is written (zeros for an expert without rows)
+ *   dw        bf16 [n_experts, 2*d_ff, d_model] or NULL; 16-byte aligned;
+ *             every element is written (zeros for an expert without rows)
  *   w_gate_up is read for dx only and x_sorted for dw only; either may be
  *   NULL otherwise.  The other arguments are as for stq_grouped_swiglu.
  *   workspace, workspace_bytes   at least what

@@ -535,8 +535,10 @@ __device__ __forceinline__ void expert_rows(const int32_t* offsets, int e, int64
 __device__ __forceinline__ int tok_swizzle(int t) { return 2 * ((t & 3) | ((t >> 1) & 4)); }
 
 __global__ __launch_bounds__(kThreads, 2) void swiglu_dw_kernel(DwArgs a) {
-  __shared__ __align__(16) char sz[kDwBuf][kTok * kTR * 2];
-  __shared__ __align__(16) char sx[kDwBuf][kTok * kTC * 2];
+  // three stages of dz and x, and after the last of them the outputs on their way
+  __shared__ __align__(16) char smem[kDwBuf * kTok * (kTR + kTC) * 2];
+  char(*const sz)[kTok * kTR * 2] = reinterpret_cast<char(*)[kTok * kTR * 2]>(smem);
+  char(*const sx)[kTok * kTC * 2] = reinterpret_cast<char(*)[kTok * kTC * 2]>(smem + kDwBuf * kTok * kTR * 2);
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int q = lane >> 4, r = lane & 15;
@@ -634,14 +636,28 @@ __global__ __launch_bounds__(kThreads, 2) void swiglu_dw_kernel(DwArgs a) {
       for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(X, Z[j], acc[i][j], 0, 0, 0);
     }
   }
-  // dw[e, r0 + 64 wave + 16j + r, c0 + 16i + 4q + 0..3]
-  uint16_t* out = a.dw + (static_cast<int64_t>(e) * a.n_r + r0 + 64 * wave) * a.n_c + c0;
+  // A lane holds dw[e, r0 + 64 wave + 16j + r, c0 + 16i + 4q + 0..3], 8 bytes in
+  // each of 16 rows an instruction: through LDS to whole rows of 256 bytes
+  // (stored straight, the 470 MB of 8 experts cost 130 us more).  Every
+  // wavefront has a part of its own, rows 16 bytes apart from a bank's period.
+  constexpr int kRowB = kTC * 2 + 16;
+  static_assert(kWaves * 64 * kRowB <= kDwBuf * kTok * (kTR + kTC) * 2, "the outputs fit where the stages were");
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // everyone has read the last stage
+  char* const mine = smem + wave * 64 * kRowB;
 #pragma unroll
   for (int j = 0; j < 4; ++j)
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      *reinterpret_cast<u32x2_t*>(out + static_cast<int64_t>(16 * j + r) * a.n_c + 16 * i + 4 * q) =
+      *reinterpret_cast<u32x2_t*>(mine + (16 * j + r) * kRowB + 32 * i + 8 * q) =
           u32x2_t{bf16_pair(acc[i][j][0], acc[i][j][1]), bf16_pair(acc[i][j][2], acc[i][j][3])};
+  __builtin_amdgcn_wave_barrier();  // LDS serves a wavefront's instructions in order
+  uint16_t* out = a.dw + (static_cast<int64_t>(e) * a.n_r + r0 + 64 * wave) * a.n_c + c0;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const int row = 4 * j + q;
+    const u32x4_t v = *reinterpret_cast<const u32x4_t*>(mine + row * kRowB + r * 16);
+    __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t*>(out + static_cast<int64_t>(row) * a.n_c) + r);
+  }
 }
 
 }  // namespace

@@ -496,8 +496,8 @@ stq_status stq_grouped_swiglu_backward(const uint8_t* w_gate_up, int64_t gate_up
   if (dx && (!aligned(w_gate_up, 16) || gate_up_stride_bytes % 16)) return fail(STQ_E_ALIGN, "%s: w_gate_up / expert stride not 16-byte aligned", who);
   if (!aligned(gate_up, 16) || !aligned(dh, 16) || (dw && !aligned(x_sorted, 16)))
     return fail(STQ_E_ALIGN, "%s: gate_up, dh or x_sorted not 16-byte aligned", who);
-  if (!aligned(expert_offsets, 4) || !aligned(dx, 8) || !aligned(dw, 8))
-    return fail(STQ_E_ALIGN, "%s: offsets not 4-byte, or dx / dw not 8-byte aligned", who);
+  if (!aligned(expert_offsets, 4) || !aligned(dx, 8) || !aligned(dw, 16))
+    return fail(STQ_E_ALIGN, "%s: offsets not 4-byte, dx not 8-byte or dw not 16-byte aligned", who);
   st = check_workspace(workspace, workspace_bytes, stq::swiglu_bwd_layout(d_ff, total_m, dx != nullptr, dw != nullptr).bytes, who);
   if (st != STQ_OK) return st;
   const stq::SwigluBwdArgs a{w_gate_up, gate_up_stride_bytes, n_experts, d_model, d_ff, x_sorted, expert_offsets,

@@ -171,7 +171,7 @@ def _bwd(L, **kw):
 
 @pytest.mark.parametrize("kw, status", SHAPE_REFUSALS + [
     (dict(gu=None), 1), (dict(dh=None), 1), (dict(x=None), 1), (dict(gu=FAKE + 8), 3), (dict(dh=FAKE + 8), 3),
-    (dict(x=FAKE + 8), 3), (dict(dx=FAKE + 4), 3), (dict(dw=FAKE + 4), 3), (dict(wsb=-1), 1),
+    (dict(x=FAKE + 8), 3), (dict(dx=FAKE + 4), 3), (dict(dw=FAKE + 8), 3), (dict(wsb=-1), 1),
     (dict(ne=60000, d=1 << 16, f=1 << 14, st=1 << 40), 2)])
 def test_swiglu_backward_refusals(L, kw, status):
     assert _bwd(L, **kw) == status
