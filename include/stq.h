@@ -317,9 +317,9 @@ stq_status stq_greedy_allocation(const double* gain, const double* extra_bytes, 
  *   expert_offsets  DEVICE int32 [n_experts+1] as in stq_grouped_gemm,
  *                   clamped the same way: rows in no range stay unwritten
  *   h               bf16 [total_m, d_ff], the down projection's input of
- *                   stq_grouped_gemm; 8-byte aligned
+ *                   stq_grouped_gemm; 16-byte aligned
  *   gate_up         bf16 [total_m, 2*d_ff] = [g | u], what the backward pass
- *                   reads, or NULL; 8-byte aligned
+ *                   reads, or NULL; 16-byte aligned
  * bf16 x ternary products are exact, sums fp32, and h and gate_up are each
  * rounded from the fp32 sums once.  Few rows run through stq_gemv's kernels
  * and need scratch:

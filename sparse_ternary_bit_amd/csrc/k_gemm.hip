@@ -343,28 +343,36 @@ __device__ __forceinline__ void run_pass(const GArgs& a, Smem<kTiles>& sh, const
     // formed in fp32 from the fp32 sums and rounded to bf16 once (the type the
     // down projection's matrix cores take); the saved pre-activations are the
     // same sums rounded to bf16
+    // A lane holds four columns of 16 tokens an instruction: through LDS (where
+    // the activations were) to the slab's whole rows of 256 bytes.
+    constexpr int kCols = kSlab / 2, kRowB = kCols * 2 + 16;
+    static_assert(NT * 16 * kRowB <= static_cast<int>(sizeof(sh.x)), "the outputs fit where the activations were");
+    char* const tile = sh.x[0];
+    auto put = [&](uint16_t* out, int64_t ld, auto value) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int tok = 16 * t + r;
-      if (tok >= mt) continue;
-      const int64_t row = row0 + tok;
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int col = hrow0 + 16 * i + 4 * q;
-        float h[4];
+        for (int i = 0; i < 2; ++i) {
+          float v[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float g = tot[i][t][j];
-          h[j] = g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504088896340736f * g)) * tot[i + 2][t][j];
+          for (int j = 0; j < 4; ++j) v[j] = value(t, i, j);
+          *reinterpret_cast<u32x2_t*>(tile + (16 * t + r) * kRowB + (wave * 32 + 16 * i + 4 * q) * 2) =
+              u32x2_t{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
         }
-        *reinterpret_cast<u32x2_t*>(a.h + row * a.d_ff + col) = u32x2_t{bf16_pair(h[0], h[1]), bf16_pair(h[2], h[3])};
-        if (a.gu) {
-          uint16_t* gr = a.gu + row * 2 * a.d_ff + col;
-          const f32x4_t g = tot[i][t], u = tot[i + 2][t];
-          *reinterpret_cast<u32x2_t*>(gr) = u32x2_t{bf16_pair(g[0], g[1]), bf16_pair(g[2], g[3])};
-          *reinterpret_cast<u32x2_t*>(gr + a.d_ff) = u32x2_t{bf16_pair(u[0], u[1]), bf16_pair(u[2], u[3])};
-        }
-      }
+      __syncthreads();
+      for (int tok = tid >> 4; tok < mt; tok += kThreads / 16)
+        *reinterpret_cast<u32x4_t*>(out + (row0 + tok) * ld + slab * kCols + 8 * (tid & 15)) =
+            *reinterpret_cast<const u32x4_t*>(tile + tok * kRowB + 16 * (tid & 15));
+    };
+    put(a.h, a.d_ff, [&](int t, int i, int j) {
+      const float g = tot[i][t][j];
+      return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504088896340736f * g)) * tot[i + 2][t][j];
+    });
+    if (a.gu) {
+      __syncthreads();
+      put(a.gu, 2 * a.d_ff, [&](int t, int i, int j) { return tot[i][t][j]; });
+      __syncthreads();
+      put(a.gu + a.d_ff, 2 * a.d_ff, [&](int t, int i, int j) { return tot[i + 2][t][j]; });
     }
     return;
   }

@@ -438,8 +438,8 @@ stq_status stq_grouped_swiglu(const uint8_t* w_gate_up, int64_t gate_up_stride_b
   if (!w_gate_up || !x_sorted || !h) return fail(STQ_E_ARG, "%s: null pointer", who);
   if (!aligned(w_gate_up, 16) || gate_up_stride_bytes % 16) return fail(STQ_E_ALIGN, "%s: w_gate_up / expert stride not 16-byte aligned", who);
   if (!aligned(x_sorted, 16)) return fail(STQ_E_ALIGN, "%s: x_sorted not 16-byte aligned", who);
-  if (!aligned(expert_offsets, 4) || !aligned(h, 8) || !aligned(gate_up, 8))
-    return fail(STQ_E_ALIGN, "%s: offsets not 4-byte, or h / gate_up not 8-byte aligned", who);
+  if (!aligned(expert_offsets, 4) || !aligned(h, 16) || !aligned(gate_up, 16))
+    return fail(STQ_E_ALIGN, "%s: offsets not 4-byte, or h / gate_up not 16-byte aligned", who);
   const stq::SwigluArgs a{w_gate_up, gate_up_stride_bytes, n_experts, d_model, d_ff, x_sorted, expert_offsets, total_m,
                           h, gate_up};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);

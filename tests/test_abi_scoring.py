@@ -154,7 +154,7 @@ SHAPE_REFUSALS = [(dict(ne=0), 1), (dict(m=-1), 1), (dict(d=100), 2), (dict(f=12
 
 
 @pytest.mark.parametrize("kw, status", SHAPE_REFUSALS + [
-    (dict(x=None), 1), (dict(h=None), 1), (dict(x=FAKE + 8), 3), (dict(h=FAKE + 4), 3), (dict(gu=FAKE + 4), 3),
+    (dict(x=None), 1), (dict(h=None), 1), (dict(x=FAKE + 8), 3), (dict(h=FAKE + 8), 3), (dict(gu=FAKE + 8), 3),
     (dict(wsb=-1), 1)])
 def test_swiglu_refusals(L, kw, status):
     assert _fw(L, **kw) == status
