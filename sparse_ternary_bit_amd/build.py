@@ -18,8 +18,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libstq.so")
 
-SOURCES = ["stq_api.hip", "k_codec.hip", "k_gemv.hip", "k_gemm.hip", "k_moe.hip", "k_sens.hip", "k_swiglu.hip", "k_q8.hip",
-           "k_logprobs.hip", "k_probe.hip"]
+SOURCES = ["stq_api.hip", "k_codec.hip", "k_gemv.hip", "k_gemm.hip", "k_moe.hip", "k_sens.hip", "k_gated.hip",
+           "k_swiglu.hip", "k_q8.hip", "k_logprobs.hip", "k_probe.hip"]
 # per-file extra flags: the encoders must not contract fp64 arithmetic; the
 # matrix-core probe keeps its accumulators in VGPRs (in the AGPR form the
 # compiler moves them between the two files every round)

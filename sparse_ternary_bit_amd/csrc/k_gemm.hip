@@ -69,7 +69,6 @@ constexpr int kMaxTiles = 5;                // token tiles of 16 per pass
 constexpr int kMaxTok = kMaxTiles * 16;     // 80 tokens per pass
 constexpr int kHalfBytes = kQK;             // one token's 128 activations: half a block
 constexpr int kXcds = 8;
-constexpr int kFewRows = 8;                 // gated form: mean rows an expert up to which passes are of 32
 constexpr int kWRaw = 3 * 1024;             // 16-byte aligned window over one 2688-byte tile run
 
 struct GArgs {
@@ -447,19 +446,19 @@ __global__ __launch_bounds__(kThreads, 2) void grouped_gemm_kernel(GArgs a) {
   }
 }
 
-// The gated form: one workgroup per (pass of an expert's tokens, slab), so an
-// expert with many tokens is spread over the chip (a router's load is rarely
-// even: 8191 rows over 32 experts with loads ~ 1/rank took 1303 us with each
-// expert's passes in turn).  Which pass a workgroup has is found on the device
-// from the offsets; the grid holds as many as the row count allows and the
-// rest leave.  Passes are dealt to the XCDs in turn, a pass's slabs sharing one.
-template <int kTiles, int kPerCu>
-__global__ __launch_bounds__(kThreads, kPerCu) void grouped_swiglu_kernel(GArgs a) {
-  __shared__ Smem<kTiles> sh;
+// The gated form for short passes: one workgroup per (pass of up to 32 of an
+// expert's tokens, slab), so an expert with many tokens is spread over the
+// chip.  Which pass a workgroup has is found on the device from the offsets;
+// the grid holds as many as the row count allows and the rest leave.  Passes
+// are dealt to the XCDs in turn, a pass's slabs sharing one.  Two thirds of
+// the plain kernel's LDS and registers: three to a CU.
+constexpr int kShortTiles = 2;
+__global__ __launch_bounds__(kThreads, 3) void grouped_swiglu_kernel(GArgs a) {
+  __shared__ Smem<kShortTiles> sh;
   const int xcd = blockIdx.x % kXcds;
   const int local = blockIdx.x / kXcds;
   const int slab = local % a.nslab;
-  const PassUnit u = find_pass(a.offsets, a.n_experts, a.total_m, (local / a.nslab) * kXcds + xcd, kTiles * 16);
+  const PassUnit u = find_pass(a.offsets, a.n_experts, a.total_m, (local / a.nslab) * kXcds + xcd, kShortTiles * 16);
   if (u.mt <= 0) return;
   if (threadIdx.x < 32) {
     sh.lut[threadIdx.x] = pattern_word(threadIdx.x, 0);
@@ -467,14 +466,8 @@ __global__ __launch_bounds__(kThreads, kPerCu) void grouped_swiglu_kernel(GArgs 
   }
   __syncthreads();
   const uint8_t* wexp = a.w + static_cast<int64_t>(u.expert) * a.estride;
-  const int nt = (u.mt + 15) >> 4;
-  if (nt == 1) run_pass<1, true>(a, sh, wexp, slab, u.row0, u.mt);
-  else if (nt == 2 || kTiles == 2) run_pass<2, true>(a, sh, wexp, slab, u.row0, u.mt);
-  else if constexpr (kTiles > 2) {
-    if (nt == 3) run_pass<3, true>(a, sh, wexp, slab, u.row0, u.mt);
-    else if (nt == 4) run_pass<4, true>(a, sh, wexp, slab, u.row0, u.mt);
-    else run_pass<5, true>(a, sh, wexp, slab, u.row0, u.mt);
-  }
+  if (u.mt <= 16) run_pass<1, true>(a, sh, wexp, slab, u.row0, u.mt);
+  else run_pass<2, true>(a, sh, wexp, slab, u.row0, u.mt);
 }
 
 }  // namespace
@@ -507,36 +500,74 @@ GemvArgs swiglu_gemv(const SwigluArgs& g, const int32_t* pe, float* gu) {
                   pe, nullptr, g.total_m, gu, 1};
 }
 
-}  // namespace
+// Which form a call takes is the cheapest by these estimates in us; they use
+// the rows' expected spread over the experts (the host does not see the
+// offsets).  The matrix-core forms take a time a 256-weight block that depends
+// on the tokens of a pass and on whether a workgroup has its CU alone:
+//   passes of 32 (three to a CU):      alone 1.2 + 0.018 t, full 2.6 + 0.035 t
+//   passes of 80 or 160 (two to a CU): alone 1.25 + 0.0195 t, full 2.05 + 0.0355 t
+// The GEMV splits k over the chip and streams packed weights at 4.6 TB/s, but
+// pays for every row beyond an expert's first.  Measured on 256 CUs, us,
+// passes of 32 / 80 / 160 / GEMV, 2 x 2048 rows of 7168 unless stated:
+//   1 expert: 1 row 39 / - / - / 14, 300 rows 48 / 76 / 117 / 231
+//   8 experts: 64 rows 39 / - / - / 38, 16384 rows 990 / 793 / 696 / -
+//   64 experts: 2048 rows 191 / 180 / 180 / -, 4096 rows 322 / 275 / 233 / -,
+//   12800 rows 860 / 719 / 643 / -
+//   256 experts: 37 rows 79 / - / - / 48, 296 rows 278 / - / - / 190, 1600
+//   rows 442 / 580 / 580 / 477, 4000 rows 472 / 602 / 601 / -
+//   2 x 1024 of 2048, 8 experts: 512 rows 17 / 26 / 26 / -, 4096 rows 50 / 42 /
+//   42 / -, 8192 rows 84 / 73 / 64 / -
+struct GatedForm {
+  int max_tok;  // rows of a pass, 0: the GEMV
+  double us;
+};
 
-// The matrix-core kernel walks a pass's blocks one after another, about 1.2 us
-// each and 0.0225 more a row, and streams packed weights at no more than 3.0
-// TB/s (its decode's LDS reads); the GEMV splits k over the chip and streams
-// at 4.6 TB/s, but pays for every row beyond an expert's first.  Both in us,
-// from the rows' expected spread over the experts; measured on 256 CUs
-// (matrix cores / GEMV, 2 x 2048 rows of 7168 unless stated):
-//   1 expert: 1 row 39 / 14, 32 rows 50 / 40, 80 rows 87 / 72, 300 rows 86 / 231
-//   8 experts: 64 rows 39 / 38, 256 rows 57 / 98
-//   256 experts: 37 rows 79 / 48, 296 rows 278 / 190, 800 rows 391 / 334, 1600
-//   rows 410 / 477
-//   2 x 1024 of 4096, 32 experts: 32 rows 24 / 24, 128 rows 25 / 33
-//   2 x 512 of 1024, 1 expert: 1 row 9 / 11
-bool swiglu_takes_gemv(const SwigluArgs& g, int cus) {
-  if (g.total_m > 4096) return false;  // the GEMV scans its pairs
-  const double rows = static_cast<double>(g.total_m), E = static_cast<double>(g.n_experts);
-  const double used = E * (1.0 - std::pow(1.0 - 1.0 / E, rows));
+double expert_count(double rows, double experts) {  // that have rows
+  return experts * (1.0 - std::pow(1.0 - 1.0 / experts, rows));
+}
+
+GatedForm passes_of(const SwigluArgs& g, int cus, int max_tok) {
+  const bool wide = max_tok > kShortTiles * 16;
+  const int per_cu = wide ? 2 : 3;
+  const double rows = static_cast<double>(g.total_m);
+  const double used = expert_count(rows, static_cast<double>(g.n_experts));
+  const double mean = rows / used, dev = std::sqrt(mean);
+  auto cut = [&](double m) { return std::ceil(std::max(m, 1.0) / max_tok); };
+  const double passes = used * (0.25 * cut(mean - dev) + 0.5 * cut(mean) + 0.25 * cut(mean + dev));
+  const double tok = rows / passes;
+  const double alone = wide ? 1.25 + 0.0195 * tok : 1.2 + 0.018 * tok;
+  const double full = wide ? 2.05 + 0.0355 * tok : 2.6 + 0.035 * tok;
+  const double load = passes * static_cast<double>(g.d_ff / (kSlab / 2)) / cus;  // workgroups of a CU
+  const double rounds = std::floor(load / per_cu), rest = load - rounds * per_cu;
+  double block = rounds * full;
+  if (rest > 0.0) block += alone + (full - alone) * std::max(0.0, rest - 1.0) / (per_cu - 1);
+  return {max_tok, 3.0 + static_cast<double>(g.d_model / kQK) * block};
+}
+
+GatedForm gemv_form(const SwigluArgs& g, int cus) {
+  const double rows = static_cast<double>(g.total_m);
+  const double used = expert_count(rows, static_cast<double>(g.n_experts));
   const double mb = 2e-6 * static_cast<double>(g.d_ff) * (g.d_model / kQK) * kBlockBytes;  // an expert's packed bytes
   const double fill = 256.0 / cus;  // rates of a chip of other size
-  const double mfma = std::max(2.0 + static_cast<double>(g.d_model / kQK) * (1.2 + 0.0225 * std::min(80.0, rows / used)),
-                               used * mb / 3.0 * fill);
-  const double gemv = 10.0 + (used * mb / 4.6 + (rows - used) * (0.13 + 0.6 / std::sqrt(used)) * mb / 4.8) * fill;
-  return gemv < mfma;
+  return {0, 10.0 + (used * mb / 4.6 + (rows - used) * (0.13 + 0.6 / std::sqrt(used)) * mb / 4.8) * fill};
 }
+
+int gated_rows_a_pass(const SwigluArgs& g, int cus) {
+  if (g.total_m == 0) return kShortTiles * 16;
+  GatedForm best = passes_of(g, cus, kShortTiles * 16);
+  for (int t : {160, 80})
+    if (const GatedForm f = passes_of(g, cus, t); f.us < best.us) best = f;
+  if (g.total_m <= 4096)  // the GEMV scans its pairs
+    if (const GatedForm f = gemv_form(g, cus); f.us < best.us) best = f;
+  return best.max_tok;
+}
+
+}  // namespace
 
 SwigluPlan plan_swiglu(const SwigluArgs& g, int cus) {
   SwigluPlan p{};
-  p.gemv = swiglu_takes_gemv(g, cus);
-  if (!p.gemv) return p;
+  p.max_tok = gated_rows_a_pass(g, cus);
+  if (p.max_tok) return p;
   auto up = [](int64_t b) { return (b + 255) / 256 * 256; };
   p.plan = plan_gemv(swiglu_gemv(g, nullptr, nullptr), cus);
   p.part = up(p.plan.partial_bytes);
@@ -548,7 +579,7 @@ SwigluPlan plan_swiglu(const SwigluArgs& g, int cus) {
 
 hipError_t launch_grouped_swiglu(const SwigluArgs& g, const SwigluPlan& plan, void* ws, hipStream_t s) {
   if (g.total_m == 0) return hipSuccess;
-  if (plan.gemv) {
+  if (plan.max_tok == 0) {
     char* b = static_cast<char*>(ws);
     int32_t* pe = reinterpret_cast<int32_t*>(b + plan.part);
     float* gu = reinterpret_cast<float*>(b + plan.part + plan.pe);
@@ -558,6 +589,7 @@ hipError_t launch_grouped_swiglu(const SwigluArgs& g, const SwigluPlan& plan, vo
     if (e != hipSuccess) return e;
     return launch_swiglu_rows(gu, gemv_partials(plan.plan, b), pe, g.n_experts, g.total_m, g.d_ff, g.h, g.gate_up, s);
   }
+  if (plan.max_tok > kShortTiles * 16) return launch_gated(g, plan.max_tok, s);
   GArgs a{};
   a.w = g.w_table;
   a.estride = g.expert_stride;
@@ -572,13 +604,8 @@ hipError_t launch_grouped_swiglu(const SwigluArgs& g, const SwigluPlan& plan, vo
   a.h = g.h;
   a.gu = g.gate_up;
   a.nslab = static_cast<int>(g.d_ff / (kSlab / 2));
-  // Few tokens an expert: the weights' stream is the bound, and a workgroup
-  // sized for 32 tokens (two thirds of the LDS and registers) runs three to a CU
-  const bool few = g.total_m <= kFewRows * g.n_experts;
-  const int64_t units = (pass_units(g.total_m, g.n_experts, few ? 32 : kMaxTok) + kXcds - 1) / kXcds * kXcds;
-  const dim3 grid(static_cast<unsigned>(units * a.nslab));
-  if (few) hipLaunchKernelGGL((grouped_swiglu_kernel<2, 3>), grid, dim3(kThreads), 0, s, a);
-  else hipLaunchKernelGGL((grouped_swiglu_kernel<kMaxTiles, 2>), grid, dim3(kThreads), 0, s, a);
+  const int64_t units = (pass_units(g.total_m, g.n_experts, kShortTiles * 16) + kXcds - 1) / kXcds * kXcds;
+  hipLaunchKernelGGL(grouped_swiglu_kernel, dim3(static_cast<unsigned>(units * a.nslab)), dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 

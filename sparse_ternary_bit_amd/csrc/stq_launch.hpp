@@ -104,15 +104,17 @@ struct SwigluArgs {
   uint16_t* gate_up;  // may be NULL
 };
 // Few rows go through the decode GEMV (one pair a row), the rest through the
-// matrix-core kernel.
+// matrix cores in passes of at most max_tok rows.
 struct SwigluPlan {
-  bool gemv;
-  GemvPlan plan;          // gemv: of the gate/up product
-  int64_t part, pe, gu;   // gemv: workspace bytes of the split outputs, the rows' experts, the fp32 rows
+  int max_tok;            // 0: the GEMV
+  GemvPlan plan;          // GEMV: of the gate/up product
+  int64_t part, pe, gu;   // GEMV: workspace bytes of the split outputs, the rows' experts, the fp32 rows
   int64_t bytes;          // workspace bytes
 };
 SwigluPlan plan_swiglu(const SwigluArgs& a, int cus);
 hipError_t launch_grouped_swiglu(const SwigluArgs& a, const SwigluPlan& plan, void* ws, hipStream_t s);
+// Its passes of more than 32 rows (k_gated.hip)
+hipError_t launch_gated(const SwigluArgs& a, int max_tok, hipStream_t s);
 
 // The GEMV form's own kernels (k_moe.hip)
 hipError_t launch_row_expert(const int32_t* offsets, int64_t n_experts, int64_t rows, int32_t* pair_expert, hipStream_t s);

@@ -402,3 +402,56 @@ def test_binding_refusals(stq):
         c.backward(need_dw=False, dw=torch.empty(2, 512, 256, dtype=torch.bfloat16, device="cuda"))
     with pytest.raises(stq.StqError, match="workspace"):
         c.backward(workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+
+
+LOADS = [1, 0, 16, 17, 33, 48, 49, 64, 65, 79, 80, 81, 95, 96, 97, 113, 127, 128, 129, 145, 159, 160, 161, 319, 320, 321, 333, 480]
+
+
+@pytest.mark.parametrize("counts, d, f, odd", [([50, 300, 0, 200, 81, 112, 449, 1400], 2048, 1024, False),
+                                               (LOADS * 5 + [3000], 256, 1024, False), (LOADS * 5, 768, 1024, True),
+                                               ([20000, 1, 12345], 512, 256, True), (LOADS * 4 + [400] * 10, 1280, 2048, False)])
+def test_long_passes(stq, counts, d, f, odd):
+    """Enough rows for passes of 80 and of 160, of every number of token tiles.
+
+    Their sums change units between two blocks: a quotient and a product, so two roundings more every
+    eight accumulations.  An accumulation rounds its result once and has 2 u above: u k / 32 of the
+    bound is for these u k / 128."""
+    c = Case(stq, counts, d, f, seed=len(counts), tail=5, odd_scales=odd, slack=256)
+    h = torch.full((c.m, f), 3.0, dtype=torch.bfloat16, device="cuda")
+    gu = torch.full((c.m, 2 * f), 3.0, dtype=torch.bfloat16, device="cuda")
+    c.forward(out=h, gate_up=gu)
+    c.check_forward(h, gu)
+    used = c.bounds[-1]
+    assert bool((h[used:] == 3.0).all()) and bool((gu[used:] == 3.0).all())
+    assert torch.equal(c.forward()[:used], h[:used])
+    c.x[0, 1] = float("nan")                               # stays in its row
+    assert torch.equal(c.forward()[1:used], h[1:used])
+    for bad in ([c.m + 7] * (c.E + 1), [-3] * (c.E + 1), list(range(c.E + 1))[::-1]):
+        c.offsets.copy_(torch.tensor(bad, dtype=torch.int32))
+        guard = torch.full((c.m + 8, f), 3.0, dtype=torch.bfloat16, device="cuda")
+        c.forward(out=guard[:c.m])
+        torch.cuda.synchronize()
+        assert bool((guard[c.m:] == 3.0).all())
+
+
+def test_long_passes_with_blocks_of_no_scale(stq):
+    """Rows whose blocks are all 0, whose first or last is, and an infinite or NaN scale, which stay in their columns."""
+    counts, d, f = [160] * 130, 768, 1024
+    c = Case(stq, counts, d, f, seed=7)
+    blocks = c.table.view(c.E, -1)[:, :2 * f * (d // QK) * BLOCK].view(c.E, 2 * f // 64, d // QK, 64, BLOCK)
+    zero = torch.tensor([0, 0], dtype=torch.uint8, device="cuda")
+    blocks[:, 1, :, 5, :2] = zero                          # row 69
+    blocks[:, 2, 0, 6, :2] = zero                          # row 134's first block
+    blocks[:, 3, 2, 7, :2] = zero                          # row 199's last
+    blocks[:, 4, 1, 8, :2] = torch.tensor([0, 128], dtype=torch.uint8, device="cuda")  # row 264: -0
+    gu = torch.empty((c.m, 2 * f), dtype=torch.bfloat16, device="cuda")
+    h = c.forward(gate_up=gu)
+    c.check_forward(h, gu)
+    assert bool((gu[:, 69] == 0).all()) and bool((h[:, 69] == 0).all())
+    for at, bits in ((5, [0, 0x7C]), (6, [0, 0x7E])):      # rows 325 and 390
+        blocks[0, at, 1, at, :2] = torch.tensor(bits, dtype=torch.uint8, device="cuda")
+    bad = c.forward()
+    keep = torch.ones(f, dtype=torch.bool, device="cuda")
+    keep[[325, 390]] = False
+    assert torch.equal(bad[:, keep], h[:, keep]) and torch.equal(bad[160:], h[160:])
+    assert not bool(torch.isfinite(bad[:160, 390]).any())
