@@ -500,12 +500,9 @@ GemvArgs swiglu_gemv(const SwigluArgs& g, const int32_t* pe, float* gu) {
                   pe, nullptr, g.total_m, gu, 1};
 }
 
-// Which form a call takes is the cheapest by these estimates in us; they use
-// the rows' expected spread over the experts (the host does not see the
-// offsets).  The matrix-core forms take a time a 256-weight block that depends
-// on the tokens of a pass and on whether a workgroup has its CU alone:
-//   passes of 32 (three to a CU):      alone 1.2 + 0.018 t, full 2.6 + 0.035 t
-//   passes of 80 or 160 (two to a CU): alone 1.25 + 0.0195 t, full 2.05 + 0.0355 t
+// Which form a call takes is the cheapest by these estimates in us.  The
+// matrix-core forms, passes of 32 rows and longer ones of 80 or 160, take a
+// time a 256-weight block that depends on a pass's rows and the chip's load.
 // The GEMV splits k over the chip and streams packed weights at 4.6 TB/s, but
 // pays for every row beyond an expert's first.  Measured on 256 CUs, us,
 // passes of 32 / 80 / 160 / GEMV, 2 x 2048 rows of 7168 unless stated:
@@ -522,31 +519,16 @@ struct GatedForm {
   double us;
 };
 
-double expert_count(double rows, double experts) {  // that have rows
-  return experts * (1.0 - std::pow(1.0 - 1.0 / experts, rows));
-}
-
 GatedForm passes_of(const SwigluArgs& g, int cus, int max_tok) {
-  const bool wide = max_tok > kShortTiles * 16;
-  const int per_cu = wide ? 2 : 3;
-  const double rows = static_cast<double>(g.total_m);
-  const double used = expert_count(rows, static_cast<double>(g.n_experts));
-  const double mean = rows / used, dev = std::sqrt(mean);
-  auto cut = [&](double m) { return std::ceil(std::max(m, 1.0) / max_tok); };
-  const double passes = used * (0.25 * cut(mean - dev) + 0.5 * cut(mean) + 0.25 * cut(mean + dev));
-  const double tok = rows / passes;
-  const double alone = wide ? 1.25 + 0.0195 * tok : 1.2 + 0.018 * tok;
-  const double full = wide ? 2.05 + 0.0355 * tok : 2.6 + 0.035 * tok;
-  const double load = passes * static_cast<double>(g.d_ff / (kSlab / 2)) / cus;  // workgroups of a CU
-  const double rounds = std::floor(load / per_cu), rest = load - rounds * per_cu;
-  double block = rounds * full;
-  if (rest > 0.0) block += alone + (full - alone) * std::max(0.0, rest - 1.0) / (per_cu - 1);
-  return {max_tok, 3.0 + static_cast<double>(g.d_model / kQK) * block};
+  constexpr PassCost kShort{3.0, {1.2, 0.018}, {2.6, 0.035}}, kLong{2.0, {1.25, 0.0195}, {2.05, 0.0355}};
+  const double step = pass_step_us(max_tok > kShortTiles * 16 ? kLong : kShort, g.total_m, g.n_experts, max_tok,
+                                   g.d_ff / (kSlab / 2), cus);
+  return {max_tok, 3.0 + static_cast<double>(g.d_model / kQK) * step};
 }
 
 GatedForm gemv_form(const SwigluArgs& g, int cus) {
   const double rows = static_cast<double>(g.total_m);
-  const double used = expert_count(rows, static_cast<double>(g.n_experts));
+  const double used = used_experts(rows, static_cast<double>(g.n_experts));
   const double mb = 2e-6 * static_cast<double>(g.d_ff) * (g.d_model / kQK) * kBlockBytes;  // an expert's packed bytes
   const double fill = 256.0 / cus;  // rates of a chip of other size
   return {0, 10.0 + (used * mb / 4.6 + (rows - used) * (0.13 + 0.6 / std::sqrt(used)) * mb / 4.8) * fill};

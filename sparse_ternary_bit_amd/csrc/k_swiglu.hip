@@ -142,7 +142,7 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
 // dx = dz W
 // ---------------------------------------------------------------------------
 // A workgroup of 4 wavefronts owns one 256-weight block column of one expert
-// (256 of dx's columns) and a pass of at most 80 of its rows; the sum runs
+// (256 of dx's columns) and a pass of at most 96 of its rows; the sum runs
 // over the matrix's 64-row tiles.  W enters transposed: an MFMA lane takes 8
 // consecutive rows of one group of four columns.
 //
@@ -162,15 +162,16 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
 // All of it runs ahead of the matrix cores: while they multiply one 32-row
 // step, the next step's table reads are in flight, and the next tile's codes
 // and dz are written between a tile's two steps.  For 16384 rows of 256
-// experts of 4096 x 7168 the products alone take about half the kernel's time;
-// the rest is the instructions of the decode (a form that multiplied d into
-// the weights and transposed the codes in registers had 135 VALU instructions
-// per tile and 34 products, and took 1270 us).
+// experts of 4096 x 7168 it takes 1060 us; the products alone would take about
+// 700, the rest is the instructions of the decode (a form that multiplied d
+// into the weights and transposed the codes in registers had 135 VALU
+// instructions per tile and 34 products, and took 1270 us).  The same rows of
+// 8 experts, in passes of 96, take 860 (passes of 80: 910).
 
 constexpr int kWaves = 4;
 constexpr int kThreads = kWaves * 64;
 constexpr int kXcds = 8;
-constexpr int kMaxTok = 80;
+constexpr int kMaxTok = 96;
 constexpr int kStageTok = (kMaxTok + 31) / 32 * 32;
 constexpr int kRing = 8;            // a power of two, at least 5 (see the order of a tile)
 constexpr int kRun = kTileRows * kBlockBytes;
@@ -186,6 +187,7 @@ struct DxArgs {
   const uint16_t* dz;  // fp16 [total_m, 64 tiles]
   const float* inv;
   uint16_t* dx;        // bf16 [total_m, 256 nb]
+  int max_tok;         // of a pass
 };
 
 struct DxSmem {
@@ -382,6 +384,9 @@ __device__ __forceinline__ void dx_pass(const DxArgs& a, DxSmem& sh, const uint8
   const int last = a.tiles - 1;  // there are at least 8 tiles
 #pragma unroll
   for (int t = 0; t < 5; ++t) stage_w(t);
+  // dz is loaded two tiles ahead, or one where two would not fit the registers
+  // (spilled, they cost 12 % at 96 rows)
+  constexpr int kDepth = NT > 5 ? 1 : 2;
   Z z[2];
   z[0] = load_z(0);
   asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
@@ -396,8 +401,8 @@ __device__ __forceinline__ void dx_pass(const DxArgs& a, DxSmem& sh, const uint8
     next = raise(d1, expo);
     put_z(z[0], read_scales(0), 0, expo);
   }
-  z[1] = load_z(1);
-  z[0] = load_z(2);
+  z[kDepth - 1] = load_z(1);
+  if (kDepth == 2) z[0] = load_z(2);
   take_codes(codes);
   Step p;
 #pragma unroll
@@ -407,10 +412,10 @@ __device__ __forceinline__ void dx_pass(const DxArgs& a, DxSmem& sh, const uint8
     combine(p, B[0], h);
   }
   // Tile t, its first step's operands ready.  nz holds dz of tile t + 1, on its
-  // way since tile t - 2, and then takes t + 3.  The run of tile t + 5 starts
-  // ahead of those loads, so when dz of tile t + 3 has arrived (in tile t + 2)
-  // it has too, and that tile's barrier shows it to every wavefront: its scales
-  // are read in tile t + 3, its codes in tile t + 4.
+  // way since tile t - kDepth, and then takes t + 1 + kDepth.  The run of tile t
+  // + 5 starts ahead of those loads, so when they have arrived (in tile t +
+  // kDepth) it has too, and that tile's barrier shows it to every wavefront: its
+  // scales are read in tile t + 3, its codes in tile t + 4.
   auto tile = [&](int t, int buf, Z& nz) {
     const Raw n = read_raw(t + 1);  // past the last tile: runs read before, not used
     const uint16_t d = read_d(t + 2);
@@ -426,7 +431,7 @@ __device__ __forceinline__ void dx_pass(const DxArgs& a, DxSmem& sh, const uint8
     });
     if (t + 5 <= last) stage_w(t + 5);
     __builtin_amdgcn_sched_barrier(0);
-    nz = load_z(min(t + 3, last));
+    nz = load_z(min(t + 1 + kDepth, last));
     // tile t + 1's dz is written and tile t's is read, by everyone
     take_codes(codes);
     multiply(buf ^ 1, 1, [&](int k) {
@@ -444,7 +449,7 @@ __device__ __forceinline__ void dx_pass(const DxArgs& a, DxSmem& sh, const uint8
     if (t + 2 <= last) next = raise(d, next);
   };
   for (int t = 0; t < last; t += 2) {  // an even number of tiles: the matrix has 512 rows or a multiple
-    tile(t, 0, z[1]);
+    tile(t, 0, z[kDepth - 1]);
     tile(t + 1, 1, z[0]);
   }
   // dx[row0 + 16i + 4q + e, 256b + 64 wave + 4r + 0..3]
@@ -474,7 +479,7 @@ __global__ __launch_bounds__(kThreads, 2) void swiglu_dx_kernel(DxArgs a) {
   const int xcd = blockIdx.x % kXcds;
   const int local = blockIdx.x / kXcds;
   const int b = local % a.nb;
-  const PassUnit u = find_pass(a.offsets, a.n_experts, a.total_m, (local / a.nb) * kXcds + xcd, kMaxTok);
+  const PassUnit u = find_pass(a.offsets, a.n_experts, a.total_m, (local / a.nb) * kXcds + xcd, a.max_tok);
   if (u.mt <= 0) return;
   if (threadIdx.x < 32) {
     uint64_t v = 0;
@@ -491,7 +496,8 @@ __global__ __launch_bounds__(kThreads, 2) void swiglu_dx_kernel(DxArgs a) {
     case 2: dx_pass<2>(a, sh, wexp, b, u.row0, u.mt); break;
     case 3: dx_pass<3>(a, sh, wexp, b, u.row0, u.mt); break;
     case 4: dx_pass<4>(a, sh, wexp, b, u.row0, u.mt); break;
-    default: dx_pass<5>(a, sh, wexp, b, u.row0, u.mt); break;
+    case 5: dx_pass<5>(a, sh, wexp, b, u.row0, u.mt); break;
+    default: dx_pass<6>(a, sh, wexp, b, u.row0, u.mt); break;
   }
 }
 
@@ -674,7 +680,22 @@ SwigluBwdLayout swiglu_bwd_layout(int64_t d_ff, int64_t total_m, bool dx, bool d
   return l;
 }
 
-hipError_t launch_swiglu_bwd(const SwigluBwdArgs& g, void* ws, hipStream_t s) {
+namespace {
+
+// Rows of a pass: 96, or 32 where those would leave much of the chip idle.
+// Measured, us of the whole call without dW, 96 / 32: one expert of 2 x 1024
+// of 4096, 100 rows 33 / 28, 500 rows 41 / 30, 4000 rows 88 / 128; 2 x 2048 of
+// 7168, 8 experts, 300 rows 57 / 61, 4096 rows 266 / 385.  (Passes of 80: 39
+// for 500 rows, 97 for 4000, 285 for 4096 of 8 experts.)
+int dx_rows_a_pass(const SwigluBwdArgs& g, int cus) {
+  constexpr PassCost kCost{2.0, {0.5, 0.007}, {0.64, 0.0108}};  // a 64-row tile
+  auto step = [&](int max_tok) { return pass_step_us(kCost, g.total_m, g.n_experts, max_tok, g.d_model / kQK, cus); };
+  return step(32) < 0.95 * step(kMaxTok) ? 32 : kMaxTok;
+}
+
+}  // namespace
+
+hipError_t launch_swiglu_bwd(const SwigluBwdArgs& g, void* ws, int cus, hipStream_t s) {
   const SwigluBwdLayout l = swiglu_bwd_layout(g.d_ff, g.total_m, g.dx != nullptr, g.dw != nullptr);
   char* base = static_cast<char*>(ws);
   uint16_t* dz16 = g.dx ? reinterpret_cast<uint16_t*>(base) : nullptr;
@@ -688,8 +709,8 @@ hipError_t launch_swiglu_bwd(const SwigluBwdArgs& g, void* ws, hipStream_t s) {
   }
   if (g.dx && g.total_m > 0) {
     DxArgs a{g.w_table, g.expert_stride, static_cast<int>(g.n_experts), static_cast<int>(g.d_model / kQK),
-             static_cast<int>(2 * g.d_ff / kTileRows), g.offsets, g.total_m, dz16, inv, g.dx};
-    const int64_t units = (pass_units(g.total_m, g.n_experts, kMaxTok) + kXcds - 1) / kXcds * kXcds;
+             static_cast<int>(2 * g.d_ff / kTileRows), g.offsets, g.total_m, dz16, inv, g.dx, dx_rows_a_pass(g, cus)};
+    const int64_t units = (pass_units(g.total_m, g.n_experts, a.max_tok) + kXcds - 1) / kXcds * kXcds;
     hipLaunchKernelGGL(swiglu_dx_kernel, dim3(static_cast<unsigned>(units * a.nb)), dim3(kThreads), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

@@ -502,7 +502,8 @@ stq_status stq_grouped_swiglu_backward(const uint8_t* w_gate_up, int64_t gate_up
   if (st != STQ_OK) return st;
   const stq::SwigluBwdArgs a{w_gate_up, gate_up_stride_bytes, n_experts, d_model, d_ff, x_sorted, expert_offsets,
                              total_m, gate_up, dh, dx, dw};
-  hipError_t e = stq::launch_swiglu_bwd(a, workspace, reinterpret_cast<hipStream_t>(stream));
+  const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  hipError_t e = stq::launch_swiglu_bwd(a, workspace, stq::cus_of_stream(s), s);
   if (e != hipSuccess) return hip_fail(e, "stq_grouped_swiglu_backward launch");
   return ok();
 }

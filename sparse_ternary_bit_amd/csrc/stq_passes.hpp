@@ -6,6 +6,9 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+#include <cmath>
+
 namespace stq {
 
 // Most passes that total_m rows of n_experts can make: sum ceil(m_e / T) over
@@ -14,6 +17,29 @@ namespace stq {
 inline int64_t pass_units(int64_t total_m, int64_t n_experts, int64_t max_tok) {
   const int64_t k = n_experts < total_m ? n_experts : total_m;
   return k + (total_m - k) / max_tok;
+}
+
+// Experts that have rows, when `rows` rows choose among `experts` evenly.
+inline double used_experts(double rows, double experts) { return experts * (1.0 - std::pow(1.0 - 1.0 / experts, rows)); }
+
+// What a kernel of such passes takes for one step of its sum (a block, a
+// tile), in us: a workgroup's step takes alone[0] + alone[1] t with a CU to
+// itself and full[0] + full[1] t with `per_cu` on one, t the rows of a pass.
+// A pass makes `slabs` workgroups; the rows' spread over the experts is the
+// even one's (the host does not see the offsets).
+struct PassCost {
+  double per_cu, alone[2], full[2];
+};
+inline double pass_step_us(const PassCost& c, int64_t total_m, int64_t n_experts, int max_tok, int64_t slabs, int cus) {
+  const double rows = static_cast<double>(total_m), used = used_experts(rows, static_cast<double>(n_experts));
+  const double mean = rows / used, dev = std::sqrt(mean);
+  auto cut = [&](double m) { return std::ceil(std::max(m, 1.0) / max_tok); };
+  const double passes = used * (0.25 * cut(mean - dev) + 0.5 * cut(mean) + 0.25 * cut(mean + dev));
+  const double tok = rows / passes;
+  const double alone = c.alone[0] + c.alone[1] * tok, full = c.full[0] + c.full[1] * tok;
+  const double load = passes * static_cast<double>(slabs) / cus;  // workgroups of a CU
+  const double rounds = std::floor(load / c.per_cu), rest = load - rounds * c.per_cu;
+  return rounds * full + (rest > 0.0 ? alone + (full - alone) * std::max(0.0, rest - 1.0) / (c.per_cu - 1.0) : 0.0);
 }
 
 struct PassUnit {

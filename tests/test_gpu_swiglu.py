@@ -455,3 +455,15 @@ def test_long_passes_with_blocks_of_no_scale(stq):
     keep[[325, 390]] = False
     assert torch.equal(bad[:, keep], h[:, keep]) and torch.equal(bad[160:], h[160:])
     assert not bool(torch.isfinite(bad[:160, 390]).any())
+
+
+@pytest.mark.parametrize("counts, d, f, odd", [(LOADS * 4 + [1500], 2048, 256, False), (LOADS * 5, 1280, 512, True),
+                                               ([96] * 40 + [95, 97, 81, 1, 0, 66, 50], 3584, 256, False),
+                                               ([9000, 1, 7000], 1024, 256, True)])
+def test_long_passes_of_the_gradients(stq, counts, d, f, odd):
+    """Enough rows for passes of 96 in the gradient of x, of every number of token tiles."""
+    c = Case(stq, counts, d, f, seed=len(counts) + 2, odd_scales=odd, slack=512)
+    dx, dw = c.backward()
+    c.check_backward(dx, dw)
+    only_x, _ = c.backward(need_dw=False)
+    assert torch.equal(only_x, dx)
