@@ -43,11 +43,12 @@
  *     the caller's next synchronisation;
  *   - the library allocates no device memory and keeps no device state: the
  *     entry points that need scratch memory (stq_gemv, stq_moe_ffn_decode,
- *     stq_layer_errors) take a caller-owned `workspace` of `workspace_bytes`
+ *     stq_layer_errors, stq_grouped_swiglu, stq_grouped_swiglu_backward,
+ *     stq_token_logprobs) take a caller-owned `workspace` of `workspace_bytes`
  *     bytes, 256-byte aligned, whose required size a host-only query gives
- *     for the same shapes (stq_gemv_plan, stq_moe_ffn_workspace,
- *     stq_layer_errors_workspace); a NULL or smaller workspace is refused
- *     with STQ_E_ARG before any launch.  The workspace is in use until the
+ *     for the same shapes (stq_gemv_plan, and the call's name with _workspace
+ *     behind it for the others: stq_moe_ffn_workspace for the FFN); a NULL or
+ *     smaller workspace is refused with STQ_E_ARG before any launch.  The workspace is in use until the
  *     call's work on `stream` completes, so calls that run concurrently need
  *     workspaces of their own; its contents between calls are meaningless;
  *   - apart from the thread-local error text the entry points are stateless
@@ -321,8 +322,12 @@ stq_status stq_greedy_allocation(const double* gain, const double* extra_bytes, 
  *   gate_up         bf16 [total_m, 2*d_ff] = [g | u], what the backward pass
  *                   reads, or NULL; 16-byte aligned
  * bf16 x ternary products are exact, sums fp32, and h and gate_up are each
- * rounded from the fp32 sums once.  Few rows run through stq_gemv's kernels
- * and need scratch:
+ * rounded from the fp32 sums once.  Sums may be held in units of the current
+ * block's d (the change of unit rounds them once a block), so a row of W
+ * should not have a d that is 3e38 times smaller than its sums.  An infinity
+ * or a NaN in x makes its row's outputs NaN, or reaches them only through
+ * weights that are not 0, depending on the form taken; other rows never see
+ * it.  Few rows run through stq_gemv's kernels and need scratch:
  *   workspace, workspace_bytes   at least what stq_grouped_swiglu_workspace
  *                   reports for these shapes on this stream's device (may be
  *                   NULL when that is 0)
@@ -404,8 +409,8 @@ stq_status stq_q8_quantize_rows(const void* x, int x_dtype, int64_t x_row_stride
  *                the fp32 value), rows y_row_stride elements apart; rows that
  *                start on four elements store faster
  * 1 <= k <= 131071 (any sum of products of bytes then fits 32 bits); m up to
- * 2^22, n up to 2^26, m * n up to 2^38.  Integer sums do not depend on their order: a result's bits do not
- * depend on m, n, the strides or the device. */
+ * 2^22, n up to 2^26, m * n up to 2^38.  Integer sums do not depend on their
+ * order: a result's bits do not depend on m, n, the strides or the device. */
 stq_status stq_q8_matmul(const int8_t* a, int64_t a_row_stride, const float* a_scale, const int8_t* w,
                          int64_t w_row_stride, const float* w_scale, int64_t m, int64_t n, int64_t k, void* y,
                          int y_dtype, int64_t y_row_stride, stq_stream_t stream);

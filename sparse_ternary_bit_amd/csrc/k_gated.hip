@@ -33,7 +33,7 @@
 // Measured against passes of 80 rows of the plain kernel's form, us: 8 experts
 // of 7168 x 2048, 16384 rows 827 -> 696 (1.38 PFLOP/s); 64 experts of 100
 // rows 390 -> 323, of 64 rows 259 -> 233; 32 uneven experts of 4096 x 1024,
-// 8191 rows 153 -> 120; 256 experts of 64 rows 980 -> 947.  What bounds it:
+// 8191 rows 155 -> 145; 256 experts of 64 rows 925 -> 925.  What bounds it:
 // the matrix cores are busy 56 % of the cycles at 64 rows a pass and the card
 // runs at 1.85 of its 2.4 GHz under this load (a loop of these products
 // alone reaches 1.97 PFLOP/s on such numbers); left out one at a time, the
@@ -66,6 +66,7 @@ constexpr int kWLoads = 3;
 constexpr int kWindow = kWLoads * 1024;
 constexpr int kCodes = 33;              // the 32 codes and one of four zeros
 constexpr int kAhead = 2;               // token tiles read ahead of their products
+constexpr int kLonger = 64;             // rows of a pass that goes first
 constexpr int kTiles = 10;              // token tiles of a pass
 
 struct GatedArgs {
@@ -346,7 +347,7 @@ __global__ __launch_bounds__(kThreads, 2) void gated_kernel(GatedArgs a) {
   const int xcd = blockIdx.x % kXcds;
   const int local = blockIdx.x / kXcds;
   const int slab = local % a.nslab;
-  const PassUnit u = find_pass(a.offsets, a.n_experts, a.total_m, (local / a.nslab) * kXcds + xcd, a.max_tok);
+  const PassUnit u = find_pass(a.offsets, a.n_experts, a.total_m, (local / a.nslab) * kXcds + xcd, a.max_tok, kLonger);
   if (u.mt <= 0) return;
   if (threadIdx.x < kCodes) {
     sh.lut[threadIdx.x] = threadIdx.x < 32 ? pattern_word(threadIdx.x, 0) : 0u;

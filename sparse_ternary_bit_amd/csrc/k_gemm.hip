@@ -458,7 +458,7 @@ __global__ __launch_bounds__(kThreads, 3) void grouped_swiglu_kernel(GArgs a) {
   const int xcd = blockIdx.x % kXcds;
   const int local = blockIdx.x / kXcds;
   const int slab = local % a.nslab;
-  const PassUnit u = find_pass(a.offsets, a.n_experts, a.total_m, (local / a.nslab) * kXcds + xcd, kShortTiles * 16);
+  const PassUnit u = find_pass(a.offsets, a.n_experts, a.total_m, (local / a.nslab) * kXcds + xcd, kShortTiles * 16, 0);
   if (u.mt <= 0) return;
   if (threadIdx.x < 32) {
     sh.lut[threadIdx.x] = pattern_word(threadIdx.x, 0);

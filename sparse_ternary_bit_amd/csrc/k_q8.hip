@@ -113,7 +113,7 @@ __device__ __forceinline__ u32x4_t quantize16(const float (&v)[16], float scale,
 // the maximum and the rounding; longer ones are read again, from cache.
 // kVec: rows start on 16 bytes.
 // A batch of rows fills the chip with workgroups of 256 (8192 rows of 7168:
-// 49 us, 57 with 512); a few rows are latency, which more threads a row shorten
+// 43 us, 57 with 512); a few rows are latency, which more threads a row shorten
 // (one row: 4.1 us against 6.1).
 template <typename T, bool kVec, int kQuantThreads>
 __global__ __launch_bounds__(kQuantThreads) void q8_quantize_kernel(QuantArgs a) {

@@ -172,6 +172,7 @@ constexpr int kWaves = 4;
 constexpr int kThreads = kWaves * 64;
 constexpr int kXcds = 8;
 constexpr int kMaxTok = 96;
+constexpr int kLonger = 64;         // rows of a pass that goes first
 constexpr int kStageTok = (kMaxTok + 31) / 32 * 32;
 constexpr int kRing = 8;            // a power of two, at least 5 (see the order of a tile)
 constexpr int kRun = kTileRows * kBlockBytes;
@@ -479,7 +480,7 @@ __global__ __launch_bounds__(kThreads, 2) void swiglu_dx_kernel(DxArgs a) {
   const int xcd = blockIdx.x % kXcds;
   const int local = blockIdx.x / kXcds;
   const int b = local % a.nb;
-  const PassUnit u = find_pass(a.offsets, a.n_experts, a.total_m, (local / a.nb) * kXcds + xcd, a.max_tok);
+  const PassUnit u = find_pass(a.offsets, a.n_experts, a.total_m, (local / a.nb) * kXcds + xcd, a.max_tok, kLonger);
   if (u.mt <= 0) return;
   if (threadIdx.x < 32) {
     uint64_t v = 0;

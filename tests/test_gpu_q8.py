@@ -122,7 +122,7 @@ def _check(y, a, sa, w, sw):
 SHAPES = [(1, 1, 1), (1, 64, 16), (1, 4096, 7168), (2, 100, 130), (7, 333, 1000), (16, 65, 4096), (17, 64, 127),
           (33, 129, 257), (64, 1003, 2049), (65, 128, 128), (100, 77, 15), (128, 256, 512), (129, 513, 333),
           (300, 200, 1111), (512, 640, 4096), (1000, 1000, 100), (257, 300, 20000), (5, 9001, 320), (20, 20011, 500), (50, 17000, 777),
-          (1100, 2100, 200), (2100, 4200, 300), (2048, 4096, 1024)]
+          (1100, 2100, 200), (2100, 4200, 300), (2048, 4096, 1024), (20, 70001, 96), (9, 70001, 130), (64, 131090, 50)]
 
 
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
