@@ -8,7 +8,7 @@
 // the current block's d: between two blocks every sum is multiplied by
 // d_before / d_now (one rounding to fp32 a block, as the other form's fused
 // add has), and by the last d at the end.  A block whose d is 0 keeps the
-// scale and gets the code of four zeros, the table's 33rd.  A sum is
+// scale and gets codes of four zeros, the table's second half.  A sum is
 // therefore held as sum / d, which leaves fp32 only for sums beyond 3e38 d.
 // The registers that frees (64 weight rows x 160 tokens a wavefront take 160
 // of 256) halve the decode per matrix product: 0.5 LDS reads and 2.2 VALU
@@ -25,20 +25,22 @@
 // in registers, so products go on while the next stage's first reads return,
 // and the buffer's next fill starts at once.  Token tiles are read kAhead
 // ahead, the weights' operands of a k-step are decoded under the products of
-// the one before.  The loop has no branch: past the last block it stages the
+// the one before, and the next block's records are made in six pieces between
+// the last stage's token tiles (in one piece ahead of them: 905 us against 880
+// for 64 rows of 256 experts).  The loop has no branch: past the last block it stages the
 // last one again, which nothing reads.  (With branches the compiler moved
 // accumulators through scratch memory, and a reload waits for every direct
 // load in flight: 5 to 12 reloads a block cost 3 to 6 %.)
 //
 // Measured against passes of 80 rows of the plain kernel's form, us: 8 experts
-// of 7168 x 2048, 16384 rows 827 -> 696 (1.38 PFLOP/s); 64 experts of 100
-// rows 390 -> 323, of 64 rows 259 -> 233; 32 uneven experts of 4096 x 1024,
-// 8191 rows 155 -> 145; 256 experts of 64 rows 925 -> 925.  What bounds it:
-// the matrix cores are busy 56 % of the cycles at 64 rows a pass and the card
-// runs at 1.85 of its 2.4 GHz under this load (a loop of these products
-// alone reaches 1.97 PFLOP/s on such numbers); left out one at a time, the
-// weights' stream, the records, the activations' stream, the pattern reads
-// and the scale give 9, 11, 8, 7 and 4 %, and all of them together 34 %.  Three
+// of 7168 x 2048, 16384 rows 819 -> 670 (1.43 PFLOP/s); 64 experts of 100
+// rows 381 -> 310; 32 uneven experts of 4096 x 1024, 8191 rows 155 -> 138; 256
+// experts of 64 rows 915 -> 882.  What bounds it: the matrix cores are busy 54 %
+// of the cycles at 64 rows a pass and the card runs at 1.9 of its 2.4 GHz
+// under this load (a loop of these products alone reaches 1.97 PFLOP/s on such
+// numbers); left out one at a time, the weights' stream, the records, the
+// activations' stream, the pattern reads and the scale gave 9, 11, 8, 7 and 4
+// %, and all of them together 34 %.  Three
 // wavefronts a SIMD (passes of 80 rows in 168 registers) and a ring of four
 // stages changed nothing there.
 #include <cstddef>
@@ -64,7 +66,7 @@ constexpr int kXcds = 8;
 constexpr int kHalfRun = kTileRows / 2 * kBlockBytes;  // half a tile's run of one block, a multiple of 16
 constexpr int kWLoads = 3;
 constexpr int kWindow = kWLoads * 1024;
-constexpr int kCodes = 33;              // the 32 codes and one of four zeros
+constexpr int kCodes = 64;              // the 32 codes, and with bit 5 set four zeros
 constexpr int kAhead = 2;               // token tiles read ahead of their products
 constexpr int kLonger = 64;             // rows of a pass that goes first
 constexpr int kTiles = 10;              // token tiles of a pass
@@ -108,14 +110,8 @@ __device__ __forceinline__ uint32_t pattern_word(uint32_t c, int lane) {
 
 __device__ __forceinline__ uint16_t bf16_bits(float v) { return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v)); }
 
-// opaque, so that what is derived from them is not kept over the loop in
+// the lane, opaque: what is derived from it is not kept over the loop in
 // registers that the sums need
-__device__ __forceinline__ int pass_tid() {
-  int t;
-  asm volatile("v_mov_b32 %0, %1" : "=v"(t) : "v"(static_cast<int>(threadIdx.x)));
-  return t;
-}
-
 __device__ __forceinline__ int lane_now() {
   int t;
   asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(t));
@@ -133,9 +129,8 @@ template <int NT>
 __device__ __forceinline__ void run_pass(const GatedArgs& a, Smem& sh, const uint8_t* wexp, int slab, int64_t row0,
                                          int mt) {
   static_assert(NT >= 2 && NT <= kTiles && kTiles % 2 == 0, "two tiles a wavefront's loads, and a stage longer than kAhead");
-  const int tid = pass_tid();
-  const int lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lane = lane_now();
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q = lane >> 4, r = lane & 15;
 
   // half a tile of gate rows and the half tile of the same up rows
@@ -180,41 +175,67 @@ __device__ __forceinline__ void run_pass(const GatedArgs& a, Smem& sh, const uin
     }
   };
 
-  // the block in the window: this lane's row's codes, each times 4, as records
-  auto make_records = [&] {
-    const int lane = lane_now();
-    // 42 bytes from an even byte: `sel` joins the halves of its words
+  // The block in the window: this lane's row's codes, each times 4, as records.
+  // 42 bytes from an even byte: `sel` joins the halves of its words.  In pieces
+  // that the products can hide: the words' reads run one piece ahead.
+  constexpr bool kSpread = NT >= 4;  // room for the pieces between the stage's tiles
+  struct Row {
+    uint32_t v[3], sel, zero;  // words of the next k-step pair; 0x80808080 if d is 0
+    uint32_t qh[2];
+  } row;
+  const char* const window = sh.wraw[wave];
+  auto read_head = [&](int lane) {
     const uint32_t off = lane * kBlockBytes;
-    const uint32_t* wv = reinterpret_cast<const uint32_t*>(sh.wraw[wave] + (off & ~3u));
-    const uint32_t sel = (off & 2u) ? 0x07060504u : 0x05040302u;
-    const uint32_t w0 = wv[0], w8 = wv[8], w9 = wv[9], w10 = wv[10];
-    const float d = half_bits_to_float((off & 2u) ? w0 >> 16 : w0);
-    const uint32_t qh[2] = {__builtin_amdgcn_perm(w9, w8, sel), __builtin_amdgcn_perm(w10, w9, sel)};
-    const bool none = d == 0.0f;
-    sh.ratio[wave][lane] = none ? 1.0f : sh.scale[wave][lane] / d;
-    if (!none) sh.scale[wave][lane] = d;
+    const uint32_t* wv = reinterpret_cast<const uint32_t*>(window + (off & ~3u));
+    row.v[0] = wv[0];
+    row.qh[0] = wv[8];
+    row.qh[1] = wv[9];
+    row.v[2] = wv[10];
+  };
+  auto read_pair = [&](int lane, int s2) {
+    const uint32_t off = lane * kBlockBytes;
+    const uint32_t* wv = reinterpret_cast<const uint32_t*>(window + (off & ~3u)) + 2 * s2;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) row.v[i] = wv[i];
+  };
+  auto put_head = [&](int lane) {
+    const bool odd = lane & 1;  // starts in the middle of a word
+    row.sel = odd ? 0x07060504u : 0x05040302u;
+    const float d0 = half_bits_to_float(odd ? row.v[0] >> 16 : row.v[0]);
+    const float was = sh.scale[wave][lane];
+    const float d = d0 == 0.0f ? was : d0;
+    row.zero = d0 == 0.0f ? 0x80808080u : 0u;
+    sh.ratio[wave][lane] = was / d;
+    sh.scale[wave][lane] = d;
+    row.qh[0] = __builtin_amdgcn_perm(row.qh[1], row.qh[0], row.sel);
+    row.qh[1] = __builtin_amdgcn_perm(row.v[2], row.qh[1], row.sel);
+  };
+  auto put_pair = [&](int lane, int s2) {
     const int ti = lane >> 4, tr = lane & 15;
+    uint32_t cl[2], cu[2];
 #pragma unroll
-    for (int s2 = 0; s2 < 4; ++s2) {
-      const uint32_t v0 = wv[2 * s2], v1 = wv[2 * s2 + 1], v2 = wv[2 * s2 + 2];
-      uint32_t cl[2], cu[2];
-#pragma unroll
-      for (int o = 0; o < 2; ++o) {
-        const int s = 2 * s2 + o;
-        const uint32_t W = o ? __builtin_amdgcn_perm(v2, v1, sel) : __builtin_amdgcn_perm(v1, v0, sel);
-        const uint32_t QH = qh[s >> 2];
-        const int sh6 = 6 - 2 * (s & 3);
-        cl[o] = ((W << 2) & 0x3C3C3C3Cu) | ((QH << sh6) & 0x40404040u);
-        cu[o] = ((W >> 2) & 0x3C3C3C3Cu) | (((QH >> 1) << sh6) & 0x40404040u);
-      }
-      sh.rec[wave][s2][0][tr][ti] = __builtin_amdgcn_perm(cl[1], cl[0], 0x05040100u);
-      sh.rec[wave][s2][1][tr][ti] = __builtin_amdgcn_perm(cl[1], cl[0], 0x07060302u);
-      sh.rec[wave][s2][2][tr][ti] = __builtin_amdgcn_perm(cu[1], cu[0], 0x05040100u);
-      sh.rec[wave][s2][3][tr][ti] = __builtin_amdgcn_perm(cu[1], cu[0], 0x07060302u);
+    for (int o = 0; o < 2; ++o) {
+      const uint32_t W = __builtin_amdgcn_perm(row.v[o + 1], row.v[o], row.sel);
+      const uint32_t QH = row.qh[s2 >> 1];
+      const int sh6 = 6 - 2 * ((2 * s2 + o) & 3);
+      cl[o] = ((W << 2) & 0x3C3C3C3Cu) | ((QH << sh6) & 0x40404040u) | row.zero;
+      cu[o] = ((W >> 2) & 0x3C3C3C3Cu) | (((QH >> 1) << sh6) & 0x40404040u) | row.zero;
     }
-    if (none) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) sh.rec[wave][i >> 2][i & 3][tr][ti] = 0x80808080u;
+    sh.rec[wave][s2][0][tr][ti] = __builtin_amdgcn_perm(cl[1], cl[0], 0x05040100u);
+    sh.rec[wave][s2][1][tr][ti] = __builtin_amdgcn_perm(cl[1], cl[0], 0x07060302u);
+    sh.rec[wave][s2][2][tr][ti] = __builtin_amdgcn_perm(cu[1], cu[0], 0x05040100u);
+    sh.rec[wave][s2][3][tr][ti] = __builtin_amdgcn_perm(cu[1], cu[0], 0x07060302u);
+  };
+  // piece i of 0 .. 5; the first pair's records are there after piece 2
+  auto records = [&](int lane, int i) {
+    if (i == 0) read_head(lane);
+    if (i == 1) {
+      put_head(lane);
+      read_pair(lane, 0);
+    }
+    if (i >= 2) {
+      put_pair(lane, i - 2);
+      if (i < 5) read_pair(lane, i - 1);
     }
   };
 
@@ -243,7 +264,8 @@ __device__ __forceinline__ void run_pass(const GatedArgs& a, Smem& sh, const uin
   stage_w(0);
   stage_x(1, 1);
   wait_and_meet<kXLoads>();
-  make_records();
+#pragma unroll
+  for (int i = 0; i < 6; ++i) records(lane, i);
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the window has been read
   stage_w(min(1, a.nb - 1));
 
@@ -263,7 +285,11 @@ __device__ __forceinline__ void run_pass(const GatedArgs& a, Smem& sh, const uin
     for (int i = 0; i < 4; ++i) up[i] = sh.ratio[wave][16 * i + rr];
 #pragma unroll
     for (int qt = 0; qt < 4; ++qt) {
-      if (qt == 3) make_records();
+      if (qt == 3 && !kSpread) {
+        const int ln = lane_now();
+#pragma unroll
+        for (int i = 0; i < 6; ++i) records(ln, i);
+      }
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
 #pragma unroll
@@ -280,6 +306,7 @@ __device__ __forceinline__ void run_pass(const GatedArgs& a, Smem& sh, const uin
           const int ahead = (p + kAhead) % (2 * NT);
           B[(g + kAhead) & 3] = *reinterpret_cast<const bf16x8_t*>(
               sh.x[(p + kAhead < 2 * NT ? qt : qt + 1) & 1] + xb[ahead / NT] + (ahead % NT) * 16 * kStageRow);
+          if (qt == 3 && kSpread && p < 6) records(lane, p);
           if (ks == 0 && t == NT - 1) Rn = *reinterpret_cast<const u32x4_t*>(&sh.rec[wave][(qt + 1) & 3][q][r][0]);
 #pragma unroll
           for (int c = 0; c < 8; ++c)
@@ -302,10 +329,11 @@ __device__ __forceinline__ void run_pass(const GatedArgs& a, Smem& sh, const uin
   }
 
   // everyone is done with the stages: the outputs go through LDS as whole rows
+  const int tid = wave * 64 + lane_now(), q1 = (tid >> 4) & 3, r1 = tid & 15;
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
   float dl[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) dl[i] = sh.scale[wave][16 * i + r];
+  for (int i = 0; i < 4; ++i) dl[i] = sh.scale[wave][16 * i + r1];
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -322,7 +350,7 @@ __device__ __forceinline__ void run_pass(const GatedArgs& a, Smem& sh, const uin
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<uint16_t*>(tile + (16 * t + 4 * q + j) * kRowB + (wave * 32 + 16 * i + r) * 2) =
+          *reinterpret_cast<uint16_t*>(tile + (16 * t + 4 * q1 + j) * kRowB + (wave * 32 + 16 * i + r1) * 2) =
               bf16_bits(value(t, i, j));
     __syncthreads();
     for (int tok = tid >> 4; tok < mt; tok += kThreads / 16)
