@@ -550,14 +550,16 @@ __global__ __launch_bounds__(kThreads, 2) void swiglu_dw_kernel(DwArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int q = lane >> 4, r = lane & 15;
   // Workgroups are dealt to the XCDs in turn: each takes one run of an
-  // expert's tiles, rows fastest, so that its L2 holds the expert's dz and a
-  // few columns of x.
+  // expert's tiles in bands of 8 rows of tiles, so that those at work together
+  // share a compact block of dz and x in its L2 (4099 rows of 8 experts of
+  // 4096 x 7168: 334 MB fetched and 267 us, 851 MB and 285 with rows fastest).
   const int tr = a.n_r / kTR, tc = a.n_c / kTC;
   const int per = (tr * tc + kXcds - 1) / kXcds;
   const int e = blockIdx.x / (per * kXcds), in = blockIdx.x % (per * kXcds);
   const int tile = (in % kXcds) * per + in / kXcds;
   if (tile >= tr * tc) return;
-  const int r0 = (tile % tr) * kTR, c0 = (tile / tr) * kTC;
+  const int band = tile / (8 * tc), rows = min(8, tr - band * 8), at = tile - band * 8 * tc;
+  const int r0 = (band * 8 + at % rows) * kTR, c0 = (at / rows) * kTC;
   int64_t lo;
   int m;
   expert_rows(a.offsets, e, a.total_m, &lo, &m);
