@@ -19,30 +19,29 @@
 // row a tile and a block's scale is four registers and not sixteen.
 //
 // Per block of 256 weights four stages of 64 activations; a stage's tokens
-// stream into one of two LDS buffers while the other is multiplied.  The
+// stream into one of two LDS buffers while the other is multiplied. The
 // stage's one barrier stands kAhead token tiles before its end, where every
 // wavefront has read the last of the buffer: the tiles behind it are already
 // in registers, so products go on while the next stage's first reads return,
-// and the buffer's next fill starts at once.  Token tiles are read kAhead
+// and the buffer's next fill starts at once. Token tiles are read kAhead
 // ahead, the weights' operands of a k-step are decoded under the products of
 // the one before, and the next block's records are made in six pieces between
 // the last stage's token tiles (in one piece ahead of them: 905 us against 880
-// for 64 rows of 256 experts).  The loop has no branch: past the last block it stages the
-// last one again, which nothing reads.  (With branches the compiler moved
-// accumulators through scratch memory, and a reload waits for every direct
-// load in flight: 5 to 12 reloads a block cost 3 to 6 %.)
+// for 64 rows of 256 experts). The loop has no branch: past the last block it
+// stages the last one again, which nothing reads. (With branches the compiler
+// moved accumulators through scratch memory, and a reload waits for every
+// direct load in flight: 5 to 12 reloads a block cost 3 to 6 %.)
 //
 // Measured against passes of 80 rows of the plain kernel's form, us: 8 experts
-// of 7168 x 2048, 16384 rows 819 -> 670 (1.43 PFLOP/s); 64 experts of 100
-// rows 381 -> 310; 32 uneven experts of 4096 x 1024, 8191 rows 155 -> 138; 256
-// experts of 64 rows 915 -> 882.  What bounds it: the matrix cores are busy 54 %
-// of the cycles at 64 rows a pass and the card runs at 1.9 of its 2.4 GHz
+// of 7168 x 2048, 16384 rows 819 -> 670 (1.43 PFLOP/s); 64 experts of 100 rows
+// 381 -> 310; 32 uneven experts of 4096 x 1024, 8191 rows 155 -> 138; 256
+// experts of 64 rows 915 -> 882. What bounds it: the matrix cores are busy 54
+// % of the cycles at 64 rows a pass and the card runs at 1.9 of its 2.4 GHz
 // under this load (a loop of these products alone reaches 1.97 PFLOP/s on such
 // numbers); left out one at a time, the weights' stream, the records, the
 // activations' stream, the pattern reads and the scale gave 9, 11, 8, 7 and 4
-// %, and all of them together 34 %.  Three
-// wavefronts a SIMD (passes of 80 rows in 168 registers) and a ring of four
-// stages changed nothing there.
+// %, and all of them together 34 %. Three wavefronts a SIMD (passes of 80 rows
+// in 168 registers) and a ring of four stages changed nothing there.
 #include <cstddef>
 #include <type_traits>
 

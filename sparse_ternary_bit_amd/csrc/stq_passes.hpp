@@ -51,10 +51,11 @@ struct PassUnit {
 // Pass `unit` counted over the experts in order, those with passes of more
 // than `longer` rows first: a launch's last workgroups are then short ones
 // (8191 uneven rows of 32 experts, one round of the chip: 142 to 150 us over
-// four draws of the loads, 141 to 171 without).  An expert's rows are clamped to [0, total_m], so that offsets outside the contract reach
-// no row that is not there, and its passes are of equal length.  Every
-// wavefront does this for itself, 256 experts a step: a lane counts the passes
-// of four experts, and a scan over the lanes finds the one that holds the unit.
+// four draws of the loads, 141 to 171 without).  An expert's rows are clamped
+// to [0, total_m], so that offsets outside the contract reach no row that is
+// not there, and its passes are of equal length.  Every wavefront does this
+// for itself, 256 experts a step: a lane counts the passes of four experts,
+// and a scan over the lanes finds the one that holds the unit.
 __device__ __forceinline__ PassUnit find_pass(const int32_t* offsets, int n_experts, int64_t total_m, int unit,
                                               int max_tok, int longer) {
   const int lane = threadIdx.x & 63;

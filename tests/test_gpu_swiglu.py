@@ -409,7 +409,8 @@ LOADS = [1, 0, 16, 17, 33, 48, 49, 64, 65, 79, 80, 81, 95, 96, 97, 113, 127, 128
 
 @pytest.mark.parametrize("counts, d, f, odd", [([50, 300, 0, 200, 81, 112, 449, 1400], 2048, 1024, False),
                                                (LOADS * 5 + [3000], 256, 1024, False), (LOADS * 5, 768, 1024, True),
-                                               ([20000, 1, 12345], 512, 256, True), (LOADS * 4 + [400] * 10, 1280, 2048, False)])
+                                               ([20000, 1, 12345], 512, 256, True), (LOADS * 4 + [400] * 10, 1280, 2048, False),
+                                               (LOADS * 19, 256, 256, True)])
 def test_long_passes(stq, counts, d, f, odd):
     """Enough rows for passes of 80 and of 160, of every number of token tiles.
 
@@ -459,7 +460,7 @@ def test_long_passes_with_blocks_of_no_scale(stq):
 
 @pytest.mark.parametrize("counts, d, f, odd", [(LOADS * 4 + [1500], 2048, 256, False), (LOADS * 5, 1280, 512, True),
                                                ([96] * 40 + [95, 97, 81, 1, 0, 66, 50], 3584, 256, False),
-                                               ([9000, 1, 7000], 1024, 256, True)])
+                                               ([9000, 1, 7000], 1024, 256, True), (LOADS * 12, 512, 256, True)])
 def test_long_passes_of_the_gradients(stq, counts, d, f, odd):
     """Enough rows for passes of 96 in the gradient of x, of every number of token tiles."""
     c = Case(stq, counts, d, f, seed=len(counts) + 2, odd_scales=odd, slack=512)
@@ -467,3 +468,43 @@ def test_long_passes_of_the_gradients(stq, counts, d, f, odd):
     c.check_backward(dx, dw)
     only_x, _ = c.backward(need_dw=False)
     assert torch.equal(only_x, dx)
+
+
+def test_long_passes_under_graph_with_other_loads(stq):
+    """One capture serves any spread of the same number of rows over the experts."""
+    E, d, f, rows = 40, 1024, 512, 9000
+    c = Case(stq, [rows // E] * E, d, f, seed=21)
+    h = torch.empty((c.m, f), dtype=torch.bfloat16, device="cuda")
+    gu = torch.empty((c.m, 2 * f), dtype=torch.bfloat16, device="cuda")
+    dx = torch.empty((c.m, d), dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(stq.grouped_swiglu_backward_workspace(E, d, f, c.m, True, False), dtype=torch.uint8, device="cuda")
+    need = stq.grouped_swiglu_workspace(E, d, f, c.m)
+    assert need == 0                                       # the matrix cores' form
+
+    def call():
+        c.forward(out=h, gate_up=gu)
+        c.stq.grouped_swiglu_backward(*c.args(), gu, c.dh, need_dw=False, dx=dx, workspace=ws)
+    call()
+    torch.cuda.synchronize()
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(g, stream=side):
+            call()
+    torch.cuda.synchronize()
+    rng = np.random.default_rng(3)
+    for loads in (rng.multinomial(rows, np.ones(E) / E), rng.multinomial(rows, 1 / np.arange(1, E + 1) / (1 / np.arange(1, E + 1)).sum()),
+                  np.eye(E, dtype=int)[7] * rows, np.minimum(np.arange(E), 1) * (rows // (E - 1))):
+        c.bounds = [0] + np.cumsum(loads).tolist()
+        c.offsets.copy_(torch.tensor(c.bounds, dtype=torch.int32))
+        c.x.copy_(torch.randn(c.x.shape, generator=torch.Generator().manual_seed(int(loads[1]))).bfloat16())
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        used = c.bounds[-1]
+        got = h[:used].clone(), gu[:used].clone(), dx[:used].clone()
+        gu2 = torch.empty_like(gu)
+        eager = c.forward(gate_up=gu2)
+        dx2, _ = c.stq.grouped_swiglu_backward(*c.args(), gu2, c.dh, need_dw=False)
+        assert all(torch.equal(a, b[:used]) for a, b in zip(got, (eager, gu2, dx2)))
+        c.check_forward(eager, gu2)
