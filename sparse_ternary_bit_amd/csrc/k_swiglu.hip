@@ -151,8 +151,8 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
 //    hands a lane its group's codes of 8 rows.  Each code is the offset of its
 //    four fp16 lanes (+-1, 0) in a 32-entry table; byte permutes pair
 //    neighbouring rows into the operands of four column sets (column 4 group +
-//    j, j = 0..3), so a lane ends with four neighbouring columns of every token
-//    it holds.
+//    j, j = 0..3), so a lane ends with 16 neighbouring columns of every token it
+//    holds.
 //  * Scales: d varies along the sum, so it goes into dz: a thread loads 8
 //    columns of a token, multiplies them by the 8 rows' d / D (packed fp16) and
 //    writes them to LDS.  D is a power of two at or above every |d| met so far,
@@ -162,7 +162,7 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
 // All of it runs ahead of the matrix cores: while they multiply one 32-row
 // step, the next step's table reads are in flight, and the next tile's codes
 // and dz are written between a tile's two steps.  For 16384 rows of 256
-// experts of 4096 x 7168 it takes 1060 us; the products alone would take about
+// experts of 4096 x 7168 it takes 1030 us; the products alone would take about
 // 700, the rest is the instructions of the decode (a form that multiplied d
 // into the weights and transposed the codes in registers had 135 VALU
 // instructions per tile and 34 products, and took 1270 us).  The same rows of
@@ -357,7 +357,9 @@ __device__ __forceinline__ void dx_pass(const DxArgs& a, DxSmem& sh, const uint8
   f16x8_t A[NT];
   u32x4_t B[2][4];
   auto read_a = [&](int buf, int s, int i) { A[i] = *reinterpret_cast<const f16x8_t*>(sh.a[buf] + 16 * i * 128 + oa[s]); };
-  // One step's products with B[s].  Each token operand is read for the step
+  // One step's products with B[s], the weights as the products' rows (as their
+  // columns they take 3 % more time, and leave a lane 4 neighbouring outputs of
+  // a token where it now has 16).  Each token operand is read for the step
   // (buf, s ^ 1) that follows as soon as its last use is issued, and `side`, the
   // work of the steps to come in four pieces, is spread between the products:
   // a wavefront can issue three other instructions while one product runs.
@@ -366,7 +368,7 @@ __device__ __forceinline__ void dx_pass(const DxArgs& a, DxSmem& sh, const uint8
     for (int i = 0; i < NT; ++i) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(A[i], __builtin_bit_cast(f16x8_t, B[s][j]), acc[j][i], 0, 0, 0);
+        acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, B[s][j]), A[i], acc[j][i], 0, 0, 0);
       read_a(buf, s ^ 1, i);
 #pragma unroll
       for (int k = 0; k < 4; ++k)
@@ -453,22 +455,19 @@ __device__ __forceinline__ void dx_pass(const DxArgs& a, DxSmem& sh, const uint8
     tile(t, 0, z[kDepth - 1]);
     tile(t + 1, 1, z[0]);
   }
-  // dx[row0 + 16i + 4q + e, 256b + 64 wave + 4r + 0..3]
+  // dx[row0 + 16i + r, 256b + 64 wave + 16q + 4e + j]: 16 neighbouring columns
   const int64_t ld = static_cast<int64_t>(a.nb) * kQK;
   const float big = ldexpf(1.0f, expo);
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
+    const int tok = 16 * i + r;
+    if (tok >= mt) continue;
+    const float inv = a.inv[row0 + tok];
+    u32x2_t* out = reinterpret_cast<u32x2_t*>(a.dx + (row0 + tok) * ld + b * kQK + 64 * wave + 16 * q);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int tok = 16 * i + 4 * q + e;
-      if (tok >= mt) continue;
-      const float inv = a.inv[row0 + tok];
-      float v[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = acc[j][i][e] * big * inv;
-      *reinterpret_cast<u32x2_t*>(a.dx + (row0 + tok) * ld + b * kQK + 64 * wave + 4 * r) =
-          u32x2_t{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
-    }
+    for (int e = 0; e < 4; ++e)
+      out[e] = u32x2_t{bf16_pair(acc[0][i][e] * big * inv, acc[1][i][e] * big * inv),
+                       bf16_pair(acc[2][i][e] * big * inv, acc[3][i][e] * big * inv)};
   }
 }
 

@@ -508,3 +508,14 @@ def test_long_passes_under_graph_with_other_loads(stq):
         dx2, _ = c.stq.grouped_swiglu_backward(*c.args(), gu2, c.dh, need_dw=False)
         assert all(torch.equal(a, b[:used]) for a, b in zip(got, (eager, gu2, dx2)))
         c.check_forward(eager, gu2)
+
+
+def test_gradient_of_x_eight_bytes_into_a_buffer(stq):
+    """dx needs 8-byte alignment only, and nothing beside it is written."""
+    c = Case(stq, [70, 0, 33, 5], 512, 256, seed=31)
+    want, _ = c.backward(need_dw=False)
+    buf = torch.full((c.m * c.d + 8,), 3.0, dtype=torch.bfloat16, device="cuda")
+    dx = buf[4:4 + c.m * c.d].view(c.m, c.d)
+    c.backward(need_dw=False, dx=dx)
+    assert torch.equal(dx, want)
+    assert bool((buf[:4] == 3.0).all()) and bool((buf[4 + c.m * c.d:] == 3.0).all())
