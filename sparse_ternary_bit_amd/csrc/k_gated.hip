@@ -14,9 +14,11 @@
 // of 256) halve the decode per matrix product: 0.5 LDS reads and 2.2 VALU
 // instructions an MFMA (itself counted) against 0.75 and 2.9.
 //
-// Operands are swapped against the plain kernel (tokens are the product's
-// rows, weight rows its columns), so that a lane's sums belong to one weight
-// row a tile and a block's scale is four registers and not sixteen.
+// Weights are the products' rows where a pass is of up to 128 tokens: 1 to 2 %
+// less time than as their columns (the card's power: a pattern has three
+// values).  In longer ones they are the columns, so that a lane's sums share a
+// weight row and a block's factors take four registers: sixteen do not fit
+// beside 160 sums (spilled, 690 us become 930 for 2048 rows of 8 experts).
 //
 // Per block of 256 weights four stages of 64 activations; a stage's tokens
 // stream into one of two LDS buffers while the other is multiplied. The
@@ -54,6 +56,7 @@ namespace {
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kWaves = 4;
@@ -90,8 +93,8 @@ struct Smem {
   // lanes 0,1 of each code as bf16, then lanes 2,3; at byte 0, so that a code
   // times 4 is its address
   uint32_t lut[2 * kCodes];
-  float ratio[kWaves][kTileRows];  // of each row's sums, into the next block's units
-  float scale[kWaves][kTileRows];  // what they are in units of
+  alignas(16) float ratio[kWaves][kTileRows];  // of each row's sums, into the next block's units
+  alignas(16) float scale[kWaves][kTileRows];  // what they are in units of
   alignas(16) char x[2][kTiles * 16 * kStageRow];
   // code records, one word for a row and two k-steps: [k-step pair][quarter of
   // a k-step][row of its tile][tile], so a lane's four tiles are one read
@@ -238,6 +241,25 @@ __device__ __forceinline__ void run_pass(const GatedArgs& a, Smem& sh, const uin
     }
   };
 
+  // Weights as the products' rows (a lane's four sums are four weight rows of a
+  // token) or as their columns (four tokens of one weight row)
+  constexpr bool kRowsFirst = NT <= 8;
+  auto multiply = [](const bf16x8_t& w, const bf16x8_t& x, const f32x4_t& c) {
+    return kRowsFirst ? __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, x, c, 0, 0, 0)
+                      : __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w, c, 0, 0, 0);
+  };
+  // the factors, one a weight row, of a lane's sums of row tile i
+  using Factors = std::conditional_t<kRowsFirst, f32x4_t, float>;
+  auto factors = [](const float* row, int lane, int i) {
+    return *reinterpret_cast<const Factors*>(row + 16 * i + (kRowsFirst ? 4 * (lane >> 4) : lane & 15));
+  };
+  auto scale_by = [](f32x4_t& c, const Factors& f) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (kRowsFirst) c[j] *= f[j];
+      else c[j] *= f;
+    }
+  };
   f32x4_t acc[4][NT];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -278,10 +300,10 @@ __device__ __forceinline__ void run_pass(const GatedArgs& a, Smem& sh, const uin
     B[p] = *reinterpret_cast<const bf16x8_t*>(sh.x[0] + xb[p / NT] + (p % NT) * 16 * kStageRow);
 
   for (int b = 0; b < a.nb; ++b) {
-    float up[4];
-    const int rr = lane_now() & 15;
+    Factors up[4];
+    const int ln = lane_now();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) up[i] = sh.ratio[wave][16 * i + rr];
+    for (int i = 0; i < 4; ++i) up[i] = factors(sh.ratio[wave], ln, i);
 #pragma unroll
     for (int qt = 0; qt < 4; ++qt) {
       if (qt == 3 && !kSpread) {
@@ -313,13 +335,11 @@ __device__ __forceinline__ void run_pass(const GatedArgs& a, Smem& sh, const uin
           if (qt == 0 && ks == 0) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) acc[i][t][j] *= up[i];
+              scale_by(acc[i][t], up[i]);
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(B[g & 3], __builtin_bit_cast(bf16x8_t, A[ks][i]),
-                                                                acc[i][t], 0, 0, 0);
+            acc[i][t] = multiply(__builtin_bit_cast(bf16x8_t, A[ks][i]), B[g & 3], acc[i][t]);
           __builtin_amdgcn_sched_barrier(0);
         }
         if (ks == 1) R = Rn;
@@ -330,15 +350,13 @@ __device__ __forceinline__ void run_pass(const GatedArgs& a, Smem& sh, const uin
   // everyone is done with the stages: the outputs go through LDS as whole rows
   const int tid = wave * 64 + lane_now(), q1 = (tid >> 4) & 3, r1 = tid & 15;
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  float dl[4];
+  Factors last[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) dl[i] = sh.scale[wave][16 * i + r1];
+  for (int i = 0; i < 4; ++i) last[i] = factors(sh.scale[wave], tid & 63, i);
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][t][j] *= dl[i];
+    for (int i = 0; i < 4; ++i) scale_by(acc[i][t], last[i]);
   constexpr int kRowB = kCols * 2 + 16;
   static_assert(offsetof(Smem, x) + kTiles * 16 * kRowB <= sizeof(Smem), "the outputs fit");
   char* const tile = reinterpret_cast<char*>(&sh) + offsetof(Smem, x);
@@ -346,11 +364,18 @@ __device__ __forceinline__ void run_pass(const GatedArgs& a, Smem& sh, const uin
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 2; ++i) {
+        if constexpr (kRowsFirst) {
+          *reinterpret_cast<u32x2_t*>(tile + (16 * t + r1) * kRowB + (wave * 32 + 16 * i + 4 * q1) * 2) =
+              u32x2_t{bf16_bits(value(t, i, 0)) | static_cast<uint32_t>(bf16_bits(value(t, i, 1))) << 16,
+                      bf16_bits(value(t, i, 2)) | static_cast<uint32_t>(bf16_bits(value(t, i, 3))) << 16};
+        } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<uint16_t*>(tile + (16 * t + 4 * q1 + j) * kRowB + (wave * 32 + 16 * i + r1) * 2) =
-              bf16_bits(value(t, i, j));
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint16_t*>(tile + (16 * t + 4 * q1 + j) * kRowB + (wave * 32 + 16 * i + r1) * 2) =
+                bf16_bits(value(t, i, j));
+        }
+      }
     __syncthreads();
     for (int tok = tid >> 4; tok < mt; tok += kThreads / 16)
       *reinterpret_cast<u32x4_t*>(out + (row0 + tok) * ld + slab * kCols + 8 * (tid & 15)) =
