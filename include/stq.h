@@ -361,10 +361,12 @@ stq_status stq_grouped_swiglu_workspace(int64_t n_experts, int64_t d_model, int6
  *   workspace, workspace_bytes   at least what
  *             stq_grouped_swiglu_backward_workspace reports
  * dz is formed in fp32 and rounded for each product: for dx to fp16 (after a
- * power-of-two scaling of each row), and once more times the block scales, so
- * that the weights' patterns enter exactly; for dw to bf16.  Sums are fp32 in
- * a fixed order; dx and dw are rounded from them once.  total_m is at most
- * 2^23. */
+ * power-of-two scaling of each row) and, times a row of W's block scale, to
+ * fp16 once more, so that the weights' patterns enter exactly; for dw to bf16.
+ * fp16 keeps 11 bits down to 2^-28 of a row's largest |dz| (the product: of
+ * that times twice the largest |d| in the 256-column block of W); what is
+ * smaller errs by at most 2^-39 of it.  Sums are fp32 in a fixed order; dx and
+ * dw are rounded from them once.  total_m is at most 2^23. */
 stq_status stq_grouped_swiglu_backward(const uint8_t* w_gate_up, int64_t gate_up_stride_bytes, int64_t n_experts,
                                        int64_t d_model, int64_t d_ff, const uint16_t* x_sorted,
                                        const int32_t* expert_offsets, int64_t total_m, const uint16_t* gate_up,

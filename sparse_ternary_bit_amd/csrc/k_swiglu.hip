@@ -9,10 +9,14 @@
 //
 // dz_kernel forms dz once per row in fp32.  The product with W takes it as
 // fp16, each row scaled by a power of two that puts its largest magnitude in
-// [2^14, 2^15), and folds the block scales d (fp16 numbers) into it: the
-// weights' patterns enter the fp16 matrix cores exactly, and dz is rounded to
-// 11 bits twice (itself, and times d) ahead of the fp32 sums.  A bf16 operand
-// would round to 8.  The product with x takes dz as bf16, x's own type.
+// [2^14, 2^15), and folds the block scales into it, as d / D with D above every
+// |d|: the weights' patterns enter the fp16 matrix cores exactly, and dz is
+// rounded to 11 bits twice (itself, and its product with d / D) ahead of the
+// fp32 sums.  Both keep their digits down to 2^-28 of the row's largest dz
+// (times D); below, fp16's subnormal step leaves 2^-39 of it.  A bf16 operand
+// would round to 8 bits everywhere.  The product with x takes dz as bf16, x's
+// own type: fp16 has not the range for x, and dz as the sum of two bf16 numbers
+// would double the products.
 #include "stq_device.hpp"
 #include "stq_launch.hpp"
 #include "stq_passes.hpp"
@@ -155,9 +159,13 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
 //    holds.
 //  * Scales: d varies along the sum, so it goes into dz: a thread loads 8
 //    columns of a token, multiplies them by the 8 rows' d / D (packed fp16) and
-//    writes them to LDS.  D is a power of two at or above every |d| met so far,
-//    so nothing leaves fp16's range; where a tile raises it the sums are scaled
-//    down once.
+//    writes them to LDS.  D is a power of two above every |d| met so far, so
+//    nothing leaves fp16's range; where a tile raises it the sums are scaled
+//    down once.  d / D is exact unless it is a subnormal fp16 number, which
+//    takes scales of 1 and more beside others 2^13 times smaller.  A pass that
+//    meets such a pair starts over with the products formed in fp32 and rounded
+//    once.  (Calls of the case below: 1210 us with all products in fp32, 1110
+//    with packed ones and the watch for such pairs, 1097 without the watch.)
 //
 // All of it runs ahead of the matrix cores: while they multiply one 32-row
 // step, the next step's table reads are in flight, and the next tile's codes
@@ -213,8 +221,11 @@ __device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
   return __builtin_amdgcn_readlane(v, 63);
 }
 
-template <int NT>
-__device__ __forceinline__ void dx_pass(const DxArgs& a, DxSmem& sh, const uint8_t* wexp, int b, int64_t row0, int mt) {
+// kFar: products with d / D formed in fp32.  Without it the pass stops, the
+// same in every wavefront, and returns true where a d lies so far below D that
+// their fp16 quotient would lose digits.
+template <int NT, bool kFar>
+__device__ __forceinline__ bool dx_pass(const DxArgs& a, DxSmem& sh, const uint8_t* wexp, int b, int64_t row0, int mt) {
   // through an opaque move: what derives from the thread index is then computed
   // in each instantiation instead of being hoisted ahead of their choice, where
   // it would cost registers
@@ -284,19 +295,29 @@ __device__ __forceinline__ void dx_pass(const DxArgs& a, DxSmem& sh, const uint8
   // D = 2^expo with 2^expo > every |d| so far; below 2^-15 there is nothing to
   // gain (1 / D has to be an fp16 number)
   int expo = -15;
+  uint64_t far = 0;  // rows whose d / D is not a normal fp16 number (nor d itself, where D <= 1 loses nothing)
   auto raise = [&](uint16_t d, int e) {
     const uint32_t mag = d & 0x7FFFu;
-    if (__ballot(mag >= static_cast<uint32_t>(e + 15) << 10) == 0) return e;  // every |d| < 2^e
-    return max(e, static_cast<int>(wave_umax(mag) >> 10) - 14);
+    if (__ballot(mag >= static_cast<uint32_t>(e + 15) << 10) != 0)  // not every |d| < 2^e
+      e = max(e, static_cast<int>(wave_umax(mag) >> 10) - 14);
+    if constexpr (!kFar) far |= __ballot(mag - 1 < (e > 0 ? static_cast<uint32_t>(e + 1) << 10 : 1u) - 1);  // 0 < |d| < 2^(e-14)
+    return e;
   };
   auto read_scales = [&](int slot) { return *reinterpret_cast<const u32x4_t*>(&sh.d[slot][wave][8 * (lane & 7)]); };
   auto put_z = [&](const Z& z, const u32x4_t& dw, int buf, int e) {
     const _Float16 f = __builtin_bit_cast(_Float16, static_cast<uint16_t>(e <= 14 ? (15 - e) << 10 : 0x0400 >> (e - 14)));  // 2^-e
+    const float f32 = __builtin_bit_cast(float, (127 - e) << 23);  // the same
     f16x2_t d[4];
+    float df[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t w = dw[i];
-      d[i] = __builtin_bit_cast(f16x2_t, w) * f;
+      if constexpr (kFar) {
+        df[2 * i] = half_bits_to_float(w) * f32;
+        df[2 * i + 1] = half_bits_to_float(w >> 16) * f32;
+      } else {
+        d[i] = __builtin_bit_cast(f16x2_t, w) * f;
+      }
     }
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
@@ -304,7 +325,9 @@ __device__ __forceinline__ void dx_pass(const DxArgs& a, DxSmem& sh, const uint8
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint32_t w = z.v[j][i];
-        o[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, w) * d[i]);
+        const f16x2_t v = __builtin_bit_cast(f16x2_t, w);
+        if constexpr (kFar) o[i] = f16_pair(static_cast<float>(v[0]) * df[2 * i], static_cast<float>(v[1]) * df[2 * i + 1]);
+        else o[i] = __builtin_bit_cast(uint32_t, v * d[i]);
       }
       *reinterpret_cast<u32x4_t*>(z_put + buf * (kStageTok * 128) + j * 32 * 128) = o;
     }
@@ -451,10 +474,11 @@ __device__ __forceinline__ void dx_pass(const DxArgs& a, DxSmem& sh, const uint8
     }
     if (t + 2 <= last) next = raise(d, next);
   };
-  for (int t = 0; t < last; t += 2) {  // an even number of tiles: the matrix has 512 rows or a multiple
+  for (int t = 0; t < last && far == 0; t += 2) {  // an even number of tiles: the matrix has 512 rows or a multiple
     tile(t, 0, z[kDepth - 1]);
     tile(t + 1, 1, z[0]);
   }
+  if (far != 0) return true;
   // dx[row0 + 16i + r, 256b + 64 wave + 16q + 4e + j]: 16 neighbouring columns
   const int64_t ld = static_cast<int64_t>(a.nb) * kQK;
   const float big = ldexpf(1.0f, expo);
@@ -469,6 +493,7 @@ __device__ __forceinline__ void dx_pass(const DxArgs& a, DxSmem& sh, const uint8
       out[e] = u32x2_t{bf16_pair(acc[0][i][e] * big * inv, acc[1][i][e] * big * inv),
                        bf16_pair(acc[2][i][e] * big * inv, acc[3][i][e] * big * inv)};
   }
+  return false;
 }
 
 // One workgroup per (pass of an expert's tokens, block), passes found on the
@@ -491,14 +516,20 @@ __global__ __launch_bounds__(kThreads, 2) void swiglu_dx_kernel(DxArgs a) {
   }
   __syncthreads();
   const uint8_t* wexp = a.w + static_cast<int64_t>(u.expert) * a.estride;
+  bool far;
   switch ((u.mt + 15) >> 4) {
-    case 1: dx_pass<1>(a, sh, wexp, b, u.row0, u.mt); break;
-    case 2: dx_pass<2>(a, sh, wexp, b, u.row0, u.mt); break;
-    case 3: dx_pass<3>(a, sh, wexp, b, u.row0, u.mt); break;
-    case 4: dx_pass<4>(a, sh, wexp, b, u.row0, u.mt); break;
-    case 5: dx_pass<5>(a, sh, wexp, b, u.row0, u.mt); break;
-    default: dx_pass<6>(a, sh, wexp, b, u.row0, u.mt); break;
+    case 1: far = dx_pass<1, false>(a, sh, wexp, b, u.row0, u.mt); break;
+    case 2: far = dx_pass<2, false>(a, sh, wexp, b, u.row0, u.mt); break;
+    case 3: far = dx_pass<3, false>(a, sh, wexp, b, u.row0, u.mt); break;
+    case 4: far = dx_pass<4, false>(a, sh, wexp, b, u.row0, u.mt); break;
+    case 5: far = dx_pass<5, false>(a, sh, wexp, b, u.row0, u.mt); break;
+    default: far = dx_pass<6, false>(a, sh, wexp, b, u.row0, u.mt); break;
   }
+  if (!far) return;
+  // what the pass had on its way to LDS has landed, for everyone
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  if (u.mt <= 32) dx_pass<2, true>(a, sh, wexp, b, u.row0, u.mt);
+  else dx_pass<6, true>(a, sh, wexp, b, u.row0, u.mt);
 }
 
 // ---------------------------------------------------------------------------

@@ -519,3 +519,43 @@ def test_gradient_of_x_eight_bytes_into_a_buffer(stq):
     c.backward(need_dw=False, dx=dx)
     assert torch.equal(dx, want)
     assert bool((buf[:4] == 3.0).all()) and bool((buf[4 + c.m * c.d:] == 3.0).all())
+
+
+@pytest.mark.parametrize("at, counts", [(0, [40, 0, 70, 100]), (1, [1, 16, 33]), (255, LOADS * 12), (511, [40, 0, 70, 100])])
+@pytest.mark.parametrize("steps, large", [(848, 17.0), (1000, 30.0), (26.5 * 2 ** 15, 3.0e4), (10.5 * 2 ** 15, 3.0e4),
+                                          (33000, 6.0e4), (40000, 6.0e4)])
+def test_gradient_of_x_beside_rows_of_a_large_scale(stq, steps, large, at, counts):
+    """Rows of W whose scales are small, `steps` of fp16's subnormal ones, beside rows with a large one
+    through which no gradient flows (dh is 0 there): what the small ones carry keeps its digits, however
+    far below the largest they lie, wherever that one stands.
+
+    Weights and dz are positive, so nothing cancels: an element errs by fp16's f for dz and once more for
+    its product with the scale, the accumulation (module docstring) and its own rounding, relative to
+    itself.  dz's lie within a factor of 6.2 of each other (dg up to 1.1 * 2e-3 * 2, du from 0.73e-3), so
+    scaled they are above 2^14 / 6.2 and their products with 2^-25 (33000 steps beside a D of 2^16) above
+    2^-13.7: normal fp16 numbers."""
+    d, f = 512, 256
+    c = Case(stq, counts, d, f, seed=int(steps) + at)
+    blocks = c.table.view(c.E, 2 * f // 64, d // QK, 64, BLOCK)
+    blocks[..., 2:34] &= 0x88                              # sign bits 0: three +d and a zero a group
+    scale = torch.full((2 * f,), steps * 2.0 ** -24)
+    scale[[at, at ^ f]] = large                            # a gate row and the up row of the same column
+    scale = scale.half().view(torch.uint8).view(1, 2 * f // 64, 1, 64, 2).cuda()
+    blocks[..., :2] = scale
+    g = torch.Generator().manual_seed(at)
+    c.gu = (1.0 + torch.rand(c.gu.shape, generator=g)).bfloat16().cuda()
+    c.dh = (1e-3 * (1.0 + torch.rand(c.dh.shape, generator=g))).bfloat16().cuda()
+    c.dh[:, at % f] = 0.0
+    dx, _ = c.backward(need_dw=False)
+    F = 2.0 ** -11
+    dz, err = c.dz_ref()
+    assert bool((dz >= 0).all())
+    for e, (lo, hi) in enumerate(zip(c.bounds, c.bounds[1:])):
+        if lo == hi:
+            continue
+        w = c.weights(e)
+        assert bool((w >= 0).all()) and w[at].max() == torch.tensor(large).half().item()
+        ref = dz[lo:hi] @ w
+        tol = ((err[lo:hi] @ w) * (1 + F) + (2 * F + F * F + 2 * U * (2 * f / 32 + 40)) * ref) * (1 + B) + B * ref
+        bad = ((dx[lo:hi].double() - ref).abs() - tol).amax()
+        assert bad <= 0, (e, (dx[lo:hi].double() / ref - 1).abs().max().item())
