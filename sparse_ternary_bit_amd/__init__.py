@@ -543,7 +543,7 @@ def _q8_stride(name: str, t: torch.Tensor) -> int:
     stride = _rows(name, t, torch.int8)
     n, k = t.shape
     kp = (k + 15) // 16 * 16
-    if n == 1:
+    if n <= 1:
         stride = kp
     if kp != k and n > 0 and t.storage_offset() + (n - 1) * stride + kp > t.untyped_storage().nbytes():
         raise ValueError(f"{name}'s last row must own its bytes up to the next multiple of 16")

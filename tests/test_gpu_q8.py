@@ -237,3 +237,18 @@ def test_binding_refusals(stq):
         stq.q8_matmul(q, s, q, s, out_dtype=torch.float16)
     with pytest.raises(ValueError, match="must be torch.float32"):
         stq.q8_quantize_rows(torch.zeros(2, 8, dtype=torch.float16, device="cuda"))
+
+
+@pytest.mark.parametrize("k", [77, 80, 1])
+def test_nothing_to_multiply(stq, k):
+    """No tokens or no channels, from the quantizer to the product, whatever k."""
+    some, none = _rand((5, k), 41).cuda(), torch.empty((0, k), device="cuda")
+    for a, w in ((none, some), (some, none), (none, none)):
+        qa, sa = stq.q8_quantize_rows(a)
+        qw, sw = stq.q8_quantize_rows(w)
+        y = stq.q8_matmul(qa, sa, qw, sw)
+        assert y.shape == (a.shape[0], w.shape[0])
+        out = torch.empty(y.shape, device="cuda")
+        assert stq.q8_matmul(qa, sa, qw, sw, out=out) is out
+    q, s = stq.q8_quantize_rows(none, out=torch.empty((0, k), dtype=torch.int8, device="cuda"))
+    assert q.shape == (0, k) and s.shape == (0,)
