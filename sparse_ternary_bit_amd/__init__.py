@@ -576,9 +576,9 @@ def q8_quantize_rows(x: torch.Tensor, out: torch.Tensor | None = None, scale: to
 
 
 def q8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
-              out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+              out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None) -> torch.Tensor:
     """y[i, j] = (a[i] . w[j]) a_scale[i] w_scale[j] for int8 rows a [m, k] and w [n, k], the sum exact;
-    y is bf16 or fp32 [m, n]."""
+    y is bf16 or fp32 [m, n]: `out`'s type, or out_dtype (bf16 when neither is given)."""
     dev = _one_gpu(a, a_scale, w, w_scale, out)
     lda, ldw = _q8_stride("a", a), _q8_stride("w", w)
     m, k = a.shape
@@ -588,6 +588,8 @@ def q8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: 
     _vector("a_scale", a_scale, torch.float32, m)
     _vector("w_scale", w_scale, torch.float32, n)
     if out is None:
+        if out_dtype is None:
+            out_dtype = torch.bfloat16
         if out_dtype not in (torch.bfloat16, torch.float32):
             raise ValueError("out_dtype must be bfloat16 or float32")
         out = torch.empty((m, n), dtype=out_dtype, device=dev)
@@ -595,6 +597,8 @@ def q8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: 
     else:
         if tuple(out.shape) != (m, n):
             raise ValueError("out must be [m, n]")
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError(f"out must be {out_dtype} like out_dtype, got {out.dtype}")
         ldy = _rows("out", out, torch.bfloat16, torch.float32)
     _call(dev, "stq_q8_matmul", a.data_ptr(), lda, a_scale.data_ptr(), w.data_ptr(), ldw, w_scale.data_ptr(), m, n, k,
           out.data_ptr(), X_BF16 if out.dtype == torch.bfloat16 else X_F32, ldy)

@@ -252,3 +252,16 @@ def test_nothing_to_multiply(stq, k):
         assert stq.q8_matmul(qa, sa, qw, sw, out=out) is out
     q, s = stq.q8_quantize_rows(none, out=torch.empty((0, k), dtype=torch.int8, device="cuda"))
     assert q.shape == (0, k) and s.shape == (0,)
+
+
+def test_out_of_another_type_than_out_dtype_is_refused(stq):
+    q, s = stq.q8_quantize_rows(_rand((3, 32), 51).cuda())
+    y = torch.full((3, 3), 7.0, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError, match="out must be torch.float32"):
+        stq.q8_matmul(q, s, q, s, out=y, out_dtype=torch.float32)
+    assert bool((y == 7.0).all())
+    want = stq.q8_matmul(q, s, q, s)
+    assert want.dtype == torch.bfloat16
+    assert torch.equal(stq.q8_matmul(q, s, q, s, out=y, out_dtype=torch.bfloat16), want)
+    full = torch.empty((3, 3), device="cuda")
+    assert torch.equal(stq.q8_matmul(q, s, q, s, out=full).bfloat16(), want)   # out alone says its type
