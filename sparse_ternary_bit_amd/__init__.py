@@ -438,18 +438,15 @@ def _matrix(name: str, t: torch.Tensor, dtype: torch.dtype, rows: int, cols: int
         raise ValueError(f"{name} must be contiguous [{rows}, {cols}], got {tuple(t.shape)}")
 
 
-def _swiglu_args(w_gate_up, expert_stride, n_experts, d_model, d_ff, x_sorted, offsets) -> int:
-    """Checks shared by the gated feed-forward and its gradients; returns the number of rows."""
-    if w_gate_up.dtype != torch.uint8 or not w_gate_up.is_contiguous():
+def _swiglu_args(w_gate_up, expert_stride, n_experts, d_model, d_ff, x_sorted, offsets, total_m: int) -> None:
+    """Checks shared by the gated feed-forward and its gradients, which may have no table or no rows."""
+    if w_gate_up is not None and (w_gate_up.dtype != torch.uint8 or not w_gate_up.is_contiguous()):
         raise ValueError("w_gate_up must be contiguous torch.uint8")
     _vector("offsets", offsets, torch.int32, int(n_experts) + 1)
-    if x_sorted.dim() != 2:
-        raise ValueError("x_sorted must be [total_m, d_model]")
-    total_m = x_sorted.shape[0]
-    _matrix("x_sorted", x_sorted, torch.bfloat16, total_m, int(d_model))
-    if total_m > 0:
+    if x_sorted is not None:
+        _matrix("x_sorted", x_sorted, torch.bfloat16, total_m, int(d_model))
+    if w_gate_up is not None and total_m > 0:
         _table("w_gate_up", w_gate_up, n_experts, expert_stride, 2 * int(d_ff), d_model)
-    return total_m
 
 
 def grouped_swiglu_workspace(n_experts: int, d_model: int, d_ff: int, total_m: int, n_cus: int = 0) -> int:
@@ -476,7 +473,10 @@ def grouped_swiglu(w_gate_up: torch.Tensor, expert_stride: int, n_experts: int, 
     `workspace` (GPU bytes, at least grouped_swiglu_workspace(...)) is allocated here when not given."""
     dev = _one_gpu(w_gate_up, x_sorted, offsets, out, gate_up, workspace)
     E, d, f = int(n_experts), int(d_model), int(d_ff)
-    total_m = _swiglu_args(w_gate_up, expert_stride, E, d, f, x_sorted, offsets)
+    if x_sorted.dim() != 2:
+        raise ValueError("x_sorted must be [total_m, d_model]")
+    total_m = x_sorted.shape[0]
+    _swiglu_args(w_gate_up, expert_stride, E, d, f, x_sorted, offsets, total_m)
     if out is None:
         out = torch.empty((total_m, f), dtype=torch.bfloat16, device=dev)
     else:
@@ -504,19 +504,27 @@ def grouped_swiglu_backward_workspace(n_experts: int, d_model: int, d_ff: int, t
     return wb.value
 
 
-def grouped_swiglu_backward(w_gate_up: torch.Tensor, expert_stride: int, n_experts: int, d_model: int, d_ff: int,
-                            x_sorted: torch.Tensor, offsets: torch.Tensor, gate_up: torch.Tensor, dh: torch.Tensor,
+def grouped_swiglu_backward(w_gate_up: torch.Tensor | None, expert_stride: int, n_experts: int, d_model: int,
+                            d_ff: int, x_sorted: torch.Tensor | None, offsets: torch.Tensor, gate_up: torch.Tensor,
+                            dh: torch.Tensor,
                             need_dx: bool = True, need_dw: bool = True, dx: torch.Tensor | None = None,
                             dw: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
     """(dx, dw) of grouped_swiglu for the gradient dh bf16 [total_m, d_ff] at h and the gate_up it saved:
     dx bf16 [total_m, d_model] through the decoded weights, dw bf16 [n_experts, 2*d_ff, d_model] the
-    gradient of the decoded weights; None for the one not needed.  `workspace` (GPU bytes, at least
+    gradient of the decoded weights; None for the one not needed.  dx reads no x_sorted and dw no
+    w_gate_up, which may be None where only the other is needed.  `workspace` (GPU bytes, at least
     grouped_swiglu_backward_workspace(...)) is allocated here when not given."""
-    dev = _one_gpu(w_gate_up, x_sorted, offsets, gate_up, dh, dx, dw,
-                    workspace)
+    dev = _one_gpu(gate_up, w_gate_up, x_sorted, offsets, dh, dx, dw, workspace)
     E, d, f = int(n_experts), int(d_model), int(d_ff)
-    total_m = _swiglu_args(w_gate_up, expert_stride, E, d, f, x_sorted, offsets)
+    if need_dx and w_gate_up is None:
+        raise ValueError("dx needs w_gate_up")
+    if need_dw and x_sorted is None:
+        raise ValueError("dw needs x_sorted")
+    if gate_up.dim() != 2:
+        raise ValueError("gate_up must be [total_m, 2 * d_ff]")
+    total_m = gate_up.shape[0]
     _matrix("gate_up", gate_up, torch.bfloat16, total_m, 2 * f)
+    _swiglu_args(w_gate_up, expert_stride, E, d, f, x_sorted, offsets, total_m)
     _matrix("dh", dh, torch.bfloat16, total_m, f)
     if need_dx:
         dx = torch.empty((total_m, d), dtype=torch.bfloat16, device=dev) if dx is None else dx
@@ -533,7 +541,7 @@ def grouped_swiglu_backward(w_gate_up: torch.Tensor, expert_stride: int, n_exper
         workspace = _workspace(None, grouped_swiglu_backward_workspace(E, d, f, total_m, need_dx, need_dw), dev)
     else:
         workspace = _workspace(workspace, 0, dev)
-    _call(dev, "stq_grouped_swiglu_backward", w_gate_up.data_ptr(), int(expert_stride), E, d, f, x_sorted.data_ptr(),
+    _call(dev, "stq_grouped_swiglu_backward", _ptr(w_gate_up), int(expert_stride), E, d, f, _ptr(x_sorted),
           offsets.data_ptr(), total_m, gate_up.data_ptr(), dh.data_ptr(), _ptr(dx), _ptr(dw), *_ws_args(workspace))
     return dx, dw
 

@@ -559,3 +559,22 @@ def test_gradient_of_x_beside_rows_of_a_large_scale(stq, steps, large, at, count
         tol = ((err[lo:hi] @ w) * (1 + F) + (2 * F + F * F + 2 * U * (2 * f / 32 + 40)) * ref) * (1 + B) + B * ref
         bad = ((dx[lo:hi].double() - ref).abs() - tol).amax()
         assert bad <= 0, (e, (dx[lo:hi].double() / ref - 1).abs().max().item())
+
+
+def test_gradients_without_the_operand_of_the_other(stq):
+    """dx reads no x and dw no weights: the one not wanted needs none."""
+    c = Case(stq, [40, 0, 33], 512, 256, seed=41, tail=3)
+    dx, dw = c.backward()
+    dims = c.E, c.d, c.f
+    only_x, none = stq.grouped_swiglu_backward(c.table, c.stride, *dims, None, c.offsets, c.gu, c.dh, need_dw=False)
+    assert none is None and torch.equal(only_x[:73], dx[:73])
+    none, only_w = stq.grouped_swiglu_backward(None, 0, *dims, c.x, c.offsets, c.gu, c.dh, need_dx=False)
+    assert none is None and torch.equal(only_w, dw)
+    with pytest.raises(ValueError, match="dx needs w_gate_up"):
+        stq.grouped_swiglu_backward(None, 0, *dims, c.x, c.offsets, c.gu, c.dh)
+    with pytest.raises(ValueError, match="dw needs x_sorted"):
+        stq.grouped_swiglu_backward(c.table, c.stride, *dims, None, c.offsets, c.gu, c.dh)
+    with pytest.raises(ValueError, match="x_sorted must be"):
+        stq.grouped_swiglu_backward(c.table, c.stride, *dims, c.x[:-1], c.offsets, c.gu, c.dh)
+    with pytest.raises(ValueError, match="gate_up must be"):
+        stq.grouped_swiglu_backward(c.table, c.stride, *dims, c.x, c.offsets, c.gu[0], c.dh)
