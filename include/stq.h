@@ -459,7 +459,8 @@ stq_status stq_token_logprobs_workspace(int x_dtype, int64_t n_rows, int64_t voc
  *                  elements apart; may be the logits themselves (same pointer
  *                  and stride), else it may not overlap them
  * A target outside [0, vocab) takes no grad_logprob; a row with lse = -inf
- * gives zeros, one with lse = NaN gives NaN.  At most 2^22 rows. */
+ * gives zeros, one with lse = NaN gives NaN.  At most 2^22 rows, and less than
+ * 2^24 started pieces of 32 KB of a row in all (logits of more than 400 GB). */
 stq_status stq_token_logprobs_backward(const void* logits, int x_dtype, int64_t row_stride, int64_t n_rows,
                                        int64_t vocab, const int32_t* targets, const float* lse, const float* entropy,
                                        const float* grad_logprob, const float* grad_entropy, void* d_logits,

@@ -649,19 +649,21 @@ hipError_t launch_logprobs(const LogprobsArgs& g, const LogprobsPlan& plan, void
 }
 
 namespace {
-int64_t bwd_parts(int64_t vocab, int elem_bytes, int chunks_per_thread) {
-  const int64_t chunks = (vocab * elem_bytes + 15) / 16 + 1;
+int64_t bwd_parts(const LogprobsBwdArgs& g, int chunks_per_thread) {
+  const int64_t esz = g.bf16 ? 2 : 4, per = 16 / esz;
+  const bool alike = g.rows == 1 || g.stride * esz % 16 == 0;  // every row starts in its chunk where the first does
+  const int64_t skew = alike ? (reinterpret_cast<uintptr_t>(g.logits) & 15) / esz : per - 1;
+  const int64_t chunks = (g.vocab + skew + per - 1) / per;
   return (chunks + kBwdThreads * chunks_per_thread - 1) / (kBwdThreads * chunks_per_thread);
 }
 }  // namespace
 
-int64_t logprobs_bwd_parts(int64_t vocab, int elem_bytes) { return bwd_parts(vocab, elem_bytes, kBwdChunks); }
+int64_t logprobs_bwd_parts(const LogprobsBwdArgs& g) { return bwd_parts(g, kBwdChunks); }
 
 hipError_t launch_logprobs_bwd(const LogprobsBwdArgs& g, hipStream_t s) {
   const BArgs a{g.logits, g.stride, g.rows, g.vocab, g.targets, g.lse, g.entropy, g.g_lp, g.g_ent, g.out, g.out_stride};
-  const int esz = g.bf16 ? 2 : 4;
-  const bool small = g.rows * bwd_parts(g.vocab, esz, kBwdChunks) < 2 * cus_of_stream(s);
-  const int64_t parts = bwd_parts(g.vocab, esz, small ? kBwdChunksSmall : kBwdChunks);
+  const bool small = g.rows * bwd_parts(g, kBwdChunks) < 2 * cus_of_stream(s);
+  const int64_t parts = bwd_parts(g, small ? kBwdChunksSmall : kBwdChunks);
   const dim3 grid(static_cast<unsigned>(g.rows * parts));
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(kBwdThreads), 0, s, a, static_cast<int>(parts)); };
   if (g.bf16) small ? go(logprobs_bwd_kernel<uint16_t, kBwdChunksSmall>) : go(logprobs_bwd_kernel<uint16_t, kBwdChunks>);

@@ -654,13 +654,14 @@ stq_status stq_token_logprobs_backward(const void* logits, int x_dtype, int64_t 
   if (!fits(n_rows, row_stride, esz) || !fits(n_rows, d_row_stride, esz)) return fail(STQ_E_SHAPE, "%s: row stride too large", who);
   if (logits == d_logits && n_rows > 1 && row_stride != d_row_stride)
     return fail(STQ_E_ARG, "%s: in place needs equal row strides", who);
-  if (n_rows * stq::logprobs_bwd_parts(vocab, esz) > (int64_t{1} << 23))
+  const stq::LogprobsBwdArgs a{logits, x_dtype == STQ_X_BF16 ? 1 : 0, row_stride, n_rows, vocab, targets, lse, entropy,
+                               grad_logprob, grad_entropy, d_logits, d_row_stride};
+  // a launch has less than 2^32 threads
+  if (n_rows * stq::logprobs_bwd_parts(a) >= (int64_t{1} << 24))
     return fail(STQ_E_SHAPE, "%s: too many rows of this vocabulary for one call", who);
   if (!aligned(logits, esz) || !aligned(d_logits, esz)) return fail(STQ_E_ALIGN, "%s: logits or d_logits not aligned to their elements", who);
   if (!aligned(targets, 4) || !aligned(lse, 4) || !aligned(entropy, 4) || !aligned(grad_logprob, 4) || !aligned(grad_entropy, 4))
     return fail(STQ_E_ALIGN, "%s: targets, lse, entropy or gradients not 4-byte aligned", who);
-  const stq::LogprobsBwdArgs a{logits, x_dtype == STQ_X_BF16 ? 1 : 0, row_stride, n_rows, vocab, targets, lse, entropy,
-                               grad_logprob, grad_entropy, d_logits, d_row_stride};
   hipError_t e = stq::launch_logprobs_bwd(a, reinterpret_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, "stq_token_logprobs_backward launch");
   return ok();

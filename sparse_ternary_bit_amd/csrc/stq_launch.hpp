@@ -214,7 +214,7 @@ struct LogprobsBwdArgs {
   void* out;
   int64_t out_stride;
 };
-int64_t logprobs_bwd_parts(int64_t vocab, int elem_bytes);  // workgroups per row
+int64_t logprobs_bwd_parts(const LogprobsBwdArgs& a);  // workgroups per row, at most
 hipError_t launch_logprobs_bwd(const LogprobsBwdArgs& a, hipStream_t s);
 
 // Streaming-read reference (measurement only): reads `bytes` bytes of `buf`

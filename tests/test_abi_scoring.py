@@ -237,3 +237,14 @@ def test_binding_refuses_cpu_tensors_and_wrong_shapes():
     q = torch.zeros(2, 32, dtype=torch.int8)
     with pytest.raises(ValueError, match="GPU"):
         stq.q8_matmul(q, x[:, 0], q, x[:, 0])
+
+
+def test_logprobs_backward_takes_what_a_gpu_can_hold(L):
+    """The joint limit on rows and vocabulary lies above any GPU's memory; calls below it get as far as
+    the alignment check."""
+    odd = dict(t=FAKE + 2)
+    for n, v, xd in ((1 << 20, 131072, 1), (1 << 22, 32768, 1), (1 << 22, 40000, 1), (1 << 21, 50021, 0), (4, 1 << 30, 1)):
+        assert _bw(L, n=n, v=v, xs=v + 8, ds=v + 8, xd=xd, **odd) == 3, (n, v)
+        assert _bw(L, n=n, v=v, xs=v + 1, ds=v + 1, xd=xd, **odd) == 3, (n, v)   # rows that start inside 16 bytes
+    assert _bw(L, n=1 << 22, v=65536, xs=65536, ds=65536, **odd) == 2             # 550 GB
+    assert "too many rows" in _err(L)

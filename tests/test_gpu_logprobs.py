@@ -363,3 +363,25 @@ def test_binding_refusals(stq):
         stq.token_logprobs_backward(x, t, f, None, f, f)
     with pytest.raises(ValueError, match="out must be"):
         stq.token_logprobs_backward(x, t, f, f, f, out=x[:1])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n", [1, 3, 1100])
+@pytest.mark.parametrize("more", [-1, 0, 1])
+def test_backward_of_rows_that_end_with_a_workgroups_piece(stq, dtype, n, more):
+    """Rows of a whole number of pieces (32 KB, 8 KB where rows are few), one entry less or more, starting on
+    16 bytes, inside them all alike, and each elsewhere."""
+    size = 2 if dtype == torch.bfloat16 else 4
+    v = (32768 if n > 500 else 8192) // size + more
+    x, t = _logits(n, v, dtype, 3), _targets(n, v, 2)
+    gen = torch.Generator().manual_seed(n)
+    g, ge = torch.randn(n, generator=gen), torch.randn(n, generator=gen)
+    per = 16 // size
+    for lead, row in ((0, -(-v // per) * per), (1, -(-(v + 1) // per) * per), (per - 1, -(-(v + per) // per) * per),
+                      (0, (v + per) // per * per + 1)):
+        buf = torch.full((n, row), 9.0, dtype=dtype, device="cuda")
+        dev = buf[:, lead:lead + v]
+        dev.copy_(x)
+        out = torch.full((n, row), 9.0, dtype=dtype, device="cuda")
+        _backward_check(stq, x, dev, t, g, ge, out[:, lead:lead + v])
+        assert bool((torch.cat([out[:, :lead], out[:, lead + v:]], 1) == 9.0).all())
