@@ -331,7 +331,10 @@ stq_status stq_greedy_allocation(const double* gain, const double* extra_bytes, 
  *   workspace, workspace_bytes   at least what stq_grouped_swiglu_workspace
  *                   reports for these shapes on this stream's device (may be
  *                   NULL when that is 0)
- * d_ff * row_bytes(d_model) is below 2^31, total_m at most 2^23.  Repeated
+ * d_ff * row_bytes(d_model) is below 2^31, d_model at most 2^22 and d_ff 2^21;
+ * n_experts is at most 65535, total_m 2^23, and with e = min(n_experts,
+ * total_m) their passes, (e + (total_m - e) / 32 + 8) * (d_ff / 128), at most
+ * 2^23 (an integer division); beyond: STQ_E_SHAPE.  Repeated
  * calls give identical bits; they depend on the form taken (and, through the
  * GEMV's plan, on the device), as stq_gemv's do. */
 stq_status stq_grouped_swiglu(const uint8_t* w_gate_up, int64_t gate_up_stride_bytes, int64_t n_experts,
@@ -366,7 +369,10 @@ stq_status stq_grouped_swiglu_workspace(int64_t n_experts, int64_t d_model, int6
  * fp16 keeps 11 bits down to 2^-28 of a row's largest |dz| (the product: of
  * that times twice the largest |d| in the 256-column block of W); what is
  * smaller errs by at most 2^-39 of it.  Sums are fp32 in a fixed order; dx and
- * dw are rounded from them once.  total_m is at most 2^23. */
+ * dw are rounded from them once.  The limits on a matrix, n_experts and total_m
+ * are the forward call's; beside them (e + (total_m - e) / 32 + 8) *
+ * (d_model / 256) is at most 2^23 where dx is wanted, and n_experts *
+ * (d_ff / 64) * (d_model / 128) where dw is. */
 stq_status stq_grouped_swiglu_backward(const uint8_t* w_gate_up, int64_t gate_up_stride_bytes, int64_t n_experts,
                                        int64_t d_model, int64_t d_ff, const uint16_t* x_sorted,
                                        const int32_t* expert_offsets, int64_t total_m, const uint16_t* gate_up,
@@ -409,7 +415,7 @@ stq_status stq_q8_quantize_rows(const void* x, int x_dtype, int64_t x_row_stride
  *                read and count for nothing
  *   y            [m, n] fp32 (STQ_X_F32) or bf16 (STQ_X_BF16, one rounding of
  *                the fp32 value), rows y_row_stride elements apart; rows that
- *                start on four elements store faster
+ *                all start on 16 bytes store faster
  * 1 <= k <= 131071 (any sum of products of bytes then fits 32 bits); m up to
  * 2^22, n up to 2^26, m * n up to 2^38.  Integer sums do not depend on their
  * order: a result's bits do not depend on m, n, the strides or the device. */

@@ -248,3 +248,46 @@ def test_logprobs_backward_takes_what_a_gpu_can_hold(L):
         assert _bw(L, n=n, v=v, xs=v + 1, ds=v + 1, xd=xd, **odd) == 3, (n, v)   # rows that start inside 16 bytes
     assert _bw(L, n=1 << 22, v=65536, xs=65536, ds=65536, **odd) == 2             # 550 GB
     assert "too many rows" in _err(L)
+
+
+def _units(ne, m):
+    e = min(ne, m)
+    return e + (m - e) // 32 + 8
+
+
+@pytest.mark.parametrize("ne, d, f", [(256, 4096, 16384), (1, 256, 65536), (65535, 256, 1024), (65535, 512, 32768)])
+def test_swiglu_limits_are_the_documented_ones(L, ne, d, f):
+    """The largest row count below the joint limit is taken as far as the alignment checks, the next
+    is not."""
+    stride = 2 * f * (d // 256) * 42
+    ok = [m for m in (1 << i for i in range(24)) if _units(ne, m) * (f // 128) <= 1 << 23]
+    assert _fw(L, ne=ne, d=d, f=f, st=stride, m=ok[-1], x=FAKE + 2) == 3
+    lo, hi = ok[-1], 1 << 23
+    if _units(ne, hi) * (f // 128) <= 1 << 23:
+        assert _fw(L, ne=ne, d=d, f=f, st=stride, m=hi + 1, x=FAKE + 2) == 2
+        return
+    while hi - lo > 1:
+        mid = (lo + hi) // 2
+        lo, hi = (mid, hi) if _units(ne, mid) * (f // 128) <= 1 << 23 else (lo, mid)
+    assert _fw(L, ne=ne, d=d, f=f, st=stride, m=lo, x=FAKE + 2) == 3
+    assert _fw(L, ne=ne, d=d, f=f, st=stride, m=hi, x=FAKE + 2) == 2
+    assert "too many rows" in _err(L)
+
+
+@pytest.mark.parametrize("ne, d, f", [(256, 65536, 256), (1, 1 << 17, 256), (65535, 8192, 256)])
+def test_swiglu_backward_limits_are_the_documented_ones(L, ne, d, f):
+    stride = 2 * f * (d // 256) * 42
+    lo, hi = 1, 1 << 23
+    assert _units(ne, lo) * (d // 256) <= 1 << 23 < _units(ne, hi) * (d // 256)
+    while hi - lo > 1:
+        mid = (lo + hi) // 2
+        lo, hi = (mid, hi) if _units(ne, mid) * (d // 256) <= 1 << 23 else (lo, mid)
+    args = dict(ne=ne, d=d, f=f, st=stride, dh=FAKE + 2)
+    assert _bwd(L, m=lo, dw=None, **args) == 3
+    assert _bwd(L, m=hi, dw=None, **args) == 2
+    ne = (1 << 23) // ((f // 64) * (d // 128))                 # dw's experts
+    args["ne"] = ne
+    assert _bwd(L, m=10, dx=None, **args) == 3
+    args["ne"] = ne + 1
+    assert _bwd(L, m=10, dx=None, **args) == 2
+    assert "weight gradients" in _err(L)
