@@ -348,6 +348,18 @@ stq_status stq_grouped_swiglu(const uint8_t* w_gate_up, int64_t gate_up_stride_b
 stq_status stq_grouped_swiglu_workspace(int64_t n_experts, int64_t d_model, int64_t d_ff, int64_t total_m,
                                         int32_t n_cus, int64_t* workspace_bytes);
 
+/* The form that stq_grouped_swiglu takes for these shapes on a device with
+ * n_cus compute units (0: the current device's): rows_per_pass is the most rows
+ * of an expert that a workgroup multiplies at a time, or 0 where the rows run
+ * through stq_gemv's kernels (and where there are none).  The choice is made
+ * for rows that spread evenly over the experts, since the offsets are on the
+ * device: a call whose rows go to few of its experts is right all the same,
+ * but may take several times as long as with n_experts (and the offsets) of
+ * those alone.  Host only, same checks and errors as the call.  rows_per_pass
+ * is a HOST pointer. */
+stq_status stq_grouped_swiglu_plan(int64_t n_experts, int64_t d_model, int64_t d_ff, int64_t total_m, int32_t n_cus,
+                                   int32_t* rows_per_pass);
+
 /* Its gradients: with s = 1 / (1 + exp(-g)) and dh the gradient at h,
  *     dg = dh u s (1 + g (1 - s)),   du = dh g s,   dz = [dg | du]
  *     dx[r] = dz_r W_e                 (through the decoded, frozen weights)
@@ -383,6 +395,10 @@ stq_status stq_grouped_swiglu_backward(const uint8_t* w_gate_up, int64_t gate_up
  * outputs wanted (0 or 1 each); host only.  workspace_bytes is a HOST pointer. */
 stq_status stq_grouped_swiglu_backward_workspace(int64_t n_experts, int64_t d_model, int64_t d_ff, int64_t total_m,
                                                  int want_dx, int want_dw, int64_t* workspace_bytes);
+
+/* The same of stq_grouped_swiglu_backward's dx, whose rows all go in passes. */
+stq_status stq_grouped_swiglu_backward_plan(int64_t n_experts, int64_t d_model, int64_t d_ff, int64_t total_m,
+                                            int32_t n_cus, int32_t* rows_per_pass);
 
 /* Rows of 8-bit integers with one fp32 scale each, the form in which a model
  * keeps what its allocation leaves above the ternary format (attention

@@ -18,8 +18,8 @@ __all__ = [
     "QK", "BLOCK_BYTES", "ENC_WLS", "ENC_AMAX", "StqError", "lib", "lib_path",
     "row_bytes", "quantize_rows", "dequantize_rows", "gemv", "gemv_noalloc", "gemv_plan", "grouped_gemm",
     "moe_ffn_decode",
-    "moe_ffn_workspace", "grouped_swiglu", "grouped_swiglu_workspace", "grouped_swiglu_backward",
-    "grouped_swiglu_backward_workspace",
+    "moe_ffn_workspace", "grouped_swiglu", "grouped_swiglu_workspace", "grouped_swiglu_plan",
+    "grouped_swiglu_backward", "grouped_swiglu_backward_workspace", "grouped_swiglu_backward_plan",
     "q8_quantize_rows", "q8_matmul", "token_logprobs",
     "token_logprobs_workspace", "token_logprobs_backward", "layer_errors", "layer_errors_workspace", "q2_roundtrip", "greedy_allocation",
     "stream_read_probe", "mfma_loop_probe", "lds_read_probe", "MFMA_PROBE_FLOP_PER_ROUND",
@@ -104,6 +104,9 @@ def lib() -> ctypes.CDLL:
     L.stq_grouped_swiglu.restype = _c_int
     L.stq_grouped_swiglu_workspace.argtypes = [_c_i64, _c_i64, _c_i64, _c_i64, ctypes.c_int32, ctypes.POINTER(_c_i64)]
     L.stq_grouped_swiglu_workspace.restype = _c_int
+    for plan in (L.stq_grouped_swiglu_plan, L.stq_grouped_swiglu_backward_plan):
+        plan.argtypes = [_c_i64, _c_i64, _c_i64, _c_i64, ctypes.c_int32, ctypes.POINTER(ctypes.c_int32)]
+        plan.restype = _c_int
     L.stq_grouped_swiglu_backward.argtypes = [_c_vp, _c_i64, _c_i64, _c_i64, _c_i64, _c_vp, _c_vp, _c_i64, _c_vp,
                                               _c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_vp]
     L.stq_grouped_swiglu_backward.restype = _c_int
@@ -459,6 +462,19 @@ def grouped_swiglu_workspace(n_experts: int, d_model: int, d_ff: int, total_m: i
     return wb.value
 
 
+def _pass_rows(func: str, n_experts: int, d_model: int, d_ff: int, total_m: int, n_cus: int) -> int:
+    rows = ctypes.c_int32()
+    _check(func, getattr(lib(), func)(int(n_experts), int(d_model), int(d_ff), int(total_m), int(n_cus),
+                                      ctypes.byref(rows)))
+    return rows.value
+
+
+def grouped_swiglu_plan(n_experts: int, d_model: int, d_ff: int, total_m: int, n_cus: int = 0) -> int:
+    """Rows per pass of an expert that grouped_swiglu takes for these shapes on n_cus compute units (0: the
+    current device's), 0 where the rows run through the GEMV's kernels; host only."""
+    return _pass_rows("stq_grouped_swiglu_plan", n_experts, d_model, d_ff, total_m, n_cus)
+
+
 @functools.lru_cache(maxsize=256)
 def _swiglu_need(n_experts: int, d_model: int, d_ff: int, total_m: int, n_cus: int, gemv_plan_override) -> int:
     return grouped_swiglu_workspace(n_experts, d_model, d_ff, total_m, n_cus)
@@ -502,6 +518,11 @@ def grouped_swiglu_backward_workspace(n_experts: int, d_model: int, d_ff: int, t
            lib().stq_grouped_swiglu_backward_workspace(int(n_experts), int(d_model), int(d_ff), int(total_m),
                                                        int(bool(need_dx)), int(bool(need_dw)), ctypes.byref(wb)))
     return wb.value
+
+
+def grouped_swiglu_backward_plan(n_experts: int, d_model: int, d_ff: int, total_m: int, n_cus: int = 0) -> int:
+    """Rows per pass of an expert that grouped_swiglu_backward's dx takes, as grouped_swiglu_plan."""
+    return _pass_rows("stq_grouped_swiglu_backward_plan", n_experts, d_model, d_ff, total_m, n_cus)
 
 
 def grouped_swiglu_backward(w_gate_up: torch.Tensor | None, expert_stride: int, n_experts: int, d_model: int,

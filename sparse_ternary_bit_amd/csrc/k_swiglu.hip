@@ -713,8 +713,6 @@ SwigluBwdLayout swiglu_bwd_layout(int64_t d_ff, int64_t total_m, bool dx, bool d
   return l;
 }
 
-namespace {
-
 // Rows of a pass: 96, or 32 where those would leave much of the chip idle.
 // Measured, us of the whole call without dW, 96 / 32: one expert of 2 x 1024
 // of 4096, 100 rows 33 / 28, 500 rows 41 / 30, 4000 rows 88 / 128; 2 x 2048 of
@@ -725,8 +723,6 @@ int dx_rows_a_pass(const SwigluBwdArgs& g, int cus) {
   auto step = [&](int max_tok) { return pass_step_us(kCost, g.total_m, g.n_experts, max_tok, g.d_model / kQK, cus); };
   return step(32) < 0.95 * step(kMaxTok) ? 32 : kMaxTok;
 }
-
-}  // namespace
 
 hipError_t launch_swiglu_bwd(const SwigluBwdArgs& g, void* ws, int cus, hipStream_t s) {
   const SwigluBwdLayout l = swiglu_bwd_layout(g.d_ff, g.total_m, g.dx != nullptr, g.dw != nullptr);

@@ -424,6 +424,21 @@ stq_status stq_grouped_swiglu_workspace(int64_t n_experts, int64_t d_model, int6
   return ok();
 }
 
+stq_status stq_grouped_swiglu_plan(int64_t n_experts, int64_t d_model, int64_t d_ff, int64_t total_m, int32_t n_cus,
+                                   int32_t* rows_per_pass) {
+  const char* who = "stq_grouped_swiglu_plan";
+  if (!rows_per_pass) return fail(STQ_E_ARG, "%s: null output pointer", who);
+  *rows_per_pass = 0;
+  if (n_cus < 0) return fail(STQ_E_ARG, "%s: n_cus < 0", who);
+  const stq_status st = swiglu_fwd_check(n_experts, d_model, d_ff, total_m, who);
+  if (st != STQ_OK) return st;
+  if (total_m == 0) return ok();
+  const stq::SwigluArgs a{nullptr, 2 * d_ff * stq_row_bytes(d_model), n_experts, d_model, d_ff, nullptr, nullptr, total_m,
+                          nullptr, nullptr};
+  *rows_per_pass = stq::plan_swiglu(a, n_cus > 0 ? n_cus : stq::cus_of_current_device()).max_tok;
+  return ok();
+}
+
 stq_status stq_grouped_swiglu(const uint8_t* w_gate_up, int64_t gate_up_stride_bytes, int64_t n_experts,
                               int64_t d_model, int64_t d_ff, const uint16_t* x_sorted, const int32_t* expert_offsets,
                               int64_t total_m, uint16_t* h, uint16_t* gate_up, void* workspace,
@@ -474,6 +489,21 @@ stq_status stq_grouped_swiglu_backward_workspace(int64_t n_experts, int64_t d_mo
   const stq_status st = swiglu_bwd_check(n_experts, d_model, d_ff, total_m, want_dx != 0, want_dw != 0, who);
   if (st != STQ_OK) return st;
   *workspace_bytes = stq::swiglu_bwd_layout(d_ff, total_m, want_dx != 0, want_dw != 0).bytes;
+  return ok();
+}
+
+stq_status stq_grouped_swiglu_backward_plan(int64_t n_experts, int64_t d_model, int64_t d_ff, int64_t total_m,
+                                            int32_t n_cus, int32_t* rows_per_pass) {
+  const char* who = "stq_grouped_swiglu_backward_plan";
+  if (!rows_per_pass) return fail(STQ_E_ARG, "%s: null output pointer", who);
+  *rows_per_pass = 0;
+  if (n_cus < 0) return fail(STQ_E_ARG, "%s: n_cus < 0", who);
+  const stq_status st = swiglu_bwd_check(n_experts, d_model, d_ff, total_m, true, false, who);
+  if (st != STQ_OK) return st;
+  if (total_m == 0) return ok();
+  const stq::SwigluBwdArgs a{nullptr, 2 * d_ff * stq_row_bytes(d_model), n_experts, d_model, d_ff, nullptr, nullptr, total_m,
+                             nullptr, nullptr, nullptr, nullptr};
+  *rows_per_pass = stq::dx_rows_a_pass(a, n_cus > 0 ? n_cus : stq::cus_of_current_device());
   return ok();
 }
 

@@ -140,6 +140,7 @@ struct SwigluBwdLayout {
   int64_t inv, dzb, bytes;
 };
 SwigluBwdLayout swiglu_bwd_layout(int64_t d_ff, int64_t total_m, bool dx, bool dw);
+int dx_rows_a_pass(const SwigluBwdArgs& a, int cus);
 hipError_t launch_swiglu_bwd(const SwigluBwdArgs& a, void* ws, int cus, hipStream_t s);
 
 // Layer error under calibration activations (full Hessian and diagonal);

@@ -291,3 +291,49 @@ def test_swiglu_backward_limits_are_the_documented_ones(L, ne, d, f):
     args["ne"] = ne + 1
     assert _bwd(L, m=10, dx=None, **args) == 2
     assert "weight gradients" in _err(L)
+
+
+def _cases(test):
+    return next(m for m in test.pytestmark if m.name == "parametrize").args[1]
+
+
+def test_swiglu_tests_reach_every_form():
+    """The form follows from estimates in the library: the GPU tests written for one of them still take it
+    on the 256 compute units of an MI355X."""
+    import sparse_ternary_bit_amd as stq
+    import test_gpu_swiglu as T
+
+    def fwd(counts, d, f, tail=0):
+        return stq.grouped_swiglu_plan(len(counts), d, f, sum(counts) + tail, 256)
+
+    def bwd(counts, d, f, tail=0):
+        return stq.grouped_swiglu_backward_plan(len(counts), d, f, sum(counts) + tail, 256)
+    assert {fwd(*c) for c in _cases(T.test_forward)} == {32}
+    assert {bwd(*c) for c in _cases(T.test_backward)} == {32, 96}
+    assert {fwd(*c) for c in _cases(T.test_few_rows_through_the_gemv)} == {0}
+    assert [fwd(*c[:3], 5) for c in _cases(T.test_long_passes)] == [80] + 5 * [160]
+    assert {fwd(*c[:3], 2) for c in _cases(T.test_passes_of_80)} == {80}
+    assert fwd([160] * 130, 768, 1024) == 160                                 # blocks of no scale
+    assert [bwd(*c[:3]) for c in _cases(T.test_long_passes_of_the_gradients)] == 5 * [96]
+    far = {bwd(c[1], 512, 256) for m in T.test_gradient_of_x_beside_rows_of_a_large_scale.pytestmark
+           if m.name == "parametrize" and m.args[0].startswith("at") for c in m.args[1]}
+    assert far == {32, 96}
+
+
+def test_swiglu_plan_refusals(L):
+    rows = ctypes.c_int32(-7)
+    for f in (L.stq_grouped_swiglu_plan, L.stq_grouped_swiglu_backward_plan):
+        assert f(4, 4096, 512, 0, 256, ctypes.byref(rows)) == 0 and rows.value == 0
+        assert f(256, 7168, 2048, 16384, 0, ctypes.byref(rows)) == 0 and rows.value > 32
+        assert f(4, 4096, 500, 10, 256, ctypes.byref(rows)) == 2
+        assert f(0, 4096, 512, 10, 256, ctypes.byref(rows)) == 1
+        assert f(4, 4096, 512, -1, 256, ctypes.byref(rows)) == 1
+        assert f(4, 4096, 512, 10, -1, ctypes.byref(rows)) == 1
+        assert f(4, 4096, 512, 10, 256, None) == 1
+        assert "_plan" in _err(L)
+    # the form that needs a workspace is the one that reports no passes
+    wb = ctypes.c_int64()
+    for m in (1, 10, 300, 2000, 20000):
+        assert L.stq_grouped_swiglu_plan(256, 7168, 2048, m, 256, ctypes.byref(rows)) == 0
+        assert L.stq_grouped_swiglu_workspace(256, 7168, 2048, m, 256, ctypes.byref(wb)) == 0
+        assert (wb.value > 0) == (rows.value == 0)

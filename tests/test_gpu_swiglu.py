@@ -578,3 +578,15 @@ def test_gradients_without_the_operand_of_the_other(stq):
         stq.grouped_swiglu_backward(c.table, c.stride, *dims, c.x[:-1], c.offsets, c.gu, c.dh)
     with pytest.raises(ValueError, match="gate_up must be"):
         stq.grouped_swiglu_backward(c.table, c.stride, *dims, c.x, c.offsets, c.gu[0], c.dh)
+
+
+@pytest.mark.parametrize("counts, d, f, odd", [(LOADS, 512, 512, False), (LOADS * 2, 768, 256, True), (LOADS * 3, 1280, 256, False)])
+def test_passes_of_80(stq, counts, d, f, odd):
+    """Every number of token tiles that passes of 80 have, cut from loads of up to 480 rows (tolerances as in
+    test_long_passes)."""
+    c = Case(stq, counts, d, f, seed=len(counts) + 9, tail=2, odd_scales=odd, slack=256)
+    assert stq.grouped_swiglu_plan(c.E, d, f, c.m) == 80
+    gu = torch.full((c.m, 2 * f), 3.0, dtype=torch.bfloat16, device="cuda")
+    h = c.forward(out=torch.full((c.m, f), 3.0, dtype=torch.bfloat16, device="cuda"), gate_up=gu)
+    c.check_forward(h, gu)
+    assert bool((h[-2:] == 3.0).all()) and bool((gu[-2:] == 3.0).all())
