@@ -117,3 +117,38 @@ def test_prompt_pass_in_one_graph(stq):
         want = p.run()
         torch.cuda.synchronize()
         assert all(torch.equal(first[n], want[n]) for n in names), r
+
+
+def test_readme_example(stq):
+    """The README's prompt pass runs as it stands, and its gradients are those of its stages.
+
+    dh is PyTorch's: an fp32 sum of d products, at most 2 u (d + 2) of their magnitudes off in any order, and
+    its rounding to bf16; d_tokens an fp32 sum of a token's top_k rows."""
+    import os
+    import re
+    with open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")) as f:
+        text = f.read()
+    part = text[text.index("\nA prompt pass."):]
+    blocks = re.findall(r"(?:^    .*\n)+", part, flags=re.M)[:2]
+    assert "token_logprobs(" in blocks[0] and "grouped_swiglu_backward(" in blocks[1]
+    T, E, d, f = 50, 5, 512, 256
+    p = Pass(stq, T, E, 2, d, f, 1003, seed=23)
+    names = dict(torch=torch, stq=stq, tokens=p.tokens, row_token=p.row_token.long(), row_weight=p.weight,
+                 offsets=p.c.offsets, bounds=p.c.bounds, gate_up=p.c.table, gate_up_stride=p.c.stride,
+                 down=p.down.table, down_stride=p.down.stride, experts=E, d_model=d, d_ff=f, head=p.head,
+                 head_scale=p.head_scale, targets=p.targets, g=p.g)
+    for b in blocks:
+        exec("".join(line[4:] for line in b.splitlines(True)), names)
+    logits = names["logits"].cpu()
+    TL._check(tuple(names[n] for n in ("logprob", "lse", "entropy", "ids", "alternatives")), logits, p.targets.cpu(), 5)
+    p.c.x, p.c.gu, p.c.dh = names["x"], names["gu"], names["dh"]
+    p.c.check_forward(names["h"], names["gu"])
+    dz = names["dz"].double()
+    for e in range(E):
+        lo, hi = p.c.bounds[e], p.c.bounds[e + 1]
+        w = p.down_w[e].double()
+        ref, A = dz[lo:hi] @ w, dz[lo:hi].abs() @ w.abs()
+        assert bool(((names["dh"][lo:hi].double() - ref).abs() <= 2 * TS.U * (d + 2) * A * (1 + TS.B) + TS.B * ref.abs()).all())
+    p.c.check_backward(names["dx"], names["dw"])
+    rows = names["dx"].double()[p.token_rows]                            # [T, top_k, d]
+    assert bool(((names["d_tokens"].double() - rows.sum(1)).abs() <= 2 * TS.U * rows.abs().sum(1)).all())
