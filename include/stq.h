@@ -354,8 +354,9 @@ stq_status stq_grouped_swiglu_workspace(int64_t n_experts, int64_t d_model, int6
  * through stq_gemv's kernels (and where there are none).  The choice is made
  * for rows that spread evenly over the experts, since the offsets are on the
  * device: a call whose rows go to few of its experts is right all the same,
- * but may take several times as long as with n_experts (and the offsets) of
- * those alone.  Host only, same checks and errors as the call.  rows_per_pass
+ * but may take many times as long as with n_experts (and the offsets) of
+ * those alone, up to 1,650 us instead of 50 for 300 rows of one of 256 experts
+ * of 2 x 2048 x 7168.  Host only, same checks and errors as the call.  rows_per_pass
  * is a HOST pointer. */
 stq_status stq_grouped_swiglu_plan(int64_t n_experts, int64_t d_model, int64_t d_ff, int64_t total_m, int32_t n_cus,
                                    int32_t* rows_per_pass);

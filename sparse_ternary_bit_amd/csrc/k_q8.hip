@@ -498,7 +498,8 @@ hipError_t launch_q8_quantize(const Q8QuantArgs& g, hipStream_t s) {
 //  * Up to 16 tokens: q8_few_kernel, until its re-reads of the tokens (once
 //    per 16 channels) weigh on a long channel list.  n = 4096: 8.2 for 1 token
 //    and 10.3 for 16, against 17 for the 64 x 64 tiles; n = 32768, k = 4096: 27
-//    and 36 against 33; n = 100003: 116 for 1 token and 178 for 16, against 122
+//    and 36 against 33 (where the rule changes over: one token still gains
+//    what 16 lose); n = 100003: 116 for 1 token and 178 for 16, against 122
 //    and 125 for the 64 x 256 tiles.
 //  * Up to 64 tokens: as wide a channel tile as leaves every CU two.  n =
 //    16384, k = 4096: 21 with 64 channels, 27 with 128, 35 with 256; 50000, k =

@@ -170,7 +170,7 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
 // All of it runs ahead of the matrix cores: while they multiply one 32-row
 // step, the next step's table reads are in flight, and the next tile's codes
 // and dz are written between a tile's two steps.  For 16384 rows of 256
-// experts of 4096 x 7168 it takes 1030 us; the products alone would take about
+// experts of 4096 x 7168 it takes 1050 us; the products alone would take about
 // 700, the rest is the instructions of the decode (a form that multiplied d
 // into the weights and transposed the codes in registers had 135 VALU
 // instructions per tile and 34 products, and took 1270 us).  The same rows of
@@ -715,8 +715,8 @@ SwigluBwdLayout swiglu_bwd_layout(int64_t d_ff, int64_t total_m, bool dx, bool d
 
 // Rows of a pass: 96, or 32 where those would leave much of the chip idle.
 // Measured, us of the whole call without dW, 96 / 32: one expert of 2 x 1024
-// of 4096, 100 rows 33 / 28, 500 rows 41 / 30, 4000 rows 88 / 128; 2 x 2048 of
-// 7168, 8 experts, 300 rows 57 / 61, 4096 rows 266 / 385.  (Passes of 80: 39
+// of 4096, 100 rows 33 / 28, 500 rows 41 / 30, 4000 rows 90 / 128; 2 x 2048 of
+// 7168, 8 experts, 300 rows 57 / 61, 4096 rows 268 / 385.  (Passes of 80: 39
 // for 500 rows, 97 for 4000, 285 for 4096 of 8 experts.)
 int dx_rows_a_pass(const SwigluBwdArgs& g, int cus) {
   constexpr PassCost kCost{2.0, {0.5, 0.007}, {0.64, 0.0108}};  // a 64-row tile
