@@ -44,7 +44,7 @@
  *   - the library allocates no device memory and keeps no device state: the
  *     entry points that need scratch memory (stq_gemv, stq_moe_ffn_decode,
  *     stq_layer_errors, stq_grouped_swiglu, stq_grouped_swiglu_backward,
- *     stq_token_logprobs) take a caller-owned `workspace` of `workspace_bytes`
+ *     stq_token_logprobs, stq_rmsnorm_rows_backward, stq_route_tokens) take a caller-owned `workspace` of `workspace_bytes`
  *     bytes, 256-byte aligned, whose required size a host-only query gives
  *     for the same shapes (stq_gemv_plan, and the call's name with _workspace
  *     behind it for the others: stq_moe_ffn_workspace for the FFN); a NULL or
@@ -488,6 +488,160 @@ stq_status stq_token_logprobs_backward(const void* logits, int x_dtype, int64_t 
                                        int64_t vocab, const int32_t* targets, const float* lse, const float* entropy,
                                        const float* grad_logprob, const float* grad_entropy, void* d_logits,
                                        int64_t d_row_stride, stq_stream_t stream);
+
+/* Residual addition, root-mean-square norm and 8-bit rows in one pass: what
+ * stands between the residual stream and the projections that
+ * stq_q8_quantize_rows and stq_q8_matmul serve, the router and the experts.
+ *     h = x + residual, rounded to the residual's type (h = x without one)
+ *     rstd = 1 / sqrt(mean h^2 + eps)
+ *     v = h * weight (one fp32 rounding),  step = fp32(max |v| / 127)
+ *     q = nearest integer to v / step (the exact quotient, halves to even),
+ *     scale = step * rstd,   y = v * rstd
+ * so that q * scale stands for y, and q does not depend on the order of the
+ * sum.  A row of zeros, or one whose step underflows to 0, gives scale 0 and q
+ * = 0; a row with a NaN or an infinity in v gives scale NaN and q = 0.  A row
+ * whose sum of squares passes fp32's range has rstd 0.
+ *   x          [n_rows, d] fp32 (STQ_X_F32) or bf16 bits (STQ_X_BF16), rows
+ *              x_row_stride elements apart
+ *   residual   [n_rows, d] likewise, or NULL
+ *   h          [n_rows, d] of the residual's type; may be the residual, or x
+ *              where the types are the same, with the same stride; read and
+ *              written only with a residual
+ *   weight     fp32 [d]
+ *   rstd       fp32 [n_rows] or NULL
+ *   q, scale   int8 rows as stq_q8_quantize_rows writes them (16-byte aligned,
+ *              q_row_stride bytes apart, a multiple of 16 and at least d
+ *              rounded up to 16; bytes from d up to that multiple are written
+ *              0), and fp32 [n_rows]; both or neither
+ *   y          bf16 bits [n_rows, d], rows y_row_stride elements apart, one
+ *              rounding of the fp32 value, or NULL
+ * Every pointer is aligned to its elements; rows that all start on 16 bytes
+ * are read and written faster.  Sums are fp32 in a fixed order: repeated calls
+ * give identical bits.  d >= 1; at most 2^22 rows and 2^26 columns. */
+stq_status stq_rmsnorm_rows(const void* x, int x_dtype, int64_t x_row_stride, const void* residual,
+                            int residual_dtype, int64_t residual_row_stride, void* h, int64_t h_row_stride,
+                            const float* weight, float eps, int64_t n_rows, int64_t d, float* rstd, int8_t* q,
+                            int64_t q_row_stride, float* scale, uint16_t* y, int64_t y_row_stride,
+                            stq_stream_t stream);
+
+/* Its gradients, for a gradient dy at the normed rows (the rounding to 8 bits
+ * taken as the identity) and one, dh, that arrives at h by another way, such as
+ * the residual stream.  With u = h * rstd and g = dy * weight:
+ *     dx = dh + rstd * (g - u * mean(g * u))     (x's gradient and the residual's)
+ *     dweight = sum over rows of dy * u
+ *   h, rstd    what the forward call gave
+ *   dy         [n_rows, d] fp32 or bf16
+ *   dh         [n_rows, d] of h's type, or NULL (zeros)
+ *   dx         [n_rows, d] of h's type, or NULL (not wanted); may be dh, or dy
+ *              where the types are the same, with the same stride
+ *   dweight    fp32 [d], or NULL (not wanted); zeros without rows
+ *   workspace, workspace_bytes   at least what
+ *              stq_rmsnorm_rows_backward_workspace reports (may be NULL when 0)
+ * Limits as above.  Sums are fp32 in an order that is fixed for a device. */
+stq_status stq_rmsnorm_rows_backward(const void* h, int h_dtype, int64_t h_row_stride, const float* weight,
+                                     const float* rstd, const void* dy, int dy_dtype, int64_t dy_row_stride,
+                                     const void* dh, int64_t dh_row_stride, void* dx, int64_t dx_row_stride,
+                                     float* dweight, int64_t n_rows, int64_t d, void* workspace,
+                                     int64_t workspace_bytes, stq_stream_t stream);
+
+/* Workspace bytes stq_rmsnorm_rows_backward needs for these shapes on a device
+ * with n_cus compute units (0: the current device's); host only.
+ * workspace_bytes is a HOST pointer. */
+stq_status stq_rmsnorm_rows_backward_workspace(int64_t n_rows, int64_t d, int want_dweight, int32_t n_cus,
+                                               int64_t* workspace_bytes);
+
+/* Routing (traictory.com, "The claim, stated precisely": every token goes to 8
+ * of 256 experts): the top_k largest of each token's logits, their weights, and
+ * the (token, expert) rows sorted by expert, stable in the tokens, as
+ * stq_gemv, stq_grouped_gemm and stq_grouped_swiglu take them.  With p =
+ * softmax(l) over all experts:
+ *     weight of a chosen expert e:  exp(l_e) / sum of exp(l) over the chosen
+ *                                   (renormalize != 0), else p_e
+ *     counts[e] = tokens that chose e,    f_e = counts[e] / sum of counts
+ *     balance = n_experts * sum_e f_e P_e,   P_e = mean of p_e over the tokens
+ * (balance is 1 where either is even; it grows with the agreement of counts and
+ * probabilities, and its gradient takes counts as given.)
+ *   logits       [n_tokens, n_experts] fp32 (STQ_X_F32) or bf16 bits
+ *                (STQ_X_BF16), rows row_stride elements apart, aligned to their
+ *                elements.  -inf masks an expert: it is chosen last, with weight
+ *                0.  Equal logits go to the lowest expert.
+ *   pair_expert, pair_weight  int32 / fp32 [n_tokens * top_k], a token's pairs
+ *                together, largest first
+ *   counts       int32 [n_experts];   offsets  int32 [n_experts + 1]
+ *   pair_row     int32 [n_tokens * top_k]: the row of each pair, -1 for none
+ *   row_token, row_weight  int32 / fp32 [n_tokens * top_k]: each row's token and
+ *                weight; token 0 and weight 0 from row offsets[n_experts] on
+ *   balance      fp32 [1]
+ * A token whose logits are all -inf (padding) goes nowhere: its pairs are expert
+ * -1 with weight 0, it has no rows and counts for nothing.  One with a NaN or a
+ * +inf goes nowhere either; its weights are NaN, and so is the balance.
+ * 1 <= n_experts <= 1024, 1 <= top_k <= min(32, n_experts), at most 2^22 tokens.
+ *   workspace, workspace_bytes   at least what stq_route_tokens_workspace
+ *                reports (may be NULL when 0)
+ * Sums are fp32 in a fixed order: repeated calls give identical bits. */
+stq_status stq_route_tokens(const void* logits, int x_dtype, int64_t row_stride, int64_t n_tokens, int64_t n_experts,
+                            int64_t top_k, int renormalize, int32_t* pair_expert, float* pair_weight, int32_t* counts,
+                            int32_t* offsets, int32_t* pair_row, int32_t* row_token, float* row_weight, float* balance,
+                            void* workspace, int64_t workspace_bytes, stq_stream_t stream);
+
+/* Workspace bytes stq_route_tokens needs for these shapes; host only, same
+ * checks and errors as the call.  workspace_bytes is a HOST pointer. */
+stq_status stq_route_tokens_workspace(int64_t n_tokens, int64_t n_experts, int64_t top_k, int64_t* workspace_bytes);
+
+/* Gradient of the weights and of the balance loss with respect to the logits,
+ * the choice and the counts taken as given: with g the gradient at a token's
+ * weights w and b the one at the balance,
+ *     renormalize: d_e += w_e (g_e - sum of g w) for the chosen
+ *     else:        d_e += p_e (g_e - sum of g p), g = 0 for the others
+ *     and          d_e += p_e (c_e - sum of c p),  c_e = b n_experts f_e / tokens
+ * (tokens: those that have rows, sum of counts / top_k).
+ *   logits, renormalize, pair_expert, counts   as given to and by the call above
+ *                (counts is read with grad_balance only; summed over the ranks of
+ *                a job, b's share of the tokens is that of the job)
+ *   grad_weight  fp32 [n_tokens * top_k] or NULL (zeros): in the order of the
+ *                pairs, or, with pair_row (else NULL), of the sorted rows
+ *   grad_balance fp32 [1] on the device, or NULL (zero)
+ *   d_logits     [n_tokens, n_experts], the logits' type, rows d_row_stride
+ *                elements apart; may be the logits themselves (same pointer and
+ *                stride), else it may not overlap them
+ * A token that went nowhere gives zeros, NaN where its logits hold a NaN or a
+ * +inf. */
+stq_status stq_route_tokens_backward(const void* logits, int x_dtype, int64_t row_stride, int64_t n_tokens,
+                                     int64_t n_experts, int64_t top_k, int renormalize, const int32_t* pair_expert,
+                                     const int32_t* counts, const float* grad_weight, const int32_t* pair_row,
+                                     const float* grad_balance, void* d_logits, int64_t d_row_stride,
+                                     stq_stream_t stream);
+
+/* A token's expert rows added up, in routing order:
+ *     y[t] = sum over j < top_k of pair_weight[t, j] * z[pair_row[t, j]]
+ * With ones for weights it is also the gradient of x_sorted = x[row_token].
+ *   z            [n_rows, d] fp32 (STQ_X_F32) or bf16 bits (STQ_X_BF16), rows
+ *                z_row_stride elements apart: the down projection's rows
+ *   pair_row     int32 [n_tokens * top_k], from stq_route_tokens; a pair whose
+ *                row is outside [0, n_rows) adds nothing
+ *   pair_weight  fp32 [n_tokens * top_k], or NULL (ones)
+ *   y            [n_tokens, d] fp32 or bf16, rows y_row_stride elements apart;
+ *                every element is written
+ * Every pointer is aligned to its elements; rows that all start on 16 bytes are
+ * read and written faster.  Sums are fp32, in order.  1 <= top_k <= 32, d >= 1;
+ * at most 2^22 tokens, 2^31 - 1 rows and 2^26 columns, and less than 2^24
+ * started pieces of 512 columns (2048 where d > 512) of a token in all. */
+stq_status stq_combine_rows(const void* z, int z_dtype, int64_t z_row_stride, int64_t n_rows, const int32_t* pair_row,
+                            const float* pair_weight, int64_t n_tokens, int64_t top_k, int64_t d, void* y, int y_dtype,
+                            int64_t y_row_stride, stq_stream_t stream);
+
+/* Its gradients, for dy [n_tokens, d] at y:
+ *     dz[pair_row[t, j]] = pair_weight[t, j] * dy[t]
+ *     dweight[t, j] = <dy[t], z[pair_row[t, j]]>, 0 for a pair without a row
+ *   dz       [n_rows, d] fp32 or bf16, or NULL (not wanted); rows of no pair stay
+ *            unwritten, and no row may have two pairs (stq_route_tokens gives none)
+ *   dweight  fp32 [n_tokens * top_k], or NULL (not wanted); reads z, which may
+ *            be NULL otherwise
+ * The other arguments and limits are as above.  dz may not overlap z or dy. */
+stq_status stq_combine_rows_backward(const void* dy, int dy_dtype, int64_t dy_row_stride, const void* z, int z_dtype,
+                                     int64_t z_row_stride, int64_t n_rows, const int32_t* pair_row,
+                                     const float* pair_weight, int64_t n_tokens, int64_t top_k, int64_t d, void* dz,
+                                     int dz_dtype, int64_t dz_row_stride, float* dweight, stq_stream_t stream);
 
 /* Measurement helper, not part of the method: reads `bytes` bytes of the
  * device buffer `buf` once with 16-byte loads, the streaming-read rate this

@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import typing
 
 import torch
 
@@ -21,7 +22,9 @@ __all__ = [
     "moe_ffn_workspace", "grouped_swiglu", "grouped_swiglu_workspace", "grouped_swiglu_plan",
     "grouped_swiglu_backward", "grouped_swiglu_backward_workspace", "grouped_swiglu_backward_plan",
     "q8_quantize_rows", "q8_matmul", "token_logprobs",
-    "token_logprobs_workspace", "token_logprobs_backward", "layer_errors", "layer_errors_workspace", "q2_roundtrip", "greedy_allocation",
+    "token_logprobs_workspace", "token_logprobs_backward", "Norm", "rmsnorm_rows", "rmsnorm_rows_backward",
+    "rmsnorm_rows_backward_workspace", "Routing", "route_tokens", "route_tokens_workspace", "route_tokens_backward",
+    "combine_rows", "combine_rows_backward", "layer_errors", "layer_errors_workspace", "q2_roundtrip", "greedy_allocation",
     "stream_read_probe", "mfma_loop_probe", "lds_read_probe", "MFMA_PROBE_FLOP_PER_ROUND",
     "LDS_PROBE_READS_PER_ROUND",
 ]
@@ -127,6 +130,28 @@ def lib() -> ctypes.CDLL:
     L.stq_token_logprobs_backward.argtypes = [_c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_vp, _c_vp, _c_vp, _c_vp,
                                               _c_vp, _c_vp, _c_i64, _c_vp]
     L.stq_token_logprobs_backward.restype = _c_int
+    L.stq_rmsnorm_rows.argtypes = [_c_vp, _c_int, _c_i64, _c_vp, _c_int, _c_i64, _c_vp, _c_i64, _c_vp, ctypes.c_float,
+                                   _c_i64, _c_i64, _c_vp, _c_vp, _c_i64, _c_vp, _c_vp, _c_i64, _c_vp]
+    L.stq_rmsnorm_rows.restype = _c_int
+    L.stq_rmsnorm_rows_backward.argtypes = [_c_vp, _c_int, _c_i64, _c_vp, _c_vp, _c_vp, _c_int, _c_i64, _c_vp, _c_i64,
+                                            _c_vp, _c_i64, _c_vp, _c_i64, _c_i64, _c_vp, _c_i64, _c_vp]
+    L.stq_rmsnorm_rows_backward.restype = _c_int
+    L.stq_rmsnorm_rows_backward_workspace.argtypes = [_c_i64, _c_i64, _c_int, ctypes.c_int32, ctypes.POINTER(_c_i64)]
+    L.stq_rmsnorm_rows_backward_workspace.restype = _c_int
+    L.stq_route_tokens.argtypes = [_c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_i64, _c_int, _c_vp, _c_vp, _c_vp, _c_vp,
+                                   _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_vp]
+    L.stq_route_tokens.restype = _c_int
+    L.stq_route_tokens_workspace.argtypes = [_c_i64, _c_i64, _c_i64, ctypes.POINTER(_c_i64)]
+    L.stq_route_tokens_workspace.restype = _c_int
+    L.stq_route_tokens_backward.argtypes = [_c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_i64, _c_int, _c_vp, _c_vp, _c_vp,
+                                            _c_vp, _c_vp, _c_vp, _c_i64, _c_vp]
+    L.stq_route_tokens_backward.restype = _c_int
+    L.stq_combine_rows.argtypes = [_c_vp, _c_int, _c_i64, _c_i64, _c_vp, _c_vp, _c_i64, _c_i64, _c_i64, _c_vp, _c_int,
+                                   _c_i64, _c_vp]
+    L.stq_combine_rows.restype = _c_int
+    L.stq_combine_rows_backward.argtypes = [_c_vp, _c_int, _c_i64, _c_vp, _c_int, _c_i64, _c_i64, _c_vp, _c_vp, _c_i64,
+                                            _c_i64, _c_i64, _c_vp, _c_int, _c_i64, _c_vp, _c_vp]
+    L.stq_combine_rows_backward.restype = _c_int
     L.stq_stream_read_probe.argtypes = [_c_vp, _c_i64, _c_vp, _c_vp]
     L.stq_stream_read_probe.restype = _c_int
     L.stq_mfma_loop_probe.argtypes = [_c_i64, _c_vp, _c_vp]
@@ -716,6 +741,310 @@ def token_logprobs_backward(logits: torch.Tensor, targets: torch.Tensor, lse: to
           stride, n, vocab, targets.data_ptr(), lse.data_ptr(), _ptr(entropy), _ptr(grad_logprob), _ptr(grad_entropy),
           out.data_ptr(), ds)
     return out
+
+
+_FLOATS = (torch.float32, torch.bfloat16)
+
+
+def _kind(t: torch.Tensor | None) -> int:
+    return X_BF16 if t is not None and t.dtype == torch.bfloat16 else X_F32
+
+
+def _out_rows(name: str, t: torch.Tensor, dtype: torch.dtype, rows: int, cols: int) -> int:
+    """Row stride of a caller's output matrix."""
+    if tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{name} must be [{rows}, {cols}], got {tuple(t.shape)}")
+    return _rows(name, t, dtype)
+
+
+class Norm(typing.NamedTuple):
+    """What rmsnorm_rows gives: the sum (x itself without a residual), 1 / rms of its rows, and the normed rows
+    as 8-bit integers with one scale each and in bf16 (None where not wanted)."""
+    h: torch.Tensor
+    rstd: torch.Tensor
+    q: torch.Tensor | None
+    scale: torch.Tensor | None
+    y: torch.Tensor | None
+
+
+def rmsnorm_rows(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: torch.Tensor | None = None,
+                 need_q: bool = True, need_y: bool = False, h: torch.Tensor | None = None,
+                 rstd: torch.Tensor | None = None, q: torch.Tensor | None = None, scale: torch.Tensor | None = None,
+                 y: torch.Tensor | None = None) -> Norm:
+    """Norm(h, rstd, q, scale, y) of x fp32 or bf16 [n, d] and a residual fp32 or bf16 [n, d]: h = x + residual in
+    the residual's type (x without one), rstd = 1 / sqrt(mean h^2 + eps), and the rows h * rstd * weight (weight
+    fp32 [d]) as q8_matmul takes them (q int8, scale fp32, wanted with need_q) and in bf16 (y, with need_y).  Outputs
+    are allocated here when not given; h may be the residual, or x where the types are the same."""
+    dev = _one_gpu(x, weight, residual, h, rstd, q, scale, y)
+    xs = _rows("x", x, *_FLOATS)
+    n, d = x.shape
+    _vector("weight", weight, torch.float32, d)
+    if residual is None:
+        if h is not None:
+            raise ValueError("h is given without a residual")
+        rs = hs = 0
+    else:
+        if tuple(residual.shape) != (n, d):
+            raise ValueError("residual must be [n, d] like x")
+        rs = _rows("residual", residual, *_FLOATS)
+        if h is None:
+            h, hs = torch.empty((n, d), dtype=residual.dtype, device=dev), d
+        else:
+            hs = _out_rows("h", h, residual.dtype, n, d)
+    if rstd is None:
+        rstd = torch.empty(n, dtype=torch.float32, device=dev)
+    else:
+        _vector("rstd", rstd, torch.float32, n)
+    qs = ys = 0
+    if need_q:
+        if q is None:
+            qs = (d + 15) // 16 * 16
+            q = torch.empty((n, qs), dtype=torch.int8, device=dev)
+            if qs != d:
+                q = q[:, :d]
+        else:
+            if tuple(q.shape) != (n, d):
+                raise ValueError("q must be [n, d] like x")
+            qs = _q8_stride("q", q)
+        if scale is None:
+            scale = torch.empty(n, dtype=torch.float32, device=dev)
+        else:
+            _vector("scale", scale, torch.float32, n)
+    elif q is not None or scale is not None:
+        raise ValueError("q or scale is given but need_q is False")
+    if need_y:
+        if y is None:
+            y, ys = torch.empty((n, d), dtype=torch.bfloat16, device=dev), d
+        else:
+            ys = _out_rows("y", y, torch.bfloat16, n, d)
+    elif y is not None:
+        raise ValueError("y is given but need_y is False")
+    _call(dev, "stq_rmsnorm_rows", x.data_ptr(), _kind(x), xs, _ptr(residual), _kind(residual), rs, _ptr(h), hs,
+          weight.data_ptr(), float(eps), n, d, rstd.data_ptr(), _ptr(q), qs, _ptr(scale), _ptr(y), ys)
+    return Norm(x if residual is None else h, rstd, q, scale, y)
+
+
+def rmsnorm_rows_backward_workspace(n_rows: int, d: int, need_dweight: bool = True, n_cus: int = 0) -> int:
+    """Workspace bytes rmsnorm_rows_backward needs for these shapes on n_cus compute units (0: the current
+    device's); host only."""
+    wb = ctypes.c_int64()
+    _check("stq_rmsnorm_rows_backward_workspace",
+           lib().stq_rmsnorm_rows_backward_workspace(int(n_rows), int(d), int(bool(need_dweight)), int(n_cus),
+                                                     ctypes.byref(wb)))
+    return wb.value
+
+
+def rmsnorm_rows_backward(h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor, dy: torch.Tensor,
+                          dh: torch.Tensor | None = None, need_dx: bool = True, need_dweight: bool = True,
+                          dx: torch.Tensor | None = None, dweight: torch.Tensor | None = None,
+                          workspace: torch.Tensor | None = None):
+    """(dx, dweight) of rmsnorm_rows for the gradient dy fp32 or bf16 [n, d] at the normed rows (the rounding to 8
+    bits taken as the identity) and dh, of h's type, that arrives at h by another way; h and rstd are what the
+    forward call gave.  dx is the gradient of x and of the residual alike, of h's type; dweight is fp32 [d]; None for
+    the one not needed.  dx may be dh, or dy where the types are the same.  `workspace` (GPU bytes, at least
+    rmsnorm_rows_backward_workspace(...)) is allocated here when not given."""
+    dev = _one_gpu(h, weight, rstd, dy, dh, dx, dweight, workspace)
+    hs = _rows("h", h, *_FLOATS)
+    n, d = h.shape
+    _vector("weight", weight, torch.float32, d)
+    _vector("rstd", rstd, torch.float32, n)
+    if tuple(dy.shape) != (n, d):
+        raise ValueError("dy must be [n, d] like h")
+    ys = _rows("dy", dy, *_FLOATS)
+    dhs = 0 if dh is None else _out_rows("dh", dh, h.dtype, n, d)
+    dxs = 0
+    if need_dx:
+        if dx is None:
+            dx, dxs = torch.empty((n, d), dtype=h.dtype, device=dev), d
+        else:
+            dxs = _out_rows("dx", dx, h.dtype, n, d)
+    elif dx is not None:
+        raise ValueError("dx is given but need_dx is False")
+    if need_dweight:
+        if dweight is None:
+            dweight = torch.empty(d, dtype=torch.float32, device=dev)
+        else:
+            _vector("dweight", dweight, torch.float32, d)
+    elif dweight is not None:
+        raise ValueError("dweight is given but need_dweight is False")
+    if workspace is None and need_dweight:
+        workspace = _workspace(None, rmsnorm_rows_backward_workspace(n, d, True, _device_cus(dev)), dev)
+    else:
+        workspace = _workspace(workspace, 0, dev)
+    _call(dev, "stq_rmsnorm_rows_backward", h.data_ptr(), _kind(h), hs, weight.data_ptr(), rstd.data_ptr(), dy.data_ptr(),
+          _kind(dy), ys, _ptr(dh), dhs, _ptr(dx), dxs, _ptr(dweight), n, d, *_ws_args(workspace))
+    return dx, dweight
+
+
+class Routing(typing.NamedTuple):
+    """What route_tokens gives.  pair_expert int32 and pair_weight fp32 [n * top_k]: a token's pairs together, as
+    moe_ffn_decode takes them; counts int32 [experts], offsets int32 [experts + 1], row_token int32 and row_weight
+    fp32 [n * top_k]: the rows sorted by expert, as grouped_swiglu and grouped_gemm take them; pair_row int32
+    [n * top_k]: the row of each pair (-1: none), as combine_rows takes it; balance fp32 [1]: the balance loss."""
+    pair_expert: torch.Tensor
+    pair_weight: torch.Tensor
+    counts: torch.Tensor
+    offsets: torch.Tensor
+    pair_row: torch.Tensor
+    row_token: torch.Tensor
+    row_weight: torch.Tensor
+    balance: torch.Tensor
+
+
+def route_tokens_workspace(n_tokens: int, n_experts: int, top_k: int) -> int:
+    """Workspace bytes route_tokens needs for these shapes (host only)."""
+    wb = ctypes.c_int64()
+    _check("stq_route_tokens_workspace",
+           lib().stq_route_tokens_workspace(int(n_tokens), int(n_experts), int(top_k), ctypes.byref(wb)))
+    return wb.value
+
+
+def route_tokens(logits: torch.Tensor, top_k: int, renormalize: bool = True, out: Routing | None = None,
+                 workspace: torch.Tensor | None = None) -> Routing:
+    """Routing of tokens by router logits fp32 or bf16 [n, experts]: the top_k largest of each row (equal logits by
+    lowest expert), with weights softmax(logits) over the chosen (renormalize) or over all experts, the rows sorted
+    by expert, per-expert counts, and the balance loss experts * sum_e (share of the rows of e) * (mean probability
+    of e).  A row of -inf is padding: it goes nowhere, with expert -1, weight 0 and no rows; rows of the output from
+    offsets[experts] on hold token 0 and weight 0.  Outputs and `workspace` (GPU bytes, at least
+    route_tokens_workspace(...)) are allocated here when not given."""
+    others = () if out is None else tuple(out)
+    dev = _one_gpu(logits, workspace, *others)
+    stride = _rows("logits", logits, *_FLOATS)
+    n, experts = logits.shape
+    top_k = int(top_k)
+    pairs = n * max(0, top_k)
+    if out is None:
+        # whole and 32-bit floating outputs, each kind in one allocation
+        whole = torch.empty(3 * pairs + 2 * experts + 1, dtype=torch.int32, device=dev)
+        pe, row, token, counts, offsets = whole.split((pairs, pairs, pairs, experts, experts + 1))
+        weight, row_weight, balance = torch.empty(2 * pairs + 1, dtype=torch.float32, device=dev).split((pairs, pairs, 1))
+        out = Routing(pe, weight, counts, offsets, row, token, row_weight, balance)
+    else:
+        if not isinstance(out, Routing):
+            raise ValueError("out must be a Routing")
+        for name, dtype, size in (("pair_expert", torch.int32, pairs), ("pair_weight", torch.float32, pairs),
+                                  ("counts", torch.int32, experts), ("offsets", torch.int32, experts + 1),
+                                  ("pair_row", torch.int32, pairs), ("row_token", torch.int32, pairs),
+                                  ("row_weight", torch.float32, pairs), ("balance", torch.float32, 1)):
+            _vector(name, getattr(out, name), dtype, size)
+    if workspace is None and n > 0:
+        workspace = _workspace(None, route_tokens_workspace(n, experts, top_k), dev)
+    else:
+        workspace = _workspace(workspace, 0, dev)
+    _call(dev, "stq_route_tokens", logits.data_ptr(), _kind(logits), stride, n, experts, top_k, int(bool(renormalize)),
+          *(t.data_ptr() for t in out), *_ws_args(workspace))
+    return out
+
+
+def route_tokens_backward(logits: torch.Tensor, pair_expert: torch.Tensor, counts: torch.Tensor | None, top_k: int,
+                          renormalize: bool = True, grad_weight: torch.Tensor | None = None,
+                          pair_row: torch.Tensor | None = None, grad_balance: torch.Tensor | None = None,
+                          out: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of route_tokens' weights and balance loss at the logits, the choice and the counts taken as given:
+    grad_weight fp32 [n * top_k] in the order of the pairs, or with pair_row in that of the sorted rows (the gradient
+    at row_weight); grad_balance fp32 [1]; either may be None.  `out` has the logits' type and shape and may be the
+    logits themselves."""
+    dev = _one_gpu(logits, pair_expert, counts, grad_weight, pair_row, grad_balance, out)
+    stride = _rows("logits", logits, *_FLOATS)
+    n, experts = logits.shape
+    top_k = int(top_k)
+    pairs = n * max(0, top_k)
+    _vector("pair_expert", pair_expert, torch.int32, pairs)
+    for name, t, dtype, size in (("counts", counts, torch.int32, experts), ("grad_weight", grad_weight, torch.float32, pairs),
+                                 ("pair_row", pair_row, torch.int32, pairs), ("grad_balance", grad_balance, torch.float32, 1)):
+        if t is not None:
+            _vector(name, t, dtype, size)
+    if grad_balance is not None and counts is None:
+        raise ValueError("grad_balance needs counts")
+    if out is None:
+        out, ds = torch.empty((n, experts), dtype=logits.dtype, device=dev), experts
+    else:
+        ds = _out_rows("out", out, logits.dtype, n, experts)
+    _call(dev, "stq_route_tokens_backward", logits.data_ptr(), _kind(logits), stride, n, experts, top_k,
+          int(bool(renormalize)), pair_expert.data_ptr(), _ptr(counts), _ptr(grad_weight), _ptr(pair_row),
+          _ptr(grad_balance), out.data_ptr(), ds)
+    return out
+
+
+def _pair_tokens(pair_row: torch.Tensor, weight: torch.Tensor | None, top_k: int) -> int:
+    """Tokens of a pair list of top_k pairs each."""
+    if top_k < 1:
+        raise ValueError("top_k must be positive")
+    pairs = pair_row.numel()
+    if pairs % top_k:
+        raise ValueError("pair_row must hold n_tokens * top_k entries")
+    _vector("pair_row", pair_row, torch.int32, pairs)
+    if weight is not None:
+        _vector("weight", weight, torch.float32, pairs)
+    return pairs // top_k
+
+
+def combine_rows(z: torch.Tensor, pair_row: torch.Tensor, top_k: int, weight: torch.Tensor | None = None,
+                 out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None) -> torch.Tensor:
+    """y[t] = sum over a token's top_k pairs, in order, of weight[t, j] * z[pair_row[t, j]] for rows z fp32 or bf16
+    [n_rows, d], pair_row int32 and weight fp32 (None: ones) [n_tokens * top_k]; a pair whose row lies outside z adds
+    nothing.  y is fp32 or bf16 [n_tokens, d]: `out`'s type, or out_dtype (z's when neither is given)."""
+    dev = _one_gpu(z, pair_row, weight, out)
+    zs = _rows("z", z, *_FLOATS)
+    rows, d = z.shape
+    top_k = int(top_k)
+    n = _pair_tokens(pair_row, weight, top_k)
+    if out is None:
+        out_dtype = z.dtype if out_dtype is None else out_dtype
+        if out_dtype not in _FLOATS:
+            raise ValueError("out_dtype must be bfloat16 or float32")
+        out, ys = torch.empty((n, d), dtype=out_dtype, device=dev), d
+    else:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError(f"out must be {out_dtype} like out_dtype, got {out.dtype}")
+        ys = _rows("out", out, *_FLOATS)
+        if tuple(out.shape) != (n, d):
+            raise ValueError(f"out must be [{n}, {d}], got {tuple(out.shape)}")
+    _call(dev, "stq_combine_rows", z.data_ptr(), _kind(z), zs, rows, pair_row.data_ptr(), _ptr(weight), n, top_k, d,
+          out.data_ptr(), _kind(out), ys)
+    return out
+
+
+def combine_rows_backward(dy: torch.Tensor, pair_row: torch.Tensor, top_k: int, z: torch.Tensor,
+                          weight: torch.Tensor | None = None, need_dz: bool = True, need_dweight: bool = True,
+                          dz: torch.Tensor | None = None, dz_dtype: torch.dtype | None = None,
+                          dweight: torch.Tensor | None = None):
+    """(dz, dweight) of combine_rows for the gradient dy fp32 or bf16 [n_tokens, d]: dz[pair_row[t, j]] =
+    weight[t, j] * dy[t], fp32 or bf16 like z ([n_rows, d]; `dz`'s type or dz_dtype, z's when neither is given; rows
+    of no pair stay unwritten), and dweight fp32 [n_tokens * top_k], the product of dy[t] and the pair's row; None for
+    the one not needed.  No row may have two pairs."""
+    dev = _one_gpu(dy, pair_row, z, weight, dz, dweight)
+    ys, zs = _rows("dy", dy, *_FLOATS), _rows("z", z, *_FLOATS)
+    rows, d = z.shape
+    top_k = int(top_k)
+    n = _pair_tokens(pair_row, weight, top_k)
+    if tuple(dy.shape) != (n, d):
+        raise ValueError(f"dy must be [{n}, {d}], got {tuple(dy.shape)}")
+    dzs = 0
+    if need_dz:
+        if dz is None:
+            dz_dtype = z.dtype if dz_dtype is None else dz_dtype
+            if dz_dtype not in _FLOATS:
+                raise ValueError("dz_dtype must be bfloat16 or float32")
+            dz, dzs = torch.empty((rows, d), dtype=dz_dtype, device=dev), d
+        else:
+            if dz_dtype is not None and dz.dtype != dz_dtype:
+                raise ValueError(f"dz must be {dz_dtype} like dz_dtype, got {dz.dtype}")
+            dzs = _rows("dz", dz, *_FLOATS)
+            if tuple(dz.shape) != (rows, d):
+                raise ValueError("dz must be [n_rows, d] like z")
+    elif dz is not None:
+        raise ValueError("dz is given but need_dz is False")
+    if need_dweight:
+        if dweight is None:
+            dweight = torch.empty(n * top_k, dtype=torch.float32, device=dev)
+        else:
+            _vector("dweight", dweight, torch.float32, n * top_k)
+    elif dweight is not None:
+        raise ValueError("dweight is given but need_dweight is False")
+    _call(dev, "stq_combine_rows_backward", dy.data_ptr(), _kind(dy), ys, z.data_ptr(), _kind(z), zs, rows,
+          pair_row.data_ptr(), _ptr(weight), n, top_k, d, _ptr(dz), _kind(dz), dzs, _ptr(dweight))
+    return dz, dweight
 
 
 def layer_errors_workspace(n_rows: int, k: int, n_calib: int) -> int:

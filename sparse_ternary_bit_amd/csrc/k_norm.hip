@@ -1,0 +1,357 @@
+// Residual addition, root-mean-square norm and the rounding of the normed rows
+// to 8-bit integers, in one pass, and the norm's gradients.
+//
+//     h = x + r (rounded to the stream's type)     rstd = 1 / sqrt(mean h^2 + eps)
+//     y = h w rstd         q = nearest integer to y / scale,  scale = max |y| / 127
+//
+// rstd is the same for the whole row, so the integers do not depend on it:
+// with v = h w and step = fp32(max |v| / 127), q is the integer nearest the
+// exact v / step and scale = step rstd.  One pass over the row therefore
+// gives the sum of squares and the largest |v| together, the row stays in
+// registers, and the integers have one right value whatever the order of the
+// sum.
+//
+// Gradients, with u = h rstd and g = dy w:
+//     dx = dh + rstd (g - u mean(g u))            dw = sum over rows of dy u
+#include <algorithm>
+#include <type_traits>
+
+#include "stq_launch.hpp"
+#include "stq_rows.hpp"
+
+namespace stq {
+namespace {
+
+struct None {};  // no residual
+
+// Sum of `v` over a workgroup in a fixed order; `slot` holds one float a
+// wavefront and is free again after the next barrier but one.
+template <int kThreads>
+__device__ __forceinline__ float block_sum(float v, float* slot) {
+  v = sum64(v);
+  if constexpr (kThreads == 64) return v;
+  if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
+  __syncthreads();
+  float s = slot[0];
+#pragma unroll
+  for (int i = 1; i < kThreads / 64; ++i) s += slot[i];
+  return s;
+}
+
+// One workgroup a row; kHeld groups of 8 values a thread stay in registers,
+// what lies beyond (rows of more than 8192 values) is read again.
+template <typename TX, typename TR, bool kVec, int kThreads, int kHeld>
+__global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs a) {
+  constexpr bool kRes = !__is_same(TR, None);
+  __shared__ float ssum[kThreads / 64];
+  __shared__ uint32_t smax[kThreads / 64];
+  const int64_t r = blockIdx.x;
+  const int64_t d = a.d, groups = (d + 7) / 8;
+  const TX* x = static_cast<const TX*>(a.x) + r * a.x_stride;
+  float ss = 0.0f;
+  uint32_t mx = 0;  // the largest |v| as bits: a NaN orders above every number and so is kept
+  // the sum as it is stored, 8 values from column c on; columns past d are 0
+  auto sum8 = [&](int64_t c, float (&f)[8], Raw8<TX> rx) {
+    unpack8<TX>(rx, f);
+    if constexpr (kRes) {
+      const TR* res = static_cast<const TR*>(a.res) + r * a.res_stride;
+      float b[8];
+      load8f<TR, kVec>(res, c, d, b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] += b[i];
+      const Raw8<TR> o = pack8<TR>(f);
+      store8<TR, kVec>(static_cast<TR*>(a.h) + r * a.h_stride, c, d, o);
+      unpack8<TR>(o, f);
+    }
+  };
+  auto weigh = [&](int64_t c, const float (&f)[8], float (&v)[8]) {
+    float w[8];
+    load8f<float, kVec>(a.weight, c, d, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = f[i] * w[i];
+      ss = fmaf(f[i], f[i], ss);
+      mx = max(mx, __builtin_bit_cast(uint32_t, v[i]) & 0x7FFFFFFFu);
+    }
+  };
+  float v[kHeld][8];
+  {
+    Raw8<TX> rx[kHeld];
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) rx[i] = load8<TX, kVec>(x, (threadIdx.x + i * kThreads) * 8, d);
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const int64_t c = (threadIdx.x + i * kThreads) * 8;
+      float f[8];
+      sum8(c, f, rx[i]);
+      weigh(c, f, v[i]);
+    }
+  }
+  for (int64_t g = threadIdx.x + kHeld * kThreads; g < groups; g += kThreads) {
+    float f[8], t[8];
+    sum8(g * 8, f, load8<TX, kVec>(x, g * 8, d));
+    weigh(g * 8, f, t);
+  }
+  ss = sum64(ss);
+  mx = max64(mx);
+  if constexpr (kThreads > 64) {
+    if ((threadIdx.x & 63) == 0) {
+      ssum[threadIdx.x >> 6] = ss;
+      smax[threadIdx.x >> 6] = mx;
+    }
+    __syncthreads();
+    ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kThreads / 64; ++i) {
+      ss += ssum[i];
+      mx = max(mx, smax[i]);
+    }
+  }
+  const float rstd = 1.0f / sqrtf(ss / static_cast<float>(d) + a.eps);
+  const bool finite = mx < 0x7F800000u;
+  const float step = finite ? __builtin_bit_cast(float, mx) / 127.0f : NAN;
+  if (threadIdx.x == 0) {
+    if (a.rstd) a.rstd[r] = rstd;
+    if (a.q) a.scale[r] = step * rstd;
+  }
+  const bool some = finite && step > 0.0f;
+  const float inv = some ? 1.0f / step : 0.0f;
+  const bool fast = step > 0x1p-100f;
+  auto put = [&](int64_t g, const float (&t)[8]) {
+    if (a.q) {
+      uint32_t o[2] = {0, 0};
+      if (some) quantize<8>(t, step, inv, fast, o);
+      *reinterpret_cast<u32x2_t*>(a.q + r * a.q_stride + g * 8) = u32x2_t{o[0], o[1]};
+      // the row's last 16 bytes are its own: the half that no group covers is 0
+      if (g == groups - 1 && (groups & 1)) *reinterpret_cast<u32x2_t*>(a.q + r * a.q_stride + g * 8 + 8) = u32x2_t{0, 0};
+    }
+    if (a.y) {
+      float y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = t[i] * rstd;
+      store8<bf16_t, kVec>(reinterpret_cast<bf16_t*>(a.y) + r * a.y_stride, g * 8, d, pack8<bf16_t>(y));
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if (threadIdx.x + i * kThreads < groups) put(threadIdx.x + i * kThreads, v[i]);
+  for (int64_t g = threadIdx.x + kHeld * kThreads; g < groups; g += kThreads) {
+    float f[8], w[8], t[8];
+    // this thread's own store of the sum, or x
+    if constexpr (kRes) load8f<TR, kVec>(static_cast<const TR*>(a.h) + r * a.h_stride, g * 8, d, f);
+    else load8f<TX, kVec>(x, g * 8, d, f);
+    load8f<float, kVec>(a.weight, g * 8, d, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = f[i] * w[i];
+    put(g, t);
+  }
+}
+
+// dx, and each workgroup's part of dw: a workgroup walks the rows blockIdx.x,
+// + gridDim.x, ..., and its threads add dy u for their columns in registers.
+// kHeld * kThreads * 8 columns at most.
+template <typename TH, typename TY, bool kVec, int kThreads, int kHeld>
+__global__ __launch_bounds__(kThreads, 2) void norm_bwd_kernel(NormBwdArgs a, float* part) {
+  __shared__ float slot[2][kThreads / 64];
+  const int64_t d = a.d;
+  float w[kHeld][8], acc[kHeld][8];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    load8f<float, kVec>(a.weight, (threadIdx.x + i * kThreads) * 8, d, w[i]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[i][e] = 0.0f;
+  }
+  int odd = 0;
+  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, odd ^= 1) {
+    const TH* h = static_cast<const TH*>(a.h) + r * a.h_stride;
+    const TY* dy = static_cast<const TY*>(a.dy) + r * a.dy_stride;
+    const float rstd = a.rstd[r];
+    Raw8<TH> rh[kHeld], rd[kHeld];
+    Raw8<TY> ry[kHeld];
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const int64_t c = (threadIdx.x + i * kThreads) * 8;
+      rh[i] = load8<TH, kVec>(h, c, d);
+      ry[i] = load8<TY, kVec>(dy, c, d);
+    }
+    if (a.dh) {
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i)
+        rd[i] = load8<TH, kVec>(static_cast<const TH*>(a.dh) + r * a.dh_stride, (threadIdx.x + i * kThreads) * 8, d);
+    }
+    float dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      float f[8], g[8];
+      unpack8<TH>(rh[i], f);
+      unpack8<TY>(ry[i], g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float u = f[e] * rstd;
+        acc[i][e] = fmaf(g[e], u, acc[i][e]);
+        dot = fmaf(g[e] * w[i][e], u, dot);
+      }
+    }
+    const float mean = block_sum<kThreads>(dot, slot[odd]) / static_cast<float>(d);
+    if (a.dx) {
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) {
+        const int64_t c = (threadIdx.x + i * kThreads) * 8;
+        float f[8], g[8], o[8];
+        unpack8<TH>(rh[i], f);
+        unpack8<TY>(ry[i], g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = rstd * (g[e] * w[i][e] - f[e] * rstd * mean);
+        if (a.dh) {
+          unpack8<TH>(rd[i], f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] += f[e];
+        }
+        if (c < d) store8<TH, kVec>(static_cast<TH*>(a.dx) + r * a.dx_stride, c, d, pack8<TH>(o));
+      }
+    }
+  }
+  if (part) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const int64_t c = (threadIdx.x + i * kThreads) * 8;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (c + e < d) part[static_cast<int64_t>(blockIdx.x) * d + c + e] = acc[i][e];
+    }
+  }
+}
+
+// Rows of more than 8192 values: dx with a second read of the row, one
+// workgroup a row ...
+template <typename TH, typename TY, bool kVec>
+__global__ __launch_bounds__(512) void norm_bwd_wide_kernel(NormBwdArgs a) {
+  __shared__ float slot[8];
+  const int64_t r = blockIdx.x, d = a.d;
+  const TH* h = static_cast<const TH*>(a.h) + r * a.h_stride;
+  const TY* dy = static_cast<const TY*>(a.dy) + r * a.dy_stride;
+  const float rstd = a.rstd[r];
+  float dot = 0.0f;
+  for (int64_t c = threadIdx.x * 8; c < d; c += 512 * 8) {
+    float f[8], g[8], w[8];
+    load8f<TH, kVec>(h, c, d, f);
+    load8f<TY, kVec>(dy, c, d, g);
+    load8f<float, kVec>(a.weight, c, d, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dot = fmaf(g[e] * w[e], f[e] * rstd, dot);
+  }
+  const float mean = block_sum<512>(dot, slot) / static_cast<float>(d);
+  for (int64_t c = threadIdx.x * 8; c < d; c += 512 * 8) {
+    float f[8], g[8], w[8], o[8];
+    load8f<TH, kVec>(h, c, d, f);
+    load8f<TY, kVec>(dy, c, d, g);
+    load8f<float, kVec>(a.weight, c, d, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = rstd * (g[e] * w[e] - f[e] * rstd * mean);
+    if (a.dh) {
+      load8f<TH, kVec>(static_cast<const TH*>(a.dh) + r * a.dh_stride, c, d, f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] += f[e];
+    }
+    store8<TH, kVec>(static_cast<TH*>(a.dx) + r * a.dx_stride, c, d, pack8<TH>(o));
+  }
+}
+
+// ... and dw column by column: workgroup (i, j) adds the rows j, j + gridDim.y,
+// ... of 256 columns.
+template <typename TH, typename TY>
+__global__ __launch_bounds__(256) void norm_dweight_wide_kernel(NormBwdArgs a, float* part) {
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (c >= a.d) return;
+  float acc = 0.0f;
+  for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y)
+    acc = fmaf(widen(static_cast<const TY*>(a.dy)[r * a.dy_stride + c]),
+               widen(static_cast<const TH*>(a.h)[r * a.h_stride + c]) * a.rstd[r], acc);
+  part[static_cast<int64_t>(blockIdx.y) * a.d + c] = acc;
+}
+
+// The workgroups' parts added up: 32 columns a workgroup, 32 threads a column
+__global__ __launch_bounds__(1024) void norm_dweight_sum_kernel(const float* part, int n, int64_t d, float* dw) {
+  __shared__ float s[32][33];
+  const int col = threadIdx.x & 31, lane = threadIdx.x >> 5;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + col;
+  float acc = 0.0f;
+  if (c < d) {
+#pragma unroll 4
+    for (int i = lane; i < n; i += 32) acc += part[static_cast<int64_t>(i) * d + c];
+  }
+  s[lane][col] = acc;
+  __syncthreads();
+  if (lane || c >= d) return;
+  acc = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) acc += s[i][col];
+  dw[c] = acc;
+}
+
+bool vec16(const void* p, int64_t stride, int64_t esz) {
+  return !p || ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride * esz % 16 == 0);
+}
+int64_t esize(int bf16) { return bf16 ? 2 : 4; }
+
+}  // namespace
+
+// Threads a row.  Few rows are latency, which more threads shorten; a batch
+// fills the chip with smaller workgroups.
+hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
+  const bool vec = vec16(a.x, a.x_stride, esize(a.x_bf16)) && vec16(a.res, a.res_stride, esize(a.res_bf16)) &&
+                   vec16(a.h, a.h_stride, esize(a.res_bf16)) && vec16(a.weight, 0, 4) && vec16(a.y, a.y_stride, 2);
+  auto go = [&](auto x, auto res, auto v) {
+    using TX = decltype(x);
+    using TR = decltype(res);
+    constexpr bool kVec = decltype(v)::value;
+    const dim3 grid(static_cast<unsigned>(a.rows));
+    if (a.d <= 512) hipLaunchKernelGGL((norm_kernel<TX, TR, kVec, 64, 1>), grid, dim3(64), 0, s, a);
+    else if (a.d <= 2048) hipLaunchKernelGGL((norm_kernel<TX, TR, kVec, 256, 1>), grid, dim3(256), 0, s, a);
+    else if (a.rows <= 512) hipLaunchKernelGGL((norm_kernel<TX, TR, kVec, 1024, 1>), grid, dim3(1024), 0, s, a);
+    else hipLaunchKernelGGL((norm_kernel<TX, TR, kVec, 256, 4>), grid, dim3(256), 0, s, a);
+  };
+  auto with_vec = [&](auto x, auto res) { vec ? go(x, res, std::true_type{}) : go(x, res, std::false_type{}); };
+  auto with_res = [&](auto x) {
+    if (!a.res) with_vec(x, None{});
+    else if (a.res_bf16) with_vec(x, bf16_t{});
+    else with_vec(x, 0.0f);
+  };
+  a.x_bf16 ? with_res(bf16_t{}) : with_res(0.0f);
+  return hipGetLastError();
+}
+
+// Workgroups that share the rows, each with a part of dw
+int norm_bwd_parts(int64_t rows, int cus) { return static_cast<int>(std::min<int64_t>(rows, 2 * cus)); }
+
+hipError_t launch_norm_bwd(const NormBwdArgs& a, float* part, int cus, hipStream_t s) {
+  const bool vec = vec16(a.h, a.h_stride, esize(a.h_bf16)) && vec16(a.dy, a.dy_stride, esize(a.dy_bf16)) &&
+                   vec16(a.dh, a.dh_stride, esize(a.h_bf16)) && vec16(a.dx, a.dx_stride, esize(a.h_bf16)) &&
+                   vec16(a.weight, 0, 4);
+  const int parts = norm_bwd_parts(a.rows, cus);
+  float* const pw = a.dw ? part : nullptr;
+  auto go = [&](auto h, auto y, auto v) {
+    using TH = decltype(h);
+    using TY = decltype(y);
+    constexpr bool kVec = decltype(v)::value;
+    const dim3 grid(static_cast<unsigned>(parts));
+    if (a.d <= 512) hipLaunchKernelGGL((norm_bwd_kernel<TH, TY, kVec, 64, 1>), grid, dim3(64), 0, s, a, pw);
+    else if (a.d <= 2048) hipLaunchKernelGGL((norm_bwd_kernel<TH, TY, kVec, 256, 1>), grid, dim3(256), 0, s, a, pw);
+    else if (a.d <= 8192) hipLaunchKernelGGL((norm_bwd_kernel<TH, TY, kVec, 256, 4>), grid, dim3(256), 0, s, a, pw);
+    else {
+      // dw first: dx may take dy's place
+      if (pw)
+        hipLaunchKernelGGL((norm_dweight_wide_kernel<TH, TY>),
+                           dim3(static_cast<unsigned>((a.d + 255) / 256), static_cast<unsigned>(parts)), dim3(256), 0, s, a, pw);
+      if (a.dx) hipLaunchKernelGGL((norm_bwd_wide_kernel<TH, TY, kVec>), dim3(static_cast<unsigned>(a.rows)), dim3(512), 0, s, a);
+    }
+  };
+  auto with_vec = [&](auto h, auto y) { vec ? go(h, y, std::true_type{}) : go(h, y, std::false_type{}); };
+  auto with_y = [&](auto h) { a.dy_bf16 ? with_vec(h, bf16_t{}) : with_vec(h, 0.0f); };
+  if (a.rows > 0) a.h_bf16 ? with_y(bf16_t{}) : with_y(0.0f);
+  if (a.dw)
+    hipLaunchKernelGGL(norm_dweight_sum_kernel, dim3(static_cast<unsigned>((a.d + 31) / 32)), dim3(1024), 0, s, part, parts, a.d, a.dw);
+  return hipGetLastError();
+}
+
+}  // namespace stq

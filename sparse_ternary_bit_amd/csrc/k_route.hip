@@ -1,0 +1,551 @@
+// Routing of tokens to experts: the top_k largest of each token's logits, their
+// weights, the rows sorted by expert, and the balance loss with its gradient.
+//
+//     p = softmax(l) over the experts
+//     weight of a chosen expert: p, or exp(l) / sum of exp(l) over the chosen
+//     balance = E sum_e f_e P_e,  f_e = rows of e / all rows,  P_e = mean p_e
+//
+// Tokens are taken 64 at a time (a chunk).  16 lanes hold a token's logits, so
+// that every reduction is four DPP rotations and serves four tokens; a key of
+// 22 bits of the logit over 10 of the expert's index makes an extraction one
+// maximum and one comparison a logit (150 instructions a token for 8 of 256
+// experts; a maximum with a separate search for its index takes twice that).
+// bf16 logits fit such a key; fp32 logits that agree in their first 22 bits
+// next to the chosen ones are chosen again with all 32.
+//
+// The sorted order is a counting sort without a sort: a token chooses an
+// expert at most once, so an expert's tokens of a chunk are 64 bits, a pair's
+// place in the chunk is a population count, and the chunks' counts need one
+// prefix sum an expert.  One chunk runs as one launch, more as three.
+#include <algorithm>
+#include <type_traits>
+
+#include "stq_launch.hpp"
+#include "stq_rows.hpp"
+
+namespace stq {
+namespace {
+
+constexpr int kChunk = 64;
+constexpr int kLanes = 16;        // lanes of a token
+constexpr int kMaxExperts = kRouteMaxExperts;
+static_assert(kRouteMaxTop <= 2 * kLanes, "a lane holds two of a token's pairs");
+constexpr int kIndexBits = 10;
+constexpr uint32_t kIndexMask = (1u << kIndexBits) - 1u;
+constexpr float kLog2e = 1.44269504088896340736f;
+
+__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+
+// Column of a lane's j-th logit: four neighbours a lane, 64 a step
+__device__ __forceinline__ int column(int lane16, int j) { return (j >> 2) * 64 + lane16 * 4 + (j & 3); }
+
+// Bits that order like the value; -0 and +0 alike.  -inf gives 0x007FFFFF, so
+// 0 stands for "none".
+__device__ __forceinline__ uint32_t order_bits(float v) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, v + 0.0f);
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+  return reduce16(v, [](uint32_t a, uint32_t b) { return max(a, b); });
+}
+__device__ __forceinline__ uint32_t min16(uint32_t v) {
+  return reduce16(v, [](uint32_t a, uint32_t b) { return min(a, b); });
+}
+__device__ __forceinline__ float fmax16(float v) {
+  return reduce16(v, [](float a, float b) { return fmaxf(a, b); });
+}
+
+// A token's logits, kN a lane; columns from `experts` on read as -inf
+template <typename T, int kN>
+__device__ __forceinline__ void load_logits(const T* row, int lane16, int experts, bool vec, bool valid, float (&v)[kN]) {
+#pragma unroll
+  for (int q = 0; q < kN / 4; ++q) {
+    const int c = column(lane16, 4 * q);
+    if (valid && vec && c + 4 <= experts) {
+      if constexpr (sizeof(T) == 4) {
+        const f32x4_t w = *reinterpret_cast<const f32x4_t*>(row + c);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[4 * q + e] = w[e];
+      } else {
+        const u32x2_t w = *reinterpret_cast<const u32x2_t*>(row + c);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          v[4 * q + e] = __builtin_bit_cast(float, (e & 1) ? (w[e >> 1] & 0xFFFF0000u) : (w[e >> 1] << 16));
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[4 * q + e] = valid && c + e < experts ? widen(row[c + e]) : -INFINITY;
+    }
+  }
+}
+
+// exp(l - max) of a token's logits into v's place; returns their sum: NaN for
+// a token with a NaN or +inf, 0 for one that is masked throughout.
+template <int kN>
+__device__ __forceinline__ float exponents(float (&v)[kN], float& top) {
+  float m = v[0];
+#pragma unroll
+  for (int j = 1; j < kN; ++j) m = fmaxf(m, v[j]);
+  m = fmax16(m);
+  top = m;
+  float s = 0.0f;
+#pragma unroll
+  for (int j = 0; j < kN; ++j) {
+    // masked logits under a masked maximum count for nothing; a NaN stays one
+    const float x = v[j] == -INFINITY ? 0.0f : exp_of(v[j] - m);
+    v[j] = x;
+    s += x;
+  }
+  return sum16(s);
+}
+
+struct RouteKernelArgs {
+  RouteArgs a;
+  int vec;
+  int chunks;
+  int32_t* hist;    // [experts][chunks]
+  float* prob;      // [experts][chunks]
+  float* prob_total;
+};
+
+// Exclusive prefix sum of n counts in LDS by one wavefront; returns the total
+__device__ __forceinline__ int scan_counts(const int* counts, int* offsets, int n) {
+  const int lane = threadIdx.x & 63;
+  const int per = (n + 63) / 64;
+  int own = 0;
+  for (int i = 0; i < per; ++i) own += lane * per + i < n ? counts[lane * per + i] : 0;
+  int sum = own;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int up = __shfl_up(sum, o);
+    if (lane >= o) sum += up;
+  }
+  int at = sum - own;
+  for (int i = 0; i < per; ++i) {
+    const int e = lane * per + i;
+    if (e < n) {
+      offsets[e] = at;
+      at += counts[e];
+    }
+  }
+  const int total = __shfl(sum, 63);
+  if (lane == 0) offsets[n] = total;
+  return total;
+}
+
+// E sum_e counts_e / total * prob_e / tokens by one wavefront
+template <typename F>
+__device__ __forceinline__ float balance_of(const int* counts, F prob, int n, int total, int top_k) {
+  float s = 0.0f;
+  for (int e = threadIdx.x & 63; e < n; e += 64) s = fmaf(static_cast<float>(counts[e]), prob(e), s);
+  s = sum64(s);
+  const float rows = static_cast<float>(max(total, 1));
+  return s * (static_cast<float>(n) / rows) * (static_cast<float>(top_k) / rows);
+}
+
+// One chunk: choice, weights, counts and summed probabilities; with kOne (the
+// only chunk) the sorted rows too.
+template <typename T, int kN, int kThreads, bool kOne>
+__global__ __launch_bounds__(kThreads) void route_kernel(RouteKernelArgs g) {
+  constexpr int kWaves = kThreads / 64, kAtOnce = kThreads / kLanes;
+  const RouteArgs& a = g.a;
+  const int E = a.experts, k = a.top_k;
+  __shared__ uint32_t mask[kMaxExperts][2];   // an expert's tokens of the chunk
+  __shared__ float slab[kWaves][kLanes * kN];
+  __shared__ int count[kOne ? kMaxExperts : 1], first[kOne ? kMaxExperts + 1 : 1];
+  __shared__ float prob[kOne ? kMaxExperts : 1];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lane16 = threadIdx.x & (kLanes - 1);
+  for (int i = threadIdx.x; i < E; i += kThreads) mask[i][0] = mask[i][1] = 0u;
+  __syncthreads();
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kChunk;
+  float acc[kN];
+#pragma unroll
+  for (int j = 0; j < kN; ++j) acc[j] = 0.0f;
+  for (int pass = 0; pass < kChunk / kAtOnce; ++pass) {
+    const int tl = pass * kAtOnce + static_cast<int>(threadIdx.x) / kLanes;
+    const int64_t t = t0 + tl;
+    const bool valid = t < a.tokens;
+    if (__ballot(valid) == 0) break;   // tokens come in order: none is left for this wavefront
+    const T* row = static_cast<const T*>(a.logits) + (valid ? t : 0) * a.stride;
+    float v[kN];
+    load_logits<T, kN>(row, lane16, E, g.vec, valid, v);
+    uint32_t key[kN];
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+      const int c = column(lane16, j);
+      key[j] = c < E ? (order_bits(v[j]) & ~kIndexMask) | (kIndexMask - c) : 0u;
+    }
+    float top;
+    const float sum = exponents<kN>(v, top);
+    const float inv = 1.0f / sum;
+    if (valid && top != -INFINITY) {
+#pragma unroll
+      for (int j = 0; j < kN; ++j) acc[j] = fmaf(v[j], inv, acc[j]);
+    }
+    // extraction: after step i, lane i % 16 holds the i-th key
+    uint32_t mine[2] = {0u, 0u}, last = 0u;
+    bool unsure = false;
+    const int steps = sizeof(T) == 4 ? min(k + 1, E) : k;
+    for (int i = 0; i < steps; ++i) {
+      uint32_t m = key[0];
+#pragma unroll
+      for (int j = 1; j < kN; ++j) m = max(m, key[j]);
+      m = max16(m);
+      unsure |= i > 0 && ((m ^ last) & ~kIndexMask) == 0u;
+      last = m;
+      if (lane16 == (i & 15) && i < k) mine[i >> 4] = m;
+#pragma unroll
+      for (int j = 0; j < kN; ++j) key[j] = key[j] == m ? 0u : key[j];
+    }
+    int pick[2] = {static_cast<int>(kIndexMask - (mine[0] & kIndexMask)), static_cast<int>(kIndexMask - (mine[1] & kIndexMask))};
+    if (sizeof(T) == 4 && __any(unsure && valid)) {
+      // some keys agree: once more with whole values, the lowest index first
+      load_logits<T, kN>(row, lane16, E, g.vec, valid, v);
+      uint64_t left = 0;
+#pragma unroll
+      for (int j = 0; j < kN; ++j) left |= column(lane16, j) < E ? 1ull << j : 0ull;
+      for (int i = 0; i < k; ++i) {
+        uint32_t m = 0u;
+#pragma unroll
+        for (int j = 0; j < kN; ++j) m = max(m, (left >> j & 1) ? order_bits(v[j]) : 0u);
+        m = max16(m);
+        uint32_t c = ~0u;
+#pragma unroll
+        for (int j = 0; j < kN; ++j)
+          if ((left >> j & 1) && order_bits(v[j]) == m) c = min(c, static_cast<uint32_t>(column(lane16, j)));
+        c = min16(c);
+#pragma unroll
+        for (int j = 0; j < kN; ++j)
+          if (static_cast<uint32_t>(column(lane16, j)) == c) left &= ~(1ull << j);
+        if (lane16 == (i & 15)) pick[i >> 4] = static_cast<int>(c);
+      }
+    }
+    // weights; a token without a distribution goes nowhere
+    const bool routed = valid && top != -INFINITY && sum == sum;
+    float w[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (routed && lane16 + 16 * h < k) {
+        const float l = widen(row[pick[h]]);
+        w[h] = l == -INFINITY ? 0.0f : exp_of(l - top);
+      }
+    const float norm = a.renorm ? 1.0f / sum16(w[0] + w[1]) : inv;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = lane16 + 16 * h;
+      if (!valid || i >= k) continue;
+      const int64_t p = t * k + i;
+      a.pair_expert[p] = routed ? pick[h] : -1;
+      a.pair_weight[p] = routed ? w[h] * norm : top == -INFINITY && sum == sum ? 0.0f : NAN;
+      if (routed) atomicOr(&mask[pick[h]][tl >> 5], 1u << (tl & 31));
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kN; ++j) {
+    float s = acc[j];
+    s += __shfl_xor(s, 16);
+    s += __shfl_xor(s, 32);
+    if (lane < kLanes) slab[wave][column(lane, j)] = s;
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += kThreads) {
+    float s = slab[0][e];
+#pragma unroll
+    for (int i = 1; i < kWaves; ++i) s += slab[i][e];
+    const int n = __popc(mask[e][0]) + __popc(mask[e][1]);
+    if constexpr (kOne) {
+      prob[e] = s;
+      count[e] = n;
+    } else {
+      g.prob[static_cast<int64_t>(e) * g.chunks + blockIdx.x] = s;
+      g.hist[static_cast<int64_t>(e) * g.chunks + blockIdx.x] = n;
+    }
+  }
+  if constexpr (kOne) {
+    __syncthreads();
+    if (wave == 0) {
+      const int total = scan_counts(count, first, E);
+      const float b = balance_of(count, [&](int e) { return prob[e]; }, E, total, k);
+      if (lane == 0) *a.balance = b;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += kThreads) {
+      a.counts[e] = count[e];
+      a.offsets[e] = first[e];
+    }
+    if (threadIdx.x == 0) a.offsets[E] = first[E];
+    const int pairs = static_cast<int>(a.tokens) * k;
+    for (int p = threadIdx.x; p < pairs; p += kThreads) {
+      const int tl = p / k, e = a.pair_expert[p];   // written by this workgroup before its barriers
+      int at = -1;
+      if (e >= 0) {
+        const uint32_t lo = tl < 32 ? mask[e][0] & ((1u << tl) - 1u) : mask[e][0];
+        const uint32_t hi = tl < 32 ? 0u : mask[e][1] & ((1u << (tl - 32)) - 1u);
+        at = first[e] + __popc(lo) + __popc(hi);
+        a.row_token[at] = tl;
+        a.row_weight[at] = a.pair_weight[p];
+      }
+      a.pair_row[p] = at;
+      if (p >= first[E]) {
+        a.row_token[p] = 0;
+        a.row_weight[p] = 0.0f;
+      }
+    }
+  }
+}
+
+// An expert's counts over the chunks turned into the rows before each chunk,
+// and its probabilities added up; a wavefront an expert.
+__global__ __launch_bounds__(256) void route_scan_kernel(RouteKernelArgs g) {
+  const int e = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+  if (e >= g.a.experts) return;
+  int32_t* hist = g.hist + static_cast<int64_t>(e) * g.chunks;
+  const float* prob = g.prob + static_cast<int64_t>(e) * g.chunks;
+  int before = 0;
+  float p = 0.0f;
+  for (int c0 = 0; c0 < g.chunks; c0 += 64) {
+    const int c = c0 + lane;
+    const int own = c < g.chunks ? hist[c] : 0;
+    if (c < g.chunks) p += prob[c];
+    int sum = own;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int up = __shfl_up(sum, o);
+      if (lane >= o) sum += up;
+    }
+    if (c < g.chunks) hist[c] = before + sum - own;
+    before += __shfl(sum, 63);
+  }
+  p = sum64(p);
+  if (lane == 0) {
+    g.a.counts[e] = before;
+    g.prob_total[e] = p;
+  }
+}
+
+// A chunk's pairs to their rows
+__global__ __launch_bounds__(256) void route_scatter_kernel(RouteKernelArgs g) {
+  __shared__ uint32_t mask[kMaxExperts][2];
+  __shared__ int count[kMaxExperts], first[kMaxExperts + 1];
+  const RouteArgs& a = g.a;
+  const int E = a.experts, k = a.top_k;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kChunk;
+  const int pairs = static_cast<int>(min(static_cast<int64_t>(kChunk), a.tokens - t0)) * k;
+  const int64_t p0 = t0 * k;
+  for (int e = threadIdx.x; e < E; e += 256) {
+    mask[e][0] = mask[e][1] = 0u;
+    count[e] = a.counts[e];
+  }
+  __syncthreads();
+  for (int p = threadIdx.x; p < pairs; p += 256) {
+    const int e = a.pair_expert[p0 + p], tl = p / k;
+    if (e >= 0) atomicOr(&mask[e][tl >> 5], 1u << (tl & 31));
+  }
+  if (threadIdx.x < 64) {
+    const int total = scan_counts(count, first, E);
+    if (blockIdx.x == 0) {
+      const float b = balance_of(count, [&](int e) { return g.prob_total[e]; }, E, total, k);
+      if (threadIdx.x == 0) *a.balance = b;
+    }
+  }
+  __syncthreads();
+  if (blockIdx.x == 0)
+    for (int e = threadIdx.x; e <= E; e += 256) a.offsets[e] = first[e];
+  const int64_t total = first[E];
+  for (int p = threadIdx.x; p < pairs; p += 256) {
+    const int tl = p / k, e = a.pair_expert[p0 + p];
+    int at = -1;
+    if (e >= 0) {
+      const uint32_t lo = tl < 32 ? mask[e][0] & ((1u << tl) - 1u) : mask[e][0];
+      const uint32_t hi = tl < 32 ? 0u : mask[e][1] & ((1u << (tl - 32)) - 1u);
+      at = first[e] + g.hist[static_cast<int64_t>(e) * g.chunks + blockIdx.x] + __popc(lo) + __popc(hi);
+      a.row_token[at] = static_cast<int32_t>(t0) + tl;
+      a.row_weight[at] = a.pair_weight[p0 + p];
+    }
+    a.pair_row[p0 + p] = at;
+    if (p0 + p >= total) {
+      a.row_token[p0 + p] = 0;
+      a.row_weight[p0 + p] = 0.0f;
+    }
+  }
+}
+
+// Gradient: 16 lanes a token again.  The chosen experts' share goes through a
+// row of LDS, from the lanes that hold the pairs to those that hold the
+// logits.
+template <typename T, int kN, int kThreads>
+__global__ __launch_bounds__(kThreads) void route_bwd_kernel(RouteBwdArgs a, int vec) {
+  constexpr int kTok = kThreads / kLanes, kCols = kLanes * kN;
+  __shared__ float coef[kCols];          // d balance / d p_e of one token, times grad_balance
+  __shared__ float chosen[kTok][kCols];
+  __shared__ float wsum[kThreads / 64];
+  const int E = a.experts, k = a.top_k;
+  const int lane16 = threadIdx.x & (kLanes - 1), tl = threadIdx.x / kLanes;
+  float total = 0.0f;
+  if (a.g_balance) {
+    int n = 0;
+    for (int e = threadIdx.x; e < E; e += kThreads) n += a.counts[e];
+    // whole numbers below 2^31: exact in two halves
+    const float hi = sum64(static_cast<float>(n >> 12)), lo = sum64(static_cast<float>(n & 4095));
+    if ((threadIdx.x & 63) == 0) wsum[threadIdx.x >> 6] = hi * 4096.0f + lo;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kThreads / 64; ++i) total += wsum[i];
+  }
+  const float rows = fmaxf(total, 1.0f);
+  const float scale = a.g_balance ? *a.g_balance * (static_cast<float>(E) / rows) * (static_cast<float>(k) / rows) : 0.0f;
+  for (int e = threadIdx.x; e < kCols; e += kThreads)
+    coef[e] = a.g_balance && e < E ? scale * static_cast<float>(a.counts[e]) : 0.0f;
+  const int64_t steps = (a.tokens + kTok - 1) / kTok;
+  for (int64_t st = blockIdx.x; st < steps; st += gridDim.x) {
+    const int64_t t = st * kTok + tl;
+    const bool valid = t < a.tokens;
+    const T* row = static_cast<const T*>(a.logits) + (valid ? t : 0) * a.stride;
+    float v[kN];
+    load_logits<T, kN>(row, lane16, E, vec, valid, v);
+    float top;
+    const float sum = exponents<kN>(v, top);
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int q = 0; q < kN / 4; ++q) *reinterpret_cast<f32x4_t*>(&chosen[tl][column(lane16, 4 * q)]) = f32x4_t{0, 0, 0, 0};
+    __syncthreads();
+    float w[2] = {0.0f, 0.0f}, gw[2] = {0.0f, 0.0f};
+    int e[2] = {-1, -1};
+    if (a.g_weight && valid) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int i = lane16 + 16 * h;
+        if (i >= k) continue;
+        const int64_t p = t * k + i;
+        const int ex = a.pair_expert[p];
+        int64_t at = p;
+        if (a.pair_row) at = a.pair_row[p];
+        if (ex < 0 || ex >= E || at < 0 || at >= a.tokens * k) continue;
+        e[h] = ex;
+        gw[h] = a.g_weight[at];
+        const float l = widen(row[ex]);
+        w[h] = l == -INFINITY ? 0.0f : exp_of(l - top);
+      }
+    }
+    if (a.renorm) {
+      const float ws = sum16(w[0] + w[1]);
+      const float winv = ws == 0.0f ? 0.0f : 1.0f / ws;
+      const float mean = sum16(fmaf(w[0], gw[0], w[1] * gw[1])) * winv;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) gw[h] = w[h] * winv * (gw[h] - mean);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (e[h] >= 0) atomicAdd(&chosen[tl][e[h]], gw[h]);
+    __syncthreads();
+    // renorm: d = p (c - sum c p) + the chosen's own; else their gradient joins c
+    float cv[kN], dot = 0.0f;
+#pragma unroll
+    for (int q = 0; q < kN / 4; ++q) {
+      const int c = column(lane16, 4 * q);
+      const f32x4_t co = *reinterpret_cast<const f32x4_t*>(&coef[c]), ch = *reinterpret_cast<const f32x4_t*>(&chosen[tl][c]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int j = 4 * q + i;
+        v[j] *= inv;
+        cv[j] = a.renorm ? co[i] : co[i] + ch[i];
+        dot = fmaf(cv[j], v[j], dot);
+      }
+    }
+    dot = sum16(dot);
+    if (!valid) {
+      __syncthreads();
+      continue;
+    }
+    T* out = static_cast<T*>(a.d_logits) + t * a.d_stride;
+#pragma unroll
+    for (int q = 0; q < kN / 4; ++q) {
+      const int c = column(lane16, 4 * q);
+      if (c >= E) continue;
+      const f32x4_t ch = *reinterpret_cast<const f32x4_t*>(&chosen[tl][c]);
+      float d[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float base = v[4 * q + i] * (cv[4 * q + i] - dot);
+        d[i] = a.renorm ? base + ch[i] : base;
+      }
+      if (vec && c + 4 <= E) {
+        if constexpr (sizeof(T) == 4) *reinterpret_cast<f32x4_t*>(out + c) = f32x4_t{d[0], d[1], d[2], d[3]};
+        else *reinterpret_cast<u32x2_t*>(out + c) = u32x2_t{bf16_round(d[0]) | bf16_round(d[1]) << 16, bf16_round(d[2]) | bf16_round(d[3]) << 16};
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (c + i < E) out[c + i] = narrow<T>(d[i]);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+bool vec4(const void* p, int64_t stride, int64_t esz) {
+  return (reinterpret_cast<uintptr_t>(p) & (4 * esz - 1)) == 0 && stride % 4 == 0;
+}
+
+int64_t round256(int64_t b) { return (b + 255) / 256 * 256; }
+
+}  // namespace
+
+RouteLayout route_layout(int64_t tokens, int64_t experts) {
+  const int64_t chunks = (tokens + kChunk - 1) / kChunk;
+  if (chunks <= 1) return RouteLayout{chunks, 0, 0, 0};
+  const int64_t part = round256(chunks * experts * 4);
+  return RouteLayout{chunks, part, 2 * part, 2 * part + round256(experts * 4)};
+}
+
+hipError_t launch_route(const RouteArgs& a, void* ws, hipStream_t s) {
+  const RouteLayout l = route_layout(a.tokens, a.experts);
+  char* base = static_cast<char*>(ws);
+  const bool one = l.chunks <= 1;
+  const RouteKernelArgs g{a, vec4(a.logits, a.stride, a.bf16 ? 2 : 4), static_cast<int>(l.chunks),
+                          one ? nullptr : reinterpret_cast<int32_t*>(base), one ? nullptr : reinterpret_cast<float*>(base + l.prob),
+                          one ? nullptr : reinterpret_cast<float*>(base + l.prob_total)};
+  const dim3 grid(static_cast<unsigned>(one ? 1 : l.chunks));
+  auto go = [&](auto t, auto n, auto threads) {
+    using T = decltype(t);
+    constexpr int kN = decltype(n)::value, kThreads = decltype(threads)::value;
+    if (one) hipLaunchKernelGGL((route_kernel<T, kN, kThreads, true>), grid, dim3(kThreads), 0, s, g);
+    else hipLaunchKernelGGL((route_kernel<T, kN, kThreads, false>), grid, dim3(kThreads), 0, s, g);
+  };
+  // logits a lane, and as many threads as their registers leave room for
+  auto with_n = [&](auto t) {
+    if (a.experts <= 64) go(t, std::integral_constant<int, 4>{}, std::integral_constant<int, 1024>{});
+    else if (a.experts <= 128) go(t, std::integral_constant<int, 8>{}, std::integral_constant<int, 1024>{});
+    else if (a.experts <= 256) go(t, std::integral_constant<int, 16>{}, std::integral_constant<int, 1024>{});
+    else if (a.experts <= 512) go(t, std::integral_constant<int, 32>{}, std::integral_constant<int, 512>{});
+    else go(t, std::integral_constant<int, 64>{}, std::integral_constant<int, 256>{});
+  };
+  a.bf16 ? with_n(bf16_t{}) : with_n(0.0f);
+  if (!one) {
+    hipLaunchKernelGGL(route_scan_kernel, dim3((a.experts + 3) / 4), dim3(256), 0, s, g);
+    hipLaunchKernelGGL(route_scatter_kernel, grid, dim3(256), 0, s, g);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_route_bwd(const RouteBwdArgs& a, hipStream_t s) {
+  const int esz = a.bf16 ? 2 : 4;
+  const bool vec = vec4(a.logits, a.stride, esz) && vec4(a.d_logits, a.d_stride, esz);
+  auto go = [&](auto t, auto n) {
+    constexpr int kN = decltype(n)::value, kThreads = 256;
+    const int64_t steps = (a.tokens + kThreads / kLanes - 1) / (kThreads / kLanes);
+    hipLaunchKernelGGL((route_bwd_kernel<decltype(t), kN, kThreads>), dim3(static_cast<unsigned>(std::min<int64_t>(steps, 8192))),
+                       dim3(kThreads), 0, s, a, vec);
+  };
+  auto with_n = [&](auto t) {
+    if (a.experts <= 64) go(t, std::integral_constant<int, 4>{});
+    else if (a.experts <= 128) go(t, std::integral_constant<int, 8>{});
+    else if (a.experts <= 256) go(t, std::integral_constant<int, 16>{});
+    else if (a.experts <= 512) go(t, std::integral_constant<int, 32>{});
+    else go(t, std::integral_constant<int, 64>{});
+  };
+  a.bf16 ? with_n(bf16_t{}) : with_n(0.0f);
+  return hipGetLastError();
+}
+
+}  // namespace stq

@@ -697,6 +697,254 @@ stq_status stq_token_logprobs_backward(const void* logits, int x_dtype, int64_t 
   return ok();
 }
 
+namespace {
+
+bool known_type(int dtype) { return dtype == STQ_X_F32 || dtype == STQ_X_BF16; }
+int64_t type_size(int dtype) { return dtype == STQ_X_BF16 ? 2 : 4; }
+
+constexpr int64_t kMaxRows = int64_t{1} << 22;
+constexpr int64_t kMaxCols = int64_t{1} << 26;
+
+// Counts of the row operators
+stq_status rows_check(int64_t n_rows, int64_t d, const char* who) {
+  if (n_rows < 0) return fail(STQ_E_ARG, "%s: negative count", who);
+  if (d < 1 || d > kMaxCols) return fail(STQ_E_SHAPE, "%s: d=%lld outside 1..2^26", who, (long long)d);
+  if (n_rows > kMaxRows) return fail(STQ_E_SHAPE, "%s: more than 2^22 rows in one call", who);
+  return STQ_OK;
+}
+
+// A matrix of n rows of d elements: row stride, size and alignment
+stq_status matrix_check(const char* name, const void* p, int dtype, int64_t stride, int64_t n, int64_t d, const char* who) {
+  const int64_t esz = type_size(dtype);
+  if (n > 1 && stride < d) return fail(STQ_E_SHAPE, "%s: row stride of %s < %lld", who, name, (long long)d);
+  if (!fits(n, stride, esz)) return fail(STQ_E_SHAPE, "%s: row stride of %s too large", who, name);
+  if (!aligned(p, esz)) return fail(STQ_E_ALIGN, "%s: %s not aligned to its elements", who, name);
+  return STQ_OK;
+}
+
+}  // namespace
+
+stq_status stq_rmsnorm_rows(const void* x, int x_dtype, int64_t x_row_stride, const void* residual,
+                            int residual_dtype, int64_t residual_row_stride, void* h, int64_t h_row_stride,
+                            const float* weight, float eps, int64_t n_rows, int64_t d, float* rstd, int8_t* q,
+                            int64_t q_row_stride, float* scale, uint16_t* y, int64_t y_row_stride,
+                            stq_stream_t stream) {
+  const char* who = "stq_rmsnorm_rows";
+  stq_status st = rows_check(n_rows, d, who);
+  if (st != STQ_OK) return st;
+  if (!known_type(x_dtype) || (residual && !known_type(residual_dtype))) return fail(STQ_E_ARG, "%s: unknown type of x or residual", who);
+  if (!(eps >= 0.0f)) return fail(STQ_E_ARG, "%s: eps must not be negative", who);
+  if ((q == nullptr) != (scale == nullptr)) return fail(STQ_E_ARG, "%s: q and scale go together", who);
+  if (n_rows == 0) return ok();
+  if (!x || !weight) return fail(STQ_E_ARG, "%s: null pointer", who);
+  if (residual && !h) return fail(STQ_E_ARG, "%s: a residual needs h", who);
+  if (q && q_row_stride < (d + 15) / 16 * 16) return fail(STQ_E_SHAPE, "%s: q_row_stride < d rounded up to 16", who);
+  if (q && !fits(n_rows, q_row_stride, 1)) return fail(STQ_E_SHAPE, "%s: q_row_stride too large", who);
+  if (!aligned(q, 16) || (q && q_row_stride % 16)) return fail(STQ_E_ALIGN, "%s: q / q_row_stride not 16-byte aligned", who);
+  if (!aligned(weight, 4) || !aligned(rstd, 4) || !aligned(scale, 4)) return fail(STQ_E_ALIGN, "%s: weight, rstd or scale not 4-byte aligned", who);
+  st = matrix_check("x", x, x_dtype, x_row_stride, n_rows, d, who);
+  if (st == STQ_OK && residual) st = matrix_check("residual", residual, residual_dtype, residual_row_stride, n_rows, d, who);
+  if (st == STQ_OK && residual) st = matrix_check("h", h, residual_dtype, h_row_stride, n_rows, d, who);
+  if (st == STQ_OK && y) st = matrix_check("y", y, STQ_X_BF16, y_row_stride, n_rows, d, who);
+  if (st != STQ_OK) return st;
+  if (residual && n_rows > 1 && h == residual && h_row_stride != residual_row_stride)
+    return fail(STQ_E_ARG, "%s: in place needs equal row strides", who);
+  if (residual && h == x && (x_dtype != residual_dtype || (n_rows > 1 && h_row_stride != x_row_stride)))
+    return fail(STQ_E_ARG, "%s: in place needs equal types and row strides", who);
+  const stq::NormArgs a{x, x_dtype == STQ_X_BF16, x_row_stride, residual, residual_dtype == STQ_X_BF16, residual_row_stride,
+                        residual ? h : nullptr, h_row_stride, weight, eps, n_rows, d, rstd, q, q_row_stride, scale, y, y_row_stride};
+  hipError_t e = stq::launch_norm(a, reinterpret_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "stq_rmsnorm_rows launch");
+  return ok();
+}
+
+stq_status stq_rmsnorm_rows_backward_workspace(int64_t n_rows, int64_t d, int want_dweight, int32_t n_cus,
+                                               int64_t* workspace_bytes) {
+  const char* who = "stq_rmsnorm_rows_backward_workspace";
+  if (!workspace_bytes) return fail(STQ_E_ARG, "%s: null output pointer", who);
+  *workspace_bytes = 0;
+  if (n_cus < 0) return fail(STQ_E_ARG, "%s: n_cus < 0", who);
+  const stq_status st = rows_check(n_rows, d, who);
+  if (st != STQ_OK) return st;
+  if (want_dweight && n_rows > 0)
+    *workspace_bytes = 4 * d * stq::norm_bwd_parts(n_rows, n_cus > 0 ? n_cus : stq::cus_of_current_device());
+  return ok();
+}
+
+stq_status stq_rmsnorm_rows_backward(const void* h, int h_dtype, int64_t h_row_stride, const float* weight,
+                                     const float* rstd, const void* dy, int dy_dtype, int64_t dy_row_stride,
+                                     const void* dh, int64_t dh_row_stride, void* dx, int64_t dx_row_stride,
+                                     float* dweight, int64_t n_rows, int64_t d, void* workspace,
+                                     int64_t workspace_bytes, stq_stream_t stream) {
+  const char* who = "stq_rmsnorm_rows_backward";
+  stq_status st = rows_check(n_rows, d, who);
+  if (st != STQ_OK) return st;
+  if (!known_type(h_dtype) || !known_type(dy_dtype)) return fail(STQ_E_ARG, "%s: unknown type of h or dy", who);
+  if (workspace_bytes < 0) return fail(STQ_E_ARG, "%s: workspace_bytes < 0", who);
+  if (!dx && !dweight) return ok();
+  if (!dweight && n_rows == 0) return ok();
+  if (n_rows > 0 && (!h || !weight || !rstd || !dy)) return fail(STQ_E_ARG, "%s: null pointer", who);
+  if (!aligned(weight, 4) || !aligned(rstd, 4) || !aligned(dweight, 4)) return fail(STQ_E_ALIGN, "%s: weight, rstd or dweight not 4-byte aligned", who);
+  st = matrix_check("h", h, h_dtype, h_row_stride, n_rows, d, who);
+  if (st == STQ_OK) st = matrix_check("dy", dy, dy_dtype, dy_row_stride, n_rows, d, who);
+  if (st == STQ_OK && dh) st = matrix_check("dh", dh, h_dtype, dh_row_stride, n_rows, d, who);
+  if (st == STQ_OK && dx) st = matrix_check("dx", dx, h_dtype, dx_row_stride, n_rows, d, who);
+  if (st != STQ_OK) return st;
+  if (dx && n_rows > 1 && dx == dh && dx_row_stride != dh_row_stride) return fail(STQ_E_ARG, "%s: in place needs equal row strides", who);
+  if (dx && dx == dy && (h_dtype != dy_dtype || (n_rows > 1 && dx_row_stride != dy_row_stride)))
+    return fail(STQ_E_ARG, "%s: in place needs equal types and row strides", who);
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const int cus = stq::cus_of_stream(s);
+  if (dweight) {
+    st = check_workspace(workspace, workspace_bytes, 4 * d * stq::norm_bwd_parts(n_rows, cus), who);
+    if (st != STQ_OK) return st;
+  }
+  const stq::NormBwdArgs a{h, h_dtype == STQ_X_BF16, h_row_stride, weight, rstd, dy, dy_dtype == STQ_X_BF16, dy_row_stride,
+                           dh, dh_row_stride, dx, dx_row_stride, dweight, n_rows, d};
+  hipError_t e = stq::launch_norm_bwd(a, static_cast<float*>(workspace), cus, s);
+  if (e != hipSuccess) return hip_fail(e, "stq_rmsnorm_rows_backward launch");
+  return ok();
+}
+
+namespace {
+
+stq_status route_check(int64_t n_tokens, int64_t n_experts, int64_t top_k, const char* who) {
+  if (n_tokens < 0) return fail(STQ_E_ARG, "%s: negative count", who);
+  if (n_experts < 1 || n_experts > stq::kRouteMaxExperts)
+    return fail(STQ_E_SHAPE, "%s: n_experts=%lld outside 1..%d", who, (long long)n_experts, stq::kRouteMaxExperts);
+  if (top_k < 1 || top_k > stq::kRouteMaxTop || top_k > n_experts)
+    return fail(STQ_E_SHAPE, "%s: top_k=%lld outside 1..%d, or above n_experts", who, (long long)top_k, stq::kRouteMaxTop);
+  if (n_tokens > kMaxRows) return fail(STQ_E_SHAPE, "%s: more than 2^22 tokens in one call", who);
+  return STQ_OK;
+}
+
+}  // namespace
+
+stq_status stq_route_tokens_workspace(int64_t n_tokens, int64_t n_experts, int64_t top_k, int64_t* workspace_bytes) {
+  const char* who = "stq_route_tokens_workspace";
+  if (!workspace_bytes) return fail(STQ_E_ARG, "%s: null output pointer", who);
+  *workspace_bytes = 0;
+  const stq_status st = route_check(n_tokens, n_experts, top_k, who);
+  if (st != STQ_OK) return st;
+  *workspace_bytes = stq::route_layout(n_tokens, n_experts).bytes;
+  return ok();
+}
+
+stq_status stq_route_tokens(const void* logits, int x_dtype, int64_t row_stride, int64_t n_tokens, int64_t n_experts,
+                            int64_t top_k, int renormalize, int32_t* pair_expert, float* pair_weight, int32_t* counts,
+                            int32_t* offsets, int32_t* pair_row, int32_t* row_token, float* row_weight, float* balance,
+                            void* workspace, int64_t workspace_bytes, stq_stream_t stream) {
+  const char* who = "stq_route_tokens";
+  stq_status st = route_check(n_tokens, n_experts, top_k, who);
+  if (st != STQ_OK) return st;
+  if (!known_type(x_dtype)) return fail(STQ_E_ARG, "%s: unknown x_dtype %d", who, x_dtype);
+  if (!counts || !offsets || !balance) return fail(STQ_E_ARG, "%s: null pointer", who);
+  if (n_tokens > 0 && (!logits || !pair_expert || !pair_weight || !pair_row || !row_token || !row_weight))
+    return fail(STQ_E_ARG, "%s: null pointer", who);
+  st = matrix_check("logits", logits, x_dtype, row_stride, n_tokens, n_experts, who);
+  if (st != STQ_OK) return st;
+  if (!aligned(pair_expert, 4) || !aligned(pair_weight, 4) || !aligned(counts, 4) || !aligned(offsets, 4) ||
+      !aligned(pair_row, 4) || !aligned(row_token, 4) || !aligned(row_weight, 4) || !aligned(balance, 4))
+    return fail(STQ_E_ALIGN, "%s: outputs not 4-byte aligned", who);
+  st = check_workspace(workspace, workspace_bytes, stq::route_layout(n_tokens, n_experts).bytes, who);
+  if (st != STQ_OK) return st;
+  const stq::RouteArgs a{logits, x_dtype == STQ_X_BF16, row_stride, n_tokens, static_cast<int>(n_experts),
+                         static_cast<int>(top_k), renormalize != 0, pair_expert, pair_weight, counts, offsets, pair_row,
+                         row_token, row_weight, balance};
+  hipError_t e = stq::launch_route(a, workspace, reinterpret_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "stq_route_tokens launch");
+  return ok();
+}
+
+stq_status stq_route_tokens_backward(const void* logits, int x_dtype, int64_t row_stride, int64_t n_tokens,
+                                     int64_t n_experts, int64_t top_k, int renormalize, const int32_t* pair_expert,
+                                     const int32_t* counts, const float* grad_weight, const int32_t* pair_row,
+                                     const float* grad_balance, void* d_logits, int64_t d_row_stride,
+                                     stq_stream_t stream) {
+  const char* who = "stq_route_tokens_backward";
+  stq_status st = route_check(n_tokens, n_experts, top_k, who);
+  if (st != STQ_OK) return st;
+  if (!known_type(x_dtype)) return fail(STQ_E_ARG, "%s: unknown x_dtype %d", who, x_dtype);
+  if (n_tokens == 0) return ok();
+  if (!logits || !d_logits) return fail(STQ_E_ARG, "%s: null pointer", who);
+  if (grad_weight && !pair_expert) return fail(STQ_E_ARG, "%s: grad_weight needs pair_expert", who);
+  if (grad_balance && !counts) return fail(STQ_E_ARG, "%s: grad_balance needs counts", who);
+  st = matrix_check("logits", logits, x_dtype, row_stride, n_tokens, n_experts, who);
+  if (st == STQ_OK) st = matrix_check("d_logits", d_logits, x_dtype, d_row_stride, n_tokens, n_experts, who);
+  if (st != STQ_OK) return st;
+  if (logits == d_logits && n_tokens > 1 && row_stride != d_row_stride)
+    return fail(STQ_E_ARG, "%s: in place needs equal row strides", who);
+  if (!aligned(pair_expert, 4) || !aligned(counts, 4) || !aligned(grad_weight, 4) || !aligned(pair_row, 4) || !aligned(grad_balance, 4))
+    return fail(STQ_E_ALIGN, "%s: pairs, counts or gradients not 4-byte aligned", who);
+  const stq::RouteBwdArgs a{logits, x_dtype == STQ_X_BF16, row_stride, n_tokens, static_cast<int>(n_experts),
+                            static_cast<int>(top_k), renormalize != 0, pair_expert, counts, grad_weight, pair_row,
+                            grad_balance, d_logits, d_row_stride};
+  hipError_t e = stq::launch_route_bwd(a, reinterpret_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "stq_route_tokens_backward launch");
+  return ok();
+}
+
+namespace {
+
+stq_status combine_check(int64_t n_tokens, int64_t top_k, int64_t d, int64_t n_rows, const char* who) {
+  const stq_status st = rows_check(n_tokens, d, who);
+  if (st != STQ_OK) return st;
+  if (n_rows < 0) return fail(STQ_E_ARG, "%s: negative count", who);
+  if (n_rows > INT_MAX) return fail(STQ_E_SHAPE, "%s: n_rows exceeds int32", who);
+  if (top_k < 1 || top_k > stq::kRouteMaxTop) return fail(STQ_E_SHAPE, "%s: top_k=%lld outside 1..%d", who, (long long)top_k, stq::kRouteMaxTop);
+  // a launch has less than 2^32 threads
+  if (n_tokens * stq::combine_col_blocks(d) >= (int64_t{1} << 24))
+    return fail(STQ_E_SHAPE, "%s: too many tokens of this width for one call", who);
+  return STQ_OK;
+}
+
+}  // namespace
+
+stq_status stq_combine_rows(const void* z, int z_dtype, int64_t z_row_stride, int64_t n_rows, const int32_t* pair_row,
+                            const float* pair_weight, int64_t n_tokens, int64_t top_k, int64_t d, void* y, int y_dtype,
+                            int64_t y_row_stride, stq_stream_t stream) {
+  const char* who = "stq_combine_rows";
+  stq_status st = combine_check(n_tokens, top_k, d, n_rows, who);
+  if (st != STQ_OK) return st;
+  if (!known_type(z_dtype) || !known_type(y_dtype)) return fail(STQ_E_ARG, "%s: unknown type of z or y", who);
+  if (n_tokens == 0) return ok();
+  if ((n_rows > 0 && !z) || !pair_row || !y) return fail(STQ_E_ARG, "%s: null pointer", who);
+  st = matrix_check("z", z, z_dtype, z_row_stride, n_rows, d, who);
+  if (st == STQ_OK) st = matrix_check("y", y, y_dtype, y_row_stride, n_tokens, d, who);
+  if (st != STQ_OK) return st;
+  if (!aligned(pair_row, 4) || !aligned(pair_weight, 4)) return fail(STQ_E_ALIGN, "%s: pairs not 4-byte aligned", who);
+  const stq::CombineArgs a{z, z_dtype == STQ_X_BF16, z_row_stride, n_rows, pair_row, pair_weight, n_tokens,
+                           static_cast<int>(top_k), d, y, y_dtype == STQ_X_BF16, y_row_stride};
+  hipError_t e = stq::launch_combine_rows(a, reinterpret_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "stq_combine_rows launch");
+  return ok();
+}
+
+stq_status stq_combine_rows_backward(const void* dy, int dy_dtype, int64_t dy_row_stride, const void* z, int z_dtype,
+                                     int64_t z_row_stride, int64_t n_rows, const int32_t* pair_row,
+                                     const float* pair_weight, int64_t n_tokens, int64_t top_k, int64_t d, void* dz,
+                                     int dz_dtype, int64_t dz_row_stride, float* dweight, stq_stream_t stream) {
+  const char* who = "stq_combine_rows_backward";
+  stq_status st = combine_check(n_tokens, top_k, d, n_rows, who);
+  if (st != STQ_OK) return st;
+  if (!known_type(dy_dtype) || (dweight && !known_type(z_dtype)) || (dz && !known_type(dz_dtype)))
+    return fail(STQ_E_ARG, "%s: unknown type of dy, z or dz", who);
+  if (n_tokens == 0 || (!dz && !dweight)) return ok();
+  if (!dy || !pair_row) return fail(STQ_E_ARG, "%s: null pointer", who);
+  if (dweight && n_rows > 0 && !z) return fail(STQ_E_ARG, "%s: dweight needs z", who);
+  st = matrix_check("dy", dy, dy_dtype, dy_row_stride, n_tokens, d, who);
+  if (st == STQ_OK && dweight) st = matrix_check("z", z, z_dtype, z_row_stride, n_rows, d, who);
+  if (st == STQ_OK && dz) st = matrix_check("dz", dz, dz_dtype, dz_row_stride, n_rows, d, who);
+  if (st != STQ_OK) return st;
+  if (!aligned(pair_row, 4) || !aligned(pair_weight, 4) || !aligned(dweight, 4)) return fail(STQ_E_ALIGN, "%s: pairs or dweight not 4-byte aligned", who);
+  const stq::CombineBwdArgs a{dy, dy_dtype == STQ_X_BF16, dy_row_stride, dweight ? z : nullptr, z_dtype == STQ_X_BF16,
+                              z_row_stride, n_rows, pair_row, pair_weight, n_tokens, static_cast<int>(top_k), d, dz,
+                              dz_dtype == STQ_X_BF16, dz_row_stride, dweight};
+  hipError_t e = stq::launch_combine_rows_bwd(a, reinterpret_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "stq_combine_rows_backward launch");
+  return ok();
+}
+
 stq_status stq_stream_read_probe(const void* buf, int64_t bytes, uint32_t* sink, stq_stream_t stream) {
   if (bytes < 0 || bytes % 16) return fail(STQ_E_ARG, "stq_stream_read_probe: bytes must be a non-negative multiple of 16");
   if (bytes == 0) return ok();

@@ -218,6 +218,129 @@ struct LogprobsBwdArgs {
 int64_t logprobs_bwd_parts(const LogprobsBwdArgs& a);  // workgroups per row, at most
 hipError_t launch_logprobs_bwd(const LogprobsBwdArgs& a, hipStream_t s);
 
+// Residual addition, root-mean-square norm and 8-bit rows; its gradients
+struct NormArgs {
+  const void* x;
+  int x_bf16;
+  int64_t x_stride;     // elements, like every stride here but q_stride
+  const void* res;      // NULL: h is x
+  int res_bf16;
+  int64_t res_stride;
+  void* h;              // the residual's type
+  int64_t h_stride;
+  const float* weight;
+  float eps;
+  int64_t rows, d;
+  float* rstd;          // may be NULL
+  int8_t* q;            // may be NULL
+  int64_t q_stride;     // bytes
+  float* scale;         // with q
+  uint16_t* y;          // may be NULL
+  int64_t y_stride;
+};
+hipError_t launch_norm(const NormArgs& a, hipStream_t s);
+
+struct NormBwdArgs {
+  const void* h;
+  int h_bf16;           // h, dh and dx
+  int64_t h_stride;
+  const float* weight;
+  const float* rstd;
+  const void* dy;
+  int dy_bf16;
+  int64_t dy_stride;
+  const void* dh;       // may be NULL
+  int64_t dh_stride;
+  void* dx;             // may be NULL
+  int64_t dx_stride;
+  float* dw;            // may be NULL
+  int64_t rows, d;
+};
+// `part`: norm_bwd_parts(rows, cus) rows of d floats, with dw
+int norm_bwd_parts(int64_t rows, int cus);
+hipError_t launch_norm_bwd(const NormBwdArgs& a, float* part, int cus, hipStream_t s);
+
+// Top-k routing, the rows sorted by expert and the balance loss; its gradient
+constexpr int kRouteMaxExperts = 1024;
+constexpr int kRouteMaxTop = 32;
+struct RouteArgs {
+  const void* logits;
+  int bf16;
+  int64_t stride;
+  int64_t tokens;
+  int experts, top_k;
+  int renorm;
+  int32_t* pair_expert;
+  float* pair_weight;
+  int32_t* counts;
+  int32_t* offsets;
+  int32_t* pair_row;
+  int32_t* row_token;
+  float* row_weight;
+  float* balance;
+};
+// Workspace (tokens of more than one chunk): per expert and chunk the count
+// (then the rows before it) at 0 and the summed probabilities at `prob`, per
+// expert the summed probabilities at `prob_total`
+struct RouteLayout {
+  int64_t chunks, prob, prob_total, bytes;
+};
+RouteLayout route_layout(int64_t tokens, int64_t experts);
+hipError_t launch_route(const RouteArgs& a, void* ws, hipStream_t s);
+
+struct RouteBwdArgs {
+  const void* logits;
+  int bf16;
+  int64_t stride;
+  int64_t tokens;
+  int experts, top_k;
+  int renorm;
+  const int32_t* pair_expert;
+  const int32_t* counts;      // with g_balance
+  const float* g_weight;      // may be NULL
+  const int32_t* pair_row;    // g_weight is in the order of the sorted rows; NULL: of the pairs
+  const float* g_balance;     // may be NULL
+  void* d_logits;
+  int64_t d_stride;
+};
+hipError_t launch_route_bwd(const RouteBwdArgs& a, hipStream_t s);
+
+// A token's rows added up with its weights; the gradients of that
+struct CombineArgs {
+  const void* z;
+  int z_bf16;
+  int64_t z_stride, n_rows;
+  const int32_t* pair_row;
+  const float* weight;  // NULL: ones
+  int64_t tokens;
+  int top_k;
+  int64_t d;
+  void* y;
+  int y_bf16;
+  int64_t y_stride;
+};
+int64_t combine_col_blocks(int64_t d);  // workgroups a token
+hipError_t launch_combine_rows(const CombineArgs& a, hipStream_t s);
+
+struct CombineBwdArgs {
+  const void* dy;
+  int dy_bf16;
+  int64_t dy_stride;
+  const void* z;        // read with dw
+  int z_bf16;
+  int64_t z_stride, n_rows;
+  const int32_t* pair_row;
+  const float* weight;
+  int64_t tokens;
+  int top_k;
+  int64_t d;
+  void* dz;             // may be NULL
+  int dz_bf16;
+  int64_t dz_stride;
+  float* dw;            // may be NULL
+};
+hipError_t launch_combine_rows_bwd(const CombineBwdArgs& a, hipStream_t s);
+
 // Streaming-read reference (measurement only): reads `bytes` bytes of `buf`
 hipError_t launch_stream_read(const void* buf, int64_t bytes, uint32_t* sink, hipStream_t s);
 

@@ -1,0 +1,178 @@
+// Device-side helpers of the row operators: rows of fp32 or bf16 elements read
+// and written eight at a time, reductions inside a wavefront, and the rounding
+// of scaled values to 8-bit integers.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace stq {
+
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+
+struct bf16_t {
+  uint16_t bits;
+};
+
+__device__ __forceinline__ uint32_t bf16_round(float f) {
+  return __builtin_bit_cast(uint16_t, static_cast<__bf16>(f));
+}
+__device__ __forceinline__ float widen(float v) { return v; }
+__device__ __forceinline__ float widen(bf16_t v) { return __builtin_bit_cast(float, static_cast<uint32_t>(v.bits) << 16); }
+template <typename T>
+__device__ __forceinline__ T narrow(float v);
+template <>
+__device__ __forceinline__ float narrow<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ bf16_t narrow<bf16_t>(float v) { return bf16_t{static_cast<uint16_t>(bf16_round(v))}; }
+
+// Eight elements as they lie in memory
+template <typename T>
+struct Raw8 {
+  static constexpr int kW = sizeof(T) / 2;  // 16-byte words
+  u32x4_t w[kW];
+};
+
+// Elements c..c+7 of a row of n; columns past n read as 0.  kVec: rows start
+// on 16 bytes.
+template <typename T, bool kVec>
+__device__ __forceinline__ Raw8<T> load8(const T* row, int64_t c, int64_t n) {
+  Raw8<T> r;
+  if (kVec && c + 8 <= n) {
+#pragma unroll
+    for (int i = 0; i < Raw8<T>::kW; ++i) r.w[i] = *reinterpret_cast<const u32x4_t*>(reinterpret_cast<const char*>(row + c) + 16 * i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < Raw8<T>::kW; ++i) r.w[i] = u32x4_t{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (c + i >= n) continue;
+      if constexpr (sizeof(T) == 4) r.w[i >> 2][i & 3] = __builtin_bit_cast(uint32_t, row[c + i]);
+      else r.w[0][i >> 1] |= static_cast<uint32_t>(row[c + i].bits) << (16 * (i & 1));
+    }
+  }
+  return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack8(const Raw8<T>& r, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (sizeof(T) == 4) v[i] = __builtin_bit_cast(float, static_cast<uint32_t>(r.w[i >> 2][i & 3]));
+    else v[i] = __builtin_bit_cast(float, (i & 1) ? (r.w[0][i >> 1] & 0xFFFF0000u) : (r.w[0][i >> 1] << 16));
+  }
+}
+
+template <typename T, bool kVec>
+__device__ __forceinline__ void load8f(const T* row, int64_t c, int64_t n, float (&v)[8]) {
+  const Raw8<T> r = load8<T, kVec>(row, c, n);
+  unpack8<T>(r, v);
+}
+
+template <typename T>
+__device__ __forceinline__ Raw8<T> pack8(const float (&v)[8]) {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (sizeof(T) == 4) r.w[i >> 2][i & 3] = __builtin_bit_cast(uint32_t, v[i]);
+    else if ((i & 1) == 0) r.w[0][i >> 1] = bf16_round(v[i]) | bf16_round(v[i + 1]) << 16;
+  }
+  return r;
+}
+
+template <typename T, bool kVec>
+__device__ __forceinline__ void store8(T* row, int64_t c, int64_t n, const Raw8<T>& r) {
+  if (kVec && c + 8 <= n) {
+#pragma unroll
+    for (int i = 0; i < Raw8<T>::kW; ++i) *reinterpret_cast<u32x4_t*>(reinterpret_cast<char*>(row + c) + 16 * i) = r.w[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (c + i >= n) continue;
+      if constexpr (sizeof(T) == 4) row[c + i] = __builtin_bit_cast(float, static_cast<uint32_t>(r.w[i >> 2][i & 3]));
+      else row[c + i] = bf16_t{static_cast<uint16_t>(r.w[0][i >> 1] >> (16 * (i & 1)))};
+    }
+  }
+}
+
+// Reductions by DPP moves.  Inside 16 lanes by rotation: every lane gets the
+// result, and the same bits, because each step adds the two halves of a set
+// that both partners then hold.
+template <int kCtrl>
+__device__ __forceinline__ uint32_t dpp_move(uint32_t v) {
+  return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), kCtrl, 0xF, 0xF, false));
+}
+template <int kCtrl>
+__device__ __forceinline__ float dpp_move(float v) {
+  return __builtin_bit_cast(float, dpp_move<kCtrl>(__builtin_bit_cast(uint32_t, v)));
+}
+template <typename T, typename F>
+__device__ __forceinline__ T reduce16(T v, F f) {
+  v = f(v, dpp_move<0x128>(v));  // row_ror:8, 4, 2, 1
+  v = f(v, dpp_move<0x124>(v));
+  v = f(v, dpp_move<0x122>(v));
+  v = f(v, dpp_move<0x121>(v));
+  return v;
+}
+template <typename T, typename F>
+__device__ __forceinline__ T reduce64(T v, F f) {
+  v = reduce16(v, f);
+  v = f(v, __shfl_xor(v, 16));
+  return f(v, __shfl_xor(v, 32));
+}
+__device__ __forceinline__ float sum16(float v) {
+  return reduce16(v, [](float a, float b) { return a + b; });
+}
+__device__ __forceinline__ float sum64(float v) {
+  return reduce64(v, [](float a, float b) { return a + b; });
+}
+__device__ __forceinline__ uint32_t max64(uint32_t v) {
+  return reduce64(v, [](uint32_t a, uint32_t b) { return max(a, b); });
+}
+
+// The nearest integer to v / scale for N values (a multiple of 4), packed; inv
+// is 1 / scale.  In fp32, adding 1.5 * 2^23 to v * (1 / scale) in one fused
+// step rounds it to an integer, halves to even, whose two's complement is the
+// sum's low byte.  The quotient is within 127 * 2^-23 of the exact one, so
+// this decides wherever it is farther than 2^-15 from a half; one lane in a
+// thousand has a value that close and redoes its N in fp64, where the
+// remainder v - q scale is exact.  (No value exceeds 127 there: |v| / scale <=
+// 127 (1 + 2^-24).)  fast: the scale is far above where the reciprocal or the
+// products leave the normal range.
+template <int N>
+__device__ __forceinline__ void quantize(const float (&v)[N], float scale, float inv, bool fast, uint32_t (&o)[N / 4]) {
+  constexpr float kMagic = 12582912.0f;
+  float far = 0.0f;
+  uint32_t b[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float s = fmaf(v[i], inv, kMagic);
+    far = fmaxf(far, fabsf(fmaf(v[i], inv, kMagic - s)));
+    b[i] = __builtin_bit_cast(uint32_t, s);
+  }
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) {
+    const uint32_t lo = __builtin_amdgcn_perm(b[4 * i + 1], b[4 * i], 0x0C0C0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(b[4 * i + 3], b[4 * i + 2], 0x04000C0Cu);
+    o[i] = lo | hi;
+  }
+  if (fast && far < 0.5f - 0x1p-15f) return;
+  const double sd = static_cast<double>(scale), invd = 1.0 / sd, half = 0.5 * sd;
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) o[i] = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const double x = static_cast<double>(v[i]);
+    double q = rint(x * invd);
+    const double rem = fma(-q, sd, x);
+    // the product can land on the wrong side only next to a half
+    const double other = q + (rem > 0.0 ? 1.0 : -1.0);
+    if (fabs(rem) > half || (fabs(rem) == half && (static_cast<int>(q) & 1))) q = other;
+    const int qi = max(-127, min(127, static_cast<int>(q)));
+    o[i >> 2] |= (static_cast<uint32_t>(qi) & 0xFFu) << (8 * (i & 3));
+  }
+}
+
+}  // namespace stq

@@ -1,0 +1,152 @@
+"""Host-side checks of the norm, the routing and the combination of rows: bad
+arguments are refused with a status and a message before any GPU call, empty
+work is fine without one, and the workspace queries agree with the calls.  No
+kernel runs."""
+import ctypes
+import os
+
+import pytest
+
+FAKE = 0x100000  # never dereferenced: every call below fails validation first
+F32, BF16 = 0, 1
+
+
+@pytest.fixture(scope="module")
+def L():
+    import sparse_ternary_bit_amd as stq
+    if not os.path.exists(stq.lib_path()):
+        from sparse_ternary_bit_amd import build
+        build.build(verbose=False)
+    return stq.lib()
+
+
+def _refused(L, name, args, kw, status):
+    a = dict(args)
+    a.update(kw)
+    assert getattr(L, name)(*a.values(), None) == status
+    assert L.stq_last_error().decode().startswith(name)
+
+
+def _done(L, name, args, kw):
+    a = dict(args)
+    a.update(kw)
+    assert getattr(L, name)(*a.values(), None) == 0
+
+
+NORM = dict(x=FAKE, xd=BF16, xs=100, r=FAKE, rd=F32, rs=100, h=FAKE + 4096, hs=100, w=FAKE, eps=1e-6, n=4, d=100, rstd=FAKE, q=FAKE,
+            qs=112, sc=FAKE, y=FAKE, ys=100)
+
+
+@pytest.mark.parametrize("kw, status", [
+    (dict(n=-1), 1), (dict(d=0), 2), (dict(d=(1 << 26) + 1), 2), (dict(n=(1 << 22) + 1), 2), (dict(xd=2), 1), (dict(rd=5), 1),
+    (dict(eps=-1.0), 1), (dict(eps=float("nan")), 1), (dict(q=None), 1), (dict(sc=None), 1), (dict(x=None), 1), (dict(w=None), 1),
+    (dict(h=None), 1), (dict(qs=96), 2), (dict(qs=120), 3), (dict(q=FAKE + 8), 3), (dict(w=FAKE + 2), 3), (dict(rstd=FAKE + 1), 3),
+    (dict(sc=FAKE + 2), 3), (dict(xs=99), 2), (dict(rs=99), 2), (dict(hs=99), 2), (dict(ys=99), 2), (dict(xs=1 << 62), 2),
+    (dict(x=FAKE + 1), 3), (dict(r=FAKE + 2), 3), (dict(h=FAKE + 2), 3), (dict(y=FAKE + 1), 3), (dict(h=FAKE, hs=104), 1),
+    (dict(h=FAKE, r=FAKE + 8192), 1), (dict(h=FAKE, r=FAKE + 8192, xd=F32, xs=104), 1),
+])
+def test_norm_refusals(L, kw, status):
+    _refused(L, "stq_rmsnorm_rows", NORM, kw, status)
+
+
+def test_norm_nothing_to_do(L):
+    _done(L, "stq_rmsnorm_rows", NORM, dict(n=0, x=None, r=None, h=None, w=None, q=None, sc=None, y=None, rstd=None))
+
+
+NORM_BWD = dict(h=FAKE, hd=BF16, hs=100, w=FAKE, rstd=FAKE, dy=FAKE, yd=F32, ys=100, dh=FAKE, dhs=100, dx=FAKE + 4096, dxs=100,
+                dw=FAKE, n=4, d=100, ws=FAKE, wsb=1 << 40)
+
+
+@pytest.mark.parametrize("kw, status", [
+    (dict(n=-1), 1), (dict(d=0), 2), (dict(hd=3), 1), (dict(yd=3), 1), (dict(h=None), 1), (dict(w=None), 1), (dict(rstd=None), 1),
+    (dict(dy=None), 1), (dict(w=FAKE + 2), 3), (dict(dw=FAKE + 2), 3), (dict(hs=99), 2), (dict(ys=99), 2), (dict(dhs=99), 2),
+    (dict(dxs=99), 2), (dict(dh=FAKE + 1), 3), (dict(dx=FAKE + 1), 3), (dict(dy=FAKE + 2), 3), (dict(wsb=-1), 1),
+    (dict(dx=FAKE + 64, dh=FAKE + 64, dxs=104), 1), (dict(dx=FAKE), 1), (dict(dx=FAKE, dh=None, hd=F32, dxs=104), 1),
+])
+def test_norm_backward_refusals(L, kw, status):
+    _refused(L, "stq_rmsnorm_rows_backward", NORM_BWD, kw, status)
+
+
+def test_norm_backward_workspace(L):
+    need = ctypes.c_int64()
+    query = L.stq_rmsnorm_rows_backward_workspace
+    assert query(4, 100, 1, 256, ctypes.byref(need)) == 0 and need.value == 4 * 100 * 4
+    assert query(5000, 7168, 1, 256, ctypes.byref(need)) == 0 and need.value == 512 * 7168 * 4
+    for args in [(4, 100, 0), (0, 100, 1)]:
+        assert query(*args, 256, ctypes.byref(need)) == 0 and need.value == 0
+    assert query(4, 0, 1, 256, ctypes.byref(need)) == 2
+    assert query(4, 100, 1, -1, ctypes.byref(need)) == 1
+    assert query(4, 100, 1, 256, None) == 1
+    none = dict(h=None, w=None, rstd=None, dy=None, dh=None, ws=None, wsb=0)
+    _done(L, "stq_rmsnorm_rows_backward", NORM_BWD, dict(none, dx=None, dw=None))
+    _done(L, "stq_rmsnorm_rows_backward", NORM_BWD, dict(none, n=0, dw=None))
+
+
+ROUTE = dict(x=FAKE, xd=F32, xs=64, n=100, e=64, k=4, renorm=1, pe=FAKE, pw=FAKE, counts=FAKE, off=FAKE, row=FAKE, tok=FAKE, rw=FAKE,
+             bal=FAKE, ws=FAKE, wsb=1 << 40)
+
+
+@pytest.mark.parametrize("kw, status", [
+    (dict(n=-1), 1), (dict(e=0), 2), (dict(e=1025, xs=1025), 2), (dict(k=0), 2), (dict(k=33), 2), (dict(k=5, e=4), 2),
+    (dict(n=(1 << 22) + 1), 2), (dict(xd=2), 1), (dict(x=None), 1), (dict(pe=None), 1), (dict(pw=None), 1), (dict(counts=None), 1),
+    (dict(off=None), 1), (dict(row=None), 1), (dict(tok=None), 1), (dict(rw=None), 1), (dict(bal=None), 1), (dict(xs=63), 2),
+    (dict(xs=1 << 62), 2), (dict(x=FAKE + 2), 3), (dict(xd=BF16, x=FAKE + 1), 3), (dict(pe=FAKE + 1), 3), (dict(bal=FAKE + 2), 3),
+    (dict(ws=None), 1), (dict(wsb=8), 1), (dict(wsb=-1), 1), (dict(ws=FAKE + 16), 3),
+])
+def test_route_refusals(L, kw, status):
+    _refused(L, "stq_route_tokens", ROUTE, kw, status)
+
+
+def test_route_workspace(L):
+    need = ctypes.c_int64()
+    query = L.stq_route_tokens_workspace
+    for n in (0, 1, 64):
+        assert query(n, 256, 8, ctypes.byref(need)) == 0 and need.value == 0
+    assert query(65, 256, 8, ctypes.byref(need)) == 0 and need.value == 2 * 2 * 256 * 4 + 256 * 4
+    assert query(65, 0, 8, ctypes.byref(need)) == 2
+    assert query(65, 256, 40, ctypes.byref(need)) == 2
+    assert query(-1, 256, 8, ctypes.byref(need)) == 1
+    assert query(65, 256, 8, None) == 1
+
+
+ROUTE_BWD = dict(x=FAKE, xd=F32, xs=64, n=100, e=64, k=4, renorm=1, pe=FAKE, counts=FAKE, gw=FAKE, row=FAKE, gb=FAKE, d=FAKE + 65536, ds=64)
+
+
+@pytest.mark.parametrize("kw, status", [
+    (dict(n=-1), 1), (dict(e=0), 2), (dict(k=33), 2), (dict(xd=2), 1), (dict(x=None), 1), (dict(d=None), 1), (dict(pe=None), 1),
+    (dict(counts=None), 1), (dict(xs=63), 2), (dict(ds=63), 2), (dict(d=FAKE, ds=65), 1), (dict(d=FAKE + 2), 3), (dict(gw=FAKE + 2), 3),
+    (dict(gb=FAKE + 1), 3), (dict(row=FAKE + 3), 3),
+])
+def test_route_backward_refusals(L, kw, status):
+    _refused(L, "stq_route_tokens_backward", ROUTE_BWD, kw, status)
+
+
+COMBINE = dict(z=FAKE, zd=F32, zs=100, rows=80, row=FAKE, w=FAKE, n=10, k=8, d=100, y=FAKE, yd=BF16, ys=100)
+
+
+@pytest.mark.parametrize("kw, status", [
+    (dict(n=-1), 1), (dict(rows=-1), 1), (dict(rows=1 << 31), 2), (dict(d=0), 2), (dict(k=0), 2), (dict(k=33), 2), (dict(zd=2), 1),
+    (dict(yd=2), 1), (dict(z=None), 1), (dict(row=None), 1), (dict(y=None), 1), (dict(zs=99), 2), (dict(ys=99), 2), (dict(zs=1 << 60), 2),
+    (dict(z=FAKE + 2), 3), (dict(y=FAKE + 1), 3), (dict(row=FAKE + 1), 3), (dict(w=FAKE + 2), 3),
+    (dict(n=1 << 22, d=7168, zs=7168, ys=7168), 2),
+])
+def test_combine_refusals(L, kw, status):
+    _refused(L, "stq_combine_rows", COMBINE, kw, status)
+
+
+COMBINE_BWD = dict(dy=FAKE, yd=F32, ys=100, z=FAKE, zd=F32, zs=100, rows=80, row=FAKE, w=FAKE, n=10, k=8, d=100, dz=FAKE, dzd=BF16,
+                   dzs=100, dw=FAKE)
+
+
+@pytest.mark.parametrize("kw, status", [
+    (dict(n=-1), 1), (dict(k=0), 2), (dict(yd=2), 1), (dict(zd=2), 1), (dict(dzd=2), 1), (dict(dy=None), 1), (dict(row=None), 1),
+    (dict(z=None), 1), (dict(ys=99), 2), (dict(zs=99), 2), (dict(dzs=99), 2), (dict(dw=FAKE + 2), 3), (dict(dz=FAKE + 1), 3),
+])
+def test_combine_backward_refusals(L, kw, status):
+    _refused(L, "stq_combine_rows_backward", COMBINE_BWD, kw, status)
+
+
+def test_combine_nothing_to_do(L):
+    _done(L, "stq_combine_rows", COMBINE, dict(n=0, z=None, row=None, y=None))
+    _done(L, "stq_combine_rows_backward", COMBINE_BWD, dict(n=0, z=None, row=None, dy=None))
+    _done(L, "stq_combine_rows_backward", COMBINE_BWD, dict(dz=None, dw=None, dy=None, row=None, z=None))
