@@ -44,7 +44,8 @@
  *   - the library allocates no device memory and keeps no device state: the
  *     entry points that need scratch memory (stq_gemv, stq_moe_ffn_decode,
  *     stq_layer_errors, stq_grouped_swiglu, stq_grouped_swiglu_backward,
- *     stq_token_logprobs, stq_rmsnorm_rows_backward, stq_route_tokens) take a caller-owned `workspace` of `workspace_bytes`
+ *     stq_token_logprobs, stq_rmsnorm_rows_backward, stq_route_tokens,
+ *     stq_head_cross_entropy, stq_head_cross_entropy_backward) take a caller-owned `workspace` of `workspace_bytes`
  *     bytes, 256-byte aligned, whose required size a host-only query gives
  *     for the same shapes (stq_gemv_plan, and the call's name with _workspace
  *     behind it for the others: stq_moe_ffn_workspace for the FFN); a NULL or
@@ -79,6 +80,7 @@ typedef enum {
 
 enum { STQ_ENC_WLS = 0, STQ_ENC_AMAX = 1 };
 enum { STQ_X_F32 = 0, STQ_X_BF16 = 1 };
+enum { STQ_X_I8 = 2 }; /* 8-bit rows with scales: the output head's operands only */
 
 /* Bytes of one packed row of k weights: k/256*42, or -1 if k is not a
  * positive multiple of 256. Pure host function. */
@@ -642,6 +644,75 @@ stq_status stq_combine_rows_backward(const void* dy, int dy_dtype, int64_t dy_ro
                                      int64_t z_row_stride, int64_t n_rows, const int32_t* pair_row,
                                      const float* pair_weight, int64_t n_tokens, int64_t top_k, int64_t d, void* dz,
                                      int dz_dtype, int64_t dz_row_stride, float* dweight, stq_stream_t stream);
+
+/* Softmax cross entropy of an output head without keeping the logits, which for
+ * a large vocabulary are many times its operands:
+ *     l_i = x . w_i  (bf16), or (x . w_i) * x_scale * w_scale_i  (8-bit rows)
+ *     lse = log sum_i exp(l_i)        loss = lse - l_target
+ *   x         [n_rows, k] bf16 bits (x_dtype STQ_X_BF16) or int8 with x_scale
+ *             fp32 [n_rows] (STQ_X_I8, as stq_q8_quantize_rows and
+ *             stq_rmsnorm_rows write them)
+ *   w         [vocab, k] of x's type, for int8 with w_scale fp32 [vocab]
+ *             both 16-byte aligned with row strides (elements) of whole 16-byte
+ *             units, at least k and at most 2^23 bytes; a row's bytes behind k,
+ *             up to a whole 16-byte unit, may be read and count for nothing
+ *   targets   int32 [n_rows]; a negative one leaves its row out (loss 0), one
+ *             past the vocabulary gives loss NaN
+ *   loss, lse fp32 [n_rows]
+ *   workspace, workspace_bytes  at least what stq_head_cross_entropy_workspace
+ *             reports
+ * bf16 products are exact and their sums fp32; integer sums are exact and scaled
+ * in fp32, as in stq_q8_matmul.  A row whose logits hold a NaN or a +inf has lse
+ * and loss NaN, one whose logits are all -inf lse -inf and loss NaN.  The order
+ * of every sum is fixed for a device: repeated calls give identical bits.
+ * 1 <= k <= 131071, 1 <= vocab <= 2^26, n_rows at most 2^20, n_rows * vocab at
+ * most 2^38. */
+stq_status stq_head_cross_entropy(const void* x, int x_dtype, int64_t x_row_stride, const float* x_scale, const void* w,
+                                  int64_t w_row_stride, const float* w_scale, int64_t n_rows, int64_t vocab, int64_t k,
+                                  const int32_t* targets, float* loss, float* lse, void* workspace,
+                                  int64_t workspace_bytes, stq_stream_t stream);
+
+/* Workspace bytes stq_head_cross_entropy needs for these shapes on a device with
+ * n_cus compute units (0: the current device's); host only, same checks and
+ * errors as the call.  workspace_bytes is a HOST pointer. */
+stq_status stq_head_cross_entropy_workspace(int x_dtype, int64_t n_rows, int64_t vocab, int64_t k, int32_t n_cus,
+                                            int64_t* workspace_bytes);
+
+/* Its gradients, for a gradient g at the losses; the logits are formed again, a
+ * piece of the vocabulary at a time:
+ *     dl_i = g (exp(l_i - lse) - 1[i = target])
+ *     dx = sum_i dl_i w_i  (8-bit rows: dl_i w_scale_i w_i, the gradient at
+ *          x * x_scale, the rounding to 8 bits taken as the identity)
+ *     dw_i = sum over rows of dl_i x       (bf16 only)
+ *   lse        fp32 [n_rows], what the forward call gave
+ *   grad_loss  fp32 [n_rows]; not read where a row is left out
+ *   dx         bf16 bits [n_rows, k], rows dx_row_stride elements apart, or NULL
+ *              (not wanted)
+ *   dw         bf16 bits [vocab, k], rows dw_row_stride elements apart, or NULL;
+ *              zeros where no row is left
+ *   workspace, workspace_bytes  at least what
+ *              stq_head_cross_entropy_backward_workspace reports
+ * The other arguments and limits are as above.  A row that is left out, whose
+ * target lies past the vocabulary or whose lse is -inf has no gradient, whatever
+ * x holds there; one with lse NaN gives NaN.  dl is formed in fp32 and rounded to
+ * bf16 for the two products (with 8-bit rows after its w_scale, so that the
+ * integers, which bf16 holds exactly, enter as they are): dx and dw err by about
+ * 0.0017 of their norm from that and as much from their own rounding.  Sums are
+ * fp32 in an order that is fixed for a device.  dx and dw are rounded from them
+ * once and may not overlap the operands; rows that all start on 16 bytes are
+ * written faster. */
+stq_status stq_head_cross_entropy_backward(const void* x, int x_dtype, int64_t x_row_stride, const float* x_scale,
+                                           const void* w, int64_t w_row_stride, const float* w_scale, int64_t n_rows,
+                                           int64_t vocab, int64_t k, const int32_t* targets, const float* lse,
+                                           const float* grad_loss, uint16_t* dx, int64_t dx_row_stride, uint16_t* dw,
+                                           int64_t dw_row_stride, void* workspace, int64_t workspace_bytes,
+                                           stq_stream_t stream);
+
+/* Workspace bytes stq_head_cross_entropy_backward needs for these shapes and the
+ * outputs wanted (0 or 1 each) on a device with n_cus compute units (0: the
+ * current device's); host only.  workspace_bytes is a HOST pointer. */
+stq_status stq_head_cross_entropy_backward_workspace(int x_dtype, int64_t n_rows, int64_t vocab, int64_t k, int want_dx,
+                                                     int want_dw, int32_t n_cus, int64_t* workspace_bytes);
 
 /* Measurement helper, not part of the method: reads `bytes` bytes of the
  * device buffer `buf` once with 16-byte loads, the streaming-read rate this

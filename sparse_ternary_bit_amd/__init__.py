@@ -24,7 +24,8 @@ __all__ = [
     "q8_quantize_rows", "q8_matmul", "token_logprobs",
     "token_logprobs_workspace", "token_logprobs_backward", "Norm", "rmsnorm_rows", "rmsnorm_rows_backward",
     "rmsnorm_rows_backward_workspace", "Routing", "route_tokens", "route_tokens_workspace", "route_tokens_backward",
-    "combine_rows", "combine_rows_backward", "layer_errors", "layer_errors_workspace", "q2_roundtrip", "greedy_allocation",
+    "combine_rows", "combine_rows_backward", "head_cross_entropy", "head_cross_entropy_workspace",
+    "head_cross_entropy_backward", "head_cross_entropy_backward_workspace", "layer_errors", "layer_errors_workspace", "q2_roundtrip", "greedy_allocation",
     "stream_read_probe", "mfma_loop_probe", "lds_read_probe", "MFMA_PROBE_FLOP_PER_ROUND",
     "LDS_PROBE_READS_PER_ROUND",
 ]
@@ -32,7 +33,7 @@ __all__ = [
 QK = 256
 BLOCK_BYTES = 42
 ENC_WLS, ENC_AMAX = 0, 1
-X_F32, X_BF16 = 0, 1
+X_F32, X_BF16, X_I8 = 0, 1, 2
 # work of one round of the measurement probes (include/stq.h)
 MFMA_PROBE_FLOP_PER_ROUND = 2147483648.0
 LDS_PROBE_READS_PER_ROUND = 131072
@@ -152,6 +153,18 @@ def lib() -> ctypes.CDLL:
     L.stq_combine_rows_backward.argtypes = [_c_vp, _c_int, _c_i64, _c_vp, _c_int, _c_i64, _c_i64, _c_vp, _c_vp, _c_i64,
                                             _c_i64, _c_i64, _c_vp, _c_int, _c_i64, _c_vp, _c_vp]
     L.stq_combine_rows_backward.restype = _c_int
+    L.stq_head_cross_entropy.argtypes = [_c_vp, _c_int, _c_i64, _c_vp, _c_vp, _c_i64, _c_vp, _c_i64, _c_i64, _c_i64, _c_vp,
+                                         _c_vp, _c_vp, _c_vp, _c_i64, _c_vp]
+    L.stq_head_cross_entropy.restype = _c_int
+    L.stq_head_cross_entropy_workspace.argtypes = [_c_int, _c_i64, _c_i64, _c_i64, ctypes.c_int32, ctypes.POINTER(_c_i64)]
+    L.stq_head_cross_entropy_workspace.restype = _c_int
+    L.stq_head_cross_entropy_backward.argtypes = [_c_vp, _c_int, _c_i64, _c_vp, _c_vp, _c_i64, _c_vp, _c_i64, _c_i64,
+                                                  _c_i64, _c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_vp, _c_i64, _c_vp, _c_i64,
+                                                  _c_vp]
+    L.stq_head_cross_entropy_backward.restype = _c_int
+    L.stq_head_cross_entropy_backward_workspace.argtypes = [_c_int, _c_i64, _c_i64, _c_i64, _c_int, _c_int, ctypes.c_int32,
+                                                            ctypes.POINTER(_c_i64)]
+    L.stq_head_cross_entropy_backward_workspace.restype = _c_int
     L.stq_stream_read_probe.argtypes = [_c_vp, _c_i64, _c_vp, _c_vp]
     L.stq_stream_read_probe.restype = _c_int
     L.stq_mfma_loop_probe.argtypes = [_c_i64, _c_vp, _c_vp]
@@ -1045,6 +1058,139 @@ def combine_rows_backward(dy: torch.Tensor, pair_row: torch.Tensor, top_k: int, 
     _call(dev, "stq_combine_rows_backward", dy.data_ptr(), _kind(dy), ys, z.data_ptr(), _kind(z), zs, rows,
           pair_row.data_ptr(), _ptr(weight), n, top_k, d, _ptr(dz), _kind(dz), dzs, _ptr(dweight))
     return dz, dweight
+
+
+def head_cross_entropy_workspace(x_dtype: int, n_rows: int, vocab: int, k: int, n_cus: int = 0) -> int:
+    """Workspace bytes head_cross_entropy needs for these shapes (x_dtype X_BF16 or X_I8) on n_cus compute units (0:
+    the current device's); host only."""
+    wb = ctypes.c_int64()
+    _check("stq_head_cross_entropy_workspace",
+           lib().stq_head_cross_entropy_workspace(int(x_dtype), int(n_rows), int(vocab), int(k), int(n_cus),
+                                                  ctypes.byref(wb)))
+    return wb.value
+
+
+@functools.lru_cache(maxsize=256)
+def _head_need(x_dtype: int, n_rows: int, vocab: int, k: int, n_cus: int) -> int:
+    return head_cross_entropy_workspace(x_dtype, n_rows, vocab, k, n_cus)
+
+
+def _unit_stride(name: str, t: torch.Tensor) -> int:
+    """Row stride in elements of bf16 or int8 rows, which own their bytes up to the next multiple of 16."""
+    if t.dtype == torch.int8:
+        return _q8_stride(name, t)
+    stride = _rows(name, t, torch.bfloat16)
+    n, k = t.shape
+    kp = (k + 7) // 8 * 8
+    if n <= 1:
+        stride = kp
+    # (a stride that starts rows elsewhere is the library's to refuse)
+    if kp != k and n > 0 and stride % 8 == 0 and 2 * (t.storage_offset() + (n - 1) * stride + kp) > t.untyped_storage().nbytes():
+        raise ValueError(f"{name}'s last row must own its bytes up to the next multiple of 16")
+    return stride
+
+
+def _head_args(x, w, targets, x_scale, w_scale) -> tuple:
+    """Checks shared by the head's loss and its gradients; the entry points' first arguments and the sizes."""
+    if x.dtype not in (torch.bfloat16, torch.int8):
+        raise ValueError(f"x must be torch.bfloat16 or torch.int8, got {x.dtype}")
+    if w.dtype != x.dtype:
+        raise ValueError(f"w must be {x.dtype} like x, got {w.dtype}")
+    xs, ws = _unit_stride("x", x), _unit_stride("w", w)
+    n, k = x.shape
+    vocab = w.shape[0]
+    if w.shape[1] != k:
+        raise ValueError("x and w must have rows of the same length")
+    _vector("targets", targets, torch.int32, n)
+    if x.dtype == torch.int8:
+        if x_scale is None or w_scale is None:
+            raise ValueError("8-bit rows need x_scale and w_scale")
+        _vector("x_scale", x_scale, torch.float32, n)
+        _vector("w_scale", w_scale, torch.float32, vocab)
+    elif x_scale is not None or w_scale is not None:
+        raise ValueError("bf16 rows have no scales")
+    kind = X_I8 if x.dtype == torch.int8 else X_BF16
+    return (x.data_ptr(), kind, xs, _ptr(x_scale), w.data_ptr(), ws, _ptr(w_scale), n, vocab, k, targets.data_ptr())
+
+
+def head_cross_entropy(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, x_scale: torch.Tensor | None = None,
+                       w_scale: torch.Tensor | None = None, loss: torch.Tensor | None = None,
+                       lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """(loss, lse) fp32 [n] of an output head: the softmax cross entropy of logits x @ w.T at targets int32 [n] (a
+    negative one leaves its row out: loss 0) and their log-sum-exp, without the logits in memory.  x [n, k] and w
+    [vocab, k] are bf16, or int8 rows with x_scale fp32 [n] and w_scale fp32 [vocab] as q8_matmul takes them; rows
+    start on 16 bytes.  `workspace` (GPU bytes, at least head_cross_entropy_workspace(...)) is allocated here when
+    not given."""
+    dev = _one_gpu(x, w, targets, x_scale, w_scale, loss, lse, workspace)
+    args = _head_args(x, w, targets, x_scale, w_scale)
+    n, vocab, k = args[7:10]
+    if loss is None:
+        loss = torch.empty(n, dtype=torch.float32, device=dev)
+    else:
+        _vector("loss", loss, torch.float32, n)
+    if lse is None:
+        lse = torch.empty(n, dtype=torch.float32, device=dev)
+    else:
+        _vector("lse", lse, torch.float32, n)
+    if workspace is None and n > 0:
+        workspace = _workspace(None, _head_need(args[1], n, vocab, k, _device_cus(dev)), dev)
+    else:
+        workspace = _workspace(workspace, 0, dev)
+    _call(dev, "stq_head_cross_entropy", *args, loss.data_ptr(), lse.data_ptr(), *_ws_args(workspace))
+    return loss, lse
+
+
+def head_cross_entropy_backward_workspace(x_dtype: int, n_rows: int, vocab: int, k: int, need_dx: bool = True,
+                                          need_dw: bool = True, n_cus: int = 0) -> int:
+    """Workspace bytes head_cross_entropy_backward needs for these shapes, as head_cross_entropy_workspace."""
+    wb = ctypes.c_int64()
+    _check("stq_head_cross_entropy_backward_workspace",
+           lib().stq_head_cross_entropy_backward_workspace(int(x_dtype), int(n_rows), int(vocab), int(k), int(bool(need_dx)),
+                                                           int(bool(need_dw)), int(n_cus), ctypes.byref(wb)))
+    return wb.value
+
+
+def _unit_rows(rows: int, k: int, device) -> torch.Tensor:
+    """bf16 [rows, k] whose rows start on 16 bytes."""
+    t = torch.empty((rows, (k + 7) // 8 * 8), dtype=torch.bfloat16, device=device)
+    return t[:, :k] if k % 8 else t
+
+
+def head_cross_entropy_backward(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor,
+                                grad_loss: torch.Tensor, x_scale: torch.Tensor | None = None,
+                                w_scale: torch.Tensor | None = None, need_dx: bool = True, need_dw: bool = True,
+                                dx: torch.Tensor | None = None, dw: torch.Tensor | None = None,
+                                workspace: torch.Tensor | None = None):
+    """(dx, dw) of head_cross_entropy for the gradient grad_loss fp32 [n] at the losses and the lse it gave: dx bf16
+    [n, k] (8-bit rows: the gradient at x * x_scale, the rounding taken as the identity) and dw bf16 [vocab, k] (bf16
+    rows only); None for the one not needed.  Rows left out have no gradient.  `workspace` (GPU bytes, at least
+    head_cross_entropy_backward_workspace(...)) is allocated here when not given."""
+    dev = _one_gpu(x, w, targets, lse, grad_loss, x_scale, w_scale, dx, dw, workspace)
+    args = _head_args(x, w, targets, x_scale, w_scale)
+    kind, n, vocab, k = args[1], *args[7:10]
+    _vector("lse", lse, torch.float32, n)
+    _vector("grad_loss", grad_loss, torch.float32, n)
+    if need_dw and kind == X_I8:
+        raise ValueError("8-bit weights have no gradient: need_dw must be False")
+    xs = ws = 0
+    if need_dx:
+        dx = _unit_rows(n, k, dev) if dx is None else dx
+        xs = _out_rows("dx", dx, torch.bfloat16, n, k)
+    elif dx is not None:
+        raise ValueError("dx is given but need_dx is False")
+    if need_dw:
+        dw = _unit_rows(vocab, k, dev) if dw is None else dw
+        ws = _out_rows("dw", dw, torch.bfloat16, vocab, k)
+    elif dw is not None:
+        raise ValueError("dw is given but need_dw is False")
+    if workspace is None and n > 0:
+        need = head_cross_entropy_backward_workspace(kind, n, vocab, k, need_dx, need_dw, _device_cus(dev))
+        workspace = _workspace(None, need, dev)
+    else:
+        workspace = _workspace(workspace, 0, dev)
+    _call(dev, "stq_head_cross_entropy_backward", *args, lse.data_ptr(), grad_loss.data_ptr(), _ptr(dx), xs, _ptr(dw), ws,
+          *_ws_args(workspace))
+    return dx, dw
 
 
 def layer_errors_workspace(n_rows: int, k: int, n_calib: int) -> int:

@@ -20,7 +20,7 @@ LIB = os.path.join(HERE, "libstq.so")
 
 SOURCES = ["stq_api.hip", "k_codec.hip", "k_gemv.hip", "k_gemm.hip", "k_moe.hip", "k_sens.hip", "k_gated.hip",
            "k_swiglu.hip", "k_q8.hip", "k_logprobs.hip", "k_norm.hip",
-           "k_route.hip", "k_combine.hip", "k_probe.hip"]
+           "k_route.hip", "k_combine.hip", "k_head.hip", "k_probe.hip"]
 # per-file extra flags: the encoders must not contract fp64 arithmetic; the
 # matrix-core probe keeps its accumulators in VGPRs (in the AGPR form the
 # compiler moves them between the two files every round)

@@ -945,6 +945,124 @@ stq_status stq_combine_rows_backward(const void* dy, int dy_dtype, int64_t dy_ro
   return ok();
 }
 
+namespace {
+
+stq_status head_check(int x_dtype, int64_t n_rows, int64_t vocab, int64_t k, const char* who) {
+  if (x_dtype != STQ_X_BF16 && x_dtype != STQ_X_I8) return fail(STQ_E_ARG, "%s: x_dtype %d is neither bf16 nor int8", who, x_dtype);
+  if (n_rows < 0) return fail(STQ_E_ARG, "%s: negative count", who);
+  if (k < 1 || k > kMaxK8) return fail(STQ_E_SHAPE, "%s: k=%lld outside 1..%lld", who, (long long)k, (long long)kMaxK8);
+  if (vocab < 1 || vocab > (int64_t{1} << 26)) return fail(STQ_E_SHAPE, "%s: vocab=%lld outside 1..2^26", who, (long long)vocab);
+  if (n_rows > (int64_t{1} << 20)) return fail(STQ_E_SHAPE, "%s: more than 2^20 rows in one call", who);
+  if (n_rows * vocab > (int64_t{1} << 38)) return fail(STQ_E_SHAPE, "%s: more than 2^38 logits in one call", who);
+  return STQ_OK;
+}
+
+stq_status head_operands(const void* x, int x_dtype, int64_t xs, const float* x_scale, const void* w, int64_t ws,
+                         const float* w_scale, int64_t n_rows, int64_t k, const int32_t* targets, const char* who) {
+  const int64_t esz = x_dtype == STQ_X_I8 ? 1 : 2, kp = (k * esz + 15) / 16 * 16;
+  if (ws < 0 || xs < 0 || ws > kMaxStride8 || xs > kMaxStride8 || ws * esz > kMaxStride8 || xs * esz > kMaxStride8)
+    return fail(STQ_E_SHAPE, "%s: row stride of x or w above 2^23 bytes", who);
+  if (xs * esz < kp || ws * esz < kp) return fail(STQ_E_SHAPE, "%s: row stride of x or w < k in whole 16-byte units", who);
+  if (n_rows == 0) return STQ_OK;
+  if (!x || !w || !targets) return fail(STQ_E_ARG, "%s: null pointer", who);
+  if (x_dtype == STQ_X_I8 && (!x_scale || !w_scale)) return fail(STQ_E_ARG, "%s: 8-bit rows need their scales", who);
+  if (!aligned(x, 16) || !aligned(w, 16) || xs * esz % 16 || ws * esz % 16)
+    return fail(STQ_E_ALIGN, "%s: x, w or their row strides not 16-byte aligned", who);
+  if (!aligned(x_scale, 4) || !aligned(w_scale, 4) || !aligned(targets, 4)) return fail(STQ_E_ALIGN, "%s: scales or targets not 4-byte aligned", who);
+  return STQ_OK;
+}
+
+stq::HeadArgs head_args(const void* x, int x_dtype, int64_t xs, const float* x_scale, const void* w, int64_t ws,
+                        const float* w_scale, int64_t n_rows, int64_t vocab, int64_t k, const int32_t* targets) {
+  const int64_t esz = x_dtype == STQ_X_I8 ? 1 : 2;
+  return stq::HeadArgs{x, xs * esz, x_scale, w, ws * esz, w_scale, x_dtype == STQ_X_I8, n_rows, vocab, k, targets};
+}
+
+}  // namespace
+
+stq_status stq_head_cross_entropy_workspace(int x_dtype, int64_t n_rows, int64_t vocab, int64_t k, int32_t n_cus,
+                                            int64_t* workspace_bytes) {
+  const char* who = "stq_head_cross_entropy_workspace";
+  if (!workspace_bytes) return fail(STQ_E_ARG, "%s: null output pointer", who);
+  *workspace_bytes = 0;
+  if (n_cus < 0) return fail(STQ_E_ARG, "%s: n_cus < 0", who);
+  const stq_status st = head_check(x_dtype, n_rows, vocab, k, who);
+  if (st != STQ_OK) return st;
+  if (n_rows > 0) *workspace_bytes = stq::head_layout(n_rows, vocab, n_cus > 0 ? n_cus : stq::cus_of_current_device()).bytes;
+  return ok();
+}
+
+stq_status stq_head_cross_entropy(const void* x, int x_dtype, int64_t x_row_stride, const float* x_scale, const void* w,
+                                  int64_t w_row_stride, const float* w_scale, int64_t n_rows, int64_t vocab, int64_t k,
+                                  const int32_t* targets, float* loss, float* lse, void* workspace,
+                                  int64_t workspace_bytes, stq_stream_t stream) {
+  const char* who = "stq_head_cross_entropy";
+  stq_status st = head_check(x_dtype, n_rows, vocab, k, who);
+  if (st == STQ_OK) st = head_operands(x, x_dtype, x_row_stride, x_scale, w, w_row_stride, w_scale, n_rows, k, targets, who);
+  if (st != STQ_OK) return st;
+  if (workspace_bytes < 0) return fail(STQ_E_ARG, "%s: workspace_bytes < 0", who);
+  if (n_rows == 0) return ok();
+  if (!loss || !lse) return fail(STQ_E_ARG, "%s: null pointer", who);
+  if (!aligned(loss, 4) || !aligned(lse, 4)) return fail(STQ_E_ALIGN, "%s: loss or lse not 4-byte aligned", who);
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const int cus = stq::cus_of_stream(s);
+  st = check_workspace(workspace, workspace_bytes, stq::head_layout(n_rows, vocab, cus).bytes, who);
+  if (st != STQ_OK) return st;
+  hipError_t e = stq::launch_head(head_args(x, x_dtype, x_row_stride, x_scale, w, w_row_stride, w_scale, n_rows, vocab, k, targets),
+                                  loss, lse, workspace, cus, s);
+  if (e != hipSuccess) return hip_fail(e, "stq_head_cross_entropy launch");
+  return ok();
+}
+
+stq_status stq_head_cross_entropy_backward_workspace(int x_dtype, int64_t n_rows, int64_t vocab, int64_t k, int want_dx,
+                                                     int want_dw, int32_t n_cus, int64_t* workspace_bytes) {
+  const char* who = "stq_head_cross_entropy_backward_workspace";
+  if (!workspace_bytes) return fail(STQ_E_ARG, "%s: null output pointer", who);
+  *workspace_bytes = 0;
+  if (n_cus < 0) return fail(STQ_E_ARG, "%s: n_cus < 0", who);
+  const stq_status st = head_check(x_dtype, n_rows, vocab, k, who);
+  if (st != STQ_OK) return st;
+  if (want_dw && x_dtype == STQ_X_I8) return fail(STQ_E_ARG, "%s: 8-bit weights have no gradient", who);
+  if (n_rows > 0 && (want_dx || want_dw))
+    *workspace_bytes = stq::plan_head_bwd(n_rows, vocab, k, want_dx != 0, want_dw != 0, n_cus > 0 ? n_cus : stq::cus_of_current_device()).bytes;
+  return ok();
+}
+
+stq_status stq_head_cross_entropy_backward(const void* x, int x_dtype, int64_t x_row_stride, const float* x_scale,
+                                           const void* w, int64_t w_row_stride, const float* w_scale, int64_t n_rows,
+                                           int64_t vocab, int64_t k, const int32_t* targets, const float* lse,
+                                           const float* grad_loss, uint16_t* dx, int64_t dx_row_stride, uint16_t* dw,
+                                           int64_t dw_row_stride, void* workspace, int64_t workspace_bytes,
+                                           stq_stream_t stream) {
+  const char* who = "stq_head_cross_entropy_backward";
+  stq_status st = head_check(x_dtype, n_rows, vocab, k, who);
+  if (st == STQ_OK) st = head_operands(x, x_dtype, x_row_stride, x_scale, w, w_row_stride, w_scale, n_rows, k, targets, who);
+  if (st != STQ_OK) return st;
+  if (workspace_bytes < 0) return fail(STQ_E_ARG, "%s: workspace_bytes < 0", who);
+  if (dw && x_dtype == STQ_X_I8) return fail(STQ_E_ARG, "%s: 8-bit weights have no gradient", who);
+  if (dx) st = matrix_check("dx", dx, STQ_X_BF16, dx_row_stride, n_rows, k, who);
+  if (st == STQ_OK && dw) st = matrix_check("dw", dw, STQ_X_BF16, dw_row_stride, vocab, k, who);
+  if (st != STQ_OK) return st;
+  if ((!dx && !dw) || (n_rows == 0 && !dw)) return ok();
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  hipError_t e;
+  if (n_rows == 0) {
+    e = stq::launch_head_zero(dw, dw_row_stride, vocab, k, s);
+  } else {
+    if (!lse || !grad_loss) return fail(STQ_E_ARG, "%s: null pointer", who);
+    if (!aligned(lse, 4) || !aligned(grad_loss, 4)) return fail(STQ_E_ALIGN, "%s: lse or grad_loss not 4-byte aligned", who);
+    const int cus = stq::cus_of_stream(s);
+    const stq::HeadBwdPlan plan = stq::plan_head_bwd(n_rows, vocab, k, dx != nullptr, dw != nullptr, cus);
+    st = check_workspace(workspace, workspace_bytes, plan.bytes, who);
+    if (st != STQ_OK) return st;
+    const stq::HeadBwdArgs b{lse, grad_loss, dx, dx_row_stride, dw, dw_row_stride};
+    e = stq::launch_head_bwd(head_args(x, x_dtype, x_row_stride, x_scale, w, w_row_stride, w_scale, n_rows, vocab, k, targets), b,
+                             plan, workspace, cus, s);
+  }
+  if (e != hipSuccess) return hip_fail(e, "stq_head_cross_entropy_backward launch");
+  return ok();
+}
+
 stq_status stq_stream_read_probe(const void* buf, int64_t bytes, uint32_t* sink, stq_stream_t stream) {
   if (bytes < 0 || bytes % 16) return fail(STQ_E_ARG, "stq_stream_read_probe: bytes must be a non-negative multiple of 16");
   if (bytes == 0) return ok();

@@ -341,6 +341,42 @@ struct CombineBwdArgs {
 };
 hipError_t launch_combine_rows_bwd(const CombineBwdArgs& a, hipStream_t s);
 
+// Softmax cross entropy of an output head and its gradients
+struct HeadArgs {
+  const void* x;          // rows: bf16, or 8-bit integers with x_scale
+  int64_t ldx;            // bytes
+  const float* x_scale;
+  const void* w;
+  int64_t ldw;            // bytes
+  const float* w_scale;
+  int i8;
+  int64_t rows, vocab, k;
+  const int32_t* targets;
+};
+struct HeadLayout {
+  int64_t hit, bytes;     // the targets' logits in the workspace; its size
+};
+HeadLayout head_layout(int64_t rows, int64_t vocab, int cus);
+hipError_t launch_head(const HeadArgs& h, float* loss, float* lse, void* ws, int cus, hipStream_t s);
+
+struct HeadBwdArgs {
+  const float* lse;
+  const float* g;
+  uint16_t* dx;           // may be NULL
+  int64_t ld_dx;          // elements
+  uint16_t* dw;           // may be NULL
+  int64_t ld_dw;
+};
+struct HeadBwdPlan {
+  int64_t width, pieces;       // of the vocabulary
+  int tile, splits;            // of dx's product
+  int64_t dlt, xt, wt, acc;    // workspace offsets
+  int64_t bytes;
+};
+HeadBwdPlan plan_head_bwd(int64_t rows, int64_t vocab, int64_t k, bool dx, bool dw, int cus);
+hipError_t launch_head_bwd(const HeadArgs& h, const HeadBwdArgs& b, const HeadBwdPlan& p, void* ws, int cus, hipStream_t s);
+hipError_t launch_head_zero(uint16_t* dw, int64_t ld, int64_t vocab, int64_t k, hipStream_t s);
+
 // Streaming-read reference (measurement only): reads `bytes` bytes of `buf`
 hipError_t launch_stream_read(const void* buf, int64_t bytes, uint32_t* sink, hipStream_t s);
 

@@ -150,3 +150,56 @@ def test_combine_nothing_to_do(L):
     _done(L, "stq_combine_rows", COMBINE, dict(n=0, z=None, row=None, y=None))
     _done(L, "stq_combine_rows_backward", COMBINE_BWD, dict(n=0, z=None, row=None, dy=None))
     _done(L, "stq_combine_rows_backward", COMBINE_BWD, dict(dz=None, dw=None, dy=None, row=None, z=None))
+
+
+HEAD = dict(x=FAKE, xd=BF16, xs=104, sx=None, w=FAKE, ws=104, sw=None, n=10, v=1000, k=100, t=FAKE, loss=FAKE, lse=FAKE, wsp=FAKE,
+            wsb=1 << 40)
+
+
+@pytest.mark.parametrize("kw, status", [
+    (dict(xd=F32), 1), (dict(xd=7), 1), (dict(n=-1), 1), (dict(k=0), 2), (dict(k=131072, xs=131072, ws=131072), 2), (dict(v=0), 2),
+    (dict(v=(1 << 26) + 1), 2), (dict(n=(1 << 20) + 1), 2), (dict(n=1 << 20, v=1 << 19), 2), (dict(xs=96), 2), (dict(ws=96), 2),
+    (dict(xs=108), 3), (dict(ws=108), 3), (dict(xs=1 << 22 | 8), 2), (dict(ws=1 << 62), 2), (dict(x=None), 1), (dict(w=None), 1),
+    (dict(t=None), 1), (dict(loss=None), 1), (dict(lse=None), 1), (dict(x=FAKE + 8), 3), (dict(w=FAKE + 8), 3), (dict(t=FAKE + 2), 3),
+    (dict(loss=FAKE + 1), 3), (dict(lse=FAKE + 2), 3), (dict(wsp=None), 1), (dict(wsb=8), 1), (dict(wsb=-1), 1), (dict(wsp=FAKE + 64), 3),
+    (dict(xd=2, xs=112, ws=112), 1), (dict(xd=2, xs=112, ws=112, sx=FAKE), 1), (dict(xd=2, xs=112, ws=112, sx=FAKE, sw=FAKE + 2), 3),
+])
+def test_head_refusals(L, kw, status):
+    _refused(L, "stq_head_cross_entropy", HEAD, kw, status)
+
+
+def test_head_nothing_to_do(L):
+    _done(L, "stq_head_cross_entropy", HEAD, dict(n=0, x=None, w=None, t=None, loss=None, lse=None, wsp=None, wsb=0))
+
+
+HEAD_BWD = dict(x=FAKE, xd=BF16, xs=104, sx=None, w=FAKE, ws=104, sw=None, n=10, v=1000, k=100, t=FAKE, lse=FAKE, g=FAKE, dx=FAKE,
+                dxs=100, dw=FAKE, dws=100, wsp=FAKE, wsb=1 << 40)
+
+
+@pytest.mark.parametrize("kw, status", [
+    (dict(xd=F32), 1), (dict(n=-1), 1), (dict(k=0), 2), (dict(v=0), 2), (dict(xs=96), 2), (dict(ws=108), 3), (dict(x=None), 1),
+    (dict(w=None), 1), (dict(t=None), 1), (dict(lse=None), 1), (dict(g=None), 1), (dict(lse=FAKE + 2), 3), (dict(g=FAKE + 1), 3),
+    (dict(dxs=99), 2), (dict(dws=99), 2), (dict(dx=FAKE + 1), 3), (dict(dw=FAKE + 1), 3), (dict(wsp=None), 1), (dict(wsb=64), 1),
+    (dict(wsb=-1), 1), (dict(xd=2, xs=112, ws=112, sx=FAKE, sw=FAKE), 1), (dict(dws=1 << 61), 2),
+])
+def test_head_backward_refusals(L, kw, status):
+    _refused(L, "stq_head_cross_entropy_backward", HEAD_BWD, kw, status)
+
+
+def test_head_workspaces(L):
+    need = ctypes.c_int64()
+    fwd, bwd = L.stq_head_cross_entropy_workspace, L.stq_head_cross_entropy_backward_workspace
+    # (maximum, sum) a row and tile, and the rows' target logits
+    assert fwd(BF16, 10, 1000, 100, 256, ctypes.byref(need)) == 0 and need.value == 16 * 10 * 8 + 256
+    assert fwd(BF16, 0, 1000, 100, 256, ctypes.byref(need)) == 0 and need.value == 0
+    assert fwd(F32, 10, 1000, 100, 256, ctypes.byref(need)) == 1
+    assert fwd(BF16, 10, 1000, 100, -1, ctypes.byref(need)) == 1
+    assert fwd(BF16, 10, 1000, 100, 256, None) == 1
+    for dx, dw in [(0, 0), (1, 0), (0, 1), (1, 1)]:
+        assert bwd(BF16, 10, 1000, 100, dx, dw, 256, ctypes.byref(need)) == 0 and (need.value > 0) == bool(dx or dw)
+    assert bwd(2, 10, 1000, 100, 1, 1, 256, ctypes.byref(need)) == 1
+    assert bwd(BF16, 10, 0, 100, 1, 1, 256, ctypes.byref(need)) == 2
+    # a piece's gradients and weights stay within a few hundred MB whatever the vocabulary
+    assert bwd(BF16, 4096, 1 << 20, 7168, 1, 1, 256, ctypes.byref(need)) == 0 and need.value < 1 << 30
+    _done(L, "stq_head_cross_entropy_backward", HEAD_BWD, dict(dx=None, dw=None, lse=None, g=None, wsp=None, wsb=0))
+    _done(L, "stq_head_cross_entropy_backward", HEAD_BWD, dict(n=0, dw=None, x=None, w=None, t=None, lse=None, g=None, wsp=None, wsb=0))
