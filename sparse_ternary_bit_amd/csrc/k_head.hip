@@ -48,7 +48,7 @@ struct NtArgs {
   const int32_t* targets;
   int64_t v0;             // vocabulary index of channel 0
   // kStats
-  float2* stats;          // [tn][m]: maximum, sum of exp(l - maximum)
+  float2* stats;          // [parts][m]: maximum, sum of exp(l - maximum), a part for each wavefront along the channels
   float* hit;             // [m]: the target's logit
   // kGrad
   const float* lse;
@@ -60,12 +60,13 @@ struct NtArgs {
   int64_t ld_dlt;
   int64_t n_pad, m_pad;
   // kSum
-  float* acc;             // [splits][m][n]
+  float* acc;             // [splits][m][ld_acc], ld_acc a multiple of 8
+  int64_t ld_acc;
   int add;                // add to acc
-  int splits;             // parts of the sum, acc [m][n] each
+  int splits;             // parts of the sum
   uint16_t* out;          // bf16 [m][ld_out] instead of acc's store (with add: acc is added first)
   int64_t ld_out;
-  int vec;                // eight outputs may be stored at once
+  int vec;                // out's rows start on 16 bytes
 };
 
 // Output channels of a pair of 16-row MFMA tiles: row r of tile h stands for
@@ -109,6 +110,245 @@ struct Mfma<false> {
 
 __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
+// Rows of bf16 that a wavefront holds as products, on their way to memory: 32
+// tokens x kC channels of LDS of its own, 16-byte chunks XORed by the token so
+// that whole rows and the transposing reads both fall on different banks.
+template <int kC>
+struct Slab {
+  static constexpr int kChunks = kC / 8;
+  char* mem;
+  int lane;
+  __device__ __forceinline__ char* at(int t, int chunk) const { return mem + t * kC * 2 + ((chunk ^ (tile_swizzle(t) & (kChunks - 1))) << 4); }
+  // this wavefront's stores before, its loads after (LDS serves a wavefront in order)
+  static __device__ __forceinline__ void fence() { asm volatile("" ::: "memory"); }
+  // rows t < rows, chunks below `width` channels, to out (16-byte aligned rows)
+  __device__ __forceinline__ void store_rows(uint16_t* out, int64_t ld, int rows, int width) const {
+#pragma unroll
+    for (int i = 0; i < 32 * kChunks / 64; ++i) {
+      const int t = (i * 64 + lane) / kChunks, c = (i * 64 + lane) % kChunks;
+      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(at(t, c));
+      if (t < rows && c * 8 < width) *reinterpret_cast<u32x4_t*>(out + t * ld + c * 8) = v;
+    }
+  }
+  // the same transposed: out[channel][token], channels below `width`, tokens below `rows` (a multiple of 8).
+  // 16 lanes give four tokens' 16 channels to the transposing read and each takes back four tokens of one.
+  __device__ __forceinline__ void store_columns(uint16_t* out, int64_t ld, int rows, int width) const {
+    const int q = lane >> 4, r = lane & 15;
+    const int t = 8 * q + (r >> 2);
+#pragma unroll
+    for (int i = 0; i < kC / 16; ++i) {
+      const uint32_t from = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(at(t, 2 * i + ((r & 3) >> 1)))) + (r & 1) * 8;
+      u32x2_t lo, hi;
+      asm volatile("ds_read_b64_tr_b16 %0, %2\n\tds_read_b64_tr_b16 %1, %2 offset:%3\n\ts_waitcnt lgkmcnt(0)"
+                   : "=&v"(lo), "=&v"(hi)
+                   : "v"(from), "n"(4 * kC * 2)
+                   : "memory");
+      if (8 * q < rows && 16 * i + r < width)
+        *reinterpret_cast<u32x4_t*>(out + (16 * i + r) * ld + 8 * q) = u32x4_t{lo[0], lo[1], hi[0], hi[1]};
+    }
+  }
+};
+
+// What becomes of a wavefront's sums: FM x 16 tokens from m0, FN x 16 channels
+// from n0, nv of them inside the product (less than 1: none).  A lane holds
+// token 16 j + r, channels 32 p + 8 q + 0..7.  `part`: this wavefront's row of
+// the statistics; `slab`: 32 x FN x 16 x 2 bytes of LDS of its own.
+// kAcc: the sums are in accumulation registers, and leave them 16 tokens at a
+// time.
+template <bool kI8, int kEpi, int FM, int FN, bool kAcc>
+__device__ __forceinline__ void finish(const NtArgs& a, typename Mfma<kI8>::acc_t (&acc)[FN][FM], int64_t m0, int64_t n0, int nv, int part,
+                                       int split, char* slab) {
+  constexpr int kC = FN * 16, kP = FN / 2;
+  // an opaque copy: what depends on the lane here is worked out here, not
+  // before the products and kept (spilled) beside them
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));
+  const int q = lane >> 4, r = lane & 15;
+  // (dl's transpose has zeros for tokens up to a whole stage)
+  if (m0 >= (kEpi == kGrad ? a.m_pad : a.m)) return;
+  auto value = [&](int j, int p, int e) -> float { return static_cast<float>(acc[2 * p + (e >> 2)][j][e & 3]); };
+  auto take = [&](int j) {
+    if constexpr (kAcc) {
+      static_assert(FN == 8, "the operands of this statement");
+      asm volatile("" : "+a"(acc[0][j]), "+a"(acc[1][j]), "+a"(acc[2][j]), "+a"(acc[3][j]), "+a"(acc[4][j]), "+a"(acc[5][j]),
+                   "+a"(acc[6][j]), "+a"(acc[7][j]));
+    }
+  };
+  if constexpr (kEpi == kSum) {
+    const Slab<kC> sl{slab, lane};
+    auto row_of = [&](int64_t tok) { return a.acc + (static_cast<int64_t>(split) * a.m + tok) * a.ld_acc; };
+    const bool rows_whole = a.out && a.vec;   // 16-byte rows of bf16, through LDS
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+      take(j);
+      const int64_t tok = m0 + 16 * j + r;
+      float v[kP][8];
+#pragma unroll
+      for (int p = 0; p < kP; ++p)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[p][e] = value(j, p, e);
+      if (a.add && tok < a.m) {
+#pragma unroll
+        for (int p = 0; p < kP; ++p) {
+          const int c = 32 * p + 8 * q;
+          if (c >= nv) continue;
+          const f32x4_t* const o = reinterpret_cast<const f32x4_t*>(row_of(tok) + n0 + c);
+          const f32x4_t lo = o[0], hi = o[1];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[p][e] += lo[e];
+            v[p][e + 4] += hi[e];
+          }
+        }
+      }
+      if (rows_whole) {
+#pragma unroll
+        for (int p = 0; p < kP; ++p) {
+          const int c = 32 * p + 8 * q;
+          const Raw8<bf16_t> o = pack8<bf16_t>(v[p]);
+          *reinterpret_cast<u32x4_t*>(sl.at(16 * (j & 1) + r, c / 8)) = o.w[0];
+          // the last channels of an odd width belong to no whole chunk
+          if (c + 8 > nv && c < nv && tok < a.m) store8<bf16_t, false>(reinterpret_cast<bf16_t*>(a.out) + tok * a.ld_out, n0 + c, a.n, o);
+        }
+        if ((j & 1) || j + 1 == FM) {
+          sl.fence();
+          const int64_t t0 = m0 + 16 * (j & ~1);
+          sl.store_rows(a.out + t0 * a.ld_out + n0, a.ld_out, static_cast<int>(min(static_cast<int64_t>(16 + 16 * (j & 1)), a.m - t0)), nv & ~7);
+          sl.fence();
+        }
+      } else if (tok < a.m) {
+#pragma unroll
+        for (int p = 0; p < kP; ++p) {
+          const int c = 32 * p + 8 * q;
+          if (c >= nv) continue;
+          if (a.out) {
+            store8<bf16_t, false>(reinterpret_cast<bf16_t*>(a.out) + tok * a.ld_out, n0 + c, a.n, pack8<bf16_t>(v[p]));
+          } else {
+            f32x4_t* const o = reinterpret_cast<f32x4_t*>(row_of(tok) + n0 + c);
+            o[0] = f32x4_t{v[p][0], v[p][1], v[p][2], v[p][3]};
+            o[1] = f32x4_t{v[p][4], v[p][5], v[p][6], v[p][7]};
+          }
+        }
+      }
+    }
+    return;
+  }
+  float wsc[kP][8];
+  if constexpr (kI8) {
+#pragma unroll
+    for (int p = 0; p < kP; ++p)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) wsc[p][e] = 32 * p + 8 * q + e < nv ? a.ws[n0 + 32 * p + 8 * q + e] : 0.0f;
+  }
+  int64_t target[FM];
+  float ts[FM];
+#pragma unroll
+  for (int j = 0; j < FM; ++j) {
+    const int64_t tok = m0 + 16 * j + r;
+    target[j] = tok < a.m ? a.targets[tok] : -1;
+    ts[j] = kI8 && tok < a.m ? a.as[tok] : 1.0f;
+  }
+  auto logit = [&](int j, int p, int e) { return kI8 ? value(j, p, e) * ts[j] * wsc[p][e] : value(j, p, e); };
+  if constexpr (kEpi == kStats) {
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+      take(j);
+      const int64_t tok = m0 + 16 * j + r;
+      float l[kP][8];
+#pragma unroll
+      for (int p = 0; p < kP; ++p)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) l[p][e] = logit(j, p, e);
+      const int64_t want = target[j] - a.v0 - n0 - 8 * q;   // (a target of -1 is below 0 here too)
+      if (__any(target[j] >= 0 && want >= 0 && want < kC)) {
+#pragma unroll
+        for (int p = 0; p < kP; ++p)
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (target[j] >= 0 && want == 32 * p + e && want + 8 * q < nv) a.hit[tok] = l[p][e];
+      }
+      if (nv < kC) {
+#pragma unroll
+        for (int p = 0; p < kP; ++p)
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (32 * p + 8 * q + e >= nv) l[p][e] = -INFINITY;
+      }
+      float m = l[0][0];
+#pragma unroll
+      for (int p = 0; p < kP; ++p)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = fmaxf(m, l[p][e]);
+      m = fmaxf(m, __shfl_xor(m, 16));
+      m = fmaxf(m, __shfl_xor(m, 32));
+      const float base = m == -INFINITY ? 0.0f : m;
+      float s[kP];
+#pragma unroll
+      for (int p = 0; p < kP; ++p) {
+        s[p] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[p] += exp_of(l[p][e] - base);
+      }
+#pragma unroll
+      for (int p = 1; p < kP; ++p) s[0] += s[p];
+      s[0] += __shfl_xor(s[0], 16);
+      s[0] += __shfl_xor(s[0], 32);
+      if (q == 0 && tok < a.m) a.stats[part * a.m + tok] = float2{m, s[0]};
+    }
+  }
+  if constexpr (kEpi == kGrad) {
+    float lse[FM], g[FM];
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+      const int64_t tok = m0 + 16 * j + r;
+      lse[j] = tok < a.m ? a.lse[tok] : 0.0f;
+      g[j] = tok < a.m ? a.g[tok] : 0.0f;
+    }
+    const Slab<kC> sl{slab, lane};
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+      take(j);
+      // no gradient: an ignored row, one without a distribution, a target past the vocabulary
+      const bool dead = target[j] < 0 || target[j] >= a.vocab || lse[j] == -INFINITY;
+      const float gj = dead ? 0.0f : g[j];
+      const int64_t want = target[j] - a.v0 - n0 - 8 * q;
+      const bool hot = __any(want >= 0 && want < kC);
+#pragma unroll
+      for (int p = 0; p < kP; ++p) {
+        float d[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) d[e] = exp_of(logit(j, p, e) - lse[j]);
+        if (hot) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) d[e] -= want == 32 * p + e ? 1.0f : 0.0f;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          d[e] *= gj;
+          if (kI8) d[e] *= wsc[p][e];
+          if (dead) d[e] = 0.0f;
+        }
+        if (nv < kC) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (32 * p + 8 * q + e >= nv) d[e] = 0.0f;
+        }
+        *reinterpret_cast<u32x4_t*>(sl.at(16 * (j & 1) + r, 4 * p + q)) = pack8<bf16_t>(d).w[0];
+      }
+      if ((j & 1) || j + 1 == FM) {
+        sl.fence();
+        const int64_t t0 = m0 + 16 * (j & ~1);
+        const int tokens = 16 + 16 * (j & 1);
+        sl.store_rows(a.dl + t0 * a.ld_dl + n0, a.ld_dl, static_cast<int>(min(static_cast<int64_t>(tokens), a.m - t0)),
+                      static_cast<int>(min(static_cast<int64_t>(kC), a.n_pad - n0)));
+        if (a.dlt)
+          sl.store_columns(a.dlt + n0 * a.ld_dlt + t0, a.ld_dlt, static_cast<int>(min(static_cast<int64_t>(tokens), a.m_pad - t0)), nv);
+        sl.fence();
+      }
+    }
+  }
+}
+
 // Workgroup of WM x WN wavefronts, TM tokens x (at most) TN channels.  Both
 // operands stream into LDS 128 bytes of the sum at a time (direct 16-byte
 // loads) through kBuf buffers.  While the matrix cores work on one 64-byte
@@ -124,7 +364,7 @@ __global__ __launch_bounds__(WM * WN * 64, kWavesPerSimd) void nt_kernel(NtArgs 
   constexpr int NA = TM / 8 / kNW, NW = TN / 8 / kNW;  // load instructions a stage and wavefront, 8 rows each
   static_assert(FN % 2 == 0, "channel tiles come in pairs");
   static_assert(NA * 8 * kNW == TM && NW * 8 * kNW == TN, "every wavefront issues the same loads");
-  static_assert(kBuf * (TM + TN) * kBK >= TM * TN * 2, "the finished tile fits where the stages were");
+  static_assert(kBuf * (TM + TN) * kBK >= kNW * 32 * FN * 16 * 2, "the slabs fit where the stages were");
   typedef typename Mfma<kI8>::acc_t acc_t;
   __shared__ __align__(16) char smem[kBuf * (TM + TN) * kBK];
   char(*const sa)[TM * kBK] = reinterpret_cast<char(*)[TM * kBK]>(smem);
@@ -267,194 +507,222 @@ __global__ __launch_bounds__(WM * WN * 64, kWavesPerSimd) void nt_kernel(NtArgs 
     for (int j = 0; j < FM; ++j) group(1, j);
   }
 
-  // token m0 + tok_row + 16 j, channels n0 + wn FN 16 + 32 p + 8 q + 0..7
-  const int ch0 = wn * FN * 16 + 8 * q;
-  auto value = [&](int j, int p, int e) -> float {
-    const acc_t& v = acc[2 * p + (e >> 2)][j];
-    return static_cast<float>(v[e & 3]);
+  // everyone has read the last stage
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  finish<kI8, kEpi, FM, FN, false>(a, acc, m0 + wm * FM * 16, n0 + wn * FN * 16, min(static_cast<int>(nv) - wn * FN * 16, FN * 16),
+                            tile_n * WN + wn, split, smem + wave * (32 * FN * 16 * 2));
+}
+
+// 256 x 256 tiles: four wavefronts of 128 x 128, one a SIMD, so that an operand
+// read from LDS serves eight products.  Nothing but its own order hides what
+// such a wavefront waits for, so the order is written out: a product, then at
+// most one LDS read of the next step's operands and one load.  The channel
+// operand has three buffers: its loads run a stage and a half ahead, between
+// the products of a stage's first step, the token operand's between those of
+// the second; all in one step would queue for 1024 cycles behind each other.
+// Workgroups stay and walk the tiles of their XCD; a tile's first loads start
+// before the previous tile's sums are put away.  (4096 rows x 65536 words x
+// 7168: 1.32 PFLOP/s with eight wavefronts of 128 x 64 and two buffers, 1.43
+// with four, 1.46 with the third buffer.)
+template <bool kI8, int kEpi>
+__global__ __launch_bounds__(256, 1) void nt_wide_kernel(NtArgs a) {
+  constexpr int T = 256, F = 8, kLoads = 8, kProducts = F * F;
+  constexpr int kRead0 = 3, kLoad0 = 4, kRead1 = 4, kLoad1 = 4;  // products between them
+  static_assert(kRead0 * 2 * F <= kProducts && kRead1 * 2 * F <= kProducts && kLoad0 * kLoads <= kProducts, "a step's reads fit into it");
+  __shared__ __align__(16) char smem[5 * T * kBK];
+  char(*const sa)[T * kBK] = reinterpret_cast<char(*)[T * kBK]>(smem);
+  char(*const sw)[T * kBK] = reinterpret_cast<char(*)[T * kBK]>(smem + 2 * T * kBK);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int q = lane >> 4, r = lane & 15, wm = wave >> 1, wn = wave & 1;
+  const int tiles = a.tm * a.tn;
+  const int per = (tiles + kXcds - 1) / kXcds, last = min(tiles, static_cast<int>(blockIdx.x % kXcds + 1) * per);
+  const int ns = static_cast<int>((a.kbytes + kBK - 1) / kBK);
+  const uint32_t kpad = static_cast<uint32_t>((a.kbytes + 15) & ~15);
+  uint32_t va[kLoads], vw[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int row = (wave + 4 * i) * 8 + (lane >> 3);
+    va[i] = row * static_cast<uint32_t>(a.lda) + (((lane & 7) ^ token_swizzle(row)) << 4);
+    vw[i] = row * static_cast<uint32_t>(a.ldw) + (((lane & 7) ^ channel_swizzle(row)) << 4);
+  }
+  int oa[2], ow[2];  // this lane's chunk of either step
+  const int tok_row = wm * 128 + r, ch_row = wn * 128 + pair_channel(r, 0);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    oa[h] = tok_row * kBK + (((4 * h + q) ^ token_swizzle(tok_row)) << 4);
+    ow[h] = ch_row * kBK + (((4 * h + q) ^ channel_swizzle(ch_row)) << 4);
+  }
+  struct Place {
+    int64_t m0, n0;
+    int tile_n;
   };
-  if constexpr (kEpi == kSum) {
+  auto place = [&](int id) {
+    const int band = id / (8 * a.tn), rows = min(8, a.tm - band * 8), in = id - band * 8 * a.tn;
+    return Place{static_cast<int64_t>(band * 8 + in % rows) * T, static_cast<int64_t>(in / rows) * T, in / rows};
+  };
+  auto tokens = [&](const Place& p, bool on) {
+    const int mv = static_cast<int>(min(static_cast<int64_t>(T), a.m - p.m0));
+    return make_rsrc(a.a + p.m0 * a.lda, on ? static_cast<uint32_t>((mv - 1) * a.lda) + kpad : 0);
+  };
+  auto channels = [&](const Place& p, bool on) {
+    const int nv = static_cast<int>(min(static_cast<int64_t>(T), a.n - p.n0));
+    return make_rsrc(a.w + p.n0 * a.ldw, on ? static_cast<uint32_t>((nv - 1) * a.ldw) + kpad : 0);
+  };
+  // the first two stages (the second reads as zeros where there is none)
+  auto begin = [&](const Place& p) {
 #pragma unroll
-    for (int j = 0; j < FM; ++j) {
-      const int64_t tok = m0 + tok_row + j * 16;
-      if (tok >= a.m) continue;
+    for (int s = 0; s < 2; ++s) {
+      const Rsrc ra = tokens(p, s < ns), rw = channels(p, s < ns);
 #pragma unroll
-      for (int p = 0; p < FN / 2; ++p) {
-        const int c = ch0 + 32 * p;
-        if (c >= nv) continue;
-        float v[8];
+      for (int i = 0; i < kLoads; ++i) lds_load16(ra, sa[s] + (wave + 4 * i) * 1024, va[i] + s * kBK);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = value(j, p, e);
-        float* acc_row = a.acc ? a.acc + (static_cast<int64_t>(split) * a.m + tok) * a.n : nullptr;
-        if (a.add) {
-          float o[8];
-          if (a.vec) load8f<float, true>(acc_row, n0 + c, a.n, o);
-          else load8f<float, false>(acc_row, n0 + c, a.n, o);
+      for (int i = 0; i < kLoads; ++i) lds_load16(rw, sw[s] + (wave + 4 * i) * 1024, vw[i] + s * kBK);
+    }
+  };
+  int id = static_cast<int>(blockIdx.x % kXcds) * per + static_cast<int>(blockIdx.x) / kXcds;
+  if (id >= last) return;
+  Place p = place(id);
+  begin(p);
+  for (;;) {
+    typename Mfma<kI8>::acc_t acc[F][F];
+    u32x4_t fa[2][F], fw[2][F];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] += o[e];
-        }
-        if (a.out) {
-          bf16_t* row = reinterpret_cast<bf16_t*>(a.out) + tok * a.ld_out;
-          if (a.vec) store8<bf16_t, true>(row, n0 + c, a.n, pack8<bf16_t>(v));
-          else store8<bf16_t, false>(row, n0 + c, a.n, pack8<bf16_t>(v));
-        } else {
-          if (a.vec) store8<float, true>(acc_row, n0 + c, a.n, pack8<float>(v));
-          else store8<float, false>(acc_row, n0 + c, a.n, pack8<float>(v));
+    for (int i = 0; i < F; ++i)
+#pragma unroll
+      for (int j = 0; j < F; ++j) acc[i][j] = typename Mfma<kI8>::acc_t{0, 0, 0, 0};
+    // The sums are all of the accumulation registers: left to the compiler, some
+    // of them move to and fro around their products.
+    auto product = [&](int h, int t) {
+      if constexpr (kI8) asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(acc[t % F][t / F]) : "v"(fw[h][t % F]), "v"(fa[h][t / F]));
+      else asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc[t % F][t / F]) : "v"(fw[h][t % F]), "v"(fa[h][t / F]));
+    };
+    // operand n of a step: the channels', then the tokens'
+    auto read = [&](int ba, int bw, int h, int n) {
+      if (n < F) fw[h][n] = *reinterpret_cast<const u32x4_t*>(sw[bw] + ow[h] + ((n >> 1) * 32 + (n & 1) * 4) * kBK);
+      else fa[h][n - F] = *reinterpret_cast<const u32x4_t*>(sa[ba] + oa[h] + (n - F) * 16 * kBK);
+    };
+    // Bytes of the last stage past the end of the sum count for nothing,
+    // whatever the rows hold there: zeros in the token operand, and, where a
+    // bf16 NaN times zero would be one, in the channel operand.
+    auto mask = [&](int h) {
+      const int left = static_cast<int>(a.kbytes) - ((ns - 1) * kBK + h * kStep + q * 16);
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const uint32_t m = byte_mask(left - 4 * d);
+#pragma unroll
+        for (int j = 0; j < F; ++j) fa[h][j][d] &= m;
+        if constexpr (!kI8) {
+#pragma unroll
+          for (int i = 0; i < F; ++i) fw[h][i][d] &= m;
         }
       }
-    }
-  }
-  if constexpr (kEpi == kStats) {
-    // a wavefront's maximum and sum of every token, then the wavefronts' of a token
-    float wsc[FN / 2][8];
+      asm volatile("s_nop 7" ::: "memory");  // the products that take these are not the compiler's to space
+    };
+    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+    // (written before the products that the compiler does not know as such)
 #pragma unroll
-    for (int p = 0; p < FN / 2; ++p)
+    for (int j = 0; j < F; ++j)
+      asm volatile("s_nop 3"
+                   : "+a"(acc[0][j]), "+a"(acc[1][j]), "+a"(acc[2][j]), "+a"(acc[3][j]), "+a"(acc[4][j]), "+a"(acc[5][j]),
+                     "+a"(acc[6][j]), "+a"(acc[7][j]));
 #pragma unroll
-      for (int e = 0; e < 8; ++e) wsc[p][e] = kI8 && ch0 + 32 * p + e < nv ? a.ws[n0 + ch0 + 32 * p + e] : 1.0f;
-    float2* const part = reinterpret_cast<float2*>(smem);  // [WN][TM]
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // everyone has read the last stage
+    for (int n = 0; n < 2 * F; ++n) read(0, 0, 0, n);
+    int ba = 0, bw = 0;
+    const bool tail = a.kbytes % kBK != 0;
+    for (int s = 0; s < ns; ++s) {
+      // past the last stage the loads have an empty range (they touch nothing)
+      // and the reads bring what no product takes
+      const Rsrc ra = tokens(p, s + 2 < ns), rw = channels(p, s + 2 < ns);
+      const uint32_t off = (s + 2) * kBK;
+      const int bw1 = bw == 2 ? 0 : bw + 1, bw2 = bw1 == 2 ? 0 : bw1 + 1;
+      if (tail && s + 1 == ns) mask(0);
 #pragma unroll
-    for (int j = 0; j < FM; ++j) {
-      const int64_t tok = m0 + tok_row + j * 16;
-      const bool on = tok < a.m;
-      const float ts = kI8 && on ? a.as[tok] : 1.0f;
-      const int64_t want = on ? a.targets[tok] - a.v0 - n0 - ch0 : -1;
-      float l[FN / 2][8], m = -INFINITY;
-#pragma unroll
-      for (int p = 0; p < FN / 2; ++p)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          l[p][e] = kI8 ? value(j, p, e) * ts * wsc[p][e] : value(j, p, e);
-          if (ch0 + 32 * p + e >= nv) l[p][e] = -INFINITY;
-          else if (want == 32 * p + e) a.hit[tok] = l[p][e];
-          m = fmaxf(m, l[p][e]);
-        }
-      m = fmaxf(m, __shfl_xor(m, 16));
-      m = fmaxf(m, __shfl_xor(m, 32));
-      const float base = m == -INFINITY ? 0.0f : m;
-      float s = 0.0f;
-#pragma unroll
-      for (int p = 0; p < FN / 2; ++p)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s += exp_of(l[p][e] - base);
-      s += __shfl_xor(s, 16);
-      s += __shfl_xor(s, 32);
-      if (q == 0) part[wn * TM + tok_row + j * 16] = float2{m, s};
-    }
-    __syncthreads();
-    for (int t = threadIdx.x; t < mv; t += kNW * 64) {
-      float m = part[t].x;
-#pragma unroll
-      for (int i = 1; i < WN; ++i) m = fmaxf(m, part[i * TM + t].x);
-      float s = 0.0f;
-#pragma unroll
-      for (int i = 0; i < WN; ++i) {
-        const float2 v = part[i * TM + t];
-        s += v.x == -INFINITY ? v.y : v.y * exp_of(v.x - m);  // (without a maximum y is 0, or NaN)
+      for (int t = 0; t < kProducts; ++t) {
+        product(0, t);
+        if (t % kRead0 == kRead0 - 1 && t / kRead0 < 2 * F) read(ba, bw, 1, t / kRead0);
+        if (t % kLoad0 == kLoad0 / 2 && t / kLoad0 < kLoads) lds_load16(rw, sw[bw2] + (wave + t / kLoad0 * 4) * 1024, vw[t / kLoad0] + off);
+        __builtin_amdgcn_sched_barrier(0);
       }
-      a.stats[tile_n * a.m + m0 + t] = float2{m, s};
-    }
-  }
-  if constexpr (kEpi == kGrad) {
-    constexpr int kChunks = TN / 8;
-    float wsc[FN / 2][8];
+      // The next stage has landed (the channel operand's loads of this step are
+      // the only ones that may still run), and everyone has read this one.
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLoads) : "memory");
+      if (tail && s + 1 == ns) mask(1);
 #pragma unroll
-    for (int p = 0; p < FN / 2; ++p)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) wsc[p][e] = kI8 && ch0 + 32 * p + e < nv ? a.ws[n0 + ch0 + 32 * p + e] : 1.0f;
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // everyone has read the last stage
-#pragma unroll
-    for (int j = 0; j < FM; ++j) {
-      const int t = tok_row + j * 16;
-      const int64_t tok = m0 + t;
-      const bool on = tok < a.m;
-      const float ts = kI8 && on ? a.as[tok] : 1.0f;
-      const int64_t target = on ? a.targets[tok] : -1;
-      const float lse = on ? a.lse[tok] : 0.0f;
-      // no gradient: an ignored row, one without a distribution, a target past the vocabulary
-      const bool dead = target < 0 || target >= a.vocab || lse == -INFINITY;
-      const float g = dead ? 0.0f : a.g[tok];
-      const int64_t want = target - a.v0 - n0 - ch0;
-#pragma unroll
-      for (int p = 0; p < FN / 2; ++p) {
-        float d[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float l = kI8 ? value(j, p, e) * ts * wsc[p][e] : value(j, p, e);
-          float v = exp_of(l - lse);
-          if (want == 32 * p + e) v -= 1.0f;
-          v = g * v;
-          if (kI8) v *= wsc[p][e];
-          d[e] = dead || ch0 + 32 * p + e >= nv ? 0.0f : v;
-        }
-        const int chunk = (ch0 + 32 * p) / 8;
-        *reinterpret_cast<u32x4_t*>(smem + t * TN * 2 + ((chunk ^ (tile_swizzle(t) & (kChunks - 1))) << 4)) = pack8<bf16_t>(d).w[0];
+      for (int t = 0; t < kProducts; ++t) {
+        product(1, t);
+        if (t % kLoad1 == kLoad1 - 1 && t / kLoad1 < kLoads) lds_load16(ra, sa[ba] + (wave + t / kLoad1 * 4) * 1024, va[t / kLoad1] + off);
+        if (t % kRead1 == kRead1 / 2 && t / kRead1 < 2 * F) read(ba ^ 1, bw1, 0, t / kRead1);
+        __builtin_amdgcn_sched_barrier(0);
       }
+      ba ^= 1;
+      bw = bw1;
     }
-    __syncthreads();
-    // the tile row by row ...
-    const int64_t n_here = min(static_cast<int64_t>(TN), a.n_pad - n0);
-    for (int i = threadIdx.x; i < TM * kChunks; i += kNW * 64) {
-      const int t = i / kChunks, c = i % kChunks;
-      if (t < mv && c * 8 < n_here)
-        *reinterpret_cast<u32x4_t*>(a.dl + (m0 + t) * a.ld_dl + n0 + c * 8) =
-            *reinterpret_cast<const u32x4_t*>(smem + t * TN * 2 + ((c ^ (tile_swizzle(t) & (kChunks - 1))) << 4));
+    // the last products' results are there after 19 wait states at most
+    asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+    // everyone has read the last stage, and no load is on its way
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    const Place done = p;
+    id += gridDim.x / kXcds;
+    const bool more = id < last;
+    if (more) {
+      p = place(id);
+      begin(p);
     }
-    // ... and column by column: 16 lanes give four tokens' 16 channels to the
-    // transposing read and each takes back four tokens of one
-    if (a.dlt) {
-      const int64_t m_here = min(static_cast<int64_t>(TM), a.m_pad - m0);
-      for (int i = wave; i < (TM / 32) * (TN / 16); i += kNW) {
-        const int g0 = i % (TM / 32) * 32, c0 = i / (TM / 32) * 16;
-        const int t = g0 + 8 * q + (r >> 2);
-        const int chunk = c0 / 8 + ((r & 3) >> 1);
-        const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(smem)) + t * TN * 2 +
-                            ((chunk ^ (tile_swizzle(t) & (kChunks - 1))) << 4) + (r & 1) * 8;
-        u32x2_t lo, hi;
-        asm volatile("ds_read_b64_tr_b16 %0, %2\n\tds_read_b64_tr_b16 %1, %2 offset:%3\n\ts_waitcnt lgkmcnt(0)"
-                     : "=&v"(lo), "=&v"(hi)
-                     : "v"(at), "n"(4 * TN * 2)
-                     : "memory");
-        if (g0 + 8 * q < m_here && c0 + r < nv)
-          *reinterpret_cast<u32x4_t*>(a.dlt + (n0 + c0 + r) * a.ld_dlt + m0 + g0 + 8 * q) = u32x4_t{lo[0], lo[1], hi[0], hi[1]};
-      }
-    }
+    // (the next tile's stages lie in the first two buffers of either operand)
+    finish<kI8, kEpi, F, F, true>(a, acc, done.m0 + wm * 128, done.n0 + wn * 128,
+                            static_cast<int>(min(static_cast<int64_t>(T), a.n - done.n0)) - wn * 128, done.tile_n * 2 + wn, 0,
+                            sw[2] + wave * (32 * 128 * 2));
+    if (!more) return;
   }
 }
 
-// The tiles' maxima and sums of a token joined; 64 tokens a workgroup, the
-// tiles shared out over 16 wavefronts.
+// (maximum, sum of exp(l - maximum)) of two sets of logits; a set without a
+// maximum has sum 0, or NaN.
+__device__ __forceinline__ float2 join(float2 a, float2 b) {
+  const float m = fmaxf(a.x, b.x);
+  return float2{m, (a.x == -INFINITY ? a.y : a.y * exp_of(a.x - m)) + (b.x == -INFINITY ? b.y : b.y * exp_of(b.x - m))};
+}
+
+// The parts of a token joined: 16 tokens a workgroup, 64 threads each, so that
+// few tokens with many parts are not one long chain (37 tokens with 1564 parts:
+// 17 us with 64 tokens a workgroup and 16 threads each).
 __global__ __launch_bounds__(1024) void head_join_kernel(const float2* stats, const float* hit, const int32_t* targets, int64_t m,
-                                                         int tn, int64_t vocab, float* loss, float* lse) {
-  __shared__ float2 part[16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * 64 + lane;
-  float top = -INFINITY, s = 0.0f;
+                                                         int parts, int64_t vocab, float* loss, float* lse) {
+  __shared__ float2 slot[16][16];
+  const int tok = threadIdx.x & 15, wave = threadIdx.x >> 6;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * 16 + tok;
+  float2 v = {-INFINITY, 0.0f};
   if (t < m) {
-#pragma unroll 4
-    for (int i = wave; i < tn; i += 16) {
-      const float2 v = stats[i * m + t];
-      const float m2 = fmaxf(top, v.x);
-      // (a part without a maximum has sum 0, or NaN)
-      s = (top == -INFINITY ? s : s * exp_of(top - m2)) + (v.x == -INFINITY ? v.y : v.y * exp_of(v.x - m2));
-      top = m2;
-    }
-  }
-  part[wave][lane] = float2{top, s};
-  __syncthreads();
-  if (wave || t >= m) return;
+    int i = threadIdx.x >> 4;
+    for (; i + 7 * 64 < parts; i += 8 * 64) {
+      float2 w[8];
 #pragma unroll
-  for (int i = 1; i < 16; ++i) {
-    const float2 v = part[i][lane];
-    const float m2 = fmaxf(top, v.x);
-    s = (top == -INFINITY ? s : s * exp_of(top - m2)) + (v.x == -INFINITY ? v.y : v.y * exp_of(v.x - m2));
-    top = m2;
+      for (int e = 0; e < 8; ++e) w[e] = stats[(i + e * 64) * m + t];
+#pragma unroll
+      for (int e = 4; e >= 1; e >>= 1)
+#pragma unroll
+        for (int f = 0; f < e; ++f) w[f] = join(w[f], w[f + e]);
+      v = join(v, w[0]);
+    }
+    for (; i < parts; i += 64) v = join(v, stats[i * m + t]);
   }
-  const float logs = __builtin_amdgcn_logf(s) * kLn2;
-  const bool none = top == -INFINITY && s == 0.0f;
-  lse[t] = none ? -INFINITY : top + logs;
+#pragma unroll
+  for (int o = 16; o <= 32; o <<= 1) v = join(v, float2{__shfl_xor(v.x, o), __shfl_xor(v.y, o)});
+  if ((threadIdx.x & 63) < 16) slot[wave][tok] = v;
+  __syncthreads();
+  if (threadIdx.x >= 64) return;
+  v = slot[threadIdx.x >> 4][tok];
+#pragma unroll
+  for (int i = 4; i < 16; i += 4) v = join(v, slot[(threadIdx.x >> 4) + i][tok]);
+#pragma unroll
+  for (int o = 16; o <= 32; o <<= 1) v = join(v, float2{__shfl_xor(v.x, o), __shfl_xor(v.y, o)});
+  if (threadIdx.x >= 16 || t >= m) return;
+  const float logs = __builtin_amdgcn_logf(v.y) * kLn2;
+  const bool none = v.x == -INFINITY && v.y == 0.0f;
+  lse[t] = none ? -INFINITY : v.x + logs;
   const int64_t target = targets[t];
-  loss[t] = target < 0 ? 0.0f : none || target >= vocab ? NAN : logs - (hit[t] - top);
+  loss[t] = target < 0 ? 0.0f : none || target >= vocab ? NAN : logs - (hit[t] - v.x);
 }
 
 // out[c][r] = in[r][c] for r < n (zeros for r = n .. n_pad - 1 and for rows
@@ -501,13 +769,14 @@ __global__ __launch_bounds__(256) void transpose_kernel(const char* in, int64_t 
 }
 
 // The parts of a split sum, in order, rounded to bf16
-__global__ __launch_bounds__(256) void join_splits_kernel(const float* acc, int splits, int64_t m, int64_t n, uint16_t* out,
-                                                          int64_t ld_out) {
+__global__ __launch_bounds__(256) void join_splits_kernel(const float* acc, int64_t ld_acc, int splits, int64_t m, int64_t n,
+                                                          uint16_t* out, int64_t ld_out) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= m * n) return;
-  float s = acc[i];
-  for (int p = 1; p < splits; ++p) s += acc[p * m * n + i];
-  out[i / n * ld_out + i % n] = static_cast<uint16_t>(bf16_round(s));
+  const int64_t row = i / n, c = i - row * n;
+  float s = acc[row * ld_acc + c];
+  for (int p = 1; p < splits; ++p) s += acc[(p * m + row) * ld_acc + c];
+  out[row * ld_out + c] = static_cast<uint16_t>(bf16_round(s));
 }
 
 __global__ __launch_bounds__(256) void zero_rows_kernel(uint16_t* out, int64_t ld, int64_t m, int64_t n) {
@@ -539,14 +808,25 @@ Tile pick_tile(int64_t m, int64_t n, int cus) {
 }
 int tile_m(Tile t) { return t == k256x256 ? 256 : t == k128x128 ? 128 : 64; }
 int tile_n(Tile t) { return t == k256x256 || t == k64x256 ? 256 : t == k128x128 ? 128 : 64; }
+int tile_parts(Tile t) { return t == k64x256 ? 4 : 2; }  // wavefronts along a tile's channels
+int64_t stat_parts(Tile t, int64_t vocab) { return (vocab + tile_n(t) - 1) / tile_n(t) * tile_parts(t); }
 
 template <bool kI8, int kEpi>
-void launch_nt(const NtArgs& a, Tile t, hipStream_t s) {
+void launch_nt(const NtArgs& a, Tile t, int cus, hipStream_t s) {
   switch (t) {
     case k64x64: launch_tile<kI8, kEpi, 64, 64, 2, 2, 3, 2>(a, 64, s); break;
     case k64x256: launch_tile<kI8, kEpi, 64, 256, 1, 4, 2, 2>(a, 256, s); break;
     case k128x128: launch_tile<kI8, kEpi, 128, 128, 2, 2, 2, 2>(a, 128, s); break;
-    case k256x256: launch_tile<kI8, kEpi, 256, 256, 2, 4, 2, 2>(a, 256, s); break;
+    case k256x256: {
+      NtArgs w = a;
+      w.tm = static_cast<int>((a.m + 255) / 256);
+      w.tn = static_cast<int>((a.n + 255) / 256);
+      const int64_t tiles = static_cast<int64_t>(w.tm) * w.tn;
+      // a workgroup a compute unit (its LDS is all of one's), as many on every XCD
+      const int64_t grid = std::min<int64_t>((tiles + kXcds - 1) / kXcds, std::max(1, cus / kXcds)) * kXcds;
+      hipLaunchKernelGGL((nt_wide_kernel<kI8, kEpi>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, w);
+      break;
+    }
   }
 }
 
@@ -570,9 +850,8 @@ NtArgs logits_args(const HeadArgs& h) {
 }  // namespace
 
 HeadLayout head_layout(int64_t rows, int64_t vocab, int cus) {
-  const int64_t tn = (vocab + tile_n(pick_tile(rows, vocab, cus)) - 1) / tile_n(pick_tile(rows, vocab, cus));
   HeadLayout l{};
-  l.hit = up(tn * rows * 8, 256);
+  l.hit = up(stat_parts(pick_tile(rows, vocab, cus), vocab) * rows * 8, 256);
   l.bytes = l.hit + up(rows * 4, 256);
   return l;
 }
@@ -583,12 +862,12 @@ hipError_t launch_head(const HeadArgs& h, float* loss, float* lse, void* ws, int
   NtArgs a = logits_args(h);
   a.stats = static_cast<float2*>(ws);
   a.hit = reinterpret_cast<float*>(static_cast<char*>(ws) + l.hit);
-  if (h.i8) launch_nt<true, kStats>(a, t, s);
-  else launch_nt<false, kStats>(a, t, s);
+  if (h.i8) launch_nt<true, kStats>(a, t, cus, s);
+  else launch_nt<false, kStats>(a, t, cus, s);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(head_join_kernel, dim3(static_cast<unsigned>((h.rows + 63) / 64)), dim3(1024), 0, s, a.stats, a.hit, h.targets,
-                     h.rows, static_cast<int>((h.vocab + tile_n(t) - 1) / tile_n(t)), h.vocab, loss, lse);
+  hipLaunchKernelGGL(head_join_kernel, dim3(static_cast<unsigned>((h.rows + 15) / 16)), dim3(1024), 0, s, a.stats, a.hit, h.targets,
+                     h.rows, static_cast<int>(stat_parts(t, h.vocab)), h.vocab, loss, lse);
   return hipGetLastError();
 }
 
@@ -620,8 +899,8 @@ HeadBwdPlan plan_head_bwd(int64_t rows, int64_t vocab, int64_t k, bool dx, bool 
   p.tile = pick_tile(rows, k, cus);
   const int64_t tiles = ((rows + tile_m(static_cast<Tile>(p.tile)) - 1) / tile_m(static_cast<Tile>(p.tile))) *
                         ((k + tile_n(static_cast<Tile>(p.tile)) - 1) / tile_n(static_cast<Tile>(p.tile)));
-  p.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({cus / tiles, p.width / 1024, 16})));
-  if (dx && (p.pieces > 1 || p.splits > 1)) at += up(p.splits * rows * k * 4, 256);
+  p.splits = p.tile == k256x256 ? 1 : static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({cus / tiles, p.width / 1024, 16})));
+  if (dx && (p.pieces > 1 || p.splits > 1)) at += up(p.splits * rows * up(k, 8) * 4, 256);
   p.bytes = at;
   return p;
 }
@@ -656,8 +935,8 @@ hipError_t launch_head_bwd(const HeadArgs& h, const HeadBwdArgs& b, const HeadBw
     a.n_pad = n_pad;
     a.m_pad = m_pad;
     const Tile t = pick_tile(h.rows, n, cus);
-    if (h.i8) launch_nt<true, kGrad>(a, t, s);
-    else launch_nt<false, kGrad>(a, t, s);
+    if (h.i8) launch_nt<true, kGrad>(a, t, cus, s);
+    else launch_nt<false, kGrad>(a, t, cus, s);
     if (b.dx) {
       const dim3 grid(static_cast<unsigned>(n_pad / 64), static_cast<unsigned>((h.k + 63) / 64));
       if (h.i8) hipLaunchKernelGGL((transpose_kernel<true>), grid, dim3(256), 0, s, a.w, h.ldw, n, h.k, nullptr, wt, p.width, n_pad);
@@ -671,13 +950,14 @@ hipError_t launch_head_bwd(const HeadArgs& h, const HeadBwdArgs& b, const HeadBw
       d.n = h.k;
       d.kbytes = n_pad * 2;
       d.acc = acc;
+      d.ld_acc = up(h.k, 8);
       d.add = i > 0;
       d.splits = p.splits;
       const bool last = p.splits == 1 && i + 1 == p.pieces;
       d.out = last ? b.dx : nullptr;
       d.ld_out = b.ld_dx;
-      d.vec = h.k % 4 == 0 && (!last || vec(b.dx, b.ld_dx * 2));
-      launch_nt<false, kSum>(d, static_cast<Tile>(p.tile), s);
+      d.vec = last && vec(b.dx, b.ld_dx * 2);
+      launch_nt<false, kSum>(d, static_cast<Tile>(p.tile), cus, s);
     }
     if (b.dw) {
       NtArgs d{};
@@ -692,13 +972,14 @@ hipError_t launch_head_bwd(const HeadArgs& h, const HeadBwdArgs& b, const HeadBw
       d.out = b.dw + v0 * b.ld_dw;
       d.ld_out = b.ld_dw;
       d.vec = vec(d.out, b.ld_dw * 2);
-      launch_nt<false, kSum>(d, pick_tile(n, h.k, cus), s);
+      launch_nt<false, kSum>(d, pick_tile(n, h.k, cus), cus, s);
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   if (b.dx && p.splits > 1)
-    hipLaunchKernelGGL(join_splits_kernel, dim3(blocks(h.rows * h.k)), dim3(256), 0, s, acc, p.splits, h.rows, h.k, b.dx, b.ld_dx);
+    hipLaunchKernelGGL(join_splits_kernel, dim3(blocks(h.rows * h.k)), dim3(256), 0, s, acc, up(h.k, 8), p.splits, h.rows, h.k, b.dx,
+                       b.ld_dx);
   return hipGetLastError();
 }
 
