@@ -30,8 +30,8 @@ constexpr int kChunk = 64;
 constexpr int kLanes = 16;        // lanes of a token
 constexpr int kMaxExperts = kRouteMaxExperts;
 static_assert(kRouteMaxTop <= 2 * kLanes, "a lane holds two of a token's pairs");
-constexpr int kIndexBits = 10;
-constexpr uint32_t kIndexMask = (1u << kIndexBits) - 1u;
+// bits of a key that hold the column, for kN logits a lane
+constexpr int index_bits(int n) { return n == 4 ? 6 : n == 8 ? 7 : n == 16 ? 8 : n == 32 ? 9 : 10; }
 constexpr float kLog2e = 1.44269504088896340736f;
 
 __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
@@ -109,185 +109,209 @@ struct RouteKernelArgs {
   float* prob_total;
 };
 
-// Exclusive prefix sum of n counts in LDS by one wavefront; returns the total
-__device__ __forceinline__ int scan_counts(const int* counts, int* offsets, int n) {
-  const int lane = threadIdx.x & 63;
-  const int per = (n + 63) / 64;
-  int own = 0;
-  for (int i = 0; i < per; ++i) own += lane * per + i < n ? counts[lane * per + i] : 0;
-  int sum = own;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int up = __shfl_up(sum, o);
-    if (lane >= o) sum += up;
-  }
-  int at = sum - own;
-  for (int i = 0; i < per; ++i) {
-    const int e = lane * per + i;
-    if (e < n) {
-      offsets[e] = at;
-      at += counts[e];
-    }
-  }
-  const int total = __shfl(sum, 63);
-  if (lane == 0) offsets[n] = total;
-  return total;
+// Inclusive prefix sum over a wavefront: shifts inside 16 lanes, then the last
+// lanes of the rows below.
+__device__ __forceinline__ int scan64(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
+  return v;
 }
 
-// E sum_e counts_e / total * prob_e / tokens by one wavefront
-template <typename F>
-__device__ __forceinline__ float balance_of(const int* counts, F prob, int n, int total, int top_k) {
+// The experts' counts turned into their first rows (`first`, LDS, n + 1
+// entries), and the balance loss, by one wavefront: a lane has kPer
+// neighbouring experts.  count(e) and prob(e) are their counts and summed
+// probabilities.
+template <int kPer, typename C, typename P>
+__device__ __forceinline__ float scan_experts(int n, int top_k, int* first, C count, P prob) {
+  const int lane = threadIdx.x & 63;
+  int c[kPer], own = 0;
   float s = 0.0f;
-  for (int e = threadIdx.x & 63; e < n; e += 64) s = fmaf(static_cast<float>(counts[e]), prob(e), s);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = lane * kPer + i;
+    c[i] = e < n ? count(e) : 0;
+    if (e < n) s = fmaf(static_cast<float>(c[i]), prob(e), s);
+    own += c[i];
+  }
+  const int sum = scan64(own);
+  int at = sum - own;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = lane * kPer + i;
+    if (e < n) first[e] = at;
+    at += c[i];
+  }
+  const int total = __builtin_amdgcn_readlane(sum, 63);
+  if (lane == 0) first[n] = total;
   s = sum64(s);
   const float rows = static_cast<float>(max(total, 1));
   return s * (static_cast<float>(n) / rows) * (static_cast<float>(top_k) / rows);
+}
+
+// Tokens of the chunk before token tl among those in an expert's 64 bits
+__device__ __forceinline__ int before(const uint32_t (&m)[2], int tl) {
+  const uint32_t lo = tl < 32 ? m[0] & ((1u << tl) - 1u) : m[0];
+  const uint32_t hi = tl < 32 ? 0u : m[1] & ((1u << (tl - 32)) - 1u);
+  return __popc(lo) + __popc(hi);
 }
 
 // One chunk: choice, weights, counts and summed probabilities; with kOne (the
 // only chunk) the sorted rows too.
 template <typename T, int kN, int kThreads, bool kOne>
 __global__ __launch_bounds__(kThreads) void route_kernel(RouteKernelArgs g) {
-  constexpr int kWaves = kThreads / 64, kAtOnce = kThreads / kLanes;
+  constexpr int kAtOnce = kThreads / kLanes, kCols = kLanes * kN;
+  constexpr uint32_t kIndex = (1u << index_bits(kN)) - 1u;
+  constexpr int kGroups = kThreads > kCols ? kThreads / kCols : 1;   // threads a column
+  constexpr int kPerThread = kCols > kThreads ? kCols / kThreads : 1;  // columns a thread
+  constexpr int kPairs = kOne ? kChunk * kRouteMaxTop : 1;
   const RouteArgs& a = g.a;
   const int E = a.experts, k = a.top_k;
-  __shared__ uint32_t mask[kMaxExperts][2];   // an expert's tokens of the chunk
-  __shared__ float slab[kWaves][kLanes * kN];
-  __shared__ int count[kOne ? kMaxExperts : 1], first[kOne ? kMaxExperts + 1 : 1];
-  __shared__ float prob[kOne ? kMaxExperts : 1];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lane16 = threadIdx.x & (kLanes - 1);
-  for (int i = threadIdx.x; i < E; i += kThreads) mask[i][0] = mask[i][1] = 0u;
+  __shared__ __align__(16) float prob[kAtOnce][kCols];
+  __shared__ uint32_t mask[kCols][2];   // an expert's tokens of the chunk
+  __shared__ int first[kOne ? kCols + 1 : 1], pair_e[kPairs];
+  __shared__ float pair_w[kPairs];
+  const int lane16 = threadIdx.x & (kLanes - 1);
+  for (int i = threadIdx.x; i < kCols; i += kThreads) mask[i][0] = mask[i][1] = 0u;
   __syncthreads();
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kChunk;
-  float acc[kN];
+  const int tokens = static_cast<int>(min(static_cast<int64_t>(kChunk), a.tokens - t0));
+  float acc[kPerThread];
 #pragma unroll
-  for (int j = 0; j < kN; ++j) acc[j] = 0.0f;
-  for (int pass = 0; pass < kChunk / kAtOnce; ++pass) {
-    const int tl = pass * kAtOnce + static_cast<int>(threadIdx.x) / kLanes;
-    const int64_t t = t0 + tl;
-    const bool valid = t < a.tokens;
-    if (__ballot(valid) == 0) break;   // tokens come in order: none is left for this wavefront
-    const T* row = static_cast<const T*>(a.logits) + (valid ? t : 0) * a.stride;
-    float v[kN];
-    load_logits<T, kN>(row, lane16, E, g.vec, valid, v);
-    uint32_t key[kN];
-#pragma unroll
-    for (int j = 0; j < kN; ++j) {
-      const int c = column(lane16, j);
-      key[j] = c < E ? (order_bits(v[j]) & ~kIndexMask) | (kIndexMask - c) : 0u;
-    }
-    float top;
-    const float sum = exponents<kN>(v, top);
-    const float inv = 1.0f / sum;
-    if (valid && top != -INFINITY) {
-#pragma unroll
-      for (int j = 0; j < kN; ++j) acc[j] = fmaf(v[j], inv, acc[j]);
-    }
-    // extraction: after step i, lane i % 16 holds the i-th key
-    uint32_t mine[2] = {0u, 0u}, last = 0u;
-    bool unsure = false;
-    const int steps = sizeof(T) == 4 ? min(k + 1, E) : k;
-    for (int i = 0; i < steps; ++i) {
-      uint32_t m = key[0];
-#pragma unroll
-      for (int j = 1; j < kN; ++j) m = max(m, key[j]);
-      m = max16(m);
-      unsure |= i > 0 && ((m ^ last) & ~kIndexMask) == 0u;
-      last = m;
-      if (lane16 == (i & 15) && i < k) mine[i >> 4] = m;
-#pragma unroll
-      for (int j = 0; j < kN; ++j) key[j] = key[j] == m ? 0u : key[j];
-    }
-    int pick[2] = {static_cast<int>(kIndexMask - (mine[0] & kIndexMask)), static_cast<int>(kIndexMask - (mine[1] & kIndexMask))};
-    if (sizeof(T) == 4 && __any(unsure && valid)) {
-      // some keys agree: once more with whole values, the lowest index first
+  for (int i = 0; i < kPerThread; ++i) acc[i] = 0.0f;
+  for (int tp = 0; tp < tokens; tp += kAtOnce) {
+    const int tl = tp + static_cast<int>(threadIdx.x) / kLanes;
+    const bool valid = tl < tokens;
+    if (__any(valid)) {
+      const int64_t t = t0 + tl;
+      const T* row = static_cast<const T*>(a.logits) + (valid ? t : 0) * a.stride;
+      float v[kN];
       load_logits<T, kN>(row, lane16, E, g.vec, valid, v);
-      uint64_t left = 0;
+      uint32_t key[kN];
 #pragma unroll
-      for (int j = 0; j < kN; ++j) left |= column(lane16, j) < E ? 1ull << j : 0ull;
-      for (int i = 0; i < k; ++i) {
-        uint32_t m = 0u;
+      for (int j = 0; j < kN; ++j) {
+        const int c = column(lane16, j);
+        key[j] = c < E ? (order_bits(v[j]) & ~kIndex) | (kIndex - c) : 0u;
+      }
+      float top;
+      const float sum = exponents<kN>(v, top);
+      // nothing for a token that is masked throughout, NaN for one without a distribution
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
-        for (int j = 0; j < kN; ++j) m = max(m, (left >> j & 1) ? order_bits(v[j]) : 0u);
+      for (int q = 0; q < kN / 4; ++q)
+        *reinterpret_cast<f32x4_t*>(&prob[tl - tp][column(lane16, 4 * q)]) =
+            f32x4_t{v[4 * q] * inv, v[4 * q + 1] * inv, v[4 * q + 2] * inv, v[4 * q + 3] * inv};
+      // extraction: after step i, lane i % 16 holds the i-th key
+      uint32_t mine[2] = {0u, 0u}, last = 0u;
+      bool unsure = false;
+      const int steps = sizeof(T) == 4 ? min(k + 1, E) : k;
+      for (int i = 0; i < steps; ++i) {
+        uint32_t m = key[0];
+#pragma unroll
+        for (int j = 1; j < kN; ++j) m = max(m, key[j]);
         m = max16(m);
-        uint32_t c = ~0u;
+        unsure |= i > 0 && ((m ^ last) & ~kIndex) == 0u;
+        last = m;
+        if (lane16 == (i & 15) && i < k) mine[i >> 4] = m;
 #pragma unroll
-        for (int j = 0; j < kN; ++j)
-          if ((left >> j & 1) && order_bits(v[j]) == m) c = min(c, static_cast<uint32_t>(column(lane16, j)));
-        c = min16(c);
+        for (int j = 0; j < kN; ++j) key[j] = key[j] == m ? 0u : key[j];
+      }
+      int pick[2] = {static_cast<int>(kIndex - (mine[0] & kIndex)), static_cast<int>(kIndex - (mine[1] & kIndex))};
+      if (sizeof(T) == 4 && __any(unsure && valid)) {
+        // some keys agree: once more with whole values, the lowest index first
+        load_logits<T, kN>(row, lane16, E, g.vec, valid, v);
 #pragma unroll
-        for (int j = 0; j < kN; ++j)
-          if (static_cast<uint32_t>(column(lane16, j)) == c) left &= ~(1ull << j);
-        if (lane16 == (i & 15)) pick[i >> 4] = static_cast<int>(c);
+        for (int j = 0; j < kN; ++j) key[j] = column(lane16, j) < E ? order_bits(v[j]) : 0u;
+        for (int i = 0; i < k; ++i) {
+          uint32_t m = key[0];
+#pragma unroll
+          for (int j = 1; j < kN; ++j) m = max(m, key[j]);
+          m = max16(m);
+          uint32_t c = ~0u;
+#pragma unroll
+          for (int j = kN - 1; j >= 0; --j) c = key[j] == m ? static_cast<uint32_t>(column(lane16, j)) : c;
+          c = min16(c);
+#pragma unroll
+          for (int j = 0; j < kN; ++j) key[j] = static_cast<uint32_t>(column(lane16, j)) == c ? 0u : key[j];
+          if (lane16 == (i & 15)) pick[i >> 4] = static_cast<int>(c);
+        }
+      }
+      // weights; a token without a distribution goes nowhere
+      const bool routed = valid && top != -INFINITY && sum == sum;
+      __builtin_amdgcn_wave_barrier();   // the token's probabilities are its own wavefront's
+      float w[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (routed && lane16 + 16 * h < k) w[h] = prob[tl - tp][pick[h]];
+      const float norm = a.renorm ? 1.0f / sum16(w[0] + w[1]) : 1.0f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int i = lane16 + 16 * h;
+        if (!valid || i >= k) continue;
+        const int64_t p = t * k + i;
+        const int e = routed ? pick[h] : -1;
+        const float weight = routed ? w[h] * norm : top == -INFINITY && sum == sum ? 0.0f : NAN;
+        a.pair_expert[p] = e;
+        a.pair_weight[p] = weight;
+        if constexpr (kOne) {
+          pair_e[p] = e;
+          pair_w[p] = weight;
+        }
+        if (routed) atomicOr(&mask[e][tl >> 5], 1u << (tl & 31));
       }
     }
-    // weights; a token without a distribution goes nowhere
-    const bool routed = valid && top != -INFINITY && sum == sum;
-    float w[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      if (routed && lane16 + 16 * h < k) {
-        const float l = widen(row[pick[h]]);
-        w[h] = l == -INFINITY ? 0.0f : exp_of(l - top);
-      }
-    const float norm = a.renorm ? 1.0f / sum16(w[0] + w[1]) : inv;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int i = lane16 + 16 * h;
-      if (!valid || i >= k) continue;
-      const int64_t p = t * k + i;
-      a.pair_expert[p] = routed ? pick[h] : -1;
-      a.pair_weight[p] = routed ? w[h] * norm : top == -INFINITY && sum == sum ? 0.0f : NAN;
-      if (routed) atomicOr(&mask[pick[h]][tl >> 5], 1u << (tl & 31));
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < kN; ++j) {
-    float s = acc[j];
-    s += __shfl_xor(s, 16);
-    s += __shfl_xor(s, 32);
-    if (lane < kLanes) slab[wave][column(lane, j)] = s;
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < E; e += kThreads) {
-    float s = slab[0][e];
-#pragma unroll
-    for (int i = 1; i < kWaves; ++i) s += slab[i][e];
-    const int n = __popc(mask[e][0]) + __popc(mask[e][1]);
-    if constexpr (kOne) {
-      prob[e] = s;
-      count[e] = n;
+    __syncthreads();
+    const int rows = min(kAtOnce, tokens - tp);
+    if constexpr (kPerThread == 1) {
+      for (int r = static_cast<int>(threadIdx.x) / kCols; r < rows; r += kGroups) acc[0] += prob[r][threadIdx.x % kCols];
     } else {
-      g.prob[static_cast<int64_t>(e) * g.chunks + blockIdx.x] = s;
-      g.hist[static_cast<int64_t>(e) * g.chunks + blockIdx.x] = n;
+#pragma unroll
+      for (int i = 0; i < kPerThread; ++i)
+        for (int r = 0; r < rows; ++r) acc[i] += prob[r][threadIdx.x + i * kThreads];
     }
+    __syncthreads();
   }
-  if constexpr (kOne) {
-    __syncthreads();
-    if (wave == 0) {
-      const int total = scan_counts(count, first, E);
-      const float b = balance_of(count, [&](int e) { return prob[e]; }, E, total, k);
-      if (lane == 0) *a.balance = b;
-    }
-    __syncthreads();
+  // the threads of a column joined, in the place of the first tokens' probabilities
+  float* const part = &prob[0][0];
+#pragma unroll
+  for (int i = 0; i < kPerThread; ++i) part[threadIdx.x + i * kThreads] = acc[i];
+  __syncthreads();
+  auto expert_prob = [&](int e) {
+    float s = part[e];
+#pragma unroll
+    for (int i = 1; i < kGroups; ++i) s += part[i * kCols + e];
+    return s;
+  };
+  auto expert_count = [&](int e) { return __popc(mask[e][0]) + __popc(mask[e][1]); };
+  if constexpr (!kOne) {
     for (int e = threadIdx.x; e < E; e += kThreads) {
-      a.counts[e] = count[e];
-      a.offsets[e] = first[e];
+      g.prob[static_cast<int64_t>(e) * g.chunks + blockIdx.x] = expert_prob(e);
+      g.hist[static_cast<int64_t>(e) * g.chunks + blockIdx.x] = expert_count(e);
     }
-    if (threadIdx.x == 0) a.offsets[E] = first[E];
-    const int pairs = static_cast<int>(a.tokens) * k;
+  } else {
+    if (threadIdx.x < 64) {
+      const float b = scan_experts<kCols / 64>(E, k, first, expert_count, expert_prob);
+      if (threadIdx.x == 0) *a.balance = b;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e <= E; e += kThreads) {
+      a.offsets[e] = first[e];
+      if (e < E) a.counts[e] = expert_count(e);
+    }
+    const int pairs = tokens * k, total = first[E];
     for (int p = threadIdx.x; p < pairs; p += kThreads) {
-      const int tl = p / k, e = a.pair_expert[p];   // written by this workgroup before its barriers
+      const int tl = p / k, e = pair_e[p];
       int at = -1;
       if (e >= 0) {
-        const uint32_t lo = tl < 32 ? mask[e][0] & ((1u << tl) - 1u) : mask[e][0];
-        const uint32_t hi = tl < 32 ? 0u : mask[e][1] & ((1u << (tl - 32)) - 1u);
-        at = first[e] + __popc(lo) + __popc(hi);
+        at = first[e] + before(mask[e], tl);
         a.row_token[at] = tl;
-        a.row_weight[at] = a.pair_weight[p];
+        a.row_weight[at] = pair_w[p];
       }
       a.pair_row[p] = at;
-      if (p >= first[E]) {
+      if (p >= total) {
         a.row_token[p] = 0;
         a.row_weight[p] = 0.0f;
       }
@@ -296,26 +320,32 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteKernelArgs g) {
 }
 
 // An expert's counts over the chunks turned into the rows before each chunk,
-// and its probabilities added up; a wavefront an expert.
+// and its probabilities added up; a wavefront an expert, 256 chunks at a time.
 __global__ __launch_bounds__(256) void route_scan_kernel(RouteKernelArgs g) {
+  constexpr int kAt = 4;
   const int e = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
   if (e >= g.a.experts) return;
   int32_t* hist = g.hist + static_cast<int64_t>(e) * g.chunks;
   const float* prob = g.prob + static_cast<int64_t>(e) * g.chunks;
   int before = 0;
   float p = 0.0f;
-  for (int c0 = 0; c0 < g.chunks; c0 += 64) {
-    const int c = c0 + lane;
-    const int own = c < g.chunks ? hist[c] : 0;
-    if (c < g.chunks) p += prob[c];
-    int sum = own;
+  for (int c0 = 0; c0 < g.chunks; c0 += 64 * kAt) {
+    int own[kAt];
+    float more[kAt];
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int up = __shfl_up(sum, o);
-      if (lane >= o) sum += up;
+    for (int i = 0; i < kAt; ++i) {
+      const int c = c0 + 64 * i + lane;
+      own[i] = c < g.chunks ? hist[c] : 0;
+      more[i] = c < g.chunks ? prob[c] : 0.0f;
     }
-    if (c < g.chunks) hist[c] = before + sum - own;
-    before += __shfl(sum, 63);
+#pragma unroll
+    for (int i = 0; i < kAt; ++i) {
+      const int c = c0 + 64 * i + lane;
+      const int sum = scan64(own[i]);
+      if (c < g.chunks) hist[c] = before + sum - own[i];
+      before += __builtin_amdgcn_readlane(sum, 63);
+      p += more[i];
+    }
   }
   p = sum64(p);
   if (lane == 0) {
@@ -324,44 +354,56 @@ __global__ __launch_bounds__(256) void route_scan_kernel(RouteKernelArgs g) {
   }
 }
 
-// A chunk's pairs to their rows
-__global__ __launch_bounds__(256) void route_scatter_kernel(RouteKernelArgs g) {
+// A chunk's pairs to their rows.  Everything it reads is on its way before the
+// first barrier.
+__global__ __launch_bounds__(512) void route_scatter_kernel(RouteKernelArgs g) {
+  constexpr int kAt = 4;   // pairs a thread: 64 tokens of 32
   __shared__ uint32_t mask[kMaxExperts][2];
-  __shared__ int count[kMaxExperts], first[kMaxExperts + 1];
+  __shared__ int count[kMaxExperts], base[kMaxExperts], first[kMaxExperts + 1];
   const RouteArgs& a = g.a;
   const int E = a.experts, k = a.top_k;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kChunk;
   const int pairs = static_cast<int>(min(static_cast<int64_t>(kChunk), a.tokens - t0)) * k;
   const int64_t p0 = t0 * k;
-  for (int e = threadIdx.x; e < E; e += 256) {
-    mask[e][0] = mask[e][1] = 0u;
-    count[e] = a.counts[e];
+  int e[kAt];
+  float w[kAt];
+#pragma unroll
+  for (int i = 0; i < kAt; ++i) {
+    const int p = threadIdx.x + 512 * i;
+    e[i] = p < pairs ? a.pair_expert[p0 + p] : -1;
+    w[i] = p < pairs ? a.pair_weight[p0 + p] : 0.0f;
+  }
+  for (int x = threadIdx.x; x < E; x += 512) {
+    mask[x][0] = mask[x][1] = 0u;
+    count[x] = a.counts[x];
+    base[x] = g.hist[static_cast<int64_t>(x) * g.chunks + blockIdx.x];
   }
   __syncthreads();
-  for (int p = threadIdx.x; p < pairs; p += 256) {
-    const int e = a.pair_expert[p0 + p], tl = p / k;
-    if (e >= 0) atomicOr(&mask[e][tl >> 5], 1u << (tl & 31));
+#pragma unroll
+  for (int i = 0; i < kAt; ++i) {
+    const int tl = (threadIdx.x + 512 * i) / k;
+    if (e[i] >= 0) atomicOr(&mask[e[i]][tl >> 5], 1u << (tl & 31));
   }
   if (threadIdx.x < 64) {
-    const int total = scan_counts(count, first, E);
-    if (blockIdx.x == 0) {
-      const float b = balance_of(count, [&](int e) { return g.prob_total[e]; }, E, total, k);
-      if (threadIdx.x == 0) *a.balance = b;
-    }
+    const bool lead = blockIdx.x == 0;
+    auto prob = [&](int x) { return lead ? g.prob_total[x] : 0.0f; };
+    auto counted = [&](int x) { return count[x]; };
+    const float b = E <= 256 ? scan_experts<4>(E, k, first, counted, prob) : scan_experts<16>(E, k, first, counted, prob);
+    if (lead && threadIdx.x == 0) *a.balance = b;
   }
   __syncthreads();
   if (blockIdx.x == 0)
-    for (int e = threadIdx.x; e <= E; e += 256) a.offsets[e] = first[e];
+    for (int x = threadIdx.x; x <= E; x += 512) a.offsets[x] = first[x];
   const int64_t total = first[E];
-  for (int p = threadIdx.x; p < pairs; p += 256) {
-    const int tl = p / k, e = a.pair_expert[p0 + p];
+#pragma unroll
+  for (int i = 0; i < kAt; ++i) {
+    const int p = threadIdx.x + 512 * i, tl = p / k;
+    if (p >= pairs) break;
     int at = -1;
-    if (e >= 0) {
-      const uint32_t lo = tl < 32 ? mask[e][0] & ((1u << tl) - 1u) : mask[e][0];
-      const uint32_t hi = tl < 32 ? 0u : mask[e][1] & ((1u << (tl - 32)) - 1u);
-      at = first[e] + g.hist[static_cast<int64_t>(e) * g.chunks + blockIdx.x] + __popc(lo) + __popc(hi);
+    if (e[i] >= 0) {
+      at = first[e[i]] + base[e[i]] + before(mask[e[i]], tl);
       a.row_token[at] = static_cast<int32_t>(t0) + tl;
-      a.row_weight[at] = a.pair_weight[p0 + p];
+      a.row_weight[at] = w[i];
     }
     a.pair_row[p0 + p] = at;
     if (p0 + p >= total) {
@@ -523,7 +565,7 @@ hipError_t launch_route(const RouteArgs& a, void* ws, hipStream_t s) {
   a.bf16 ? with_n(bf16_t{}) : with_n(0.0f);
   if (!one) {
     hipLaunchKernelGGL(route_scan_kernel, dim3((a.experts + 3) / 4), dim3(256), 0, s, g);
-    hipLaunchKernelGGL(route_scatter_kernel, grid, dim3(256), 0, s, g);
+    hipLaunchKernelGGL(route_scatter_kernel, grid, dim3(512), 0, s, g);
   }
   return hipGetLastError();
 }
