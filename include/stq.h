@@ -517,9 +517,9 @@ stq_status stq_token_logprobs_backward(const void* logits, int x_dtype, int64_t 
  *              0), and fp32 [n_rows]; both or neither
  *   y          bf16 bits [n_rows, d], rows y_row_stride elements apart, one
  *              rounding of the fp32 value, or NULL
- * Every pointer is aligned to its elements; rows that all start on 16 bytes
- * are read and written faster.  Sums are fp32 in a fixed order: repeated calls
- * give identical bits.  d >= 1; at most 2^22 rows and 2^26 columns. */
+ * Every pointer is aligned to its elements.  Sums are fp32 in a fixed order:
+ * repeated calls give identical bits.  d >= 1; at most 2^22 rows and 2^26
+ * columns. */
 stq_status stq_rmsnorm_rows(const void* x, int x_dtype, int64_t x_row_stride, const void* residual,
                             int residual_dtype, int64_t residual_row_stride, void* h, int64_t h_row_stride,
                             const float* weight, float eps, int64_t n_rows, int64_t d, float* rstd, int8_t* q,
@@ -624,9 +624,8 @@ stq_status stq_route_tokens_backward(const void* logits, int x_dtype, int64_t ro
  *   pair_weight  fp32 [n_tokens * top_k], or NULL (ones)
  *   y            [n_tokens, d] fp32 or bf16, rows y_row_stride elements apart;
  *                every element is written
- * Every pointer is aligned to its elements; rows that all start on 16 bytes are
- * read and written faster.  Sums are fp32, in order.  1 <= top_k <= 32, d >= 1;
- * at most 2^22 tokens, 2^31 - 1 rows and 2^26 columns, and less than 2^24
+ * Every pointer is aligned to its elements.  Sums are fp32, in order.  1 <=
+ * top_k <= 32, d >= 1; at most 2^22 tokens, 2^31 - 1 rows and 2^26 columns, and less than 2^24
  * started pieces of 512 columns (2048 where d > 512) of a token in all. */
 stq_status stq_combine_rows(const void* z, int z_dtype, int64_t z_row_stride, int64_t n_rows, const int32_t* pair_row,
                             const float* pair_weight, int64_t n_tokens, int64_t top_k, int64_t d, void* y, int y_dtype,

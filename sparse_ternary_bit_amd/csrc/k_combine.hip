@@ -18,7 +18,7 @@ namespace {
 constexpr int kBatch = 8;  // rows of a token in flight
 
 // Workgroup: one token, blockDim.x * 8 columns
-template <typename TZ, typename TY, bool kVec>
+template <typename TZ, typename TY>
 __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a, int col_blocks) {
   const int64_t t = blockIdx.x / col_blocks;
   const int64_t c = (static_cast<int64_t>(blockIdx.x % col_blocks) * blockDim.x + threadIdx.x) * 8;
@@ -38,7 +38,7 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a, int col_blo
       const int32_t row = rows[jj];
       on[j] = j0 + j < a.top_k && row >= 0 && row < a.n_rows;
       w[j] = a.weight ? a.weight[t * a.top_k + jj] : 1.0f;
-      if (on[j]) raw[j] = load8<TZ, kVec>(z + row * a.z_stride, c, a.d);
+      if (on[j]) raw[j] = load8<TZ>(z + row * a.z_stride, c, a.d);
     }
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
@@ -49,12 +49,12 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a, int col_blo
       for (int e = 0; e < 8; ++e) y[e] = fmaf(w[j], v[e], y[e]);
     }
   }
-  store8<TY, kVec>(static_cast<TY*>(a.y) + t * a.y_stride, c, a.d, pack8<TY>(y));
+  store8<TY>(static_cast<TY*>(a.y) + t * a.y_stride, c, a.d, pack8<TY>(y));
 }
 
 // Workgroup: one token; its rows in batches of kBatch, dy read again for each
 // batch (from cache)
-template <typename TY, typename TZ, typename TD, bool kVec, int kThreads>
+template <typename TY, typename TZ, typename TD, int kThreads>
 __global__ __launch_bounds__(kThreads) void combine_bwd_kernel(CombineBwdArgs a) {
   __shared__ float part[kThreads / 64][kBatch];
   const int64_t t = blockIdx.x;
@@ -76,11 +76,11 @@ __global__ __launch_bounds__(kThreads) void combine_bwd_kernel(CombineBwdArgs a)
     for (int64_t c = threadIdx.x * 8; c < a.d; c += kThreads * 8) {
       float g[8];
       Raw8<TZ> raw[kBatch];
-      const Raw8<TY> ry = load8<TY, kVec>(dy, c, a.d);
+      const Raw8<TY> ry = load8<TY>(dy, c, a.d);
       if (a.dw) {
 #pragma unroll
         for (int j = 0; j < kBatch; ++j)
-          if (row[j] >= 0) raw[j] = load8<TZ, kVec>(z + row[j] * a.z_stride, c, a.d);
+          if (row[j] >= 0) raw[j] = load8<TZ>(z + row[j] * a.z_stride, c, a.d);
       }
       unpack8<TY>(ry, g);
 #pragma unroll
@@ -96,7 +96,7 @@ __global__ __launch_bounds__(kThreads) void combine_bwd_kernel(CombineBwdArgs a)
           float o[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) o[e] = w[j] * g[e];
-          store8<TD, kVec>(dz + row[j] * a.dz_stride, c, a.d, pack8<TD>(o));
+          store8<TD>(dz + row[j] * a.dz_stride, c, a.d, pack8<TD>(o));
         }
       }
     }
@@ -118,10 +118,6 @@ __global__ __launch_bounds__(kThreads) void combine_bwd_kernel(CombineBwdArgs a)
   }
 }
 
-bool vec16(const void* p, int64_t stride, int64_t esz) {
-  return !p || ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride * esz % 16 == 0);
-}
-int64_t esize(int bf16) { return bf16 ? 2 : 4; }
 
 int combine_threads(int64_t d) { return d <= 512 ? 64 : 256; }
 
@@ -133,30 +129,23 @@ int64_t combine_col_blocks(int64_t d) {
 }
 
 hipError_t launch_combine_rows(const CombineArgs& a, hipStream_t s) {
-  const bool vec = vec16(a.z, a.z_stride, esize(a.z_bf16)) && vec16(a.y, a.y_stride, esize(a.y_bf16));
   const int64_t cb = combine_col_blocks(a.d);
-  auto go = [&](auto z, auto y, auto v) {
-    hipLaunchKernelGGL((combine_kernel<decltype(z), decltype(y), decltype(v)::value>), dim3(static_cast<unsigned>(a.tokens * cb)),
-                       dim3(combine_threads(a.d)), 0, s, a, static_cast<int>(cb));
+  auto go = [&](auto z, auto y) {
+    hipLaunchKernelGGL((combine_kernel<decltype(z), decltype(y)>), dim3(static_cast<unsigned>(a.tokens * cb)), dim3(combine_threads(a.d)), 0,
+                       s, a, static_cast<int>(cb));
   };
-  auto with_vec = [&](auto z, auto y) { vec ? go(z, y, std::true_type{}) : go(z, y, std::false_type{}); };
-  auto with_y = [&](auto z) { a.y_bf16 ? with_vec(z, bf16_t{}) : with_vec(z, 0.0f); };
+  auto with_y = [&](auto z) { a.y_bf16 ? go(z, bf16_t{}) : go(z, 0.0f); };
   a.z_bf16 ? with_y(bf16_t{}) : with_y(0.0f);
   return hipGetLastError();
 }
 
 hipError_t launch_combine_rows_bwd(const CombineBwdArgs& a, hipStream_t s) {
-  const bool vec = vec16(a.dy, a.dy_stride, esize(a.dy_bf16)) && vec16(a.z, a.z_stride, esize(a.z_bf16)) &&
-                   vec16(a.dz, a.dz_stride, esize(a.dz_bf16));
-  auto go = [&](auto y, auto z, auto dz, auto v) {
+  auto go = [&](auto y, auto z, auto dz) {
     const dim3 grid(static_cast<unsigned>(a.tokens));
-    if (a.d <= 512)
-      hipLaunchKernelGGL((combine_bwd_kernel<decltype(y), decltype(z), decltype(dz), decltype(v)::value, 64>), grid, dim3(64), 0, s, a);
-    else
-      hipLaunchKernelGGL((combine_bwd_kernel<decltype(y), decltype(z), decltype(dz), decltype(v)::value, 256>), grid, dim3(256), 0, s, a);
+    if (a.d <= 512) hipLaunchKernelGGL((combine_bwd_kernel<decltype(y), decltype(z), decltype(dz), 64>), grid, dim3(64), 0, s, a);
+    else hipLaunchKernelGGL((combine_bwd_kernel<decltype(y), decltype(z), decltype(dz), 256>), grid, dim3(256), 0, s, a);
   };
-  auto with_vec = [&](auto y, auto z, auto dz) { vec ? go(y, z, dz, std::true_type{}) : go(y, z, dz, std::false_type{}); };
-  auto with_dz = [&](auto y, auto z) { a.dz_bf16 ? with_vec(y, z, bf16_t{}) : with_vec(y, z, 0.0f); };
+  auto with_dz = [&](auto y, auto z) { a.dz_bf16 ? go(y, z, bf16_t{}) : go(y, z, 0.0f); };
   auto with_z = [&](auto y) { a.z_bf16 ? with_dz(y, bf16_t{}) : with_dz(y, 0.0f); };
   a.dy_bf16 ? with_z(bf16_t{}) : with_z(0.0f);
   return hipGetLastError();

@@ -66,7 +66,6 @@ struct NtArgs {
   int splits;             // parts of the sum
   uint16_t* out;          // bf16 [m][ld_out] instead of acc's store (with add: acc is added first)
   int64_t ld_out;
-  int vec;                // out's rows start on 16 bytes
 };
 
 // Output channels of a pair of 16-row MFMA tiles: row r of tile h stands for
@@ -121,13 +120,17 @@ struct Slab {
   __device__ __forceinline__ char* at(int t, int chunk) const { return mem + t * kC * 2 + ((chunk ^ (tile_swizzle(t) & (kChunks - 1))) << 4); }
   // this wavefront's stores before, its loads after (LDS serves a wavefront in order)
   static __device__ __forceinline__ void fence() { asm volatile("" ::: "memory"); }
-  // rows t < rows, chunks below `width` channels, to out (16-byte aligned rows)
-  __device__ __forceinline__ void store_rows(uint16_t* out, int64_t ld, int rows, int width) const {
+  // rows t < rows, chunks below `width` channels, to out; once: whole lines that
+  // nothing reads again soon pass the caches by
+  __device__ __forceinline__ void store_rows(uint16_t* out, int64_t ld, int rows, int width, bool once = false) const {
 #pragma unroll
     for (int i = 0; i < 32 * kChunks / 64; ++i) {
       const int t = (i * 64 + lane) / kChunks, c = (i * 64 + lane) % kChunks;
       const u32x4_t v = *reinterpret_cast<const u32x4_t*>(at(t, c));
-      if (t < rows && c * 8 < width) *reinterpret_cast<u32x4_t*>(out + t * ld + c * 8) = v;
+      if (t < rows && c * 8 < width) {
+        if (once) __builtin_nontemporal_store(v, &reinterpret_cast<Words16*>(out + t * ld + c * 8)->v);
+        else store16b(out + t * ld + c * 8, v);
+      }
     }
   }
   // the same transposed: out[channel][token], channels below `width`, tokens below `rows` (a multiple of 8).
@@ -177,7 +180,6 @@ __device__ __forceinline__ void finish(const NtArgs& a, typename Mfma<kI8>::acc_
   if constexpr (kEpi == kSum) {
     const Slab<kC> sl{slab, lane};
     auto row_of = [&](int64_t tok) { return a.acc + (static_cast<int64_t>(split) * a.m + tok) * a.ld_acc; };
-    const bool rows_whole = a.out && a.vec;   // 16-byte rows of bf16, through LDS
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
       take(j);
@@ -201,14 +203,14 @@ __device__ __forceinline__ void finish(const NtArgs& a, typename Mfma<kI8>::acc_
           }
         }
       }
-      if (rows_whole) {
+      if (a.out) {   // whole rows, through LDS
 #pragma unroll
         for (int p = 0; p < kP; ++p) {
           const int c = 32 * p + 8 * q;
           const Raw8<bf16_t> o = pack8<bf16_t>(v[p]);
           *reinterpret_cast<u32x4_t*>(sl.at(16 * (j & 1) + r, c / 8)) = o.w[0];
           // the last channels of an odd width belong to no whole chunk
-          if (c + 8 > nv && c < nv && tok < a.m) store8<bf16_t, false>(reinterpret_cast<bf16_t*>(a.out) + tok * a.ld_out, n0 + c, a.n, o);
+          if (c + 8 > nv && c < nv && tok < a.m) store8<bf16_t>(reinterpret_cast<bf16_t*>(a.out) + tok * a.ld_out, n0 + c, a.n, o);
         }
         if ((j & 1) || j + 1 == FM) {
           sl.fence();
@@ -221,13 +223,9 @@ __device__ __forceinline__ void finish(const NtArgs& a, typename Mfma<kI8>::acc_
         for (int p = 0; p < kP; ++p) {
           const int c = 32 * p + 8 * q;
           if (c >= nv) continue;
-          if (a.out) {
-            store8<bf16_t, false>(reinterpret_cast<bf16_t*>(a.out) + tok * a.ld_out, n0 + c, a.n, pack8<bf16_t>(v[p]));
-          } else {
-            f32x4_t* const o = reinterpret_cast<f32x4_t*>(row_of(tok) + n0 + c);
-            o[0] = f32x4_t{v[p][0], v[p][1], v[p][2], v[p][3]};
-            o[1] = f32x4_t{v[p][4], v[p][5], v[p][6], v[p][7]};
-          }
+          f32x4_t* const o = reinterpret_cast<f32x4_t*>(row_of(tok) + n0 + c);
+          o[0] = f32x4_t{v[p][0], v[p][1], v[p][2], v[p][3]};
+          o[1] = f32x4_t{v[p][4], v[p][5], v[p][6], v[p][7]};
         }
       }
     }
@@ -677,6 +675,335 @@ __global__ __launch_bounds__(256, 1) void nt_wide_kernel(NtArgs a) {
   }
 }
 
+// At most 16 tokens: the head's stream is the bound, or, under a short
+// vocabulary, the chain along the sum.  A workgroup of 8 wavefronts owns 16
+// channels and all tokens; the wavefronts share the sum, each loading its part
+// of the head once, straight into matrix-core operands (16 bytes a lane, kBatch
+// steps in flight), the tokens from cache the same way, and the eight sums are
+// added through LDS.  (2 rows under a head of 566 x 5863, the logits of the
+// gradient: 24 us in tiles of 64.)
+constexpr int kFewWaves = 8, kFewBatch = 8;
+
+template <bool kI8, int kEpi>
+__global__ __launch_bounds__(kFewWaves * 64, 2) void nt_few_kernel(NtArgs a) {
+  typedef typename Mfma<kI8>::acc_t acc_t;
+  __shared__ acc_t part[kFewWaves][64];
+  __shared__ __align__(16) uint16_t turned[16][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int q = lane >> 4, r = lane & 15;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
+  const int nv = static_cast<int>(min(int64_t{16}, a.n - n0));   // none in the padding of dl
+  if (nv > 0) {
+    const uint32_t kpad = static_cast<uint32_t>((a.kbytes + 15) & ~15);
+    const Rsrc rw = make_rsrc(a.w + n0 * a.ldw, static_cast<uint32_t>((nv - 1) * a.ldw) + kpad);
+    const Rsrc ra = make_rsrc(a.a, static_cast<uint32_t>((a.m - 1) * a.lda) + kpad);
+    const int steps = static_cast<int>((a.kbytes + kStep - 1) / kStep);
+    const int per = (steps + kFewWaves - 1) / kFewWaves, s0 = wave * per, s1 = min(steps, s0 + per);
+    constexpr uint32_t kOut = 0xFFFFFFF0u;  // past every range: reads as 0, touches nothing
+    const uint32_t vw = r < nv ? r * static_cast<uint32_t>(a.ldw) + q * 16 : kOut;
+    const uint32_t va = r < a.m ? r * static_cast<uint32_t>(a.lda) + q * 16 : kOut;
+    auto load = [&](Rsrc rs, uint32_t base, int s) {
+      // a row's bytes from kpad on belong to the next row: not read
+      const uint32_t off = base != kOut && s < s1 && s * kStep + q * 16 < static_cast<int>(kpad) ? base + s * kStep : kOut;
+      return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, static_cast<int>(off), 0, 0));
+    };
+    acc_t acc = acc_t{0, 0, 0, 0};
+    for (int s = s0; s < s1; s += kFewBatch) {
+      u32x4_t w[kFewBatch], x[kFewBatch];
+#pragma unroll
+      for (int b = 0; b < kFewBatch; ++b) {
+        w[b] = load(rw, vw, s + b);
+        x[b] = load(ra, va, s + b);
+      }
+      if (s + kFewBatch >= steps && (a.kbytes & 15)) {
+        // the last chunk's bytes behind the end count for nothing
+#pragma unroll
+        for (int b = 0; b < kFewBatch; ++b) {
+          const int left = static_cast<int>(a.kbytes) - ((s + b) * kStep + q * 16);
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            x[b][d] &= byte_mask(left - 4 * d);
+            if constexpr (!kI8) w[b][d] &= byte_mask(left - 4 * d);
+          }
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < kFewBatch; ++b) acc = Mfma<kI8>::run(w[b], x[b], acc);
+    }
+    part[wave][lane] = acc;
+  }
+  __syncthreads();
+  if (wave) return;
+  // token r, channels n0 + 4 q + 0..3
+  float l[4], scale[4];
+  const bool on = r < a.m;
+  const float ts = kI8 && on ? a.as[r] : 1.0f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) scale[e] = kI8 && 4 * q + e < nv ? a.ws[n0 + 4 * q + e] : 1.0f;
+  acc_t sum = acc_t{0, 0, 0, 0};
+  if (nv > 0) {
+    sum = part[0][lane];
+#pragma unroll
+    for (int i = 1; i < kFewWaves; ++i) sum += part[i][lane];
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) l[e] = kI8 ? static_cast<float>(sum[e]) * ts * scale[e] : static_cast<float>(sum[e]);
+  const int64_t target = on ? a.targets[r] : -1;
+  const int64_t want = target - a.v0 - n0 - 4 * q;
+  if constexpr (kEpi == kStats) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (4 * q + e >= nv) l[e] = -INFINITY;
+      else if (target >= 0 && want == e) a.hit[r] = l[e];
+      m = fmaxf(m, l[e]);
+    }
+    m = fmaxf(m, __shfl_xor(m, 16));
+    m = fmaxf(m, __shfl_xor(m, 32));
+    const float base = m == -INFINITY ? 0.0f : m;
+    float s = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s += exp_of(l[e] - base);
+    s += __shfl_xor(s, 16);
+    s += __shfl_xor(s, 32);
+    if (q == 0 && on) a.stats[static_cast<int64_t>(blockIdx.x) * a.m + r] = float2{m, s};
+  } else {
+    const float lse = on ? a.lse[r] : 0.0f;
+    const bool dead = target < 0 || target >= a.vocab || lse == -INFINITY;
+    const float g = dead ? 0.0f : a.g[r];
+    uint32_t d[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float v = exp_of(l[e] - lse) - (want == e ? 1.0f : 0.0f);
+      v *= g;
+      if (kI8) v *= scale[e];
+      d[e] = bf16_round(dead || 4 * q + e >= nv ? 0.0f : v);
+    }
+    if (on) *reinterpret_cast<u32x2_t*>(a.dl + r * a.ld_dl + n0 + 4 * q) = u32x2_t{d[0] | d[1] << 16, d[2] | d[3] << 16};
+    if (a.dlt) {
+      // [channel][token], zeros for tokens up to a whole stage
+      u32x4_t* const flat = reinterpret_cast<u32x4_t*>(&turned[0][0]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) flat[lane + 64 * i] = u32x4_t{0, 0, 0, 0};
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int e = 0; e < 4; ++e) turned[4 * q + e][r] = static_cast<uint16_t>(d[e]);
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int c = (lane + 64 * i) >> 3, t = (lane & 7) * 8;
+        if (c < nv) *reinterpret_cast<u32x4_t*>(a.dlt + (n0 + c) * a.ld_dlt + t) = flat[lane + 64 * i];
+      }
+    }
+  }
+}
+
+// dx of few rows, straight from the head as it lies, which is read once more:
+// a workgroup adds dl[., v] w[v, c] for 128 columns c and its share of the
+// words v, 64 at a time.  The matrix cores want eight words of one column, so
+// the head's tile [word][column] is read with the transposing LDS read; 8-bit
+// words become bf16, which holds them exactly, on their way through LDS.
+// Direct loads run two stages (8-bit: three) ahead.  (36 rows under 44492 x
+// 4782: 48 us and 110 for a transposed copy of the head before it.)
+constexpr int kDxWords = 64, kDxCols = 128;
+
+struct DxFewArgs {
+  const uint16_t* dl;   // [m][ld_dl], zeros from n to n_pad
+  int64_t ld_dl;
+  const char* w;
+  int64_t ldw;          // bytes
+  int64_t m, n, k;
+  float* acc;           // [splits][m][ld_acc]
+  int64_t ld_acc;
+  int strips, per;      // column strips; stages of a split
+};
+
+template <bool kI8, int NT>
+__global__ __launch_bounds__(256) void head_dx_few_kernel(DxFewArgs a) {
+  constexpr int kBuf = kI8 ? 4 : 3;
+  constexpr int kWBytes = kDxWords * kDxCols * (kI8 ? 1 : 2), kTBytes = NT * 16 * kDxWords * 2;
+  constexpr int kLW = kWBytes / 1024 / 4, kLT = kTBytes / 1024 / 4;  // load instructions a stage and wavefront
+  static_assert(kLT >= 1, "every wavefront issues the same loads");
+  __shared__ __align__(16) char sw[kBuf][kWBytes];
+  __shared__ __align__(16) char st[kBuf][kTBytes];
+  __shared__ __align__(16) char wide[kI8 ? 2 : 1][kI8 ? kDxWords * kDxCols * 2 : 16];  // 8-bit words as bf16
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int q = lane >> 4, r = lane & 15;
+  const int strip = blockIdx.x % a.strips, split = blockIdx.x / a.strips;
+  const int64_t c0 = static_cast<int64_t>(strip) * kDxCols;
+  const int esz = kI8 ? 1 : 2;
+  const int width = static_cast<int>(min(static_cast<int64_t>(kDxCols) * esz, ((a.k * esz + 15) & ~int64_t{15}) - c0 * esz));  // bytes of a row here
+  const int all = static_cast<int>((a.n + kDxWords - 1) / kDxWords);
+  const int s_lo = split * a.per, ns = max(0, min(all - s_lo, a.per));
+  auto stage = [&](int s) {
+    const int buf = s % kBuf;
+    const int64_t v0 = static_cast<int64_t>(s_lo + s) * kDxWords;
+    const bool real = s < ns;
+    const int vv = real ? static_cast<int>(min(static_cast<int64_t>(kDxWords), a.n - v0)) : 0;
+    const Rsrc rw = make_rsrc(a.w + (real ? v0 * a.ldw + c0 * esz : 0), real ? static_cast<uint32_t>((vv - 1) * a.ldw) + width : 0);
+    const Rsrc rt = make_rsrc(a.dl + (real ? v0 : 0), real ? static_cast<uint32_t>((a.m - 1) * a.ld_dl * 2) + kDxWords * 2 : 0);
+    constexpr int kPer = kI8 ? 8 : 16;  // 16-byte chunks of a word's row
+#pragma unroll
+    for (int i = 0; i < kLW; ++i) {
+      const int ins = wave + 4 * i, t = ins * (64 / kPer) + lane / kPer;
+      const int c = (lane % kPer) ^ (kI8 ? 0 : tile_swizzle(t));
+      lds_load16(rw, sw[buf] + ins * 1024, t < vv && c * 16 < width ? t * static_cast<uint32_t>(a.ldw) + c * 16 : 0xFFFFFFF0u);
+    }
+#pragma unroll
+    for (int i = 0; i < kLT; ++i) {
+      const int ins = wave + 4 * i, t = ins * 8 + (lane >> 3);
+      lds_load16(rt, st[buf] + ins * 1024, t < a.m ? t * static_cast<uint32_t>(a.ld_dl * 2) + (((lane & 7) ^ token_swizzle(t)) << 4) : 0xFFFFFFF0u);
+    }
+  };
+  f32x4_t acc[2][NT];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+  for (int s = 0; s < kBuf - 1; ++s) stage(s);
+  for (int s = 0; s < ns; ++s) {
+    // stage s has landed, here and for everyone, and everyone has read stage s - 1
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((kLW + kLT) * (kBuf - 2)) : "memory");
+    stage(s + kBuf - 1);
+    const char* tile = sw[s % kBuf];
+    if constexpr (kI8) {
+      char* const to = wide[s & 1];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int idx = threadIdx.x + 256 * i, t = idx >> 3, c = idx & 7;
+        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(tile + idx * 16);
+        float f[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) f[e] = static_cast<float>(static_cast<int8_t>(v[e >> 2] >> (8 * (e & 3))));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          u32x4_t o;
+          // whole numbers of at most 8 bits: their lower halves are zeros
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            o[e] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, f[8 * h + 2 * e + 1]), __builtin_bit_cast(uint32_t, f[8 * h + 2 * e]), 0x07060302u);
+          *reinterpret_cast<u32x4_t*>(to + t * 256 + (((2 * c + h) ^ tile_swizzle(t)) << 4)) = o;
+        }
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      tile = to;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int t = 32 * h + 8 * q + (r >> 2);
+      u32x2_t lo[2], hi[2];
+      uint32_t at[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        at[i] = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(tile)) + t * 256 + (((wave * 4 + 2 * i + ((r & 3) >> 1)) ^ tile_swizzle(t)) << 4) + (r & 1) * 8;
+      asm volatile(
+          "ds_read_b64_tr_b16 %0, %4\n\tds_read_b64_tr_b16 %1, %4 offset:1024\n\t"
+          "ds_read_b64_tr_b16 %2, %5\n\tds_read_b64_tr_b16 %3, %5 offset:1024\n\ts_waitcnt lgkmcnt(0)"
+          : "=&v"(lo[0]), "=&v"(hi[0]), "=&v"(lo[1]), "=&v"(hi[1])
+          : "v"(at[0]), "v"(at[1])
+          : "memory");
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const int row = 16 * j + r;
+        const u32x4_t x = *reinterpret_cast<const u32x4_t*>(st[s % kBuf] + row * kBK + (((4 * h + q) ^ token_swizzle(row)) << 4));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) acc[i][j] = Mfma<false>::run(u32x4_t{lo[i][0], lo[i][1], hi[i][0], hi[i][1]}, x, acc[i][j]);
+      }
+    }
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // nothing is on its way to LDS when it is given back
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int64_t tok = 16 * j + r;
+    if (tok >= a.m) continue;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t c = c0 + wave * 32 + 16 * i + 4 * q;
+      if (c < a.ld_acc) *reinterpret_cast<f32x4_t*>(a.acc + (split * a.m + tok) * a.ld_acc + c) = acc[i][j];
+    }
+  }
+}
+
+// dW of few rows: the sum is so short that dW's own stream is the bound.  A
+// wavefront holds dl's transpose of 64 words as operands and walks the
+// columns, 64 at a time, with x's transpose from cache.  Eight
+// neighbouring columns of a lane pass through LDS, so that rows leave in pieces
+// of 128 bytes; where those are whole lines, past the caches.  (10 rows of
+// 129372 words: x 7168 422 us, 558 through the caches; x 7024, whose rows start
+// inside lines, 655, 991 past the caches, 1030 in 256 x 256 tiles.)
+struct DwFewArgs {
+  const uint16_t* dlt;   // [n][ld], zeros for tokens up to ld
+  const uint16_t* xt;    // [k][ld], likewise
+  int64_t ld;            // 64 or 128
+  int64_t n, k;
+  uint16_t* dw;
+  int64_t ld_dw;
+};
+
+template <int kHalves>  // 64 tokens each
+__global__ __launch_bounds__(256) void head_dw_few_kernel(DwFewArgs a) {
+  constexpr int kSteps = 2 * kHalves;  // of 32 tokens
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int q = lane >> 4, r = lane & 15;
+  __shared__ __align__(16) char slab[4][32 * 64 * 2];
+  const Slab<64> sl{slab[wave], lane};
+  const bool lines = ((reinterpret_cast<uintptr_t>(a.dw) | static_cast<uintptr_t>(a.ld_dw * 2)) & 127) == 0;
+  const int64_t v0 = static_cast<int64_t>(blockIdx.x) * 64;
+  u32x4_t d[4][kSteps];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int64_t row = min(v0 + 16 * j + r, a.n - 1);
+#pragma unroll
+    for (int h = 0; h < kSteps; ++h) d[j][h] = *reinterpret_cast<const u32x4_t*>(a.dlt + row * a.ld + 32 * h + 8 * q);
+  }
+  const int64_t groups = (a.k + 63) / 64;
+  for (int64_t g = blockIdx.y * 4 + wave; g < groups; g += gridDim.y * 4) {
+    const int64_t c0 = g * 64;
+    f32x4_t acc[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+    for (int h = 0; h < kSteps; ++h) {
+      u32x4_t x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t col = min(c0 + 32 * (i >> 1) + pair_channel(r, i & 1), a.k - 1);
+        x[i] = *reinterpret_cast<const u32x4_t*>(a.xt + col * a.ld + 32 * h + 8 * q);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = Mfma<false>::run(x[i], d[j][h], acc[i][j]);
+    }
+    // word v0 + 16 j + r, columns c0 + 32 p + 8 q + 0..7: to pieces of 128 bytes
+    // through LDS
+    const int nv = static_cast<int>(min(int64_t{64}, a.k - c0));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t row = v0 + 16 * j + r;
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const int c = 32 * p + 8 * q;
+        float o[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = acc[2 * p + (e >> 2)][j][e & 3];
+        const Raw8<bf16_t> b = pack8<bf16_t>(o);
+        *reinterpret_cast<u32x4_t*>(sl.at(16 * (j & 1) + r, c / 8)) = b.w[0];
+        if (c + 8 > nv && c < nv && row < a.n) store8<bf16_t>(reinterpret_cast<bf16_t*>(a.dw) + row * a.ld_dw, c0 + c, a.k, b);
+      }
+      if (j & 1) {
+        sl.fence();
+        const int64_t t0 = v0 + 16 * (j - 1);
+        sl.store_rows(a.dw + t0 * a.ld_dw + c0, a.ld_dw, static_cast<int>(min(int64_t{32}, a.n - t0)), nv & ~7, lines);
+        sl.fence();
+      }
+    }
+  }
+}
+
 // (maximum, sum of exp(l - maximum)) of two sets of logits; a set without a
 // maximum has sum 0, or NaN.
 __device__ __forceinline__ float2 join(float2 a, float2 b) {
@@ -684,40 +1011,43 @@ __device__ __forceinline__ float2 join(float2 a, float2 b) {
   return float2{m, (a.x == -INFINITY ? a.y : a.y * exp_of(a.x - m)) + (b.x == -INFINITY ? b.y : b.y * exp_of(b.x - m))};
 }
 
-// The parts of a token joined: 16 tokens a workgroup, 64 threads each, so that
-// few tokens with many parts are not one long chain (37 tokens with 1564 parts:
-// 17 us with 64 tokens a workgroup and 16 threads each).
+// The parts of a token joined, kTok tokens a workgroup: 16 of them, whose
+// parts lie side by side, or, where there are few, one (one token with 6250
+// parts: 24 us with 16).
+template <int kTok>
 __global__ __launch_bounds__(1024) void head_join_kernel(const float2* stats, const float* hit, const int32_t* targets, int64_t m,
                                                          int parts, int64_t vocab, float* loss, float* lse) {
-  __shared__ float2 slot[16][16];
-  const int tok = threadIdx.x & 15, wave = threadIdx.x >> 6;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * 16 + tok;
+  constexpr int kShare = 1024 / kTok;  // threads a token
+  __shared__ float2 slot[16][kTok];
+  const int tok = threadIdx.x % kTok, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kTok + tok;
   float2 v = {-INFINITY, 0.0f};
   if (t < m) {
-    int i = threadIdx.x >> 4;
-    for (; i + 7 * 64 < parts; i += 8 * 64) {
+    int i = threadIdx.x / kTok;
+    for (; i + 7 * kShare < parts; i += 8 * kShare) {
       float2 w[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = stats[(i + e * 64) * m + t];
+      for (int e = 0; e < 8; ++e) w[e] = stats[(i + e * kShare) * m + t];
 #pragma unroll
       for (int e = 4; e >= 1; e >>= 1)
 #pragma unroll
         for (int f = 0; f < e; ++f) w[f] = join(w[f], w[f + e]);
       v = join(v, w[0]);
     }
-    for (; i < parts; i += 64) v = join(v, stats[i * m + t]);
+    for (; i < parts; i += kShare) v = join(v, stats[i * m + t]);
   }
+  auto lanes = [&] {
 #pragma unroll
-  for (int o = 16; o <= 32; o <<= 1) v = join(v, float2{__shfl_xor(v.x, o), __shfl_xor(v.y, o)});
-  if ((threadIdx.x & 63) < 16) slot[wave][tok] = v;
+    for (int o = kTok; o < 64; o <<= 1) v = join(v, float2{__shfl_xor(v.x, o), __shfl_xor(v.y, o)});
+  };
+  lanes();
+  if (lane < kTok) slot[wave][lane] = v;
   __syncthreads();
-  if (threadIdx.x >= 64) return;
-  v = slot[threadIdx.x >> 4][tok];
-#pragma unroll
-  for (int i = 4; i < 16; i += 4) v = join(v, slot[(threadIdx.x >> 4) + i][tok]);
-#pragma unroll
-  for (int o = 16; o <= 32; o <<= 1) v = join(v, float2{__shfl_xor(v.x, o), __shfl_xor(v.y, o)});
-  if (threadIdx.x >= 16 || t >= m) return;
+  if (wave) return;
+  v = float2{-INFINITY, 0.0f};
+  for (int i = lane / kTok; i < 16; i += 64 / kTok) v = join(v, slot[i][tok]);
+  lanes();
+  if (lane >= kTok || t >= m) return;
   const float logs = __builtin_amdgcn_logf(v.y) * kLn2;
   const bool none = v.x == -INFINITY && v.y == 0.0f;
   lse[t] = none ? -INFINITY : v.x + logs;
@@ -768,15 +1098,30 @@ __global__ __launch_bounds__(256) void transpose_kernel(const char* in, int64_t 
   }
 }
 
-// The parts of a split sum, in order, rounded to bf16
+// The parts of a split sum, rounded to bf16: 64 sums a workgroup, every fourth
+// part a thread.
 __global__ __launch_bounds__(256) void join_splits_kernel(const float* acc, int64_t ld_acc, int splits, int64_t m, int64_t n,
                                                           uint16_t* out, int64_t ld_out) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= m * n) return;
+  __shared__ float part[4][64];
+  const int lane = threadIdx.x & 63, g = threadIdx.x >> 6;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 64 + lane;
   const int64_t row = i / n, c = i - row * n;
-  float s = acc[row * ld_acc + c];
-  for (int p = 1; p < splits; ++p) s += acc[(p * m + row) * ld_acc + c];
-  out[row * ld_out + c] = static_cast<uint16_t>(bf16_round(s));
+  float s = 0.0f;
+  if (i < m * n) {
+    int p = g;
+    for (; p + 28 < splits; p += 32) {
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = acc[((p + 4 * e) * m + row) * ld_acc + c];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s += v[e];
+    }
+    for (; p < splits; p += 4) s += acc[(p * m + row) * ld_acc + c];
+  }
+  part[g][lane] = s;
+  __syncthreads();
+  if (g || i >= m * n) return;
+  out[row * ld_out + c] = static_cast<uint16_t>(bf16_round((part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane])));
 }
 
 __global__ __launch_bounds__(256) void zero_rows_kernel(uint16_t* out, int64_t ld, int64_t m, int64_t n) {
@@ -794,11 +1139,16 @@ void launch_tile(NtArgs a, int step_n, hipStream_t s) {
   hipLaunchKernelGGL((nt_kernel<kI8, kEpi, TM, TN, WM, WN, kBuf, kWavesPerSimd>), grid, dim3(WM * WN * 64), 0, s, a);
 }
 
-// The tile for m tokens and n channels
-enum Tile { k64x64, k64x256, k128x128, k256x256 };
+// The tile for m tokens and n channels.
+//  * Few tokens under a head: a workgroup for 16 channels, until its re-reads of
+//    the tokens weigh on a long channel list.
+//  * Up to 64 tokens: as wide a channel tile as leaves every CU two.
+//  * More: the smallest of three estimates, in rounds of the chip.
+enum Tile { kFew, k64x64, k64x128, k64x256, k128x128, k256x256 };
 
-Tile pick_tile(int64_t m, int64_t n, int cus) {
-  if (m <= 64) return n <= 64 * cus ? k64x64 : k64x256;
+Tile pick_tile(int64_t m, int64_t n, int cus, bool few) {
+  if (few && (m <= 4 || (m <= 16 && n <= 128 * cus))) return kFew;
+  if (m <= 64) return n <= 128 * cus ? k64x64 : n <= 256 * cus ? k64x128 : k64x256;
   auto per_cu = [&](int64_t t) { return (((m + t - 1) / t) * ((n + t - 1) / t) + cus - 1) / cus; };
   const int64_t u256 = per_cu(256), u128 = per_cu(128), u64 = per_cu(64);
   constexpr int64_t k64[3] = {0, 17, 25};
@@ -806,15 +1156,22 @@ Tile pick_tile(int64_t m, int64_t n, int cus) {
   if (t256 <= t128 && t256 <= t64) return k256x256;
   return t128 <= t64 ? k128x128 : k64x64;
 }
-int tile_m(Tile t) { return t == k256x256 ? 256 : t == k128x128 ? 128 : 64; }
-int tile_n(Tile t) { return t == k256x256 || t == k64x256 ? 256 : t == k128x128 ? 128 : 64; }
-int tile_parts(Tile t) { return t == k64x256 ? 4 : 2; }  // wavefronts along a tile's channels
+int tile_m(Tile t) { return t == k256x256 ? 256 : t == k128x128 ? 128 : t == kFew ? 16 : 64; }
+int tile_n(Tile t) { return t == k256x256 || t == k64x256 ? 256 : t == k128x128 || t == k64x128 ? 128 : t == kFew ? 16 : 64; }
+int tile_parts(Tile t) { return t == k64x256 || t == k64x128 ? 4 : t == kFew ? 1 : 2; }  // wavefronts along a tile's channels
 int64_t stat_parts(Tile t, int64_t vocab) { return (vocab + tile_n(t) - 1) / tile_n(t) * tile_parts(t); }
 
 template <bool kI8, int kEpi>
 void launch_nt(const NtArgs& a, Tile t, int cus, hipStream_t s) {
   switch (t) {
+    case kFew:
+      if constexpr (kEpi != kSum) {
+        const int64_t n = kEpi == kGrad ? a.n_pad : a.n;
+        hipLaunchKernelGGL((nt_few_kernel<kI8, kEpi>), dim3(static_cast<unsigned>((n + 15) / 16)), dim3(kFewWaves * 64), 0, s, a);
+      }
+      break;
     case k64x64: launch_tile<kI8, kEpi, 64, 64, 2, 2, 3, 2>(a, 64, s); break;
+    case k64x128: launch_tile<kI8, kEpi, 64, 128, 1, 4, 3, 2>(a, 128, s); break;
     case k64x256: launch_tile<kI8, kEpi, 64, 256, 1, 4, 2, 2>(a, 256, s); break;
     case k128x128: launch_tile<kI8, kEpi, 128, 128, 2, 2, 2, 2>(a, 128, s); break;
     case k256x256: {
@@ -829,6 +1186,8 @@ void launch_nt(const NtArgs& a, Tile t, int cus, hipStream_t s) {
     }
   }
 }
+
+constexpr int64_t kFewRows = 128;   // rows whose gradient reads the head as it lies
 
 int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
@@ -851,13 +1210,13 @@ NtArgs logits_args(const HeadArgs& h) {
 
 HeadLayout head_layout(int64_t rows, int64_t vocab, int cus) {
   HeadLayout l{};
-  l.hit = up(stat_parts(pick_tile(rows, vocab, cus), vocab) * rows * 8, 256);
+  l.hit = up(stat_parts(pick_tile(rows, vocab, cus, true), vocab) * rows * 8, 256);
   l.bytes = l.hit + up(rows * 4, 256);
   return l;
 }
 
 hipError_t launch_head(const HeadArgs& h, float* loss, float* lse, void* ws, int cus, hipStream_t s) {
-  const Tile t = pick_tile(h.rows, h.vocab, cus);
+  const Tile t = pick_tile(h.rows, h.vocab, cus, true);
   const HeadLayout l = head_layout(h.rows, h.vocab, cus);
   NtArgs a = logits_args(h);
   a.stats = static_cast<float2*>(ws);
@@ -866,8 +1225,13 @@ hipError_t launch_head(const HeadArgs& h, float* loss, float* lse, void* ws, int
   else launch_nt<false, kStats>(a, t, cus, s);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(head_join_kernel, dim3(static_cast<unsigned>((h.rows + 15) / 16)), dim3(1024), 0, s, a.stats, a.hit, h.targets,
-                     h.rows, static_cast<int>(stat_parts(t, h.vocab)), h.vocab, loss, lse);
+  const int parts = static_cast<int>(stat_parts(t, h.vocab));
+  if (h.rows <= 256)
+    hipLaunchKernelGGL((head_join_kernel<1>), dim3(static_cast<unsigned>(h.rows)), dim3(1024), 0, s, a.stats, a.hit, h.targets, h.rows, parts,
+                       h.vocab, loss, lse);
+  else
+    hipLaunchKernelGGL((head_join_kernel<16>), dim3(static_cast<unsigned>((h.rows + 15) / 16)), dim3(1024), 0, s, a.stats, a.hit, h.targets,
+                       h.rows, parts, h.vocab, loss, lse);
   return hipGetLastError();
 }
 
@@ -875,6 +1239,27 @@ hipError_t launch_head(const HeadArgs& h, float* loss, float* lse, void* ws, int
 // those the width whose tiles fill whole rounds of the chip best.
 HeadBwdPlan plan_head_bwd(int64_t rows, int64_t vocab, int64_t k, bool dx, bool dw, int cus) {
   HeadBwdPlan p{};
+  const int64_t m_pad = up(rows, 64);
+  if (rows <= kFewRows && rows * up(vocab, 64) <= int64_t{1} << 30) {
+    // the whole vocabulary at once: dl is small beside the head (and its rows within 32-bit offsets)
+    p.few = 1;
+    p.width = up(vocab, 64);
+    p.pieces = 1;
+    int64_t at = up(rows * p.width * 2, 256);
+    p.dlt = at;
+    if (dw) at += up(p.width * m_pad * 2, 256);
+    p.xt = at;
+    if (dw) at += up(k * m_pad * 2, 256);
+    p.acc = at;
+    // two workgroups a CU, of four stages of words at least
+    const int64_t strips = (k + kDxCols - 1) / kDxCols, stages = (vocab + kDxWords - 1) / kDxWords;
+    const int64_t want = std::max<int64_t>(1, std::min((2 * cus + strips - 1) / strips, (stages + 3) / 4));
+    p.per = static_cast<int>((stages + want - 1) / want);
+    p.splits = static_cast<int>((stages + p.per - 1) / p.per);
+    if (dx) at += up(p.splits * rows * up(k, 8) * 4, 256);
+    p.bytes = at;
+    return p;
+  }
   const int64_t cap = std::max<int64_t>(1, std::min((int64_t{1} << 26) / rows, (int64_t{1} << 27) / k) / 256);
   const int64_t cols = (vocab + 255) / 256;
   const int64_t tm = (rows + 255) / 256;
@@ -886,7 +1271,6 @@ HeadBwdPlan plan_head_bwd(int64_t rows, int64_t vocab, int64_t k, bool dx, bool 
   }
   p.width = std::min(best * 256, up(vocab, 64));
   p.pieces = (vocab + p.width - 1) / p.width;
-  const int64_t m_pad = up(rows, 64);
   int64_t at = up(rows * p.width * 2, 256);
   p.dlt = at;
   if (dw) at += up(p.width * m_pad * 2, 256);
@@ -896,7 +1280,7 @@ HeadBwdPlan plan_head_bwd(int64_t rows, int64_t vocab, int64_t k, bool dx, bool 
   if (dx) at += up(k * p.width * 2, 256);
   p.acc = at;
   // few tokens leave few tiles: the sum over the vocabulary is shared out
-  p.tile = pick_tile(rows, k, cus);
+  p.tile = pick_tile(rows, k, cus, false);
   const int64_t tiles = ((rows + tile_m(static_cast<Tile>(p.tile)) - 1) / tile_m(static_cast<Tile>(p.tile))) *
                         ((k + tile_n(static_cast<Tile>(p.tile)) - 1) / tile_n(static_cast<Tile>(p.tile)));
   p.splits = p.tile == k256x256 ? 1 : static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({cus / tiles, p.width / 1024, 16})));
@@ -911,10 +1295,8 @@ hipError_t launch_head_bwd(const HeadArgs& h, const HeadBwdArgs& b, const HeadBw
   uint16_t* dlt = reinterpret_cast<uint16_t*>(base + p.dlt);
   uint16_t* xt = reinterpret_cast<uint16_t*>(base + p.xt);
   uint16_t* wt = reinterpret_cast<uint16_t*>(base + p.wt);
-  float* acc = p.pieces > 1 || p.splits > 1 ? reinterpret_cast<float*>(base + p.acc) : nullptr;
+  float* acc = p.few || p.pieces > 1 || p.splits > 1 ? reinterpret_cast<float*>(base + p.acc) : nullptr;
   const int64_t m_pad = up(h.rows, 64);
-  auto vec = [](const void* q, int64_t ld_bytes) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0 && ld_bytes % 16 == 0; };
-  auto blocks = [](int64_t n) { return static_cast<unsigned>((n + 255) / 256); };
   if (b.dw)
     hipLaunchKernelGGL((transpose_kernel<false>), dim3(static_cast<unsigned>(m_pad / 64), static_cast<unsigned>((h.k + 63) / 64)), dim3(256),
                        0, s, static_cast<const char*>(h.x), h.ldx, h.rows, h.k, h.targets, xt, m_pad, m_pad);
@@ -934,10 +1316,17 @@ hipError_t launch_head_bwd(const HeadArgs& h, const HeadBwdArgs& b, const HeadBw
     a.vocab = h.vocab;
     a.n_pad = n_pad;
     a.m_pad = m_pad;
-    const Tile t = pick_tile(h.rows, n, cus);
+    const Tile t = pick_tile(h.rows, n, cus, true);
     if (h.i8) launch_nt<true, kGrad>(a, t, cus, s);
     else launch_nt<false, kGrad>(a, t, cus, s);
-    if (b.dx) {
+    if (b.dx && p.few) {
+      const int64_t strips = (h.k + kDxCols - 1) / kDxCols;
+      const DxFewArgs d{dl, p.width, a.w, h.ldw, h.rows, n, h.k, acc, up(h.k, 8), static_cast<int>(strips), p.per};
+      const dim3 grid(static_cast<unsigned>(strips * p.splits));
+      auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, d); };
+      if (h.i8) h.rows <= 32 ? go(head_dx_few_kernel<true, 2>) : h.rows <= 64 ? go(head_dx_few_kernel<true, 4>) : go(head_dx_few_kernel<true, 8>);
+      else h.rows <= 32 ? go(head_dx_few_kernel<false, 2>) : h.rows <= 64 ? go(head_dx_few_kernel<false, 4>) : go(head_dx_few_kernel<false, 8>);
+    } else if (b.dx) {
       const dim3 grid(static_cast<unsigned>(n_pad / 64), static_cast<unsigned>((h.k + 63) / 64));
       if (h.i8) hipLaunchKernelGGL((transpose_kernel<true>), grid, dim3(256), 0, s, a.w, h.ldw, n, h.k, nullptr, wt, p.width, n_pad);
       else hipLaunchKernelGGL((transpose_kernel<false>), grid, dim3(256), 0, s, a.w, h.ldw, n, h.k, nullptr, wt, p.width, n_pad);
@@ -956,10 +1345,16 @@ hipError_t launch_head_bwd(const HeadArgs& h, const HeadBwdArgs& b, const HeadBw
       const bool last = p.splits == 1 && i + 1 == p.pieces;
       d.out = last ? b.dx : nullptr;
       d.ld_out = b.ld_dx;
-      d.vec = last && vec(b.dx, b.ld_dx * 2);
       launch_nt<false, kSum>(d, static_cast<Tile>(p.tile), cus, s);
     }
-    if (b.dw) {
+    if (b.dw && p.few) {
+      const DwFewArgs d{dlt, xt, m_pad, n, h.k, b.dw, b.ld_dw};
+      const int64_t words = (n + 63) / 64, groups = (h.k + 255) / 256;
+      // a workgroup's columns: all of them, or as many shares as give every CU four workgroups
+      const dim3 grid(static_cast<unsigned>(words), static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(groups, 4 * cus / words))));
+      if (m_pad == 64) hipLaunchKernelGGL((head_dw_few_kernel<1>), grid, dim3(256), 0, s, d);
+      else hipLaunchKernelGGL((head_dw_few_kernel<2>), grid, dim3(256), 0, s, d);
+    } else if (b.dw) {
       NtArgs d{};
       d.a = reinterpret_cast<const char*>(dlt);
       d.lda = m_pad * 2;
@@ -971,14 +1366,13 @@ hipError_t launch_head_bwd(const HeadArgs& h, const HeadBwdArgs& b, const HeadBw
       d.splits = 1;
       d.out = b.dw + v0 * b.ld_dw;
       d.ld_out = b.ld_dw;
-      d.vec = vec(d.out, b.ld_dw * 2);
-      launch_nt<false, kSum>(d, pick_tile(n, h.k, cus), cus, s);
+      launch_nt<false, kSum>(d, pick_tile(n, h.k, cus, false), cus, s);
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (b.dx && p.splits > 1)
-    hipLaunchKernelGGL(join_splits_kernel, dim3(blocks(h.rows * h.k)), dim3(256), 0, s, acc, up(h.k, 8), p.splits, h.rows, h.k, b.dx,
+  if (b.dx && (p.few || p.splits > 1))
+    hipLaunchKernelGGL(join_splits_kernel, dim3(static_cast<unsigned>((h.rows * h.k + 63) / 64)), dim3(256), 0, s, acc, up(h.k, 8), p.splits, h.rows, h.k, b.dx,
                        b.ld_dx);
   return hipGetLastError();
 }

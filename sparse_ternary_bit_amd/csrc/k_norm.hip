@@ -40,7 +40,7 @@ __device__ __forceinline__ float block_sum(float v, float* slot) {
 
 // One workgroup a row; kHeld groups of 8 values a thread stay in registers,
 // what lies beyond (rows of more than 8192 values) is read again.
-template <typename TX, typename TR, bool kVec, int kThreads, int kHeld>
+template <typename TX, typename TR, int kThreads, int kHeld>
 __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs a) {
   constexpr bool kRes = !__is_same(TR, None);
   __shared__ float ssum[kThreads / 64];
@@ -56,17 +56,17 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs a) {
     if constexpr (kRes) {
       const TR* res = static_cast<const TR*>(a.res) + r * a.res_stride;
       float b[8];
-      load8f<TR, kVec>(res, c, d, b);
+      load8f<TR>(res, c, d, b);
 #pragma unroll
       for (int i = 0; i < 8; ++i) f[i] += b[i];
       const Raw8<TR> o = pack8<TR>(f);
-      store8<TR, kVec>(static_cast<TR*>(a.h) + r * a.h_stride, c, d, o);
+      store8<TR>(static_cast<TR*>(a.h) + r * a.h_stride, c, d, o);
       unpack8<TR>(o, f);
     }
   };
   auto weigh = [&](int64_t c, const float (&f)[8], float (&v)[8]) {
     float w[8];
-    load8f<float, kVec>(a.weight, c, d, w);
+    load8f<float>(a.weight, c, d, w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       v[i] = f[i] * w[i];
@@ -78,7 +78,7 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs a) {
   {
     Raw8<TX> rx[kHeld];
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) rx[i] = load8<TX, kVec>(x, (threadIdx.x + i * kThreads) * 8, d);
+    for (int i = 0; i < kHeld; ++i) rx[i] = load8<TX>(x, (threadIdx.x + i * kThreads) * 8, d);
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
       const int64_t c = (threadIdx.x + i * kThreads) * 8;
@@ -89,7 +89,7 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs a) {
   }
   for (int64_t g = threadIdx.x + kHeld * kThreads; g < groups; g += kThreads) {
     float f[8], t[8];
-    sum8(g * 8, f, load8<TX, kVec>(x, g * 8, d));
+    sum8(g * 8, f, load8<TX>(x, g * 8, d));
     weigh(g * 8, f, t);
   }
   ss = sum64(ss);
@@ -129,7 +129,7 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs a) {
       float y[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) y[i] = t[i] * rstd;
-      store8<bf16_t, kVec>(reinterpret_cast<bf16_t*>(a.y) + r * a.y_stride, g * 8, d, pack8<bf16_t>(y));
+      store8<bf16_t>(reinterpret_cast<bf16_t*>(a.y) + r * a.y_stride, g * 8, d, pack8<bf16_t>(y));
     }
   };
 #pragma unroll
@@ -138,9 +138,9 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs a) {
   for (int64_t g = threadIdx.x + kHeld * kThreads; g < groups; g += kThreads) {
     float f[8], w[8], t[8];
     // this thread's own store of the sum, or x
-    if constexpr (kRes) load8f<TR, kVec>(static_cast<const TR*>(a.h) + r * a.h_stride, g * 8, d, f);
-    else load8f<TX, kVec>(x, g * 8, d, f);
-    load8f<float, kVec>(a.weight, g * 8, d, w);
+    if constexpr (kRes) load8f<TR>(static_cast<const TR*>(a.h) + r * a.h_stride, g * 8, d, f);
+    else load8f<TX>(x, g * 8, d, f);
+    load8f<float>(a.weight, g * 8, d, w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) t[i] = f[i] * w[i];
     put(g, t);
@@ -150,14 +150,14 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs a) {
 // dx, and each workgroup's part of dw: a workgroup walks the rows blockIdx.x,
 // + gridDim.x, ..., and its threads add dy u for their columns in registers.
 // kHeld * kThreads * 8 columns at most.
-template <typename TH, typename TY, bool kVec, int kThreads, int kHeld>
+template <typename TH, typename TY, int kThreads, int kHeld>
 __global__ __launch_bounds__(kThreads, 2) void norm_bwd_kernel(NormBwdArgs a, float* part) {
   __shared__ float slot[2][kThreads / 64];
   const int64_t d = a.d;
   float w[kHeld][8], acc[kHeld][8];
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) {
-    load8f<float, kVec>(a.weight, (threadIdx.x + i * kThreads) * 8, d, w[i]);
+    load8f<float>(a.weight, (threadIdx.x + i * kThreads) * 8, d, w[i]);
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[i][e] = 0.0f;
   }
@@ -171,13 +171,13 @@ __global__ __launch_bounds__(kThreads, 2) void norm_bwd_kernel(NormBwdArgs a, fl
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
       const int64_t c = (threadIdx.x + i * kThreads) * 8;
-      rh[i] = load8<TH, kVec>(h, c, d);
-      ry[i] = load8<TY, kVec>(dy, c, d);
+      rh[i] = load8<TH>(h, c, d);
+      ry[i] = load8<TY>(dy, c, d);
     }
     if (a.dh) {
 #pragma unroll
       for (int i = 0; i < kHeld; ++i)
-        rd[i] = load8<TH, kVec>(static_cast<const TH*>(a.dh) + r * a.dh_stride, (threadIdx.x + i * kThreads) * 8, d);
+        rd[i] = load8<TH>(static_cast<const TH*>(a.dh) + r * a.dh_stride, (threadIdx.x + i * kThreads) * 8, d);
     }
     float dot = 0.0f;
 #pragma unroll
@@ -207,7 +207,7 @@ __global__ __launch_bounds__(kThreads, 2) void norm_bwd_kernel(NormBwdArgs a, fl
 #pragma unroll
           for (int e = 0; e < 8; ++e) o[e] += f[e];
         }
-        if (c < d) store8<TH, kVec>(static_cast<TH*>(a.dx) + r * a.dx_stride, c, d, pack8<TH>(o));
+        if (c < d) store8<TH>(static_cast<TH*>(a.dx) + r * a.dx_stride, c, d, pack8<TH>(o));
       }
     }
   }
@@ -215,16 +215,14 @@ __global__ __launch_bounds__(kThreads, 2) void norm_bwd_kernel(NormBwdArgs a, fl
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
       const int64_t c = (threadIdx.x + i * kThreads) * 8;
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (c + e < d) part[static_cast<int64_t>(blockIdx.x) * d + c + e] = acc[i][e];
+      if (c < d) store8<float>(part + static_cast<int64_t>(blockIdx.x) * d, c, d, pack8<float>(acc[i]));
     }
   }
 }
 
 // Rows of more than 8192 values: dx with a second read of the row, one
 // workgroup a row ...
-template <typename TH, typename TY, bool kVec>
+template <typename TH, typename TY>
 __global__ __launch_bounds__(512) void norm_bwd_wide_kernel(NormBwdArgs a) {
   __shared__ float slot[8];
   const int64_t r = blockIdx.x, d = a.d;
@@ -234,26 +232,26 @@ __global__ __launch_bounds__(512) void norm_bwd_wide_kernel(NormBwdArgs a) {
   float dot = 0.0f;
   for (int64_t c = threadIdx.x * 8; c < d; c += 512 * 8) {
     float f[8], g[8], w[8];
-    load8f<TH, kVec>(h, c, d, f);
-    load8f<TY, kVec>(dy, c, d, g);
-    load8f<float, kVec>(a.weight, c, d, w);
+    load8f<TH>(h, c, d, f);
+    load8f<TY>(dy, c, d, g);
+    load8f<float>(a.weight, c, d, w);
 #pragma unroll
     for (int e = 0; e < 8; ++e) dot = fmaf(g[e] * w[e], f[e] * rstd, dot);
   }
   const float mean = block_sum<512>(dot, slot) / static_cast<float>(d);
   for (int64_t c = threadIdx.x * 8; c < d; c += 512 * 8) {
     float f[8], g[8], w[8], o[8];
-    load8f<TH, kVec>(h, c, d, f);
-    load8f<TY, kVec>(dy, c, d, g);
-    load8f<float, kVec>(a.weight, c, d, w);
+    load8f<TH>(h, c, d, f);
+    load8f<TY>(dy, c, d, g);
+    load8f<float>(a.weight, c, d, w);
 #pragma unroll
     for (int e = 0; e < 8; ++e) o[e] = rstd * (g[e] * w[e] - f[e] * rstd * mean);
     if (a.dh) {
-      load8f<TH, kVec>(static_cast<const TH*>(a.dh) + r * a.dh_stride, c, d, f);
+      load8f<TH>(static_cast<const TH*>(a.dh) + r * a.dh_stride, c, d, f);
 #pragma unroll
       for (int e = 0; e < 8; ++e) o[e] += f[e];
     }
-    store8<TH, kVec>(static_cast<TH*>(a.dx) + r * a.dx_stride, c, d, pack8<TH>(o));
+    store8<TH>(static_cast<TH*>(a.dx) + r * a.dx_stride, c, d, pack8<TH>(o));
   }
 }
 
@@ -289,33 +287,25 @@ __global__ __launch_bounds__(1024) void norm_dweight_sum_kernel(const float* par
   dw[c] = acc;
 }
 
-bool vec16(const void* p, int64_t stride, int64_t esz) {
-  return !p || ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride * esz % 16 == 0);
-}
-int64_t esize(int bf16) { return bf16 ? 2 : 4; }
 
 }  // namespace
 
 // Threads a row.  Few rows are latency, which more threads shorten; a batch
 // fills the chip with smaller workgroups.
 hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
-  const bool vec = vec16(a.x, a.x_stride, esize(a.x_bf16)) && vec16(a.res, a.res_stride, esize(a.res_bf16)) &&
-                   vec16(a.h, a.h_stride, esize(a.res_bf16)) && vec16(a.weight, 0, 4) && vec16(a.y, a.y_stride, 2);
-  auto go = [&](auto x, auto res, auto v) {
+  auto go = [&](auto x, auto res) {
     using TX = decltype(x);
     using TR = decltype(res);
-    constexpr bool kVec = decltype(v)::value;
     const dim3 grid(static_cast<unsigned>(a.rows));
-    if (a.d <= 512) hipLaunchKernelGGL((norm_kernel<TX, TR, kVec, 64, 1>), grid, dim3(64), 0, s, a);
-    else if (a.d <= 2048) hipLaunchKernelGGL((norm_kernel<TX, TR, kVec, 256, 1>), grid, dim3(256), 0, s, a);
-    else if (a.rows <= 512) hipLaunchKernelGGL((norm_kernel<TX, TR, kVec, 1024, 1>), grid, dim3(1024), 0, s, a);
-    else hipLaunchKernelGGL((norm_kernel<TX, TR, kVec, 256, 4>), grid, dim3(256), 0, s, a);
+    if (a.d <= 512) hipLaunchKernelGGL((norm_kernel<TX, TR, 64, 1>), grid, dim3(64), 0, s, a);
+    else if (a.d <= 2048) hipLaunchKernelGGL((norm_kernel<TX, TR, 256, 1>), grid, dim3(256), 0, s, a);
+    else if (a.rows <= 512) hipLaunchKernelGGL((norm_kernel<TX, TR, 1024, 1>), grid, dim3(1024), 0, s, a);
+    else hipLaunchKernelGGL((norm_kernel<TX, TR, 256, 4>), grid, dim3(256), 0, s, a);
   };
-  auto with_vec = [&](auto x, auto res) { vec ? go(x, res, std::true_type{}) : go(x, res, std::false_type{}); };
   auto with_res = [&](auto x) {
-    if (!a.res) with_vec(x, None{});
-    else if (a.res_bf16) with_vec(x, bf16_t{});
-    else with_vec(x, 0.0f);
+    if (!a.res) go(x, None{});
+    else if (a.res_bf16) go(x, bf16_t{});
+    else go(x, 0.0f);
   };
   a.x_bf16 ? with_res(bf16_t{}) : with_res(0.0f);
   return hipGetLastError();
@@ -325,29 +315,24 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
 int norm_bwd_parts(int64_t rows, int cus) { return static_cast<int>(std::min<int64_t>(rows, 2 * cus)); }
 
 hipError_t launch_norm_bwd(const NormBwdArgs& a, float* part, int cus, hipStream_t s) {
-  const bool vec = vec16(a.h, a.h_stride, esize(a.h_bf16)) && vec16(a.dy, a.dy_stride, esize(a.dy_bf16)) &&
-                   vec16(a.dh, a.dh_stride, esize(a.h_bf16)) && vec16(a.dx, a.dx_stride, esize(a.h_bf16)) &&
-                   vec16(a.weight, 0, 4);
   const int parts = norm_bwd_parts(a.rows, cus);
   float* const pw = a.dw ? part : nullptr;
-  auto go = [&](auto h, auto y, auto v) {
+  auto go = [&](auto h, auto y) {
     using TH = decltype(h);
     using TY = decltype(y);
-    constexpr bool kVec = decltype(v)::value;
     const dim3 grid(static_cast<unsigned>(parts));
-    if (a.d <= 512) hipLaunchKernelGGL((norm_bwd_kernel<TH, TY, kVec, 64, 1>), grid, dim3(64), 0, s, a, pw);
-    else if (a.d <= 2048) hipLaunchKernelGGL((norm_bwd_kernel<TH, TY, kVec, 256, 1>), grid, dim3(256), 0, s, a, pw);
-    else if (a.d <= 8192) hipLaunchKernelGGL((norm_bwd_kernel<TH, TY, kVec, 256, 4>), grid, dim3(256), 0, s, a, pw);
+    if (a.d <= 512) hipLaunchKernelGGL((norm_bwd_kernel<TH, TY, 64, 1>), grid, dim3(64), 0, s, a, pw);
+    else if (a.d <= 2048) hipLaunchKernelGGL((norm_bwd_kernel<TH, TY, 256, 1>), grid, dim3(256), 0, s, a, pw);
+    else if (a.d <= 8192) hipLaunchKernelGGL((norm_bwd_kernel<TH, TY, 256, 4>), grid, dim3(256), 0, s, a, pw);
     else {
       // dw first: dx may take dy's place
       if (pw)
         hipLaunchKernelGGL((norm_dweight_wide_kernel<TH, TY>),
                            dim3(static_cast<unsigned>((a.d + 255) / 256), static_cast<unsigned>(parts)), dim3(256), 0, s, a, pw);
-      if (a.dx) hipLaunchKernelGGL((norm_bwd_wide_kernel<TH, TY, kVec>), dim3(static_cast<unsigned>(a.rows)), dim3(512), 0, s, a);
+      if (a.dx) hipLaunchKernelGGL((norm_bwd_wide_kernel<TH, TY>), dim3(static_cast<unsigned>(a.rows)), dim3(512), 0, s, a);
     }
   };
-  auto with_vec = [&](auto h, auto y) { vec ? go(h, y, std::true_type{}) : go(h, y, std::false_type{}); };
-  auto with_y = [&](auto h) { a.dy_bf16 ? with_vec(h, bf16_t{}) : with_vec(h, 0.0f); };
+  auto with_y = [&](auto h) { a.dy_bf16 ? go(h, bf16_t{}) : go(h, 0.0f); };
   if (a.rows > 0) a.h_bf16 ? with_y(bf16_t{}) : with_y(0.0f);
   if (a.dw)
     hipLaunchKernelGGL(norm_dweight_sum_kernel, dim3(static_cast<unsigned>((a.d + 31) / 32)), dim3(1024), 0, s, part, parts, a.d, a.dw);

@@ -58,17 +58,17 @@ __device__ __forceinline__ float fmax16(float v) {
 
 // A token's logits, kN a lane; columns from `experts` on read as -inf
 template <typename T, int kN>
-__device__ __forceinline__ void load_logits(const T* row, int lane16, int experts, bool vec, bool valid, float (&v)[kN]) {
+__device__ __forceinline__ void load_logits(const T* row, int lane16, int experts, bool valid, float (&v)[kN]) {
 #pragma unroll
   for (int q = 0; q < kN / 4; ++q) {
     const int c = column(lane16, 4 * q);
-    if (valid && vec && c + 4 <= experts) {
+    if (valid && c + 4 <= experts) {
       if constexpr (sizeof(T) == 4) {
-        const f32x4_t w = *reinterpret_cast<const f32x4_t*>(row + c);
+        const u32x4_t w = load16b(row + c);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[4 * q + e] = w[e];
+        for (int e = 0; e < 4; ++e) v[4 * q + e] = __builtin_bit_cast(float, static_cast<uint32_t>(w[e]));
       } else {
-        const u32x2_t w = *reinterpret_cast<const u32x2_t*>(row + c);
+        const u32x2_t w = reinterpret_cast<const Words8*>(row + c)->v;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           v[4 * q + e] = __builtin_bit_cast(float, (e & 1) ? (w[e >> 1] & 0xFFFF0000u) : (w[e >> 1] << 16));
@@ -102,7 +102,6 @@ __device__ __forceinline__ float exponents(float (&v)[kN], float& top) {
 
 struct RouteKernelArgs {
   RouteArgs a;
-  int vec;
   int chunks;
   int32_t* hist;    // [experts][chunks]
   float* prob;      // [experts][chunks]
@@ -189,7 +188,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteKernelArgs g) {
       const int64_t t = t0 + tl;
       const T* row = static_cast<const T*>(a.logits) + (valid ? t : 0) * a.stride;
       float v[kN];
-      load_logits<T, kN>(row, lane16, E, g.vec, valid, v);
+      load_logits<T, kN>(row, lane16, E, valid, v);
       uint32_t key[kN];
 #pragma unroll
       for (int j = 0; j < kN; ++j) {
@@ -222,7 +221,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteKernelArgs g) {
       int pick[2] = {static_cast<int>(kIndex - (mine[0] & kIndex)), static_cast<int>(kIndex - (mine[1] & kIndex))};
       if (sizeof(T) == 4 && __any(unsure && valid)) {
         // some keys agree: once more with whole values, the lowest index first
-        load_logits<T, kN>(row, lane16, E, g.vec, valid, v);
+        load_logits<T, kN>(row, lane16, E, valid, v);
 #pragma unroll
         for (int j = 0; j < kN; ++j) key[j] = column(lane16, j) < E ? order_bits(v[j]) : 0u;
         for (int i = 0; i < k; ++i) {
@@ -417,7 +416,7 @@ __global__ __launch_bounds__(512) void route_scatter_kernel(RouteKernelArgs g) {
 // row of LDS, from the lanes that hold the pairs to those that hold the
 // logits.
 template <typename T, int kN, int kThreads>
-__global__ __launch_bounds__(kThreads) void route_bwd_kernel(RouteBwdArgs a, int vec) {
+__global__ __launch_bounds__(kThreads) void route_bwd_kernel(RouteBwdArgs a) {
   constexpr int kTok = kThreads / kLanes, kCols = kLanes * kN;
   __shared__ float coef[kCols];          // d balance / d p_e of one token, times grad_balance
   __shared__ float chosen[kTok][kCols];
@@ -445,7 +444,7 @@ __global__ __launch_bounds__(kThreads) void route_bwd_kernel(RouteBwdArgs a, int
     const bool valid = t < a.tokens;
     const T* row = static_cast<const T*>(a.logits) + (valid ? t : 0) * a.stride;
     float v[kN];
-    load_logits<T, kN>(row, lane16, E, vec, valid, v);
+    load_logits<T, kN>(row, lane16, E, valid, v);
     float top;
     const float sum = exponents<kN>(v, top);
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
@@ -512,9 +511,9 @@ __global__ __launch_bounds__(kThreads) void route_bwd_kernel(RouteBwdArgs a, int
         const float base = v[4 * q + i] * (cv[4 * q + i] - dot);
         d[i] = a.renorm ? base + ch[i] : base;
       }
-      if (vec && c + 4 <= E) {
-        if constexpr (sizeof(T) == 4) *reinterpret_cast<f32x4_t*>(out + c) = f32x4_t{d[0], d[1], d[2], d[3]};
-        else *reinterpret_cast<u32x2_t*>(out + c) = u32x2_t{bf16_round(d[0]) | bf16_round(d[1]) << 16, bf16_round(d[2]) | bf16_round(d[3]) << 16};
+      if (c + 4 <= E) {
+        if constexpr (sizeof(T) == 4) store16b(out + c, __builtin_bit_cast(u32x4_t, f32x4_t{d[0], d[1], d[2], d[3]}));
+        else reinterpret_cast<Words8*>(out + c)->v = u32x2_t{bf16_round(d[0]) | bf16_round(d[1]) << 16, bf16_round(d[2]) | bf16_round(d[3]) << 16};
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -523,10 +522,6 @@ __global__ __launch_bounds__(kThreads) void route_bwd_kernel(RouteBwdArgs a, int
     }
     __syncthreads();
   }
-}
-
-bool vec4(const void* p, int64_t stride, int64_t esz) {
-  return (reinterpret_cast<uintptr_t>(p) & (4 * esz - 1)) == 0 && stride % 4 == 0;
 }
 
 int64_t round256(int64_t b) { return (b + 255) / 256 * 256; }
@@ -544,7 +539,7 @@ hipError_t launch_route(const RouteArgs& a, void* ws, hipStream_t s) {
   const RouteLayout l = route_layout(a.tokens, a.experts);
   char* base = static_cast<char*>(ws);
   const bool one = l.chunks <= 1;
-  const RouteKernelArgs g{a, vec4(a.logits, a.stride, a.bf16 ? 2 : 4), static_cast<int>(l.chunks),
+  const RouteKernelArgs g{a, static_cast<int>(l.chunks),
                           one ? nullptr : reinterpret_cast<int32_t*>(base), one ? nullptr : reinterpret_cast<float*>(base + l.prob),
                           one ? nullptr : reinterpret_cast<float*>(base + l.prob_total)};
   const dim3 grid(static_cast<unsigned>(one ? 1 : l.chunks));
@@ -571,13 +566,11 @@ hipError_t launch_route(const RouteArgs& a, void* ws, hipStream_t s) {
 }
 
 hipError_t launch_route_bwd(const RouteBwdArgs& a, hipStream_t s) {
-  const int esz = a.bf16 ? 2 : 4;
-  const bool vec = vec4(a.logits, a.stride, esz) && vec4(a.d_logits, a.d_stride, esz);
   auto go = [&](auto t, auto n) {
     constexpr int kN = decltype(n)::value, kThreads = 256;
     const int64_t steps = (a.tokens + kThreads / kLanes - 1) / (kThreads / kLanes);
     hipLaunchKernelGGL((route_bwd_kernel<decltype(t), kN, kThreads>), dim3(static_cast<unsigned>(std::min<int64_t>(steps, 8192))),
-                       dim3(kThreads), 0, s, a, vec);
+                       dim3(kThreads), 0, s, a);
   };
   auto with_n = [&](auto t) {
     if (a.experts <= 64) go(t, std::integral_constant<int, 4>{});

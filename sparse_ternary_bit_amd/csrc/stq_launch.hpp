@@ -369,7 +369,8 @@ struct HeadBwdArgs {
 };
 struct HeadBwdPlan {
   int64_t width, pieces;       // of the vocabulary
-  int tile, splits;            // of dx's product
+  int few;                     // few rows: dx from the head as it lies
+  int tile, splits, per;       // of dx's product; stages of a split (few rows)
   int64_t dlt, xt, wt, acc;    // workspace offsets
   int64_t bytes;
 };

@@ -189,8 +189,9 @@ def test_head_backward_refusals(L, kw, status):
 def test_head_workspaces(L):
     need = ctypes.c_int64()
     fwd, bwd = L.stq_head_cross_entropy_workspace, L.stq_head_cross_entropy_backward_workspace
-    # (maximum, sum) of every row for two wavefronts a tile, and the rows' target logits
-    assert fwd(BF16, 10, 1000, 100, 256, ctypes.byref(need)) == 0 and need.value == 2 * 16 * 10 * 8 + 256
+    # (maximum, sum) of every row for each 16 words, or for two wavefronts a tile of 64, and the rows' target logits
+    assert fwd(BF16, 10, 1000, 100, 256, ctypes.byref(need)) == 0 and need.value == 5120 + 256 and 63 * 10 * 8 <= 5120
+    assert fwd(BF16, 20, 1000, 100, 256, ctypes.byref(need)) == 0 and need.value == 2 * 16 * 20 * 8 + 256
     assert fwd(BF16, 0, 1000, 100, 256, ctypes.byref(need)) == 0 and need.value == 0
     assert fwd(F32, 10, 1000, 100, 256, ctypes.byref(need)) == 1
     assert fwd(BF16, 10, 1000, 100, -1, ctypes.byref(need)) == 1

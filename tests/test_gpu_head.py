@@ -117,9 +117,11 @@ class Case:
             assert bool(((dw.double() - ref).abs() <= tol * (1 + B) + B * ref.abs() + TINY).all())
 
 
-# every tile of either product: 64 x 64, 64 x 256 (more than 16384 words, few rows), 128 x 128, 256 x 256
+# every tile of either product: 16 channels (up to 16 rows), 64 x 64, 64 x 128 and 64 x 256 (more than 32768 and 65536
+# words), 128 x 128, 256 x 256; dx of up to 128 rows reads the head as it lies, of more a transposed piece
 SHAPES = [(1, 1, 1), (1, 2, 9), (3, 65, 8), (5, 130, 100), (64, 1000, 64), (65, 257, 130), (37, 16450, 33), (64, 16500, 72),
-          (1, 20000, 17), (300, 700, 129), (129, 4099, 200), (700, 9001, 65), (512, 66000, 64), (513, 65537, 40)]
+          (1, 20000, 17), (300, 700, 129), (129, 4099, 200), (700, 9001, 65), (512, 66000, 64), (513, 65537, 40),
+          (40, 40000, 24), (50, 70000, 24), (16, 4000, 260), (17, 3000, 96), (128, 3333, 150)]
 
 
 @pytest.mark.parametrize("i8", [False, True])
