@@ -41,6 +41,7 @@ struct NtArgs {
   int64_t ldw;
   int64_t m, n;
   int64_t kbytes;         // bytes of a row that count
+  int64_t words;          // channels that lie along the other way: rows of w
   int tm, tn, step_n;     // tiles, and channels between tiles
   // logits
   const float* as;        // 8-bit rows: scales of tokens and channels
@@ -89,6 +90,17 @@ __device__ __forceinline__ int token_swizzle(int row) { return (row >> 1) & 7; }
 __device__ __forceinline__ int channel_swizzle(int row) { return ((row >> 1) & 1) | ((row >> 2) & 6); }
 // The same for the finished tile [token][channel], which is read along either
 __device__ __forceinline__ int tile_swizzle(int t) { return 2 * ((t & 3) | ((t >> 1) & 4)); }
+
+// Transposing LDS reads of 8 bytes a lane: 16 lanes give 4 rows of 16 16-bit
+// elements, or 8 rows of 16 bytes, and lane r takes back column r.
+__device__ __forceinline__ u32x2_t turned16(const char* at) {
+  typedef int16_t i16x4_t __attribute__((ext_vector_type(4)));
+  return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4_t*)at));
+}
+__device__ __forceinline__ u32x2_t turned8(const char* at) {
+  typedef int32_t i32x2_t __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) i32x2_t*)at));
+}
 
 template <bool kI8>
 struct Mfma;
@@ -511,6 +523,67 @@ __global__ __launch_bounds__(WM * WN * 64, kWavesPerSimd) void nt_kernel(NtArgs 
                             tile_n * WN + wn, split, smem + wave * (32 * FN * 16 * 2));
 }
 
+// How the channel operand lies in memory: a row for every channel, like the
+// token operand, or a row for every term of the sum (bf16, or 8-bit integers
+// that become bf16, which holds them exactly).
+enum Lies { kRows, kAcross16, kAcross8 };
+
+// 16 channels of one row of tiles of a wavefront that read its operand across:
+// lane (q, r) holds token 16 j + r, channels 16 i + 4 q + 0..3.  Sums only.
+template <int FM, int FN>
+__device__ __forceinline__ void finish_across(const NtArgs& a, f32x4_t (&acc)[FN][FM], int64_t m0, int64_t n0, int nv, char* slab) {
+  constexpr int kC = FN * 16;
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));
+  const int q = lane >> 4, r = lane & 15;
+  if (m0 >= a.m) return;
+  const Slab<kC> sl{slab, lane};
+#pragma unroll
+  for (int j = 0; j < FM; ++j) {
+    static_assert(FN == 8, "the operands of this statement");
+    asm volatile("" : "+a"(acc[0][j]), "+a"(acc[1][j]), "+a"(acc[2][j]), "+a"(acc[3][j]), "+a"(acc[4][j]), "+a"(acc[5][j]),
+                 "+a"(acc[6][j]), "+a"(acc[7][j]));
+    const int64_t tok = m0 + 16 * j + r;
+    f32x4_t v[FN];
+#pragma unroll
+    for (int i = 0; i < FN; ++i) v[i] = acc[i][j];
+    float* const row = a.acc + tok * a.ld_acc + n0 + 4 * q;
+    if (a.add && tok < a.m) {
+#pragma unroll
+      for (int i = 0; i < FN; ++i)
+        if (16 * i + 4 * q < nv) {
+          const f32x4_t o = *reinterpret_cast<const f32x4_t*>(row + 16 * i);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[i][e] += o[e];
+        }
+    }
+    if (a.out) {   // whole rows, through LDS
+#pragma unroll
+      for (int i = 0; i < FN; ++i) {
+        const int c = 16 * i + 4 * q;
+        const uint32_t o[4] = {bf16_round(v[i][0]), bf16_round(v[i][1]), bf16_round(v[i][2]), bf16_round(v[i][3])};
+        *reinterpret_cast<u32x2_t*>(sl.at(16 * (j & 1) + r, 2 * i + (q >> 1)) + (q & 1) * 8) = u32x2_t{o[0] | o[1] << 16, o[2] | o[3] << 16};
+        // the last channels of an odd width belong to no whole chunk
+        if (c >= (nv & ~7) && c < nv && tok < a.m) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (c + e < nv) a.out[tok * a.ld_out + n0 + c + e] = static_cast<uint16_t>(o[e]);
+        }
+      }
+      if ((j & 1) || j + 1 == FM) {
+        sl.fence();
+        const int64_t t0 = m0 + 16 * (j & ~1);
+        sl.store_rows(a.out + t0 * a.ld_out + n0, a.ld_out, static_cast<int>(min(static_cast<int64_t>(16 + 16 * (j & 1)), a.m - t0)), nv & ~7);
+        sl.fence();
+      }
+    } else if (tok < a.m) {
+#pragma unroll
+      for (int i = 0; i < FN; ++i)
+        if (16 * i + 4 * q < nv) *reinterpret_cast<f32x4_t*>(row + 16 * i) = v[i];
+    }
+  }
+}
+
 // 256 x 256 tiles: four wavefronts of 128 x 128, one a SIMD, so that an operand
 // read from LDS serves eight products.  Nothing but its own order hides what
 // such a wavefront waits for, so the order is written out: a product, then at
@@ -522,14 +595,26 @@ __global__ __launch_bounds__(WM * WN * 64, kWavesPerSimd) void nt_kernel(NtArgs 
 // before the previous tile's sums are put away.  (4096 rows x 65536 words x
 // 7168: 1.32 PFLOP/s with eight wavefronts of 128 x 64 and two buffers, 1.43
 // with four, 1.46 with the third buffer.)
-template <bool kI8, int kEpi>
+//
+// A channel operand that lies across is read with the transposing LDS reads,
+// 64 rows of 256 channels a stage; 8-bit integers become bf16 between the
+// products, two and their packing at a time, so that three vector instructions
+// follow a product at most, which is what one of 16 cycles hides.
+template <bool kI8, int kEpi, int kLies>
 __global__ __launch_bounds__(256, 1) void nt_wide_kernel(NtArgs a) {
+  static_assert(kLies == kRows || (!kI8 && kEpi == kSum), "the gradient's products alone read across");
   constexpr int T = 256, F = 8, kLoads = 8, kProducts = F * F;
   constexpr int kRead0 = 3, kLoad0 = 4, kRead1 = 4, kLoad1 = 4;  // products between them
   static_assert(kRead0 * 2 * F <= kProducts && kRead1 * 2 * F <= kProducts && kLoad0 * kLoads <= kProducts, "a step's reads fit into it");
-  __shared__ __align__(16) char smem[5 * T * kBK];
-  char(*const sa)[T * kBK] = reinterpret_cast<char(*)[T * kBK]>(smem);
-  char(*const sw)[T * kBK] = reinterpret_cast<char(*)[T * kBK]>(smem + 2 * T * kBK);
+  constexpr bool kAcross = kLies != kRows;
+  constexpr int kWStage = kLies == kAcross8 ? T * kBK / 2 : T * kBK, kWLoads = kWStage / 1024 / 4;
+  constexpr int kWElem = kLies == kAcross8 ? 1 : 2, kWRow = T * kWElem;   // (across) bytes of an element and of a row in LDS
+  constexpr int kSlabs = 4 * 32 * 128 * 2;
+  // (two objects: the compiler then knows the transposing reads for reads of
+  // one, and puts no wait for every load to LDS in front of each)
+  __shared__ __align__(16) char sa[2][T * kBK];
+  __shared__ __align__(16) char channel_mem[3 * kWStage > 2 * kWStage + kSlabs ? 3 * kWStage : 2 * kWStage + kSlabs];
+  char(*const sw)[kWStage] = reinterpret_cast<char(*)[kWStage]>(channel_mem);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q = lane >> 4, r = lane & 15, wm = wave >> 1, wn = wave & 1;
@@ -542,7 +627,23 @@ __global__ __launch_bounds__(256, 1) void nt_wide_kernel(NtArgs a) {
   for (int i = 0; i < kLoads; ++i) {
     const int row = (wave + 4 * i) * 8 + (lane >> 3);
     va[i] = row * static_cast<uint32_t>(a.lda) + (((lane & 7) ^ token_swizzle(row)) << 4);
-    vw[i] = row * static_cast<uint32_t>(a.ldw) + (((lane & 7) ^ channel_swizzle(row)) << 4);
+    if constexpr (!kAcross) vw[i] = row * static_cast<uint32_t>(a.ldw) + (((lane & 7) ^ channel_swizzle(row)) << 4);
+  }
+  // across: a row's 16-byte chunks are XORed by the row, so that the rows that
+  // one transposing read takes (16, or 32 of 8 bits) fall on all banks evenly
+  auto across_swizzle = [](int t) { return kLies == kAcross8 ? t & 15 : tile_swizzle(t); };
+  uint32_t ow_across = 0;   // this lane's place in a stage: fragment 0 of the wavefront's eight
+  if constexpr (kAcross) {
+    constexpr int kChunks = kWRow / 16;
+#pragma unroll
+    for (int i = 0; i < kWLoads; ++i) {
+      const int t = (wave + 4 * i) * (64 / kChunks) + lane / kChunks;
+      vw[i] = t * static_cast<uint32_t>(a.ldw) + ((lane % kChunks ^ across_swizzle(t)) << 4);
+    }
+    // bf16: 16 lanes give 4 rows' 16 channels, 8 bytes a lane, and each takes back 4 rows of one; 8-bit: 8 rows' 16
+    const int t = 8 * q + (kLies == kAcross8 ? r >> 1 : r >> 2);
+    const int chunk = kLies == kAcross8 ? wn * F : wn * 2 * F + ((r & 3) >> 1);
+    ow_across = t * kWRow + ((chunk ^ across_swizzle(t)) << 4) + (r & 1) * 8;
   }
   int oa[2], ow[2];  // this lane's chunk of either step
   const int tok_row = wm * 128 + r, ch_row = wn * 128 + pair_channel(r, 0);
@@ -563,7 +664,14 @@ __global__ __launch_bounds__(256, 1) void nt_wide_kernel(NtArgs a) {
     const int mv = static_cast<int>(min(static_cast<int64_t>(T), a.m - p.m0));
     return make_rsrc(a.a + p.m0 * a.lda, on ? static_cast<uint32_t>((mv - 1) * a.lda) + kpad : 0);
   };
-  auto channels = [&](const Place& p, bool on) {
+  auto channels = [&](const Place& p, bool on, int s) {
+    if constexpr (kAcross) {
+      constexpr int kStageRows = kBK / 2;
+      const int64_t w0 = static_cast<int64_t>(s) * kStageRows;
+      const int rows = static_cast<int>(min(static_cast<int64_t>(kStageRows), a.words - w0));
+      const uint32_t width = static_cast<uint32_t>(((a.n * kWElem + 15) & ~int64_t{15}) - p.n0 * kWElem);
+      return make_rsrc(a.w + (on ? w0 * a.ldw : 0) + p.n0 * kWElem, on ? static_cast<uint32_t>((rows - 1) * a.ldw) + width : 0);
+    }
     const int nv = static_cast<int>(min(static_cast<int64_t>(T), a.n - p.n0));
     return make_rsrc(a.w + p.n0 * a.ldw, on ? static_cast<uint32_t>((nv - 1) * a.ldw) + kpad : 0);
   };
@@ -571,11 +679,11 @@ __global__ __launch_bounds__(256, 1) void nt_wide_kernel(NtArgs a) {
   auto begin = [&](const Place& p) {
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      const Rsrc ra = tokens(p, s < ns), rw = channels(p, s < ns);
+      const Rsrc ra = tokens(p, s < ns), rw = channels(p, s < ns, s);
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) lds_load16(ra, sa[s] + (wave + 4 * i) * 1024, va[i] + s * kBK);
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) lds_load16(rw, sw[s] + (wave + 4 * i) * 1024, vw[i] + s * kBK);
+      for (int i = 0; i < kWLoads; ++i) lds_load16(rw, sw[s] + (wave + 4 * i) * 1024, vw[i] + (kAcross ? 0 : s * kBK));
     }
   };
   int id = static_cast<int>(blockIdx.x % kXcds) * per + static_cast<int>(blockIdx.x) / kXcds;
@@ -585,6 +693,7 @@ __global__ __launch_bounds__(256, 1) void nt_wide_kernel(NtArgs a) {
   for (;;) {
     typename Mfma<kI8>::acc_t acc[F][F];
     u32x4_t fa[2][F], fw[2][F];
+    u32x2_t raw[F];   // 8-bit channels on their way to fw
 #pragma unroll
     for (int i = 0; i < F; ++i)
 #pragma unroll
@@ -597,8 +706,27 @@ __global__ __launch_bounds__(256, 1) void nt_wide_kernel(NtArgs a) {
     };
     // operand n of a step: the channels', then the tokens'
     auto read = [&](int ba, int bw, int h, int n) {
-      if (n < F) fw[h][n] = *reinterpret_cast<const u32x4_t*>(sw[bw] + ow[h] + ((n >> 1) * 32 + (n & 1) * 4) * kBK);
-      else fa[h][n - F] = *reinterpret_cast<const u32x4_t*>(sa[ba] + oa[h] + (n - F) * 16 * kBK);
+      if (n < F) {
+        if constexpr (kAcross) {
+          // (a wavefront's fragments lie in bits of the place that only the swizzle shares)
+          const char* const at = sw[bw] + (ow_across ^ (n << (kLies == kAcross8 ? 4 : 5))) + h * (kBK / 4) * kWRow;
+          if constexpr (kLies == kAcross8) {
+            raw[n] = turned8(at);
+          } else {
+            const u32x2_t lo = turned16(at), hi = turned16(at + 4 * kWRow);
+            fw[h][n] = u32x4_t{lo[0], lo[1], hi[0], hi[1]};
+          }
+        } else {
+          fw[h][n] = *reinterpret_cast<const u32x4_t*>(sw[bw] + ow[h] + ((n >> 1) * 32 + (n & 1) * 4) * kBK);
+        }
+      } else fa[h][n - F] = *reinterpret_cast<const u32x4_t*>(sa[ba] + oa[h] + (n - F) * 16 * kBK);
+    };
+    // words 2 c and 2 c + 1 of a fragment: whole numbers of at most 8 bits,
+    // whose lower halves as fp32 are zeros
+    auto widen8 = [&](int h, int n, int c) {
+      const uint32_t v = raw[n][c >> 1] >> (16 * (c & 1));
+      const float lo = static_cast<float>(static_cast<int8_t>(v)), hi = static_cast<float>(static_cast<int8_t>(v >> 8));
+      fw[h][n][c] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, hi), __builtin_bit_cast(uint32_t, lo), 0x07060302u);
     };
     // Bytes of the last stage past the end of the sum count for nothing,
     // whatever the rows hold there: zeros in the token operand, and, where a
@@ -626,31 +754,50 @@ __global__ __launch_bounds__(256, 1) void nt_wide_kernel(NtArgs a) {
                      "+a"(acc[6][j]), "+a"(acc[7][j]));
 #pragma unroll
     for (int n = 0; n < 2 * F; ++n) read(0, 0, 0, n);
+    if constexpr (kLies == kAcross8) {
+#pragma unroll
+      for (int c = 0; c < 4 * F; ++c) widen8(0, c >> 2, c & 3);
+      asm volatile("s_nop 7" ::: "memory");  // (as in mask)
+    }
     int ba = 0, bw = 0;
-    const bool tail = a.kbytes % kBK != 0;
+    const bool tail = !kAcross && a.kbytes % kBK != 0;
+    // what follows product t of a step: the next step's operands, one read every
+    // `every` products; 8-bit channels first, then their conversions
+    auto between = [&](int buf_a, int buf_w, int h, int t, int every, int at) {
+      if constexpr (kLies == kAcross8) {
+        if (t < 2 * F && (t & 1) == 0) read(buf_a, buf_w, h, t / 2);
+        if (t >= 2 * F && t % 3 == 1 && (t - 2 * F) / 3 < F) read(buf_a, buf_w, h, F + (t - 2 * F) / 3);
+        if (t >= F && t % 3 != 1 && t - F - (t - F) / 3 < 4 * F) {
+          const int c = t - F - (t - F) / 3;
+          widen8(h, c >> 2, c & 3);
+        }
+      } else {
+        if (t % every == at && t / every < 2 * F) read(buf_a, buf_w, h, t / every);
+      }
+    };
     for (int s = 0; s < ns; ++s) {
       // past the last stage the loads have an empty range (they touch nothing)
       // and the reads bring what no product takes
-      const Rsrc ra = tokens(p, s + 2 < ns), rw = channels(p, s + 2 < ns);
-      const uint32_t off = (s + 2) * kBK;
+      const Rsrc ra = tokens(p, s + 2 < ns), rw = channels(p, s + 2 < ns, s + 2);
+      const uint32_t off = (s + 2) * kBK, off_w = kAcross ? 0 : off;
       const int bw1 = bw == 2 ? 0 : bw + 1, bw2 = bw1 == 2 ? 0 : bw1 + 1;
       if (tail && s + 1 == ns) mask(0);
 #pragma unroll
       for (int t = 0; t < kProducts; ++t) {
         product(0, t);
-        if (t % kRead0 == kRead0 - 1 && t / kRead0 < 2 * F) read(ba, bw, 1, t / kRead0);
-        if (t % kLoad0 == kLoad0 / 2 && t / kLoad0 < kLoads) lds_load16(rw, sw[bw2] + (wave + t / kLoad0 * 4) * 1024, vw[t / kLoad0] + off);
+        between(ba, bw, 1, t, kRead0, kRead0 - 1);
+        if (t % kLoad0 == kLoad0 / 2 && t / kLoad0 < kWLoads) lds_load16(rw, sw[bw2] + (wave + t / kLoad0 * 4) * 1024, vw[t / kLoad0] + off_w);
         __builtin_amdgcn_sched_barrier(0);
       }
       // The next stage has landed (the channel operand's loads of this step are
       // the only ones that may still run), and everyone has read this one.
-      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLoads) : "memory");
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kWLoads) : "memory");
       if (tail && s + 1 == ns) mask(1);
 #pragma unroll
       for (int t = 0; t < kProducts; ++t) {
         product(1, t);
         if (t % kLoad1 == kLoad1 - 1 && t / kLoad1 < kLoads) lds_load16(ra, sa[ba] + (wave + t / kLoad1 * 4) * 1024, va[t / kLoad1] + off);
-        if (t % kRead1 == kRead1 / 2 && t / kRead1 < 2 * F) read(ba ^ 1, bw1, 0, t / kRead1);
+        between(ba ^ 1, bw1, 0, t, kRead1, kRead1 / 2);
         __builtin_amdgcn_sched_barrier(0);
       }
       ba ^= 1;
@@ -668,9 +815,10 @@ __global__ __launch_bounds__(256, 1) void nt_wide_kernel(NtArgs a) {
       begin(p);
     }
     // (the next tile's stages lie in the first two buffers of either operand)
-    finish<kI8, kEpi, F, F, true>(a, acc, done.m0 + wm * 128, done.n0 + wn * 128,
-                            static_cast<int>(min(static_cast<int64_t>(T), a.n - done.n0)) - wn * 128, done.tile_n * 2 + wn, 0,
-                            sw[2] + wave * (32 * 128 * 2));
+    const int nv = static_cast<int>(min(static_cast<int64_t>(T), a.n - done.n0)) - wn * 128;
+    char* const slab = sw[2] + wave * (kSlabs / 4);
+    if constexpr (kAcross) finish_across<F, F>(a, acc, done.m0 + wm * 128, done.n0 + wn * 128, nv, slab);
+    else finish<kI8, kEpi, F, F, true>(a, acc, done.m0 + wm * 128, done.n0 + wn * 128, nv, done.tile_n * 2 + wn, 0, slab);
     if (!more) return;
   }
 }
@@ -1161,6 +1309,16 @@ int tile_n(Tile t) { return t == k256x256 || t == k64x256 ? 256 : t == k128x128 
 int tile_parts(Tile t) { return t == k64x256 || t == k64x128 ? 4 : t == kFew ? 1 : 2; }  // wavefronts along a tile's channels
 int64_t stat_parts(Tile t, int64_t vocab) { return (vocab + tile_n(t) - 1) / tile_n(t) * tile_parts(t); }
 
+template <bool kI8, int kEpi, int kLies>
+void launch_wide(NtArgs a, int cus, hipStream_t s) {
+  a.tm = static_cast<int>((a.m + 255) / 256);
+  a.tn = static_cast<int>((a.n + 255) / 256);
+  const int64_t tiles = static_cast<int64_t>(a.tm) * a.tn;
+  // a workgroup a compute unit (its LDS is all of one's), as many on every XCD
+  const int64_t grid = std::min<int64_t>((tiles + kXcds - 1) / kXcds, std::max(1, cus / kXcds)) * kXcds;
+  hipLaunchKernelGGL((nt_wide_kernel<kI8, kEpi, kLies>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, a);
+}
+
 template <bool kI8, int kEpi>
 void launch_nt(const NtArgs& a, Tile t, int cus, hipStream_t s) {
   switch (t) {
@@ -1174,16 +1332,7 @@ void launch_nt(const NtArgs& a, Tile t, int cus, hipStream_t s) {
     case k64x128: launch_tile<kI8, kEpi, 64, 128, 1, 4, 3, 2>(a, 128, s); break;
     case k64x256: launch_tile<kI8, kEpi, 64, 256, 1, 4, 2, 2>(a, 256, s); break;
     case k128x128: launch_tile<kI8, kEpi, 128, 128, 2, 2, 2, 2>(a, 128, s); break;
-    case k256x256: {
-      NtArgs w = a;
-      w.tm = static_cast<int>((a.m + 255) / 256);
-      w.tn = static_cast<int>((a.n + 255) / 256);
-      const int64_t tiles = static_cast<int64_t>(w.tm) * w.tn;
-      // a workgroup a compute unit (its LDS is all of one's), as many on every XCD
-      const int64_t grid = std::min<int64_t>((tiles + kXcds - 1) / kXcds, std::max(1, cus / kXcds)) * kXcds;
-      hipLaunchKernelGGL((nt_wide_kernel<kI8, kEpi>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, w);
-      break;
-    }
+    case k256x256: launch_wide<kI8, kEpi, kRows>(a, cus, s); break;
   }
 }
 
@@ -1277,10 +1426,10 @@ HeadBwdPlan plan_head_bwd(int64_t rows, int64_t vocab, int64_t k, bool dx, bool 
   p.xt = at;
   if (dw) at += up(k * m_pad * 2, 256);
   p.wt = at;
-  if (dx) at += up(k * p.width * 2, 256);
-  p.acc = at;
   // few tokens leave few tiles: the sum over the vocabulary is shared out
   p.tile = pick_tile(rows, k, cus, false);
+  if (dx && p.tile != k256x256) at += up(k * p.width * 2, 256);
+  p.acc = at;
   const int64_t tiles = ((rows + tile_m(static_cast<Tile>(p.tile)) - 1) / tile_m(static_cast<Tile>(p.tile))) *
                         ((k + tile_n(static_cast<Tile>(p.tile)) - 1) / tile_n(static_cast<Tile>(p.tile)));
   p.splits = p.tile == k256x256 ? 1 : static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({cus / tiles, p.width / 1024, 16})));
@@ -1327,14 +1476,9 @@ hipError_t launch_head_bwd(const HeadArgs& h, const HeadBwdArgs& b, const HeadBw
       if (h.i8) h.rows <= 32 ? go(head_dx_few_kernel<true, 2>) : h.rows <= 64 ? go(head_dx_few_kernel<true, 4>) : go(head_dx_few_kernel<true, 8>);
       else h.rows <= 32 ? go(head_dx_few_kernel<false, 2>) : h.rows <= 64 ? go(head_dx_few_kernel<false, 4>) : go(head_dx_few_kernel<false, 8>);
     } else if (b.dx) {
-      const dim3 grid(static_cast<unsigned>(n_pad / 64), static_cast<unsigned>((h.k + 63) / 64));
-      if (h.i8) hipLaunchKernelGGL((transpose_kernel<true>), grid, dim3(256), 0, s, a.w, h.ldw, n, h.k, nullptr, wt, p.width, n_pad);
-      else hipLaunchKernelGGL((transpose_kernel<false>), grid, dim3(256), 0, s, a.w, h.ldw, n, h.k, nullptr, wt, p.width, n_pad);
       NtArgs d{};
       d.a = reinterpret_cast<const char*>(dl);
       d.lda = p.width * 2;
-      d.w = reinterpret_cast<const char*>(wt);
-      d.ldw = p.width * 2;
       d.m = h.rows;
       d.n = h.k;
       d.kbytes = n_pad * 2;
@@ -1345,7 +1489,20 @@ hipError_t launch_head_bwd(const HeadArgs& h, const HeadBwdArgs& b, const HeadBw
       const bool last = p.splits == 1 && i + 1 == p.pieces;
       d.out = last ? b.dx : nullptr;
       d.ld_out = b.ld_dx;
-      launch_nt<false, kSum>(d, static_cast<Tile>(p.tile), cus, s);
+      if (p.tile == k256x256) {
+        d.w = a.w;
+        d.ldw = h.ldw;
+        d.words = n;
+        if (h.i8) launch_wide<false, kSum, kAcross8>(d, cus, s);
+        else launch_wide<false, kSum, kAcross16>(d, cus, s);
+      } else {
+        d.w = reinterpret_cast<const char*>(wt);
+        d.ldw = p.width * 2;
+        const dim3 grid(static_cast<unsigned>(n_pad / 64), static_cast<unsigned>((h.k + 63) / 64));
+        if (h.i8) hipLaunchKernelGGL((transpose_kernel<true>), grid, dim3(256), 0, s, a.w, h.ldw, n, h.k, nullptr, wt, p.width, n_pad);
+        else hipLaunchKernelGGL((transpose_kernel<false>), grid, dim3(256), 0, s, a.w, h.ldw, n, h.k, nullptr, wt, p.width, n_pad);
+        launch_nt<false, kSum>(d, static_cast<Tile>(p.tile), cus, s);
+      }
     }
     if (b.dw && p.few) {
       const DwFewArgs d{dlt, xt, m_pad, n, h.k, b.dw, b.ld_dw};
