@@ -548,15 +548,6 @@ __device__ __forceinline__ void finish_across(const NtArgs& a, f32x4_t (&acc)[FN
 #pragma unroll
     for (int i = 0; i < FN; ++i) v[i] = acc[i][j];
     float* const row = a.acc + tok * a.ld_acc + n0 + 4 * q;
-    if (a.add && tok < a.m) {
-#pragma unroll
-      for (int i = 0; i < FN; ++i)
-        if (16 * i + 4 * q < nv) {
-          const f32x4_t o = *reinterpret_cast<const f32x4_t*>(row + 16 * i);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[i][e] += o[e];
-        }
-    }
     if (a.out) {   // whole rows, through LDS
 #pragma unroll
       for (int i = 0; i < FN; ++i) {
@@ -694,10 +685,27 @@ __global__ __launch_bounds__(256, 1) void nt_wide_kernel(NtArgs a) {
     typename Mfma<kI8>::acc_t acc[F][F];
     u32x4_t fa[2][F], fw[2][F];
     u32x2_t raw[F];   // 8-bit channels on their way to fw
+    // Earlier pieces' sums are where these begin: read all at once, they cost one
+    // latency (added at the end, 16 tokens at a time, they cost eight).
+    if (kAcross && a.add) {
+      if constexpr (kAcross) {
+        const int64_t m = p.m0 + wm * 128;
+        const int rows = static_cast<int>(max(int64_t{0}, min(int64_t{128}, a.m - m)));
+        const Rsrc rs = make_rsrc(a.acc + m * a.ld_acc + p.n0, static_cast<uint32_t>(rows * a.ld_acc - (rows ? p.n0 : 0)) * 4);
+        // (channels past a row's end are another row's, and nobody's results)
+        const uint32_t at = (r * static_cast<uint32_t>(a.ld_acc) + wn * 128 + 4 * q) * 4;
 #pragma unroll
-    for (int i = 0; i < F; ++i)
+        for (int j = 0; j < F; ++j)
 #pragma unroll
-      for (int j = 0; j < F; ++j) acc[i][j] = typename Mfma<kI8>::acc_t{0, 0, 0, 0};
+          for (int i = 0; i < F; ++i)
+            acc[i][j] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, static_cast<int>(at + j * 64 * static_cast<uint32_t>(a.ld_acc) + i * 64), 0, 0));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < F; ++i)
+#pragma unroll
+        for (int j = 0; j < F; ++j) acc[i][j] = typename Mfma<kI8>::acc_t{0, 0, 0, 0};
+    }
     // The sums are all of the accumulation registers: left to the compiler, some
     // of them move to and fro around their products.
     auto product = [&](int h, int t) {

@@ -131,9 +131,10 @@ def test_forward(stq, n, v, k, i8):
     c.check_forward(*stq.head_cross_entropy(c.x, c.w, c.targets, **c.args()))
 
 
-# dW's 256 x 256 tiles; several pieces of the vocabulary, dx's sum shared out or not
+# dW's 256 x 256 tiles; several pieces of the vocabulary, dx's sum shared out or not, or its last round's alone
 @pytest.mark.parametrize("i8", [False, True])
-@pytest.mark.parametrize("n, v, k", SHAPES + [(70, 8192, 2048), (20, 17000, 8000), (900, 17000, 8000)])
+@pytest.mark.parametrize("n, v, k", SHAPES + [(70, 8192, 2048), (20, 17000, 8000), (900, 17000, 8000),
+                                              (1300, 4500, 6501), (4097, 3001, 7000)])
 def test_backward(stq, n, v, k, i8):
     c = Case(n, v, k, i8, 2 * n + v + k)
     _, lse = stq.head_cross_entropy(c.x, c.w, c.targets, **c.args())
