@@ -61,12 +61,13 @@ struct NtArgs {
   int64_t ld_dlt;
   int64_t n_pad, m_pad;
   // kSum
-  float* acc;             // [splits][m][ld_acc], ld_acc a multiple of 8
-  int64_t ld_acc;
-  int add;                // add to acc
-  int splits;             // parts of the sum
-  uint16_t* out;          // bf16 [m][ld_out] instead of acc's store (with add: acc is added first)
+  uint16_t* out;          // bf16 [m][ld_out]
   int64_t ld_out;
+  // sums of channels that lie across
+  float* acc;             // [splits][m][ld_acc], ld_acc a multiple of 8: where the sums go if out is NULL
+  int64_t ld_acc;
+  int add;                // begin with what acc holds
+  int splits;             // parts of the sum
 };
 
 // Output channels of a pair of 16-row MFMA tiles: row r of tile h stands for
@@ -172,7 +173,7 @@ struct Slab {
 // time.
 template <bool kI8, int kEpi, int FM, int FN, bool kAcc>
 __device__ __forceinline__ void finish(const NtArgs& a, typename Mfma<kI8>::acc_t (&acc)[FN][FM], int64_t m0, int64_t n0, int nv, int part,
-                                       int split, char* slab) {
+                                       char* slab) {
   constexpr int kC = FN * 16, kP = FN / 2;
   // an opaque copy: what depends on the lane here is worked out here, not
   // before the products and kept (spilled) beside them
@@ -191,54 +192,26 @@ __device__ __forceinline__ void finish(const NtArgs& a, typename Mfma<kI8>::acc_
   };
   if constexpr (kEpi == kSum) {
     const Slab<kC> sl{slab, lane};
-    auto row_of = [&](int64_t tok) { return a.acc + (static_cast<int64_t>(split) * a.m + tok) * a.ld_acc; };
 #pragma unroll
-    for (int j = 0; j < FM; ++j) {
+    for (int j = 0; j < FM; ++j) {   // whole rows, through LDS
       take(j);
       const int64_t tok = m0 + 16 * j + r;
-      float v[kP][8];
 #pragma unroll
-      for (int p = 0; p < kP; ++p)
+      for (int p = 0; p < kP; ++p) {
+        const int c = 32 * p + 8 * q;
+        float v[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[p][e] = value(j, p, e);
-      if (a.add && tok < a.m) {
-#pragma unroll
-        for (int p = 0; p < kP; ++p) {
-          const int c = 32 * p + 8 * q;
-          if (c >= nv) continue;
-          const f32x4_t* const o = reinterpret_cast<const f32x4_t*>(row_of(tok) + n0 + c);
-          const f32x4_t lo = o[0], hi = o[1];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[p][e] += lo[e];
-            v[p][e + 4] += hi[e];
-          }
-        }
+        for (int e = 0; e < 8; ++e) v[e] = value(j, p, e);
+        const Raw8<bf16_t> o = pack8<bf16_t>(v);
+        *reinterpret_cast<u32x4_t*>(sl.at(16 * (j & 1) + r, c / 8)) = o.w[0];
+        // the last channels of an odd width belong to no whole chunk
+        if (c + 8 > nv && c < nv && tok < a.m) store8<bf16_t>(reinterpret_cast<bf16_t*>(a.out) + tok * a.ld_out, n0 + c, a.n, o);
       }
-      if (a.out) {   // whole rows, through LDS
-#pragma unroll
-        for (int p = 0; p < kP; ++p) {
-          const int c = 32 * p + 8 * q;
-          const Raw8<bf16_t> o = pack8<bf16_t>(v[p]);
-          *reinterpret_cast<u32x4_t*>(sl.at(16 * (j & 1) + r, c / 8)) = o.w[0];
-          // the last channels of an odd width belong to no whole chunk
-          if (c + 8 > nv && c < nv && tok < a.m) store8<bf16_t>(reinterpret_cast<bf16_t*>(a.out) + tok * a.ld_out, n0 + c, a.n, o);
-        }
-        if ((j & 1) || j + 1 == FM) {
-          sl.fence();
-          const int64_t t0 = m0 + 16 * (j & ~1);
-          sl.store_rows(a.out + t0 * a.ld_out + n0, a.ld_out, static_cast<int>(min(static_cast<int64_t>(16 + 16 * (j & 1)), a.m - t0)), nv & ~7);
-          sl.fence();
-        }
-      } else if (tok < a.m) {
-#pragma unroll
-        for (int p = 0; p < kP; ++p) {
-          const int c = 32 * p + 8 * q;
-          if (c >= nv) continue;
-          f32x4_t* const o = reinterpret_cast<f32x4_t*>(row_of(tok) + n0 + c);
-          o[0] = f32x4_t{v[p][0], v[p][1], v[p][2], v[p][3]};
-          o[1] = f32x4_t{v[p][4], v[p][5], v[p][6], v[p][7]};
-        }
+      if ((j & 1) || j + 1 == FM) {
+        sl.fence();
+        const int64_t t0 = m0 + 16 * (j & ~1);
+        sl.store_rows(a.out + t0 * a.ld_out + n0, a.ld_out, static_cast<int>(min(static_cast<int64_t>(16 + 16 * (j & 1)), a.m - t0)), nv & ~7);
+        sl.fence();
       }
     }
     return;
@@ -385,7 +358,7 @@ __global__ __launch_bounds__(WM * WN * 64, kWavesPerSimd) void nt_kernel(NtArgs 
   // Workgroups are dealt to the XCDs in turn: each XCD takes one run of tiles,
   // in bands of 8 token tiles, so that its L2 serves a compact block of both
   // operands.
-  const int tiles = a.tm * a.tn, split = kEpi == kSum ? static_cast<int>(blockIdx.y) : 0;
+  const int tiles = a.tm * a.tn;
   const int per = (tiles + kXcds - 1) / kXcds;
   const int id = (blockIdx.x % kXcds) * per + blockIdx.x / kXcds;
   if (id >= tiles) return;
@@ -408,15 +381,12 @@ __global__ __launch_bounds__(WM * WN * 64, kWavesPerSimd) void nt_kernel(NtArgs 
     const int row = (wave + i * kNW) * 8 + (lane >> 3);
     vw[i] = row * static_cast<uint32_t>(a.ldw) + (((lane & 7) ^ channel_swizzle(row)) << 4);
   }
-  // this split's stages
-  const int all = static_cast<int>((a.kbytes + kBK - 1) / kBK);
-  const int s_per = kEpi == kSum ? (all + a.splits - 1) / a.splits : all;
-  const int s_lo = split * s_per, ns = max(0, min(all - s_lo, s_per));
+  const int ns = static_cast<int>((a.kbytes + kBK - 1) / kBK);
   auto stage = [&](int s, int buf) {
 #pragma unroll
-    for (int i = 0; i < NA; ++i) lds_load16(ra, sa[buf] + (wave + i * kNW) * 1024, va[i] + (s_lo + s) * kBK);
+    for (int i = 0; i < NA; ++i) lds_load16(ra, sa[buf] + (wave + i * kNW) * 1024, va[i] + s * kBK);
 #pragma unroll
-    for (int i = 0; i < NW; ++i) lds_load16(rw, sw[buf] + (wave + i * kNW) * 1024, vw[i] + (s_lo + s) * kBK);
+    for (int i = 0; i < NW; ++i) lds_load16(rw, sw[buf] + (wave + i * kNW) * 1024, vw[i] + s * kBK);
   };
   acc_t acc[FN][FM];
 #pragma unroll
@@ -460,7 +430,7 @@ __global__ __launch_bounds__(WM * WN * 64, kWavesPerSimd) void nt_kernel(NtArgs 
   // the rows hold there: zeros in the token operand, and, where a bf16 NaN
   // times zero would be one, in the channel operand.
   auto mask = [&](int s, int h) {
-    const int left = static_cast<int>(a.kbytes) - ((s_lo + s) * kBK + h * kStep + q * 16);
+    const int left = static_cast<int>(a.kbytes) - (s * kBK + h * kStep + q * 16);
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
       const uint32_t m = byte_mask(left - 4 * d);
@@ -505,7 +475,7 @@ __global__ __launch_bounds__(WM * WN * 64, kWavesPerSimd) void nt_kernel(NtArgs 
       }
       buf = next;
     }
-    const bool tail = a.kbytes % kBK != 0 && s_lo + ns == all;
+    const bool tail = a.kbytes % kBK != 0;
     if (tail) mask(ns - 1, 0);
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
@@ -520,7 +490,7 @@ __global__ __launch_bounds__(WM * WN * 64, kWavesPerSimd) void nt_kernel(NtArgs 
   // everyone has read the last stage
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
   finish<kI8, kEpi, FM, FN, false>(a, acc, m0 + wm * FM * 16, n0 + wn * FN * 16, min(static_cast<int>(nv) - wn * FN * 16, FN * 16),
-                            tile_n * WN + wn, split, smem + wave * (32 * FN * 16 * 2));
+                            tile_n * WN + wn, smem + wave * (32 * FN * 16 * 2));
 }
 
 // How the channel operand lies in memory: a row for every channel, like the
@@ -531,7 +501,7 @@ enum Lies { kRows, kAcross16, kAcross8 };
 // 16 channels of one row of tiles of a wavefront that read its operand across:
 // lane (q, r) holds token 16 j + r, channels 16 i + 4 q + 0..3.  Sums only.
 template <int FM, int FN>
-__device__ __forceinline__ void finish_across(const NtArgs& a, f32x4_t (&acc)[FN][FM], int64_t m0, int64_t n0, int nv, char* slab) {
+__device__ __forceinline__ void finish_across(const NtArgs& a, f32x4_t (&acc)[FN][FM], int64_t m0, int64_t n0, int nv, int split, char* slab) {
   constexpr int kC = FN * 16;
   int lane = threadIdx.x & 63;
   asm volatile("" : "+v"(lane));
@@ -547,7 +517,7 @@ __device__ __forceinline__ void finish_across(const NtArgs& a, f32x4_t (&acc)[FN
     f32x4_t v[FN];
 #pragma unroll
     for (int i = 0; i < FN; ++i) v[i] = acc[i][j];
-    float* const row = a.acc + tok * a.ld_acc + n0 + 4 * q;
+    float* const row = a.acc + (split * a.m + tok) * a.ld_acc + n0 + 4 * q;
     if (a.out) {   // whole rows, through LDS
 #pragma unroll
       for (int i = 0; i < FN; ++i) {
@@ -609,9 +579,10 @@ __global__ __launch_bounds__(256, 1) void nt_wide_kernel(NtArgs a) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q = lane >> 4, r = lane & 15, wm = wave >> 1, wn = wave & 1;
-  const int tiles = a.tm * a.tn;
-  const int per = (tiles + kXcds - 1) / kXcds, last = min(tiles, static_cast<int>(blockIdx.x % kXcds + 1) * per);
-  const int ns = static_cast<int>((a.kbytes + kBK - 1) / kBK);
+  // (across, the sum may be shared out: one part after the other, each with all its tiles)
+  const int tiles = a.tm * a.tn, splits = kAcross ? a.splits : 1, all = tiles * splits;
+  const int per = (all + kXcds - 1) / kXcds, last = min(all, static_cast<int>(blockIdx.x % kXcds + 1) * per);
+  const int ns = static_cast<int>((a.kbytes + kBK - 1) / kBK), chunk = (ns + splits - 1) / splits;
   const uint32_t kpad = static_cast<uint32_t>((a.kbytes + 15) & ~15);
   uint32_t va[kLoads], vw[kLoads];
 #pragma unroll
@@ -645,11 +616,14 @@ __global__ __launch_bounds__(256, 1) void nt_wide_kernel(NtArgs a) {
   }
   struct Place {
     int64_t m0, n0;
-    int tile_n;
+    int tile_n, split, s0, s1;   // stages s0 .. s1 - 1
   };
   auto place = [&](int id) {
+    const int split = kAcross ? id / tiles : 0;
+    if constexpr (kAcross) id -= split * tiles;
     const int band = id / (8 * a.tn), rows = min(8, a.tm - band * 8), in = id - band * 8 * a.tn;
-    return Place{static_cast<int64_t>(band * 8 + in % rows) * T, static_cast<int64_t>(in / rows) * T, in / rows};
+    return Place{static_cast<int64_t>(band * 8 + in % rows) * T, static_cast<int64_t>(in / rows) * T, in / rows, split,
+                 kAcross ? split * chunk : 0, kAcross ? min(ns, (split + 1) * chunk) : ns};
   };
   auto tokens = [&](const Place& p, bool on) {
     const int mv = static_cast<int>(min(static_cast<int64_t>(T), a.m - p.m0));
@@ -669,12 +643,13 @@ __global__ __launch_bounds__(256, 1) void nt_wide_kernel(NtArgs a) {
   // the first two stages (the second reads as zeros where there is none)
   auto begin = [&](const Place& p) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const Rsrc ra = tokens(p, s < ns), rw = channels(p, s < ns, s);
+    for (int b = 0; b < 2; ++b) {
+      const int s = p.s0 + b;
+      const Rsrc ra = tokens(p, s < p.s1), rw = channels(p, s < p.s1, s);
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) lds_load16(ra, sa[s] + (wave + 4 * i) * 1024, va[i] + s * kBK);
+      for (int i = 0; i < kLoads; ++i) lds_load16(ra, sa[b] + (wave + 4 * i) * 1024, va[i] + s * kBK);
 #pragma unroll
-      for (int i = 0; i < kWLoads; ++i) lds_load16(rw, sw[s] + (wave + 4 * i) * 1024, vw[i] + (kAcross ? 0 : s * kBK));
+      for (int i = 0; i < kWLoads; ++i) lds_load16(rw, sw[b] + (wave + 4 * i) * 1024, vw[i] + (kAcross ? 0 : s * kBK));
     }
   };
   int id = static_cast<int>(blockIdx.x % kXcds) * per + static_cast<int>(blockIdx.x) / kXcds;
@@ -691,7 +666,7 @@ __global__ __launch_bounds__(256, 1) void nt_wide_kernel(NtArgs a) {
       if constexpr (kAcross) {
         const int64_t m = p.m0 + wm * 128;
         const int rows = static_cast<int>(max(int64_t{0}, min(int64_t{128}, a.m - m)));
-        const Rsrc rs = make_rsrc(a.acc + m * a.ld_acc + p.n0, static_cast<uint32_t>(rows * a.ld_acc - (rows ? p.n0 : 0)) * 4);
+        const Rsrc rs = make_rsrc(a.acc + (p.split * a.m + m) * a.ld_acc + p.n0, static_cast<uint32_t>(rows * a.ld_acc - (rows ? p.n0 : 0)) * 4);
         // (channels past a row's end are another row's, and nobody's results)
         const uint32_t at = (r * static_cast<uint32_t>(a.ld_acc) + wn * 128 + 4 * q) * 4;
 #pragma unroll
@@ -783,10 +758,10 @@ __global__ __launch_bounds__(256, 1) void nt_wide_kernel(NtArgs a) {
         if (t % every == at && t / every < 2 * F) read(buf_a, buf_w, h, t / every);
       }
     };
-    for (int s = 0; s < ns; ++s) {
+    for (int s = p.s0; s < p.s1; ++s) {
       // past the last stage the loads have an empty range (they touch nothing)
       // and the reads bring what no product takes
-      const Rsrc ra = tokens(p, s + 2 < ns), rw = channels(p, s + 2 < ns, s + 2);
+      const Rsrc ra = tokens(p, s + 2 < p.s1), rw = channels(p, s + 2 < p.s1, s + 2);
       const uint32_t off = (s + 2) * kBK, off_w = kAcross ? 0 : off;
       const int bw1 = bw == 2 ? 0 : bw + 1, bw2 = bw1 == 2 ? 0 : bw1 + 1;
       if (tail && s + 1 == ns) mask(0);
@@ -825,8 +800,8 @@ __global__ __launch_bounds__(256, 1) void nt_wide_kernel(NtArgs a) {
     // (the next tile's stages lie in the first two buffers of either operand)
     const int nv = static_cast<int>(min(static_cast<int64_t>(T), a.n - done.n0)) - wn * 128;
     char* const slab = sw[2] + wave * (kSlabs / 4);
-    if constexpr (kAcross) finish_across<F, F>(a, acc, done.m0 + wm * 128, done.n0 + wn * 128, nv, slab);
-    else finish<kI8, kEpi, F, F, true>(a, acc, done.m0 + wm * 128, done.n0 + wn * 128, nv, done.tile_n * 2 + wn, 0, slab);
+    if constexpr (kAcross) finish_across<F, F>(a, acc, done.m0 + wm * 128, done.n0 + wn * 128, nv, done.split, slab);
+    else finish<kI8, kEpi, F, F, true>(a, acc, done.m0 + wm * 128, done.n0 + wn * 128, nv, done.tile_n * 2 + wn, slab);
     if (!more) return;
   }
 }
@@ -1212,9 +1187,7 @@ __global__ __launch_bounds__(1024) void head_join_kernel(const float2* stats, co
 }
 
 // out[c][r] = in[r][c] for r < n (zeros for r = n .. n_pad - 1 and for rows
-// whose target is ignored), c < k: bf16 or 8-bit integers in, bf16 out; 64 x
-// 64 a workgroup.
-template <bool kI8>
+// whose target is ignored), c < k; 64 x 64 a workgroup.
 __global__ __launch_bounds__(256) void transpose_kernel(const char* in, int64_t ld, int64_t n, int64_t k, const int32_t* targets,
                                                         uint16_t* out, int64_t ld_out, int64_t n_pad) {
   __shared__ uint16_t tile[64][66];
@@ -1228,16 +1201,9 @@ __global__ __launch_bounds__(256) void transpose_kernel(const char* in, int64_t 
     for (int e = 0; e < 8; ++e) v[e] = 0;
     if (rr < n && c0 + c < k && !(targets && targets[rr] < 0)) {
       // a row owns its bytes up to the next multiple of 16
-      if constexpr (kI8) {
-        const u32x2_t w = *reinterpret_cast<const u32x2_t*>(in + rr * ld + c0 + c);
+      const u32x4_t w = *reinterpret_cast<const u32x4_t*>(in + rr * ld + (c0 + c) * 2);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          v[e] = static_cast<uint16_t>(bf16_round(static_cast<float>(static_cast<int8_t>(w[e >> 2] >> (8 * (e & 3))))));
-      } else {
-        const u32x4_t w = *reinterpret_cast<const u32x4_t*>(in + rr * ld + (c0 + c) * 2);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
-      }
+      for (int e = 0; e < 8; ++e) v[e] = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) tile[c + e][row + 32 * h] = v[e];
@@ -1291,7 +1257,7 @@ void launch_tile(NtArgs a, int step_n, hipStream_t s) {
   a.tm = static_cast<int>((a.m + TM - 1) / TM);
   a.tn = static_cast<int>((a.n + step_n - 1) / step_n);
   const int64_t tiles = static_cast<int64_t>(a.tm) * a.tn;
-  const dim3 grid(static_cast<unsigned>((tiles + kXcds - 1) / kXcds * kXcds), kEpi == kSum ? a.splits : 1);
+  const dim3 grid(static_cast<unsigned>((tiles + kXcds - 1) / kXcds * kXcds));
   hipLaunchKernelGGL((nt_kernel<kI8, kEpi, TM, TN, WM, WN, kBuf, kWavesPerSimd>), grid, dim3(WM * WN * 64), 0, s, a);
 }
 
@@ -1321,7 +1287,7 @@ template <bool kI8, int kEpi, int kLies>
 void launch_wide(NtArgs a, int cus, hipStream_t s) {
   a.tm = static_cast<int>((a.m + 255) / 256);
   a.tn = static_cast<int>((a.n + 255) / 256);
-  const int64_t tiles = static_cast<int64_t>(a.tm) * a.tn;
+  const int64_t tiles = static_cast<int64_t>(a.tm) * a.tn * (kLies == kRows ? 1 : a.splits);
   // a workgroup a compute unit (its LDS is all of one's), as many on every XCD
   const int64_t grid = std::min<int64_t>((tiles + kXcds - 1) / kXcds, std::max(1, cus / kXcds)) * kXcds;
   hipLaunchKernelGGL((nt_wide_kernel<kI8, kEpi, kLies>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, a);
@@ -1394,6 +1360,21 @@ hipError_t launch_head(const HeadArgs& h, float* loss, float* lse, void* ws, int
 
 // Pieces of the vocabulary: at most 2^26 logits and 2^27 weights each, and of
 // those the width whose tiles fill whole rounds of the chip best.
+// Parts that dx's sum over `stages` x 64 words is shared out into when its tiles
+// leave compute units idle: the fewest of what a tile's stages and its end (1.4
+// us a stage, 8 stages an end) and the parts' store and join cost together.
+static int dx_splits(int64_t rows, int64_t k, int64_t stages, int64_t pieces, int cus) {
+  const int64_t tiles = (rows + 255) / 256 * ((k + 255) / 256);
+  int best = 1;
+  double best_us = 0;
+  for (int64_t s = 1; s <= std::min<int64_t>(64, (stages + 3) / 4); ++s) {
+    const double walk = 1.4 * pieces * ((tiles * s + cus - 1) / cus) * ((stages + s - 1) / s + 8);
+    const double us = walk + (s > 1 ? s * rows * k * 8 / 4.7e6 : 0.0);
+    if (s == 1 || us < best_us) best = static_cast<int>(s), best_us = us;
+  }
+  return best;
+}
+
 HeadBwdPlan plan_head_bwd(int64_t rows, int64_t vocab, int64_t k, bool dx, bool dw, int cus) {
   HeadBwdPlan p{};
   const int64_t m_pad = up(rows, 64);
@@ -1417,7 +1398,8 @@ HeadBwdPlan plan_head_bwd(int64_t rows, int64_t vocab, int64_t k, bool dx, bool 
     p.bytes = at;
     return p;
   }
-  const int64_t cap = std::max<int64_t>(1, std::min((int64_t{1} << 26) / rows, (int64_t{1} << 27) / k) / 256);
+  // pieces of the vocabulary whose dl (and its transpose) stay in the last-level cache
+  const int64_t cap = std::max<int64_t>(1, (int64_t{1} << 26) / rows / 256);
   const int64_t cols = (vocab + 255) / 256;
   const int64_t tm = (rows + 255) / 256;
   auto rounds = [&](int64_t c) { return (tm * c + cus - 1) / cus; };
@@ -1433,14 +1415,8 @@ HeadBwdPlan plan_head_bwd(int64_t rows, int64_t vocab, int64_t k, bool dx, bool 
   if (dw) at += up(p.width * m_pad * 2, 256);
   p.xt = at;
   if (dw) at += up(k * m_pad * 2, 256);
-  p.wt = at;
-  // few tokens leave few tiles: the sum over the vocabulary is shared out
-  p.tile = pick_tile(rows, k, cus, false);
-  if (dx && p.tile != k256x256) at += up(k * p.width * 2, 256);
   p.acc = at;
-  const int64_t tiles = ((rows + tile_m(static_cast<Tile>(p.tile)) - 1) / tile_m(static_cast<Tile>(p.tile))) *
-                        ((k + tile_n(static_cast<Tile>(p.tile)) - 1) / tile_n(static_cast<Tile>(p.tile)));
-  p.splits = p.tile == k256x256 ? 1 : static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({cus / tiles, p.width / 1024, 16})));
+  p.splits = dx ? dx_splits(rows, k, std::min(p.width, up(vocab, 64)) / 64, p.pieces, cus) : 1;
   if (dx && (p.pieces > 1 || p.splits > 1)) at += up(p.splits * rows * up(k, 8) * 4, 256);
   p.bytes = at;
   return p;
@@ -1451,11 +1427,10 @@ hipError_t launch_head_bwd(const HeadArgs& h, const HeadBwdArgs& b, const HeadBw
   uint16_t* dl = reinterpret_cast<uint16_t*>(base);
   uint16_t* dlt = reinterpret_cast<uint16_t*>(base + p.dlt);
   uint16_t* xt = reinterpret_cast<uint16_t*>(base + p.xt);
-  uint16_t* wt = reinterpret_cast<uint16_t*>(base + p.wt);
   float* acc = p.few || p.pieces > 1 || p.splits > 1 ? reinterpret_cast<float*>(base + p.acc) : nullptr;
   const int64_t m_pad = up(h.rows, 64);
   if (b.dw)
-    hipLaunchKernelGGL((transpose_kernel<false>), dim3(static_cast<unsigned>(m_pad / 64), static_cast<unsigned>((h.k + 63) / 64)), dim3(256),
+    hipLaunchKernelGGL(transpose_kernel, dim3(static_cast<unsigned>(m_pad / 64), static_cast<unsigned>((h.k + 63) / 64)), dim3(256),
                        0, s, static_cast<const char*>(h.x), h.ldx, h.rows, h.k, h.targets, xt, m_pad, m_pad);
   for (int64_t i = 0; i < p.pieces; ++i) {
     const int64_t v0 = i * p.width, n = std::min(p.width, h.vocab - v0), n_pad = up(n, 64);
@@ -1497,20 +1472,11 @@ hipError_t launch_head_bwd(const HeadArgs& h, const HeadBwdArgs& b, const HeadBw
       const bool last = p.splits == 1 && i + 1 == p.pieces;
       d.out = last ? b.dx : nullptr;
       d.ld_out = b.ld_dx;
-      if (p.tile == k256x256) {
-        d.w = a.w;
-        d.ldw = h.ldw;
-        d.words = n;
-        if (h.i8) launch_wide<false, kSum, kAcross8>(d, cus, s);
-        else launch_wide<false, kSum, kAcross16>(d, cus, s);
-      } else {
-        d.w = reinterpret_cast<const char*>(wt);
-        d.ldw = p.width * 2;
-        const dim3 grid(static_cast<unsigned>(n_pad / 64), static_cast<unsigned>((h.k + 63) / 64));
-        if (h.i8) hipLaunchKernelGGL((transpose_kernel<true>), grid, dim3(256), 0, s, a.w, h.ldw, n, h.k, nullptr, wt, p.width, n_pad);
-        else hipLaunchKernelGGL((transpose_kernel<false>), grid, dim3(256), 0, s, a.w, h.ldw, n, h.k, nullptr, wt, p.width, n_pad);
-        launch_nt<false, kSum>(d, static_cast<Tile>(p.tile), cus, s);
-      }
+      d.w = a.w;
+      d.ldw = h.ldw;
+      d.words = n;
+      if (h.i8) launch_wide<false, kSum, kAcross8>(d, cus, s);
+      else launch_wide<false, kSum, kAcross16>(d, cus, s);
     }
     if (b.dw && p.few) {
       const DwFewArgs d{dlt, xt, m_pad, n, h.k, b.dw, b.ld_dw};
@@ -1528,7 +1494,6 @@ hipError_t launch_head_bwd(const HeadArgs& h, const HeadBwdArgs& b, const HeadBw
       d.m = n;
       d.n = h.k;
       d.kbytes = m_pad * 2;
-      d.splits = 1;
       d.out = b.dw + v0 * b.ld_dw;
       d.ld_out = b.ld_dw;
       launch_nt<false, kSum>(d, pick_tile(n, h.k, cus, false), cus, s);
