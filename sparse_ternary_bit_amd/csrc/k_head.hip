@@ -929,13 +929,15 @@ __global__ __launch_bounds__(kFewWaves * 64, 2) void nt_few_kernel(NtArgs a) {
   }
 }
 
-// dx of few rows, straight from the head as it lies, which is read once more:
-// a workgroup adds dl[., v] w[v, c] for 128 columns c and its share of the
-// words v, 64 at a time.  The matrix cores want eight words of one column, so
-// the head's tile [word][column] is read with the transposing LDS read; 8-bit
-// words become bf16, which holds them exactly, on their way through LDS.
-// Direct loads run two stages (8-bit: three) ahead.  (36 rows under 44492 x
-// 4782: 48 us and 110 for a transposed copy of the head before it.)
+// dx of few rows under an 8-bit head, whose stream is then the bound: a
+// workgroup adds dl[., v] w[v, c] for 128 columns c and its share of the words
+// v, 64 at a time.  The matrix cores want eight words of one column, so the
+// head's tile [word][column] becomes bf16, which holds 8-bit integers exactly,
+// on its way through LDS and is read with the transposing LDS read.  Direct
+// loads run three stages ahead.  (Gradient of 1 to 32 rows under 32000 x 4096:
+// 67 to 74 us, 80 to 89 in tiles of 256 x 256; of 64 rows under 131072 x 7168:
+// 606 and 476.)
+constexpr int64_t kFewRows = 32;
 constexpr int kDxWords = 64, kDxCols = 128;
 
 struct DxFewArgs {
@@ -949,21 +951,19 @@ struct DxFewArgs {
   int strips, per;      // column strips; stages of a split
 };
 
-template <bool kI8, int NT>
 __global__ __launch_bounds__(256) void head_dx_few_kernel(DxFewArgs a) {
-  constexpr int kBuf = kI8 ? 4 : 3;
-  constexpr int kWBytes = kDxWords * kDxCols * (kI8 ? 1 : 2), kTBytes = NT * 16 * kDxWords * 2;
+  constexpr int NT = kFewRows / 16, kBuf = 4;
+  constexpr int kWBytes = kDxWords * kDxCols, kTBytes = NT * 16 * kDxWords * 2;
   constexpr int kLW = kWBytes / 1024 / 4, kLT = kTBytes / 1024 / 4;  // load instructions a stage and wavefront
   static_assert(kLT >= 1, "every wavefront issues the same loads");
   __shared__ __align__(16) char sw[kBuf][kWBytes];
   __shared__ __align__(16) char st[kBuf][kTBytes];
-  __shared__ __align__(16) char wide[kI8 ? 2 : 1][kI8 ? kDxWords * kDxCols * 2 : 16];  // 8-bit words as bf16
+  __shared__ __align__(16) char wide[2][kDxWords * kDxCols * 2];  // as bf16
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q = lane >> 4, r = lane & 15;
   const int strip = blockIdx.x % a.strips, split = blockIdx.x / a.strips;
   const int64_t c0 = static_cast<int64_t>(strip) * kDxCols;
-  const int esz = kI8 ? 1 : 2;
-  const int width = static_cast<int>(min(static_cast<int64_t>(kDxCols) * esz, ((a.k * esz + 15) & ~int64_t{15}) - c0 * esz));  // bytes of a row here
+  const int width = static_cast<int>(min(static_cast<int64_t>(kDxCols), ((a.k + 15) & ~int64_t{15}) - c0));  // bytes of a row here
   const int all = static_cast<int>((a.n + kDxWords - 1) / kDxWords);
   const int s_lo = split * a.per, ns = max(0, min(all - s_lo, a.per));
   auto stage = [&](int s) {
@@ -971,13 +971,13 @@ __global__ __launch_bounds__(256) void head_dx_few_kernel(DxFewArgs a) {
     const int64_t v0 = static_cast<int64_t>(s_lo + s) * kDxWords;
     const bool real = s < ns;
     const int vv = real ? static_cast<int>(min(static_cast<int64_t>(kDxWords), a.n - v0)) : 0;
-    const Rsrc rw = make_rsrc(a.w + (real ? v0 * a.ldw + c0 * esz : 0), real ? static_cast<uint32_t>((vv - 1) * a.ldw) + width : 0);
+    const Rsrc rw = make_rsrc(a.w + (real ? v0 * a.ldw + c0 : 0), real ? static_cast<uint32_t>((vv - 1) * a.ldw) + width : 0);
     const Rsrc rt = make_rsrc(a.dl + (real ? v0 : 0), real ? static_cast<uint32_t>((a.m - 1) * a.ld_dl * 2) + kDxWords * 2 : 0);
-    constexpr int kPer = kI8 ? 8 : 16;  // 16-byte chunks of a word's row
+    constexpr int kPer = kDxCols / 16;  // 16-byte chunks of a word's row
 #pragma unroll
     for (int i = 0; i < kLW; ++i) {
       const int ins = wave + 4 * i, t = ins * (64 / kPer) + lane / kPer;
-      const int c = (lane % kPer) ^ (kI8 ? 0 : tile_swizzle(t));
+      const int c = lane % kPer;
       lds_load16(rw, sw[buf] + ins * 1024, t < vv && c * 16 < width ? t * static_cast<uint32_t>(a.ldw) + c * 16 : 0xFFFFFFF0u);
     }
 #pragma unroll
@@ -997,29 +997,26 @@ __global__ __launch_bounds__(256) void head_dx_few_kernel(DxFewArgs a) {
     // stage s has landed, here and for everyone, and everyone has read stage s - 1
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((kLW + kLT) * (kBuf - 2)) : "memory");
     stage(s + kBuf - 1);
-    const char* tile = sw[s % kBuf];
-    if constexpr (kI8) {
-      char* const to = wide[s & 1];
+    const char* const from = sw[s % kBuf];
+    char* const tile = wide[s & 1];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int idx = threadIdx.x + 256 * i, t = idx >> 3, c = idx & 7;
-        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(tile + idx * 16);
-        float f[16];
+    for (int i = 0; i < 2; ++i) {
+      const int idx = threadIdx.x + 256 * i, t = idx >> 3, c = idx & 7;
+      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(from + idx * 16);
+      float f[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) f[e] = static_cast<float>(static_cast<int8_t>(v[e >> 2] >> (8 * (e & 3))));
+      for (int e = 0; e < 16; ++e) f[e] = static_cast<float>(static_cast<int8_t>(v[e >> 2] >> (8 * (e & 3))));
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          u32x4_t o;
-          // whole numbers of at most 8 bits: their lower halves are zeros
+      for (int h = 0; h < 2; ++h) {
+        u32x4_t o;
+        // whole numbers of at most 8 bits: their lower halves are zeros
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            o[e] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, f[8 * h + 2 * e + 1]), __builtin_bit_cast(uint32_t, f[8 * h + 2 * e]), 0x07060302u);
-          *reinterpret_cast<u32x4_t*>(to + t * 256 + (((2 * c + h) ^ tile_swizzle(t)) << 4)) = o;
-        }
+        for (int e = 0; e < 4; ++e)
+          o[e] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, f[8 * h + 2 * e + 1]), __builtin_bit_cast(uint32_t, f[8 * h + 2 * e]), 0x07060302u);
+        *reinterpret_cast<u32x4_t*>(tile + t * 256 + (((2 * c + h) ^ tile_swizzle(t)) << 4)) = o;
       }
-      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-      tile = to;
     }
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int t = 32 * h + 8 * q + (r >> 2);
@@ -1052,85 +1049,6 @@ __global__ __launch_bounds__(256) void head_dx_few_kernel(DxFewArgs a) {
     for (int i = 0; i < 2; ++i) {
       const int64_t c = c0 + wave * 32 + 16 * i + 4 * q;
       if (c < a.ld_acc) *reinterpret_cast<f32x4_t*>(a.acc + (split * a.m + tok) * a.ld_acc + c) = acc[i][j];
-    }
-  }
-}
-
-// dW of few rows: the sum is so short that dW's own stream is the bound.  A
-// wavefront holds dl's transpose of 64 words as operands and walks the
-// columns, 64 at a time, with x's transpose from cache.  Eight
-// neighbouring columns of a lane pass through LDS, so that rows leave in pieces
-// of 128 bytes; where those are whole lines, past the caches.  (10 rows of
-// 129372 words: x 7168 422 us, 558 through the caches; x 7024, whose rows start
-// inside lines, 655, 991 past the caches, 1030 in 256 x 256 tiles.)
-struct DwFewArgs {
-  const uint16_t* dlt;   // [n][ld], zeros for tokens up to ld
-  const uint16_t* xt;    // [k][ld], likewise
-  int64_t ld;            // 64 or 128
-  int64_t n, k;
-  uint16_t* dw;
-  int64_t ld_dw;
-};
-
-template <int kHalves>  // 64 tokens each
-__global__ __launch_bounds__(256) void head_dw_few_kernel(DwFewArgs a) {
-  constexpr int kSteps = 2 * kHalves;  // of 32 tokens
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int q = lane >> 4, r = lane & 15;
-  __shared__ __align__(16) char slab[4][32 * 64 * 2];
-  const Slab<64> sl{slab[wave], lane};
-  const bool lines = ((reinterpret_cast<uintptr_t>(a.dw) | static_cast<uintptr_t>(a.ld_dw * 2)) & 127) == 0;
-  const int64_t v0 = static_cast<int64_t>(blockIdx.x) * 64;
-  u32x4_t d[4][kSteps];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int64_t row = min(v0 + 16 * j + r, a.n - 1);
-#pragma unroll
-    for (int h = 0; h < kSteps; ++h) d[j][h] = *reinterpret_cast<const u32x4_t*>(a.dlt + row * a.ld + 32 * h + 8 * q);
-  }
-  const int64_t groups = (a.k + 63) / 64;
-  for (int64_t g = blockIdx.y * 4 + wave; g < groups; g += gridDim.y * 4) {
-    const int64_t c0 = g * 64;
-    f32x4_t acc[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0, 0, 0, 0};
-#pragma unroll
-    for (int h = 0; h < kSteps; ++h) {
-      u32x4_t x[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t col = min(c0 + 32 * (i >> 1) + pair_channel(r, i & 1), a.k - 1);
-        x[i] = *reinterpret_cast<const u32x4_t*>(a.xt + col * a.ld + 32 * h + 8 * q);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = Mfma<false>::run(x[i], d[j][h], acc[i][j]);
-    }
-    // word v0 + 16 j + r, columns c0 + 32 p + 8 q + 0..7: to pieces of 128 bytes
-    // through LDS
-    const int nv = static_cast<int>(min(int64_t{64}, a.k - c0));
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t row = v0 + 16 * j + r;
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const int c = 32 * p + 8 * q;
-        float o[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = acc[2 * p + (e >> 2)][j][e & 3];
-        const Raw8<bf16_t> b = pack8<bf16_t>(o);
-        *reinterpret_cast<u32x4_t*>(sl.at(16 * (j & 1) + r, c / 8)) = b.w[0];
-        if (c + 8 > nv && c < nv && row < a.n) store8<bf16_t>(reinterpret_cast<bf16_t*>(a.dw) + row * a.ld_dw, c0 + c, a.k, b);
-      }
-      if (j & 1) {
-        sl.fence();
-        const int64_t t0 = v0 + 16 * (j - 1);
-        sl.store_rows(a.dw + t0 * a.ld_dw + c0, a.ld_dw, static_cast<int>(min(int64_t{32}, a.n - t0)), nv & ~7, lines);
-        sl.fence();
-      }
     }
   }
 }
@@ -1220,30 +1138,38 @@ __global__ __launch_bounds__(256) void transpose_kernel(const char* in, int64_t 
   }
 }
 
-// The parts of a split sum, rounded to bf16: 64 sums a workgroup, every fourth
-// part a thread.
+// The parts of a split sum, rounded to bf16: four columns a thread, every
+// fourth part a wavefront.  (9 parts of 256 x 7168: 46 us a column a thread.)
 __global__ __launch_bounds__(256) void join_splits_kernel(const float* acc, int64_t ld_acc, int splits, int64_t m, int64_t n,
                                                           uint16_t* out, int64_t ld_out) {
-  __shared__ float part[4][64];
+  __shared__ f32x4_t part[4][64];
   const int lane = threadIdx.x & 63, g = threadIdx.x >> 6;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 64 + lane;
-  const int64_t row = i / n, c = i - row * n;
-  float s = 0.0f;
-  if (i < m * n) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 64 + lane, quads = ld_acc / 4;
+  const int64_t row = i / quads, c = (i - row * quads) * 4;
+  const bool on = row < m;
+  f32x4_t s = {0, 0, 0, 0};
+  auto add = [&](const f32x4_t& v) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[e] += v[e];
+  };
+  if (on) {
+    const float* const at = acc + row * ld_acc + c;
     int p = g;
-    for (; p + 28 < splits; p += 32) {
-      float v[8];
+    for (; p + 12 < splits; p += 16) {
+      f32x4_t v[4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = acc[((p + 4 * e) * m + row) * ld_acc + c];
+      for (int e = 0; e < 4; ++e) v[e] = *reinterpret_cast<const f32x4_t*>(at + (p + 4 * e) * m * ld_acc);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s += v[e];
+      for (int e = 0; e < 4; ++e) add(v[e]);
     }
-    for (; p < splits; p += 4) s += acc[(p * m + row) * ld_acc + c];
+    for (; p < splits; p += 4) add(*reinterpret_cast<const f32x4_t*>(at + p * m * ld_acc));
   }
   part[g][lane] = s;
   __syncthreads();
-  if (g || i >= m * n) return;
-  out[row * ld_out + c] = static_cast<uint16_t>(bf16_round((part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane])));
+  if (g || !on) return;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (c + e < n) out[row * ld_out + c + e] = static_cast<uint16_t>(bf16_round((part[0][lane][e] + part[1][lane][e]) + (part[2][lane][e] + part[3][lane][e])));
 }
 
 __global__ __launch_bounds__(256) void zero_rows_kernel(uint16_t* out, int64_t ld, int64_t m, int64_t n) {
@@ -1310,7 +1236,6 @@ void launch_nt(const NtArgs& a, Tile t, int cus, hipStream_t s) {
   }
 }
 
-constexpr int64_t kFewRows = 128;   // rows whose gradient reads the head as it lies
 
 int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
@@ -1375,19 +1300,15 @@ static int dx_splits(int64_t rows, int64_t k, int64_t stages, int64_t pieces, in
   return best;
 }
 
-HeadBwdPlan plan_head_bwd(int64_t rows, int64_t vocab, int64_t k, bool dx, bool dw, int cus) {
+HeadBwdPlan plan_head_bwd(bool i8, int64_t rows, int64_t vocab, int64_t k, bool dx, bool dw, int cus) {
   HeadBwdPlan p{};
   const int64_t m_pad = up(rows, 64);
-  if (rows <= kFewRows && rows * up(vocab, 64) <= int64_t{1} << 30) {
+  if (i8 && rows <= kFewRows && rows * up(vocab, 64) <= int64_t{1} << 30) {
     // the whole vocabulary at once: dl is small beside the head (and its rows within 32-bit offsets)
     p.few = 1;
     p.width = up(vocab, 64);
     p.pieces = 1;
     int64_t at = up(rows * p.width * 2, 256);
-    p.dlt = at;
-    if (dw) at += up(p.width * m_pad * 2, 256);
-    p.xt = at;
-    if (dw) at += up(k * m_pad * 2, 256);
     p.acc = at;
     // two workgroups a CU, of four stages of words at least
     const int64_t strips = (k + kDxCols - 1) / kDxCols, stages = (vocab + kDxWords - 1) / kDxWords;
@@ -1455,9 +1376,7 @@ hipError_t launch_head_bwd(const HeadArgs& h, const HeadBwdArgs& b, const HeadBw
       const int64_t strips = (h.k + kDxCols - 1) / kDxCols;
       const DxFewArgs d{dl, p.width, a.w, h.ldw, h.rows, n, h.k, acc, up(h.k, 8), static_cast<int>(strips), p.per};
       const dim3 grid(static_cast<unsigned>(strips * p.splits));
-      auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, d); };
-      if (h.i8) h.rows <= 32 ? go(head_dx_few_kernel<true, 2>) : h.rows <= 64 ? go(head_dx_few_kernel<true, 4>) : go(head_dx_few_kernel<true, 8>);
-      else h.rows <= 32 ? go(head_dx_few_kernel<false, 2>) : h.rows <= 64 ? go(head_dx_few_kernel<false, 4>) : go(head_dx_few_kernel<false, 8>);
+      hipLaunchKernelGGL(head_dx_few_kernel, grid, dim3(256), 0, s, d);
     } else if (b.dx) {
       NtArgs d{};
       d.a = reinterpret_cast<const char*>(dl);
@@ -1478,14 +1397,7 @@ hipError_t launch_head_bwd(const HeadArgs& h, const HeadBwdArgs& b, const HeadBw
       if (h.i8) launch_wide<false, kSum, kAcross8>(d, cus, s);
       else launch_wide<false, kSum, kAcross16>(d, cus, s);
     }
-    if (b.dw && p.few) {
-      const DwFewArgs d{dlt, xt, m_pad, n, h.k, b.dw, b.ld_dw};
-      const int64_t words = (n + 63) / 64, groups = (h.k + 255) / 256;
-      // a workgroup's columns: all of them, or as many shares as give every CU four workgroups
-      const dim3 grid(static_cast<unsigned>(words), static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(groups, 4 * cus / words))));
-      if (m_pad == 64) hipLaunchKernelGGL((head_dw_few_kernel<1>), grid, dim3(256), 0, s, d);
-      else hipLaunchKernelGGL((head_dw_few_kernel<2>), grid, dim3(256), 0, s, d);
-    } else if (b.dw) {
+    if (b.dw) {
       NtArgs d{};
       d.a = reinterpret_cast<const char*>(dlt);
       d.lda = m_pad * 2;
@@ -1502,7 +1414,7 @@ hipError_t launch_head_bwd(const HeadArgs& h, const HeadBwdArgs& b, const HeadBw
     if (e != hipSuccess) return e;
   }
   if (b.dx && (p.few || p.splits > 1))
-    hipLaunchKernelGGL(join_splits_kernel, dim3(static_cast<unsigned>((h.rows * h.k + 63) / 64)), dim3(256), 0, s, acc, up(h.k, 8), p.splits, h.rows, h.k, b.dx,
+    hipLaunchKernelGGL(join_splits_kernel, dim3(static_cast<unsigned>((h.rows * (up(h.k, 8) / 4) + 63) / 64)), dim3(256), 0, s, acc, up(h.k, 8), p.splits, h.rows, h.k, b.dx,
                        b.ld_dx);
   return hipGetLastError();
 }

@@ -1024,7 +1024,7 @@ stq_status stq_head_cross_entropy_backward_workspace(int x_dtype, int64_t n_rows
   if (st != STQ_OK) return st;
   if (want_dw && x_dtype == STQ_X_I8) return fail(STQ_E_ARG, "%s: 8-bit weights have no gradient", who);
   if (n_rows > 0 && (want_dx || want_dw))
-    *workspace_bytes = stq::plan_head_bwd(n_rows, vocab, k, want_dx != 0, want_dw != 0, n_cus > 0 ? n_cus : stq::cus_of_current_device()).bytes;
+    *workspace_bytes = stq::plan_head_bwd(x_dtype == STQ_X_I8, n_rows, vocab, k, want_dx != 0, want_dw != 0, n_cus > 0 ? n_cus : stq::cus_of_current_device()).bytes;
   return ok();
 }
 
@@ -1052,7 +1052,7 @@ stq_status stq_head_cross_entropy_backward(const void* x, int x_dtype, int64_t x
     if (!lse || !grad_loss) return fail(STQ_E_ARG, "%s: null pointer", who);
     if (!aligned(lse, 4) || !aligned(grad_loss, 4)) return fail(STQ_E_ALIGN, "%s: lse or grad_loss not 4-byte aligned", who);
     const int cus = stq::cus_of_stream(s);
-    const stq::HeadBwdPlan plan = stq::plan_head_bwd(n_rows, vocab, k, dx != nullptr, dw != nullptr, cus);
+    const stq::HeadBwdPlan plan = stq::plan_head_bwd(x_dtype == STQ_X_I8, n_rows, vocab, k, dx != nullptr, dw != nullptr, cus);
     st = check_workspace(workspace, workspace_bytes, plan.bytes, who);
     if (st != STQ_OK) return st;
     const stq::HeadBwdArgs b{lse, grad_loss, dx, dx_row_stride, dw, dw_row_stride};

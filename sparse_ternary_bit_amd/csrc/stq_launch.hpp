@@ -374,7 +374,7 @@ struct HeadBwdPlan {
   int64_t dlt, xt, acc;        // workspace offsets
   int64_t bytes;
 };
-HeadBwdPlan plan_head_bwd(int64_t rows, int64_t vocab, int64_t k, bool dx, bool dw, int cus);
+HeadBwdPlan plan_head_bwd(bool i8, int64_t rows, int64_t vocab, int64_t k, bool dx, bool dw, int cus);
 hipError_t launch_head_bwd(const HeadArgs& h, const HeadBwdArgs& b, const HeadBwdPlan& p, void* ws, int cus, hipStream_t s);
 hipError_t launch_head_zero(uint16_t* dw, int64_t ld, int64_t vocab, int64_t k, hipStream_t s);
 

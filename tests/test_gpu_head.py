@@ -118,7 +118,7 @@ class Case:
 
 
 # every tile of either product: 16 channels (up to 16 rows), 64 x 64, 64 x 128 and 64 x 256 (more than 32768 and 65536
-# words), 128 x 128, 256 x 256; dx of up to 128 rows reads the head as it lies, of more a transposed piece
+# words), 128 x 128, 256 x 256; dx of up to 32 rows and of more (8-bit heads)
 SHAPES = [(1, 1, 1), (1, 2, 9), (3, 65, 8), (5, 130, 100), (64, 1000, 64), (65, 257, 130), (37, 16450, 33), (64, 16500, 72),
           (1, 20000, 17), (300, 700, 129), (129, 4099, 200), (700, 9001, 65), (512, 66000, 64), (513, 65537, 40),
           (40, 40000, 24), (50, 70000, 24), (16, 4000, 260), (17, 3000, 96), (128, 3333, 150)]
@@ -131,7 +131,7 @@ def test_forward(stq, n, v, k, i8):
     c.check_forward(*stq.head_cross_entropy(c.x, c.w, c.targets, **c.args()))
 
 
-# dW's 256 x 256 tiles; several pieces of the vocabulary, dx's sum shared out or not, or its last round's alone
+# dW's 256 x 256 tiles; several pieces of the vocabulary, dx's sum shared out or not, in two rounds of tiles or one
 @pytest.mark.parametrize("i8", [False, True])
 @pytest.mark.parametrize("n, v, k", SHAPES + [(70, 8192, 2048), (20, 17000, 8000), (900, 17000, 8000),
                                               (1300, 4500, 6501), (4097, 3001, 7000)])
