@@ -89,13 +89,13 @@ __device__ __forceinline__ float exponents(float (&v)[kN], float& top) {
   for (int j = 1; j < kN; ++j) m = fmaxf(m, v[j]);
   m = fmax16(m);
   top = m;
+  // masked logits count for nothing, under a masked maximum too; a NaN stays one
+  const float base = m == -INFINITY ? 0.0f : m;
   float s = 0.0f;
 #pragma unroll
   for (int j = 0; j < kN; ++j) {
-    // masked logits under a masked maximum count for nothing; a NaN stays one
-    const float x = v[j] == -INFINITY ? 0.0f : exp_of(v[j] - m);
-    v[j] = x;
-    s += x;
+    v[j] = exp_of(v[j] - base);
+    s += v[j];
   }
   return sum16(s);
 }
@@ -191,10 +191,8 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteKernelArgs g) {
       load_logits<T, kN>(row, lane16, E, valid, v);
       uint32_t key[kN];
 #pragma unroll
-      for (int j = 0; j < kN; ++j) {
-        const int c = column(lane16, j);
-        key[j] = c < E ? (order_bits(v[j]) & ~kIndex) | (kIndex - c) : 0u;
-      }
+      for (int j = 0; j < kN; ++j)   // (columns past the experts: below a masked expert's, so never among E)
+        key[j] = (order_bits(v[j]) & ~kIndex) | (kIndex - column(lane16, j));
       float top;
       const float sum = exponents<kN>(v, top);
       // nothing for a token that is masked throughout, NaN for one without a distribution
@@ -203,20 +201,20 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteKernelArgs g) {
       for (int q = 0; q < kN / 4; ++q)
         *reinterpret_cast<f32x4_t*>(&prob[tl - tp][column(lane16, 4 * q)]) =
             f32x4_t{v[4 * q] * inv, v[4 * q + 1] * inv, v[4 * q + 2] * inv, v[4 * q + 3] * inv};
-      // extraction: after step i, lane i % 16 holds the i-th key
+      // extraction: after step i, lane i % 16 holds the i-th key.  Less the last
+      // one, in 32 bits that wrap, keys taken already are small and those that
+      // are left are large, so nothing has to be taken out.
       uint32_t mine[2] = {0u, 0u}, last = 0u;
       bool unsure = false;
       const int steps = sizeof(T) == 4 ? min(k + 1, E) : k;
       for (int i = 0; i < steps; ++i) {
-        uint32_t m = key[0];
+        uint32_t m = key[0] - last;
 #pragma unroll
-        for (int j = 1; j < kN; ++j) m = max(m, key[j]);
-        m = max16(m);
+        for (int j = 1; j < kN; ++j) m = max(m, key[j] - last);
+        m = max16(m) + last;
         unsure |= i > 0 && ((m ^ last) & ~kIndex) == 0u;
         last = m;
         if (lane16 == (i & 15) && i < k) mine[i >> 4] = m;
-#pragma unroll
-        for (int j = 0; j < kN; ++j) key[j] = key[j] == m ? 0u : key[j];
       }
       int pick[2] = {static_cast<int>(kIndex - (mine[0] & kIndex)), static_cast<int>(kIndex - (mine[1] & kIndex))};
       if (sizeof(T) == 4 && __any(unsure && valid)) {
