@@ -9,10 +9,21 @@
 // operands' memory), so one kernel does all of it, with what belongs to each
 // product behind its sums: the running maximum and sum of exponentials of a
 // tile of logits (forward), dl in bf16 (the logits once more, a piece of the
-// vocabulary at a time), or sums stored or added up (dx, dW).  The gradients'
-// other operands are laid out along their sums first: W's piece and x
-// transposed, and dl stored both ways from the tile in LDS.  A piece's dl, its
-// transpose and W's piece stay near the 256 MB of the last-level cache.
+// vocabulary at a time), or sums stored or added up (dx, dW).  dl is stored both
+// ways from the tile in LDS, and x transposed once, so that dW is such a product
+// too; dx takes W as it lies, a row for every term of its sum, with transposing
+// reads.  A piece's dl and its transpose stay near the 256 MB of the last-level
+// cache.
+//
+// Sums are in fp32 (8-bit operands': exact, in int32), statistics in fp32.  dl
+// is rounded to bf16 once, half a step of 2^-8 relative to each of its values,
+// because the matrix cores take dx's and dW's factors in it.
+//
+// 4096 rows under 131072 x 7168 in bf16: 5.2 to 5.3 ms, 1.46 PFLOP/s (a large
+// library product 1.56); matrix cores 75 % busy at 1.8 of 2.4 GHz, so the card's
+// power is the bound.  The same vocabulary's gradients: 2048 rows under the head
+// in 8 bits 4.4 to 4.5 ms (8-bit logits 2.5 POP/s, dx 1.3 to 1.4 PFLOP/s), 4099
+// rows under a bf16 head with dW 6.8 to 6.9 ms, 1.30 PFLOP/s.
 #include <algorithm>
 #include <type_traits>
 
@@ -811,8 +822,8 @@ __global__ __launch_bounds__(256, 1) void nt_wide_kernel(NtArgs a) {
 // channels and all tokens; the wavefronts share the sum, each loading its part
 // of the head once, straight into matrix-core operands (16 bytes a lane, kBatch
 // steps in flight), the tokens from cache the same way, and the eight sums are
-// added through LDS.  (2 rows under a head of 566 x 5863, the logits of the
-// gradient: 24 us in tiles of 64.)
+// added through LDS.  (2 rows under a head of 566 x 5863: 11 us, 25 in tiles of
+// 64 x 64.)
 constexpr int kFewWaves = 8, kFewBatch = 8;
 
 template <bool kI8, int kEpi>
@@ -1188,14 +1199,19 @@ void launch_tile(NtArgs a, int step_n, hipStream_t s) {
 }
 
 // The tile for m tokens and n channels.
-//  * Few tokens under a head: a workgroup for 16 channels, until its re-reads of
-//    the tokens weigh on a long channel list.
-//  * Up to 64 tokens: as wide a channel tile as leaves every CU two.
-//  * More: the smallest of three estimates, in rounds of the chip.
+//  * Few tokens under a head: a workgroup for 16 channels, until there are as
+//    many tiles of 64 as half the compute units (8 x 7168: 4000 words 17 us, 31 in
+//    tiles of 64 x 64; 8000 words 28 and 32; 12000 words 38 and 33).
+//  * Up to 64 tokens: as wide a channel tile as leaves every CU two (40 rows of
+//    4096 in 8 bits, 50000 words: 41, 37 and 40 us in tiles of 64, 128 and 256; 37
+//    x 7168, 100003 words: 142, 147 and 133).
+//  * More: the smallest of three estimates, in rounds of the chip (tiles of 64,
+//    128 and 256: 300 x 1024 x 8000 words in bf16 15.0, 15.6, 32 us; 512 x 4096 x
+//    32000 203, 134, 106).
 enum Tile { kFew, k64x64, k64x128, k64x256, k128x128, k256x256 };
 
 Tile pick_tile(int64_t m, int64_t n, int cus, bool few) {
-  if (few && (m <= 4 || (m <= 16 && n <= 128 * cus))) return kFew;
+  if (few && m <= 16 && n <= 32 * cus) return kFew;
   if (m <= 64) return n <= 128 * cus ? k64x64 : n <= 256 * cus ? k64x128 : k64x256;
   auto per_cu = [&](int64_t t) { return (((m + t - 1) / t) * ((n + t - 1) / t) + cus - 1) / cus; };
   const int64_t u256 = per_cu(256), u128 = per_cu(128), u64 = per_cu(64);

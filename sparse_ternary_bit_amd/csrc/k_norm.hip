@@ -39,7 +39,9 @@ __device__ __forceinline__ float block_sum(float v, float* slot) {
 }
 
 // One workgroup a row; kHeld groups of 8 values a thread stay in registers,
-// what lies beyond (rows of more than 8192 values) is read again.
+// what lies beyond (rows of more than 8192 values) is read again.  HBM bounds
+// it: 8192 rows of 7168, bf16 with a residual to 8 bits, 76 us for 411 MB, 5.4
+// TB/s read and written.
 template <typename TX, typename TR, int kThreads, int kHeld>
 __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs a) {
   constexpr bool kRes = !__is_same(TR, None);
@@ -148,8 +150,9 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs a) {
 }
 
 // dx, and each workgroup's part of dw: a workgroup walks the rows blockIdx.x,
-// + gridDim.x, ..., and its threads add dy u for their columns in registers.
-// kHeld * kThreads * 8 columns at most.
+// + gridDim.x, ..., and its threads add dy u for their columns in registers, so
+// that dw costs no pass of its own.  kHeld * kThreads * 8 columns at most.  HBM
+// bounds it: 4099 rows of 7168 with dh, all bf16, 47 us for 235 MB, 5.0 TB/s.
 template <typename TH, typename TY, int kThreads, int kHeld>
 __global__ __launch_bounds__(kThreads, 2) void norm_bwd_kernel(NormBwdArgs a, float* part) {
   __shared__ float slot[2][kThreads / 64];
@@ -297,6 +300,11 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
     using TX = decltype(x);
     using TR = decltype(res);
     const dim3 grid(static_cast<unsigned>(a.rows));
+    // one wavefront a short row, no barrier (8192 x 512: 8.1 us, 17 in four); a row
+    // held in one group a thread while it fits (8192 x 2048: 23 us, 45 with four
+    // groups); more rows than the chip takes at once in fewer, longer threads (7168
+    // values by 1024 threads and by 256: 1 row 4.3 and 5.7 us, 512 rows 9.1 and 10.0,
+    // 1024 rows 16.0 and 14.6, 8192 rows 107 and 82)
     if (a.d <= 512) hipLaunchKernelGGL((norm_kernel<TX, TR, 64, 1>), grid, dim3(64), 0, s, a);
     else if (a.d <= 2048) hipLaunchKernelGGL((norm_kernel<TX, TR, 256, 1>), grid, dim3(256), 0, s, a);
     else if (a.rows <= 512) hipLaunchKernelGGL((norm_kernel<TX, TR, 1024, 1>), grid, dim3(1024), 0, s, a);
@@ -321,6 +329,7 @@ hipError_t launch_norm_bwd(const NormBwdArgs& a, float* part, int cus, hipStream
     using TH = decltype(h);
     using TY = decltype(y);
     const dim3 grid(static_cast<unsigned>(parts));
+    // (as in the forward: 4099 x 512 9.8 us, 12.0 by 256 threads; x 2048 14.5 us, 27 with four groups)
     if (a.d <= 512) hipLaunchKernelGGL((norm_bwd_kernel<TH, TY, 64, 1>), grid, dim3(64), 0, s, a, pw);
     else if (a.d <= 2048) hipLaunchKernelGGL((norm_bwd_kernel<TH, TY, 256, 1>), grid, dim3(256), 0, s, a, pw);
     else if (a.d <= 8192) hipLaunchKernelGGL((norm_bwd_kernel<TH, TY, 256, 4>), grid, dim3(256), 0, s, a, pw);

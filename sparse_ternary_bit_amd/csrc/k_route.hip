@@ -8,8 +8,8 @@
 // Tokens are taken 64 at a time (a chunk).  16 lanes hold a token's logits, so
 // that every reduction is four DPP rotations and serves four tokens; a key of
 // 22 bits of the logit over 10 of the expert's index makes an extraction one
-// maximum and one comparison a logit (150 instructions a token for 8 of 256
-// experts; a maximum with a separate search for its index takes twice that).
+// subtraction and half a maximum a logit (a maximum with a separate search for
+// its index takes three times that).
 // bf16 logits fit such a key; fp32 logits that agree in their first 22 bits
 // next to the chosen ones are chosen again with all 32.
 //
@@ -17,6 +17,10 @@
 // expert at most once, so an expert's tokens of a chunk are 64 bits, a pair's
 // place in the chunk is a population count, and the chunks' counts need one
 // prefix sum an expert.  One chunk runs as one launch, more as three.
+//
+// One token of 256 experts 5.3 us; 16384 tokens 16.0 (choice, its instructions
+// and one latency of the logits: a chunk a compute unit) + 4.0 + 5.0 us, where
+// the 19 MB alone would take 4.
 #include <algorithm>
 #include <type_traits>
 
