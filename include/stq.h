@@ -653,8 +653,9 @@ stq_status stq_combine_rows_backward(const void* dy, int dy_dtype, int64_t dy_ro
  *             stq_rmsnorm_rows write them)
  *   w         [vocab, k] of x's type, for int8 with w_scale fp32 [vocab]
  *             both 16-byte aligned with row strides (elements) of whole 16-byte
- *             units, at least k and at most 2^23 bytes; a row's bytes behind k,
- *             up to a whole 16-byte unit, may be read and count for nothing
+ *             units, at least k and at most 2^23 bytes; the bytes between one
+ *             row's k elements and the next row, and behind the last row up
+ *             to a whole 16-byte unit, may be read and count for nothing
  *   targets   int32 [n_rows]; a negative one leaves its row out (loss 0), one
  *             past the vocabulary gives loss NaN
  *   loss, lse fp32 [n_rows]

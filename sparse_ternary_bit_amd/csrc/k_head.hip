@@ -1303,12 +1303,13 @@ hipError_t launch_head(const HeadArgs& h, float* loss, float* lse, void* ws, int
 // those the width whose tiles fill whole rounds of the chip best.
 // Parts that dx's sum over `stages` x 64 words is shared out into when its tiles
 // leave compute units idle: the fewest of what a tile's stages and its end (1.4
-// us a stage, 8 stages an end) and the parts' store and join cost together.
+// us a stage, 8 stages an end) and the parts' store and join cost together.  Above
+// 16 rounds there is nothing to gain (and the join's launch stays small).
 static int dx_splits(int64_t rows, int64_t k, int64_t stages, int64_t pieces, int cus) {
   const int64_t tiles = (rows + 255) / 256 * ((k + 255) / 256);
   int best = 1;
   double best_us = 0;
-  for (int64_t s = 1; s <= std::min<int64_t>(64, (stages + 3) / 4); ++s) {
+  for (int64_t s = 1; s <= std::min<int64_t>(64, (stages + 3) / 4) && (s == 1 || tiles * s <= 16 * cus); ++s) {
     const double walk = 1.4 * pieces * ((tiles * s + cus - 1) / cus) * ((stages + s - 1) / s + 8);
     const double us = walk + (s > 1 ? s * rows * k * 8 / 4.7e6 : 0.0);
     if (s == 1 || us < best_us) best = static_cast<int>(s), best_us = us;

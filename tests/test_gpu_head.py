@@ -134,7 +134,7 @@ def test_forward(stq, n, v, k, i8):
 # dW's 256 x 256 tiles; several pieces of the vocabulary, dx's sum shared out or not, in two rounds of tiles or one
 @pytest.mark.parametrize("i8", [False, True])
 @pytest.mark.parametrize("n, v, k", SHAPES + [(70, 8192, 2048), (20, 17000, 8000), (900, 17000, 8000),
-                                              (1300, 4500, 6501), (4097, 3001, 7000)])
+                                              (1300, 4500, 6501), (4097, 3001, 6999)])
 def test_backward(stq, n, v, k, i8):
     c = Case(n, v, k, i8, 2 * n + v + k)
     _, lse = stq.head_cross_entropy(c.x, c.w, c.targets, **c.args())
@@ -161,6 +161,22 @@ def test_backward_one_output_and_given_ones(stq):
     stq.head_cross_entropy_backward(xw[:, 8:211], ww[:, 16:219], c.targets, lse, c.grad, dx=dxw[:, 3:206], dw=dww[:, 1:204])
     assert torch.equal(dxw[:, 3:206], dx) and torch.equal(dww[:, 1:204], dw)
     assert bool((dxw[:, :3] == 7).all()) and bool((dxw[:, 206:] == 7).all()) and bool((dww[:, :1] == 7).all()) and bool((dww[:, 204:] == 7).all())
+
+
+@pytest.mark.parametrize("i8", [False, True])
+@pytest.mark.parametrize("n, v, k", [(600, 250, 701), (300, 100, 1030), (260, 256, 515)])
+def test_rows_of_any_stride_and_offset(stq, n, v, k, i8):
+    # one part of the sum: the tiles of 256 x 256 write dx themselves, on odd element boundaries
+    c = Case(n, v, k, i8, n + k)
+    _, lse = stq.head_cross_entropy(c.x, c.w, c.targets, **c.args())
+    wide = torch.full((n, k + 5), 7.0, dtype=torch.bfloat16, device="cuda")
+    big = None if i8 else torch.full((v, k + 3), 7.0, dtype=torch.bfloat16, device="cuda")
+    dx, dw = wide[:, 3:3 + k], None if i8 else big[:, 1:1 + k]
+    stq.head_cross_entropy_backward(c.x, c.w, c.targets, lse, c.grad, need_dw=not i8, dx=dx, dw=dw, **c.args())
+    c.check_backward(dx, dw, lse)
+    assert bool((wide[:, :3] == 7).all()) and bool((wide[:, 3 + k:] == 7).all())
+    if not i8:
+        assert bool((big[:, :1] == 7).all()) and bool((big[:, 1 + k:] == 7).all())
 
 
 def test_rows_left_out_are_not_looked_at(stq):
