@@ -847,6 +847,11 @@ def rmsnorm_rows_backward_workspace(n_rows: int, d: int, need_dweight: bool = Tr
     return wb.value
 
 
+@functools.lru_cache(maxsize=256)
+def _norm_need(n_rows: int, d: int, n_cus: int) -> int:
+    return rmsnorm_rows_backward_workspace(n_rows, d, True, n_cus)
+
+
 def rmsnorm_rows_backward(h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor, dy: torch.Tensor,
                           dh: torch.Tensor | None = None, need_dx: bool = True, need_dweight: bool = True,
                           dx: torch.Tensor | None = None, dweight: torch.Tensor | None = None,
@@ -881,7 +886,7 @@ def rmsnorm_rows_backward(h: torch.Tensor, weight: torch.Tensor, rstd: torch.Ten
     elif dweight is not None:
         raise ValueError("dweight is given but need_dweight is False")
     if workspace is None and need_dweight:
-        workspace = _workspace(None, rmsnorm_rows_backward_workspace(n, d, True, _device_cus(dev)), dev)
+        workspace = _workspace(None, _norm_need(n, d, _device_cus(dev)), dev)
     else:
         workspace = _workspace(workspace, 0, dev)
     _call(dev, "stq_rmsnorm_rows_backward", h.data_ptr(), _kind(h), hs, weight.data_ptr(), rstd.data_ptr(), dy.data_ptr(),

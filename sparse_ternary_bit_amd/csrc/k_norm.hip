@@ -50,15 +50,22 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs a) {
   const int64_t r = blockIdx.x;
   const int64_t d = a.d, groups = (d + 7) / 8;
   const TX* x = static_cast<const TX*>(a.x) + r * a.x_stride;
+  // the residual's type, or any where there is none
+  using Res = std::conditional_t<kRes, TR, bf16_t>;
+  auto load_res = [&](int64_t c) {
+    if constexpr (kRes) return load8<TR>(static_cast<const TR*>(a.res) + r * a.res_stride, c, d);
+    else return Raw8<Res>{};
+  };
   float ss = 0.0f;
   uint32_t mx = 0;  // the largest |v| as bits: a NaN orders above every number and so is kept
   // the sum as it is stored, 8 values from column c on; columns past d are 0
-  auto sum8 = [&](int64_t c, float (&f)[8], Raw8<TX> rx) {
+  auto sum8 = [&](int64_t c, float (&f)[8], Raw8<TX> rx, Raw8<Res> rr) {
+    settle8<TX>(rx, c, d);
     unpack8<TX>(rx, f);
     if constexpr (kRes) {
-      const TR* res = static_cast<const TR*>(a.res) + r * a.res_stride;
       float b[8];
-      load8f<TR>(res, c, d, b);
+      settle8<TR>(rr, c, d);
+      unpack8<TR>(rr, b);
 #pragma unroll
       for (int i = 0; i < 8; ++i) f[i] += b[i];
       const Raw8<TR> o = pack8<TR>(f);
@@ -79,19 +86,23 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs a) {
   float v[kHeld][8];
   {
     Raw8<TX> rx[kHeld];
+    Raw8<Res> rr[kHeld];
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) rx[i] = load8<TX>(x, (threadIdx.x + i * kThreads) * 8, d);
+    for (int i = 0; i < kHeld; ++i) {
+      rx[i] = load8<TX>(x, (threadIdx.x + i * kThreads) * 8, d);
+      rr[i] = load_res((threadIdx.x + i * kThreads) * 8);
+    }
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
       const int64_t c = (threadIdx.x + i * kThreads) * 8;
       float f[8];
-      sum8(c, f, rx[i]);
+      sum8(c, f, rx[i], rr[i]);
       weigh(c, f, v[i]);
     }
   }
   for (int64_t g = threadIdx.x + kHeld * kThreads; g < groups; g += kThreads) {
     float f[8], t[8];
-    sum8(g * 8, f, load8<TX>(x, g * 8, d));
+    sum8(g * 8, f, load8<TX>(x, g * 8, d), load_res(g * 8));
     weigh(g * 8, f, t);
   }
   ss = sum64(ss);
@@ -155,7 +166,10 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs a) {
 // bounds it: 4099 rows of 7168 with dh, all bf16, 47 us for 235 MB, 5.0 TB/s.
 template <typename TH, typename TY, int kThreads, int kHeld>
 __global__ __launch_bounds__(kThreads, 2) void norm_bwd_kernel(NormBwdArgs a, float* part) {
-  __shared__ float slot[2][kThreads / 64];
+  // rows that are read at once: where a row is one group a thread, the latency of
+  // its loads would stand alone (6845 rows of 87, cold: 43 us a row at a time, 24 so)
+  constexpr int kBatch = kHeld == 1 ? 4 : 1, kWaves = kThreads / 64;
+  __shared__ float slot[2][kBatch][kWaves];
   const int64_t d = a.d;
   float w[kHeld][8], acc[kHeld][8];
 #pragma unroll
@@ -165,52 +179,70 @@ __global__ __launch_bounds__(kThreads, 2) void norm_bwd_kernel(NormBwdArgs a, fl
     for (int e = 0; e < 8; ++e) acc[i][e] = 0.0f;
   }
   int odd = 0;
-  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, odd ^= 1) {
-    const TH* h = static_cast<const TH*>(a.h) + r * a.h_stride;
-    const TY* dy = static_cast<const TY*>(a.dy) + r * a.dy_stride;
-    const float rstd = a.rstd[r];
-    Raw8<TH> rh[kHeld], rd[kHeld];
-    Raw8<TY> ry[kHeld];
+  for (int64_t r0 = blockIdx.x; r0 < a.rows; r0 += kBatch * static_cast<int64_t>(gridDim.x), odd ^= 1) {
+    float rstd[kBatch], dot[kBatch];
+    Raw8<TH> rh[kBatch][kHeld], rd[kBatch][kHeld];
+    Raw8<TY> ry[kBatch][kHeld];
+    auto row = [&](int b) { return r0 + static_cast<int64_t>(b) * gridDim.x; };
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      const int64_t c = (threadIdx.x + i * kThreads) * 8;
-      rh[i] = load8<TH>(h, c, d);
-      ry[i] = load8<TY>(dy, c, d);
-    }
-    if (a.dh) {
+    for (int b = 0; b < kBatch; ++b) {
+      const int64_t r = min(row(b), a.rows - 1);   // (past the last: read, and not looked at)
+      rstd[b] = a.rstd[r];
 #pragma unroll
-      for (int i = 0; i < kHeld; ++i)
-        rd[i] = load8<TH>(static_cast<const TH*>(a.dh) + r * a.dh_stride, (threadIdx.x + i * kThreads) * 8, d);
-    }
-    float dot = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      float f[8], g[8];
-      unpack8<TH>(rh[i], f);
-      unpack8<TY>(ry[i], g);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float u = f[e] * rstd;
-        acc[i][e] = fmaf(g[e], u, acc[i][e]);
-        dot = fmaf(g[e] * w[i][e], u, dot);
+      for (int i = 0; i < kHeld; ++i) {
+        const int64_t c = (threadIdx.x + i * kThreads) * 8;
+        rh[b][i] = load8<TH>(static_cast<const TH*>(a.h) + r * a.h_stride, c, d);
+        ry[b][i] = load8<TY>(static_cast<const TY*>(a.dy) + r * a.dy_stride, c, d);
+        if (a.dh) rd[b][i] = load8<TH>(static_cast<const TH*>(a.dh) + r * a.dh_stride, c, d);
       }
     }
-    const float mean = block_sum<kThreads>(dot, slot[odd]) / static_cast<float>(d);
-    if (a.dx) {
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      if (row(b) >= a.rows) break;
+      dot[b] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) {
+        float f[8], g[8];
+        settle8<TH>(rh[b][i], (threadIdx.x + i * kThreads) * 8, d);
+        settle8<TY>(ry[b][i], (threadIdx.x + i * kThreads) * 8, d);
+        unpack8<TH>(rh[b][i], f);
+        unpack8<TY>(ry[b][i], g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float u = f[e] * rstd[b];
+          acc[i][e] = fmaf(g[e], u, acc[i][e]);
+          dot[b] = fmaf(g[e] * w[i][e], u, dot[b]);
+        }
+      }
+      dot[b] = sum64(dot[b]);
+      if (kWaves > 1 && (threadIdx.x & 63) == 0) slot[odd][b][threadIdx.x >> 6] = dot[b];
+    }
+    if constexpr (kWaves > 1) __syncthreads();
+    if (!a.dx) continue;
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      if (row(b) >= a.rows) break;
+      if constexpr (kWaves > 1) {
+        dot[b] = slot[odd][b][0];
+#pragma unroll
+        for (int i = 1; i < kWaves; ++i) dot[b] += slot[odd][b][i];
+      }
+      const float mean = dot[b] / static_cast<float>(d);
 #pragma unroll
       for (int i = 0; i < kHeld; ++i) {
         const int64_t c = (threadIdx.x + i * kThreads) * 8;
         float f[8], g[8], o[8];
-        unpack8<TH>(rh[i], f);
-        unpack8<TY>(ry[i], g);
+        unpack8<TH>(rh[b][i], f);
+        unpack8<TY>(ry[b][i], g);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = rstd * (g[e] * w[i][e] - f[e] * rstd * mean);
+        for (int e = 0; e < 8; ++e) o[e] = rstd[b] * (g[e] * w[i][e] - f[e] * rstd[b] * mean);
         if (a.dh) {
-          unpack8<TH>(rd[i], f);
+          settle8<TH>(rd[b][i], c, d);
+          unpack8<TH>(rd[b][i], f);
 #pragma unroll
           for (int e = 0; e < 8; ++e) o[e] += f[e];
         }
-        if (c < d) store8<TH>(static_cast<TH*>(a.dx) + r * a.dx_stride, c, d, pack8<TH>(o));
+        if (c < d) store8<TH>(static_cast<TH*>(a.dx) + row(b) * a.dx_stride, c, d, pack8<TH>(o));
       }
     }
   }
@@ -223,17 +255,15 @@ __global__ __launch_bounds__(kThreads, 2) void norm_bwd_kernel(NormBwdArgs a, fl
   }
 }
 
-// Rows of more than 8192 values: dx with a second read of the row, one
-// workgroup a row ...
-template <typename TH, typename TY>
-__global__ __launch_bounds__(512) void norm_bwd_wide_kernel(NormBwdArgs a) {
-  __shared__ float slot[8];
-  const int64_t r = blockIdx.x, d = a.d;
+// dx of row r by a workgroup, with a second read of the row
+template <typename TH, typename TY, int kThreads>
+__device__ __forceinline__ void dx_row(const NormBwdArgs& a, int64_t r, float* slot) {
+  const int64_t d = a.d;
   const TH* h = static_cast<const TH*>(a.h) + r * a.h_stride;
   const TY* dy = static_cast<const TY*>(a.dy) + r * a.dy_stride;
   const float rstd = a.rstd[r];
   float dot = 0.0f;
-  for (int64_t c = threadIdx.x * 8; c < d; c += 512 * 8) {
+  for (int64_t c = threadIdx.x * 8; c < d; c += kThreads * 8) {
     float f[8], g[8], w[8];
     load8f<TH>(h, c, d, f);
     load8f<TY>(dy, c, d, g);
@@ -241,8 +271,8 @@ __global__ __launch_bounds__(512) void norm_bwd_wide_kernel(NormBwdArgs a) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) dot = fmaf(g[e] * w[e], f[e] * rstd, dot);
   }
-  const float mean = block_sum<512>(dot, slot) / static_cast<float>(d);
-  for (int64_t c = threadIdx.x * 8; c < d; c += 512 * 8) {
+  const float mean = block_sum<kThreads>(dot, slot) / static_cast<float>(d);
+  for (int64_t c = threadIdx.x * 8; c < d; c += kThreads * 8) {
     float f[8], g[8], w[8], o[8];
     load8f<TH>(h, c, d, f);
     load8f<TY>(dy, c, d, g);
@@ -256,6 +286,66 @@ __global__ __launch_bounds__(512) void norm_bwd_wide_kernel(NormBwdArgs a) {
     }
     store8<TH>(static_cast<TH*>(a.dx) + r * a.dx_stride, c, d, pack8<TH>(o));
   }
+}
+
+// Few rows: a workgroup a row for dx, and one for 64 columns of dw, whose 32
+// shares of the rows are joined through LDS.  One launch and no parts, for a
+// second read of dy and h.  (Cold, events around the call: 64 x 878 12.0 us, 14.3
+// with parts; 256 x 512 10.8 and 12.6, x 7168 14.9 and 19.6; 400 x 512 as one
+// launch 14.1, with parts 13.3.)
+template <typename TH, typename TY>
+__global__ __launch_bounds__(256) void norm_bwd_few_kernel(NormBwdArgs a, int dx_rows) {
+  __shared__ float part[32][64];
+  if (static_cast<int>(blockIdx.x) < dx_rows) {
+    dx_row<TH, TY, 256>(a, blockIdx.x, part[0]);
+    return;
+  }
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x - dx_rows) * 64, c = c0 + (threadIdx.x & 7) * 8;
+  const int g = threadIdx.x >> 3;
+  float acc[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
+  if (c < a.d) {
+    constexpr int kAt = 4;   // rows in flight
+    for (int64_t r0 = g; r0 < a.rows; r0 += 32 * kAt) {
+      Raw8<TH> rh[kAt];
+      Raw8<TY> ry[kAt];
+      float rstd[kAt];
+#pragma unroll
+      for (int i = 0; i < kAt; ++i) {
+        const int64_t r = min(r0 + 32 * i, a.rows - 1);
+        rh[i] = load8<TH>(static_cast<const TH*>(a.h) + r * a.h_stride, c, a.d);
+        ry[i] = load8<TY>(static_cast<const TY*>(a.dy) + r * a.dy_stride, c, a.d);
+        rstd[i] = a.rstd[r];
+      }
+#pragma unroll
+      for (int i = 0; i < kAt; ++i) {
+        if (r0 + 32 * i >= a.rows) break;
+        float f[8], y[8];
+        settle8<TH>(rh[i], c, a.d);
+        settle8<TY>(ry[i], c, a.d);
+        unpack8<TH>(rh[i], f);
+        unpack8<TY>(ry[i], y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = fmaf(y[e], f[e] * rstd[i], acc[e]);
+      }
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) part[g][(threadIdx.x & 7) * 8 + e] = acc[e];
+  __syncthreads();
+  if (threadIdx.x >= 64 || c0 + threadIdx.x >= a.d) return;
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) s += part[i][threadIdx.x];
+  a.dw[c0 + threadIdx.x] = s;
+}
+
+// Rows of more than 8192 values: dx a workgroup a row ...
+template <typename TH, typename TY>
+__global__ __launch_bounds__(512) void norm_bwd_wide_kernel(NormBwdArgs a) {
+  __shared__ float slot[8];
+  dx_row<TH, TY, 512>(a, blockIdx.x, slot);
 }
 
 // ... and dw column by column: workgroup (i, j) adds the rows j, j + gridDim.y,
@@ -319,8 +409,10 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+constexpr int64_t kFewRows = 256;
+
 // Workgroups that share the rows, each with a part of dw
-int norm_bwd_parts(int64_t rows, int cus) { return static_cast<int>(std::min<int64_t>(rows, 2 * cus)); }
+int norm_bwd_parts(int64_t rows, int cus) { return rows <= kFewRows ? 0 : static_cast<int>(std::min<int64_t>(rows, 2 * cus)); }
 
 hipError_t launch_norm_bwd(const NormBwdArgs& a, float* part, int cus, hipStream_t s) {
   const int parts = norm_bwd_parts(a.rows, cus);
@@ -329,6 +421,19 @@ hipError_t launch_norm_bwd(const NormBwdArgs& a, float* part, int cus, hipStream
     using TH = decltype(h);
     using TY = decltype(y);
     const dim3 grid(static_cast<unsigned>(parts));
+    if (a.rows <= kFewRows) {
+      const unsigned rows = a.dx ? static_cast<unsigned>(a.rows) : 0, cols = a.dw ? static_cast<unsigned>((a.d + 63) / 64) : 0;
+      auto few = [&](unsigned r, unsigned c) {
+        hipLaunchKernelGGL((norm_bwd_few_kernel<TH, TY>), dim3(r + c), dim3(256), 0, s, a, static_cast<int>(r));
+      };
+      if (rows && cols && a.dx == a.dy) {   // dw first: dx takes dy's place
+        few(0, cols);
+        few(rows, 0);
+      } else {
+        few(rows, cols);
+      }
+      return;
+    }
     // (as in the forward: 4099 x 512 9.8 us, 12.0 by 256 threads; x 2048 14.5 us, 27 with four groups)
     if (a.d <= 512) hipLaunchKernelGGL((norm_bwd_kernel<TH, TY, 64, 1>), grid, dim3(64), 0, s, a, pw);
     else if (a.d <= 2048) hipLaunchKernelGGL((norm_bwd_kernel<TH, TY, 256, 1>), grid, dim3(256), 0, s, a, pw);
@@ -343,7 +448,7 @@ hipError_t launch_norm_bwd(const NormBwdArgs& a, float* part, int cus, hipStream
   };
   auto with_y = [&](auto h) { a.dy_bf16 ? go(h, bf16_t{}) : go(h, 0.0f); };
   if (a.rows > 0) a.h_bf16 ? with_y(bf16_t{}) : with_y(0.0f);
-  if (a.dw)
+  if (a.dw && (parts > 0 || a.rows == 0))
     hipLaunchKernelGGL(norm_dweight_sum_kernel, dim3(static_cast<unsigned>((a.d + 31) / 32)), dim3(1024), 0, s, part, parts, a.d, a.dw);
   return hipGetLastError();
 }

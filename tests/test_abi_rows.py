@@ -70,9 +70,9 @@ def test_norm_backward_refusals(L, kw, status):
 def test_norm_backward_workspace(L):
     need = ctypes.c_int64()
     query = L.stq_rmsnorm_rows_backward_workspace
-    assert query(4, 100, 1, 256, ctypes.byref(need)) == 0 and need.value == 4 * 100 * 4
+    assert query(300, 100, 1, 256, ctypes.byref(need)) == 0 and need.value == 300 * 100 * 4
     assert query(5000, 7168, 1, 256, ctypes.byref(need)) == 0 and need.value == 512 * 7168 * 4
-    for args in [(4, 100, 0), (0, 100, 1)]:
+    for args in [(4, 100, 0), (0, 100, 1), (256, 100, 1), (300, 100, 0)]:
         assert query(*args, 256, ctypes.byref(need)) == 0 and need.value == 0
     assert query(4, 0, 1, 256, ctypes.byref(need)) == 2
     assert query(4, 100, 1, -1, ctypes.byref(need)) == 1

@@ -181,7 +181,7 @@ def _bwd_check(got, args):
 
 @pytest.mark.parametrize("ht", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("yt", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("n, d", SHAPES + [(1030, 300), (2000, 2000)])
+@pytest.mark.parametrize("n, d", SHAPES + [(1030, 300), (2000, 2000), (256, 700), (257, 700), (270, 8200), (260, 9001)])
 def test_backward(stq, n, d, ht, yt):
     for joined in (False, True):
         args = _bwd_inputs(n, d, ht, yt, joined, n + 3 * d)
@@ -189,9 +189,10 @@ def test_backward(stq, n, d, ht, yt):
         _bwd_check(stq.rmsnorm_rows_backward(h, w, rstd, dy, dh), args)
 
 
+@pytest.mark.parametrize("n", [40, 300])
 @pytest.mark.parametrize("d", [200, 4096, 9001])
-def test_backward_one_output_and_in_place(stq, d):
-    args = _bwd_inputs(40, d, torch.float32, torch.float32, True, d)
+def test_backward_one_output_and_in_place(stq, n, d):
+    args = _bwd_inputs(n, d, torch.float32, torch.float32, True, d)
     h, w, rstd, dy, dh = (t.cuda() for t in args)
     both = stq.rmsnorm_rows_backward(h, w, rstd, dy, dh)
     dx, none = stq.rmsnorm_rows_backward(h, w, rstd, dy, dh, need_dweight=False)
@@ -296,4 +297,5 @@ def test_binding_refusals(stq):
     with pytest.raises(ValueError, match="need_dx"):
         stq.rmsnorm_rows_backward(x, w, r, x, need_dx=False, dx=x)
     with pytest.raises(stq.StqError, match="workspace"):
-        stq.rmsnorm_rows_backward(x, w, r, x, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
+        many = x.repeat(150, 1)
+        stq.rmsnorm_rows_backward(many, w, r.repeat(150), many, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
