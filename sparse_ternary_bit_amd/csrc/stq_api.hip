@@ -1024,7 +1024,8 @@ stq_status stq_head_cross_entropy_backward_workspace(int x_dtype, int64_t n_rows
   if (st != STQ_OK) return st;
   if (want_dw && x_dtype == STQ_X_I8) return fail(STQ_E_ARG, "%s: 8-bit weights have no gradient", who);
   if (n_rows > 0 && (want_dx || want_dw))
-    *workspace_bytes = stq::plan_head_bwd(x_dtype == STQ_X_I8, n_rows, vocab, k, want_dx != 0, want_dw != 0, n_cus > 0 ? n_cus : stq::cus_of_current_device()).bytes;
+    *workspace_bytes = stq::plan_head_bwd(x_dtype == STQ_X_I8, n_rows, vocab, k, want_dx != 0, want_dw != 0,
+                                          n_cus > 0 ? n_cus : stq::cus_of_current_device()).bytes;
   return ok();
 }
 
