@@ -206,6 +206,16 @@ def test_backward_one_output_and_in_place(stq, n, d):
     assert torch.equal(dy, both[0]) and torch.equal(dw, both[1])
 
 
+@pytest.mark.parametrize("d", list(range(8, 26)) + list(range(1200, 1208)))
+def test_every_end_of_a_row(stq, d):
+    for xt, rt in ((torch.float32, torch.bfloat16), (torch.bfloat16, torch.float32)):
+        x, r, w = _inputs(6, d, xt, rt, d)
+        _check(stq.rmsnorm_rows(x.cuda(), w.cuda(), EPS, r.cuda(), need_y=True), x, r, w)
+        for n in (6, 270):
+            args = _bwd_inputs(n, d, xt, rt, True, d)
+            _bwd_check(stq.rmsnorm_rows_backward(*(t.cuda() for t in args)), args)
+
+
 def test_gradient_against_differences(stq):
     # the loss is a fixed weighting c of y; central differences of the 64-bit norm, whose error is of the
     # order of step^2 and far below the bound

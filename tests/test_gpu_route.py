@@ -336,6 +336,26 @@ def test_combine_gradients(stq, n, k, d, yt, zt, dt):
     assert none is None and torch.equal(dw, got[1])
 
 
+@pytest.mark.parametrize("d", list(range(8, 26)) + list(range(1200, 1208)))
+def test_combine_every_end_of_a_row(stq, d):
+    n, k = 9, 3
+    row, w = _pairs(n, k, 2, 4, d)
+    on = row >= 0
+    for zt, yt in ((torch.float32, torch.bfloat16), (torch.bfloat16, torch.float32)):
+        g = torch.Generator().manual_seed(d)
+        z, dy = torch.randn((n * k + 2, d), generator=g).to(zt), torch.randn((n, d), generator=g).to(yt)
+        want, tol = _combine_ref(z, row, w, k, yt)
+        assert bool(((stq.combine_rows(z.cuda(), row.cuda(), k, w.cuda(), out_dtype=yt).cpu().double() - want).abs() <= tol).all())
+        dz, dw = stq.combine_rows_backward(dy.cuda(), row.cuda(), k, z.cuda(), w.cuda(), dz_dtype=torch.float32)
+        share = dy.double().repeat_interleave(k, 0)
+        want = share[on] * w.double()[on, None]
+        assert bool(((dz.cpu().double()[row[on].long()] - want).abs() <= U * want.abs() + TINY).all())
+        terms = torch.zeros(n * k, d, dtype=torch.float64)
+        terms[on] = share[on] * z.double()[row[on].long()]
+        tol = (8 * -(-d // 512) + 24) * U * terms.abs().sum(1) + TINY
+        assert bool(((dw.cpu().double() - terms.sum(1)).abs() <= tol).all())
+
+
 def test_combine_strides_and_offsets(stq):
     n, k, d = 20, 4, 300
     row, w = (t.cuda() for t in _pairs(n, k, 0, 5, 1))
