@@ -497,15 +497,11 @@ __global__ __launch_bounds__(kThreads) void route_bwd_kernel(RouteBwdArgs a) {
       }
     }
     dot = sum16(dot);
-    if (!valid) {
-      __syncthreads();
-      continue;
-    }
     T* out = static_cast<T*>(a.d_logits) + t * a.d_stride;
 #pragma unroll
     for (int q = 0; q < kN / 4; ++q) {
       const int c = column(lane16, 4 * q);
-      if (c >= E) continue;
+      if (!valid || c >= E) continue;
       const f32x4_t ch = *reinterpret_cast<const f32x4_t*>(&chosen[tl][c]);
       float d[4];
 #pragma unroll
@@ -522,6 +518,7 @@ __global__ __launch_bounds__(kThreads) void route_bwd_kernel(RouteBwdArgs a) {
           if (c + i < E) out[c + i] = narrow<T>(d[i]);
       }
     }
+    // (lanes of tokens past the end come here too: a wavefront may hold both)
     __syncthreads();
   }
 }

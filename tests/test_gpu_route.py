@@ -234,6 +234,20 @@ def test_gradient(stq, n, e, k, pads, renorm, dtype):
     assert torch.equal(stq.route_tokens_backward(xc, got.pair_expert, got.counts, k, renorm, g.cuda(), None, b, out=xc), d)
 
 
+# wavefronts of four tokens of which the last few are missing, and more tokens than the workgroups of a launch take at once
+@pytest.mark.parametrize("n, e, k", [(n, 20, 3) for n in list(range(1, 20)) + [31, 33]] + [(131100, 6, 2), (131083, 5, 1)])
+def test_gradient_of_every_number_of_tokens(stq, n, e, k):
+    x = _logits(n, e, torch.float32, n, n // 7)
+    r = _ref(x, k, True)
+    got = stq.route_tokens(x.cuda(), k)
+    g = torch.randn(n * k, generator=torch.Generator().manual_seed(n))
+    b = torch.full((1,), 0.5, device="cuda")
+    want, tol = _bwd_ref(x, k, True, r, g.double().view(n, k), 0.5)
+    wide = torch.full((n + 1, e), 7.0, device="cuda")
+    d = stq.route_tokens_backward(x.cuda(), got.pair_expert, got.counts, k, grad_weight=g.cuda(), grad_balance=b, out=wide[:n])
+    assert bool(((d.cpu().double() - want).abs() <= tol).all()) and bool((wide[n] == 7).all())
+
+
 @pytest.mark.parametrize("renorm", [True, False])
 def test_gradient_against_differences(stq, renorm):
     # differences of the 64-bit weights and balance with the choice and the counts held, the step far from any tie
