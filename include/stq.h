@@ -693,8 +693,9 @@ stq_status stq_head_cross_entropy_workspace(int x_dtype, int64_t n_rows, int64_t
  *   workspace, workspace_bytes  at least what
  *              stq_head_cross_entropy_backward_workspace reports
  * The other arguments and limits are as above.  A row that is left out, whose
- * target lies past the vocabulary or whose lse is -inf has no gradient, whatever
- * x holds there; one with lse NaN gives NaN.  dl is formed in fp32 and rounded to
+ * target lies past the vocabulary or whose lse is -inf has no gradient: its dx is
+ * 0 and it adds nothing to dw, whatever x and w hold; another whose lse is NaN gives
+ * NaN.  dl is formed in fp32 and rounded to
  * bf16 for the two products (with 8-bit rows after its w_scale, so that the
  * integers, which bf16 holds exactly, enter as they are): dx and dw err by about
  * 0.0017 of their norm from that and as much from their own rounding.  Sums are

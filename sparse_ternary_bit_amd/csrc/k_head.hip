@@ -131,6 +131,11 @@ struct Mfma<false> {
   }
 };
 
+// A row without a gradient: left out, its target past the vocabulary, or every logit -inf
+__device__ __forceinline__ bool no_gradient(int64_t target, int64_t vocab, float lse) {
+  return target < 0 || target >= vocab || lse == -INFINITY;
+}
+
 __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
 // Rows of bf16 that a wavefront holds as products, on their way to memory: 32
@@ -302,8 +307,7 @@ __device__ __forceinline__ void finish(const NtArgs& a, typename Mfma<kI8>::acc_
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
       take(j);
-      // no gradient: an ignored row, one without a distribution, a target past the vocabulary
-      const bool dead = target[j] < 0 || target[j] >= a.vocab || lse[j] == -INFINITY;
+      const bool dead = no_gradient(target[j], a.vocab, lse[j]);
       const float gj = dead ? 0.0f : g[j];
       const int64_t want = target[j] - a.v0 - n0 - 8 * q;
       const bool hot = __any(want >= 0 && want < kC);
@@ -530,8 +534,11 @@ __device__ __forceinline__ void finish_across(const NtArgs& a, f32x4_t (&acc)[FN
     for (int i = 0; i < FN; ++i) v[i] = acc[i][j];
     float* const row = a.acc + (split * a.m + tok) * a.ld_acc + n0 + 4 * q;
     if (a.out) {   // whole rows, through LDS
+      // (zeros under an infinite head too, where dl = 0 gives NaN)
+      const bool dead = tok < a.m && no_gradient(a.targets[tok], a.vocab, a.lse[tok]);
 #pragma unroll
       for (int i = 0; i < FN; ++i) {
+        if (dead) v[i] = f32x4_t{0, 0, 0, 0};
         const int c = 16 * i + 4 * q;
         const uint32_t o[4] = {bf16_round(v[i][0]), bf16_round(v[i][1]), bf16_round(v[i][2]), bf16_round(v[i][3])};
         *reinterpret_cast<u32x2_t*>(sl.at(16 * (j & 1) + r, 2 * i + (q >> 1)) + (q & 1) * 8) = u32x2_t{o[0] | o[1] << 16, o[2] | o[3] << 16};
@@ -915,7 +922,7 @@ __global__ __launch_bounds__(kFewWaves * 64, 2) void nt_few_kernel(NtArgs a) {
     if (q == 0 && on) a.stats[static_cast<int64_t>(blockIdx.x) * a.m + r] = float2{m, s};
   } else {
     const float lse = on ? a.lse[r] : 0.0f;
-    const bool dead = target < 0 || target >= a.vocab || lse == -INFINITY;
+    const bool dead = no_gradient(target, a.vocab, lse);
     const float g = dead ? 0.0f : a.g[r];
     uint32_t d[4];
 #pragma unroll
@@ -1121,9 +1128,10 @@ __global__ __launch_bounds__(1024) void head_join_kernel(const float2* stats, co
 }
 
 // out[c][r] = in[r][c] for r < n (zeros for r = n .. n_pad - 1 and for rows
-// whose target is ignored), c < k; 64 x 64 a workgroup.
+// without a gradient, whatever they hold), c < k; 64 x 64 a workgroup.
 __global__ __launch_bounds__(256) void transpose_kernel(const char* in, int64_t ld, int64_t n, int64_t k, const int32_t* targets,
-                                                        uint16_t* out, int64_t ld_out, int64_t n_pad) {
+                                                        const float* lse, int64_t vocab, uint16_t* out, int64_t ld_out,
+                                                        int64_t n_pad) {
   __shared__ uint16_t tile[64][66];
   const int64_t r0 = static_cast<int64_t>(blockIdx.x) * 64, c0 = static_cast<int64_t>(blockIdx.y) * 64;
   const int row = threadIdx.x >> 3, c = (threadIdx.x & 7) * 8;
@@ -1133,7 +1141,7 @@ __global__ __launch_bounds__(256) void transpose_kernel(const char* in, int64_t 
     uint16_t v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = 0;
-    if (rr < n && c0 + c < k && !(targets && targets[rr] < 0)) {
+    if (rr < n && c0 + c < k && !no_gradient(targets[rr], vocab, lse[rr])) {
       // a row owns its bytes up to the next multiple of 16
       const u32x4_t w = *reinterpret_cast<const u32x4_t*>(in + rr * ld + (c0 + c) * 2);
 #pragma unroll
@@ -1157,7 +1165,8 @@ __global__ __launch_bounds__(256) void transpose_kernel(const char* in, int64_t 
 // The parts of a split sum, rounded to bf16: four columns a thread, every
 // fourth part a wavefront.  (9 parts of 256 x 7168: 46 us a column a thread.)
 __global__ __launch_bounds__(256) void join_splits_kernel(const float* acc, int64_t ld_acc, int splits, int64_t m, int64_t n,
-                                                          uint16_t* out, int64_t ld_out) {
+                                                          const int32_t* targets, const float* lse, int64_t vocab, uint16_t* out,
+                                                          int64_t ld_out) {
   __shared__ f32x4_t part[4][64];
   const int lane = threadIdx.x & 63, g = threadIdx.x >> 6;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 64 + lane, quads = ld_acc / 4;
@@ -1183,11 +1192,12 @@ __global__ __launch_bounds__(256) void join_splits_kernel(const float* acc, int6
   part[g][lane] = s;
   __syncthreads();
   if (g || !on) return;
+  const bool dead = no_gradient(targets[row], vocab, lse[row]);   // (as in finish_across)
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (c + e < n)
-      out[row * ld_out + c + e] = static_cast<uint16_t>(
-          bf16_round((part[0][lane][e] + part[1][lane][e]) + (part[2][lane][e] + part[3][lane][e])));
+  for (int e = 0; e < 4; ++e) {
+    const float v = (part[0][lane][e] + part[1][lane][e]) + (part[2][lane][e] + part[3][lane][e]);
+    if (c + e < n) out[row * ld_out + c + e] = static_cast<uint16_t>(dead ? 0u : bf16_round(v));
+  }
 }
 
 __global__ __launch_bounds__(256) void zero_rows_kernel(uint16_t* out, int64_t ld, int64_t m, int64_t n) {
@@ -1376,7 +1386,8 @@ hipError_t launch_head_bwd(const HeadArgs& h, const HeadBwdArgs& b, const HeadBw
   const int64_t m_pad = up(h.rows, 64);
   if (b.dw)
     hipLaunchKernelGGL(transpose_kernel, dim3(static_cast<unsigned>(m_pad / 64), static_cast<unsigned>((h.k + 63) / 64)), dim3(256),
-                       0, s, static_cast<const char*>(h.x), h.ldx, h.rows, h.k, h.targets, xt, m_pad, m_pad);
+                       0, s, static_cast<const char*>(h.x), h.ldx, h.rows, h.k, h.targets, b.lse, h.vocab, xt, m_pad,
+                       m_pad);
   for (int64_t i = 0; i < p.pieces; ++i) {
     const int64_t v0 = i * p.width, n = std::min(p.width, h.vocab - v0), n_pad = up(n, 64);
     NtArgs a = logits_args(h);
@@ -1415,6 +1426,9 @@ hipError_t launch_head_bwd(const HeadArgs& h, const HeadBwdArgs& b, const HeadBw
       const bool last = p.splits == 1 && i + 1 == p.pieces;
       d.out = last ? b.dx : nullptr;
       d.ld_out = b.ld_dx;
+      d.targets = h.targets;
+      d.lse = b.lse;
+      d.vocab = h.vocab;
       d.w = a.w;
       d.ldw = h.ldw;
       d.words = n;
@@ -1439,7 +1453,7 @@ hipError_t launch_head_bwd(const HeadArgs& h, const HeadBwdArgs& b, const HeadBw
   }
   if (b.dx && (p.few || p.splits > 1))
     hipLaunchKernelGGL(join_splits_kernel, dim3(static_cast<unsigned>((h.rows * (up(h.k, 8) / 4) + 63) / 64)), dim3(256), 0, s, acc,
-                       up(h.k, 8), p.splits, h.rows, h.k, b.dx, b.ld_dx);
+                       up(h.k, 8), p.splits, h.rows, h.k, h.targets, b.lse, h.vocab, b.dx, b.ld_dx);
   return hipGetLastError();
 }
 

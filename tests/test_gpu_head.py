@@ -212,6 +212,52 @@ def test_targets_past_the_vocabulary(stq):
     assert torch.equal(dx, want[0]) and torch.equal(dw, want[1])
 
 
+# tiles of 16, 64, 128 and 256; dx joined from parts of the sum, and written by the tiles themselves
+@pytest.mark.parametrize("n, v, k", [(12, 500, 72), (66, 1000, 64), (300, 700, 129), (600, 250, 701), (513, 9000, 96)])
+def test_rows_without_a_gradient_may_hold_anything(stq, n, v, k):
+    c = Case(n, v, k, False, n, ignored=0.1)
+    c.targets[[1, 2, 4, 7, 9]] = torch.tensor([v, 2 ** 31 - 1, v + 1, 3, 5], dtype=torch.int32, device="cuda")
+    c.x[1, 3], c.x[2, 5], c.x[4] = float("nan"), float("inf"), -float("inf")
+    # a row whose logits are all -inf, under a head with one column above zero
+    c.w[:, 1] = c.w[:, 1].abs() + 0.125
+    c.x[7] = 0
+    c.x[7, 1] = -float("inf")
+    loss, lse = stq.head_cross_entropy(c.x, c.w, c.targets)
+    assert bool(torch.isneginf(lse[7])) and bool(torch.isnan(loss[[1, 2, 4, 7]]).all())
+    dx, dw = stq.head_cross_entropy_backward(c.x, c.w, c.targets, lse, c.grad)
+    assert not dx[[1, 2, 4, 7]].any() and bool(torch.isfinite(dx).all()) and bool(torch.isfinite(dw).all())
+    c.targets[[1, 2, 4, 7]] = -1
+    c.x[[1, 2, 4, 7]] = 1.0
+    want = stq.head_cross_entropy_backward(c.x, c.w, c.targets, lse, c.grad)
+    assert torch.equal(dx, want[0]) and torch.equal(dw, want[1])
+    c.check_backward(dx, dw, torch.where(c.targets < 0, 0.0, lse))
+
+
+@pytest.mark.parametrize("n, v, k", [(12, 500, 72), (66, 1000, 64), (600, 250, 701)])
+def test_rows_under_a_head_of_minus_infinity(stq, n, v, k):
+    c = Case(n, v, k, False, n, ignored=0.1)
+    c.x.abs_()
+    c.w[:] = -float("inf")
+    _, lse = stq.head_cross_entropy(c.x, c.w, c.targets)
+    assert bool(torch.isneginf(lse).all())
+    dx, dw = stq.head_cross_entropy_backward(c.x, c.w, c.targets, lse, c.grad)
+    assert not dx.any() and not dw.any()
+
+
+@pytest.mark.parametrize("n, v, k", [(12, 500, 72), (66, 1000, 64), (600, 250, 701)])
+def test_8_bit_rows_without_a_gradient(stq, n, v, k):
+    c = Case(n, v, k, True, n, ignored=0.1)
+    c.targets[[1, 2]] = torch.tensor([v, 2 ** 31 - 1], dtype=torch.int32, device="cuda")
+    c.x_scale[[1, 2]] = torch.tensor([float("nan"), float("inf")], device="cuda")
+    _, lse = stq.head_cross_entropy(c.x, c.w, c.targets, **c.args())
+    dx, _ = stq.head_cross_entropy_backward(c.x, c.w, c.targets, lse, c.grad, need_dw=False, **c.args())
+    assert not dx[[1, 2]].any() and bool(torch.isfinite(dx).all())
+    c.targets[[1, 2]] = -1
+    c.x_scale[[1, 2]] = 1.0
+    want = stq.head_cross_entropy_backward(c.x, c.w, c.targets, lse, c.grad, need_dw=False, **c.args())
+    assert torch.equal(dx, want[0])
+
+
 @pytest.mark.parametrize("v", [300, 20000])
 def test_rows_that_are_not_finite(stq, v):
     c = Case(50, v, 64, False, 6, ignored=0.0)
