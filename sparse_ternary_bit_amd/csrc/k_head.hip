@@ -17,7 +17,9 @@
 //
 // Sums are in fp32 (8-bit operands': exact, in int32), statistics in fp32.  dl
 // is rounded to bf16 once, half a step of 2^-8 relative to each of its values,
-// because the matrix cores take dx's and dW's factors in it.
+// because the matrix cores take dx's and dW's factors in it.  The many small
+// terms' roundings average out in dx; the target's is as large as all the others
+// together, so what its rounding leaves is kept in fp32 and enters dx at the end.
 //
 // 4096 rows under 131072 x 7168 in bf16: 5.2 to 5.3 ms, 1.46 PFLOP/s (a large
 // library product 1.56); matrix cores 75 % busy at 1.8 of 2.4 GHz, so the card's
@@ -68,9 +70,11 @@ struct NtArgs {
   int64_t vocab;          // the whole vocabulary
   uint16_t* dl;           // [m][ld_dl], zeros in channels n .. n_pad - 1
   int64_t ld_dl;
+  float* rest;            // [m]: what the rounding of the target's dl leaves
   uint16_t* dlt;          // [n][ld_dlt], zeros in tokens m .. m_pad - 1; may be NULL
   int64_t ld_dlt;
   int64_t n_pad, m_pad;
+  const char* head;       // (dx) the whole head, for the targets' rows
   // kSum
   uint16_t* out;          // bf16 [m][ld_out]
   int64_t ld_out;
@@ -134,6 +138,12 @@ struct Mfma<false> {
 // A row without a gradient: left out, its target past the vocabulary, or every logit -inf
 __device__ __forceinline__ bool no_gradient(int64_t target, int64_t vocab, float lse) {
   return target < 0 || target >= vocab || lse == -INFINITY;
+}
+
+// What the rounding of d to the bf16 `bits` leaves (nothing, if that is infinite or no number)
+__device__ __forceinline__ float rounding_rest(float d, uint32_t bits) {
+  const float f = __builtin_bit_cast(float, bits << 16);
+  return fabsf(f) < INFINITY ? d - f : 0.0f;
 }
 
 __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
@@ -331,7 +341,14 @@ __device__ __forceinline__ void finish(const NtArgs& a, typename Mfma<kI8>::acc_
           for (int e = 0; e < 8; ++e)
             if (32 * p + 8 * q + e >= nv) d[e] = 0.0f;
         }
-        *reinterpret_cast<u32x4_t*>(sl.at(16 * (j & 1) + r, 4 * p + q)) = pack8<bf16_t>(d).w[0];
+        const u32x4_t o = pack8<bf16_t>(d).w[0];
+        *reinterpret_cast<u32x4_t*>(sl.at(16 * (j & 1) + r, 4 * p + q)) = o;
+        if (hot && !dead) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (want == 32 * p + e && want + 8 * q < nv)
+              a.rest[m0 + 16 * j + r] = rounding_rest(d[e], (o[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
+        }
       }
       if ((j & 1) || j + 1 == FM) {
         sl.fence();
@@ -513,9 +530,21 @@ __global__ __launch_bounds__(WM * WN * 64, kWavesPerSimd) void nt_kernel(NtArgs 
 // that become bf16, which holds them exactly).
 enum Lies { kRows, kAcross16, kAcross8 };
 
+// Columns c .. c + 3 (c a multiple of 4) of a row of the head, as they lie, and their values
+template <bool k8>
+__device__ __forceinline__ u32x2_t head4(const char* row, int64_t c) {
+  if constexpr (k8) return u32x2_t{*reinterpret_cast<const uint32_t*>(row + c), 0};
+  else return *reinterpret_cast<const u32x2_t*>(row + 2 * c);
+}
+template <bool k8>
+__device__ __forceinline__ float head_value(u32x2_t v, int e) {
+  if constexpr (k8) return static_cast<float>(static_cast<int8_t>(v[0] >> (8 * e)));
+  else return __builtin_bit_cast(float, (e & 1) ? (v[e >> 1] & 0xFFFF0000u) : (v[e >> 1] << 16));
+}
+
 // 16 channels of one row of tiles of a wavefront that read its operand across:
 // lane (q, r) holds token 16 j + r, channels 16 i + 4 q + 0..3.  Sums only.
-template <int FM, int FN>
+template <int kLies, int FM, int FN>
 __device__ __forceinline__ void finish_across(const NtArgs& a, f32x4_t (&acc)[FN][FM], int64_t m0, int64_t n0, int nv, int split, char* slab) {
   constexpr int kC = FN * 16;
   int lane = threadIdx.x & 63;
@@ -535,10 +564,22 @@ __device__ __forceinline__ void finish_across(const NtArgs& a, f32x4_t (&acc)[FN
     float* const row = a.acc + (split * a.m + tok) * a.ld_acc + n0 + 4 * q;
     if (a.out) {   // whole rows, through LDS
       // (zeros under an infinite head too, where dl = 0 gives NaN)
-      const bool dead = tok < a.m && no_gradient(a.targets[tok], a.vocab, a.lse[tok]);
+      const int64_t target = tok < a.m ? a.targets[tok] : -1;
+      const bool dead = tok >= a.m || no_gradient(target, a.vocab, a.lse[tok]);
+      const float rest = dead ? 0.0f : a.rest[tok];
+      u32x4_t hot[FN / 2];
 #pragma unroll
       for (int i = 0; i < FN; ++i) {
-        if (dead) v[i] = f32x4_t{0, 0, 0, 0};
+        const bool on = !dead && 16 * i + 4 * q < nv;
+        const u32x2_t o = on ? head4<kLies == kAcross8>(a.head + target * a.ldw, n0 + 16 * i + 4 * q) : u32x2_t{0, 0};
+        hot[i / 2][2 * (i % 2)] = o[0];
+        hot[i / 2][2 * (i % 2) + 1] = o[1];
+      }
+#pragma unroll
+      for (int i = 0; i < FN; ++i) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          v[i][e] = dead ? 0.0f : fmaf(rest, head_value<kLies == kAcross8>(u32x2_t{hot[i / 2][2 * (i % 2)], hot[i / 2][2 * (i % 2) + 1]}, e), v[i][e]);
         const int c = 16 * i + 4 * q;
         const uint32_t o[4] = {bf16_round(v[i][0]), bf16_round(v[i][1]), bf16_round(v[i][2]), bf16_round(v[i][3])};
         *reinterpret_cast<u32x2_t*>(sl.at(16 * (j & 1) + r, 2 * i + (q >> 1)) + (q & 1) * 8) = u32x2_t{o[0] | o[1] << 16, o[2] | o[3] << 16};
@@ -822,7 +863,7 @@ __global__ __launch_bounds__(256, 1) void nt_wide_kernel(NtArgs a) {
     // (the next tile's stages lie in the first two buffers of either operand)
     const int nv = static_cast<int>(min(static_cast<int64_t>(T), a.n - done.n0)) - wn * 128;
     char* const slab = sw[2] + wave * (kSlabs / 4);
-    if constexpr (kAcross) finish_across<F, F>(a, acc, done.m0 + wm * 128, done.n0 + wn * 128, nv, done.split, slab);
+    if constexpr (kAcross) finish_across<kLies, F, F>(a, acc, done.m0 + wm * 128, done.n0 + wn * 128, nv, done.split, slab);
     else finish<kI8, kEpi, F, F, true>(a, acc, done.m0 + wm * 128, done.n0 + wn * 128, nv, done.tile_n * 2 + wn, slab);
     if (!more) return;
   }
@@ -931,6 +972,7 @@ __global__ __launch_bounds__(kFewWaves * 64, 2) void nt_few_kernel(NtArgs a) {
       v *= g;
       if (kI8) v *= scale[e];
       d[e] = bf16_round(dead || 4 * q + e >= nv ? 0.0f : v);
+      if (!dead && want == e && 4 * q + e < nv) a.rest[r] = rounding_rest(v, d[e]);
     }
     if (on) *reinterpret_cast<u32x2_t*>(a.dl + r * a.ld_dl + n0 + 4 * q) = u32x2_t{d[0] | d[1] << 16, d[2] | d[3] << 16};
     if (a.dlt) {
@@ -1162,41 +1204,59 @@ __global__ __launch_bounds__(256) void transpose_kernel(const char* in, int64_t 
   }
 }
 
-// The parts of a split sum, rounded to bf16: four columns a thread, every
-// fourth part a wavefront.  (9 parts of 256 x 7168: 46 us a column a thread.)
-__global__ __launch_bounds__(256) void join_splits_kernel(const float* acc, int64_t ld_acc, int splits, int64_t m, int64_t n,
-                                                          const int32_t* targets, const float* lse, int64_t vocab, uint16_t* out,
-                                                          int64_t ld_out) {
+struct JoinArgs {
+  const float* acc;       // [splits][m][ld_acc]
+  int64_t ld_acc;
+  int splits;
+  int64_t m, n, vocab;
+  const int32_t* targets;
+  const float* lse;
+  const float* rest;
+  const char* head;
+  int64_t ldw;            // bytes
+  uint16_t* out;
+  int64_t ld_out;
+};
+
+// The parts of dx's sum and its targets' rest, rounded to bf16: four columns a
+// thread, every fourth part a wavefront.  (9 parts of 256 x 7168: 46 us a column
+// a thread.)
+template <bool k8>
+__global__ __launch_bounds__(256) void join_splits_kernel(JoinArgs a) {
   __shared__ f32x4_t part[4][64];
   const int lane = threadIdx.x & 63, g = threadIdx.x >> 6;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 64 + lane, quads = ld_acc / 4;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 64 + lane, quads = a.ld_acc / 4;
   const int64_t row = i / quads, c = (i - row * quads) * 4;
-  const bool on = row < m;
+  const bool on = row < a.m;
   f32x4_t s = {0, 0, 0, 0};
   auto add = [&](const f32x4_t& v) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) s[e] += v[e];
   };
+  const int64_t target = on && g == 0 ? a.targets[row] : -1;
+  // (zeros as in finish_across)
+  const bool dead = target < 0 || no_gradient(target, a.vocab, a.lse[row]);
+  const float rest = dead ? 0.0f : a.rest[row];
+  const u32x2_t hot = dead || c >= a.n ? u32x2_t{0, 0} : head4<k8>(a.head + target * a.ldw, c);
   if (on) {
-    const float* const at = acc + row * ld_acc + c;
+    const float* const at = a.acc + row * a.ld_acc + c;
     int p = g;
-    for (; p + 12 < splits; p += 16) {
+    for (; p + 12 < a.splits; p += 16) {
       f32x4_t v[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = *reinterpret_cast<const f32x4_t*>(at + (p + 4 * e) * m * ld_acc);
+      for (int e = 0; e < 4; ++e) v[e] = *reinterpret_cast<const f32x4_t*>(at + (p + 4 * e) * a.m * a.ld_acc);
 #pragma unroll
       for (int e = 0; e < 4; ++e) add(v[e]);
     }
-    for (; p < splits; p += 4) add(*reinterpret_cast<const f32x4_t*>(at + p * m * ld_acc));
+    for (; p < a.splits; p += 4) add(*reinterpret_cast<const f32x4_t*>(at + p * a.m * a.ld_acc));
   }
   part[g][lane] = s;
   __syncthreads();
   if (g || !on) return;
-  const bool dead = no_gradient(targets[row], vocab, lse[row]);   // (as in finish_across)
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const float v = (part[0][lane][e] + part[1][lane][e]) + (part[2][lane][e] + part[3][lane][e]);
-    if (c + e < n) out[row * ld_out + c + e] = static_cast<uint16_t>(dead ? 0u : bf16_round(v));
+    const float v = fmaf(rest, head_value<k8>(hot, e), (part[0][lane][e] + part[1][lane][e]) + (part[2][lane][e] + part[3][lane][e]));
+    if (c + e < a.n) a.out[row * a.ld_out + c + e] = static_cast<uint16_t>(dead ? 0u : bf16_round(v));
   }
 }
 
@@ -1350,7 +1410,8 @@ HeadBwdPlan plan_head_bwd(bool i8, int64_t rows, int64_t vocab, int64_t k, bool 
     p.per = static_cast<int>((stages + want - 1) / want);
     p.splits = static_cast<int>((stages + p.per - 1) / p.per);
     if (dx) at += up(p.splits * rows * up(k, 8) * 4, 256);
-    p.bytes = at;
+    p.rest = at;
+    p.bytes = at + up(rows * 4, 256);
     return p;
   }
   // pieces of the vocabulary whose dl (and its transpose) stay in the last-level cache
@@ -1373,13 +1434,15 @@ HeadBwdPlan plan_head_bwd(bool i8, int64_t rows, int64_t vocab, int64_t k, bool 
   p.acc = at;
   p.splits = dx ? dx_splits(rows, k, std::min(p.width, up(vocab, 64)) / 64, p.pieces, cus) : 1;
   if (dx && (p.pieces > 1 || p.splits > 1)) at += up(p.splits * rows * up(k, 8) * 4, 256);
-  p.bytes = at;
+  p.rest = at;
+  p.bytes = at + up(rows * 4, 256);
   return p;
 }
 
 hipError_t launch_head_bwd(const HeadArgs& h, const HeadBwdArgs& b, const HeadBwdPlan& p, void* ws, int cus, hipStream_t s) {
   char* base = static_cast<char*>(ws);
   uint16_t* dl = reinterpret_cast<uint16_t*>(base);
+  float* rest = reinterpret_cast<float*>(base + p.rest);
   uint16_t* dlt = reinterpret_cast<uint16_t*>(base + p.dlt);
   uint16_t* xt = reinterpret_cast<uint16_t*>(base + p.xt);
   float* acc = p.few || p.pieces > 1 || p.splits > 1 ? reinterpret_cast<float*>(base + p.acc) : nullptr;
@@ -1399,6 +1462,7 @@ hipError_t launch_head_bwd(const HeadArgs& h, const HeadBwdArgs& b, const HeadBw
     a.g = b.g;
     a.dl = dl;
     a.ld_dl = p.width;
+    a.rest = rest;
     a.dlt = b.dw ? dlt : nullptr;
     a.ld_dlt = m_pad;
     a.vocab = h.vocab;
@@ -1429,6 +1493,8 @@ hipError_t launch_head_bwd(const HeadArgs& h, const HeadBwdArgs& b, const HeadBw
       d.targets = h.targets;
       d.lse = b.lse;
       d.vocab = h.vocab;
+      d.rest = rest;
+      d.head = static_cast<const char*>(h.w);
       d.w = a.w;
       d.ldw = h.ldw;
       d.words = n;
@@ -1451,9 +1517,12 @@ hipError_t launch_head_bwd(const HeadArgs& h, const HeadBwdArgs& b, const HeadBw
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (b.dx && (p.few || p.splits > 1))
-    hipLaunchKernelGGL(join_splits_kernel, dim3(static_cast<unsigned>((h.rows * (up(h.k, 8) / 4) + 63) / 64)), dim3(256), 0, s, acc,
-                       up(h.k, 8), p.splits, h.rows, h.k, h.targets, b.lse, h.vocab, b.dx, b.ld_dx);
+  if (b.dx && (p.few || p.splits > 1)) {
+    const JoinArgs j{acc, up(h.k, 8), p.splits, h.rows, h.k, h.vocab, h.targets, b.lse, rest, static_cast<const char*>(h.w), h.ldw, b.dx, b.ld_dx};
+    const dim3 grid(static_cast<unsigned>((h.rows * (up(h.k, 8) / 4) + 63) / 64));
+    if (h.i8) hipLaunchKernelGGL(join_splits_kernel<true>, grid, dim3(256), 0, s, j);
+    else hipLaunchKernelGGL(join_splits_kernel<false>, grid, dim3(256), 0, s, j);
+  }
   return hipGetLastError();
 }
 

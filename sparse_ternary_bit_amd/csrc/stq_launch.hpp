@@ -371,7 +371,7 @@ struct HeadBwdPlan {
   int64_t width, pieces;       // of the vocabulary
   int few;                     // few rows: dx from the head as it lies
   int splits, per;             // of dx's sum; stages of a split (few rows)
-  int64_t dlt, xt, acc;        // workspace offsets
+  int64_t rest, dlt, xt, acc;  // workspace offsets
   int64_t bytes;
 };
 HeadBwdPlan plan_head_bwd(bool i8, int64_t rows, int64_t vocab, int64_t k, bool dx, bool dw, int cus);

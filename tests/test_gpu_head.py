@@ -163,6 +163,31 @@ def test_backward_one_output_and_given_ones(stq):
     assert bool((dxw[:, :3] == 7).all()) and bool((dxw[:, 206:] == 7).all()) and bool((dww[:, :1] == 7).all()) and bool((dww[:, 204:] == 7).all())
 
 
+# One word alone has weights: dx is its term d w, which has two roundings, that of d (in fp32: the errors of p and U
+# |g|) and its own to bf16.  Every tile of the logits; dx of 8-bit heads by few rows, from parts of the sum, and by the
+# tiles themselves.
+@pytest.mark.parametrize("i8", [False, True])
+@pytest.mark.parametrize("n, v, k", [(1, 40, 24), (12, 500, 72), (20, 1000, 200), (66, 1000, 64), (300, 700, 129), (600, 250, 701),
+                                     (513, 9000, 96), (50, 70000, 24)])
+def test_the_targets_term_of_the_rows_gradient(stq, n, v, k, i8):
+    c = Case(n, v, k, i8, 3 * n, ignored=0.1 if n > 9 else 0.0)
+    word = v // 3
+    only = c.w[word].clone()
+    c.w.zero_()
+    c.w[word] = only
+    c.targets[c.targets >= 0] = word
+    if i8:
+        c.w_scale.fill_(c.w_scale[word].item())
+    _, lse = stq.head_cross_entropy(c.x, c.w, c.targets, **c.args())
+    dx, _ = stq.head_cross_entropy_backward(c.x, c.w, c.targets, lse, c.grad, need_dw=False, **c.args())
+    d, err = c.gradient_ref(lse)
+    d, err = d[:, word:word + 1], (err[:, word:word + 1] - B * d[:, word:word + 1].abs()) / (1 + B)
+    w = c.w[word].double()
+    ref = d * w
+    tol = (err + 2 * U * d.abs()) * w.abs()
+    assert bool(((dx.double() - ref).abs() <= tol * (1 + B) + B * ref.abs() + TINY).all())
+
+
 @pytest.mark.parametrize("i8", [False, True])
 @pytest.mark.parametrize("n, v, k", [(600, 250, 701), (300, 100, 1030), (260, 256, 515)])
 def test_rows_of_any_stride_and_offset(stq, n, v, k, i8):
