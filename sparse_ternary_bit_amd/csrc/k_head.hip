@@ -140,9 +140,9 @@ __device__ __forceinline__ bool no_gradient(int64_t target, int64_t vocab, float
   return target < 0 || target >= vocab || lse == -INFINITY;
 }
 
-// What the rounding of d to the bf16 `bits` leaves (nothing, if that is infinite or no number)
-__device__ __forceinline__ float rounding_rest(float d, uint32_t bits) {
-  const float f = __builtin_bit_cast(float, bits << 16);
+// What the rounding of d to bf16 leaves (nothing, if that is infinite or no number)
+__device__ __forceinline__ float rounding_rest(float d) {
+  const float f = __builtin_bit_cast(float, bf16_round(d) << 16);
   return fabsf(f) < INFINITY ? d - f : 0.0f;
 }
 
@@ -341,13 +341,15 @@ __device__ __forceinline__ void finish(const NtArgs& a, typename Mfma<kI8>::acc_
           for (int e = 0; e < 8; ++e)
             if (32 * p + 8 * q + e >= nv) d[e] = 0.0f;
         }
-        const u32x4_t o = pack8<bf16_t>(d).w[0];
-        *reinterpret_cast<u32x4_t*>(sl.at(16 * (j & 1) + r, 4 * p + q)) = o;
-        if (hot && !dead) {
+        *reinterpret_cast<u32x4_t*>(sl.at(16 * (j & 1) + r, 4 * p + q)) = pack8<bf16_t>(d).w[0];
+        if (hot) {
+          const int64_t at = want - 32 * p;
+          if (!dead && at >= 0 && at < 8 && want + 8 * q < nv) {
+            float t = d[0];
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (want == 32 * p + e && want + 8 * q < nv)
-              a.rest[m0 + 16 * j + r] = rounding_rest(d[e], (o[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
+            for (int e = 1; e < 8; ++e) t = at == e ? d[e] : t;
+            a.rest[m0 + 16 * j + r] = rounding_rest(t);
+          }
         }
       }
       if ((j & 1) || j + 1 == FM) {
@@ -530,16 +532,23 @@ __global__ __launch_bounds__(WM * WN * 64, kWavesPerSimd) void nt_kernel(NtArgs 
 // that become bf16, which holds them exactly).
 enum Lies { kRows, kAcross16, kAcross8 };
 
-// Columns c .. c + 3 (c a multiple of 4) of a row of the head, as they lie, and their values
+// Columns c .. c + 3 (c a multiple of 4) of a row of the head as they lie, and their values
+template <bool k8>
+__device__ __forceinline__ float head_value(u32x2_t v, int e) {
+  if constexpr (k8) return static_cast<float>(static_cast<int8_t>(v[0] >> (8 * e)));
+  else return __builtin_bit_cast(float, (e & 1) ? (v[e >> 1] & 0xFFFF0000u) : (v[e >> 1] << 16));
+}
 template <bool k8>
 __device__ __forceinline__ u32x2_t head4(const char* row, int64_t c) {
   if constexpr (k8) return u32x2_t{*reinterpret_cast<const uint32_t*>(row + c), 0};
   else return *reinterpret_cast<const u32x2_t*>(row + 2 * c);
 }
-template <bool k8>
-__device__ __forceinline__ float head_value(u32x2_t v, int e) {
-  if constexpr (k8) return static_cast<float>(static_cast<int8_t>(v[0] >> (8 * e)));
-  else return __builtin_bit_cast(float, (e & 1) ? (v[e >> 1] & 0xFFFF0000u) : (v[e >> 1] << 16));
+
+// Rows of 16 lanes 1 and 3 of x and 0 and 2 of y change places
+__device__ __forceinline__ void exchange16(uint32_t& x, uint32_t& y) {
+  const auto o = __builtin_amdgcn_permlane16_swap(x, y, false, false);
+  x = o[0];
+  y = o[1];
 }
 
 // 16 channels of one row of tiles of a wavefront that read its operand across:
@@ -552,6 +561,35 @@ __device__ __forceinline__ void finish_across(const NtArgs& a, f32x4_t (&acc)[FN
   const int q = lane >> 4, r = lane & 15;
   if (m0 >= a.m) return;
   const Slab<kC> sl{slab, lane};
+  // Whole sums: the targets' rest times their rows of the head, which are on their
+  // way while the 16 tokens before are put away.  A lane loads eight channels, for
+  // itself and the lane 16 from it, of fragment 2 i or 2 i + 1, and they exchange
+  // halves.  (4000 rows of 1024 under 600 words, one round of tiles: 28 us, 34 with
+  // a lane's own four channels loaded where they are used, 23 without the rest.)
+  constexpr bool k8 = kLies == kAcross8;
+  int32_t target[FM];   // -1: no gradient
+  float rest = 0.0f;
+  using Chunk = std::conditional_t<k8, u32x2_t, u32x4_t>;
+  Chunk hot[FN / 2];
+  auto rows_of = [&](int j) {
+    rest = a.rest[min(m0 + 16 * j + r, a.m - 1)];
+#pragma unroll
+    for (int i = 0; i < FN / 2; ++i) {
+      const int c = 32 * i + 16 * (q & 1) + 8 * (q >> 1);
+      hot[i] = Chunk{};
+      if (target[j] >= 0 && c < nv)
+        hot[i] = *reinterpret_cast<const Chunk*>(a.head + target[j] * a.ldw + (n0 + c) * (k8 ? 1 : 2));
+    }
+  };
+  if (a.out) {
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+      const int64_t tok = min(m0 + 16 * j + r, a.m - 1);
+      const int32_t t = a.targets[tok];
+      target[j] = no_gradient(t, a.vocab, a.lse[tok]) ? -1 : t;
+    }
+    rows_of(0);
+  }
 #pragma unroll
   for (int j = 0; j < FM; ++j) {
     static_assert(FN == 8, "the operands of this statement");
@@ -563,23 +601,30 @@ __device__ __forceinline__ void finish_across(const NtArgs& a, f32x4_t (&acc)[FN
     for (int i = 0; i < FN; ++i) v[i] = acc[i][j];
     float* const row = a.acc + (split * a.m + tok) * a.ld_acc + n0 + 4 * q;
     if (a.out) {   // whole rows, through LDS
-      // (zeros under an infinite head too, where dl = 0 gives NaN)
-      const int64_t target = tok < a.m ? a.targets[tok] : -1;
-      const bool dead = tok >= a.m || no_gradient(target, a.vocab, a.lse[tok]);
-      const float rest = dead ? 0.0f : a.rest[tok];
-      u32x4_t hot[FN / 2];
 #pragma unroll
-      for (int i = 0; i < FN; ++i) {
-        const bool on = !dead && 16 * i + 4 * q < nv;
-        const u32x2_t o = on ? head4<kLies == kAcross8>(a.head + target * a.ldw, n0 + 16 * i + 4 * q) : u32x2_t{0, 0};
-        hot[i / 2][2 * (i % 2)] = o[0];
-        hot[i / 2][2 * (i % 2) + 1] = o[1];
+      for (int i = 0; i < FN / 2; ++i) {
+        u32x2_t w[2];
+        if constexpr (k8) {
+          uint32_t lo = hot[i][0], hi = hot[i][1];
+          exchange16(lo, hi);
+          w[0] = u32x2_t{lo, 0}, w[1] = u32x2_t{hi, 0};
+        } else {
+          uint32_t lo[2] = {hot[i][0], hot[i][1]}, hi[2] = {hot[i][2], hot[i][3]};
+          exchange16(lo[0], hi[0]);
+          exchange16(lo[1], hi[1]);
+          w[0] = u32x2_t{lo[0], lo[1]}, w[1] = u32x2_t{hi[0], hi[1]};
+        }
+        // (zeros without a gradient, under an infinite head too, where dl = 0 gives NaN)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            v[2 * i + h][e] = target[j] < 0 ? 0.0f : fmaf(rest, head_value<k8>(w[h], e), v[2 * i + h][e]);
       }
+      __builtin_amdgcn_sched_barrier(0);
+      if (j + 1 < FM) rows_of(j + 1);
 #pragma unroll
       for (int i = 0; i < FN; ++i) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          v[i][e] = dead ? 0.0f : fmaf(rest, head_value<kLies == kAcross8>(u32x2_t{hot[i / 2][2 * (i % 2)], hot[i / 2][2 * (i % 2) + 1]}, e), v[i][e]);
         const int c = 16 * i + 4 * q;
         const uint32_t o[4] = {bf16_round(v[i][0]), bf16_round(v[i][1]), bf16_round(v[i][2]), bf16_round(v[i][3])};
         *reinterpret_cast<u32x2_t*>(sl.at(16 * (j & 1) + r, 2 * i + (q >> 1)) + (q & 1) * 8) = u32x2_t{o[0] | o[1] << 16, o[2] | o[3] << 16};
@@ -972,7 +1017,7 @@ __global__ __launch_bounds__(kFewWaves * 64, 2) void nt_few_kernel(NtArgs a) {
       v *= g;
       if (kI8) v *= scale[e];
       d[e] = bf16_round(dead || 4 * q + e >= nv ? 0.0f : v);
-      if (!dead && want == e && 4 * q + e < nv) a.rest[r] = rounding_rest(v, d[e]);
+      if (!dead && want == e && 4 * q + e < nv) a.rest[r] = rounding_rest(v);
     }
     if (on) *reinterpret_cast<u32x2_t*>(a.dl + r * a.ld_dl + n0 + 4 * q) = u32x2_t{d[0] | d[1] << 16, d[2] | d[3] << 16};
     if (a.dlt) {
@@ -1233,12 +1278,13 @@ __global__ __launch_bounds__(256) void join_splits_kernel(JoinArgs a) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) s[e] += v[e];
   };
-  const int64_t target = on && g == 0 ? a.targets[row] : -1;
-  // (zeros as in finish_across)
-  const bool dead = target < 0 || no_gradient(target, a.vocab, a.lse[row]);
-  const float rest = dead ? 0.0f : a.rest[row];
-  const u32x2_t hot = dead || c >= a.n ? u32x2_t{0, 0} : head4<k8>(a.head + target * a.ldw, c);
+  int32_t target = -1;
+  float lse = 0.0f, rest = 0.0f;
   if (on) {
+    // (on their way beside the sums)
+    target = a.targets[row];
+    lse = a.lse[row];
+    rest = a.rest[row];
     const float* const at = a.acc + row * a.ld_acc + c;
     int p = g;
     for (; p + 12 < a.splits; p += 16) {
@@ -1250,6 +1296,8 @@ __global__ __launch_bounds__(256) void join_splits_kernel(JoinArgs a) {
     }
     for (; p < a.splits; p += 4) add(*reinterpret_cast<const f32x4_t*>(at + p * a.m * a.ld_acc));
   }
+  const bool dead = no_gradient(target, a.vocab, lse);   // (zeros as in finish_across)
+  const u32x2_t hot = g || dead || c >= a.n ? u32x2_t{0, 0} : head4<k8>(a.head + target * a.ldw, c);
   part[g][lane] = s;
   __syncthreads();
   if (g || !on) return;
