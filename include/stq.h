@@ -697,11 +697,12 @@ stq_status stq_head_cross_entropy_workspace(int x_dtype, int64_t n_rows, int64_t
  * 0 and it adds nothing to dw, whatever x and w hold; another whose lse is NaN gives
  * NaN.  dl is formed in fp32 and rounded to bf16 for the two products (with 8-bit
  * rows after its w_scale, so that the integers, which bf16 holds exactly, enter as
- * they are): a term is off by at most 2^-8 of itself, half a bf16 step.  In dx the
- * target's term, as large as all the others of its row together, is added in fp32
- * instead; the others' roundings average out beside dx's own.  dw errs by about
- * 0.0017 of its norm from that and as much from its own rounding, up to 0.0039 where
- * one row makes it up.  Sums are fp32 in an order that is fixed for a device.  dx and dw are rounded from them
+ * they are): a term is off by at most 2^-8 of itself, half a bf16 step.  The target's
+ * term, as large as all the others of its row together, is added in fp32 to dx, and
+ * to dw where there are at most 32 rows; the others' roundings average out beside
+ * the results' own.  dw of more rows errs by about 0.0017 of its norm from that
+ * (0.0022 with 33) and as much from its own rounding.  Sums are fp32 in an order that
+ * is fixed for a device.  dx and dw are rounded from them
  * once and may not overlap the operands; rows that all start on 16 bytes are
  * written faster. */
 stq_status stq_head_cross_entropy_backward(const void* x, int x_dtype, int64_t x_row_stride, const float* x_scale,

@@ -20,6 +20,8 @@
 // because the matrix cores take dx's and dW's factors in it.  The many small
 // terms' roundings average out in dx; the target's is as large as all the others
 // together, so what its rounding leaves is kept in fp32 and enters dx at the end.
+// dW of few rows, where a target's term makes up its word's row, takes that rest
+// as rows of its own; those of many rows average out there as well.
 //
 // 4096 rows under 131072 x 7168 in bf16: 5.2 to 5.3 ms, 1.46 PFLOP/s (a large
 // library product 1.56); matrix cores 75 % busy at 1.8 of 2.4 GHz, so the card's
@@ -73,6 +75,7 @@ struct NtArgs {
   float* rest;            // [m]: what the rounding of the target's dl leaves
   uint16_t* dlt;          // [n][ld_dlt], zeros in tokens m .. m_pad - 1; may be NULL
   int64_t ld_dlt;
+  int64_t rest_at;        // few rows: the targets' rest in dlt's columns from here on, beside zeros; 0: not there
   int64_t n_pad, m_pad;
   const char* head;       // (dx) the whole head, for the targets' rows
   // kSum
@@ -314,9 +317,13 @@ __device__ __forceinline__ void finish(const NtArgs& a, typename Mfma<kI8>::acc_
       g[j] = tok < a.m ? a.g[tok] : 0.0f;
     }
     const Slab<kC> sl{slab, lane};
+    constexpr bool kRestRows = !kI8 && FM <= 4;   // (the tiles of few rows)
+    float rest[2];
+    int hot_at[2];   // this lane's target: channels from 8 q on
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
       take(j);
+      if constexpr (kRestRows) rest[j & 1] = 0.0f, hot_at[j & 1] = -1;
       const bool dead = no_gradient(target[j], a.vocab, lse[j]);
       const float gj = dead ? 0.0f : g[j];
       const int64_t want = target[j] - a.v0 - n0 - 8 * q;
@@ -348,7 +355,9 @@ __device__ __forceinline__ void finish(const NtArgs& a, typename Mfma<kI8>::acc_
             float t = d[0];
 #pragma unroll
             for (int e = 1; e < 8; ++e) t = at == e ? d[e] : t;
-            a.rest[m0 + 16 * j + r] = rounding_rest(t);
+            t = rounding_rest(t);
+            a.rest[m0 + 16 * j + r] = t;
+            if constexpr (kRestRows) rest[j & 1] = t, hot_at[j & 1] = static_cast<int>(want);
           }
         }
       }
@@ -360,6 +369,20 @@ __device__ __forceinline__ void finish(const NtArgs& a, typename Mfma<kI8>::acc_
                       static_cast<int>(min(static_cast<int64_t>(kC), a.n_pad - n0)));
         if (a.dlt)
           sl.store_columns(a.dlt + n0 * a.ld_dlt + t0, a.ld_dlt, static_cast<int>(min(static_cast<int64_t>(tokens), a.m_pad - t0)), nv);
+        if constexpr (kRestRows) {
+          if (a.dlt && a.rest_at) {
+            sl.fence();
+#pragma unroll
+            for (int h = 0; h <= (j & 1); ++h) {
+#pragma unroll
+              for (int p = 0; p < kP; ++p) *reinterpret_cast<u32x4_t*>(sl.at(16 * h + r, 4 * p + q)) = u32x4_t{0, 0, 0, 0};
+              if (hot_at[h] >= 0)
+                reinterpret_cast<uint16_t*>(sl.at(16 * h + r, 4 * (hot_at[h] >> 5) + q))[hot_at[h] & 7] = static_cast<uint16_t>(bf16_round(rest[h]));
+            }
+            sl.fence();
+            sl.store_columns(a.dlt + n0 * a.ld_dlt + a.rest_at + t0, a.ld_dlt, static_cast<int>(min(static_cast<int64_t>(tokens), a.m_pad - t0)), nv);
+          }
+        }
         sl.fence();
       }
     }
@@ -1010,6 +1033,7 @@ __global__ __launch_bounds__(kFewWaves * 64, 2) void nt_few_kernel(NtArgs a) {
     const float lse = on ? a.lse[r] : 0.0f;
     const bool dead = no_gradient(target, a.vocab, lse);
     const float g = dead ? 0.0f : a.g[r];
+    float rest = 0.0f;
     uint32_t d[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -1017,17 +1041,20 @@ __global__ __launch_bounds__(kFewWaves * 64, 2) void nt_few_kernel(NtArgs a) {
       v *= g;
       if (kI8) v *= scale[e];
       d[e] = bf16_round(dead || 4 * q + e >= nv ? 0.0f : v);
-      if (!dead && want == e && 4 * q + e < nv) a.rest[r] = rounding_rest(v);
+      if (!dead && want == e && 4 * q + e < nv) a.rest[r] = rest = rounding_rest(v);
     }
     if (on) *reinterpret_cast<u32x2_t*>(a.dl + r * a.ld_dl + n0 + 4 * q) = u32x2_t{d[0] | d[1] << 16, d[2] | d[3] << 16};
     if (a.dlt) {
-      // [channel][token], zeros for tokens up to a whole stage
+      // [channel][token], zeros for tokens up to a whole stage; from rest_at on the rest
       u32x4_t* const flat = reinterpret_cast<u32x4_t*>(&turned[0][0]);
 #pragma unroll
       for (int i = 0; i < 2; ++i) flat[lane + 64 * i] = u32x4_t{0, 0, 0, 0};
       __builtin_amdgcn_wave_barrier();
 #pragma unroll
-      for (int e = 0; e < 4; ++e) turned[4 * q + e][r] = static_cast<uint16_t>(d[e]);
+      for (int e = 0; e < 4; ++e) {
+        turned[4 * q + e][r] = static_cast<uint16_t>(d[e]);
+        if (!dead && want == e && 4 * q + e < nv) turned[4 * q + e][a.rest_at + r] = static_cast<uint16_t>(bf16_round(rest));
+      }
       __builtin_amdgcn_wave_barrier();
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -1215,10 +1242,11 @@ __global__ __launch_bounds__(1024) void head_join_kernel(const float2* stats, co
 }
 
 // out[c][r] = in[r][c] for r < n (zeros for r = n .. n_pad - 1 and for rows
-// without a gradient, whatever they hold), c < k; 64 x 64 a workgroup.
+// without a gradient, whatever they hold), c < k; 64 x 64 a workgroup.  The same
+// again from column `again` on, if that is not 0.
 __global__ __launch_bounds__(256) void transpose_kernel(const char* in, int64_t ld, int64_t n, int64_t k, const int32_t* targets,
                                                         const float* lse, int64_t vocab, uint16_t* out, int64_t ld_out,
-                                                        int64_t n_pad) {
+                                                        int64_t n_pad, int64_t again) {
   __shared__ uint16_t tile[64][66];
   const int64_t r0 = static_cast<int64_t>(blockIdx.x) * 64, c0 = static_cast<int64_t>(blockIdx.y) * 64;
   const int row = threadIdx.x >> 3, c = (threadIdx.x & 7) * 8;
@@ -1246,6 +1274,7 @@ __global__ __launch_bounds__(256) void transpose_kernel(const char* in, int64_t 
 #pragma unroll
     for (int e = 0; e < 4; ++e) w[e] = tile[col][c + 2 * e] | static_cast<uint32_t>(tile[col][c + 2 * e + 1]) << 16;
     *reinterpret_cast<u32x4_t*>(out + (c0 + col) * ld_out + r0 + c) = w;
+    if (again) *reinterpret_cast<u32x4_t*>(out + (c0 + col) * ld_out + again + r0 + c) = w;
   }
 }
 
@@ -1442,9 +1471,18 @@ static int dx_splits(int64_t rows, int64_t k, int64_t stages, int64_t pieces, in
   return best;
 }
 
+// Tokens along dW's sum: their dl, up to m_pad of them, and of up to 32 rows the
+// targets' rest behind it, in the one stage that their sum takes anyway.  (A second
+// stage for 33 to 64 rows: 64 under 131072 x 7168 1292 us, 1193 without.)
+struct DwTokens {
+  int64_t m_pad, rest_at, all;
+};
+static DwTokens dw_tokens(int64_t rows) {
+  return rows <= 32 ? DwTokens{32, 32, 64} : DwTokens{up(rows, 64), 0, up(rows, 64)};
+}
+
 HeadBwdPlan plan_head_bwd(bool i8, int64_t rows, int64_t vocab, int64_t k, bool dx, bool dw, int cus) {
   HeadBwdPlan p{};
-  const int64_t m_pad = up(rows, 64);
   if (i8 && rows <= kFewRows && rows * up(vocab, 64) <= int64_t{1} << 30) {
     // the whole vocabulary at once: dl is small beside the head (and its rows within 32-bit offsets)
     p.few = 1;
@@ -1476,9 +1514,10 @@ HeadBwdPlan plan_head_bwd(bool i8, int64_t rows, int64_t vocab, int64_t k, bool 
   p.pieces = (vocab + p.width - 1) / p.width;
   int64_t at = up(rows * p.width * 2, 256);
   p.dlt = at;
-  if (dw) at += up(p.width * m_pad * 2, 256);
+  const int64_t tokens = dw_tokens(rows).all;
+  if (dw) at += up(p.width * tokens * 2, 256);
   p.xt = at;
-  if (dw) at += up(k * m_pad * 2, 256);
+  if (dw) at += up(k * tokens * 2, 256);
   p.acc = at;
   p.splits = dx ? dx_splits(rows, k, std::min(p.width, up(vocab, 64)) / 64, p.pieces, cus) : 1;
   if (dx && (p.pieces > 1 || p.splits > 1)) at += up(p.splits * rows * up(k, 8) * 4, 256);
@@ -1494,11 +1533,11 @@ hipError_t launch_head_bwd(const HeadArgs& h, const HeadBwdArgs& b, const HeadBw
   uint16_t* dlt = reinterpret_cast<uint16_t*>(base + p.dlt);
   uint16_t* xt = reinterpret_cast<uint16_t*>(base + p.xt);
   float* acc = p.few || p.pieces > 1 || p.splits > 1 ? reinterpret_cast<float*>(base + p.acc) : nullptr;
-  const int64_t m_pad = up(h.rows, 64);
+  const DwTokens tokens = dw_tokens(h.rows);
   if (b.dw)
-    hipLaunchKernelGGL(transpose_kernel, dim3(static_cast<unsigned>(m_pad / 64), static_cast<unsigned>((h.k + 63) / 64)), dim3(256),
-                       0, s, static_cast<const char*>(h.x), h.ldx, h.rows, h.k, h.targets, b.lse, h.vocab, xt, m_pad,
-                       m_pad);
+    hipLaunchKernelGGL(transpose_kernel, dim3(static_cast<unsigned>((tokens.m_pad + 63) / 64), static_cast<unsigned>((h.k + 63) / 64)),
+                       dim3(256), 0, s, static_cast<const char*>(h.x), h.ldx, h.rows, h.k, h.targets, b.lse, h.vocab, xt, tokens.all,
+                       tokens.m_pad, tokens.rest_at);
   for (int64_t i = 0; i < p.pieces; ++i) {
     const int64_t v0 = i * p.width, n = std::min(p.width, h.vocab - v0), n_pad = up(n, 64);
     NtArgs a = logits_args(h);
@@ -1512,10 +1551,11 @@ hipError_t launch_head_bwd(const HeadArgs& h, const HeadBwdArgs& b, const HeadBw
     a.ld_dl = p.width;
     a.rest = rest;
     a.dlt = b.dw ? dlt : nullptr;
-    a.ld_dlt = m_pad;
+    a.ld_dlt = tokens.all;
+    a.rest_at = tokens.rest_at;
     a.vocab = h.vocab;
     a.n_pad = n_pad;
-    a.m_pad = m_pad;
+    a.m_pad = tokens.m_pad;
     const Tile t = pick_tile(h.rows, n, cus, true);
     if (h.i8) launch_nt<true, kGrad>(a, t, cus, s);
     else launch_nt<false, kGrad>(a, t, cus, s);
@@ -1552,12 +1592,12 @@ hipError_t launch_head_bwd(const HeadArgs& h, const HeadBwdArgs& b, const HeadBw
     if (b.dw) {
       NtArgs d{};
       d.a = reinterpret_cast<const char*>(dlt);
-      d.lda = m_pad * 2;
+      d.lda = tokens.all * 2;
       d.w = reinterpret_cast<const char*>(xt);
-      d.ldw = m_pad * 2;
+      d.ldw = tokens.all * 2;
       d.m = n;
       d.n = h.k;
-      d.kbytes = m_pad * 2;
+      d.kbytes = tokens.all * 2;
       d.out = b.dw + v0 * b.ld_dw;
       d.ld_out = b.ld_dw;
       launch_nt<false, kSum>(d, pick_tile(n, h.k, cus, false), cus, s);

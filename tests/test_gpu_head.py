@@ -188,6 +188,48 @@ def test_the_targets_term_of_the_rows_gradient(stq, n, v, k, i8):
     assert bool(((dx.double() - ref).abs() <= tol * (1 + B) + B * ref.abs() + TINY).all())
 
 
+# Each row of x has two columns of its own, so that dW's row of its target has there one term d x, with two roundings as
+# above (and the rest's own, B B |d x|), for up to 32 rows: targets apart, a few that many rows share, one for all, in
+# every tile of the logits.
+@pytest.mark.parametrize("n, v, words", [(1, 40, 40), (2, 500, 1), (12, 500, 500), (16, 20000, 3), (17, 3000, 3000), (30, 3000, 7), (32, 200, 200),
+                                         (31, 40000, 40000), (20, 70000, 1), (9, 33000, 33000)])
+def test_the_targets_term_of_the_heads_gradient(stq, n, v, words):
+    k = 2 * n + 3
+    c = Case(n, v, k, False, n, ignored=0.0)
+    own = torch.arange(n, device="cuda") * 2
+    keep = torch.zeros(n, k, dtype=torch.bool, device="cuda")
+    keep[torch.arange(n, device="cuda"), own] = keep[torch.arange(n, device="cuda"), own + 1] = True
+    c.x.copy_(torch.where(keep, c.x * 4, 0))
+    c.targets.remainder_(words)
+    dead = torch.rand(n, device="cuda", generator=torch.Generator(device="cuda").manual_seed(n)) < 0.1
+    c.targets[dead] = -1
+    c.x[dead] = float("nan")
+    _, lse = stq.head_cross_entropy(c.x, c.w, c.targets)
+    _, dw = stq.head_cross_entropy_backward(c.x, c.w, c.targets, lse, c.grad, need_dx=False)
+    assert bool(torch.isfinite(dw).all())
+    r = torch.arange(n, device="cuda")[~dead]
+    c.x[dead] = 0
+    t = c.targets[r].long()
+    d, err = c.gradient_ref(torch.where(dead, 0.0, lse))
+    d, err = d[r, t][:, None], ((err[r, t] - B * d[r, t].abs()) / (1 + B))[:, None]
+    col = torch.stack([own[r], own[r] + 1], 1)
+    x, got = c.x.double()[r[:, None], col], dw.double()[t[:, None], col]
+    tol = (err + (2 * U + B * B) * d.abs()) * x.abs()
+    assert bool(((got - d * x).abs() <= tol * (1 + B) + B * (d * x).abs() + TINY).all())
+    again = stq.head_cross_entropy_backward(c.x, c.w, c.targets, lse, c.grad, need_dx=False)[1]
+    assert torch.equal(again, dw)
+
+
+# many rows to a word: sums in the rows' order, targets of every kind beside each other
+@pytest.mark.parametrize("n, v, k, words", [(20, 30, 515, 3), (300, 700, 129, 5), (1300, 4000, 701, 40), (2500, 300, 96, 2)])
+def test_gradients_of_words_that_rows_share(stq, n, v, k, words):
+    c = Case(n, v, k, False, n + k)
+    c.targets.copy_(torch.where(c.targets < 0, c.targets, c.targets % words + v - words))
+    _, lse = stq.head_cross_entropy(c.x, c.w, c.targets)
+    dx, dw = stq.head_cross_entropy_backward(c.x, c.w, c.targets, lse, c.grad)
+    c.check_backward(dx, dw, lse)
+
+
 @pytest.mark.parametrize("i8", [False, True])
 @pytest.mark.parametrize("n, v, k", [(600, 250, 701), (300, 100, 1030), (260, 256, 515)])
 def test_rows_of_any_stride_and_offset(stq, n, v, k, i8):
