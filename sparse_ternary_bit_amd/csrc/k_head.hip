@@ -149,6 +149,8 @@ __device__ __forceinline__ float rounding_rest(float d) {
   return fabsf(f) < INFINITY ? d - f : 0.0f;
 }
 
+// exp(x) with the error of exp2's rounded argument, |x| 2^-24 of it: a logit |x| below
+// the largest is as far off in its own last digits, and its term then counts e^-|x|
 __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
 // Rows of bf16 that a wavefront holds as products, on their way to memory: 32

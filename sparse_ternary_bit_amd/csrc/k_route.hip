@@ -36,9 +36,20 @@ constexpr int kMaxExperts = kRouteMaxExperts;
 static_assert(kRouteMaxTop <= 2 * kLanes, "a lane holds two of a token's pairs");
 // bits of a key that hold the column, for kN logits a lane
 constexpr int index_bits(int n) { return n == 4 ? 6 : n == 8 ? 7 : n == 16 ? 8 : n == 32 ? 9 : 10; }
-constexpr float kLog2e = 1.44269504088896340736f;
 
-__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+// exp(x) within three halves of a step of fp32 or so for x from -87 to 0, 0 below:
+// exp2 of the rounded product x log2(e), times one plus what the rounding left (the
+// exponent's own rounding would cost 40 steps at x = -60).  -inf counts as -200, a
+// NaN stays one.
+__device__ __forceinline__ float exp_of(float x) {
+  constexpr double kLog2e = 1.44269504088896340736;
+  constexpr float kHigh = static_cast<float>(kLog2e), kLow = static_cast<float>(kLog2e - kHigh), kLn2 = 0.69314718055994530942f;
+  x = x < -200.0f ? -200.0f : x;
+  const float t = x * kHigh;
+  const float left = fmaf(x, kLow, fmaf(x, kHigh, -t));
+  const float e = __builtin_amdgcn_exp2f(t);
+  return fmaf(e, left * kLn2, e);
+}
 
 // Column of a lane's j-th logit: four neighbours a lane, 64 a step
 __device__ __forceinline__ int column(int lane16, int j) { return (j >> 2) * 64 + lane16 * 4 + (j & 3); }

@@ -94,6 +94,23 @@ def test_routing(stq, n, e, k, renorm, dtype):
     _check(stq.route_tokens(x.cuda(), k, renorm), x, k, renorm)
 
 
+def test_probabilities_far_below_the_largest(stq):
+    # Two experts x = 0 and -i / 8, whose difference is exact: exp errs by 3 u (2 u the instruction, u its last step),
+    # the sum by as much and u more, its reciprocal and the product by u each: 9 u at any distance.  In the gradient at
+    # the lower expert, p (1 - p) with g = 1 there alone, the second factor adds at most 9 u p / (1 - p) + 2 u and the
+    # last product u.
+    low = torch.arange(1, 680) / 8.0
+    x = torch.stack([torch.zeros_like(low), -low], 1)
+    p = 1.0 / (1.0 + torch.exp(low.double()))
+    r = stq.route_tokens(x.cuda(), 2, False)
+    got = r.pair_weight.cpu().double().view(-1, 2)
+    assert bool(((got[:, 1] - p).abs() <= 9 * U * p).all()) and bool(((got[:, 0] - (1 - p)).abs() <= 9 * U * (1 - p)).all())
+    g = torch.tensor([0.0, 1.0]).repeat(len(low))
+    d = stq.route_tokens_backward(x.cuda(), r.pair_expert, None, 2, False, grad_weight=g.cuda()).cpu().double()
+    want = p * (1 - p)
+    assert bool(((d[:, 1] - want).abs() <= U * (12 + 9 * p / (1 - p)) * want).all())
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("n, e, k, pads", [(1, 16, 2, 1), (50, 64, 4, 20), (500, 256, 8, 77), (130, 40, 3, 130), (64, 512, 8, 64)])
 def test_padding(stq, n, e, k, pads, dtype):
