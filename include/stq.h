@@ -502,7 +502,8 @@ stq_status stq_token_logprobs_backward(const void* logits, int x_dtype, int64_t 
  * so that q * scale stands for y, and q does not depend on the order of the
  * sum.  A row of zeros, or one whose step underflows to 0, gives scale 0 and q
  * = 0; a row with a NaN or an infinity in v gives scale NaN and q = 0.  A row
- * whose sum of squares passes fp32's range has rstd 0.
+ * whose sum of squares passes fp32's range has rstd 0, one whose sum is 0 there
+ * rstd 1 / sqrt(eps): infinite for eps 0, and its y not finite.
  *   x          [n_rows, d] fp32 (STQ_X_F32) or bf16 bits (STQ_X_BF16), rows
  *              x_row_stride elements apart
  *   residual   [n_rows, d] likewise, or NULL

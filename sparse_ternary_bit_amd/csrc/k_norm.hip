@@ -125,7 +125,7 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs a) {
   const float step = finite ? __builtin_bit_cast(float, mx) / 127.0f : NAN;
   if (threadIdx.x == 0) {
     if (a.rstd) a.rstd[r] = rstd;
-    if (a.q) a.scale[r] = step * rstd;
+    if (a.q) a.scale[r] = step == 0.0f ? 0.0f : step * rstd;   // (zeros without eps: rstd is infinite)
   }
   const bool some = finite && step > 0.0f;
   const float inv = some ? 1.0f / step : 0.0f;

@@ -128,6 +128,16 @@ def test_rows_that_are_empty_or_not_finite(stq, d):
     assert np.isnan(got.rstd[2].item()) and got.rstd[3].item() == 0.0 and got.rstd[4].item() == 0.0
 
 
+@pytest.mark.parametrize("n, d", [(3, 100), (3, 700), (2, 4000), (2, 9000), (600, 2500)])
+def test_rows_of_zeros_without_eps(stq, n, d):
+    x, _, w = _inputs(n, d, torch.float32, None, d)
+    x[1] = 0.0
+    got = stq.rmsnorm_rows(x.cuda(), w.cuda(), 0.0)
+    assert got.scale[1].item() == 0.0 and not got.q[1].any() and np.isinf(got.rstd[1].item())
+    rest = [i for i in range(n) if i != 1]
+    assert bool(torch.isfinite(got.scale[rest]).all()) and bool((got.scale[rest] > 0).all())
+
+
 def test_halves_go_to_even(stq):
     # weight 1 and max 127: the quotients are the values themselves
     row = torch.tensor([127.0] + [i + 0.5 for i in range(-126, 126)] + [0.25, -0.75, 63.0])
