@@ -536,7 +536,7 @@ stq_status stq_rmsnorm_rows(const void* x, int x_dtype, int64_t x_row_stride, co
  *   dy         [n_rows, d] fp32 or bf16
  *   dh         [n_rows, d] of h's type, or NULL (zeros)
  *   dx         [n_rows, d] of h's type, or NULL (not wanted); may be dh, or dy
- *              where the types are the same, with the same stride
+ *              where the types are the same, with the same stride, but not h
  *   dweight    fp32 [d], or NULL (not wanted); zeros without rows
  *   workspace, workspace_bytes   at least what
  *              stq_rmsnorm_rows_backward_workspace reports (may be NULL when 0)

@@ -791,6 +791,7 @@ stq_status stq_rmsnorm_rows_backward(const void* h, int h_dtype, int64_t h_row_s
   if (st == STQ_OK && dx) st = matrix_check("dx", dx, h_dtype, dx_row_stride, n_rows, d, who);
   if (st != STQ_OK) return st;
   if (dx && n_rows > 1 && dx == dh && dx_row_stride != dh_row_stride) return fail(STQ_E_ARG, "%s: in place needs equal row strides", who);
+  if (dx && dx == h) return fail(STQ_E_ARG, "%s: dx may not be h", who);
   if (dx && dx == dy && (h_dtype != dy_dtype || (n_rows > 1 && dx_row_stride != dy_row_stride)))
     return fail(STQ_E_ARG, "%s: in place needs equal types and row strides", who);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);

@@ -204,3 +204,10 @@ def test_head_workspaces(L):
     assert bwd(BF16, 4096, 1 << 20, 7168, 1, 1, 256, ctypes.byref(need)) == 0 and need.value < 1 << 30
     _done(L, "stq_head_cross_entropy_backward", HEAD_BWD, dict(dx=None, dw=None, lse=None, g=None, wsp=None, wsb=0))
     _done(L, "stq_head_cross_entropy_backward", HEAD_BWD, dict(n=0, dw=None, x=None, w=None, t=None, lse=None, g=None, wsp=None, wsb=0))
+
+
+def test_norm_gradient_in_the_place_of_h(L):
+    # with few rows the workgroups of dweight read h beside those that write dx
+    far = dict(dy=FAKE + 4096, dh=None, yd=BF16)
+    _refused(L, "stq_rmsnorm_rows_backward", NORM_BWD, dict(far, dx=FAKE), 1)
+    _refused(L, "stq_rmsnorm_rows_backward", NORM_BWD, dict(far, dx=FAKE, dw=None), 1)
