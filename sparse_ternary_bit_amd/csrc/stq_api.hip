@@ -1057,6 +1057,8 @@ stq_status stq_head_cross_entropy_backward(const void* x, int x_dtype, int64_t x
     const stq::HeadBwdPlan plan = stq::plan_head_bwd(x_dtype == STQ_X_I8, n_rows, vocab, k, dx != nullptr, dw != nullptr, cus);
     st = check_workspace(workspace, workspace_bytes, plan.bytes, who);
     if (st != STQ_OK) return st;
+    if ((dx && (dx == x || dx == w)) || (dw && (dw == x || dw == w || dw == dx)))
+      return fail(STQ_E_ARG, "%s: dx or dw may not be an operand or one another", who);
     const stq::HeadBwdArgs b{lse, grad_loss, dx, dx_row_stride, dw, dw_row_stride};
     e = stq::launch_head_bwd(head_args(x, x_dtype, x_row_stride, x_scale, w, w_row_stride, w_scale, n_rows, vocab, k, targets), b,
                              plan, workspace, cus, s);

@@ -211,3 +211,9 @@ def test_norm_gradient_in_the_place_of_h(L):
     far = dict(dy=FAKE + 4096, dh=None, yd=BF16)
     _refused(L, "stq_rmsnorm_rows_backward", NORM_BWD, dict(far, dx=FAKE), 1)
     _refused(L, "stq_rmsnorm_rows_backward", NORM_BWD, dict(far, dx=FAKE, dw=None), 1)
+
+
+def test_head_gradients_in_an_operands_place(L):
+    far = dict(x=FAKE, w=FAKE + 65536, dx=FAKE + 131072, dw=FAKE + 262144)
+    for kw in [dict(dx=FAKE), dict(dx=FAKE + 65536), dict(dw=FAKE, dws=104), dict(dw=FAKE + 65536, dws=104), dict(dw=FAKE + 131072)]:
+        _refused(L, "stq_head_cross_entropy_backward", HEAD_BWD, dict(far, **kw), 1)
