@@ -639,7 +639,8 @@ stq_status stq_combine_rows(const void* z, int z_dtype, int64_t z_row_stride, in
  *            unwritten, and no row may have two pairs (stq_route_tokens gives none)
  *   dweight  fp32 [n_tokens * top_k], or NULL (not wanted); reads z, which may
  *            be NULL otherwise
- * The other arguments and limits are as above.  dz may not overlap z or dy. */
+ * The other arguments and limits are as above.  dz may be z where types and strides
+ * are the same; else it may not overlap z or dy. */
 stq_status stq_combine_rows_backward(const void* dy, int dy_dtype, int64_t dy_row_stride, const void* z, int z_dtype,
                                      int64_t z_row_stride, int64_t n_rows, const int32_t* pair_row,
                                      const float* pair_weight, int64_t n_tokens, int64_t top_k, int64_t d, void* dz,

@@ -1030,7 +1030,7 @@ def combine_rows_backward(dy: torch.Tensor, pair_row: torch.Tensor, top_k: int, 
     """(dz, dweight) of combine_rows for the gradient dy fp32 or bf16 [n_tokens, d]: dz[pair_row[t, j]] =
     weight[t, j] * dy[t], fp32 or bf16 like z ([n_rows, d]; `dz`'s type or dz_dtype, z's when neither is given; rows
     of no pair stay unwritten), and dweight fp32 [n_tokens * top_k], the product of dy[t] and the pair's row; None for
-    the one not needed.  No row may have two pairs."""
+    the one not needed.  No row may have two pairs.  dz may be z where the types are the same."""
     dev = _one_gpu(dy, pair_row, z, weight, dz, dweight)
     ys, zs = _rows("dy", dy, *_FLOATS), _rows("z", z, *_FLOATS)
     rows, d = z.shape

@@ -938,6 +938,9 @@ stq_status stq_combine_rows_backward(const void* dy, int dy_dtype, int64_t dy_ro
   if (st == STQ_OK && dz) st = matrix_check("dz", dz, dz_dtype, dz_row_stride, n_rows, d, who);
   if (st != STQ_OK) return st;
   if (!aligned(pair_row, 4) || !aligned(pair_weight, 4) || !aligned(dweight, 4)) return fail(STQ_E_ALIGN, "%s: pairs or dweight not 4-byte aligned", who);
+  if (dz && dz == dy) return fail(STQ_E_ARG, "%s: dz may not be dy", who);
+  if (dz && dweight && dz == z && (dz_dtype != z_dtype || (n_rows > 1 && dz_row_stride != z_row_stride)))
+    return fail(STQ_E_ARG, "%s: in place needs equal types and row strides", who);
   const stq::CombineBwdArgs a{dy, dy_dtype == STQ_X_BF16, dy_row_stride, dweight ? z : nullptr, z_dtype == STQ_X_BF16,
                               z_row_stride, n_rows, pair_row, pair_weight, n_tokens, static_cast<int>(top_k), d, dz,
                               dz_dtype == STQ_X_BF16, dz_row_stride, dweight};

@@ -217,3 +217,10 @@ def test_head_gradients_in_an_operands_place(L):
     far = dict(x=FAKE, w=FAKE + 65536, dx=FAKE + 131072, dw=FAKE + 262144)
     for kw in [dict(dx=FAKE), dict(dx=FAKE + 65536), dict(dw=FAKE, dws=104), dict(dw=FAKE + 65536, dws=104), dict(dw=FAKE + 131072)]:
         _refused(L, "stq_head_cross_entropy_backward", HEAD_BWD, dict(far, **kw), 1)
+
+
+def test_combine_gradient_in_an_operands_place(L):
+    far = dict(dy=FAKE + 4096, z=FAKE + 8192, zd=BF16)
+    _refused(L, "stq_combine_rows_backward", COMBINE_BWD, dict(far, dz=FAKE + 4096), 1)
+    _refused(L, "stq_combine_rows_backward", COMBINE_BWD, dict(far, dz=FAKE + 8192, zd=F32), 1)
+    _refused(L, "stq_combine_rows_backward", COMBINE_BWD, dict(far, dz=FAKE + 8192, dzs=104), 1)

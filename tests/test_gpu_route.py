@@ -402,6 +402,17 @@ def test_combine_strides_and_offsets(stq):
     assert torch.equal(dz, want_dz) and torch.equal(dw, want_dw) and not dzw[:, 0].any() and not dzw[:, d + 1].any()
 
 
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n, k, d", [(9, 3, 87), (5, 32, 1203), (40, 8, 4099), (3, 2, 264)])
+def test_combine_gradient_in_the_rows_place(stq, n, k, d, dt):
+    row, w = (t.cuda() for t in _pairs(n, k, 3, n * k // 5, n + d))
+    g = torch.Generator().manual_seed(d)
+    z, dy = torch.randn((n * k + 3, d), generator=g).to(dt).cuda(), torch.randn((n, d), generator=g).cuda()
+    want, want_dw = stq.combine_rows_backward(dy, row, k, z, w, dz=z.clone())
+    got, dw = stq.combine_rows_backward(dy, row, k, z, w, dz=z)
+    assert got.data_ptr() == z.data_ptr() and torch.equal(got, want) and torch.equal(dw, want_dw)
+
+
 def test_rows_past_32_bits(stq):
     # rows of z that start beyond 2^32 bytes and 2^31 elements
     rows, d = 600, 4_000_000
