@@ -131,7 +131,7 @@ def test_forward(stq, n, v, k, i8):
     c.check_forward(*stq.head_cross_entropy(c.x, c.w, c.targets, **c.args()))
 
 
-# dW's 256 x 256 tiles; several pieces of the vocabulary, dx's sum shared out or not, in two rounds of tiles or one
+# dW's 256 x 256 tiles; dx's sum shared out or not, in two rounds of tiles or one (all in one piece of the vocabulary)
 @pytest.mark.parametrize("i8", [False, True])
 @pytest.mark.parametrize("n, v, k", SHAPES + [(70, 8192, 2048), (20, 17000, 8000), (900, 17000, 8000),
                                               (1300, 4500, 6501), (4097, 3001, 6999)])
@@ -140,6 +140,27 @@ def test_backward(stq, n, v, k, i8):
     _, lse = stq.head_cross_entropy(c.x, c.w, c.targets, **c.args())
     dx, dw = stq.head_cross_entropy_backward(c.x, c.w, c.targets, lse, c.grad, need_dw=not i8, **c.args())
     assert dx.shape == (n, k) and (dw is None if i8 else dw.shape == (v, k))
+    c.check_backward(dx, dw, lse)
+
+
+# Above 2^26 logits the vocabulary is taken in pieces: sums that begin with the pieces before, targets on either side of
+# a piece's end, a narrow last piece; dx's sum shared out (short rows) and not (a tile for every compute unit); more rows
+# than leave a piece more than its least width.
+@pytest.mark.parametrize("i8", [False, True])
+@pytest.mark.parametrize("n, v, k", [(4100, 40000, 72), (4100, 40003, 4099), (9001, 20011, 40), (263000, 700, 24)])
+def test_backward_in_pieces_of_the_vocabulary(stq, n, v, k, i8):
+    c = Case(n, v, k, i8, n + v + k)
+    width = max(2 ** 26 // n // 256, 1) * 256
+    edges = sorted({e for w in (width, width - 256, width - 512) if w > 0 for p in range(w, v, w) for e in (p - 1, p) if e < v} | {0, v - 1})
+    for i in range(0, n, 7):
+        if i // 7 < 400:
+            c.targets[i] = edges[i // 7 % len(edges)]
+    kind = stq.X_I8 if i8 else stq.X_BF16
+    # (dl of the whole vocabulary alone takes this much, where the outputs' sums are small)
+    assert k > 100 or stq.head_cross_entropy_backward_workspace(kind, n, v, k, True, False) < 2 * n * v
+    loss, lse = stq.head_cross_entropy(c.x, c.w, c.targets, **c.args())
+    c.check_forward(loss, lse)
+    dx, dw = stq.head_cross_entropy_backward(c.x, c.w, c.targets, lse, c.grad, need_dw=not i8, **c.args())
     c.check_backward(dx, dw, lse)
 
 
