@@ -111,6 +111,13 @@ def test_probabilities_far_below_the_largest(stq):
     assert bool(((d[:, 1] - want).abs() <= U * (12 + 9 * p / (1 - p)) * want).all())
 
 
+# more chunks than the prefix sums take at once
+@pytest.mark.parametrize("n, e, k, pads", [(16450, 20, 2, 300), (33000, 70, 3, 0), (49153, 5, 1, 7)])
+def test_routing_of_long_prompts(stq, n, e, k, pads):
+    x = _logits(n, e, torch.float32, n, pads)
+    _check(stq.route_tokens(x.cuda(), k), x, k, True)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("n, e, k, pads", [(1, 16, 2, 1), (50, 64, 4, 20), (500, 256, 8, 77), (130, 40, 3, 130), (64, 512, 8, 64)])
 def test_padding(stq, n, e, k, pads, dtype):
