@@ -79,6 +79,33 @@ def test_forward(stq, n, d, xt, rt):
     _check(got, x, r, w)
 
 
+# many rows of more than a thread's held columns
+@pytest.mark.parametrize("rt", [None, torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n, d", [(520, 8203), (513, 16385)])
+def test_forward_of_many_wide_rows(stq, n, d, rt):
+    x, r, w = _inputs(n, d, torch.bfloat16, rt, n + d)
+    _check(stq.rmsnorm_rows(x.cuda(), w.cuda(), EPS, residual=None if r is None else r.cuda(), need_y=True), x, r, w)
+
+
+# the row's last columns are read whole, over those that a neighbour writes
+@pytest.mark.parametrize("t", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n, d", [(5, 9), (9, 87), (600, 87), (3, 515), (7, 4099), (600, 4099), (4, 9001), (530, 9001)])
+def test_in_place_of_ragged_rows(stq, n, d, t):
+    x, r, w = _inputs(n, d, t, t, n + d)
+    xc, rc, wc = x.cuda(), r.cuda(), w.cuda()
+    want = stq.rmsnorm_rows(xc, wc, EPS, rc, need_y=True)
+    for over_x in (False, True):
+        a, b = xc.clone(), rc.clone()
+        got = stq.rmsnorm_rows(a, wc, EPS, b, need_y=True, h=a if over_x else b)
+        assert got.h.data_ptr() == (a if over_x else b).data_ptr() and all(torch.equal(g, e) for g, e in zip(got, want))
+    dy, dh = _rand((n, d), 1).to(t).cuda(), _rand((n, d), 2).to(t).cuda()
+    dx, dw = stq.rmsnorm_rows_backward(want.h, wc, want.rstd, dy, dh=dh)
+    for name in ("dy", "dh"):
+        g = dict(dy=dy.clone(), dh=dh.clone())
+        dx2, dw2 = stq.rmsnorm_rows_backward(want.h, wc, want.rstd, g["dy"], dh=g["dh"], dx=g[name])
+        assert dx2.data_ptr() == g[name].data_ptr() and torch.equal(dx2, dx) and torch.equal(dw2, dw)
+
+
 def test_forward_single_outputs_and_given_ones(stq):
     x, r, w = _inputs(33, 1000, torch.bfloat16, torch.float32, 5)
     xc, rc, wc = x.cuda(), r.cuda(), w.cuda()
