@@ -17,6 +17,7 @@
 #include <type_traits>
 
 #include "stq_launch.hpp"
+#include "stq_round8.hpp"
 #include "stq_rows.hpp"
 
 namespace stq {
