@@ -57,7 +57,7 @@ struct NtArgs {
   int64_t m, n;
   int64_t kbytes;         // bytes of a row that count
   int64_t words;          // channels that lie along the other way: rows of w
-  int tm, tn, step_n;     // tiles, and channels between tiles
+  int tm, tn;             // tiles
   // logits
   const float* as;        // 8-bit rows: scales of tokens and channels
   const float* ws;
@@ -164,17 +164,13 @@ struct Slab {
   __device__ __forceinline__ char* at(int t, int chunk) const { return mem + t * kC * 2 + ((chunk ^ (tile_swizzle(t) & (kChunks - 1))) << 4); }
   // this wavefront's stores before, its loads after (LDS serves a wavefront in order)
   static __device__ __forceinline__ void fence() { asm volatile("" ::: "memory"); }
-  // rows t < rows, chunks below `width` channels, to out; once: whole lines that
-  // nothing reads again soon pass the caches by
-  __device__ __forceinline__ void store_rows(uint16_t* out, int64_t ld, int rows, int width, bool once = false) const {
+  // rows t < rows, chunks below `width` channels, to out
+  __device__ __forceinline__ void store_rows(uint16_t* out, int64_t ld, int rows, int width) const {
 #pragma unroll
     for (int i = 0; i < 32 * kChunks / 64; ++i) {
       const int t = (i * 64 + lane) / kChunks, c = (i * 64 + lane) % kChunks;
       const u32x4_t v = *reinterpret_cast<const u32x4_t*>(at(t, c));
-      if (t < rows && c * 8 < width) {
-        if (once) __builtin_nontemporal_store(v, &reinterpret_cast<Words16*>(out + t * ld + c * 8)->v);
-        else store16b(out + t * ld + c * 8, v);
-      }
+      if (t < rows && c * 8 < width) store16b(out + t * ld + c * 8, v);
     }
   }
   // the same transposed: out[channel][token], channels below `width`, tokens below `rows` (a multiple of 8).
@@ -391,7 +387,7 @@ __device__ __forceinline__ void finish(const NtArgs& a, typename Mfma<kI8>::acc_
   }
 }
 
-// Workgroup of WM x WN wavefronts, TM tokens x (at most) TN channels.  Both
+// Workgroup of WM x WN wavefronts, TM tokens x TN channels.  Both
 // operands stream into LDS 128 bytes of the sum at a time (direct 16-byte
 // loads) through kBuf buffers.  While the matrix cores work on one 64-byte
 // step, the operands of the next are read from LDS: a token operand into the
@@ -423,9 +419,9 @@ __global__ __launch_bounds__(WM * WN * 64, kWavesPerSimd) void nt_kernel(NtArgs 
   if (id >= tiles) return;
   const int band = id / (8 * a.tn), rows = min(8, a.tm - band * 8), in = id - band * 8 * a.tn;
   const int tile_n = in / rows;
-  const int64_t m0 = static_cast<int64_t>(band * 8 + in % rows) * TM, n0 = static_cast<int64_t>(tile_n) * a.step_n;
+  const int64_t m0 = static_cast<int64_t>(band * 8 + in % rows) * TM, n0 = static_cast<int64_t>(tile_n) * TN;
   const int mv = static_cast<int>(min(static_cast<int64_t>(TM), a.m - m0));
-  const int nv = static_cast<int>(min(static_cast<int64_t>(a.step_n), a.n - n0));
+  const int nv = static_cast<int>(min(static_cast<int64_t>(TN), a.n - n0));
   const uint32_t kpad = static_cast<uint32_t>((a.kbytes + 15) & ~15);
   const Rsrc ra = make_rsrc(a.a + m0 * a.lda, static_cast<uint32_t>((mv - 1) * a.lda) + kpad);
   const Rsrc rw = make_rsrc(a.w + n0 * a.ldw, static_cast<uint32_t>((nv - 1) * a.ldw) + kpad);
@@ -1345,10 +1341,9 @@ __global__ __launch_bounds__(256) void zero_rows_kernel(uint16_t* out, int64_t l
 }
 
 template <bool kI8, int kEpi, int TM, int TN, int WM, int WN, int kBuf, int kWavesPerSimd>
-void launch_tile(NtArgs a, int step_n, hipStream_t s) {
-  a.step_n = step_n;
+void launch_tile(NtArgs a, hipStream_t s) {
   a.tm = static_cast<int>((a.m + TM - 1) / TM);
-  a.tn = static_cast<int>((a.n + step_n - 1) / step_n);
+  a.tn = static_cast<int>((a.n + TN - 1) / TN);
   const int64_t tiles = static_cast<int64_t>(a.tm) * a.tn;
   const dim3 grid(static_cast<unsigned>((tiles + kXcds - 1) / kXcds * kXcds));
   hipLaunchKernelGGL((nt_kernel<kI8, kEpi, TM, TN, WM, WN, kBuf, kWavesPerSimd>), grid, dim3(WM * WN * 64), 0, s, a);
@@ -1400,10 +1395,10 @@ void launch_nt(const NtArgs& a, Tile t, int cus, hipStream_t s) {
         hipLaunchKernelGGL((nt_few_kernel<kI8, kEpi>), dim3(static_cast<unsigned>((n + 15) / 16)), dim3(kFewWaves * 64), 0, s, a);
       }
       break;
-    case k64x64: launch_tile<kI8, kEpi, 64, 64, 2, 2, 3, 2>(a, 64, s); break;
-    case k64x128: launch_tile<kI8, kEpi, 64, 128, 1, 4, 3, 2>(a, 128, s); break;
-    case k64x256: launch_tile<kI8, kEpi, 64, 256, 1, 4, 2, 2>(a, 256, s); break;
-    case k128x128: launch_tile<kI8, kEpi, 128, 128, 2, 2, 2, 2>(a, 128, s); break;
+    case k64x64: launch_tile<kI8, kEpi, 64, 64, 2, 2, 3, 2>(a, s); break;
+    case k64x128: launch_tile<kI8, kEpi, 64, 128, 1, 4, 3, 2>(a, s); break;
+    case k64x256: launch_tile<kI8, kEpi, 64, 256, 1, 4, 2, 2>(a, s); break;
+    case k128x128: launch_tile<kI8, kEpi, 128, 128, 2, 2, 2, 2>(a, s); break;
     case k256x256: launch_wide<kI8, kEpi, kRows>(a, cus, s); break;
   }
 }
