@@ -12,8 +12,8 @@
 // vocabulary at a time), or sums stored or added up (dx, dW).  dl is stored both
 // ways from the tile in LDS, and x transposed once, so that dW is such a product
 // too; dx takes W as it lies, a row for every term of its sum, with transposing
-// reads.  A piece's dl and its transpose stay near the 256 MB of the last-level
-// cache.
+// reads.  A piece has at most 2^26 logits (256 words under more than 2^18 rows), so
+// that its dl, 134 MB, and its transpose stay near the 256 MB of the last-level cache.
 //
 // Sums are in fp32 (8-bit operands': exact, in int32), statistics in fp32.  dl
 // is rounded to bf16 once, half a step of 2^-8 relative to each of its values,
@@ -1196,8 +1196,8 @@ __device__ __forceinline__ float2 join(float2 a, float2 b) {
 }
 
 // The parts of a token joined, kTok tokens a workgroup: 16 of them, whose
-// parts lie side by side, or, where there are few, one (one token with 6250
-// parts: 24 us with 16).
+// parts lie side by side, or, up to 256 tokens, one (2048 parts of one token, from
+// 131072 words: 4.7 us, 8.2 with 16; of 37 5.3 and 8.3, of 256 5.6 and 5.5).
 template <int kTok>
 __global__ __launch_bounds__(1024) void head_join_kernel(const float2* stats, const float* hit, const int32_t* targets, int64_t m,
                                                          int parts, int64_t vocab, float* loss, float* lse) {
@@ -1353,9 +1353,9 @@ void launch_tile(NtArgs a, hipStream_t s) {
 //  * Few tokens under a head: a workgroup for 16 channels, until there are as
 //    many tiles of 64 as half the compute units (8 x 7168: 4000 words 17 us, 31 in
 //    tiles of 64 x 64; 8000 words 28 and 32; 12000 words 38 and 33).
-//  * Up to 64 tokens: as wide a channel tile as leaves every CU two (40 rows of
-//    4096 in 8 bits, 50000 words: 41, 37 and 40 us in tiles of 64, 128 and 256; 37
-//    x 7168, 100003 words: 142, 147 and 133).
+//  * Up to 64 tokens: the narrower of 64 and 128 channels whose tiles are two a CU
+//    at most, else 256 (40 rows of 4096 in 8 bits, 50000 words: 41, 37 and 40 us in
+//    tiles of 64, 128 and 256; 37 x 7168, 100003 words: 142, 147 and 133).
 //  * More: the smallest of three estimates, in rounds of the chip (tiles of 64,
 //    128 and 256: 300 x 1024 x 8000 words in bf16 15.0, 15.6, 32 us; 512 x 4096 x
 //    32000 203, 134, 106).
@@ -1450,8 +1450,6 @@ hipError_t launch_head(const HeadArgs& h, float* loss, float* lse, void* ws, int
   return hipGetLastError();
 }
 
-// Pieces of the vocabulary: at most 2^26 logits and 2^27 weights each, and of
-// those the width whose tiles fill whole rounds of the chip best.
 // Parts that dx's sum over `stages` x 64 words is shared out into when its tiles
 // leave compute units idle: the fewest of what a tile's stages and its end (1.4
 // us a stage, 8 stages an end) and the parts' store and join cost together.  Above
@@ -1481,7 +1479,7 @@ static DwTokens dw_tokens(int64_t rows) {
 HeadBwdPlan plan_head_bwd(bool i8, int64_t rows, int64_t vocab, int64_t k, bool dx, bool dw, int cus) {
   HeadBwdPlan p{};
   if (i8 && rows <= kFewRows && rows * up(vocab, 64) <= int64_t{1} << 30) {
-    // the whole vocabulary at once: dl is small beside the head (and its rows within 32-bit offsets)
+    // the whole vocabulary at once, up to 2^30 logits: dl is small beside the head (and its rows within 32-bit offsets)
     p.few = 1;
     p.width = up(vocab, 64);
     p.pieces = 1;
@@ -1497,7 +1495,8 @@ HeadBwdPlan plan_head_bwd(bool i8, int64_t rows, int64_t vocab, int64_t k, bool 
     p.bytes = at + up(rows * 4, 256);
     return p;
   }
-  // pieces of the vocabulary whose dl (and its transpose) stay in the last-level cache
+  // pieces of the vocabulary: at most 2^26 logits, but 256 words at least, and of those
+  // widths the one whose tiles fill whole rounds of the chip best
   const int64_t cap = std::max<int64_t>(1, (int64_t{1} << 26) / rows / 256);
   const int64_t cols = (vocab + 255) / 256;
   const int64_t tm = (rows + 255) / 256;
